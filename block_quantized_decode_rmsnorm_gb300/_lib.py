@@ -15,6 +15,7 @@ LIB_PATH = os.path.join(_HERE, "libqgemv.so")
 
 QG_OK, QG_ERR_NULL, QG_ERR_ALIGN, QG_ERR_SHAPE, QG_ERR_UNSUPPORTED, QG_ERR_CUDA = range(6)
 QG_EPI_NONE, QG_EPI_SILU_MUL_HALVES, QG_EPI_RESIDUAL_ADD = 0, 1, 2
+QG_F32, QG_BF16 = 0, 1
 
 P = ctypes.c_void_p
 I64 = ctypes.c_int64
@@ -59,6 +60,11 @@ SIGNATURES = {
     "qg_q8_0_pack_f16": (ST, [P, P, I64, I64, P, P, P]),
     "quantize_act_q8_0_f16": (ST, [P, I64, I64, P, P, P]),
     "qgemm_q8_0_prefill_tc2": (ST, [P, P, I64, I64, P, P, I64, P, I32, P]),
+    "quantize_act_e4m3": (ST, [P, I32, I64, I64, P, P, P]),
+    "rmsnorm_add_quantize_e4m3": (ST, [P, P, P, I32, I64, I64, F32, P, P, P, P]),
+    "qgemm_e4m3": (ST, [P, P, I64, I64, P, P, I64, I32, P, P, I32, P]),
+    "qg_ffn_up_e4m3": (ST, [P, P, I64, I64, P, P, I64, P, P, P]),
+    "qg_ffn_e4m3": (ST, [P, P, P, I32, I64, I64, I64, F32, P, P, P, P, P, P, P, P, P, P]),
 }
 
 _lib = None
@@ -92,7 +98,7 @@ def load(path: str | None = None):
 
 def call(name: str, *args) -> None:
     """Call a qg_status-returning entry point; raise QGError on failure."""
-    lib = load()
+    lib = _lib or load()
     st = getattr(lib, name)(*args)
     if st != QG_OK:
         raise QGError(name, st, lib.qg_status_str(st).decode())

@@ -11,6 +11,9 @@ Tensor formats
   [rows, k/32]`` (the library reads the binary16 bit patterns).
 * Weights in the packed layout: a ``Q8Weight(qs, d)`` pair as above.
 * bf16 tensors: ``torch.bfloat16``.
+* e4m3 codes: ``torch.float8_e4m3fn [rows, k]``; their scales: ``torch.float32``,
+  ``[rows, ceil(k/128)]`` for activations, ``[ceil(n_rows/128), ceil(k/128)]`` for
+  weights (an ``E4M3Weight(codes, scales)`` pair).
 """
 
 from __future__ import annotations
@@ -776,6 +779,264 @@ class DecodeStack:
     def reset(self) -> None:
         """Zero-fill the workspace again (after a launch that set the status)."""
         self.workspace.zero_()
+
+
+# --------------------------------------------------------------------------
+# 8-bit floating point: e4m3 codes, one f32 scale per block of 128
+# --------------------------------------------------------------------------
+
+_E4M3 = torch.float8_e4m3fn
+_STREAM_TYPES = {torch.float32: _lib.QG_F32, torch.bfloat16: _lib.QG_BF16}
+
+
+@dataclass
+class E4M3Weight:
+    """e4m3 weight: codes float8_e4m3fn [n_rows, k] and f32 scales, one per
+    128 x 128 block [ceil(n_rows/128), ceil(k/128)].  A stacked gate|up weight
+    holds the two matrices' codes and the two matrices' scales one after the
+    other: codes [2 ffn, k], scales [2 ceil(ffn/128), ceil(k/128)]."""
+
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+    @property
+    def n_rows(self) -> int:
+        return self.codes.shape[0]
+
+    @property
+    def k(self) -> int:
+        return self.codes.shape[1]
+
+    @property
+    def nbytes(self) -> int:
+        return self.codes.numel() + 4 * self.scales.numel()
+
+
+def _blocks128(n: int) -> int:
+    return (n + 127) // 128
+
+
+def _current_device(t: torch.Tensor, name: str) -> int:
+    """The tensor's device, which has to be the current one: kernels are launched there."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device (there is no CPU path)")
+    dev = t.get_device()
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{name} is on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
+    return dev
+
+
+def _check(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, dev: int) -> None:
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev \
+            and t.is_contiguous():
+        return
+    _need(t, name, dtype, shape)
+    raise ValueError(f"{name} must be on cuda:{dev}")
+
+
+def _new(shape: tuple, dtype: torch.dtype, dev: int, stream) -> torch.Tensor:
+    """An output, allocated for the stream that writes it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream_handle(stream))
+    with torch.cuda.stream(s):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _stream_type(x: torch.Tensor, name: str) -> int:
+    t = _STREAM_TYPES.get(x.dtype)
+    if t is None:
+        raise TypeError(f"{name} must be torch.float32 or torch.bfloat16, got {x.dtype}")
+    return t
+
+
+def _rows_of(x: torch.Tensor, name: str) -> tuple:
+    if x.dim() not in (1, 2):
+        raise ValueError(f"{name} must have shape [rows, k] or [k], got {tuple(x.shape)}")
+    return (1, x.shape[0]) if x.dim() == 1 else (x.shape[0], x.shape[1])
+
+
+def _codes_out(rows: int, k: int, q, d, dev: int, stream, names=("q", "d")):
+    shape, scales = (rows, k), (rows, _blocks128(k))
+    if q is None:
+        q = _new(shape, _E4M3, dev, stream)
+    else:
+        _check(q, names[0], _E4M3, shape, dev)
+    if d is None:
+        d = _new(scales, torch.float32, dev, stream)
+    else:
+        _check(d, names[1], torch.float32, scales, dev)
+    return q, d
+
+
+def quantize_act_e4m3(x: torch.Tensor, q: torch.Tensor | None = None, d: torch.Tensor | None = None, stream=None):
+    """f32 or bf16 [rows, k] (or [k]) -> (q float8_e4m3fn [rows, k], d f32 [rows, ceil(k/128)]);
+    k a multiple of 16."""
+    dev = _current_device(x, "x")
+    kind = _stream_type(x, "x")
+    rows, k = _rows_of(x, "x")
+    _check(x, "x", x.dtype, x.shape, dev)
+    q, d = _codes_out(rows, k, q, d, dev, stream)
+    _lib.call("quantize_act_e4m3", x.data_ptr(), kind, rows, k, q.data_ptr(), d.data_ptr(), _stream_handle(stream))
+    return q, d
+
+
+def rmsnorm_add_quantize_e4m3(x: torch.Tensor, gamma: torch.Tensor, residual: torch.Tensor | None = None,
+                              eps: float = 1e-6, s: torch.Tensor | None = None, q: torch.Tensor | None = None,
+                              d: torch.Tensor | None = None, stream=None):
+    """s = x + residual; codes and scales of RMSNorm(s) * gamma; returns (q, d, s).
+
+    x, residual, s and gamma are all f32 or all bf16, [rows, k] (or [k]); s may be
+    x or residual (the sum in place).  Without a residual s is x itself."""
+    dev = _current_device(x, "x")
+    kind = _stream_type(x, "x")
+    rows, k = _rows_of(x, "x")
+    _check(x, "x", x.dtype, x.shape, dev)
+    _check(gamma, "gamma", x.dtype, (k,), dev)
+    if residual is None:
+        if s is not None and s is not x:
+            raise ValueError("s is written only with a residual")
+        s = x
+    else:
+        _check(residual, "residual", x.dtype, x.shape, dev)
+        if s is None:
+            s = _new(x.shape, x.dtype, dev, stream)
+        else:
+            _check(s, "s", x.dtype, x.shape, dev)
+    q, d = _codes_out(rows, k, q, d, dev, stream)
+    _lib.call("rmsnorm_add_quantize_e4m3", x.data_ptr(), _ptr(residual), gamma.data_ptr(), kind, rows, k, eps,
+              s.data_ptr(), q.data_ptr(), d.data_ptr(), _stream_handle(stream))
+    return q, d, s
+
+
+def _check_e4m3_operands(codes, scales, blocks: int, xq, xd, dev: int):
+    """Shapes of a weight (`blocks` rows of scales) and the activations that it meets; returns (m, k)."""
+    if not isinstance(codes, torch.Tensor) or codes.dim() != 2:
+        raise ValueError("w.codes must be a tensor of shape [n_rows, k]")
+    n_rows, k = codes.shape
+    kb = _blocks128(k)
+    _check(codes, "w.codes", _E4M3, (n_rows, k), dev)
+    _check(scales, "w.scales", torch.float32, (blocks, kb), dev)
+    if xq.dim() == 1 and xd.dim() == 1:
+        m = 1
+        _check(xq, "xq", _E4M3, (k,), dev)
+        _check(xd, "xd", torch.float32, (kb,), dev)
+    else:
+        m = xq.shape[0]
+        _check(xq, "xq", _E4M3, (m, k), dev)
+        _check(xd, "xd", torch.float32, (m, kb), dev)
+    return m, k
+
+
+def qgemm_e4m3(w: E4M3Weight, xq: torch.Tensor, xd: torch.Tensor, epilogue: str | int = "none",
+               residual: torch.Tensor | None = None, y: torch.Tensor | None = None,
+               out_dtype: torch.dtype | None = None, stream=None) -> torch.Tensor:
+    """Block-scaled e4m3 product of m >= 0 activation rows; y [m, n_rows], f32 or
+    bf16 (out_dtype, by default y's or the residual's type, else f32).  The
+    residual has y's type and may be y itself."""
+    dev = _current_device(xq, "xq")
+    epi = EPILOGUES[epilogue] if isinstance(epilogue, str) else int(epilogue)
+    n = w.codes.shape[0]
+    m, k = _check_e4m3_operands(w.codes, w.scales, _blocks128(n), xq, xd, dev)
+    if epi == QG_EPI_RESIDUAL_ADD:
+        if residual is None:
+            raise ValueError("the residual epilogue needs a residual")
+    elif residual is not None:
+        raise ValueError("a residual goes with epilogue='residual'")
+    if out_dtype is None:
+        out_dtype = y.dtype if y is not None else residual.dtype if residual is not None else torch.float32
+    kind = _STREAM_TYPES.get(out_dtype)
+    if kind is None:
+        raise TypeError(f"out_dtype must be torch.float32 or torch.bfloat16, got {out_dtype}")
+    if y is None:
+        y = _new((m, n), out_dtype, dev, stream)
+    else:
+        _check(y, "y", out_dtype, (m, n), dev)
+    if residual is not None:
+        _check(residual, "residual", out_dtype, (m, n), dev)
+    _lib.call("qgemm_e4m3", w.codes.data_ptr(), w.scales.data_ptr(), n, k, xq.data_ptr(), xd.data_ptr(), m, epi,
+              _ptr(residual), y.data_ptr(), kind, _stream_handle(stream))
+    return y
+
+
+def qg_ffn_up_e4m3(w: E4M3Weight, xq: torch.Tensor, xd: torch.Tensor, hq: torch.Tensor | None = None,
+                   hd: torch.Tensor | None = None, stream=None):
+    """Stacked gate|up product, SiLU(g) * u and its quantization in one launch:
+    (hq float8_e4m3fn [m, ffn], hd f32 [m, ceil(ffn/128)])."""
+    dev = _current_device(xq, "xq")
+    n2 = w.codes.shape[0]
+    if n2 % 32:
+        raise ValueError(f"a stacked gate|up weight has 2 ffn rows, ffn a multiple of 16: got {n2}")
+    ffn = n2 // 2
+    m, k = _check_e4m3_operands(w.codes, w.scales, 2 * _blocks128(ffn), xq, xd, dev)
+    hq, hd = _codes_out(m, ffn, hq, hd, dev, stream, ("hq", "hd"))
+    _lib.call("qg_ffn_up_e4m3", w.codes.data_ptr(), w.scales.data_ptr(), ffn, k, xq.data_ptr(), xd.data_ptr(), m,
+              hq.data_ptr(), hd.data_ptr(), _stream_handle(stream))
+    return hq, hd
+
+
+@dataclass
+class E4M3Layer:
+    """Weights of one e4m3 feed-forward block: RMSNorm gain (in the stream's type),
+    stacked gate|up (scales [2 ceil(ffn/128), .]) and down."""
+
+    gamma: torch.Tensor  # [hidden]
+    gate_up: E4M3Weight  # [2*ffn, hidden]
+    down: E4M3Weight     # [hidden, ffn]
+
+    @property
+    def nbytes(self) -> int:
+        return self.gate_up.nbytes + self.down.nbytes
+
+
+@dataclass
+class E4M3Buffers:
+    """Work buffers of qg_ffn_e4m3 for m rows (graph replay needs fixed addresses)."""
+
+    xq: torch.Tensor
+    xd: torch.Tensor
+    hq: torch.Tensor
+    hd: torch.Tensor
+
+    @staticmethod
+    def allocate(m: int, hidden: int, ffn: int, device) -> "E4M3Buffers":
+        return E4M3Buffers(torch.empty((m, hidden), dtype=_E4M3, device=device),
+                           torch.empty((m, _blocks128(hidden)), dtype=torch.float32, device=device),
+                           torch.empty((m, ffn), dtype=_E4M3, device=device),
+                           torch.empty((m, _blocks128(ffn)), dtype=torch.float32, device=device))
+
+
+def qg_ffn_e4m3(x: torch.Tensor, layer: E4M3Layer, residual: torch.Tensor | None = None, eps: float = 1e-6,
+                buf: E4M3Buffers | None = None, y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """s = x + residual; y = s + down(SiLU(g) * u), (g|u) = gate|up(RMSNorm(s) * gamma),
+    over m rows in three launches.  x, residual and y are [m, hidden], all f32 or all
+    bf16; y may be x or residual (in place)."""
+    dev = _current_device(x, "x")
+    kind = _stream_type(x, "x")
+    m, hidden = _rows_of(x, "x")
+    ffn = layer.down.codes.shape[1]
+    hb, fb = _blocks128(hidden), _blocks128(ffn)
+    _check(x, "x", x.dtype, x.shape, dev)
+    if residual is not None:
+        _check(residual, "residual", x.dtype, x.shape, dev)
+    _check(layer.gamma, "layer.gamma", x.dtype, (hidden,), dev)
+    _check(layer.gate_up.codes, "layer.gate_up.codes", _E4M3, (2 * ffn, hidden), dev)
+    _check(layer.gate_up.scales, "layer.gate_up.scales", torch.float32, (2 * fb, hb), dev)
+    _check(layer.down.codes, "layer.down.codes", _E4M3, (hidden, ffn), dev)
+    _check(layer.down.scales, "layer.down.scales", torch.float32, (hb, fb), dev)
+    xq, xd = _codes_out(m, hidden, buf and buf.xq, buf and buf.xd, dev, stream, ("buf.xq", "buf.xd"))
+    hq, hd = _codes_out(m, ffn, buf and buf.hq, buf and buf.hd, dev, stream, ("buf.hq", "buf.hd"))
+    if y is None:
+        y = _new(x.shape, x.dtype, dev, stream)
+    else:
+        _check(y, "y", x.dtype, x.shape, dev)
+    _lib.call("qg_ffn_e4m3", x.data_ptr(), _ptr(residual), layer.gamma.data_ptr(), kind, m, hidden, ffn, eps,
+              layer.gate_up.codes.data_ptr(), layer.gate_up.scales.data_ptr(), layer.down.codes.data_ptr(),
+              layer.down.scales.data_ptr(), xq.data_ptr(), xd.data_ptr(), hq.data_ptr(), hd.data_ptr(), y.data_ptr(),
+              _stream_handle(stream))
+    return y
 
 
 # --------------------------------------------------------------------------

@@ -69,6 +69,13 @@ int stack_max_layers();
 cudaError_t launch_decode_stack(const float *, float *, int, const float *const *, const int8_t *const *,
                                 const uint16_t *const *, const int8_t *const *, const uint16_t *const *, int64_t,
                                 int64_t, float, void *, float *, int8_t *, uint16_t *, uint64_t, cudaStream_t);
+cudaError_t launch_quantize_e4m3(const void *, int, int64_t, int64_t, uint8_t *, float *, cudaStream_t);
+cudaError_t launch_norm_e4m3(const void *, const void *, const void *, int, int64_t, int64_t, float, void *, uint8_t *,
+                             float *, cudaStream_t);
+cudaError_t launch_rows_e4m3(const uint8_t *, const float *, int64_t, int64_t, const uint8_t *, const float *, int64_t,
+                             const void *, void *, int, cudaStream_t);
+cudaError_t launch_rows_up_e4m3(const uint8_t *, const float *, int64_t, int64_t, const uint8_t *, const float *,
+                                int64_t, uint8_t *, float *, cudaStream_t);
 
 // SM count of the current device, read once per device.
 int num_sms()
@@ -129,6 +136,34 @@ qg_status check_q8_k(int64_t k)
 {
     if (k <= 0 || k % 32 != 0 || k > kMaxK) return QG_ERR_SHAPE;
     return QG_OK;
+}
+
+// 8-bit floating point path
+constexpr int64_t kE4M3MaxM = int64_t(1) << 24;
+
+int64_t e4m3_kb(int64_t k) { return (k + 127) / 128; }
+bool dtype_ok(int t) { return t == QG_F32 || t == QG_BF16; }
+int64_t dtype_size(int t) { return t == QG_BF16 ? 2 : 4; }
+bool e4m3_k_ok(int64_t k, int64_t most) { return k > 0 && k % 16 == 0 && k <= most; }
+
+struct Span {
+    const void *p;
+    int64_t n;
+};
+
+size_t bytes(const Span &s) { return static_cast<size_t>(s.n); }
+
+// Some output shares a byte with an input or with another output.
+template <size_t NO, size_t NI>
+bool any_overlap(const Span (&out)[NO], const Span (&in)[NI])
+{
+    for (size_t i = 0; i < NO; ++i) {
+        for (size_t j = 0; j < NI; ++j)
+            if (out[i].p && in[j].p && overlap(out[i].p, bytes(out[i]), in[j].p, bytes(in[j]))) return true;
+        for (size_t j = i + 1; j < NO; ++j)
+            if (out[i].p && out[j].p && overlap(out[i].p, bytes(out[i]), out[j].p, bytes(out[j]))) return true;
+    }
+    return false;
 }
 
 }  // namespace
@@ -610,6 +645,110 @@ qg_status qg_debug_block_dots_q8_0(const int8_t *w_qs, int64_t n_rows, int64_t k
     if (!w_qs || !xq || !s) return QG_ERR_NULL;
     if (!aligned(w_qs, 32) || !aligned(xq, 16) || !aligned(s, 4)) return QG_ERR_ALIGN;
     return from_cuda(qg::launch_block_dots(w_qs, n_rows, k, xq, batch, s, stream));
+}
+
+// ---- 8-bit floating point path ---------------------------------------------
+qg_status quantize_act_e4m3(const void *x, int dtype, int64_t rows, int64_t k, uint8_t *q, float *d,
+                            qg_stream_t stream)
+{
+    if (!dtype_ok(dtype)) return QG_ERR_UNSUPPORTED;
+    if (!e4m3_k_ok(k, kMaxK) || rows < 0 || rows > (int64_t(1) << 34) / e4m3_kb(k)) return QG_ERR_SHAPE;
+    if (rows == 0) return QG_OK;
+    if (!x || !q || !d) return QG_ERR_NULL;
+    if (!aligned(x, 16) || !aligned(q, 16) || !aligned(d, 4)) return QG_ERR_ALIGN;
+    const int64_t rk = rows * k;
+    const Span out[] = {{q, rk}, {d, rows * e4m3_kb(k) * 4}}, in[] = {{x, rk * dtype_size(dtype)}};
+    if (any_overlap(out, in)) return QG_ERR_SHAPE;
+    return from_cuda(qg::launch_quantize_e4m3(x, dtype, rows, k, q, d, stream));
+}
+
+qg_status rmsnorm_add_quantize_e4m3(const void *x, const void *residual, const void *gamma, int dtype, int64_t rows,
+                                    int64_t k, float eps, void *s, uint8_t *q, float *d, qg_stream_t stream)
+{
+    if (!dtype_ok(dtype)) return QG_ERR_UNSUPPORTED;
+    if (!e4m3_k_ok(k, 65536) || rows < 0 || rows > INT32_MAX) return QG_ERR_SHAPE;
+    if (!(eps >= 0.0f)) return QG_ERR_SHAPE;
+    if (rows == 0) return QG_OK;
+    if (!residual) s = nullptr;
+    if (!x || !gamma || !q || !d || (residual && !s)) return QG_ERR_NULL;
+    if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(gamma, 16) || !aligned(s, 16) || !aligned(q, 16) ||
+        !aligned(d, 4))
+        return QG_ERR_ALIGN;
+    const int64_t rk = rows * k, e = dtype_size(dtype);
+    const Span out[] = {{s, rk * e}, {q, rk}, {d, rows * e4m3_kb(k) * 4}},
+               in[] = {{s == x ? nullptr : x, rk * e}, {s == residual ? nullptr : residual, rk * e},
+                       {gamma, k * e}};
+    if (any_overlap(out, in)) return QG_ERR_SHAPE;
+    return from_cuda(qg::launch_norm_e4m3(x, residual, gamma, dtype, rows, k, eps, s, q, d, stream));
+}
+
+qg_status qgemm_e4m3(const uint8_t *w, const float *wd, int64_t n_rows, int64_t k, const uint8_t *xq, const float *xd,
+                     int64_t m, int epilogue, const void *residual, void *y, int y_dtype, qg_stream_t stream)
+{
+    if (!dtype_ok(y_dtype)) return QG_ERR_UNSUPPORTED;
+    if (epilogue != QG_EPI_NONE && epilogue != QG_EPI_RESIDUAL_ADD) return QG_ERR_UNSUPPORTED;
+    if (!e4m3_k_ok(k, kMaxK) || m < 0 || m > kE4M3MaxM || n_rows < 0 || n_rows >= (int64_t(1) << 31) - 256)
+        return QG_ERR_SHAPE;
+    if (m == 0 || n_rows == 0) return QG_OK;
+    if (epilogue == QG_EPI_NONE) residual = nullptr;
+    if (!w || !wd || !xq || !xd || !y || (epilogue == QG_EPI_RESIDUAL_ADD && !residual)) return QG_ERR_NULL;
+    if (!aligned(w, 16) || !aligned(wd, 4) || !aligned(xq, 16) || !aligned(xd, 4) || !aligned(y, 16) ||
+        !aligned(residual, 16))
+        return QG_ERR_ALIGN;
+    const int64_t yb = m * n_rows * dtype_size(y_dtype), kb = e4m3_kb(k);
+    const Span out[] = {{y, yb}},
+               in[] = {{w, n_rows * k}, {wd, e4m3_kb(n_rows) * kb * 4},
+                       {xq, m * k}, {xd, m * kb * 4}, {residual == y ? nullptr : residual, yb}};
+    if (any_overlap(out, in)) return QG_ERR_SHAPE;
+    return from_cuda(qg::launch_rows_e4m3(w, wd, n_rows, k, xq, xd, m, residual, y, y_dtype, stream));
+}
+
+qg_status qg_ffn_up_e4m3(const uint8_t *w, const float *wd, int64_t ffn, int64_t k, const uint8_t *xq, const float *xd,
+                         int64_t m, uint8_t *hq, float *hd, qg_stream_t stream)
+{
+    if (!e4m3_k_ok(k, kMaxK) || m < 0 || m > kE4M3MaxM || ffn < 0 || ffn % 16 != 0 ||
+        ffn >= (int64_t(1) << 30) - 256)
+        return QG_ERR_SHAPE;
+    if (m == 0 || ffn == 0) return QG_OK;
+    if (!w || !wd || !xq || !xd || !hq || !hd) return QG_ERR_NULL;
+    if (!aligned(w, 16) || !aligned(wd, 4) || !aligned(xq, 16) || !aligned(xd, 4) || !aligned(hq, 16) ||
+        !aligned(hd, 4))
+        return QG_ERR_ALIGN;
+    const int64_t kb = e4m3_kb(k);
+    const Span out[] = {{hq, m * ffn}, {hd, m * e4m3_kb(ffn) * 4}},
+               in[] = {{w, (2 * ffn) * k}, {wd, 2 * e4m3_kb(ffn) * kb * 4},
+                       {xq, m * k}, {xd, m * kb * 4}};
+    if (any_overlap(out, in)) return QG_ERR_SHAPE;
+    return from_cuda(qg::launch_rows_up_e4m3(w, wd, ffn, k, xq, xd, m, hq, hd, stream));
+}
+
+qg_status qg_ffn_e4m3(const void *x, const void *residual, const void *gamma, int dtype, int64_t m, int64_t hidden,
+                      int64_t ffn, float eps, const uint8_t *wgu, const float *wgu_d, const uint8_t *wdn,
+                      const float *wdn_d, uint8_t *xq, float *xd, uint8_t *hq, float *hd, void *y, qg_stream_t stream)
+{
+    // every check before the first launch: the three calls' own, then what they do not see of one another
+    if (!dtype_ok(dtype)) return QG_ERR_UNSUPPORTED;
+    if (!e4m3_k_ok(hidden, 65536) || !e4m3_k_ok(ffn, kMaxK) || m < 0 || m > kE4M3MaxM) return QG_ERR_SHAPE;
+    if (!(eps >= 0.0f)) return QG_ERR_SHAPE;
+    if (m == 0) return QG_OK;
+    if (!x || !gamma || !wgu || !wgu_d || !wdn || !wdn_d || !xq || !xd || !hq || !hd || !y) return QG_ERR_NULL;
+    if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(gamma, 16) || !aligned(wgu, 16) || !aligned(wgu_d, 4) ||
+        !aligned(wdn, 16) || !aligned(wdn_d, 4) || !aligned(xq, 16) || !aligned(xd, 4) || !aligned(hq, 16) ||
+        !aligned(hd, 4) || !aligned(y, 16))
+        return QG_ERR_ALIGN;
+    const int64_t e = dtype_size(dtype), hb = e4m3_kb(hidden), fb = e4m3_kb(ffn), xb = m * hidden * e;
+    const Span out[] = {{y, xb}, {xq, m * hidden}, {xd, m * hb * 4},
+                        {hq, m * ffn}, {hd, m * fb * 4}},
+               in[] = {{y == x ? nullptr : x, xb}, {y == residual ? nullptr : residual, xb},
+                       {gamma, hidden * e}, {wgu, (2 * ffn) * hidden},
+                       {wgu_d, 2 * fb * hb * 4}, {wdn, hidden * ffn}, {wdn_d, hb * fb * 4}};
+    if (any_overlap(out, in)) return QG_ERR_SHAPE;
+    const void *s = residual ? y : x;
+    if (qg_status st = rmsnorm_add_quantize_e4m3(x, residual, gamma, dtype, m, hidden, eps, y, xq, xd, stream);
+        st != QG_OK)
+        return st;
+    if (qg_status st = qg_ffn_up_e4m3(wgu, wgu_d, ffn, hidden, xq, xd, m, hq, hd, stream); st != QG_OK) return st;
+    return qgemm_e4m3(wdn, wdn_d, hidden, ffn, hq, hd, m, QG_EPI_RESIDUAL_ADD, s, y, dtype, stream);
 }
 
 }  // extern "C"

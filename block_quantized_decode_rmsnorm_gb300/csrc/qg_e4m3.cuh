@@ -1,0 +1,90 @@
+// The e4m3 block format of the 8-bit floating point path, and its device helpers.
+//
+// Values are held as e4m3 codes (sign, 4 exponent bits, 3 mantissa bits, largest
+// 448, no infinity) with one f32 scale per block of 128 along the reduction (the
+// last block of a row may be shorter): activations one scale per row and block,
+// weights one per 128 rows and block.  Quantizing a block:
+//   a = max(max|v|, 2^-100)      (a NaN is passed over by the maximum)
+//   code = e4m3(v * fl(448 / a)) (nearest even; |v| <= a, so nothing saturates
+//                                 but by the rounding of the factor; NaN stays NaN)
+//   scale = fl(a / 448)
+// The floor keeps 448 / a finite and makes a block of zeros an ordinary one.  One
+// reciprocal factor per block instead of a division per value: the f32 rounding
+// of the factor and of the product move a value by 2^-23 of itself against a
+// code's own half step of 2^-4, so a code differs from that of the real quotient
+// only where the quotient lies that close to the middle of two codes.  A block
+// with an infinity has scale infinity and NaN for every value it stands for.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "qg_common.cuh"
+
+namespace qg {
+
+constexpr int EB = 128;  // values per scale
+
+__host__ __device__ constexpr int64_t e4m3_blocks(int64_t k) { return (k + EB - 1) / EB; }
+
+// Largest magnitude of a block, from the warp's (or half-warp's) values.
+__device__ __forceinline__ float e4m3_floor(float a) { return fmaxf(a, 0x1p-100f); }
+
+// max over the warp of non-negative floats, none of them NaN: their bit patterns
+// order as unsigned integers.
+__device__ __forceinline__ float warp_max_nonneg(float a)
+{
+    return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(a)));
+}
+
+// Two codes, lo in bits 0-7.
+__device__ __forceinline__ uint32_t e4m3_pack2(float lo, float hi)
+{
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t e4m3_pack4(float a, float b, float c, float d)
+{
+    return e4m3_pack2(a, b) | (e4m3_pack2(c, d) << 16);
+}
+
+// Four stream values (f32, or bf16 widened exactly).
+template <typename T>
+struct Vec4;
+template <>
+struct Vec4<float> {
+    using raw = float4;
+    static __device__ __forceinline__ float4 widen(raw v) { return v; }
+    static __device__ __forceinline__ raw narrow(float4 v) { return v; }
+};
+template <>
+struct Vec4<__nv_bfloat16> {
+    using raw = uint2;
+    static __device__ __forceinline__ float4 widen(raw v)
+    {
+        return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
+                           __uint_as_float(v.y & 0xffff0000u));
+    }
+    static __device__ __forceinline__ raw narrow(float4 v)
+    {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+        return make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+    }
+};
+
+__device__ __forceinline__ float max_abs4(float4 v)
+{
+    // fmaxf passes over NaN; four NaN leave 0
+    return fmaxf(fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))), 0.0f);
+}
+
+// SiLU(g) * u to a few f32 ulp over the whole range: e = e^-|g| in (0, 1] never
+// overflows, silu(g) = g / (1 + e) for g >= 0 and (g e) / (1 + e) below.
+__device__ __forceinline__ float silu_mul_e(float g, float u)
+{
+    const float e = expf(-fabsf(g));
+    const float num = g >= 0.0f ? g : g * e;
+    return __fdividef(num, 1.0f + e) * u;
+}
+
+}  // namespace qg

@@ -600,6 +600,111 @@ QG_API qg_status qgemm_bf16_prefill(const uint16_t *w, int64_t n_rows, int64_t k
                                     int64_t m, const uint16_t *gamma, float eps, int epilogue,
                                     uint16_t *xhat, float *y, qg_stream_t stream);
 
+/*
+ * The 8-bit floating point path: e4m3 codes (sign, 4 exponent bits, 3 mantissa
+ * bits, largest 448) with one f32 scale per block of 128 values along the
+ * reduction, the block-quantized form of checkpoints stored in 8-bit floating
+ * point ([Phobos] Fast Decode: quantize the activation once and share it, stack
+ * the projections, fold the residual into the matmul; [Herbert] Emitting for a
+ * GPU: fuse the normalization and the activation with the projections around
+ * them).  The four calls follow one another in a feed-forward block, for one
+ * token as for a prompt: rmsnorm_add_quantize_e4m3, qg_ffn_up_e4m3, qgemm_e4m3
+ * (qg_ffn_e4m3 makes the three calls), and quantize_act_e4m3 for any other input.
+ *
+ * Format.  KB = ceil(k / 128); the last block of a row is the shorter one.
+ *   activations: codes uint8[rows][k], scales f32[rows][KB]
+ *   weights:     codes uint8[n_rows][k], scales f32[ceil(n_rows/128)][KB], one
+ *                per 128 rows x 128 columns
+ *   value = code * scale.  Quantizing a block of values v:
+ *     a = max(max|v|, 2^-100)  (NaN passed over),  scale = fl(a / 448),
+ *     code = e4m3(fl(v * fl(448 / a))), round to nearest even; NaN keeps a NaN
+ *     code, and a block with an infinity stands for NaN throughout.
+ * k: a positive multiple of 16 up to 2^20 (rmsnorm_add_quantize_e4m3: up to
+ * 65536).  Code planes and stream tensors 16-byte aligned, scales 4-byte aligned.
+ * Outputs must not overlap inputs or one another (QG_ERR_SHAPE) except where
+ * stated.  Every sum is taken in a fixed order: results repeat bit for bit.
+ */
+typedef enum {
+    QG_F32 = 0,
+    QG_BF16 = 1
+} qg_dtype;
+
+/*
+ * quantize_act_e4m3 - activations -> codes and scales.
+ *   x: device f32 or bf16 (dtype, a qg_dtype) [rows][k] (read)
+ *   q: device uint8[rows][k], d: device f32[rows][KB] (written)
+ *   rows * KB <= 2^34.
+ */
+QG_API qg_status quantize_act_e4m3(const void *x, int dtype, int64_t rows, int64_t k, uint8_t *q, float *d,
+                                   qg_stream_t stream);
+
+/*
+ * rmsnorm_add_quantize_e4m3 - the residual's addition, RMSNorm and quantization
+ * of each row in one pass:
+ *   s = x + residual        (f32 sum, rounded once to the stream's type)
+ *   r = 1 / sqrt(mean_k(s^2) + eps), evaluated in f64 and rounded once to f32
+ *   q, d = codes and scales of (s * r) * gamma (two f32 products)
+ * as rmsnorm_quantize does for Q8_0 without the addition; the same range holds
+ * (s^2 must not overflow f32).
+ *   x, residual, s: device f32 or bf16 (dtype, a qg_dtype) [rows][k]; gamma [k] of
+ *   the same type.  residual NULL: s = x, and the argument s is not used (NULL
+ *   allowed); otherwise s is written, and may be x or residual itself.
+ *   rows < 2^31, k <= 65536, eps >= 0.
+ */
+QG_API qg_status rmsnorm_add_quantize_e4m3(const void *x, const void *residual, const void *gamma, int dtype,
+                                           int64_t rows, int64_t k, float eps, void *s, uint8_t *q, float *d,
+                                           qg_stream_t stream);
+
+/*
+ * qgemm_e4m3 - the block-scaled product, for 1 to 2^24 activation rows:
+ *   acc[m][n] = sum_b (xd[m][b] * wd[n / 128][b]) * S_b,
+ *   S_b = sum over block b of x[m][i] * w[n][i]  (products exact, f32 sums)
+ *   y = acc (QG_EPI_NONE) or residual + acc (QG_EPI_RESIDUAL_ADD), rounded once
+ *   to y's type.  QG_EPI_SILU_MUL_HALVES is qg_ffn_up_e4m3 (QG_ERR_UNSUPPORTED).
+ *   w, wd: weights [n_rows][k]; xq, xd: activations [m][k] (read)
+ *   y, residual: device f32 or bf16 (y_dtype, a qg_dtype) [m][n_rows], 16-byte
+ *   aligned; residual may be y itself (otherwise no overlap).
+ *   n_rows < 2^31 - 256.
+ * If an operand copy stalls beyond one second the kernel stops waiting and
+ * writes NaN for the tiles it has left, rather than hanging.
+ */
+QG_API qg_status qgemm_e4m3(const uint8_t *w, const float *wd, int64_t n_rows, int64_t k, const uint8_t *xq,
+                            const float *xd, int64_t m, int epilogue, const void *residual, void *y, int y_dtype,
+                            qg_stream_t stream);
+
+/*
+ * qg_ffn_up_e4m3 - gate|up, SiLU(g) * u and the quantization of h in one launch:
+ *   g = x_hat gate^T, u = x_hat up^T (as qgemm_e4m3, kept in f32),
+ *   h = silu(g) * u,  hq, hd = codes and scales of h.
+ *   w: stacked codes uint8[2 * ffn][k], gate rows [0, ffn), up rows [ffn, 2 ffn);
+ *   wd: f32[2 * ceil(ffn/128)][KB], each half with blocks of its own: gate row i
+ *   has scale row i / 128, up row i has ceil(ffn/128) + i / 128 (the two matrices'
+ *   planes one after the other; with ffn a multiple of 128 that of the stacked
+ *   matrix).  ffn a multiple of 16, ffn < 2^30 - 256.
+ *   xq, xd: activations [m][k], m up to 2^24 (read)
+ *   hq: device uint8[m][ffn], hd: device f32[m][ceil(ffn/128)] (written)
+ * Stalled copies as qgemm_e4m3 (codes and scales NaN).
+ */
+QG_API qg_status qg_ffn_up_e4m3(const uint8_t *w, const float *wd, int64_t ffn, int64_t k, const uint8_t *xq,
+                                const float *xd, int64_t m, uint8_t *hq, float *hd, qg_stream_t stream);
+
+/*
+ * qg_ffn_e4m3 - a feed-forward block over m rows, in three launches:
+ *   s = x + residual;  y = s + down(h),  h = SiLU(g) * u,  (g|u) = gate|up(RMSNorm(s) * gamma)
+ * by rmsnorm_add_quantize_e4m3, qg_ffn_up_e4m3 and qgemm_e4m3 (QG_EPI_RESIDUAL_ADD).
+ *   x, residual, y: device f32 or bf16 (dtype) [m][hidden]; gamma [hidden].
+ *   residual NULL: s = x.  y receives s before the last launch reads it, and may
+ *   be x or residual itself.
+ *   wgu, wgu_d: as qg_ffn_up_e4m3 (k = hidden); wdn, wdn_d: weights [hidden][ffn]
+ *   xq, xd, hq, hd: caller-owned work buffers uint8[m][hidden],
+ *   f32[m][ceil(hidden/128)], uint8[m][ffn], f32[m][ceil(ffn/128)]
+ *   hidden and ffn multiples of 16, hidden <= 65536, ffn <= 2^20.
+ */
+QG_API qg_status qg_ffn_e4m3(const void *x, const void *residual, const void *gamma, int dtype, int64_t m,
+                             int64_t hidden, int64_t ffn, float eps, const uint8_t *wgu, const float *wgu_d,
+                             const uint8_t *wdn, const float *wdn_d, uint8_t *xq, float *xd, uint8_t *hq, float *hd,
+                             void *y, qg_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
