@@ -21,7 +21,8 @@ def __getattr__(name):
     if name in _API_NAMES:
         from . import api
 
-        return getattr(api, name)
+        value = globals()[name] = getattr(api, name)  # found here from now on
+        return value
     raise AttributeError(name)
 
 

@@ -76,6 +76,10 @@ cudaError_t launch_rows_e4m3(const uint8_t *, const float *, int64_t, int64_t, c
                              const void *, void *, int, cudaStream_t);
 cudaError_t launch_rows_up_e4m3(const uint8_t *, const float *, int64_t, int64_t, const uint8_t *, const float *,
                                 int64_t, uint8_t *, float *, cudaStream_t);
+cudaError_t launch_tiles_e4m3(const uint8_t *, const float *, int64_t, int64_t, const uint8_t *, const float *, int64_t,
+                              const void *, void *, int, cudaStream_t);
+cudaError_t launch_tiles_up_e4m3(const uint8_t *, const float *, int64_t, int64_t, const uint8_t *, const float *,
+                                 int64_t, uint8_t *, float *, cudaStream_t);
 
 // SM count of the current device, read once per device.
 int num_sms()
@@ -140,6 +144,7 @@ qg_status check_q8_k(int64_t k)
 
 // 8-bit floating point path
 constexpr int64_t kE4M3MaxM = int64_t(1) << 24;
+constexpr int64_t kE4M3FewRows = 16;  // activation rows that the few-row kernel takes
 
 int64_t e4m3_kb(int64_t k) { return (k + 127) / 128; }
 bool dtype_ok(int t) { return t == QG_F32 || t == QG_BF16; }
@@ -700,6 +705,8 @@ qg_status qgemm_e4m3(const uint8_t *w, const float *wd, int64_t n_rows, int64_t 
                in[] = {{w, n_rows * k}, {wd, e4m3_kb(n_rows) * kb * 4},
                        {xq, m * k}, {xd, m * kb * 4}, {residual == y ? nullptr : residual, yb}};
     if (any_overlap(out, in)) return QG_ERR_SHAPE;
+    if (m > kE4M3FewRows)
+        return from_cuda(qg::launch_tiles_e4m3(w, wd, n_rows, k, xq, xd, m, residual, y, y_dtype, stream));
     return from_cuda(qg::launch_rows_e4m3(w, wd, n_rows, k, xq, xd, m, residual, y, y_dtype, stream));
 }
 
@@ -719,6 +726,7 @@ qg_status qg_ffn_up_e4m3(const uint8_t *w, const float *wd, int64_t ffn, int64_t
                in[] = {{w, (2 * ffn) * k}, {wd, 2 * e4m3_kb(ffn) * kb * 4},
                        {xq, m * k}, {xd, m * kb * 4}};
     if (any_overlap(out, in)) return QG_ERR_SHAPE;
+    if (m > kE4M3FewRows) return from_cuda(qg::launch_tiles_up_e4m3(w, wd, ffn, k, xq, xd, m, hq, hd, stream));
     return from_cuda(qg::launch_rows_up_e4m3(w, wd, ffn, k, xq, xd, m, hq, hd, stream));
 }
 

@@ -1,4 +1,4 @@
-// The block-scaled e4m3 product for a few activation rows: the weights are read
+// The block-scaled e4m3 product for up to 16 activation rows: the weights are read
 // once, straight into the fragments of mma.sync m16n8k32.
 //
 //   y[m][n] = sum_b (d_x[m][b] d_w[n/128][b]) S_b[m][n],  S_b = sum of x w over block b
@@ -51,7 +51,7 @@ __device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1
 
 __device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
-// NT: groups of 8 activation rows.
+// NT: groups of 8 activation rows; m <= 8 NT.
 template <int NT, bool UP>
 __global__ void __launch_bounds__(RW * 32) rows_e4m3_kernel(const RowsArgs p)
 {
@@ -78,126 +78,123 @@ __global__ void __launch_bounds__(RW * 32) rows_e4m3_kernel(const RowsArgs p)
     pdl_wait();
     pdl_trigger();
 
-    for (int64_t m0 = static_cast<int64_t>(blockIdx.y) * (NT * 8); m0 < p.m; m0 += static_cast<int64_t>(gridDim.y) * (NT * 8)) {
-        const uint8_t *xr[NT];
-        const float *xd[NT][2];
+    const uint8_t *xr[NT];
+    const float *xd[NT][2];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            const int64_t row = m0 + 8 * j + g;
-            xr[j] = row < p.m ? p.x + row * p.k : nullptr;
+    for (int j = 0; j < NT; ++j) {
+        const int64_t row = 8 * j + g;
+        xr[j] = row < p.m ? p.x + row * p.k : nullptr;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int64_t r2 = m0 + 8 * j + 2 * c + h;
-                xd[j][h] = r2 < p.m ? p.xd + r2 * p.kb : nullptr;
-            }
+        for (int h = 0; h < 2; ++h) {
+            const int64_t r2 = 8 * j + 2 * c + h;
+            xd[j][h] = r2 < p.m ? p.xd + r2 * p.kb : nullptr;
         }
-        float acc[RT][NT][4];
+    }
+    float acc[RT][NT][4];
 #pragma unroll
-        for (int t = 0; t < RT; ++t)
+    for (int t = 0; t < RT; ++t)
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
+        for (int j = 0; j < NT; ++j)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[t][j][i] = 0.0f;
+            for (int i = 0; i < 4; ++i) acc[t][j][i] = 0.0f;
 
-        for (int b0 = warp; b0 < p.kb; b0 += RW * U) {
-            uint4 wv[U][RT][2][2], xv[U][NT][2];
-            float sw[U][RT], sx[U][NT][2];
+    for (int b0 = warp; b0 < p.kb; b0 += RW * U) {
+        uint4 wv[U][RT][2][2], xv[U][NT][2];
+        float sw[U][RT], sx[U][NT][2];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int b = b0 + u * RW;
-                const bool in = b < p.kb;
+        for (int u = 0; u < U; ++u) {
+            const int b = b0 + u * RW;
+            const bool in = b < p.kb;
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const int col = b * EB + 64 * q + 16 * c;
-                    const bool ok = in && col < p.k;
-#pragma unroll
-                    for (int t = 0; t < RT; ++t)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
-                            wv[u][t][h][q] = ok && wr[t][h] ? ld_stream_16B(wr[t][h] + col) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                    for (int j = 0; j < NT; ++j)
-                        xv[u][j][q] = ok && xr[j] ? ld_16B(xr[j] + col) : make_uint4(0, 0, 0, 0);
-                }
-#pragma unroll
-                for (int t = 0; t < RT; ++t) sw[u][t] = in ? wd[t][b] : 0.0f;
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) sx[u][j][h] = in && xd[j][h] ? xd[j][h][b] : 0.0f;
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (b0 + u * RW >= p.kb) break;
+            for (int q = 0; q < 2; ++q) {
+                const int col = b * EB + 64 * q + 16 * c;
+                const bool ok = in && col < p.k;
 #pragma unroll
                 for (int t = 0; t < RT; ++t)
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) {
-                        float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    for (int h = 0; h < 2; ++h)
+                        wv[u][t][h][q] = ok && wr[t][h] ? ld_stream_16B(wr[t][h] + col) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            const uint4 a = wv[u][t][0][q], a8 = wv[u][t][1][q], x = xv[u][j][q];
-                            mma_e4m3(d, a.x, a8.x, a.y, a8.y, x.x, x.y);
-                            mma_e4m3(d, a.z, a8.z, a.w, a8.w, x.z, x.w);
-                        }
-                        const float s0 = sx[u][j][0] * sw[u][t], s1 = sx[u][j][1] * sw[u][t];
-                        acc[t][j][0] = fmaf(d[0], s0, acc[t][j][0]);
-                        acc[t][j][1] = fmaf(d[1], s1, acc[t][j][1]);
-                        acc[t][j][2] = fmaf(d[2], s0, acc[t][j][2]);
-                        acc[t][j][3] = fmaf(d[3], s1, acc[t][j][3]);
-                    }
+                for (int j = 0; j < NT; ++j)
+                    xv[u][j][q] = ok && xr[j] ? ld_16B(xr[j] + col) : make_uint4(0, 0, 0, 0);
             }
-        }
-        // [activation row][weight row]: d[0], d[1] are row g of activations 2c, 2c + 1, d[2], d[3] row g + 8
 #pragma unroll
-        for (int t = 0; t < RT; ++t)
+            for (int t = 0; t < RT; ++t) sw[u][t] = in ? wd[t][b] : 0.0f;
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    red[warp][t][(8 * j + 2 * c + (i & 1)) * RR + g + 8 * (i >> 1)] = acc[t][j][i];
-        __syncthreads();
+                for (int h = 0; h < 2; ++h) sx[u][j][h] = in && xd[j][h] ? xd[j][h][b] : 0.0f;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (b0 + u * RW >= p.kb) break;
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const uint4 a = wv[u][t][0][q], a8 = wv[u][t][1][q], x = xv[u][j][q];
+                        mma_e4m3(d, a.x, a8.x, a.y, a8.y, x.x, x.y);
+                        mma_e4m3(d, a.z, a8.z, a.w, a8.w, x.z, x.w);
+                    }
+                    const float s0 = sx[u][j][0] * sw[u][t], s1 = sx[u][j][1] * sw[u][t];
+                    acc[t][j][0] = fmaf(d[0], s0, acc[t][j][0]);
+                    acc[t][j][1] = fmaf(d[1], s1, acc[t][j][1]);
+                    acc[t][j][2] = fmaf(d[2], s0, acc[t][j][2]);
+                    acc[t][j][3] = fmaf(d[3], s1, acc[t][j][3]);
+                }
+        }
+    }
+    // [activation row][weight row]: d[0], d[1] are row g of activations 2c, 2c + 1, d[2], d[3] row g + 8
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                red[warp][t][(8 * j + 2 * c + (i & 1)) * RR + g + 8 * (i >> 1)] = acc[t][j][i];
+    __syncthreads();
 
-        const int o = threadIdx.x;  // output: activation row o / 16, weight row o % 16
-        const int64_t row = m0 + o / RR, col = n0 + o % RR;
-        const bool mine = o < NT * 8 * RR, live = mine && row < p.m && col < p.n;
-        float v[RT];
+    const int o = threadIdx.x;  // output: activation row o / 16, weight row o % 16
+    const int64_t row = o / RR, col = n0 + o % RR;
+    const bool mine = o < NT * 8 * RR, live = mine && row < p.m && col < p.n;
+    float v[RT];
 #pragma unroll
-        for (int t = 0; t < RT; ++t) {
-            v[t] = mine ? red[0][t][o] : 0.0f;
+    for (int t = 0; t < RT; ++t) {
+        v[t] = mine ? red[0][t][o] : 0.0f;
 #pragma unroll
-            for (int w = 1; w < RW; ++w) v[t] += mine ? red[w][t][o] : 0.0f;
+        for (int w = 1; w < RW; ++w) v[t] += mine ? red[w][t][o] : 0.0f;
+    }
+    if constexpr (UP) {
+        const float h = silu_mul_e(v[0], v[RT - 1]);
+        float a = live ? fmaxf(fabsf(h), 0.0f) : 0.0f;
+#pragma unroll
+        for (int s = RR / 2; s >= 1; s >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, s));
+        if (mine && o % RR == 0) top[o / RR] = a;
+        cluster_sync();
+        if (mine) {
+            a = 0.0f;
+#pragma unroll
+            for (int r = 0; r < UP_CLUSTER; ++r) a = fmaxf(a, ld_cluster_f32(&top[o / RR], r));
         }
-        if constexpr (UP) {
-            const float h = silu_mul_e(v[0], v[RT - 1]);
-            float a = live ? fmaxf(fabsf(h), 0.0f) : 0.0f;
-#pragma unroll
-            for (int s = RR / 2; s >= 1; s >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, s));
-            if (mine && o % RR == 0) top[o / RR] = a;
-            cluster_sync();
-            if (mine) {
-                a = 0.0f;
-#pragma unroll
-                for (int r = 0; r < UP_CLUSTER; ++r) a = fmaxf(a, ld_cluster_f32(&top[o / RR], r));
-            }
-            a = e4m3_floor(a);
-            if (live) {
-                p.hq[row * p.n + col] = static_cast<uint8_t>(e4m3_pack2(h * __fdiv_rn(448.0f, a), 0.0f));
-                if (col % EB == 0) p.hd[row * e4m3_blocks(p.n) + col / EB] = __fdiv_rn(a, 448.0f);
-            }
-            cluster_sync();  // the others have read this CTA's maxima
-        } else if (live) {
-            const int64_t at = row * p.n + col;
-            if (p.y_bf16) {
-                const __nv_bfloat16 *res = static_cast<const __nv_bfloat16 *>(p.residual);
-                const float out = res ? v[0] + __bfloat162float(res[at]) : v[0];
-                static_cast<__nv_bfloat16 *>(p.y)[at] = __float2bfloat16_rn(out);
-            } else {
-                const float *res = static_cast<const float *>(p.residual);
-                static_cast<float *>(p.y)[at] = res ? v[0] + res[at] : v[0];
-            }
+        a = e4m3_floor(a);
+        if (live) {
+            p.hq[row * p.n + col] = static_cast<uint8_t>(e4m3_pack2(h * __fdiv_rn(448.0f, a), 0.0f));
+            if (col % EB == 0) p.hd[row * e4m3_blocks(p.n) + col / EB] = __fdiv_rn(a, 448.0f);
         }
-        __syncthreads();
+        cluster_sync();  // the others have read this CTA's maxima
+    } else if (live) {
+        const int64_t at = row * p.n + col;
+        if (p.y_bf16) {
+            const __nv_bfloat16 *res = static_cast<const __nv_bfloat16 *>(p.residual);
+            const float out = res ? v[0] + __bfloat162float(res[at]) : v[0];
+            static_cast<__nv_bfloat16 *>(p.y)[at] = __float2bfloat16_rn(out);
+        } else {
+            const float *res = static_cast<const float *>(p.residual);
+            static_cast<float *>(p.y)[at] = res ? v[0] + res[at] : v[0];
+        }
     }
 }
 
@@ -218,9 +215,7 @@ cudaError_t launch_rows_e4m3(const uint8_t *w, const float *wd, int64_t n, int64
     p.y_bf16 = y_dtype == QG_BF16;
     const unsigned gx = static_cast<unsigned>((n + RR - 1) / RR);
     if (m <= 8) return launch_pdl(rows_e4m3_kernel<1, false>, dim3(gx), dim3(RW * 32), 0, s, p);
-    const int64_t gy = (m + 15) / 16;
-    return launch_pdl(rows_e4m3_kernel<2, false>, dim3(gx, static_cast<unsigned>(gy < 65535 ? gy : 65535)),
-                      dim3(RW * 32), 0, s, p);
+    return launch_pdl(rows_e4m3_kernel<2, false>, dim3(gx), dim3(RW * 32), 0, s, p);
 }
 
 cudaError_t launch_rows_up_e4m3(const uint8_t *w, const float *wd, int64_t ffn, int64_t k, const uint8_t *x,
@@ -241,9 +236,7 @@ cudaError_t launch_rows_up_e4m3(const uint8_t *w, const float *wd, int64_t ffn, 
     p.hd = hd;
     const unsigned gx = static_cast<unsigned>(e4m3_blocks(ffn) * UP_CLUSTER);
     if (m <= 8) return launch_pdl_cluster(rows_e4m3_kernel<1, true>, dim3(gx), dim3(RW * 32), 0, s, UP_CLUSTER, p);
-    const int64_t gy = (m + 15) / 16;
-    return launch_pdl_cluster(rows_e4m3_kernel<2, true>, dim3(gx, static_cast<unsigned>(gy < 65535 ? gy : 65535)),
-                              dim3(RW * 32), 0, s, UP_CLUSTER, p);
+    return launch_pdl_cluster(rows_e4m3_kernel<2, true>, dim3(gx), dim3(RW * 32), 0, s, UP_CLUSTER, p);
 }
 
 }  // namespace qg

@@ -1,0 +1,636 @@
+// The block-scaled e4m3 product on tcgen05, for more rows than the few-row kernel
+// takes.
+//
+//   y[m][n] = sum_b (d_x[m][b] d_w[n/128][b]) S_b[m][n],  S_b = sum of x w over block b
+//
+// A tile is 128 activation rows (TMEM lanes) by BN weight rows (TMEM columns).  Per
+// block of 128, one thread copies the 128-byte wide slabs of both operands by TMA
+// (128-byte swizzle), one thread issues four tcgen05.mma kind::f8f6f4 (K = 32) into
+// one of two TMEM buffers, and eight epilogue warps bring the block sum into f32
+// registers: two warps per quarter of the lanes, each half of the columns, a thread
+// with one activation row.  A 32-column segment lies in one block of weight rows, so
+// its factor d_x d_w is one register and a value costs half a packed FMA.
+//
+// Gate|up: 128 gate rows and the 128 matching up rows make the 256 columns; a warp
+// takes 64 of each, so that SiLU(g) * u stays in its registers, and the two warps of
+// a quarter exchange their rows' largest magnitudes before the codes are written.
+//
+// Two forms.  tiles_e4m3_kernel walks the tiles with one CTA per SM.  Where there
+// are too few tiles for the SMs, split_e4m3_kernel puts a cluster on each tile: its
+// CTAs take consecutive parts of k, leave their sums in shared memory, and each adds
+// up (in rank order, through distributed shared memory) and finishes a share of the
+// rows.
+//
+// Every barrier wait is bounded by the global timer; a stalled pipeline aborts (NaN
+// outputs for the tiles left) instead of hanging.
+#include <cuda.h>
+
+#include "qg_e4m3.cuh"
+#include "qg_tc.cuh"
+
+namespace qg {
+
+constexpr int TM = 128;                // activation rows per tile
+constexpr int T_EW = 8;                // epilogue warps
+constexpr int T_TMA = 8, T_MMA = 9;    // copy and MMA warps
+constexpr int T_THREADS = 10 * 32;
+constexpr int T_XP = 33;               // row stride (floats) of a warp's 32 x 32 transpose buffer
+
+template <int BN>
+struct TileLayout {
+    static constexpr int A = TM * EB;
+    static constexpr int STAGE = A + BN * EB;
+    static constexpr int FIT = 196608 / STAGE;
+    static constexpr int STAGES = FIT < 8 ? FIT : 8;
+    static constexpr int SEG = BN / 64;                 // 32-column segments per epilogue warp
+    static constexpr int TMEM = BN == 192 ? 512 : 2 * BN;  // columns allocated: a power of two
+    static constexpr int XPOSE = T_EW * 32 * T_XP * 4;
+    static constexpr int UP_BYTES = STAGES * STAGE + 1024;  // + alignment of the base
+    static constexpr int BYTES = UP_BYTES + XPOSE;
+    static constexpr int LD = BN + 4;                   // row stride (floats) of a split tile's sums
+    static constexpr int SPLIT_BYTES = (STAGES * STAGE > TM * LD * 4 ? STAGES * STAGE : TM * LD * 4) + 1024;
+    static_assert(BYTES <= 227 * 1024 - 512 && SPLIT_BYTES <= 227 * 1024 - 512, "shared memory");
+};
+
+struct TileArgs {
+    const float *wd, *xd;
+    int64_t m, n;        // n: output columns
+    int64_t up_row, up_block;
+    int kb;
+    int64_t m_tiles, tiles;
+    int box_m;           // activation rows per copy
+    int split;
+    const void *residual;
+    void *y;
+    int y_bf16;
+    uint8_t *hq;
+    float *hd;
+};
+
+__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile("{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p; }" ::"r"(
+                     d_tmem),
+                 "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+
+struct TileBars {
+    uint64_t full[8], empty[8], tfull[2], tempty[2];
+    uint32_t tmem;
+    int abort_flag;
+};
+
+// First column (in the tile) of segment i of column group hf.
+template <int BN, bool UP>
+__device__ __forceinline__ constexpr int seg_col(int hf, int i)
+{
+    return UP ? (i >> 1) * 128 + 64 * hf + 32 * (i & 1) : (BN / 2) * hf + 32 * i;
+}
+
+template <int BN>
+__device__ __forceinline__ void tile_setup(TileBars &b, int warp)
+{
+    if (threadIdx.x == 0) {
+        b.abort_flag = 0;
+        for (int i = 0; i < TileLayout<BN>::STAGES; ++i) {
+            mbar_init(&b.full[i], 1);   // the copy thread's expect_tx
+            mbar_init(&b.empty[i], 1);  // the MMA thread's commit
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&b.tfull[i], 1);      // the MMA thread's commit
+            mbar_init(&b.tempty[i], T_EW);  // one arrival per epilogue warp
+        }
+    }
+    if (warp == T_MMA) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&b.tmem)),
+                     "r"(TileLayout<BN>::TMEM)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+}
+
+// Copies of blocks [kb0, kb1) of one tile; `it` counts blocks over all tiles.
+template <int BN, bool UP>
+__device__ __forceinline__ bool tile_copies(const CUtensorMap &tx, const CUtensorMap &tw, const TileArgs &p,
+                                            TileBars &b, uint8_t *smem, int m0, int64_t n0, int kb0, int kb1,
+                                            uint32_t &it)
+{
+    using L = TileLayout<BN>;
+    for (int kb = kb0; kb < kb1; ++kb, ++it) {
+        const uint32_t s = it % L::STAGES, use = it / L::STAGES;
+        if (!tc_wait(&b.empty[s], (use & 1) ^ 1, &b.abort_flag)) return false;
+        uint8_t *st = smem + s * L::STAGE;
+        mbar_expect_tx(&b.full[s], (p.box_m + BN) * EB);
+        tma_load_2d(st, &tx, kb * EB, m0, &b.full[s]);
+        if constexpr (UP) {
+            tma_load_2d(st + L::A, &tw, kb * EB, static_cast<int>(n0), &b.full[s]);
+            tma_load_2d(st + L::A + 128 * EB, &tw, kb * EB, static_cast<int>(p.up_row + n0), &b.full[s]);
+        } else {
+            tma_load_2d(st + L::A, &tw, kb * EB, static_cast<int>(n0), &b.full[s]);
+        }
+    }
+    return true;
+}
+
+// The MMAs of one tile's blocks, each into its own TMEM buffer.
+template <int BN>
+__device__ __forceinline__ bool tile_mmas(TileBars &b, uint8_t *smem, int blocks, uint32_t &it)
+{
+    using L = TileLayout<BN>;
+    // D f32, A and B e4m3, both K-major
+    constexpr uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(BN >> 3) << 17) | (static_cast<uint32_t>(TM >> 4) << 24);
+    for (int i = 0; i < blocks; ++i, ++it) {
+        const uint32_t s = it % L::STAGES, use = it / L::STAGES, t = it & 1, tuse = it >> 1;
+        if (!tc_wait(&b.full[s], use & 1, &b.abort_flag)) return false;
+        if (!tc_wait(&b.tempty[t], (tuse & 1) ^ 1, &b.abort_flag)) return false;
+        tc_fence_after();
+        const uint32_t a = smem_addr(smem + s * L::STAGE), w = a + L::A;
+#pragma unroll
+        for (int k = 0; k < EB / 32; ++k)
+            umma_f8(b.tmem + t * BN, umma_desc_sw128(a + 32 * k), umma_desc_sw128(w + 32 * k), idesc, k != 0);
+        umma_commit(&b.empty[s]);
+        umma_commit(&b.tfull[t]);
+    }
+    return true;
+}
+
+// The sums of blocks [kb0, kb1) of one tile in registers: 32 columns of this
+// thread's row per segment, in adjacent pairs.
+template <int BN, bool UP>
+__device__ __forceinline__ bool tile_sums(const TileArgs &p, TileBars &b, int q, int hf, int lane, int64_t m0,
+                                          int64_t n0, int kb0, int kb1, uint32_t &it,
+                                          uint64_t (&acc)[TileLayout<BN>::SEG][16])
+{
+    constexpr int SEG = TileLayout<BN>::SEG;
+    const int64_t row = min(m0 + 32 * q + lane, p.m - 1);
+    const float *xd = p.xd + row * p.kb;
+    const float *wd[SEG];
+#pragma unroll
+    for (int i = 0; i < SEG; ++i) {
+        const int c = seg_col<BN, UP>(hf, i);
+        const int64_t blk = UP ? (i >> 1) * p.up_block + n0 / EB : min(n0 + c, p.n - 1) / EB;
+        wd[i] = p.wd + blk * p.kb;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) acc[i][j] = 0;
+    }
+    float xn = xd[kb0], wn[SEG];
+#pragma unroll
+    for (int i = 0; i < SEG; ++i) wn[i] = wd[i][kb0];
+    for (int kb = kb0; kb < kb1; ++kb, ++it) {
+        uint64_t f[SEG];
+#pragma unroll
+        for (int i = 0; i < SEG; ++i) {
+            const float v = xn * wn[i];
+            f[i] = pack2(v, v);
+        }
+        if (kb + 1 < kb1) {  // the next block's factors arrive behind this block's work
+            xn = xd[kb + 1];
+#pragma unroll
+            for (int i = 0; i < SEG; ++i) wn[i] = wd[i][kb + 1];
+        }
+        const uint32_t t = it & 1, tuse = it >> 1;
+        // tcgen05.ld is warp-collective: the whole warp proceeds or stops
+        if (!__all_sync(0xffffffffu, tc_wait(&b.tfull[t], tuse & 1, &b.abort_flag))) return false;
+        tc_fence_after();
+        const uint32_t ta = b.tmem + (static_cast<uint32_t>(32 * q) << 16) + t * BN;
+        uint32_t v[2][32];
+        tmem_ld_32(ta + seg_col<BN, UP>(hf, 0), v[0]);
+#pragma unroll
+        for (int i = 0; i < SEG; ++i) {
+            uint32_t *u = v[i & 1];
+            tmem_ld_wait_regs(u, u + 16);
+            if (i + 1 < SEG) {
+                tmem_ld_32(ta + seg_col<BN, UP>(hf, i + 1), v[(i + 1) & 1]);
+            } else {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&b.tempty[t]);
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j) acc[i][j] = fma2(pack2u(u[2 * j], u[2 * j + 1]), f[i], acc[i][j]);
+        }
+    }
+    return true;
+}
+
+__device__ __forceinline__ float load_y(const void *p, int64_t at, int bf16)
+{
+    return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[at]) : static_cast<const float *>(p)[at];
+}
+
+// ---------------------------------------------------------------------------
+// one CTA per SM over all tiles
+// ---------------------------------------------------------------------------
+// A 32 x 32 block of y from the warp's transpose buffer, 128 (f32) or 64 bytes of a
+// row at a time.
+__device__ __forceinline__ void store_block(const TileArgs &p, const float *xp, int64_t r0, int64_t c0, int lane)
+{
+    if (p.y_bf16 && (p.n & 1) == 0) {
+        const int64_t col = c0 + 2 * (lane & 15);
+        if (col >= p.n) return;
+#pragma unroll 8
+        for (int r = 0; r < 32; r += 2) {
+            const int rr = r + (lane >> 4);
+            if (r0 + rr >= p.m) break;
+            const int64_t at = (r0 + rr) * p.n + col;
+            float2 v = make_float2(xp[rr * T_XP + 2 * (lane & 15)], xp[rr * T_XP + 2 * (lane & 15) + 1]);
+            if (p.residual) {
+                const float2 e = __bfloat1622float2(
+                    *reinterpret_cast<const __nv_bfloat162 *>(static_cast<const __nv_bfloat16 *>(p.residual) + at));
+                v.x += e.x;
+                v.y += e.y;
+            }
+            *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(p.y) + at) = __floats2bfloat162_rn(v.x, v.y);
+        }
+        return;
+    }
+    const int64_t col = c0 + lane;
+    if (col >= p.n) return;
+#pragma unroll 8
+    for (int r = 0; r < 32; ++r) {
+        if (r0 + r >= p.m) break;
+        const int64_t at = (r0 + r) * p.n + col;
+        float v = xp[r * T_XP + lane];
+        if (p.residual) v += load_y(p.residual, at, p.y_bf16);
+        if (p.y_bf16)
+            static_cast<__nv_bfloat16 *>(p.y)[at] = __float2bfloat16_rn(v);
+        else
+            static_cast<float *>(p.y)[at] = v;
+    }
+}
+
+template <int BN, bool UP>
+__global__ void __launch_bounds__(T_THREADS, 1)
+    tiles_e4m3_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tw, const TileArgs p)
+{
+    using L = TileLayout<BN>;
+    constexpr int BO = UP ? 128 : BN;  // output columns per tile
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) TileBars b;
+    __shared__ float top[2][2][TM];  // [tile parity][column group][row]
+    uint8_t *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    tile_setup<BN>(b, warp);
+    pdl_trigger();
+    pdl_wait();  // the activations come from the previous kernel
+
+    uint32_t it = 0;
+    bool ok = true;
+    if (warp == T_TMA) {
+        if (lane == 0) {
+            for (int64_t tile = blockIdx.x; ok && tile < p.tiles; tile += gridDim.x)
+                ok = tile_copies<BN, UP>(tx, tw, p, b, smem, static_cast<int>((tile % p.m_tiles) * TM),
+                                         (tile / p.m_tiles) * BO, 0, p.kb, it);
+            // After an abort the last copies may still be landing: let them finish
+            // (bounded) before the CTA's shared memory goes away.
+            if (!ok && it > 0) mbar_wait_bounded(&b.full[(it - 1) % L::STAGES], ((it - 1) / L::STAGES) & 1, kCopyWaitLimitNs);
+        }
+        __syncwarp();
+    } else if (warp == T_MMA) {
+        if (lane == 0) {
+            for (int64_t tile = blockIdx.x; ok && tile < p.tiles; tile += gridDim.x) ok = tile_mmas<BN>(b, smem, p.kb, it);
+            // After an abort, wait (bounded) for the last issued MMAs before TMEM is freed.
+            if (!ok && it > 0) mbar_wait_bounded(&b.tfull[(it - 1) & 1], ((it - 1) >> 1) & 1, kCopyWaitLimitNs);
+        }
+        __syncwarp();
+    } else {
+        const int q = warp & 3, hf = warp >> 2;
+        float *xp = reinterpret_cast<float *>(smem + L::STAGES * L::STAGE) + warp * 32 * T_XP;
+        uint32_t parity = 0;
+        for (int64_t tile = blockIdx.x; tile < p.tiles; tile += gridDim.x, parity ^= 1) {
+            const int64_t m0 = (tile % p.m_tiles) * TM, n0 = (tile / p.m_tiles) * BO;
+            uint64_t acc[L::SEG][16];
+            ok = ok && tile_sums<BN, UP>(p, b, q, hf, lane, m0, n0, 0, p.kb, it, acc);
+            if (!ok) {
+#pragma unroll
+                for (int i = 0; i < L::SEG; ++i)
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) acc[i][j] = pack2(__int_as_float(0x7fc00000), __int_as_float(0x7fc00000));
+            }
+            if constexpr (UP) {
+                // 64 values of h, in place of the gate's sums
+                const int64_t row = m0 + 32 * q + lane, c0 = n0 + 64 * hf;
+                float a = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const float2 g = unpack2(acc[i][j]), u = unpack2(acc[i + 2][j]);
+                        const float h0 = silu_mul_e(g.x, u.x), h1 = silu_mul_e(g.y, u.y);
+                        if (c0 + 32 * i + 2 * j < p.n) a = fmaxf(a, fmaxf(fabsf(h0), fabsf(h1)));
+                        acc[i][j] = pack2(h0, h1);
+                    }
+                top[parity][hf][32 * q + lane] = a;
+                asm volatile("bar.sync %0, 64;" ::"r"(1 + q) : "memory");
+                a = e4m3_floor(fmaxf(a, top[parity][hf ^ 1][32 * q + lane]));
+                const float f = __fdiv_rn(448.0f, a);
+                if (row < p.m) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {  // 16 codes each
+                        uint32_t w[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float2 h0 = unpack2(acc[i >> 1][8 * (i & 1) + 2 * j]);
+                            const float2 h1 = unpack2(acc[i >> 1][8 * (i & 1) + 2 * j + 1]);
+                            w[j] = e4m3_pack4(h0.x * f, h0.y * f, h1.x * f, h1.y * f);
+                        }
+                        if (c0 + 16 * i < p.n)
+                            *reinterpret_cast<uint4 *>(p.hq + row * p.n + c0 + 16 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                    if (hf == 0)
+                        p.hd[row * e4m3_blocks(p.n) + n0 / EB] = ok ? __fdiv_rn(a, 448.0f) : __int_as_float(0x7fc00000);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < L::SEG; ++i) {
+                    // lane l holds row l: turned around in shared memory (row stride
+                    // 33 floats, free of conflicts both ways)
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const float2 v = unpack2(acc[i][j]);
+                        xp[lane * T_XP + 2 * j] = v.x;
+                        xp[lane * T_XP + 2 * j + 1] = v.y;
+                    }
+                    __syncwarp();
+                    store_block(p, xp, m0 + 32 * q, n0 + seg_col<BN, UP>(hf, i), lane);
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == T_MMA) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(b.tmem), "r"(L::TMEM) : "memory");
+    }
+}
+
+// ---------------------------------------------------------------------------
+// one cluster per tile, its CTAs sharing k
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ float4 ld_cluster_f32x4(const float *local, uint32_t rank)
+{
+    uint32_t remote;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_addr(local)), "r"(rank));
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(remote)
+                 : "memory");
+    return v;
+}
+
+// Four neighbouring sums of the tile over the cluster's CTAs, in rank order.
+__device__ __forceinline__ float4 cluster_sum4(const float *at, int split)
+{
+    float4 v = ld_cluster_f32x4(at, 0);
+    for (int r = 1; r < split; ++r) {
+        const float4 e = ld_cluster_f32x4(at, r);
+        v = make_float4(v.x + e.x, v.y + e.y, v.z + e.z, v.w + e.w);
+    }
+    return v;
+}
+
+template <int BN, bool UP>
+__global__ void __launch_bounds__(T_THREADS, 1)
+    split_e4m3_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tw, const TileArgs p)
+{
+    using L = TileLayout<BN>;
+    constexpr int BO = UP ? 128 : BN;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) TileBars b;
+    uint8_t *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = static_cast<int>(cluster_ctarank());
+    const int64_t tile = blockIdx.x / p.split;
+    const int64_t m0 = (tile % p.m_tiles) * TM, n0 = (tile / p.m_tiles) * BO;
+    const int kb0 = static_cast<int>(static_cast<int64_t>(rank) * p.kb / p.split);
+    const int kb1 = static_cast<int>(static_cast<int64_t>(rank + 1) * p.kb / p.split);
+    tile_setup<BN>(b, warp);
+    pdl_trigger();
+    pdl_wait();
+
+    const int q = warp & 3, hf = warp >> 2;
+    uint32_t it = 0;
+    bool ok = true;
+    uint64_t acc[L::SEG][16];
+    if (warp == T_TMA) {
+        if (lane == 0) {
+            ok = tile_copies<BN, UP>(tx, tw, p, b, smem, static_cast<int>(m0), n0, kb0, kb1, it);
+            if (!ok && it > 0) mbar_wait_bounded(&b.full[(it - 1) % L::STAGES], ((it - 1) / L::STAGES) & 1, kCopyWaitLimitNs);
+        }
+        __syncwarp();
+    } else if (warp == T_MMA) {
+        if (lane == 0) {
+            ok = tile_mmas<BN>(b, smem, kb1 - kb0, it);
+            if (!ok && it > 0) mbar_wait_bounded(&b.tfull[(it - 1) & 1], ((it - 1) >> 1) & 1, kCopyWaitLimitNs);
+        }
+        __syncwarp();
+    } else {
+        ok = tile_sums<BN, UP>(p, b, q, hf, lane, m0, n0, kb0, kb1, it, acc);
+    }
+    tc_fence_before();
+    __syncthreads();  // every copy has landed and every MMA is done: the stages are free
+    if (warp == T_MMA) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(b.tmem), "r"(L::TMEM) : "memory");
+    }
+    float *sums = reinterpret_cast<float *>(smem);  // [128][LD]
+    const int rows = static_cast<int>(min(p.m - m0, static_cast<int64_t>(TM)));
+    if (warp < T_EW && 32 * q + lane < rows) {
+        const float nan = __int_as_float(0x7fc00000);
+        float *r = sums + (32 * q + lane) * L::LD;
+#pragma unroll
+        for (int i = 0; i < L::SEG; ++i)
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+                const float2 v0 = unpack2(acc[i][j]), v1 = unpack2(acc[i][j + 1]);
+                *reinterpret_cast<float4 *>(r + seg_col<BN, UP>(hf, i) + 2 * j) =
+                    ok ? make_float4(v0.x, v0.y, v1.x, v1.y) : make_float4(nan, nan, nan, nan);
+            }
+    }
+    cluster_sync();
+
+    // this CTA's share of the rows
+    const int per = (rows + p.split - 1) / p.split;
+    const int r_end = min(rows, (rank + 1) * per);
+    if constexpr (UP) {
+        // a warp per row: four columns of both halves per lane, the row's block of h in the warp
+        for (int r = rank * per + warp; r < r_end; r += T_THREADS / 32) {
+            const float4 g = cluster_sum4(sums + r * L::LD + 4 * lane, p.split);
+            const float4 u = cluster_sum4(sums + r * L::LD + 128 + 4 * lane, p.split);
+            const bool live = n0 + 4 * lane < p.n;
+            float4 h = make_float4(silu_mul_e(g.x, u.x), silu_mul_e(g.y, u.y), silu_mul_e(g.z, u.z), silu_mul_e(g.w, u.w));
+            const bool bad = h.x != h.x && h.y != h.y && h.z != h.z && h.w != h.w;
+            const float a = e4m3_floor(warp_max_nonneg(live ? max_abs4(h) : 0.0f));
+            const float f = __fdiv_rn(448.0f, a);
+            const int64_t row = m0 + r;
+            if (live)
+                *reinterpret_cast<uint32_t *>(p.hq + row * p.n + n0 + 4 * lane) =
+                    e4m3_pack4(h.x * f, h.y * f, h.z * f, h.w * f);
+            if (lane == 0) p.hd[row * e4m3_blocks(p.n) + n0 / EB] = bad && a == 0x1p-100f ? h.x : __fdiv_rn(a, 448.0f);
+        }
+    } else {
+        constexpr int G = BN / 4;  // groups of four columns
+        const bool whole = (p.n & 3) == 0;
+        for (int i = threadIdx.x; i < (r_end - rank * per) * G; i += T_THREADS) {
+            const int r = rank * per + i / G, c = 4 * (i % G);
+            if (n0 + c >= p.n) continue;
+            const float4 s = cluster_sum4(sums + r * L::LD + c, p.split);
+            float v[4] = {s.x, s.y, s.z, s.w};
+            const int64_t at = (m0 + r) * p.n + n0 + c;
+            if (whole) {
+                if (p.y_bf16) {
+                    using V = Vec4<__nv_bfloat16>;
+                    float4 o = make_float4(v[0], v[1], v[2], v[3]);
+                    if (p.residual) {
+                        const float4 e = V::widen(*reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p.residual) + at));
+                        o = make_float4(o.x + e.x, o.y + e.y, o.z + e.z, o.w + e.w);
+                    }
+                    *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.y) + at) = V::narrow(o);
+                } else {
+                    float4 o = make_float4(v[0], v[1], v[2], v[3]);
+                    if (p.residual) {
+                        const float4 e = *reinterpret_cast<const float4 *>(static_cast<const float *>(p.residual) + at);
+                        o = make_float4(o.x + e.x, o.y + e.y, o.z + e.z, o.w + e.w);
+                    }
+                    *reinterpret_cast<float4 *>(static_cast<float *>(p.y) + at) = o;
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (n0 + c + e >= p.n) break;
+                    const float o = p.residual ? v[e] + load_y(p.residual, at + e, p.y_bf16) : v[e];
+                    if (p.y_bf16)
+                        static_cast<__nv_bfloat16 *>(p.y)[at + e] = __float2bfloat16_rn(o);
+                    else
+                        static_cast<float *>(p.y)[at + e] = o;
+                }
+            }
+        }
+    }
+    cluster_sync();  // the others have read this CTA's sums
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+static cudaError_t e4m3_map(EncodeTiledFn enc, CUtensorMap *map, const uint8_t *base, int64_t rows, int64_t k, int box)
+{
+    const cuuint64_t dim[2] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t stride[1] = {static_cast<cuuint64_t>(k)};
+    const cuuint32_t size[2] = {EB, static_cast<cuuint32_t>(box)};
+    const cuuint32_t estride[2] = {1, 1};
+    if (enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(base), dim, stride, size, estride,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    return cudaSuccess;
+}
+
+// The operands' maps and the tile counts of BN-wide tiles.
+template <int BN, bool UP>
+static cudaError_t tile_maps(const uint8_t *w, int64_t w_rows, int64_t k, const uint8_t *x, TileArgs &p,
+                             CUtensorMap &tx, CUtensorMap &tw)
+{
+    EncodeTiledFn enc = encode_tiled();
+    if (!enc) return cudaErrorNotSupported;
+    constexpr int BO = UP ? 128 : BN;
+    p.box_m = static_cast<int>(p.m >= TM ? TM : (p.m + 7) / 8 * 8);
+    p.m_tiles = (p.m + TM - 1) / TM;
+    p.tiles = p.m_tiles * ((p.n + BO - 1) / BO);
+    if (cudaError_t e = e4m3_map(enc, &tx, x, p.m, k, p.box_m); e != cudaSuccess) return e;
+    return e4m3_map(enc, &tw, w, w_rows, k, UP ? 128 : BN);
+}
+
+template <int BN, bool UP>
+static cudaError_t launch_tiles(const uint8_t *w, int64_t w_rows, int64_t k, const uint8_t *x, TileArgs p, cudaStream_t s)
+{
+    using L = TileLayout<BN>;
+    CUtensorMap tx, tw;
+    if (cudaError_t e = tile_maps<BN, UP>(w, w_rows, k, x, p, tx, tw); e != cudaSuccess) return e;
+    constexpr int bytes = UP ? L::UP_BYTES : L::BYTES;
+    if (cudaError_t e = opt_in_smem(reinterpret_cast<const void *>(tiles_e4m3_kernel<BN, UP>), bytes); e != cudaSuccess)
+        return e;
+    const int64_t grid = p.tiles < num_sms() ? p.tiles : num_sms();
+    return launch_pdl(tiles_e4m3_kernel<BN, UP>, dim3(static_cast<unsigned>(grid)), dim3(T_THREADS),
+                      static_cast<size_t>(bytes), s, tx, tw, p);
+}
+
+template <int BN, bool UP>
+static cudaError_t launch_split(const uint8_t *w, int64_t w_rows, int64_t k, const uint8_t *x, TileArgs p, int split,
+                                cudaStream_t s)
+{
+    using L = TileLayout<BN>;
+    CUtensorMap tx, tw;
+    p.split = split;
+    if (cudaError_t e = tile_maps<BN, UP>(w, w_rows, k, x, p, tx, tw); e != cudaSuccess) return e;
+    if (cudaError_t e = opt_in_smem(reinterpret_cast<const void *>(split_e4m3_kernel<BN, UP>), L::SPLIT_BYTES);
+        e != cudaSuccess)
+        return e;
+    return launch_pdl_cluster(split_e4m3_kernel<BN, UP>, dim3(static_cast<unsigned>(p.tiles * split)), dim3(T_THREADS),
+                              static_cast<size_t>(L::SPLIT_BYTES), s, static_cast<unsigned>(split), tx, tw, p);
+}
+
+// CTAs per tile: a power of two up to 8 that leaves each a block of k and does not
+// pass the SM count.
+static int split_of(int64_t tiles, int64_t kb)
+{
+    int split = 1;
+    while (split < 8 && 2 * split <= kb && tiles * split * 2 <= num_sms()) split *= 2;
+    return split;
+}
+
+cudaError_t launch_tiles_e4m3(const uint8_t *w, const float *wd, int64_t n, int64_t k, const uint8_t *x,
+                              const float *xd, int64_t m, const void *residual, void *y, int y_dtype, cudaStream_t s)
+{
+    TileArgs p = {};
+    p.wd = wd;
+    p.xd = xd;
+    p.m = m;
+    p.n = n;
+    p.kb = static_cast<int>(e4m3_blocks(k));
+    p.residual = residual;
+    p.y = y;
+    p.y_bf16 = y_dtype == QG_BF16;
+    const int64_t sms = num_sms(), mt = (m + TM - 1) / TM;
+    if (const int64_t t = mt * ((n + 63) / 64); t <= sms)
+        return launch_split<64, false>(w, n, k, x, p, split_of(t, p.kb), s);
+    if (const int64_t t = mt * ((n + 127) / 128); t <= sms)
+        return launch_split<128, false>(w, n, k, x, p, split_of(t, p.kb), s);
+    // the tile width whose busiest SM covers the fewest columns
+    int best = 256;
+    int64_t cost = INT64_MAX;
+    for (int bn : {256, 192, 128}) {
+        const int64_t c = (mt * ((n + bn - 1) / bn) + sms - 1) / sms * bn;
+        if (c < cost) cost = c, best = bn;
+    }
+    if (best == 256) return launch_tiles<256, false>(w, n, k, x, p, s);
+    if (best == 192) return launch_tiles<192, false>(w, n, k, x, p, s);
+    return launch_tiles<128, false>(w, n, k, x, p, s);
+}
+
+cudaError_t launch_tiles_up_e4m3(const uint8_t *w, const float *wd, int64_t ffn, int64_t k, const uint8_t *x,
+                                 const float *xd, int64_t m, uint8_t *hq, float *hd, cudaStream_t s)
+{
+    TileArgs p = {};
+    p.wd = wd;
+    p.xd = xd;
+    p.m = m;
+    p.n = ffn;
+    p.up_row = ffn;
+    p.up_block = e4m3_blocks(ffn);
+    p.kb = static_cast<int>(e4m3_blocks(k));
+    p.hq = hq;
+    p.hd = hd;
+    const int64_t tiles = (m + TM - 1) / TM * e4m3_blocks(ffn);
+    if (tiles <= num_sms()) return launch_split<256, true>(w, 2 * ffn, k, x, p, split_of(tiles, p.kb), s);
+    return launch_tiles<256, true>(w, 2 * ffn, k, x, p, s);
+}
+
+}  // namespace qg

@@ -220,6 +220,13 @@ def test_product_many_tiles(torch, qg):
     check_product(torch, qg, np.random.default_rng(6), 17, 5001, 1040, "f32", None)
 
 
+# tiles walked by one CTA per SM: 256, 192 and 128 columns wide
+@pytest.mark.parametrize("m,n,kind", [(4800, 1024, "bf16"), (2600, 999, "f32"), (2601, 1000, "bf16"), (5100, 1400, "bf16"),
+                                      (5100, 1401, "bf16")])
+def test_product_prompts(torch, qg, m, n, kind):
+    check_product(torch, qg, np.random.default_rng(n), m, n, 272, kind, "place" if n % 2 else None)
+
+
 def test_product_largest_codes(torch, qg):
     """Every code 448 or -448: the largest block sums; exact in f32 where they do not cancel."""
     for m in (3, 140):
@@ -302,6 +309,11 @@ def test_up_columns(torch, qg, m, f):
 @pytest.mark.parametrize("k", [16, 112, 128, 144, 1024, 2560, 4112])
 def test_up_depths(torch, qg, m, k):
     check_up(torch, qg, np.random.default_rng(k), m, 144, k)
+
+
+@pytest.mark.parametrize("m,f,k", [(2500, 1040, 272), (2433, 1072, 656)])
+def test_up_prompts(torch, qg, m, f, k):
+    check_up(torch, qg, np.random.default_rng(f), m, f, k)
 
 
 def test_up_large_arguments(torch, qg):
