@@ -78,13 +78,38 @@ __device__ __forceinline__ float max_abs4(float4 v)
     return fmaxf(fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))), 0.0f);
 }
 
-// SiLU(g) * u to a few f32 ulp over the whole range: e = e^-|g| in (0, 1] never
-// overflows, silu(g) = g / (1 + e) for g >= 0 and (g e) / (1 + e) below.
+// SiLU(g) * u to a few f32 ulp over the whole range.  t = e^(-|g|/2) lies in (0, 1]
+// and does not underflow before |g| = 170, where t^2 has long left f32's range; with
+// t^2 = e^-|g|, silu(g) = g / (1 + t^2) for g >= 0 and (g t) t / (1 + t^2) below.
+// The exponent -|g| log2(e) / 2 is carried as a rounded product and its remainder
+// (an FMA, and the constant's own second part), so that the error of t does not grow
+// with |g|: 2^t's approximation is all that is left of it.
+constexpr float kHalfLog2e = -0.72134752044448f;     // -log2(e) / 2 rounded to f32
+constexpr float kHalfLog2eRest = -9.629815e-9f;      // and what that leaves
+constexpr float kLn2 = 0.693147181f;
+
+__device__ __forceinline__ float ex2_approx(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp_approx(float x)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 __device__ __forceinline__ float silu_mul_e(float g, float u)
 {
-    const float e = expf(-fabsf(g));
-    const float num = g >= 0.0f ? g : g * e;
-    return __fdividef(num, 1.0f + e) * u;
+    const float a = fminf(fabsf(g), 170.0f);
+    const float hi = a * kHalfLog2e;
+    const float lo = fmaf(a, kHalfLog2eRest, fmaf(a, kHalfLog2e, -hi));
+    float t = ex2_approx(hi);
+    t = fmaf(t, lo * kLn2, t);
+    const float num = g >= 0.0f ? g : (g * t) * t;
+    return num * rcp_approx(fmaf(t, t, 1.0f)) * u;
 }
 
 }  // namespace qg

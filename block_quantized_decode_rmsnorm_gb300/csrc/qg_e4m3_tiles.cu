@@ -6,13 +6,14 @@
 // A tile is 128 activation rows (TMEM lanes) by BN weight rows (TMEM columns).  Per
 // block of 128, one thread copies the 128-byte wide slabs of both operands by TMA
 // (128-byte swizzle), one thread issues four tcgen05.mma kind::f8f6f4 (K = 32) into
-// one of two TMEM buffers, and eight epilogue warps bring the block sum into f32
-// registers: two warps per quarter of the lanes, each half of the columns, a thread
-// with one activation row.  A 32-column segment lies in one block of weight rows, so
-// its factor d_x d_w is one register and a value costs half a packed FMA.
+// one of two TMEM buffers, and the epilogue warps bring the block sum into f32
+// registers: a warp takes a quarter of the lanes and 64 columns, a thread one
+// activation row of them.  Those lie in one block of weight rows, so the factor
+// d_x d_w is one register and a value costs half a packed FMA.  One more warp reads
+// the scales ahead, four blocks at a time, into shared memory.
 //
 // Gate|up: 128 gate rows and the 128 matching up rows make the 256 columns; a warp
-// takes 64 of each, so that SiLU(g) * u stays in its registers, and the two warps of
+// takes 32 of each, so that SiLU(g) * u stays in its registers, and the four warps of
 // a quarter exchange their rows' largest magnitudes before the codes are written.
 //
 // Two forms.  tiles_e4m3_kernel walks the tiles with one CTA per SM.  Where there
@@ -30,26 +31,27 @@
 
 namespace qg {
 
-constexpr int TM = 128;                // activation rows per tile
-constexpr int T_EW = 8;                // epilogue warps
-constexpr int T_TMA = 8, T_MMA = 9;    // copy and MMA warps
-constexpr int T_THREADS = 10 * 32;
-constexpr int T_XP = 33;               // row stride (floats) of a warp's 32 x 32 transpose buffer
+constexpr int TM = 128;    // activation rows per tile
+constexpr int T_CW = 64;   // tile columns per epilogue warp
+constexpr int T_XP = 9;    // row stride (floats) of a warp's 32 x 8 transpose buffer
+constexpr int T_SB = 4;    // blocks of k per buffer of scales
 
 template <int BN>
 struct TileLayout {
+    static constexpr int CG = BN / T_CW;  // column groups
+    static constexpr int EW = 4 * CG;     // epilogue warps: four lane quarters x column groups
+    static constexpr int TMA_WARP = EW, MMA_WARP = EW + 1, SCALE_WARP = EW + 2;
+    static constexpr int THREADS = (EW + 3) * 32;
     static constexpr int A = TM * EB;
     static constexpr int STAGE = A + BN * EB;
     static constexpr int FIT = 196608 / STAGE;
     static constexpr int STAGES = FIT < 8 ? FIT : 8;
-    static constexpr int SEG = BN / 64;                 // 32-column segments per epilogue warp
-    static constexpr int TMEM = BN == 192 ? 512 : 2 * BN;  // columns allocated: a power of two
-    static constexpr int XPOSE = T_EW * 32 * T_XP * 4;
+    static constexpr int TMEM = BN == 192 ? 512 : 2 * BN;   // columns allocated: a power of two
     static constexpr int UP_BYTES = STAGES * STAGE + 1024;  // + alignment of the base
-    static constexpr int BYTES = UP_BYTES + XPOSE;
-    static constexpr int LD = BN + 4;                   // row stride (floats) of a split tile's sums
+    static constexpr int BYTES = UP_BYTES + EW * 32 * T_XP * 4;
+    static constexpr int LD = BN + 4;                       // row stride (floats) of a split tile's sums
     static constexpr int SPLIT_BYTES = (STAGES * STAGE > TM * LD * 4 ? STAGES * STAGE : TM * LD * 4) + 1024;
-    static_assert(BYTES <= 227 * 1024 - 512 && SPLIT_BYTES <= 227 * 1024 - 512, "shared memory");
+    static_assert(BYTES <= 220 * 1024 && SPLIT_BYTES <= 220 * 1024, "shared memory");
 };
 
 struct TileArgs {
@@ -63,6 +65,7 @@ struct TileArgs {
     const void *residual;
     void *y;
     int y_bf16;
+    int rows32;          // every row of y (and of the residual) starts on 32 bytes
     uint8_t *hq;
     float *hd;
 };
@@ -75,36 +78,44 @@ __device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a, uint64_t b,
                  : "memory");
 }
 
-struct TileBars {
-    uint64_t full[8], empty[8], tfull[2], tempty[2];
+// Barriers, and the scales of T_SB blocks of k at a time, in two buffers: of the
+// tile's activation rows, and of the weight rows of each column group (gate|up: of
+// the gate and the up rows).
+struct TileShared {
+    uint64_t full[8], empty[8], tfull[2], tempty[2], sfull[2], sempty[2];
+    float sx[2][T_SB][TM];
+    float sw[2][4][T_SB];
     uint32_t tmem;
     int abort_flag;
 };
 
-// First column (in the tile) of segment i of column group hf.
-template <int BN, bool UP>
-__device__ __forceinline__ constexpr int seg_col(int hf, int i)
+// First column (in the tile) of half i (32 columns) of column group cg.
+template <bool UP>
+__device__ __forceinline__ constexpr int half_col(int cg, int i)
 {
-    return UP ? (i >> 1) * 128 + 64 * hf + 32 * (i & 1) : (BN / 2) * hf + 32 * i;
+    return UP ? 128 * i + 32 * cg : T_CW * cg + 32 * i;
 }
 
 template <int BN>
-__device__ __forceinline__ void tile_setup(TileBars &b, int warp)
+__device__ __forceinline__ void tile_setup(TileShared &b, int warp)
 {
+    using L = TileLayout<BN>;
     if (threadIdx.x == 0) {
         b.abort_flag = 0;
-        for (int i = 0; i < TileLayout<BN>::STAGES; ++i) {
+        for (int i = 0; i < L::STAGES; ++i) {
             mbar_init(&b.full[i], 1);   // the copy thread's expect_tx
             mbar_init(&b.empty[i], 1);  // the MMA thread's commit
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&b.tfull[i], 1);      // the MMA thread's commit
-            mbar_init(&b.tempty[i], T_EW);  // one arrival per epilogue warp
+            mbar_init(&b.tfull[i], 1);       // the MMA thread's commit
+            mbar_init(&b.tempty[i], L::EW);  // one arrival per epilogue warp
+            mbar_init(&b.sfull[i], 1);       // the scale warp
+            mbar_init(&b.sempty[i], L::EW);  // one arrival per epilogue warp
         }
     }
-    if (warp == T_MMA) {
+    if (warp == L::MMA_WARP) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&b.tmem)),
-                     "r"(TileLayout<BN>::TMEM)
+                     "r"(L::TMEM)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
@@ -116,7 +127,7 @@ __device__ __forceinline__ void tile_setup(TileBars &b, int warp)
 // Copies of blocks [kb0, kb1) of one tile; `it` counts blocks over all tiles.
 template <int BN, bool UP>
 __device__ __forceinline__ bool tile_copies(const CUtensorMap &tx, const CUtensorMap &tw, const TileArgs &p,
-                                            TileBars &b, uint8_t *smem, int m0, int64_t n0, int kb0, int kb1,
+                                            TileShared &b, uint8_t *smem, int m0, int64_t n0, int kb0, int kb1,
                                             uint32_t &it)
 {
     using L = TileLayout<BN>;
@@ -138,7 +149,7 @@ __device__ __forceinline__ bool tile_copies(const CUtensorMap &tx, const CUtenso
 
 // The MMAs of one tile's blocks, each into its own TMEM buffer.
 template <int BN>
-__device__ __forceinline__ bool tile_mmas(TileBars &b, uint8_t *smem, int blocks, uint32_t &it)
+__device__ __forceinline__ bool tile_mmas(TileShared &b, uint8_t *smem, int blocks, uint32_t &it)
 {
     using L = TileLayout<BN>;
     // D f32, A and B e4m3, both K-major
@@ -158,63 +169,117 @@ __device__ __forceinline__ bool tile_mmas(TileBars &b, uint8_t *smem, int blocks
     return true;
 }
 
-// The sums of blocks [kb0, kb1) of one tile in registers: 32 columns of this
-// thread's row per segment, in adjacent pairs.
+// The scale warp: the scales of blocks [kb0, kb1) of one tile, T_SB at a time, the
+// next ones on their way while the last are waited for.  `c` counts buffers.
 template <int BN, bool UP>
-__device__ __forceinline__ bool tile_sums(const TileArgs &p, TileBars &b, int q, int hf, int lane, int64_t m0,
-                                          int64_t n0, int kb0, int kb1, uint32_t &it,
-                                          uint64_t (&acc)[TileLayout<BN>::SEG][16])
+__device__ __forceinline__ bool tile_scales(const TileArgs &p, TileShared &b, int lane, int64_t m0, int64_t n0, int kb0,
+                                            int kb1, uint32_t &c)
 {
-    constexpr int SEG = TileLayout<BN>::SEG;
-    const int64_t row = min(m0 + 32 * q + lane, p.m - 1);
-    const float *xd = p.xd + row * p.kb;
-    const float *wd[SEG];
+    constexpr int GROUPS = UP ? 2 : TileLayout<BN>::CG;
+    const float *xr[TM / 32];
 #pragma unroll
-    for (int i = 0; i < SEG; ++i) {
-        const int c = seg_col<BN, UP>(hf, i);
-        const int64_t blk = UP ? (i >> 1) * p.up_block + n0 / EB : min(n0 + c, p.n - 1) / EB;
-        wd[i] = p.wd + blk * p.kb;
+    for (int i = 0; i < TM / 32; ++i) xr[i] = p.xd + min(m0 + 32 * i + lane, p.m - 1) * p.kb;
+    const int cg = lane / T_SB, o = lane % T_SB;  // this lane's weight scale: group and block
+    const int64_t blk = UP ? cg * p.up_block + n0 / EB : min(n0 + T_CW * cg, p.n - 1) / EB;
+    const float *wr = p.wd + (cg < GROUPS ? blk : 0) * p.kb;
+    const bool vec = (p.kb % 4 == 0) && (kb0 % 4 == 0) && (reinterpret_cast<uintptr_t>(p.xd) & 15) == 0;
+    for (int kb = kb0; kb < kb1; kb += T_SB, ++c) {
+        float4 x[TM / 32];
+#pragma unroll
+        for (int i = 0; i < TM / 32; ++i) {
+            if (vec) {
+                x[i] = *reinterpret_cast<const float4 *>(xr[i] + kb);  // kb % 4 == 0 and so is the row's length
+            } else {
+                x[i].x = xr[i][kb];
+                x[i].y = kb + 1 < kb1 ? xr[i][kb + 1] : 0.0f;
+                x[i].z = kb + 2 < kb1 ? xr[i][kb + 2] : 0.0f;
+                x[i].w = kb + 3 < kb1 ? xr[i][kb + 3] : 0.0f;
+            }
+        }
+        const float w = cg < GROUPS && kb + o < kb1 ? wr[kb + o] : 0.0f;
+        const uint32_t t = c & 1, use = c >> 1;
+        if (!__all_sync(0xffffffffu, tc_wait(&b.sempty[t], (use & 1) ^ 1, &b.abort_flag))) return false;
+#pragma unroll
+        for (int i = 0; i < TM / 32; ++i) {
+            float *sx = b.sx[t][0] + 32 * i + lane;
+            sx[0] = x[i].x;
+            sx[TM] = x[i].y;
+            sx[2 * TM] = x[i].z;
+            sx[3 * TM] = x[i].w;
+        }
+        if (cg < GROUPS) b.sw[t][cg][o] = w;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b.sfull[t]);
+    }
+    return true;
+}
+
+// The sums of blocks [kb0, kb1) of one tile in registers: two halves of 32 columns of
+// this thread's row, in adjacent pairs.  `it` counts blocks, `c` buffers of scales.
+template <int BN, bool UP>
+__device__ __forceinline__ bool tile_sums(TileShared &b, int q, int cg, int lane, int kb0, int kb1, uint32_t &it,
+                                          uint32_t &c, uint64_t (&acc)[2][16])
+{
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int j = 0; j < 16; ++j) acc[i][j] = 0;
-    }
-    float xn = xd[kb0], wn[SEG];
-#pragma unroll
-    for (int i = 0; i < SEG; ++i) wn[i] = wd[i][kb0];
-    for (int kb = kb0; kb < kb1; ++kb, ++it) {
-        uint64_t f[SEG];
-#pragma unroll
-        for (int i = 0; i < SEG; ++i) {
-            const float v = xn * wn[i];
-            f[i] = pack2(v, v);
-        }
-        if (kb + 1 < kb1) {  // the next block's factors arrive behind this block's work
-            xn = xd[kb + 1];
-#pragma unroll
-            for (int i = 0; i < SEG; ++i) wn[i] = wd[i][kb + 1];
-        }
-        const uint32_t t = it & 1, tuse = it >> 1;
-        // tcgen05.ld is warp-collective: the whole warp proceeds or stops
-        if (!__all_sync(0xffffffffu, tc_wait(&b.tfull[t], tuse & 1, &b.abort_flag))) return false;
-        tc_fence_after();
-        const uint32_t ta = b.tmem + (static_cast<uint32_t>(32 * q) << 16) + t * BN;
-        uint32_t v[2][32];
-        tmem_ld_32(ta + seg_col<BN, UP>(hf, 0), v[0]);
-#pragma unroll
-        for (int i = 0; i < SEG; ++i) {
-            uint32_t *u = v[i & 1];
-            tmem_ld_wait_regs(u, u + 16);
-            if (i + 1 < SEG) {
-                tmem_ld_32(ta + seg_col<BN, UP>(hf, i + 1), v[(i + 1) & 1]);
-            } else {
-                tc_fence_before();
+    for (int kb = kb0; kb < kb1; kb += T_SB, ++c) {
+        const uint32_t sb = c & 1, suse = c >> 1;
+        if (!__all_sync(0xffffffffu, tc_wait(&b.sfull[sb], suse & 1, &b.abort_flag))) return false;
+        const float *sx = b.sx[sb][0] + 32 * q + lane, *s0 = b.sw[sb][UP ? 0 : cg], *s1 = b.sw[sb][UP ? 1 : cg];
+#pragma unroll 1
+        for (int o = 0; o < T_SB; ++o) {
+            if (kb + o >= kb1) break;
+            const float f0 = sx[o * TM] * s0[o], f1 = UP ? sx[o * TM] * s1[o] : f0;
+            if (o == T_SB - 1 || kb + o + 1 == kb1) {  // the buffer's last: every lane has read it
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&b.tempty[t]);
+                if (lane == 0) mbar_arrive(&b.sempty[sb]);
             }
+            const uint32_t t = it & 1, tuse = it >> 1;
+            // tcgen05.ld is warp-collective: the whole warp proceeds or stops
+            if (!__all_sync(0xffffffffu, tc_wait(&b.tfull[t], tuse & 1, &b.abort_flag))) return false;
+            tc_fence_after();
+            const uint32_t ta = b.tmem + (static_cast<uint32_t>(32 * q) << 16) + t * BN;
 #pragma unroll
-            for (int j = 0; j < 16; ++j) acc[i][j] = fma2(pack2u(u[2 * j], u[2 * j + 1]), f[i], acc[i][j]);
+            for (int i = 0; i < 4; ++i) {
+                uint32_t v[16];
+                tmem_ld_16(ta + half_col<UP>(cg, i >> 1) + 16 * (i & 1), v);
+                tmem_ld_wait_regs16(v);
+                if (i == 3) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&b.tempty[t]);
+                }
+                const float f = i >> 1 ? f1 : f0;
+                const uint64_t ff = pack2(f, f);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    uint64_t &s = acc[i >> 1][8 * (i & 1) + j];
+                    s = fma2(pack2u(v[2 * j], v[2 * j + 1]), ff, s);
+                }
+            }
+            ++it;
         }
     }
     return true;
+}
+
+// silu_mul_e of two values, the products and FMAs packed.
+__device__ __forceinline__ uint64_t silu_mul2(uint64_t g2, uint64_t u2)
+{
+    const float2 g = unpack2(g2);
+    const uint64_t a = pack2(fminf(fabsf(g.x), 170.0f), fminf(fabsf(g.y), 170.0f));
+    const uint64_t c = pack2(kHalfLog2e, kHalfLog2e), cr = pack2(kHalfLog2eRest, kHalfLog2eRest);
+    const uint64_t one = pack2(1.0f, 1.0f), ln2 = pack2(kLn2, kLn2), minus = pack2(-1.0f, -1.0f);
+    const uint64_t hi = mul2(a, c);
+    const uint64_t lo = fma2(a, cr, fma2(a, c, mul2(hi, minus)));
+    const float2 h = unpack2(hi);
+    uint64_t t = pack2(ex2_approx(h.x), ex2_approx(h.y));
+    t = fma2(t, mul2(lo, ln2), t);
+    const float2 d = unpack2(fma2(t, t, one)), n = unpack2(mul2(mul2(g2, t), t));
+    const uint64_t num = pack2(g.x >= 0.0f ? g.x : n.x, g.y >= 0.0f ? g.y : n.y);
+    return mul2(mul2(num, pack2(rcp_approx(d.x), rcp_approx(d.y))), u2);
 }
 
 __device__ __forceinline__ float load_y(const void *p, int64_t at, int bf16)
@@ -225,62 +290,109 @@ __device__ __forceinline__ float load_y(const void *p, int64_t at, int bf16)
 // ---------------------------------------------------------------------------
 // one CTA per SM over all tiles
 // ---------------------------------------------------------------------------
-// A 32 x 32 block of y from the warp's transpose buffer, 128 (f32) or 64 bytes of a
-// row at a time.
-__device__ __forceinline__ void store_block(const TileArgs &p, const float *xp, int64_t r0, int64_t c0, int lane)
+__device__ __forceinline__ void st_32B(void *p, const uint32_t (&v)[8])
 {
-    if (p.y_bf16 && (p.n & 1) == 0) {
-        const int64_t col = c0 + 2 * (lane & 15);
-        if (col >= p.n) return;
-#pragma unroll 8
-        for (int r = 0; r < 32; r += 2) {
-            const int rr = r + (lane >> 4);
-            if (r0 + rr >= p.m) break;
-            const int64_t at = (r0 + rr) * p.n + col;
-            float2 v = make_float2(xp[rr * T_XP + 2 * (lane & 15)], xp[rr * T_XP + 2 * (lane & 15) + 1]);
-            if (p.residual) {
-                const float2 e = __bfloat1622float2(
-                    *reinterpret_cast<const __nv_bfloat162 *>(static_cast<const __nv_bfloat16 *>(p.residual) + at));
-                v.x += e.x;
-                v.y += e.y;
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+__device__ __forceinline__ void ld_32B(const void *p, uint32_t (&v)[8])
+{
+    asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "l"(p)
+                 : "memory");
+}
+
+// 32 columns from c0 of this thread's row of y, 32 bytes (a whole sector) per store;
+// every row of y starts on 32 bytes and n is a multiple of those 8 or 16 columns.
+__device__ __forceinline__ void store_row(const TileArgs &p, const uint64_t (&acc)[16], int64_t row, int64_t c0)
+{
+    const int64_t at = row * p.n + c0;
+    if (p.y_bf16) {
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            if (c0 + 16 * g >= p.n) break;
+            uint32_t e[8] = {0, 0, 0, 0, 0, 0, 0, 0}, o[8];
+            if (p.residual) ld_32B(static_cast<const __nv_bfloat16 *>(p.residual) + at + 16 * g, e);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float2 v = unpack2(acc[8 * g + j]);
+                if (p.residual) {
+                    v.x += __uint_as_float(e[j] << 16);
+                    v.y += __uint_as_float(e[j] & 0xffff0000u);
+                }
+                const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
+                o[j] = *reinterpret_cast<const uint32_t *>(&h);
             }
-            *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(p.y) + at) = __floats2bfloat162_rn(v.x, v.y);
+            st_32B(static_cast<__nv_bfloat16 *>(p.y) + at + 16 * g, o);
         }
-        return;
+    } else {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            if (c0 + 8 * g >= p.n) break;
+            uint32_t e[8] = {0, 0, 0, 0, 0, 0, 0, 0}, o[8];
+            if (p.residual) ld_32B(static_cast<const float *>(p.residual) + at + 8 * g, e);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 v = unpack2(acc[4 * g + j]);
+                o[2 * j] = __float_as_uint(p.residual ? v.x + __uint_as_float(e[2 * j]) : v.x);
+                o[2 * j + 1] = __float_as_uint(p.residual ? v.y + __uint_as_float(e[2 * j + 1]) : v.y);
+            }
+            st_32B(static_cast<float *>(p.y) + at + 8 * g, o);
+        }
     }
-    const int64_t col = c0 + lane;
-    if (col >= p.n) return;
-#pragma unroll 8
-    for (int r = 0; r < 32; ++r) {
-        if (r0 + r >= p.m) break;
-        const int64_t at = (r0 + r) * p.n + col;
-        float v = xp[r * T_XP + lane];
-        if (p.residual) v += load_y(p.residual, at, p.y_bf16);
-        if (p.y_bf16)
-            static_cast<__nv_bfloat16 *>(p.y)[at] = __float2bfloat16_rn(v);
-        else
-            static_cast<float *>(p.y)[at] = v;
+}
+
+// The same for any n: eight columns of the warp's 32 rows at a time through its
+// transpose buffer, so that eight lanes write neighbouring values.
+__device__ __forceinline__ void store_any(const TileArgs &p, const uint64_t (&acc)[16], float *xp, int64_t r0, int64_t c0,
+                                          int lane)
+{
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 v = unpack2(acc[4 * g + j]);
+            xp[lane * T_XP + 2 * j] = v.x;
+            xp[lane * T_XP + 2 * j + 1] = v.y;
+        }
+        __syncwarp();
+        const int64_t col = c0 + 8 * g + (lane & 7);
+        if (col >= p.n) continue;
+#pragma unroll 1
+        for (int r = lane >> 3; r < 32; r += 4) {
+            if (r0 + r >= p.m) break;
+            const int64_t at = (r0 + r) * p.n + col;
+            const float v = xp[r * T_XP + (lane & 7)];
+            const float o = p.residual ? v + load_y(p.residual, at, p.y_bf16) : v;
+            if (p.y_bf16)
+                static_cast<__nv_bfloat16 *>(p.y)[at] = __float2bfloat16_rn(o);
+            else
+                static_cast<float *>(p.y)[at] = o;
+        }
     }
 }
 
 template <int BN, bool UP>
-__global__ void __launch_bounds__(T_THREADS, 1)
+__global__ void __launch_bounds__(TileLayout<BN>::THREADS, 1)
     tiles_e4m3_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tw, const TileArgs p)
 {
     using L = TileLayout<BN>;
     constexpr int BO = UP ? 128 : BN;  // output columns per tile
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) TileBars b;
-    __shared__ float top[2][2][TM];  // [tile parity][column group][row]
+    __shared__ __align__(16) TileShared b;
+    __shared__ float top[2][4][TM];  // [tile parity][column group][row]
     uint8_t *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     tile_setup<BN>(b, warp);
     pdl_trigger();
     pdl_wait();  // the activations come from the previous kernel
 
-    uint32_t it = 0;
+    uint32_t it = 0, c = 0;
     bool ok = true;
-    if (warp == T_TMA) {
+    if (warp == L::TMA_WARP) {
         if (lane == 0) {
             for (int64_t tile = blockIdx.x; ok && tile < p.tiles; tile += gridDim.x)
                 ok = tile_copies<BN, UP>(tx, tw, p, b, smem, static_cast<int>((tile % p.m_tiles) * TM),
@@ -290,81 +402,76 @@ __global__ void __launch_bounds__(T_THREADS, 1)
             if (!ok && it > 0) mbar_wait_bounded(&b.full[(it - 1) % L::STAGES], ((it - 1) / L::STAGES) & 1, kCopyWaitLimitNs);
         }
         __syncwarp();
-    } else if (warp == T_MMA) {
+    } else if (warp == L::MMA_WARP) {
         if (lane == 0) {
             for (int64_t tile = blockIdx.x; ok && tile < p.tiles; tile += gridDim.x) ok = tile_mmas<BN>(b, smem, p.kb, it);
             // After an abort, wait (bounded) for the last issued MMAs before TMEM is freed.
             if (!ok && it > 0) mbar_wait_bounded(&b.tfull[(it - 1) & 1], ((it - 1) >> 1) & 1, kCopyWaitLimitNs);
         }
         __syncwarp();
+    } else if (warp == L::SCALE_WARP) {
+        for (int64_t tile = blockIdx.x; ok && tile < p.tiles; tile += gridDim.x)
+            ok = tile_scales<BN, UP>(p, b, lane, (tile % p.m_tiles) * TM, (tile / p.m_tiles) * BO, 0, p.kb, c);
     } else {
-        const int q = warp & 3, hf = warp >> 2;
+        const int q = warp & 3, cg = warp >> 2;
         float *xp = reinterpret_cast<float *>(smem + L::STAGES * L::STAGE) + warp * 32 * T_XP;
         uint32_t parity = 0;
         for (int64_t tile = blockIdx.x; tile < p.tiles; tile += gridDim.x, parity ^= 1) {
             const int64_t m0 = (tile % p.m_tiles) * TM, n0 = (tile / p.m_tiles) * BO;
-            uint64_t acc[L::SEG][16];
-            ok = ok && tile_sums<BN, UP>(p, b, q, hf, lane, m0, n0, 0, p.kb, it, acc);
+            const int64_t row = m0 + 32 * q + lane;
+            uint64_t acc[2][16];
+            ok = ok && tile_sums<BN, UP>(b, q, cg, lane, 0, p.kb, it, c, acc);
             if (!ok) {
 #pragma unroll
-                for (int i = 0; i < L::SEG; ++i)
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
                     for (int j = 0; j < 16; ++j) acc[i][j] = pack2(__int_as_float(0x7fc00000), __int_as_float(0x7fc00000));
             }
             if constexpr (UP) {
-                // 64 values of h, in place of the gate's sums
-                const int64_t row = m0 + 32 * q + lane, c0 = n0 + 64 * hf;
+                // 32 values of h, in place of the gate's sums
+                const int64_t c0 = n0 + 32 * cg;
                 float a = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
+                for (int j = 0; j < 16; ++j) {
+                    acc[0][j] = silu_mul2(acc[0][j], acc[1][j]);
+                    const float2 h = unpack2(acc[0][j]);
+                    if (c0 + 2 * j < p.n) a = fmaxf(a, fmaxf(fabsf(h.x), fabsf(h.y)));
+                }
+                top[parity][cg][32 * q + lane] = a;
+                asm volatile("bar.sync %0, 128;" ::"r"(1 + q) : "memory");
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const float2 g = unpack2(acc[i][j]), u = unpack2(acc[i + 2][j]);
-                        const float h0 = silu_mul_e(g.x, u.x), h1 = silu_mul_e(g.y, u.y);
-                        if (c0 + 32 * i + 2 * j < p.n) a = fmaxf(a, fmaxf(fabsf(h0), fabsf(h1)));
-                        acc[i][j] = pack2(h0, h1);
-                    }
-                top[parity][hf][32 * q + lane] = a;
-                asm volatile("bar.sync %0, 64;" ::"r"(1 + q) : "memory");
-                a = e4m3_floor(fmaxf(a, top[parity][hf ^ 1][32 * q + lane]));
+                for (int i = 0; i < 4; ++i) a = fmaxf(a, top[parity][i][32 * q + lane]);
+                a = e4m3_floor(a);
                 const float f = __fdiv_rn(448.0f, a);
                 if (row < p.m) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {  // 16 codes each
+                    for (int i = 0; i < 2; ++i) {  // 16 codes each
                         uint32_t w[4];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const float2 h0 = unpack2(acc[i >> 1][8 * (i & 1) + 2 * j]);
-                            const float2 h1 = unpack2(acc[i >> 1][8 * (i & 1) + 2 * j + 1]);
+                            const float2 h0 = unpack2(acc[0][8 * i + 2 * j]), h1 = unpack2(acc[0][8 * i + 2 * j + 1]);
                             w[j] = e4m3_pack4(h0.x * f, h0.y * f, h1.x * f, h1.y * f);
                         }
                         if (c0 + 16 * i < p.n)
                             *reinterpret_cast<uint4 *>(p.hq + row * p.n + c0 + 16 * i) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
-                    if (hf == 0)
+                    if (cg == 0)
                         p.hd[row * e4m3_blocks(p.n) + n0 / EB] = ok ? __fdiv_rn(a, 448.0f) : __int_as_float(0x7fc00000);
+                }
+            } else if (p.rows32) {
+                if (row < p.m) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) store_row(p, acc[i], row, n0 + half_col<UP>(cg, i));
                 }
             } else {
 #pragma unroll
-                for (int i = 0; i < L::SEG; ++i) {
-                    // lane l holds row l: turned around in shared memory (row stride
-                    // 33 floats, free of conflicts both ways)
-                    __syncwarp();
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const float2 v = unpack2(acc[i][j]);
-                        xp[lane * T_XP + 2 * j] = v.x;
-                        xp[lane * T_XP + 2 * j + 1] = v.y;
-                    }
-                    __syncwarp();
-                    store_block(p, xp, m0 + 32 * q, n0 + seg_col<BN, UP>(hf, i), lane);
-                }
+                for (int i = 0; i < 2; ++i) store_any(p, acc[i], xp, m0 + 32 * q, n0 + half_col<UP>(cg, i), lane);
             }
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == T_MMA) {
+    if (warp == L::MMA_WARP) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(b.tmem), "r"(L::TMEM) : "memory");
     }
@@ -397,13 +504,13 @@ __device__ __forceinline__ float4 cluster_sum4(const float *at, int split)
 }
 
 template <int BN, bool UP>
-__global__ void __launch_bounds__(T_THREADS, 1)
+__global__ void __launch_bounds__(TileLayout<BN>::THREADS, 1)
     split_e4m3_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tw, const TileArgs p)
 {
     using L = TileLayout<BN>;
     constexpr int BO = UP ? 128 : BN;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) TileBars b;
+    __shared__ __align__(16) TileShared b;
     uint8_t *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = static_cast<int>(cluster_ctarank());
@@ -415,42 +522,44 @@ __global__ void __launch_bounds__(T_THREADS, 1)
     pdl_trigger();
     pdl_wait();
 
-    const int q = warp & 3, hf = warp >> 2;
-    uint32_t it = 0;
+    const int q = warp & 3, cg = warp >> 2;
+    uint32_t it = 0, c = 0;
     bool ok = true;
-    uint64_t acc[L::SEG][16];
-    if (warp == T_TMA) {
+    uint64_t acc[2][16];
+    if (warp == L::TMA_WARP) {
         if (lane == 0) {
             ok = tile_copies<BN, UP>(tx, tw, p, b, smem, static_cast<int>(m0), n0, kb0, kb1, it);
             if (!ok && it > 0) mbar_wait_bounded(&b.full[(it - 1) % L::STAGES], ((it - 1) / L::STAGES) & 1, kCopyWaitLimitNs);
         }
         __syncwarp();
-    } else if (warp == T_MMA) {
+    } else if (warp == L::MMA_WARP) {
         if (lane == 0) {
             ok = tile_mmas<BN>(b, smem, kb1 - kb0, it);
             if (!ok && it > 0) mbar_wait_bounded(&b.tfull[(it - 1) & 1], ((it - 1) >> 1) & 1, kCopyWaitLimitNs);
         }
         __syncwarp();
+    } else if (warp == L::SCALE_WARP) {
+        tile_scales<BN, UP>(p, b, lane, m0, n0, kb0, kb1, c);
     } else {
-        ok = tile_sums<BN, UP>(p, b, q, hf, lane, m0, n0, kb0, kb1, it, acc);
+        ok = tile_sums<BN, UP>(b, q, cg, lane, kb0, kb1, it, c, acc);
     }
     tc_fence_before();
     __syncthreads();  // every copy has landed and every MMA is done: the stages are free
-    if (warp == T_MMA) {
+    if (warp == L::MMA_WARP) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(b.tmem), "r"(L::TMEM) : "memory");
     }
     float *sums = reinterpret_cast<float *>(smem);  // [128][LD]
     const int rows = static_cast<int>(min(p.m - m0, static_cast<int64_t>(TM)));
-    if (warp < T_EW && 32 * q + lane < rows) {
+    if (warp < L::EW && 32 * q + lane < rows) {
         const float nan = __int_as_float(0x7fc00000);
         float *r = sums + (32 * q + lane) * L::LD;
 #pragma unroll
-        for (int i = 0; i < L::SEG; ++i)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int j = 0; j < 16; j += 2) {
                 const float2 v0 = unpack2(acc[i][j]), v1 = unpack2(acc[i][j + 1]);
-                *reinterpret_cast<float4 *>(r + seg_col<BN, UP>(hf, i) + 2 * j) =
+                *reinterpret_cast<float4 *>(r + half_col<UP>(cg, i) + 2 * j) =
                     ok ? make_float4(v0.x, v0.y, v1.x, v1.y) : make_float4(nan, nan, nan, nan);
             }
     }
@@ -461,7 +570,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
     const int r_end = min(rows, (rank + 1) * per);
     if constexpr (UP) {
         // a warp per row: four columns of both halves per lane, the row's block of h in the warp
-        for (int r = rank * per + warp; r < r_end; r += T_THREADS / 32) {
+        for (int r = rank * per + warp; r < r_end; r += L::THREADS / 32) {
             const float4 g = cluster_sum4(sums + r * L::LD + 4 * lane, p.split);
             const float4 u = cluster_sum4(sums + r * L::LD + 128 + 4 * lane, p.split);
             const bool live = n0 + 4 * lane < p.n;
@@ -478,7 +587,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
     } else {
         constexpr int G = BN / 4;  // groups of four columns
         const bool whole = (p.n & 3) == 0;
-        for (int i = threadIdx.x; i < (r_end - rank * per) * G; i += T_THREADS) {
+        for (int i = threadIdx.x; i < (r_end - rank * per) * G; i += L::THREADS) {
             const int r = rank * per + i / G, c = 4 * (i % G);
             if (n0 + c >= p.n) continue;
             const float4 s = cluster_sum4(sums + r * L::LD + c, p.split);
@@ -558,7 +667,7 @@ static cudaError_t launch_tiles(const uint8_t *w, int64_t w_rows, int64_t k, con
     if (cudaError_t e = opt_in_smem(reinterpret_cast<const void *>(tiles_e4m3_kernel<BN, UP>), bytes); e != cudaSuccess)
         return e;
     const int64_t grid = p.tiles < num_sms() ? p.tiles : num_sms();
-    return launch_pdl(tiles_e4m3_kernel<BN, UP>, dim3(static_cast<unsigned>(grid)), dim3(T_THREADS),
+    return launch_pdl(tiles_e4m3_kernel<BN, UP>, dim3(static_cast<unsigned>(grid)), dim3(L::THREADS),
                       static_cast<size_t>(bytes), s, tx, tw, p);
 }
 
@@ -573,7 +682,7 @@ static cudaError_t launch_split(const uint8_t *w, int64_t w_rows, int64_t k, con
     if (cudaError_t e = opt_in_smem(reinterpret_cast<const void *>(split_e4m3_kernel<BN, UP>), L::SPLIT_BYTES);
         e != cudaSuccess)
         return e;
-    return launch_pdl_cluster(split_e4m3_kernel<BN, UP>, dim3(static_cast<unsigned>(p.tiles * split)), dim3(T_THREADS),
+    return launch_pdl_cluster(split_e4m3_kernel<BN, UP>, dim3(static_cast<unsigned>(p.tiles * split)), dim3(L::THREADS),
                               static_cast<size_t>(L::SPLIT_BYTES), s, static_cast<unsigned>(split), tx, tw, p);
 }
 
@@ -598,6 +707,8 @@ cudaError_t launch_tiles_e4m3(const uint8_t *w, const float *wd, int64_t n, int6
     p.residual = residual;
     p.y = y;
     p.y_bf16 = y_dtype == QG_BF16;
+    p.rows32 = n % (p.y_bf16 ? 16 : 8) == 0 && reinterpret_cast<uintptr_t>(y) % 32 == 0 &&
+               reinterpret_cast<uintptr_t>(residual) % 32 == 0;
     const int64_t sms = num_sms(), mt = (m + TM - 1) / TM;
     if (const int64_t t = mt * ((n + 63) / 64); t <= sms)
         return launch_split<64, false>(w, n, k, x, p, split_of(t, p.kb), s);
