@@ -82,7 +82,7 @@ __device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a, uint64_t b,
 // tile's activation rows, and of the weight rows of each column group (gate|up: of
 // the gate and the up rows).
 struct TileShared {
-    uint64_t full[8], empty[8], tfull[2], tempty[2], sfull[2], sempty[2];
+    uint64_t full[8], done[8], tempty[2], sfull[2], sempty[2];
     float sx[2][T_SB][TM];
     float sw[2][4][T_SB];
     uint32_t tmem;
@@ -103,11 +103,10 @@ __device__ __forceinline__ void tile_setup(TileShared &b, int warp)
     if (threadIdx.x == 0) {
         b.abort_flag = 0;
         for (int i = 0; i < L::STAGES; ++i) {
-            mbar_init(&b.full[i], 1);   // the copy thread's expect_tx
-            mbar_init(&b.empty[i], 1);  // the MMA thread's commit
+            mbar_init(&b.full[i], 1);  // the copy thread's expect_tx
+            mbar_init(&b.done[i], 1);  // the MMA thread's commit
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&b.tfull[i], 1);       // the MMA thread's commit
             mbar_init(&b.tempty[i], L::EW);  // one arrival per epilogue warp
             mbar_init(&b.sfull[i], 1);       // the scale warp
             mbar_init(&b.sempty[i], L::EW);  // one arrival per epilogue warp
@@ -124,6 +123,23 @@ __device__ __forceinline__ void tile_setup(TileShared &b, int warp)
     tc_fence_after();
 }
 
+// One lane of a converged warp.  The tensor core's and the copy engine's
+// instructions take uniform registers: behind elect.sync the compiler knows that one
+// lane is left, behind a lane's number it does not, and an MMA then took 148 cycles
+// to issue, whatever its size (104 here, and 128 of the tensor core's for N = 256).
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{ .reg .pred q; elect.sync _|q, 0xffffffff; selp.u32 %0, 1, 0, q; }" : "=r"(p));
+    return p != 0;
+}
+
+// done[s] completes when the MMAs that read stage s have: the stage may be filled
+// again, and the block's sums may be read.  (One commit for both: a second one per
+// block cost the issuing thread as much as an MMA.)  The copy warp is never more than
+// STAGES blocks and the epilogue never more than two behind it, so that a phase's
+// parity says which one it is.
+
 // Copies of blocks [kb0, kb1) of one tile; `it` counts blocks over all tiles.
 template <int BN, bool UP>
 __device__ __forceinline__ bool tile_copies(const CUtensorMap &tx, const CUtensorMap &tw, const TileArgs &p,
@@ -133,38 +149,40 @@ __device__ __forceinline__ bool tile_copies(const CUtensorMap &tx, const CUtenso
     using L = TileLayout<BN>;
     for (int kb = kb0; kb < kb1; ++kb, ++it) {
         const uint32_t s = it % L::STAGES, use = it / L::STAGES;
-        if (!tc_wait(&b.empty[s], (use & 1) ^ 1, &b.abort_flag)) return false;
-        uint8_t *st = smem + s * L::STAGE;
-        mbar_expect_tx(&b.full[s], (p.box_m + BN) * EB);
-        tma_load_2d(st, &tx, kb * EB, m0, &b.full[s]);
-        if constexpr (UP) {
+        if (!__all_sync(0xffffffffu, tc_wait(&b.done[s], (use & 1) ^ 1, &b.abort_flag))) return false;
+        if (elect_one()) {
+            uint8_t *st = smem + s * L::STAGE;
+            mbar_expect_tx(&b.full[s], (p.box_m + BN) * EB);
+            tma_load_2d(st, &tx, kb * EB, m0, &b.full[s]);
             tma_load_2d(st + L::A, &tw, kb * EB, static_cast<int>(n0), &b.full[s]);
-            tma_load_2d(st + L::A + 128 * EB, &tw, kb * EB, static_cast<int>(p.up_row + n0), &b.full[s]);
-        } else {
-            tma_load_2d(st + L::A, &tw, kb * EB, static_cast<int>(n0), &b.full[s]);
+            if constexpr (UP)
+                tma_load_2d(st + L::A + 128 * EB, &tw, kb * EB, static_cast<int>(p.up_row + n0), &b.full[s]);
         }
+        __syncwarp();
     }
     return true;
 }
 
 // The MMAs of one tile's blocks, each into its own TMEM buffer.
 template <int BN>
-__device__ __forceinline__ bool tile_mmas(TileShared &b, uint8_t *smem, int blocks, uint32_t &it)
+__device__ __forceinline__ bool tile_mmas(TileShared &b, uint32_t tmem, uint64_t desc0, int blocks, uint32_t &it)
 {
     using L = TileLayout<BN>;
     // D f32, A and B e4m3, both K-major
     constexpr uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(BN >> 3) << 17) | (static_cast<uint32_t>(TM >> 4) << 24);
     for (int i = 0; i < blocks; ++i, ++it) {
         const uint32_t s = it % L::STAGES, use = it / L::STAGES, t = it & 1, tuse = it >> 1;
-        if (!tc_wait(&b.full[s], use & 1, &b.abort_flag)) return false;
-        if (!tc_wait(&b.tempty[t], (tuse & 1) ^ 1, &b.abort_flag)) return false;
+        const bool ok = tc_wait(&b.full[s], use & 1, &b.abort_flag) &&
+                        tc_wait(&b.tempty[t], (tuse & 1) ^ 1, &b.abort_flag);
+        if (!__all_sync(0xffffffffu, ok)) return false;
         tc_fence_after();
-        const uint32_t a = smem_addr(smem + s * L::STAGE), w = a + L::A;
+        if (elect_one()) {
+            const uint64_t a = desc0 + s * (L::STAGE >> 4), w = a + (L::A >> 4);  // the address field, in 16 bytes
 #pragma unroll
-        for (int k = 0; k < EB / 32; ++k)
-            umma_f8(b.tmem + t * BN, umma_desc_sw128(a + 32 * k), umma_desc_sw128(w + 32 * k), idesc, k != 0);
-        umma_commit(&b.empty[s]);
-        umma_commit(&b.tfull[t]);
+            for (int k = 0; k < EB / 32; ++k) umma_f8(tmem + t * BN, a + 2 * k, w + 2 * k, idesc, k != 0);
+            umma_commit(&b.done[s]);
+        }
+        __syncwarp();
     }
     return true;
 }
@@ -217,7 +235,7 @@ __device__ __forceinline__ bool tile_scales(const TileArgs &p, TileShared &b, in
 // The sums of blocks [kb0, kb1) of one tile in registers: two halves of 32 columns of
 // this thread's row, in adjacent pairs.  `it` counts blocks, `c` buffers of scales.
 template <int BN, bool UP>
-__device__ __forceinline__ bool tile_sums(TileShared &b, int q, int cg, int lane, int kb0, int kb1, uint32_t &it,
+__device__ __forceinline__ bool tile_sums(TileShared &b, uint32_t tmem, int q, int cg, int lane, int kb0, int kb1, uint32_t &it,
                                           uint32_t &c, uint64_t (&acc)[2][16])
 {
 #pragma unroll
@@ -236,11 +254,11 @@ __device__ __forceinline__ bool tile_sums(TileShared &b, int q, int cg, int lane
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&b.sempty[sb]);
             }
-            const uint32_t t = it & 1, tuse = it >> 1;
+            const uint32_t t = it & 1, s = it % TileLayout<BN>::STAGES, use = it / TileLayout<BN>::STAGES;
             // tcgen05.ld is warp-collective: the whole warp proceeds or stops
-            if (!__all_sync(0xffffffffu, tc_wait(&b.tfull[t], tuse & 1, &b.abort_flag))) return false;
+            if (!__all_sync(0xffffffffu, tc_wait(&b.done[s], use & 1, &b.abort_flag))) return false;
             tc_fence_after();
-            const uint32_t ta = b.tmem + (static_cast<uint32_t>(32 * q) << 16) + t * BN;
+            const uint32_t ta = tmem + (static_cast<uint32_t>(32 * q) << 16) + t * BN;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 uint32_t v[16];
@@ -255,8 +273,8 @@ __device__ __forceinline__ bool tile_sums(TileShared &b, int q, int cg, int lane
                 const uint64_t ff = pack2(f, f);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    uint64_t &s = acc[i >> 1][8 * (i & 1) + j];
-                    s = fma2(pack2u(v[2 * j], v[2 * j + 1]), ff, s);
+                    uint64_t &sum = acc[i >> 1][8 * (i & 1) + j];
+                    sum = fma2(pack2u(v[2 * j], v[2 * j + 1]), ff, sum);
                 }
             }
             ++it;
@@ -390,25 +408,22 @@ __global__ void __launch_bounds__(TileLayout<BN>::THREADS, 1)
     pdl_trigger();
     pdl_wait();  // the activations come from the previous kernel
 
+    const uint32_t tmem = b.tmem;
+    const uint64_t desc0 = umma_desc_sw128(smem_addr(smem));
     uint32_t it = 0, c = 0;
     bool ok = true;
     if (warp == L::TMA_WARP) {
-        if (lane == 0) {
-            for (int64_t tile = blockIdx.x; ok && tile < p.tiles; tile += gridDim.x)
-                ok = tile_copies<BN, UP>(tx, tw, p, b, smem, static_cast<int>((tile % p.m_tiles) * TM),
-                                         (tile / p.m_tiles) * BO, 0, p.kb, it);
-            // After an abort the last copies may still be landing: let them finish
-            // (bounded) before the CTA's shared memory goes away.
-            if (!ok && it > 0) mbar_wait_bounded(&b.full[(it - 1) % L::STAGES], ((it - 1) / L::STAGES) & 1, kCopyWaitLimitNs);
-        }
-        __syncwarp();
+        for (int64_t tile = blockIdx.x; ok && tile < p.tiles; tile += gridDim.x)
+            ok = tile_copies<BN, UP>(tx, tw, p, b, smem, static_cast<int>((tile % p.m_tiles) * TM),
+                                     (tile / p.m_tiles) * BO, 0, p.kb, it);
+        // After an abort the last copies may still be landing: let them finish
+        // (bounded) before the CTA's shared memory goes away.
+        if (!ok && it > 0) mbar_wait_bounded(&b.full[(it - 1) % L::STAGES], ((it - 1) / L::STAGES) & 1, kCopyWaitLimitNs);
     } else if (warp == L::MMA_WARP) {
-        if (lane == 0) {
-            for (int64_t tile = blockIdx.x; ok && tile < p.tiles; tile += gridDim.x) ok = tile_mmas<BN>(b, smem, p.kb, it);
-            // After an abort, wait (bounded) for the last issued MMAs before TMEM is freed.
-            if (!ok && it > 0) mbar_wait_bounded(&b.tfull[(it - 1) & 1], ((it - 1) >> 1) & 1, kCopyWaitLimitNs);
-        }
-        __syncwarp();
+        for (int64_t tile = blockIdx.x; ok && tile < p.tiles; tile += gridDim.x)
+            ok = tile_mmas<BN>(b, tmem, desc0, p.kb, it);
+        // After an abort, wait (bounded) for the last issued MMAs before TMEM is freed.
+        if (!ok && it > 0) mbar_wait_bounded(&b.done[(it - 1) % L::STAGES], ((it - 1) / L::STAGES) & 1, kCopyWaitLimitNs);
     } else if (warp == L::SCALE_WARP) {
         for (int64_t tile = blockIdx.x; ok && tile < p.tiles; tile += gridDim.x)
             ok = tile_scales<BN, UP>(p, b, lane, (tile % p.m_tiles) * TM, (tile / p.m_tiles) * BO, 0, p.kb, c);
@@ -420,7 +435,7 @@ __global__ void __launch_bounds__(TileLayout<BN>::THREADS, 1)
             const int64_t m0 = (tile % p.m_tiles) * TM, n0 = (tile / p.m_tiles) * BO;
             const int64_t row = m0 + 32 * q + lane;
             uint64_t acc[2][16];
-            ok = ok && tile_sums<BN, UP>(b, q, cg, lane, 0, p.kb, it, c, acc);
+            ok = ok && tile_sums<BN, UP>(b, tmem, q, cg, lane, 0, p.kb, it, c, acc);
             if (!ok) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
@@ -430,12 +445,13 @@ __global__ void __launch_bounds__(TileLayout<BN>::THREADS, 1)
             if constexpr (UP) {
                 // 32 values of h, in place of the gate's sums
                 const int64_t c0 = n0 + 32 * cg;
+                const int cols = static_cast<int>(min(p.n - c0, static_cast<int64_t>(32)));  // 32, 16 or none
                 float a = 0.0f;
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
                     acc[0][j] = silu_mul2(acc[0][j], acc[1][j]);
                     const float2 h = unpack2(acc[0][j]);
-                    if (c0 + 2 * j < p.n) a = fmaxf(a, fmaxf(fabsf(h.x), fabsf(h.y)));
+                    if (2 * j < cols) a = fmaxf(a, fmaxf(fabsf(h.x), fabsf(h.y)));
                 }
                 top[parity][cg][32 * q + lane] = a;
                 asm volatile("bar.sync %0, 128;" ::"r"(1 + q) : "memory");
@@ -452,7 +468,7 @@ __global__ void __launch_bounds__(TileLayout<BN>::THREADS, 1)
                             const float2 h0 = unpack2(acc[0][8 * i + 2 * j]), h1 = unpack2(acc[0][8 * i + 2 * j + 1]);
                             w[j] = e4m3_pack4(h0.x * f, h0.y * f, h1.x * f, h1.y * f);
                         }
-                        if (c0 + 16 * i < p.n)
+                        if (16 * i < cols)
                             *reinterpret_cast<uint4 *>(p.hq + row * p.n + c0 + 16 * i) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                     if (cg == 0)
@@ -473,7 +489,7 @@ __global__ void __launch_bounds__(TileLayout<BN>::THREADS, 1)
     __syncthreads();
     if (warp == L::MMA_WARP) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(b.tmem), "r"(L::TMEM) : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(L::TMEM) : "memory");
     }
 }
 
@@ -523,31 +539,27 @@ __global__ void __launch_bounds__(TileLayout<BN>::THREADS, 1)
     pdl_wait();
 
     const int q = warp & 3, cg = warp >> 2;
+    const uint32_t tmem = b.tmem;
+    const uint64_t desc0 = umma_desc_sw128(smem_addr(smem));
     uint32_t it = 0, c = 0;
     bool ok = true;
     uint64_t acc[2][16];
     if (warp == L::TMA_WARP) {
-        if (lane == 0) {
-            ok = tile_copies<BN, UP>(tx, tw, p, b, smem, static_cast<int>(m0), n0, kb0, kb1, it);
-            if (!ok && it > 0) mbar_wait_bounded(&b.full[(it - 1) % L::STAGES], ((it - 1) / L::STAGES) & 1, kCopyWaitLimitNs);
-        }
-        __syncwarp();
+        ok = tile_copies<BN, UP>(tx, tw, p, b, smem, static_cast<int>(m0), n0, kb0, kb1, it);
+        if (!ok && it > 0) mbar_wait_bounded(&b.full[(it - 1) % L::STAGES], ((it - 1) / L::STAGES) & 1, kCopyWaitLimitNs);
     } else if (warp == L::MMA_WARP) {
-        if (lane == 0) {
-            ok = tile_mmas<BN>(b, smem, kb1 - kb0, it);
-            if (!ok && it > 0) mbar_wait_bounded(&b.tfull[(it - 1) & 1], ((it - 1) >> 1) & 1, kCopyWaitLimitNs);
-        }
-        __syncwarp();
+        ok = tile_mmas<BN>(b, tmem, desc0, kb1 - kb0, it);
+        if (!ok && it > 0) mbar_wait_bounded(&b.done[(it - 1) % L::STAGES], ((it - 1) / L::STAGES) & 1, kCopyWaitLimitNs);
     } else if (warp == L::SCALE_WARP) {
         tile_scales<BN, UP>(p, b, lane, m0, n0, kb0, kb1, c);
     } else {
-        ok = tile_sums<BN, UP>(b, q, cg, lane, kb0, kb1, it, c, acc);
+        ok = tile_sums<BN, UP>(b, tmem, q, cg, lane, kb0, kb1, it, c, acc);
     }
     tc_fence_before();
     __syncthreads();  // every copy has landed and every MMA is done: the stages are free
     if (warp == L::MMA_WARP) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(b.tmem), "r"(L::TMEM) : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(L::TMEM) : "memory");
     }
     float *sums = reinterpret_cast<float *>(smem);  // [128][LD]
     const int rows = static_cast<int>(min(p.m - m0, static_cast<int64_t>(TM)));
