@@ -59,7 +59,7 @@ struct TileArgs {
     int64_t m, n;        // n: output columns
     int64_t up_row, up_block;
     int kb;
-    int64_t m_tiles, tiles;
+    int m_tiles, tiles;
     int box_m;           // activation rows per copy
     int split;
     const void *residual;
@@ -123,6 +123,14 @@ __device__ __forceinline__ void tile_setup(TileShared &b, int warp)
     tc_fence_after();
 }
 
+// tc_wait for barriers that have mostly completed by the time they are asked for: one
+// plain try first, 13 cycles against the 103 of tc_wait's way in (its suspended try and
+// what surrounds it), five times per block.
+__device__ __forceinline__ bool stage_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag)
+{
+    return mbar_try_wait(bar, parity) || tc_wait(bar, parity, abort_flag);
+}
+
 // One lane of a converged warp.  The tensor core's and the copy engine's
 // instructions take uniform registers: behind elect.sync the compiler knows that one
 // lane is left, behind a lane's number it does not, and an MMA then took 148 cycles
@@ -143,18 +151,18 @@ __device__ __forceinline__ bool elect_one()
 // Copies of blocks [kb0, kb1) of one tile; `it` counts blocks over all tiles.
 template <int BN, bool UP>
 __device__ __forceinline__ bool tile_copies(const CUtensorMap &tx, const CUtensorMap &tw, const TileArgs &p,
-                                            TileShared &b, uint8_t *smem, int m0, int64_t n0, int kb0, int kb1,
+                                            TileShared &b, uint8_t *smem, int m0, int n0, int kb0, int kb1,
                                             uint32_t &it)
 {
     using L = TileLayout<BN>;
     for (int kb = kb0; kb < kb1; ++kb, ++it) {
         const uint32_t s = it % L::STAGES, use = it / L::STAGES;
-        if (!__all_sync(0xffffffffu, tc_wait(&b.done[s], (use & 1) ^ 1, &b.abort_flag))) return false;
+        if (!__all_sync(0xffffffffu, stage_wait(&b.done[s], (use & 1) ^ 1, &b.abort_flag))) return false;
         if (elect_one()) {
             uint8_t *st = smem + s * L::STAGE;
             mbar_expect_tx(&b.full[s], (p.box_m + BN) * EB);
             tma_load_2d(st, &tx, kb * EB, m0, &b.full[s]);
-            tma_load_2d(st + L::A, &tw, kb * EB, static_cast<int>(n0), &b.full[s]);
+            tma_load_2d(st + L::A, &tw, kb * EB, n0, &b.full[s]);
             if constexpr (UP)
                 tma_load_2d(st + L::A + 128 * EB, &tw, kb * EB, static_cast<int>(p.up_row + n0), &b.full[s]);
         }
@@ -172,8 +180,8 @@ __device__ __forceinline__ bool tile_mmas(TileShared &b, uint32_t tmem, uint64_t
     constexpr uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(BN >> 3) << 17) | (static_cast<uint32_t>(TM >> 4) << 24);
     for (int i = 0; i < blocks; ++i, ++it) {
         const uint32_t s = it % L::STAGES, use = it / L::STAGES, t = it & 1, tuse = it >> 1;
-        const bool ok = tc_wait(&b.full[s], use & 1, &b.abort_flag) &&
-                        tc_wait(&b.tempty[t], (tuse & 1) ^ 1, &b.abort_flag);
+        const bool ok = stage_wait(&b.full[s], use & 1, &b.abort_flag) &&
+                        stage_wait(&b.tempty[t], (tuse & 1) ^ 1, &b.abort_flag);
         if (!__all_sync(0xffffffffu, ok)) return false;
         tc_fence_after();
         if (elect_one()) {
@@ -190,15 +198,15 @@ __device__ __forceinline__ bool tile_mmas(TileShared &b, uint32_t tmem, uint64_t
 // The scale warp: the scales of blocks [kb0, kb1) of one tile, T_SB at a time, the
 // next ones on their way while the last are waited for.  `c` counts buffers.
 template <int BN, bool UP>
-__device__ __forceinline__ bool tile_scales(const TileArgs &p, TileShared &b, int lane, int64_t m0, int64_t n0, int kb0,
+__device__ __forceinline__ bool tile_scales(const TileArgs &p, TileShared &b, int lane, int m0, int n0, int kb0,
                                             int kb1, uint32_t &c)
 {
     constexpr int GROUPS = UP ? 2 : TileLayout<BN>::CG;
     const float *xr[TM / 32];
 #pragma unroll
-    for (int i = 0; i < TM / 32; ++i) xr[i] = p.xd + min(m0 + 32 * i + lane, p.m - 1) * p.kb;
+    for (int i = 0; i < TM / 32; ++i) xr[i] = p.xd + min(static_cast<int64_t>(m0 + 32 * i + lane), p.m - 1) * p.kb;
     const int cg = lane / T_SB, o = lane % T_SB;  // this lane's weight scale: group and block
-    const int64_t blk = UP ? cg * p.up_block + n0 / EB : min(n0 + T_CW * cg, p.n - 1) / EB;
+    const int64_t blk = UP ? cg * p.up_block + n0 / EB : min(static_cast<int64_t>(n0 + T_CW * cg), p.n - 1) / EB;
     const float *wr = p.wd + (cg < GROUPS ? blk : 0) * p.kb;
     const bool vec = (p.kb % 4 == 0) && (kb0 % 4 == 0) && (reinterpret_cast<uintptr_t>(p.xd) & 15) == 0;
     for (int kb = kb0; kb < kb1; kb += T_SB, ++c) {
@@ -216,7 +224,7 @@ __device__ __forceinline__ bool tile_scales(const TileArgs &p, TileShared &b, in
         }
         const float w = cg < GROUPS && kb + o < kb1 ? wr[kb + o] : 0.0f;
         const uint32_t t = c & 1, use = c >> 1;
-        if (!__all_sync(0xffffffffu, tc_wait(&b.sempty[t], (use & 1) ^ 1, &b.abort_flag))) return false;
+        if (!__all_sync(0xffffffffu, stage_wait(&b.sempty[t], (use & 1) ^ 1, &b.abort_flag))) return false;
 #pragma unroll
         for (int i = 0; i < TM / 32; ++i) {
             float *sx = b.sx[t][0] + 32 * i + lane;
@@ -244,7 +252,7 @@ __device__ __forceinline__ bool tile_sums(TileShared &b, uint32_t tmem, int q, i
         for (int j = 0; j < 16; ++j) acc[i][j] = 0;
     for (int kb = kb0; kb < kb1; kb += T_SB, ++c) {
         const uint32_t sb = c & 1, suse = c >> 1;
-        if (!__all_sync(0xffffffffu, tc_wait(&b.sfull[sb], suse & 1, &b.abort_flag))) return false;
+        if (!__all_sync(0xffffffffu, stage_wait(&b.sfull[sb], suse & 1, &b.abort_flag))) return false;
         const float *sx = b.sx[sb][0] + 32 * q + lane, *s0 = b.sw[sb][UP ? 0 : cg], *s1 = b.sw[sb][UP ? 1 : cg];
 #pragma unroll 1
         for (int o = 0; o < T_SB; ++o) {
@@ -256,24 +264,24 @@ __device__ __forceinline__ bool tile_sums(TileShared &b, uint32_t tmem, int q, i
             }
             const uint32_t t = it & 1, s = it % TileLayout<BN>::STAGES, use = it / TileLayout<BN>::STAGES;
             // tcgen05.ld is warp-collective: the whole warp proceeds or stops
-            if (!__all_sync(0xffffffffu, tc_wait(&b.done[s], use & 1, &b.abort_flag))) return false;
+            if (!__all_sync(0xffffffffu, stage_wait(&b.done[s], use & 1, &b.abort_flag))) return false;
             tc_fence_after();
             const uint32_t ta = tmem + (static_cast<uint32_t>(32 * q) << 16) + t * BN;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t v[16];
-                tmem_ld_16(ta + half_col<UP>(cg, i >> 1) + 16 * (i & 1), v);
-                tmem_ld_wait_regs16(v);
-                if (i == 3) {
+            for (int i = 0; i < 8; ++i) {
+                uint32_t v[8];
+                tmem_ld_8(ta + half_col<UP>(cg, i >> 2) + 8 * (i & 3), v);
+                tmem_ld_wait_regs8(v);
+                if (i == 7) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&b.tempty[t]);
                 }
-                const float f = i >> 1 ? f1 : f0;
+                const float f = i >> 2 ? f1 : f0;
                 const uint64_t ff = pack2(f, f);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    uint64_t &sum = acc[i >> 1][8 * (i & 1) + j];
+                for (int j = 0; j < 4; ++j) {
+                    uint64_t &sum = acc[i >> 2][4 * (i & 3) + j];
                     sum = fma2(pack2u(v[2 * j], v[2 * j + 1]), ff, sum);
                 }
             }
@@ -413,27 +421,25 @@ __global__ void __launch_bounds__(TileLayout<BN>::THREADS, 1)
     uint32_t it = 0, c = 0;
     bool ok = true;
     if (warp == L::TMA_WARP) {
-        for (int64_t tile = blockIdx.x; ok && tile < p.tiles; tile += gridDim.x)
-            ok = tile_copies<BN, UP>(tx, tw, p, b, smem, static_cast<int>((tile % p.m_tiles) * TM),
+        for (int tile = blockIdx.x; ok && tile < p.tiles; tile += gridDim.x)
+            ok = tile_copies<BN, UP>(tx, tw, p, b, smem, (tile % p.m_tiles) * TM,
                                      (tile / p.m_tiles) * BO, 0, p.kb, it);
         // After an abort the last copies may still be landing: let them finish
         // (bounded) before the CTA's shared memory goes away.
         if (!ok && it > 0) mbar_wait_bounded(&b.full[(it - 1) % L::STAGES], ((it - 1) / L::STAGES) & 1, kCopyWaitLimitNs);
     } else if (warp == L::MMA_WARP) {
-        for (int64_t tile = blockIdx.x; ok && tile < p.tiles; tile += gridDim.x)
+        for (int tile = blockIdx.x; ok && tile < p.tiles; tile += gridDim.x)
             ok = tile_mmas<BN>(b, tmem, desc0, p.kb, it);
         // After an abort, wait (bounded) for the last issued MMAs before TMEM is freed.
         if (!ok && it > 0) mbar_wait_bounded(&b.done[(it - 1) % L::STAGES], ((it - 1) / L::STAGES) & 1, kCopyWaitLimitNs);
     } else if (warp == L::SCALE_WARP) {
-        for (int64_t tile = blockIdx.x; ok && tile < p.tiles; tile += gridDim.x)
+        for (int tile = blockIdx.x; ok && tile < p.tiles; tile += gridDim.x)
             ok = tile_scales<BN, UP>(p, b, lane, (tile % p.m_tiles) * TM, (tile / p.m_tiles) * BO, 0, p.kb, c);
     } else {
         const int q = warp & 3, cg = warp >> 2;
         float *xp = reinterpret_cast<float *>(smem + L::STAGES * L::STAGE) + warp * 32 * T_XP;
         uint32_t parity = 0;
-        for (int64_t tile = blockIdx.x; tile < p.tiles; tile += gridDim.x, parity ^= 1) {
-            const int64_t m0 = (tile % p.m_tiles) * TM, n0 = (tile / p.m_tiles) * BO;
-            const int64_t row = m0 + 32 * q + lane;
+        for (int tile = blockIdx.x; tile < p.tiles; tile += gridDim.x, parity ^= 1) {
             uint64_t acc[2][16];
             ok = ok && tile_sums<BN, UP>(b, tmem, q, cg, lane, 0, p.kb, it, c, acc);
             if (!ok) {
@@ -442,10 +448,12 @@ __global__ void __launch_bounds__(TileLayout<BN>::THREADS, 1)
 #pragma unroll
                     for (int j = 0; j < 16; ++j) acc[i][j] = pack2(__int_as_float(0x7fc00000), __int_as_float(0x7fc00000));
             }
+            const int m0 = tile % p.m_tiles * TM, n0 = tile / p.m_tiles * BO;
+            const int64_t row = m0 + 32 * q + lane;
             if constexpr (UP) {
                 // 32 values of h, in place of the gate's sums
-                const int64_t c0 = n0 + 32 * cg;
-                const int cols = static_cast<int>(min(p.n - c0, static_cast<int64_t>(32)));  // 32, 16 or none
+                const int c0 = n0 + 32 * cg;
+                const int cols = static_cast<int>(min(p.n - c0, int64_t(32)));  // 32, 16 or none
                 float a = 0.0f;
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
@@ -530,8 +538,8 @@ __global__ void __launch_bounds__(TileLayout<BN>::THREADS, 1)
     uint8_t *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = static_cast<int>(cluster_ctarank());
-    const int64_t tile = blockIdx.x / p.split;
-    const int64_t m0 = (tile % p.m_tiles) * TM, n0 = (tile / p.m_tiles) * BO;
+    const int tile = blockIdx.x / p.split;
+    const int m0 = tile % p.m_tiles * TM, n0 = tile / p.m_tiles * BO;
     const int kb0 = static_cast<int>(static_cast<int64_t>(rank) * p.kb / p.split);
     const int kb1 = static_cast<int>(static_cast<int64_t>(rank + 1) * p.kb / p.split);
     tile_setup<BN>(b, warp);
@@ -545,7 +553,7 @@ __global__ void __launch_bounds__(TileLayout<BN>::THREADS, 1)
     bool ok = true;
     uint64_t acc[2][16];
     if (warp == L::TMA_WARP) {
-        ok = tile_copies<BN, UP>(tx, tw, p, b, smem, static_cast<int>(m0), n0, kb0, kb1, it);
+        ok = tile_copies<BN, UP>(tx, tw, p, b, smem, m0, n0, kb0, kb1, it);
         if (!ok && it > 0) mbar_wait_bounded(&b.full[(it - 1) % L::STAGES], ((it - 1) / L::STAGES) & 1, kCopyWaitLimitNs);
     } else if (warp == L::MMA_WARP) {
         ok = tile_mmas<BN>(b, tmem, desc0, kb1 - kb0, it);
@@ -604,7 +612,7 @@ __global__ void __launch_bounds__(TileLayout<BN>::THREADS, 1)
             if (n0 + c >= p.n) continue;
             const float4 s = cluster_sum4(sums + r * L::LD + c, p.split);
             float v[4] = {s.x, s.y, s.z, s.w};
-            const int64_t at = (m0 + r) * p.n + n0 + c;
+            const int64_t at = static_cast<int64_t>(m0 + r) * p.n + n0 + c;
             if (whole) {
                 if (p.y_bf16) {
                     using V = Vec4<__nv_bfloat16>;
@@ -663,8 +671,10 @@ static cudaError_t tile_maps(const uint8_t *w, int64_t w_rows, int64_t k, const 
     if (!enc) return cudaErrorNotSupported;
     constexpr int BO = UP ? 128 : BN;
     p.box_m = static_cast<int>(p.m >= TM ? TM : (p.m + 7) / 8 * 8);
-    p.m_tiles = (p.m + TM - 1) / TM;
-    p.tiles = p.m_tiles * ((p.n + BO - 1) / BO);
+    const int64_t m_tiles = (p.m + TM - 1) / TM, tiles = m_tiles * ((p.n + BO - 1) / BO);
+    if (tiles > INT32_MAX) return cudaErrorInvalidValue;  // an output of 2^45 values and more
+    p.m_tiles = static_cast<int>(m_tiles);
+    p.tiles = static_cast<int>(tiles);
     if (cudaError_t e = e4m3_map(enc, &tx, x, p.m, k, p.box_m); e != cudaSuccess) return e;
     return e4m3_map(enc, &tw, w, w_rows, k, UP ? 128 : BN);
 }

@@ -124,12 +124,11 @@ __device__ __forceinline__ void tmem_ld_wait_regs(uint32_t *a, uint32_t *b)
                  : "memory");
 }
 
-// The same for one load of 16 registers.
-__device__ __forceinline__ void tmem_ld_wait_regs16(uint32_t *a)
+// The same for one load of 8 registers.
+__device__ __forceinline__ void tmem_ld_wait_regs8(uint32_t *a)
 {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]), "+r"(a[6]), "+r"(a[7]),
-                   "+r"(a[8]), "+r"(a[9]), "+r"(a[10]), "+r"(a[11]), "+r"(a[12]), "+r"(a[13]), "+r"(a[14]), "+r"(a[15])
+                 : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]), "+r"(a[6]), "+r"(a[7])
                  :
                  : "memory");
 }
