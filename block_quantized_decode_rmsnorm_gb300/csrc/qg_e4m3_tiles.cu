@@ -260,7 +260,7 @@ __device__ __forceinline__ bool tile_sums(TileShared &b, uint32_t tmem, int q, i
             const float f0 = sx[o * TM] * s0[o], f1 = UP ? sx[o * TM] * s1[o] : f0;
             if (o == T_SB - 1 || kb + o + 1 == kb1) {  // the buffer's last: every lane has read it
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&b.sempty[sb]);
+                if (elect_one()) mbar_arrive(&b.sempty[sb]);
             }
             const uint32_t t = it & 1, s = it % TileLayout<BN>::STAGES, use = it / TileLayout<BN>::STAGES;
             // tcgen05.ld is warp-collective: the whole warp proceeds or stops
@@ -275,7 +275,7 @@ __device__ __forceinline__ bool tile_sums(TileShared &b, uint32_t tmem, int q, i
                 if (i == 7) {
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&b.tempty[t]);
+                    if (elect_one()) mbar_arrive(&b.tempty[t]);
                 }
                 const float f = i >> 2 ? f1 : f0;
                 const uint64_t ff = pack2(f, f);
@@ -411,12 +411,12 @@ __global__ void __launch_bounds__(TileLayout<BN>::THREADS, 1)
     __shared__ __align__(16) TileShared b;
     __shared__ float top[2][4][TM];  // [tile parity][column group][row]
     uint8_t *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
     tile_setup<BN>(b, warp);
     pdl_trigger();
     pdl_wait();  // the activations come from the previous kernel
 
-    const uint32_t tmem = b.tmem;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, b.tmem, 0);
     const uint64_t desc0 = umma_desc_sw128(smem_addr(smem));
     uint32_t it = 0, c = 0;
     bool ok = true;
@@ -536,7 +536,7 @@ __global__ void __launch_bounds__(TileLayout<BN>::THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(16) TileShared b;
     uint8_t *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
     const int rank = static_cast<int>(cluster_ctarank());
     const int tile = blockIdx.x / p.split;
     const int m0 = tile % p.m_tiles * TM, n0 = tile / p.m_tiles * BO;
@@ -547,7 +547,7 @@ __global__ void __launch_bounds__(TileLayout<BN>::THREADS, 1)
     pdl_wait();
 
     const int q = warp & 3, cg = warp >> 2;
-    const uint32_t tmem = b.tmem;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, b.tmem, 0);
     const uint64_t desc0 = umma_desc_sw128(smem_addr(smem));
     uint32_t it = 0, c = 0;
     bool ok = true;
