@@ -78,13 +78,12 @@ __device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a, uint64_t b,
                  : "memory");
 }
 
-// Barriers, and the scales of T_SB blocks of k at a time, in two buffers: of the
-// tile's activation rows, and of the weight rows of each column group (gate|up: of
-// the gate and the up rows).
+// Barriers, and the factors d_x d_w of T_SB blocks of k at a time, in two buffers: per
+// activation row two, as a tile's columns lie in at most two blocks of weight rows
+// (gate|up: the gate's and the up's).
 struct TileShared {
     uint64_t full[8], done[8], tempty[2], sfull[2], sempty[2];
-    float sx[2][T_SB][TM];
-    float sw[2][4][T_SB];
+    float2 f[2][T_SB][TM];
     uint32_t tmem;
     int abort_flag;
 };
@@ -195,47 +194,43 @@ __device__ __forceinline__ bool tile_mmas(TileShared &b, uint32_t tmem, uint64_t
     return true;
 }
 
-// The scale warp: the scales of blocks [kb0, kb1) of one tile, T_SB at a time, the
-// next ones on their way while the last are waited for.  `c` counts buffers.
+// The scale warp: the factors of blocks [kb0, kb1) of one tile, T_SB at a time, the
+// next scales on their way while the last factors are waited for.  `c` counts buffers.
 template <int BN, bool UP>
 __device__ __forceinline__ bool tile_scales(const TileArgs &p, TileShared &b, int lane, int m0, int n0, int kb0,
                                             int kb1, uint32_t &c)
 {
-    constexpr int GROUPS = UP ? 2 : TileLayout<BN>::CG;
     const float *xr[TM / 32];
 #pragma unroll
     for (int i = 0; i < TM / 32; ++i) xr[i] = p.xd + min(static_cast<int64_t>(m0 + 32 * i + lane), p.m - 1) * p.kb;
-    const int cg = lane / T_SB, o = lane % T_SB;  // this lane's weight scale: group and block
-    const int64_t blk = UP ? cg * p.up_block + n0 / EB : min(static_cast<int64_t>(n0 + T_CW * cg), p.n - 1) / EB;
-    const float *wr = p.wd + (cg < GROUPS ? blk : 0) * p.kb;
+    const int64_t b0 = n0 / EB, b1 = UP ? p.up_block + b0 : min(b0 + 1, (p.n - 1) / EB);
+    const float *w0 = p.wd + b0 * p.kb, *w1 = p.wd + b1 * p.kb;
     const bool vec = (p.kb % 4 == 0) && (kb0 % 4 == 0) && (reinterpret_cast<uintptr_t>(p.xd) & 15) == 0;
     for (int kb = kb0; kb < kb1; kb += T_SB, ++c) {
-        float4 x[TM / 32];
+        float x[TM / 32][T_SB], wa[T_SB], wb[T_SB];
 #pragma unroll
         for (int i = 0; i < TM / 32; ++i) {
             if (vec) {
-                x[i] = *reinterpret_cast<const float4 *>(xr[i] + kb);  // kb % 4 == 0 and so is the row's length
+                const float4 v = *reinterpret_cast<const float4 *>(xr[i] + kb);  // kb % 4 == 0 and so is the row's length
+                x[i][0] = v.x, x[i][1] = v.y, x[i][2] = v.z, x[i][3] = v.w;
             } else {
-                x[i].x = xr[i][kb];
-                x[i].y = kb + 1 < kb1 ? xr[i][kb + 1] : 0.0f;
-                x[i].z = kb + 2 < kb1 ? xr[i][kb + 2] : 0.0f;
-                x[i].w = kb + 3 < kb1 ? xr[i][kb + 3] : 0.0f;
+#pragma unroll
+                for (int o = 0; o < T_SB; ++o) x[i][o] = kb + o < kb1 ? xr[i][kb + o] : 0.0f;
             }
         }
-        const float w = cg < GROUPS && kb + o < kb1 ? wr[kb + o] : 0.0f;
+#pragma unroll
+        for (int o = 0; o < T_SB; ++o) {
+            wa[o] = kb + o < kb1 ? w0[kb + o] : 0.0f;
+            wb[o] = kb + o < kb1 ? w1[kb + o] : 0.0f;
+        }
         const uint32_t t = c & 1, use = c >> 1;
         if (!__all_sync(0xffffffffu, stage_wait(&b.sempty[t], (use & 1) ^ 1, &b.abort_flag))) return false;
 #pragma unroll
-        for (int i = 0; i < TM / 32; ++i) {
-            float *sx = b.sx[t][0] + 32 * i + lane;
-            sx[0] = x[i].x;
-            sx[TM] = x[i].y;
-            sx[2 * TM] = x[i].z;
-            sx[3 * TM] = x[i].w;
-        }
-        if (cg < GROUPS) b.sw[t][cg][o] = w;
+        for (int i = 0; i < TM / 32; ++i)
+#pragma unroll
+            for (int o = 0; o < T_SB; ++o) b.f[t][o][32 * i + lane] = make_float2(x[i][o] * wa[o], x[i][o] * wb[o]);
         __syncwarp();
-        if (lane == 0) mbar_arrive(&b.sfull[t]);
+        if (elect_one()) mbar_arrive(&b.sfull[t]);
     }
     return true;
 }
@@ -243,21 +238,27 @@ __device__ __forceinline__ bool tile_scales(const TileArgs &p, TileShared &b, in
 // The sums of blocks [kb0, kb1) of one tile in registers: two halves of 32 columns of
 // this thread's row, in adjacent pairs.  `it` counts blocks, `c` buffers of scales.
 template <int BN, bool UP>
-__device__ __forceinline__ bool tile_sums(TileShared &b, uint32_t tmem, int q, int cg, int lane, int kb0, int kb1, uint32_t &it,
-                                          uint32_t &c, uint64_t (&acc)[2][16])
+__device__ __forceinline__ bool tile_sums(TileShared &b, uint32_t tmem, int q, int cg, int lane, int n0, int kb0,
+                                          int kb1, uint32_t &it, uint32_t &c, uint64_t (&acc)[2][16])
 {
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int j = 0; j < 16; ++j) acc[i][j] = 0;
+    const int second = UP ? 0 : (n0 + T_CW * cg) / EB - n0 / EB;  // this warp's columns lie in the second block
     for (int kb = kb0; kb < kb1; kb += T_SB, ++c) {
         const uint32_t sb = c & 1, suse = c >> 1;
         if (!__all_sync(0xffffffffu, stage_wait(&b.sfull[sb], suse & 1, &b.abort_flag))) return false;
-        const float *sx = b.sx[sb][0] + 32 * q + lane, *s0 = b.sw[sb][UP ? 0 : cg], *s1 = b.sw[sb][UP ? 1 : cg];
 #pragma unroll 1
         for (int o = 0; o < T_SB; ++o) {
             if (kb + o >= kb1) break;
-            const float f0 = sx[o * TM] * s0[o], f1 = UP ? sx[o * TM] * s1[o] : f0;
+            float f0, f1;
+            if constexpr (UP) {
+                const float2 f = b.f[sb][o][32 * q + lane];
+                f0 = f.x, f1 = f.y;
+            } else {
+                f0 = f1 = reinterpret_cast<const float *>(&b.f[sb][o][32 * q + lane])[second];
+            }
             if (o == T_SB - 1 || kb + o + 1 == kb1) {  // the buffer's last: every lane has read it
                 __syncwarp();
                 if (elect_one()) mbar_arrive(&b.sempty[sb]);
@@ -305,7 +306,8 @@ __device__ __forceinline__ uint64_t silu_mul2(uint64_t g2, uint64_t u2)
     t = fma2(t, mul2(lo, ln2), t);
     const float2 d = unpack2(fma2(t, t, one)), n = unpack2(mul2(mul2(g2, t), t));
     const uint64_t num = pack2(g.x >= 0.0f ? g.x : n.x, g.y >= 0.0f ? g.y : n.y);
-    return mul2(mul2(num, pack2(rcp_approx(d.x), rcp_approx(d.y))), u2);
+    const float r = rcp_approx(d.x * d.y);  // one reciprocal for both: 1/dx = r dy
+    return mul2(mul2(num, mul2(pack2(r, r), pack2(d.y, d.x))), u2);
 }
 
 __device__ __forceinline__ float load_y(const void *p, int64_t at, int bf16)
@@ -441,7 +443,7 @@ __global__ void __launch_bounds__(TileLayout<BN>::THREADS, 1)
         uint32_t parity = 0;
         for (int tile = blockIdx.x; tile < p.tiles; tile += gridDim.x, parity ^= 1) {
             uint64_t acc[2][16];
-            ok = ok && tile_sums<BN, UP>(b, tmem, q, cg, lane, 0, p.kb, it, c, acc);
+            ok = ok && tile_sums<BN, UP>(b, tmem, q, cg, lane, tile / p.m_tiles * BO, 0, p.kb, it, c, acc);
             if (!ok) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
@@ -561,7 +563,7 @@ __global__ void __launch_bounds__(TileLayout<BN>::THREADS, 1)
     } else if (warp == L::SCALE_WARP) {
         tile_scales<BN, UP>(p, b, lane, m0, n0, kb0, kb1, c);
     } else {
-        ok = tile_sums<BN, UP>(b, tmem, q, cg, lane, kb0, kb1, it, c, acc);
+        ok = tile_sums<BN, UP>(b, tmem, q, cg, lane, n0, kb0, kb1, it, c, acc);
     }
     tc_fence_before();
     __syncthreads();  // every copy has landed and every MMA is done: the stages are free
