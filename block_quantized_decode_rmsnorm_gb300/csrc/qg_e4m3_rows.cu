@@ -53,10 +53,10 @@ __device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefe
 
 // NT: groups of 8 activation rows; m <= 8 NT.
 template <int NT, bool UP>
-__global__ void __launch_bounds__(RW * 32) rows_e4m3_kernel(const RowsArgs p)
+__global__ void __launch_bounds__(RW * 32, NT == 1 ? 3 : 2) rows_e4m3_kernel(const RowsArgs p)
 {
     constexpr int RT = UP ? 2 : 1;  // weight tiles per CTA
-    constexpr int U = UP ? 2 : 4;   // blocks of k in flight per warp
+    constexpr int U = UP ? 1 : 2;   // blocks of k in flight per warp
     __shared__ float red[RW][RT][NT * 8 * RR];
     __shared__ float top[NT * 8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
