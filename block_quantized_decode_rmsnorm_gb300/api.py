@@ -786,7 +786,6 @@ class DecodeStack:
 # --------------------------------------------------------------------------
 
 _E4M3 = torch.float8_e4m3fn
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 _STREAM_TYPES = {torch.float32: _lib.QG_F32, torch.bfloat16: _lib.QG_BF16}
 
 
@@ -813,81 +812,40 @@ class E4M3Weight:
         return self.codes.numel() + 4 * self.scales.numel()
 
 
+_front = None  # the native front end: checks, outputs and the C call (csrc/qg_torch.cpp)
+
+
+def _load_front():
+    global _front
+    _lib.load()
+    try:
+        from . import _qg_torch
+    except ImportError as e:
+        raise RuntimeError("_qg_torch.so is missing or was built for another torch: build it first (python -m "
+                           "block_quantized_decode_rmsnorm_gb300.builder, or __graft_entry__.build())") from e
+    _qg_torch.set_error(_lib.QGError)
+    _front = _qg_torch
+    return _front
+
+
+def _on(stream):
+    """`stream` (a torch stream or a raw handle) as the current stream: outputs are
+    allocated for it and the kernels launched on it."""
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
+                             else torch.cuda.ExternalStream(_stream_handle(stream)))
+
+
 def _blocks128(n: int) -> int:
     return (n + 127) // 128
-
-
-def _stream_on(stream, dev: int) -> int:
-    """The stream's handle; None: the device's current stream (its raw handle costs 0.1 us
-    on the host, the Stream object around it 3 us, as much as the launch)."""
-    return _raw_stream(dev) if stream is None else _stream_handle(stream)
-
-
-def _current_device(t: torch.Tensor, name: str) -> int:
-    """The tensor's device, which has to be the current one: kernels are launched there."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be on a CUDA device (there is no CPU path)")
-    dev = t.get_device()
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"{name} is on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
-    return dev
-
-
-def _check(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, dev: int) -> None:
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev \
-            and t.is_contiguous():
-        return
-    _need(t, name, dtype, shape)
-    raise ValueError(f"{name} must be on cuda:{dev}")
-
-
-def _new(shape: tuple, dtype: torch.dtype, dev: int, stream) -> torch.Tensor:
-    """An output, allocated for the stream that writes it."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream_handle(stream))
-    with torch.cuda.stream(s):
-        return torch.empty(shape, dtype=dtype, device=dev)
-
-
-def _stream_type(x: torch.Tensor, name: str) -> int:
-    t = _STREAM_TYPES.get(x.dtype)
-    if t is None:
-        raise TypeError(f"{name} must be torch.float32 or torch.bfloat16, got {x.dtype}")
-    return t
-
-
-def _rows_of(x: torch.Tensor, name: str) -> tuple:
-    if x.dim() not in (1, 2):
-        raise ValueError(f"{name} must have shape [rows, k] or [k], got {tuple(x.shape)}")
-    return (1, x.shape[0]) if x.dim() == 1 else (x.shape[0], x.shape[1])
-
-
-def _codes_out(rows: int, k: int, q, d, dev: int, stream, names=("q", "d")):
-    shape, scales = (rows, k), (rows, _blocks128(k))
-    if q is None:
-        q = _new(shape, _E4M3, dev, stream)
-    else:
-        _check(q, names[0], _E4M3, shape, dev)
-    if d is None:
-        d = _new(scales, torch.float32, dev, stream)
-    else:
-        _check(d, names[1], torch.float32, scales, dev)
-    return q, d
 
 
 def quantize_act_e4m3(x: torch.Tensor, q: torch.Tensor | None = None, d: torch.Tensor | None = None, stream=None):
     """f32 or bf16 [rows, k] (or [k]) -> (q float8_e4m3fn [rows, k], d f32 [rows, ceil(k/128)]);
     k a multiple of 16."""
-    dev = _current_device(x, "x")
-    kind = _stream_type(x, "x")
-    rows, k = _rows_of(x, "x")
-    _check(x, "x", x.dtype, x.shape, dev)
-    q, d = _codes_out(rows, k, q, d, dev, stream)
-    _lib.call("quantize_act_e4m3", x.data_ptr(), kind, rows, k, q.data_ptr(), d.data_ptr(), _stream_on(stream, dev))
-    return q, d
+    if stream is not None:
+        with _on(stream):
+            return quantize_act_e4m3(x, q, d)
+    return (_front or _load_front()).quantize_act(x, q, d)
 
 
 def rmsnorm_add_quantize_e4m3(x: torch.Tensor, gamma: torch.Tensor, residual: torch.Tensor | None = None,
@@ -897,44 +855,10 @@ def rmsnorm_add_quantize_e4m3(x: torch.Tensor, gamma: torch.Tensor, residual: to
 
     x, residual, s and gamma are all f32 or all bf16, [rows, k] (or [k]); s may be
     x or residual (the sum in place).  Without a residual s is x itself."""
-    dev = _current_device(x, "x")
-    kind = _stream_type(x, "x")
-    rows, k = _rows_of(x, "x")
-    _check(x, "x", x.dtype, x.shape, dev)
-    _check(gamma, "gamma", x.dtype, (k,), dev)
-    if residual is None:
-        if s is not None and s is not x:
-            raise ValueError("s is written only with a residual")
-        s = x
-    else:
-        _check(residual, "residual", x.dtype, x.shape, dev)
-        if s is None:
-            s = _new(x.shape, x.dtype, dev, stream)
-        else:
-            _check(s, "s", x.dtype, x.shape, dev)
-    q, d = _codes_out(rows, k, q, d, dev, stream)
-    _lib.call("rmsnorm_add_quantize_e4m3", x.data_ptr(), _ptr(residual), gamma.data_ptr(), kind, rows, k, eps,
-              s.data_ptr(), q.data_ptr(), d.data_ptr(), _stream_on(stream, dev))
-    return q, d, s
-
-
-def _check_e4m3_operands(codes, scales, blocks: int, xq, xd, dev: int):
-    """Shapes of a weight (`blocks` rows of scales) and the activations that it meets; returns (m, k)."""
-    if not isinstance(codes, torch.Tensor) or codes.dim() != 2:
-        raise ValueError("w.codes must be a tensor of shape [n_rows, k]")
-    n_rows, k = codes.shape
-    kb = _blocks128(k)
-    _check(codes, "w.codes", _E4M3, (n_rows, k), dev)
-    _check(scales, "w.scales", torch.float32, (blocks, kb), dev)
-    if xq.dim() == 1 and xd.dim() == 1:
-        m = 1
-        _check(xq, "xq", _E4M3, (k,), dev)
-        _check(xd, "xd", torch.float32, (kb,), dev)
-    else:
-        m = xq.shape[0]
-        _check(xq, "xq", _E4M3, (m, k), dev)
-        _check(xd, "xd", torch.float32, (m, kb), dev)
-    return m, k
+    if stream is not None:
+        with _on(stream):
+            return rmsnorm_add_quantize_e4m3(x, gamma, residual, eps, s, q, d)
+    return (_front or _load_front()).rmsnorm_add_quantize(x, gamma, residual, eps, s, q, d)
 
 
 def qgemm_e4m3(w: E4M3Weight, xq: torch.Tensor, xd: torch.Tensor, epilogue: str | int = "none",
@@ -943,45 +867,26 @@ def qgemm_e4m3(w: E4M3Weight, xq: torch.Tensor, xd: torch.Tensor, epilogue: str 
     """Block-scaled e4m3 product of m >= 0 activation rows; y [m, n_rows], f32 or
     bf16 (out_dtype, by default y's or the residual's type, else f32).  The
     residual has y's type and may be y itself."""
-    dev = _current_device(xq, "xq")
+    if stream is not None:
+        with _on(stream):
+            return qgemm_e4m3(w, xq, xd, epilogue, residual, y, out_dtype)
     epi = EPILOGUES[epilogue] if isinstance(epilogue, str) else int(epilogue)
-    n = w.codes.shape[0]
-    m, k = _check_e4m3_operands(w.codes, w.scales, _blocks128(n), xq, xd, dev)
-    if epi == QG_EPI_RESIDUAL_ADD:
-        if residual is None:
-            raise ValueError("the residual epilogue needs a residual")
-    elif residual is not None:
-        raise ValueError("a residual goes with epilogue='residual'")
-    if out_dtype is None:
-        out_dtype = y.dtype if y is not None else residual.dtype if residual is not None else torch.float32
-    kind = _STREAM_TYPES.get(out_dtype)
-    if kind is None:
-        raise TypeError(f"out_dtype must be torch.float32 or torch.bfloat16, got {out_dtype}")
-    if y is None:
-        y = _new((m, n), out_dtype, dev, stream)
-    else:
-        _check(y, "y", out_dtype, (m, n), dev)
-    if residual is not None:
-        _check(residual, "residual", out_dtype, (m, n), dev)
-    _lib.call("qgemm_e4m3", w.codes.data_ptr(), w.scales.data_ptr(), n, k, xq.data_ptr(), xd.data_ptr(), m, epi,
-              _ptr(residual), y.data_ptr(), kind, _stream_on(stream, dev))
-    return y
+    if out_dtype is not None:
+        kind = _STREAM_TYPES.get(out_dtype)
+        if kind is None:
+            raise TypeError(f"out_dtype must be torch.float32 or torch.bfloat16, got {out_dtype}")
+        out_dtype = kind
+    return (_front or _load_front()).qgemm(w.codes, w.scales, xq, xd, epi, residual, y, out_dtype)
 
 
 def qg_ffn_up_e4m3(w: E4M3Weight, xq: torch.Tensor, xd: torch.Tensor, hq: torch.Tensor | None = None,
                    hd: torch.Tensor | None = None, stream=None):
     """Stacked gate|up product, SiLU(g) * u and its quantization in one launch:
     (hq float8_e4m3fn [m, ffn], hd f32 [m, ceil(ffn/128)])."""
-    dev = _current_device(xq, "xq")
-    n2 = w.codes.shape[0]
-    if n2 % 32:
-        raise ValueError(f"a stacked gate|up weight has 2 ffn rows, ffn a multiple of 16: got {n2}")
-    ffn = n2 // 2
-    m, k = _check_e4m3_operands(w.codes, w.scales, 2 * _blocks128(ffn), xq, xd, dev)
-    hq, hd = _codes_out(m, ffn, hq, hd, dev, stream, ("hq", "hd"))
-    _lib.call("qg_ffn_up_e4m3", w.codes.data_ptr(), w.scales.data_ptr(), ffn, k, xq.data_ptr(), xd.data_ptr(), m,
-              hq.data_ptr(), hd.data_ptr(), _stream_on(stream, dev))
-    return hq, hd
+    if stream is not None:
+        with _on(stream):
+            return qg_ffn_up_e4m3(w, xq, xd, hq, hd)
+    return (_front or _load_front()).ffn_up(w.codes, w.scales, xq, xd, hq, hd)
 
 
 @dataclass
@@ -1020,30 +925,12 @@ def qg_ffn_e4m3(x: torch.Tensor, layer: E4M3Layer, residual: torch.Tensor | None
     """s = x + residual; y = s + down(SiLU(g) * u), (g|u) = gate|up(RMSNorm(s) * gamma),
     over m rows in three launches.  x, residual and y are [m, hidden], all f32 or all
     bf16; y may be x or residual (in place)."""
-    dev = _current_device(x, "x")
-    kind = _stream_type(x, "x")
-    m, hidden = _rows_of(x, "x")
-    ffn = layer.down.codes.shape[1]
-    hb, fb = _blocks128(hidden), _blocks128(ffn)
-    _check(x, "x", x.dtype, x.shape, dev)
-    if residual is not None:
-        _check(residual, "residual", x.dtype, x.shape, dev)
-    _check(layer.gamma, "layer.gamma", x.dtype, (hidden,), dev)
-    _check(layer.gate_up.codes, "layer.gate_up.codes", _E4M3, (2 * ffn, hidden), dev)
-    _check(layer.gate_up.scales, "layer.gate_up.scales", torch.float32, (2 * fb, hb), dev)
-    _check(layer.down.codes, "layer.down.codes", _E4M3, (hidden, ffn), dev)
-    _check(layer.down.scales, "layer.down.scales", torch.float32, (hb, fb), dev)
-    xq, xd = _codes_out(m, hidden, buf and buf.xq, buf and buf.xd, dev, stream, ("buf.xq", "buf.xd"))
-    hq, hd = _codes_out(m, ffn, buf and buf.hq, buf and buf.hd, dev, stream, ("buf.hq", "buf.hd"))
-    if y is None:
-        y = _new(x.shape, x.dtype, dev, stream)
-    else:
-        _check(y, "y", x.dtype, x.shape, dev)
-    _lib.call("qg_ffn_e4m3", x.data_ptr(), _ptr(residual), layer.gamma.data_ptr(), kind, m, hidden, ffn, eps,
-              layer.gate_up.codes.data_ptr(), layer.gate_up.scales.data_ptr(), layer.down.codes.data_ptr(),
-              layer.down.scales.data_ptr(), xq.data_ptr(), xd.data_ptr(), hq.data_ptr(), hd.data_ptr(), y.data_ptr(),
-              _stream_on(stream, dev))
-    return y
+    if stream is not None:
+        with _on(stream):
+            return qg_ffn_e4m3(x, layer, residual, eps, buf, y)
+    b = (buf.xq, buf.xd, buf.hq, buf.hd) if buf is not None else (None, None, None, None)
+    return (_front or _load_front()).ffn(x, residual, layer.gamma, layer.gate_up.codes, layer.gate_up.scales,
+                                         layer.down.codes, layer.down.scales, eps, *b, y)
 
 
 # --------------------------------------------------------------------------

@@ -150,7 +150,7 @@ def test_ffn_refusals(lib):
 
 # ---------------------------------------------------------------- binding refusals
 
-def test_binding_refuses_cpu_tensors():
+def test_binding_refuses_cpu_tensors(lib):
     torch = pytest.importorskip("torch")
     import block_quantized_decode_rmsnorm_gb300 as qg
 
