@@ -144,7 +144,7 @@ qg_status check_q8_k(int64_t k)
 
 // 8-bit floating point path
 constexpr int64_t kE4M3MaxM = int64_t(1) << 24;
-constexpr int64_t kE4M3FewRows = 16;  // activation rows that the few-row kernel takes
+constexpr int64_t kE4M3FewRows = 8;  // activation rows that the few-row kernel takes
 
 int64_t e4m3_kb(int64_t k) { return (k + 127) / 128; }
 bool dtype_ok(int t) { return t == QG_F32 || t == QG_BF16; }

@@ -1,5 +1,5 @@
-// The block-scaled e4m3 product for up to 16 activation rows: the weights are read
-// once, straight into the fragments of mma.sync m16n8k32.
+// The block-scaled e4m3 product for up to 8 activation rows: the weights are read
+// once, in the order in which mma.sync m16n8k32 takes them.
 //
 //   y[m][n] = sum_b (d_x[m][b] d_w[n/128][b]) S_b[m][n],  S_b = sum of x w over block b
 //
@@ -7,10 +7,18 @@
 // N side) over one block of 128 per step: four MMAs into a zeroed accumulator
 // give S_b, which one product and one FMA per value bring into the sum.  The
 // order of the values inside a block does not matter to S_b as long as both
-// operands agree, so lane 4g+c loads bytes 16c..16c+15 of each half of its rows'
+// operands agree, so lane 4g+c takes bytes 16c..16c+15 of each half of its rows'
 // block (two 64-byte pieces per row and instruction, whole sectors) and the eight
-// words serve as the MMAs' register pairs as they are.  Eight warps split the
-// blocks of k; their sums meet in shared memory in warp order.
+// words serve as the MMAs' register pairs as they are.  The warps of a CTA split
+// the blocks of k; their sums meet in shared memory in warp order.
+//
+// What bounds it is the bytes in flight: a lane copies its own pieces of the next
+// blocks to shared memory by cp.async (no barrier: nobody else reads them), without
+// registers, from before the previous kernel has ended on.  A product's CTA has eight
+// warps, so that few rows still fill the SMs' queues (1x1024x3584: 2.3 us; four CTAs
+// of a cluster sharing k took 3.5); gate|up has twice the rows and four warps per CTA,
+// four CTAs an SM, so that one wave holds them all (1x9216x2560: 10.5 us, 14.3 with
+// eight warps).
 //
 // Gate|up: 16 gate and the 16 matching up rows per CTA, eight CTAs of a cluster
 // hold the 128 outputs of one block of h, and exchange their largest magnitudes
@@ -19,9 +27,9 @@
 
 namespace qg {
 
-constexpr int RW = 8;           // warps per CTA
 constexpr int RR = 16;          // weight rows per CTA (and half, for gate|up)
 constexpr int UP_CLUSTER = EB / RR;
+constexpr int R_TILE = RR * EB; // bytes of one tile's block
 
 struct RowsArgs {
     const uint8_t *w;
@@ -49,19 +57,29 @@ __device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+template <bool UP>
+struct RowsLayout {
+    static constexpr int W = UP ? 4 : 8;   // warps per CTA
+    static constexpr int T = UP ? 2 : 1;   // weight tiles per CTA
+    static constexpr int D = UP ? 2 : 6;   // blocks on their way per warp
+    static constexpr int F = 3;            // blocks whose activations are
+    static constexpr int RING = W * D * T * R_TILE;  // 32 and 96 KB
+    static constexpr int CTAS = UP ? 4 : 2;          // per SM
+};
 
-// NT: groups of 8 activation rows; m <= 8 NT.
-template <int NT, bool UP>
-__global__ void __launch_bounds__(RW * 32, NT == 1 ? 3 : 2) rows_e4m3_kernel(const RowsArgs p)
+template <bool UP>
+__global__ void __launch_bounds__(RowsLayout<UP>::W * 32, RowsLayout<UP>::CTAS) rows_e4m3_kernel(const RowsArgs p)
 {
-    constexpr int RT = UP ? 2 : 1;  // weight tiles per CTA
-    constexpr int U = UP ? 1 : 2;   // blocks of k in flight per warp
-    __shared__ float red[RW][RT][NT * 8 * RR];
-    __shared__ float top[NT * 8];
+    using L = RowsLayout<UP>;
+    constexpr int RW = L::W, RT = L::T, D = L::D, F = L::F;
+    extern __shared__ __align__(16) uint8_t ring_raw[];  // [warp][slot][tile][row half][block half][lane] of 16 bytes
+    __shared__ float red[RW][RT][8 * RR];
+    __shared__ float top[8];  // gate|up: the rows' largest magnitudes
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, c = lane & 3;
     const int64_t n0 = static_cast<int64_t>(blockIdx.x) * RR;
+    const int slots = min(D, (p.kb + RW - 1) / RW);
+    uint8_t *ring = ring_raw + static_cast<size_t>(warp) * slots * RT * R_TILE + lane * 16;
 
     // this lane's two rows of each tile: columns 0 ..  of row n0 + g (+ 8)
     const uint8_t *wr[RT][2];
@@ -75,91 +93,95 @@ __global__ void __launch_bounds__(RW * 32, NT == 1 ? 3 : 2) rows_e4m3_kernel(con
             wr[t][h] = row < p.n ? p.w + ((t ? p.up_row : 0) + row) * p.k : nullptr;
         }
     }
-    pdl_wait();
-    pdl_trigger();
-
-    const uint8_t *xr[NT];
-    const float *xd[NT][2];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-        const int64_t row = 8 * j + g;
-        xr[j] = row < p.m ? p.x + row * p.k : nullptr;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int64_t r2 = 8 * j + 2 * c + h;
-            xd[j][h] = r2 < p.m ? p.xd + r2 * p.kb : nullptr;
-        }
-    }
-    float acc[RT][NT][4];
-#pragma unroll
-    for (int t = 0; t < RT; ++t)
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[t][j][i] = 0.0f;
-
-    for (int b0 = warp; b0 < p.kb; b0 += RW * U) {
-        uint4 wv[U][RT][2][2], xv[U][NT][2];
-        float sw[U][RT], sx[U][NT][2];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int b = b0 + u * RW;
-            const bool in = b < p.kb;
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const int col = b * EB + 64 * q + 16 * c;
-                const bool ok = in && col < p.k;
-#pragma unroll
-                for (int t = 0; t < RT; ++t)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        wv[u][t][h][q] = ok && wr[t][h] ? ld_stream_16B(wr[t][h] + col) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-                    xv[u][j][q] = ok && xr[j] ? ld_16B(xr[j] + col) : make_uint4(0, 0, 0, 0);
-            }
-#pragma unroll
-            for (int t = 0; t < RT; ++t) sw[u][t] = in ? wd[t][b] : 0.0f;
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) sx[u][j][h] = in && xd[j][h] ? xd[j][h][b] : 0.0f;
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (b0 + u * RW >= p.kb) break;
+    // this warp's i-th block, warp + RW i, into its slot: zeros where there are no
+    // weights; one group per block, empty past the last
+    auto stage = [&](int i) {
+        const int b = warp + RW * i;
+        if (b < p.kb) {
+            uint8_t *slot = ring + (i % D) * RT * R_TILE;
 #pragma unroll
             for (int t = 0; t < RT; ++t)
 #pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
-                        const uint4 a = wv[u][t][0][q], a8 = wv[u][t][1][q], x = xv[u][j][q];
-                        mma_e4m3(d, a.x, a8.x, a.y, a8.y, x.x, x.y);
-                        mma_e4m3(d, a.z, a8.z, a.w, a8.w, x.z, x.w);
+                        const int col = b * EB + 64 * q + 16 * c;
+                        uint8_t *to = slot + ((t * 2 + h) * 2 + q) * 512;
+                        if (wr[t][h] && col < p.k)
+                            cp_async_16(smem_addr(to), wr[t][h] + col);
+                        else
+                            *reinterpret_cast<uint4 *>(to) = make_uint4(0, 0, 0, 0);
                     }
-                    const float s0 = sx[u][j][0] * sw[u][t], s1 = sx[u][j][1] * sw[u][t];
-                    acc[t][j][0] = fmaf(d[0], s0, acc[t][j][0]);
-                    acc[t][j][1] = fmaf(d[1], s1, acc[t][j][1]);
-                    acc[t][j][2] = fmaf(d[2], s0, acc[t][j][2]);
-                    acc[t][j][3] = fmaf(d[3], s1, acc[t][j][3]);
-                }
         }
-    }
-    // [activation row][weight row]: d[0], d[1] are row g of activations 2c, 2c + 1, d[2], d[3] row g + 8
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < D; ++i) stage(i);
+    pdl_wait();
+    pdl_trigger();
+
+    const uint8_t *xr = g < p.m ? p.x + g * p.k : nullptr;
+    const float *xd[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) xd[h] = 2 * c + h < p.m ? p.xd + (2 * c + h) * p.kb : nullptr;
+    float acc[RT][4];
 #pragma unroll
     for (int t = 0; t < RT; ++t)
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+        for (int e = 0; e < 4; ++e) acc[t][e] = 0.0f;
+
+    // the activations and scales of the next F blocks, in registers
+    uint4 xn[F][2];
+    float fw[F][RT], fx[F][2];
+    auto fetch = [&](int u, int b) {
+        const bool in = b < p.kb;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                red[warp][t][(8 * j + 2 * c + (i & 1)) * RR + g + 8 * (i >> 1)] = acc[t][j][i];
+        for (int q = 0; q < 2; ++q) {
+            const int col = b * EB + 64 * q + 16 * c;
+            xn[u][q] = in && xr && col < p.k ? ld_16B(xr + col) : make_uint4(0, 0, 0, 0);
+            fx[u][q] = in && xd[q] ? xd[q][b] : 0.0f;
+        }
+#pragma unroll
+        for (int t = 0; t < RT; ++t) fw[u][t] = in ? wd[t][b] : 0.0f;
+    };
+#pragma unroll
+    for (int u = 0; u < F; ++u) fetch(u, warp + RW * u);
+#pragma unroll 1
+    for (int i0 = 0; warp + RW * i0 < p.kb; i0 += F) {
+#pragma unroll
+        for (int u = 0; u < F; ++u) {
+            const int i = i0 + u, b = warp + RW * i;
+            if (b >= p.kb) break;
+            cp_async_wait<D - 1>();
+            const uint8_t *slot = ring + (i % D) * RT * R_TILE;
+#pragma unroll
+            for (int t = 0; t < RT; ++t) {
+                float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const uint4 a = *reinterpret_cast<const uint4 *>(slot + (t * 4 + q) * 512);
+                    const uint4 a8 = *reinterpret_cast<const uint4 *>(slot + (t * 4 + 2 + q) * 512);
+                    mma_e4m3(d, a.x, a8.x, a.y, a8.y, xn[u][q].x, xn[u][q].y);
+                    mma_e4m3(d, a.z, a8.z, a.w, a8.w, xn[u][q].z, xn[u][q].w);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[t][e] = fmaf(d[e], fx[u][e & 1] * fw[u][t], acc[t][e]);
+            }
+            stage(i + D);  // into the slot just read
+            fetch(u, b + RW * F);
+        }
+    }
+    // [activation row][weight row]: values 0 and 1 are row g of activations 2c, 2c + 1, the others row g + 8
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) red[warp][t][(2 * c + (e & 1)) * RR + g + 8 * (e >> 1)] = acc[t][e];
     __syncthreads();
 
-    const int o = threadIdx.x;  // output: activation row o / 16, weight row o % 16
-    const int64_t row = o / RR, col = n0 + o % RR;
-    const bool mine = o < NT * 8 * RR, live = mine && row < p.m && col < p.n;
+    // a thread per output: activation row o / 16, weight row o % 16
+    const int o = threadIdx.x, row = o / RR;
+    const int64_t col = n0 + o % RR;
+    const bool mine = o < 8 * RR, live = mine && row < p.m && col < p.n;
     float v[RT];
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
@@ -172,15 +194,12 @@ __global__ void __launch_bounds__(RW * 32, NT == 1 ? 3 : 2) rows_e4m3_kernel(con
         float a = live ? fmaxf(fabsf(h), 0.0f) : 0.0f;
 #pragma unroll
         for (int s = RR / 2; s >= 1; s >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, s));
-        if (mine && o % RR == 0) top[o / RR] = a;
+        if (mine && o % RR == 0) top[row] = a;
         cluster_sync();
-        if (mine) {
-            a = 0.0f;
-#pragma unroll
-            for (int r = 0; r < UP_CLUSTER; ++r) a = fmaxf(a, ld_cluster_f32(&top[o / RR], r));
-        }
-        a = e4m3_floor(a);
         if (live) {
+#pragma unroll
+            for (int r = 0; r < UP_CLUSTER; ++r) a = fmaxf(a, ld_cluster_f32(&top[row], r));
+            a = e4m3_floor(a);
             p.hq[row * p.n + col] = static_cast<uint8_t>(e4m3_pack2(h * __fdiv_rn(448.0f, a), 0.0f));
             if (col % EB == 0) p.hd[row * e4m3_blocks(p.n) + col / EB] = __fdiv_rn(a, 448.0f);
         }
@@ -198,6 +217,18 @@ __global__ void __launch_bounds__(RW * 32, NT == 1 ? 3 : 2) rows_e4m3_kernel(con
     }
 }
 
+template <bool UP>
+static cudaError_t launch_rows(int64_t tiles, const RowsArgs &p, cudaStream_t s)
+{
+    using L = RowsLayout<UP>;
+    const int need = (p.kb + L::W - 1) / L::W;
+    const int bytes = L::W * (need < L::D ? need : L::D) * L::T * R_TILE;
+    if (cudaError_t e = opt_in_smem(reinterpret_cast<const void *>(rows_e4m3_kernel<UP>), L::RING); e != cudaSuccess)
+        return e;
+    return launch_pdl_cluster(rows_e4m3_kernel<UP>, dim3(static_cast<unsigned>(tiles)), dim3(L::W * 32),
+                              static_cast<size_t>(bytes), s, UP ? UP_CLUSTER : 1, p);
+}
+
 cudaError_t launch_rows_e4m3(const uint8_t *w, const float *wd, int64_t n, int64_t k, const uint8_t *x, const float *xd,
                              int64_t m, const void *residual, void *y, int y_dtype, cudaStream_t s)
 {
@@ -213,9 +244,7 @@ cudaError_t launch_rows_e4m3(const uint8_t *w, const float *wd, int64_t n, int64
     p.residual = residual;
     p.y = y;
     p.y_bf16 = y_dtype == QG_BF16;
-    const unsigned gx = static_cast<unsigned>((n + RR - 1) / RR);
-    if (m <= 8) return launch_pdl(rows_e4m3_kernel<1, false>, dim3(gx), dim3(RW * 32), 0, s, p);
-    return launch_pdl(rows_e4m3_kernel<2, false>, dim3(gx), dim3(RW * 32), 0, s, p);
+    return launch_rows<false>((n + RR - 1) / RR, p, s);
 }
 
 cudaError_t launch_rows_up_e4m3(const uint8_t *w, const float *wd, int64_t ffn, int64_t k, const uint8_t *x,
@@ -234,9 +263,7 @@ cudaError_t launch_rows_up_e4m3(const uint8_t *w, const float *wd, int64_t ffn, 
     p.m = m;
     p.hq = hq;
     p.hd = hd;
-    const unsigned gx = static_cast<unsigned>(e4m3_blocks(ffn) * UP_CLUSTER);
-    if (m <= 8) return launch_pdl_cluster(rows_e4m3_kernel<1, true>, dim3(gx), dim3(RW * 32), 0, s, UP_CLUSTER, p);
-    return launch_pdl_cluster(rows_e4m3_kernel<2, true>, dim3(gx), dim3(RW * 32), 0, s, UP_CLUSTER, p);
+    return launch_rows<true>(e4m3_blocks(ffn) * UP_CLUSTER, p, s);
 }
 
 }  // namespace qg

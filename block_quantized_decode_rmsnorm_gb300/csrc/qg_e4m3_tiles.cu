@@ -24,6 +24,7 @@
 //
 // Every barrier wait is bounded by the global timer; a stalled pipeline aborts (NaN
 // outputs for the tiles left) instead of hanging.
+#include <algorithm>
 #include <cuda.h>
 
 #include "qg_e4m3.cuh"
@@ -35,6 +36,7 @@ constexpr int TM = 128;    // activation rows per tile
 constexpr int T_CW = 64;   // tile columns per epilogue warp
 constexpr int T_XP = 9;    // row stride (floats) of a warp's 32 x 8 transpose buffer
 constexpr int T_SB = 4;    // blocks of k per buffer of scales
+constexpr int T_STAGES = 8;  // stages at most
 
 template <int BN>
 struct TileLayout {
@@ -42,16 +44,16 @@ struct TileLayout {
     static constexpr int EW = 4 * CG;     // epilogue warps: four lane quarters x column groups
     static constexpr int TMA_WARP = EW, MMA_WARP = EW + 1, SCALE_WARP = EW + 2;
     static constexpr int THREADS = (EW + 3) * 32;
-    static constexpr int A = TM * EB;
-    static constexpr int STAGE = A + BN * EB;
+    static constexpr int W = BN * EB;          // a stage: the weights' slab, then the activations'
+    static constexpr int STAGE = W + TM * EB;
     static constexpr int FIT = 196608 / STAGE;
-    static constexpr int STAGES = FIT < 8 ? FIT : 8;
+    static constexpr int STAGES = FIT < T_STAGES ? FIT : T_STAGES;
     static constexpr int TMEM = BN == 192 ? 512 : 2 * BN;   // columns allocated: a power of two
     static constexpr int UP_BYTES = STAGES * STAGE + 1024;  // + alignment of the base
     static constexpr int BYTES = UP_BYTES + EW * 32 * T_XP * 4;
+    static constexpr int SPLIT_CTAS = BN == 64 ? 2 : 1;     // per SM, of the split kernel
     static constexpr int LD = BN + 4;                       // row stride (floats) of a split tile's sums
-    static constexpr int SPLIT_BYTES = (STAGES * STAGE > TM * LD * 4 ? STAGES * STAGE : TM * LD * 4) + 1024;
-    static_assert(BYTES <= 220 * 1024 && SPLIT_BYTES <= 220 * 1024, "shared memory");
+    static_assert(BYTES <= 220 * 1024 && STAGES >= 3, "shared memory");
 };
 
 struct TileArgs {
@@ -61,7 +63,8 @@ struct TileArgs {
     int kb;
     int m_tiles, tiles;
     int box_m;           // activation rows per copy
-    int split;
+    int split;           // CTAs per tile, and of each the stages and their bytes
+    int stages, stage;
     const void *residual;
     void *y;
     int y_bf16;
@@ -82,7 +85,7 @@ __device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a, uint64_t b,
 // activation row two, as a tile's columns lie in at most two blocks of weight rows
 // (gate|up: the gate's and the up's).
 struct TileShared {
-    uint64_t full[8], done[8], tempty[2], sfull[2], sempty[2];
+    uint64_t full[T_STAGES], done[T_STAGES], tempty[2], sfull[2], sempty[2];
     float2 f[2][T_SB][TM];
     uint32_t tmem;
     int abort_flag;
@@ -101,7 +104,7 @@ __device__ __forceinline__ void tile_setup(TileShared &b, int warp)
     using L = TileLayout<BN>;
     if (threadIdx.x == 0) {
         b.abort_flag = 0;
-        for (int i = 0; i < L::STAGES; ++i) {
+        for (int i = 0; i < T_STAGES; ++i) {
             mbar_init(&b.full[i], 1);  // the copy thread's expect_tx
             mbar_init(&b.done[i], 1);  // the MMA thread's commit
         }
@@ -144,26 +147,55 @@ __device__ __forceinline__ bool elect_one()
 // done[s] completes when the MMAs that read stage s have: the stage may be filled
 // again, and the block's sums may be read.  (One commit for both: a second one per
 // block cost the issuing thread as much as an MMA.)  The copy warp is never more than
-// STAGES blocks and the epilogue never more than two behind it, so that a phase's
-// parity says which one it is.
+// the stages' number of blocks and the epilogue never more than two behind it, so that
+// a phase's parity says which one it is.
 
-// Copies of blocks [kb0, kb1) of one tile; `it` counts blocks over all tiles.
+// Number and bytes of the stages: the layout's, or what a split tile's launch chose.
+template <int BN, bool SPLIT>
+__device__ __forceinline__ uint32_t stages_of(const TileArgs &p)
+{
+    return SPLIT ? p.stages : TileLayout<BN>::STAGES;
+}
+template <int BN, bool SPLIT>
+__device__ __forceinline__ uint32_t stage_bytes(const TileArgs &p)
+{
+    return SPLIT ? p.stage : TileLayout<BN>::STAGE;
+}
+
 template <int BN, bool UP>
+__device__ __forceinline__ void copy_weights(const CUtensorMap &tw, const TileArgs &p, TileShared &b, uint8_t *st,
+                                             uint32_t s, int n0, int kb)
+{
+    mbar_expect_tx(&b.full[s], (p.box_m + BN) * EB);
+    tma_load_2d(st, &tw, kb * EB, n0, &b.full[s]);
+    if constexpr (UP) tma_load_2d(st + 128 * EB, &tw, kb * EB, static_cast<int>(p.up_row + n0), &b.full[s]);
+}
+
+// Copies of blocks [kb0, kb1) of one tile; `it` counts blocks over all tiles.  A split
+// tile's first weights go out before the wait for the previous kernel, which makes the
+// activations.
+template <int BN, bool UP, bool SPLIT>
 __device__ __forceinline__ bool tile_copies(const CUtensorMap &tx, const CUtensorMap &tw, const TileArgs &p,
                                             TileShared &b, uint8_t *smem, int m0, int n0, int kb0, int kb1,
                                             uint32_t &it)
 {
     using L = TileLayout<BN>;
+    const uint32_t S = stages_of<BN, SPLIT>(p), bytes = stage_bytes<BN, SPLIT>(p);
+    int early = kb0;  // weights of the blocks before this one are on their way
+    if constexpr (SPLIT) {
+        early = min(kb1, kb0 + static_cast<int>(S));
+        if (elect_one())
+            for (int kb = kb0; kb < early; ++kb) copy_weights<BN, UP>(tw, p, b, smem + (kb - kb0) * bytes, kb - kb0, n0, kb);
+        __syncwarp();
+        pdl_wait();
+    }
     for (int kb = kb0; kb < kb1; ++kb, ++it) {
-        const uint32_t s = it % L::STAGES, use = it / L::STAGES;
+        const uint32_t s = it % S, use = it / S;
         if (!__all_sync(0xffffffffu, stage_wait(&b.done[s], (use & 1) ^ 1, &b.abort_flag))) return false;
         if (elect_one()) {
-            uint8_t *st = smem + s * L::STAGE;
-            mbar_expect_tx(&b.full[s], (p.box_m + BN) * EB);
-            tma_load_2d(st, &tx, kb * EB, m0, &b.full[s]);
-            tma_load_2d(st + L::A, &tw, kb * EB, n0, &b.full[s]);
-            if constexpr (UP)
-                tma_load_2d(st + L::A + 128 * EB, &tw, kb * EB, static_cast<int>(p.up_row + n0), &b.full[s]);
+            uint8_t *st = smem + s * bytes;
+            if (kb >= early) copy_weights<BN, UP>(tw, p, b, st, s, n0, kb);
+            tma_load_2d(st + L::W, &tx, kb * EB, m0, &b.full[s]);
         }
         __syncwarp();
     }
@@ -171,20 +203,22 @@ __device__ __forceinline__ bool tile_copies(const CUtensorMap &tx, const CUtenso
 }
 
 // The MMAs of one tile's blocks, each into its own TMEM buffer.
-template <int BN>
-__device__ __forceinline__ bool tile_mmas(TileShared &b, uint32_t tmem, uint64_t desc0, int blocks, uint32_t &it)
+template <int BN, bool SPLIT>
+__device__ __forceinline__ bool tile_mmas(const TileArgs &p, TileShared &b, uint32_t tmem, uint64_t desc0, int blocks,
+                                          uint32_t &it)
 {
     using L = TileLayout<BN>;
+    const uint32_t S = stages_of<BN, SPLIT>(p), step = stage_bytes<BN, SPLIT>(p) >> 4;
     // D f32, A and B e4m3, both K-major
     constexpr uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(BN >> 3) << 17) | (static_cast<uint32_t>(TM >> 4) << 24);
     for (int i = 0; i < blocks; ++i, ++it) {
-        const uint32_t s = it % L::STAGES, use = it / L::STAGES, t = it & 1, tuse = it >> 1;
+        const uint32_t s = it % S, use = it / S, t = it & 1, tuse = it >> 1;
         const bool ok = stage_wait(&b.full[s], use & 1, &b.abort_flag) &&
                         stage_wait(&b.tempty[t], (tuse & 1) ^ 1, &b.abort_flag);
         if (!__all_sync(0xffffffffu, ok)) return false;
         tc_fence_after();
         if (elect_one()) {
-            const uint64_t a = desc0 + s * (L::STAGE >> 4), w = a + (L::A >> 4);  // the address field, in 16 bytes
+            const uint64_t w = desc0 + s * step, a = w + (L::W >> 4);  // the address field, in 16 bytes
 #pragma unroll
             for (int k = 0; k < EB / 32; ++k) umma_f8(tmem + t * BN, a + 2 * k, w + 2 * k, idesc, k != 0);
             umma_commit(&b.done[s]);
@@ -237,8 +271,8 @@ __device__ __forceinline__ bool tile_scales(const TileArgs &p, TileShared &b, in
 
 // The sums of blocks [kb0, kb1) of one tile in registers: two halves of 32 columns of
 // this thread's row, in adjacent pairs.  `it` counts blocks, `c` buffers of scales.
-template <int BN, bool UP>
-__device__ __forceinline__ bool tile_sums(TileShared &b, uint32_t tmem, int q, int cg, int lane, int n0, int kb0,
+template <int BN, bool UP, bool SPLIT>
+__device__ __forceinline__ bool tile_sums(const TileArgs &p, TileShared &b, uint32_t tmem, int q, int cg, int lane, int n0, int kb0,
                                           int kb1, uint32_t &it, uint32_t &c, uint64_t (&acc)[2][16])
 {
 #pragma unroll
@@ -263,7 +297,8 @@ __device__ __forceinline__ bool tile_sums(TileShared &b, uint32_t tmem, int q, i
                 __syncwarp();
                 if (elect_one()) mbar_arrive(&b.sempty[sb]);
             }
-            const uint32_t t = it & 1, s = it % TileLayout<BN>::STAGES, use = it / TileLayout<BN>::STAGES;
+            const uint32_t t = it & 1, s = it % stages_of<BN, SPLIT>(p),
+                           use = it / stages_of<BN, SPLIT>(p);
             // tcgen05.ld is warp-collective: the whole warp proceeds or stops
             if (!__all_sync(0xffffffffu, stage_wait(&b.done[s], use & 1, &b.abort_flag))) return false;
             tc_fence_after();
@@ -424,14 +459,14 @@ __global__ void __launch_bounds__(TileLayout<BN>::THREADS, 1)
     bool ok = true;
     if (warp == L::TMA_WARP) {
         for (int tile = blockIdx.x; ok && tile < p.tiles; tile += gridDim.x)
-            ok = tile_copies<BN, UP>(tx, tw, p, b, smem, (tile % p.m_tiles) * TM,
+            ok = tile_copies<BN, UP, false>(tx, tw, p, b, smem, (tile % p.m_tiles) * TM,
                                      (tile / p.m_tiles) * BO, 0, p.kb, it);
         // After an abort the last copies may still be landing: let them finish
         // (bounded) before the CTA's shared memory goes away.
         if (!ok && it > 0) mbar_wait_bounded(&b.full[(it - 1) % L::STAGES], ((it - 1) / L::STAGES) & 1, kCopyWaitLimitNs);
     } else if (warp == L::MMA_WARP) {
         for (int tile = blockIdx.x; ok && tile < p.tiles; tile += gridDim.x)
-            ok = tile_mmas<BN>(b, tmem, desc0, p.kb, it);
+            ok = tile_mmas<BN, false>(p, b, tmem, desc0, p.kb, it);
         // After an abort, wait (bounded) for the last issued MMAs before TMEM is freed.
         if (!ok && it > 0) mbar_wait_bounded(&b.done[(it - 1) % L::STAGES], ((it - 1) / L::STAGES) & 1, kCopyWaitLimitNs);
     } else if (warp == L::SCALE_WARP) {
@@ -443,7 +478,7 @@ __global__ void __launch_bounds__(TileLayout<BN>::THREADS, 1)
         uint32_t parity = 0;
         for (int tile = blockIdx.x; tile < p.tiles; tile += gridDim.x, parity ^= 1) {
             uint64_t acc[2][16];
-            ok = ok && tile_sums<BN, UP>(b, tmem, q, cg, lane, tile / p.m_tiles * BO, 0, p.kb, it, c, acc);
+            ok = ok && tile_sums<BN, UP, false>(p, b, tmem, q, cg, lane, tile / p.m_tiles * BO, 0, p.kb, it, c, acc);
             if (!ok) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
@@ -530,7 +565,7 @@ __device__ __forceinline__ float4 cluster_sum4(const float *at, int split)
 }
 
 template <int BN, bool UP>
-__global__ void __launch_bounds__(TileLayout<BN>::THREADS, 1)
+__global__ void __launch_bounds__(TileLayout<BN>::THREADS, TileLayout<BN>::SPLIT_CTAS)
     split_e4m3_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tw, const TileArgs p)
 {
     using L = TileLayout<BN>;
@@ -546,7 +581,6 @@ __global__ void __launch_bounds__(TileLayout<BN>::THREADS, 1)
     const int kb1 = static_cast<int>(static_cast<int64_t>(rank + 1) * p.kb / p.split);
     tile_setup<BN>(b, warp);
     pdl_trigger();
-    pdl_wait();
 
     const int q = warp & 3, cg = warp >> 2;
     const uint32_t tmem = __shfl_sync(0xffffffffu, b.tmem, 0);
@@ -555,15 +589,18 @@ __global__ void __launch_bounds__(TileLayout<BN>::THREADS, 1)
     bool ok = true;
     uint64_t acc[2][16];
     if (warp == L::TMA_WARP) {
-        ok = tile_copies<BN, UP>(tx, tw, p, b, smem, m0, n0, kb0, kb1, it);
-        if (!ok && it > 0) mbar_wait_bounded(&b.full[(it - 1) % L::STAGES], ((it - 1) / L::STAGES) & 1, kCopyWaitLimitNs);
+        ok = tile_copies<BN, UP, true>(tx, tw, p, b, smem, m0, n0, kb0, kb1, it);
+        if (!ok && it > 0) mbar_wait_bounded(&b.full[(it - 1) % p.stages], ((it - 1) / p.stages) & 1, kCopyWaitLimitNs);
     } else if (warp == L::MMA_WARP) {
-        ok = tile_mmas<BN>(b, tmem, desc0, kb1 - kb0, it);
-        if (!ok && it > 0) mbar_wait_bounded(&b.done[(it - 1) % L::STAGES], ((it - 1) / L::STAGES) & 1, kCopyWaitLimitNs);
+        pdl_wait();
+        ok = tile_mmas<BN, true>(p, b, tmem, desc0, kb1 - kb0, it);
+        if (!ok && it > 0) mbar_wait_bounded(&b.done[(it - 1) % p.stages], ((it - 1) / p.stages) & 1, kCopyWaitLimitNs);
     } else if (warp == L::SCALE_WARP) {
+        pdl_wait();
         tile_scales<BN, UP>(p, b, lane, m0, n0, kb0, kb1, c);
     } else {
-        ok = tile_sums<BN, UP>(b, tmem, q, cg, lane, n0, kb0, kb1, it, c, acc);
+        pdl_wait();
+        ok = tile_sums<BN, UP, true>(p, b, tmem, q, cg, lane, n0, kb0, kb1, it, c, acc);
     }
     tc_fence_before();
     __syncthreads();  // every copy has landed and every MMA is done: the stages are free
@@ -703,20 +740,26 @@ static cudaError_t launch_split(const uint8_t *w, int64_t w_rows, int64_t k, con
     CUtensorMap tx, tw;
     p.split = split;
     if (cudaError_t e = tile_maps<BN, UP>(w, w_rows, k, x, p, tx, tw); e != cudaSuccess) return e;
-    if (cudaError_t e = opt_in_smem(reinterpret_cast<const void *>(split_e4m3_kernel<BN, UP>), L::SPLIT_BYTES);
+    // Stages for the blocks that a CTA has, as far as they fit: two at least where it has
+    // as many.  The MMA reads 128 rows of activations whatever the copies bring: room for
+    // them behind the last stage (their sums are not looked at).
+    p.stage = L::W + p.box_m * EB;
+    const int blocks = (p.kb + split - 1) / split, pad = (TM - p.box_m) * EB;
+    const int room = (L::SPLIT_CTAS == 2 ? 100 : 210) * 1024 - pad;
+    p.stages = std::min({blocks, T_STAGES, room / p.stage});
+    const int rows = static_cast<int>(std::min<int64_t>(p.m, TM));
+    const int bytes = std::max(p.stages * p.stage + pad, rows * L::LD * 4) + 1024;
+    if (cudaError_t e = opt_in_smem(reinterpret_cast<const void *>(split_e4m3_kernel<BN, UP>), 215 * 1024);
         e != cudaSuccess)
         return e;
     return launch_pdl_cluster(split_e4m3_kernel<BN, UP>, dim3(static_cast<unsigned>(p.tiles * split)), dim3(L::THREADS),
-                              static_cast<size_t>(L::SPLIT_BYTES), s, static_cast<unsigned>(split), tx, tw, p);
+                              static_cast<size_t>(bytes), s, static_cast<unsigned>(split), tx, tw, p);
 }
 
-// CTAs per tile: a power of two up to 8 that leaves each a block of k and does not
-// pass the SM count.
-static int split_of(int64_t tiles, int64_t kb)
+// CTAs per tile: as many as `slots` places allow, each with a block of k at least.
+static int split_of(int64_t tiles, int64_t kb, int64_t slots)
 {
-    int split = 1;
-    while (split < 8 && 2 * split <= kb && tiles * split * 2 <= num_sms()) split *= 2;
-    return split;
+    return static_cast<int>(std::max<int64_t>(1, std::min({int64_t(8), kb, slots / tiles})));
 }
 
 cudaError_t launch_tiles_e4m3(const uint8_t *w, const float *wd, int64_t n, int64_t k, const uint8_t *x,
@@ -735,9 +778,9 @@ cudaError_t launch_tiles_e4m3(const uint8_t *w, const float *wd, int64_t n, int6
                reinterpret_cast<uintptr_t>(residual) % 32 == 0;
     const int64_t sms = num_sms(), mt = (m + TM - 1) / TM;
     if (const int64_t t = mt * ((n + 63) / 64); t <= sms)
-        return launch_split<64, false>(w, n, k, x, p, split_of(t, p.kb), s);
+        return launch_split<64, false>(w, n, k, x, p, split_of(t, p.kb, 2 * sms), s);
     if (const int64_t t = mt * ((n + 127) / 128); t <= sms)
-        return launch_split<128, false>(w, n, k, x, p, split_of(t, p.kb), s);
+        return launch_split<128, false>(w, n, k, x, p, split_of(t, p.kb, sms), s);
     // the tile width whose busiest SM covers the fewest columns
     int best = 256;
     int64_t cost = INT64_MAX;
@@ -764,7 +807,7 @@ cudaError_t launch_tiles_up_e4m3(const uint8_t *w, const float *wd, int64_t ffn,
     p.hq = hq;
     p.hd = hd;
     const int64_t tiles = (m + TM - 1) / TM * e4m3_blocks(ffn);
-    if (tiles <= num_sms()) return launch_split<256, true>(w, 2 * ffn, k, x, p, split_of(tiles, p.kb), s);
+    if (tiles <= num_sms()) return launch_split<256, true>(w, 2 * ffn, k, x, p, split_of(tiles, p.kb, num_sms()), s);
     return launch_tiles<256, true>(w, 2 * ffn, k, x, p, s);
 }
 
