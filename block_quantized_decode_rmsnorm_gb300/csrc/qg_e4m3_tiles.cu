@@ -6,7 +6,7 @@
 // A tile is 128 activation rows (TMEM lanes) by BN weight rows (TMEM columns).  Per
 // block of 128, one thread copies the 128-byte wide slabs of both operands by TMA
 // (128-byte swizzle), one thread issues four tcgen05.mma kind::f8f6f4 (K = 32) into
-// one of two TMEM buffers, and the epilogue warps bring the block sum into f32
+// one of two to four TMEM buffers, and the epilogue warps bring the block sum into f32
 // registers: a warp takes a quarter of the lanes and 64 columns, a thread one
 // activation row of them.  Those lie in one block of weight rows, so the factor
 // d_x d_w is one register and a value costs half a packed FMA.  One more warp reads
@@ -37,6 +37,7 @@ constexpr int T_CW = 64;   // tile columns per epilogue warp
 constexpr int T_XP = 9;    // row stride (floats) of a warp's 32 x 8 transpose buffer
 constexpr int T_SB = 4;    // blocks of k per buffer of scales
 constexpr int T_STAGES = 8;  // stages at most
+constexpr int T_SPLIT = 6;   // CTAs sharing a tile at most
 
 template <int BN>
 struct TileLayout {
@@ -48,12 +49,17 @@ struct TileLayout {
     static constexpr int STAGE = W + TM * EB;
     static constexpr int FIT = 196608 / STAGE;
     static constexpr int STAGES = FIT < T_STAGES ? FIT : T_STAGES;
-    static constexpr int TMEM = BN == 192 ? 512 : 2 * BN;   // columns allocated: a power of two
+    // TMEM buffers: narrow tiles' blocks take less time than it takes from an MMA's issue
+    // to its buffer's release, so they have four on their way (two CTAs an SM share TMEM
+    // where BN is 64).  Never more than the stages, or a phase could be missed.
+    static constexpr int BUFS = BN <= 128 ? 4 : 2;
+    static constexpr int TMEM = BN == 192 ? 512 : BUFS * BN;  // columns allocated: a power of two
     static constexpr int UP_BYTES = STAGES * STAGE + 1024;  // + alignment of the base
     static constexpr int BYTES = UP_BYTES + EW * 32 * T_XP * 4;
     static constexpr int SPLIT_CTAS = BN == 64 ? 2 : 1;     // per SM, of the split kernel
+    static constexpr int SPLIT_ROOM = (SPLIT_CTAS == 2 ? 100 : 210) * 1024;  // shared memory of its stages at most
     static constexpr int LD = BN + 4;                       // row stride (floats) of a split tile's sums
-    static_assert(BYTES <= 220 * 1024 && STAGES >= 3, "shared memory");
+    static_assert(BYTES <= 220 * 1024 && STAGES >= BUFS, "shared memory");
 };
 
 struct TileArgs {
@@ -85,7 +91,7 @@ __device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a, uint64_t b,
 // activation row two, as a tile's columns lie in at most two blocks of weight rows
 // (gate|up: the gate's and the up's).
 struct TileShared {
-    uint64_t full[T_STAGES], done[T_STAGES], tempty[2], sfull[2], sempty[2];
+    uint64_t full[T_STAGES], done[T_STAGES], tempty[4], sfull[2], sempty[2];
     float2 f[2][T_SB][TM];
     uint32_t tmem;
     int abort_flag;
@@ -108,8 +114,8 @@ __device__ __forceinline__ void tile_setup(TileShared &b, int warp)
             mbar_init(&b.full[i], 1);  // the copy thread's expect_tx
             mbar_init(&b.done[i], 1);  // the MMA thread's commit
         }
+        for (int i = 0; i < L::BUFS; ++i) mbar_init(&b.tempty[i], L::EW);  // one arrival per epilogue warp
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&b.tempty[i], L::EW);  // one arrival per epilogue warp
             mbar_init(&b.sfull[i], 1);       // the scale warp
             mbar_init(&b.sempty[i], L::EW);  // one arrival per epilogue warp
         }
@@ -147,8 +153,9 @@ __device__ __forceinline__ bool elect_one()
 // done[s] completes when the MMAs that read stage s have: the stage may be filled
 // again, and the block's sums may be read.  (One commit for both: a second one per
 // block cost the issuing thread as much as an MMA.)  The copy warp is never more than
-// the stages' number of blocks and the epilogue never more than two behind it, so that
-// a phase's parity says which one it is.
+// the stages' number of blocks ahead of the MMAs, nor the MMAs more than the buffers'
+// number, which is no larger, ahead of the epilogue: a phase's parity says which one
+// it is.
 
 // Number and bytes of the stages: the layout's, or what a split tile's launch chose.
 template <int BN, bool SPLIT>
@@ -212,7 +219,7 @@ __device__ __forceinline__ bool tile_mmas(const TileArgs &p, TileShared &b, uint
     // D f32, A and B e4m3, both K-major
     constexpr uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(BN >> 3) << 17) | (static_cast<uint32_t>(TM >> 4) << 24);
     for (int i = 0; i < blocks; ++i, ++it) {
-        const uint32_t s = it % S, use = it / S, t = it & 1, tuse = it >> 1;
+        const uint32_t s = it % S, use = it / S, t = it % L::BUFS, tuse = it / L::BUFS;
         const bool ok = stage_wait(&b.full[s], use & 1, &b.abort_flag) &&
                         stage_wait(&b.tempty[t], (tuse & 1) ^ 1, &b.abort_flag);
         if (!__all_sync(0xffffffffu, ok)) return false;
@@ -297,7 +304,7 @@ __device__ __forceinline__ bool tile_sums(const TileArgs &p, TileShared &b, uint
                 __syncwarp();
                 if (elect_one()) mbar_arrive(&b.sempty[sb]);
             }
-            const uint32_t t = it & 1, s = it % stages_of<BN, SPLIT>(p),
+            const uint32_t t = it % TileLayout<BN>::BUFS, s = it % stages_of<BN, SPLIT>(p),
                            use = it / stages_of<BN, SPLIT>(p);
             // tcgen05.ld is warp-collective: the whole warp proceeds or stops
             if (!__all_sync(0xffffffffu, stage_wait(&b.done[s], use & 1, &b.abort_flag))) return false;
@@ -745,21 +752,62 @@ static cudaError_t launch_split(const uint8_t *w, int64_t w_rows, int64_t k, con
     // them behind the last stage (their sums are not looked at).
     p.stage = L::W + p.box_m * EB;
     const int blocks = (p.kb + split - 1) / split, pad = (TM - p.box_m) * EB;
-    const int room = (L::SPLIT_CTAS == 2 ? 100 : 210) * 1024 - pad;
-    p.stages = std::min({blocks, T_STAGES, room / p.stage});
+    p.stages = std::min({blocks, T_STAGES, (L::SPLIT_ROOM - pad) / p.stage});
     const int rows = static_cast<int>(std::min<int64_t>(p.m, TM));
     const int bytes = std::max(p.stages * p.stage + pad, rows * L::LD * 4) + 1024;
-    if (cudaError_t e = opt_in_smem(reinterpret_cast<const void *>(split_e4m3_kernel<BN, UP>), 215 * 1024);
+    if (cudaError_t e = opt_in_smem(reinterpret_cast<const void *>(split_e4m3_kernel<BN, UP>), L::SPLIT_ROOM + 1024);
         e != cudaSuccess)
         return e;
     return launch_pdl_cluster(split_e4m3_kernel<BN, UP>, dim3(static_cast<unsigned>(p.tiles * split)), dim3(L::THREADS),
                               static_cast<size_t>(bytes), s, static_cast<unsigned>(split), tx, tw, p);
 }
 
-// CTAs per tile: as many as `slots` places allow, each with a block of k at least.
-static int split_of(int64_t tiles, int64_t kb, int64_t slots)
+// How many clusters of `split` CTAs the device holds at once (asked once per device).
+// A cluster stays inside one processing cluster of the chip, of 18 to 20 SMs: 46
+// clusters of 6 CTAs at two an SM, but 30 of 7.  A grid one cluster too large takes
+// twice as long (2560 columns, 17 rows, k = 9216: 9.0 us with 6 a tile, 15.4 with 7).
+// The query is made for one CTA an SM, which is all that it counts for a kernel of
+// this kind.
+template <int BN, bool UP>
+static int clusters_at_once(int split)
 {
-    return static_cast<int>(std::max<int64_t>(1, std::min({int64_t(8), kb, slots / tiles})));
+    using L = TileLayout<BN>;
+    static std::mutex mu;
+    static int cache[64][T_SPLIT + 1] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    std::lock_guard<std::mutex> lock(mu);
+    int &n = cache[dev][split];
+    if (n == 0) {
+        cudaLaunchAttribute attr = {};
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim = {static_cast<unsigned>(split), 1, 1};
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(split);
+        cfg.blockDim = dim3(L::THREADS);
+        cfg.dynamicSmemBytes = L::SPLIT_ROOM + 1024;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        int one = 0;
+        if (opt_in_smem(reinterpret_cast<const void *>(split_e4m3_kernel<BN, UP>), L::SPLIT_ROOM + 1024) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&one, split_e4m3_kernel<BN, UP>, &cfg) != cudaSuccess || one <= 0) {
+            cudaGetLastError();
+            one = 1;
+        }
+        n = one * L::SPLIT_CTAS;
+    }
+    return n;
+}
+
+// CTAs per tile: the most that find room at once with four blocks of k each, below
+// which the cluster's own cost is no longer earned (gate|up 16x3584x1024: 5.4 us with
+// 2 of 4 blocks, 6.1 with 5).
+template <int BN, bool UP>
+static int split_of(int64_t tiles, int64_t kb)
+{
+    for (int split = T_SPLIT; split > 1; --split)
+        if (4 * split <= kb && tiles <= clusters_at_once<BN, UP>(split)) return split;
+    return 1;
 }
 
 cudaError_t launch_tiles_e4m3(const uint8_t *w, const float *wd, int64_t n, int64_t k, const uint8_t *x,
@@ -777,10 +825,11 @@ cudaError_t launch_tiles_e4m3(const uint8_t *w, const float *wd, int64_t n, int6
     p.rows32 = n % (p.y_bf16 ? 16 : 8) == 0 && reinterpret_cast<uintptr_t>(y) % 32 == 0 &&
                reinterpret_cast<uintptr_t>(residual) % 32 == 0;
     const int64_t sms = num_sms(), mt = (m + TM - 1) / TM;
-    if (const int64_t t = mt * ((n + 63) / 64); t <= sms)
-        return launch_split<64, false>(w, n, k, x, p, split_of(t, p.kb, 2 * sms), s);
-    if (const int64_t t = mt * ((n + 127) / 128); t <= sms)
-        return launch_split<128, false>(w, n, k, x, p, split_of(t, p.kb, sms), s);
+    // Too few tiles for the SMs: 64 columns wide, and a cluster to each.  Where a cluster of
+    // two does not find room the walk over wider tiles is as fast or faster (512x2560x9216:
+    // 25.8 us against 33.3 with one CTA to each tile of 64).
+    if (const int split = split_of<64, false>(mt * ((n + 63) / 64), p.kb); split > 1)
+        return launch_split<64, false>(w, n, k, x, p, split, s);
     // the tile width whose busiest SM covers the fewest columns
     int best = 256;
     int64_t cost = INT64_MAX;
@@ -807,7 +856,8 @@ cudaError_t launch_tiles_up_e4m3(const uint8_t *w, const float *wd, int64_t ffn,
     p.hq = hq;
     p.hd = hd;
     const int64_t tiles = (m + TM - 1) / TM * e4m3_blocks(ffn);
-    if (tiles <= num_sms()) return launch_split<256, true>(w, 2 * ffn, k, x, p, split_of(tiles, p.kb, num_sms()), s);
+    if (const int split = split_of<256, true>(tiles, p.kb); split > 1)
+        return launch_split<256, true>(w, 2 * ffn, k, x, p, split, s);
     return launch_tiles<256, true>(w, 2 * ffn, k, x, p, s);
 }
 
