@@ -78,15 +78,16 @@ __device__ __forceinline__ float max_abs4(float4 v)
     return fmaxf(fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))), 0.0f);
 }
 
-// SiLU(g) * u to a few f32 ulp over the whole range.  t = e^(-|g|/2) lies in (0, 1]
-// and does not underflow before |g| = 170, where t^2 has long left f32's range; with
-// t^2 = e^-|g|, silu(g) = g / (1 + t^2) for g >= 0 and (g t) t / (1 + t^2) below.
-// The exponent -|g| log2(e) / 2 is carried as a rounded product and its remainder
-// (an FMA, and the constant's own second part), so that the error of t does not grow
-// with |g|: 2^t's approximation is all that is left of it.
-constexpr float kHalfLog2e = -0.72134752044448f;     // -log2(e) / 2 rounded to f32
-constexpr float kHalfLog2eRest = -9.629815e-9f;      // and what that leaves
+// SiLU(g) * u = g u / (1 + e^-g) to a few f32 ulp over the whole range.  The exponent
+// is carried as a rounded product -x log2(e) and its remainder (an FMA, and the
+// constant's own second part), so that the error of e^-x does not grow with |x|: the
+// approximation of 2^y is all that is left of it.  x is g held within +-87, where
+// neither e^-x nor its reciprocal leaves f32's normal range; below, g's own product
+// with 2^-125 is smaller than any value that a code stands for.
+constexpr float kLog2e = 1.4426950216293335f;       // log2(e) rounded to f32
+constexpr float kLog2eRest = 1.925963033500011e-08f;  // and what that leaves
 constexpr float kLn2 = 0.693147181f;
+constexpr float kSiluRange = 87.0f;
 
 __device__ __forceinline__ float ex2_approx(float x)
 {
@@ -103,13 +104,12 @@ __device__ __forceinline__ float rcp_approx(float x)
 
 __device__ __forceinline__ float silu_mul_e(float g, float u)
 {
-    const float a = fminf(fabsf(g), 170.0f);
-    const float hi = a * kHalfLog2e;
-    const float lo = fmaf(a, kHalfLog2eRest, fmaf(a, kHalfLog2e, -hi));
-    float t = ex2_approx(hi);
-    t = fmaf(t, lo * kLn2, t);
-    const float num = g >= 0.0f ? g : (g * t) * t;
-    return num * rcp_approx(fmaf(t, t, 1.0f)) * u;
+    const float x = fminf(fmaxf(g, -kSiluRange), kSiluRange);
+    const float hi = x * -kLog2e;
+    const float rest = fmaf(x, kLog2eRest, fmaf(x, kLog2e, hi));  // x log2(e) + hi
+    float e = ex2_approx(hi);
+    e = fmaf(e, rest * -kLn2, e);
+    return g * rcp_approx(1.0f + e) * u;
 }
 
 }  // namespace qg

@@ -338,18 +338,15 @@ __device__ __forceinline__ bool tile_sums(const TileArgs &p, TileShared &b, uint
 __device__ __forceinline__ uint64_t silu_mul2(uint64_t g2, uint64_t u2)
 {
     const float2 g = unpack2(g2);
-    const uint64_t a = pack2(fminf(fabsf(g.x), 170.0f), fminf(fabsf(g.y), 170.0f));
-    const uint64_t c = pack2(kHalfLog2e, kHalfLog2e), cr = pack2(kHalfLog2eRest, kHalfLog2eRest);
-    const uint64_t one = pack2(1.0f, 1.0f), ln2 = pack2(kLn2, kLn2), minus = pack2(-1.0f, -1.0f);
-    const uint64_t hi = mul2(a, c);
-    const uint64_t lo = fma2(a, cr, fma2(a, c, mul2(hi, minus)));
+    const uint64_t x = pack2(fminf(fmaxf(g.x, -kSiluRange), kSiluRange), fminf(fmaxf(g.y, -kSiluRange), kSiluRange));
+    const uint64_t one = pack2(1.0f, 1.0f);
+    const uint64_t hi = mul2(x, pack2(-kLog2e, -kLog2e));
+    const uint64_t rest = fma2(x, pack2(kLog2eRest, kLog2eRest), fma2(x, pack2(kLog2e, kLog2e), hi));
     const float2 h = unpack2(hi);
-    uint64_t t = pack2(ex2_approx(h.x), ex2_approx(h.y));
-    t = fma2(t, mul2(lo, ln2), t);
-    const float2 d = unpack2(fma2(t, t, one)), n = unpack2(mul2(mul2(g2, t), t));
-    const uint64_t num = pack2(g.x >= 0.0f ? g.x : n.x, g.y >= 0.0f ? g.y : n.y);
-    const float r = rcp_approx(d.x * d.y);  // one reciprocal for both: 1/dx = r dy
-    return mul2(mul2(num, mul2(pack2(r, r), pack2(d.y, d.x))), u2);
+    uint64_t e = pack2(ex2_approx(h.x), ex2_approx(h.y));
+    e = fma2(e, mul2(rest, pack2(-kLn2, -kLn2)), e);
+    const float2 d = unpack2(fma2(e, one, one));
+    return mul2(mul2(g2, pack2(rcp_approx(d.x), rcp_approx(d.y))), u2);
 }
 
 __device__ __forceinline__ float load_y(const void *p, int64_t at, int bf16)
@@ -498,13 +495,14 @@ __global__ void __launch_bounds__(TileLayout<BN>::THREADS, 1)
                 // 32 values of h, in place of the gate's sums
                 const int c0 = n0 + 32 * cg;
                 const int cols = static_cast<int>(min(p.n - c0, int64_t(32)));  // 32, 16 or none
-                float a = 0.0f;
+                float half[2] = {0.0f, 0.0f};  // the largest of each 16 columns
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
                     acc[0][j] = silu_mul2(acc[0][j], acc[1][j]);
                     const float2 h = unpack2(acc[0][j]);
-                    if (2 * j < cols) a = fmaxf(a, fmaxf(fabsf(h.x), fabsf(h.y)));
+                    half[j >> 3] = fmaxf(half[j >> 3], fmaxf(fabsf(h.x), fabsf(h.y)));
                 }
+                float a = fmaxf(cols > 0 ? half[0] : 0.0f, cols > 16 ? half[1] : 0.0f);
                 top[parity][cg][32 * q + lane] = a;
                 asm volatile("bar.sync %0, 128;" ::"r"(1 + q) : "memory");
 #pragma unroll
