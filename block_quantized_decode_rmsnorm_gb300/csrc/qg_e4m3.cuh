@@ -48,6 +48,12 @@ __device__ __forceinline__ uint32_t e4m3_pack4(float a, float b, float c, float 
     return e4m3_pack2(a, b) | (e4m3_pack2(c, d) << 16);
 }
 
+__device__ __forceinline__ float max_abs4(float4 v)
+{
+    // fmaxf passes over NaN; four NaN leave 0
+    return fmaxf(fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))), 0.0f);
+}
+
 // Four stream values (f32, or bf16 widened exactly).
 template <typename T>
 struct Vec4;
@@ -56,6 +62,7 @@ struct Vec4<float> {
     using raw = float4;
     static __device__ __forceinline__ float4 widen(raw v) { return v; }
     static __device__ __forceinline__ raw narrow(float4 v) { return v; }
+    static __device__ __forceinline__ float max_abs(raw v) { return max_abs4(v); }
 };
 template <>
 struct Vec4<__nv_bfloat16> {
@@ -70,13 +77,14 @@ struct Vec4<__nv_bfloat16> {
         const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
         return make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
     }
+    // two at a time; like fmaxf the packed maximum passes over NaN
+    static __device__ __forceinline__ float max_abs(raw v)
+    {
+        const __nv_bfloat162 m = __hmax2(__habs2(*reinterpret_cast<const __nv_bfloat162 *>(&v.x)),
+                                         __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&v.y)));
+        return fmaxf(fmaxf(__low2float(m), __high2float(m)), 0.0f);
+    }
 };
-
-__device__ __forceinline__ float max_abs4(float4 v)
-{
-    // fmaxf passes over NaN; four NaN leave 0
-    return fmaxf(fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))), 0.0f);
-}
 
 // SiLU(g) * u = g u / (1 + e^-g) to a few f32 ulp over the whole range.  The exponent
 // is carried as a rounded product -x log2(e) and its remainder (an FMA, and the

@@ -110,7 +110,8 @@ def test_quantize_one_row_and_none(torch, qg):
 # ---------------------------------------------------------------- norm
 
 NORM_SHAPES = [(1, 16), (1, 1024), (3, 144), (2, 1040), (257, 256), (5, 2560), (3, 4112), (4, 8192), (2, 8208),
-               (2, 16384), (2, 16400), (1, 65536)]
+               (2, 16384), (2, 16400), (1, 65536),
+               (310, 1024), (311, 1536), (312, 2448), (313, 4096), (314, 4112)]  # rows that fill the SMs
 
 
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
