@@ -558,14 +558,18 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(const float *local, uint32_t 
     return v;
 }
 
-// Four neighbouring sums of the tile over the cluster's CTAs, in rank order.
+// Four neighbouring sums of the tile over the cluster's CTAs: every load first (one
+// takes about 0.3 us), then the additions in rank order.
 __device__ __forceinline__ float4 cluster_sum4(const float *at, int split)
 {
-    float4 v = ld_cluster_f32x4(at, 0);
-    for (int r = 1; r < split; ++r) {
-        const float4 e = ld_cluster_f32x4(at, r);
-        v = make_float4(v.x + e.x, v.y + e.y, v.z + e.z, v.w + e.w);
-    }
+    float4 e[T_SPLIT];
+#pragma unroll
+    for (int r = 0; r < T_SPLIT; ++r)
+        if (r < split) e[r] = ld_cluster_f32x4(at, r);
+    float4 v = e[0];
+#pragma unroll
+    for (int r = 1; r < T_SPLIT; ++r)
+        if (r < split) v = make_float4(v.x + e[r].x, v.y + e[r].y, v.z + e[r].z, v.w + e[r].w);
     return v;
 }
 
