@@ -35,6 +35,7 @@ struct RowsArgs {
     const uint8_t *w;
     const float *wd;
     int64_t n;         // output columns
+    int64_t tiles;     // of 16 weight rows
     int64_t up_row;    // gate|up: first up row
     int64_t up_block;  // and its first row of scales
     int k, kb;
@@ -62,43 +63,46 @@ struct RowsLayout {
     static constexpr int W = UP ? 4 : 8;   // warps per CTA
     static constexpr int T = UP ? 2 : 1;   // weight tiles per CTA
     static constexpr int D = UP ? 2 : 6;   // blocks on their way per warp
-    static constexpr int F = 3;            // blocks whose activations are
+    static constexpr int F = 3;            // steps whose activations are
     static constexpr int RING = W * D * T * R_TILE;  // 32 and 96 KB
     static constexpr int CTAS = UP ? 4 : 2;          // per SM
 };
 
-template <bool UP>
+// MANY: a CTA walks over several tiles, the next one's weights on their way while a tile
+// ends; without it the tile is the CTA's only one and nothing is kept of the next.
+template <bool UP, bool MANY>
 __global__ void __launch_bounds__(RowsLayout<UP>::W * 32, RowsLayout<UP>::CTAS) rows_e4m3_kernel(const RowsArgs p)
 {
     using L = RowsLayout<UP>;
     constexpr int RW = L::W, RT = L::T, D = L::D, F = L::F;
     extern __shared__ __align__(16) uint8_t ring_raw[];  // [warp][slot][tile][row half][block half][lane] of 16 bytes
-    __shared__ float red[RW][RT][8 * RR];
+    __shared__ float red[2][RW][RT][8 * RR];             // [tile parity][warp]: one barrier a tile
     __shared__ float top[8];  // gate|up: the rows' largest magnitudes
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, c = lane & 3;
-    const int64_t n0 = static_cast<int64_t>(blockIdx.x) * RR;
-    const int slots = min(D, (p.kb + RW - 1) / RW);
+    const int steps = (p.kb + RW - 1) / RW;  // of a tile: warp w takes blocks w, w + RW, ...
+    const int slots = MANY ? D : min(D, steps);
     uint8_t *ring = ring_raw + static_cast<size_t>(warp) * slots * RT * R_TILE + lane * 16;
 
-    // this lane's two rows of each tile: columns 0 ..  of row n0 + g (+ 8)
-    const uint8_t *wr[RT][2];
-    const float *wd[RT];
+    // The next step's weights into its slot, tile after tile: zeros where there are
+    // none; one group per step, empty past the last.
+    int64_t s_tile = blockIdx.x;
+    int s_step = 0, s_slot = 0;
+    const uint8_t *wr[RT][2];  // this lane's rows of s_tile: columns 0 .. of row g (+ 8), or null
+    auto rows = [&]() {
 #pragma unroll
-    for (int t = 0; t < RT; ++t) {
-        wd[t] = p.wd + ((t ? p.up_block : 0) + n0 / EB) * p.kb;
+        for (int t = 0; t < RT; ++t)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int64_t row = n0 + g + 8 * h;
-            wr[t][h] = row < p.n ? p.w + ((t ? p.up_row : 0) + row) * p.k : nullptr;
-        }
-    }
-    // this warp's i-th block, warp + RW i, into its slot: zeros where there are no
-    // weights; one group per block, empty past the last
-    auto stage = [&](int i) {
-        const int b = warp + RW * i;
-        if (b < p.kb) {
-            uint8_t *slot = ring + (i % D) * RT * R_TILE;
+            for (int h = 0; h < 2; ++h) {
+                const int64_t row = s_tile * RR + g + 8 * h;
+                wr[t][h] = row < p.n ? p.w + ((t ? p.up_row : 0) + row) * p.k : nullptr;
+            }
+    };
+    rows();
+    auto stage = [&]() {
+        const int b = warp + RW * s_step;
+        if ((!MANY || s_tile < p.tiles) && b < p.kb) {
+            uint8_t *slot = ring + s_slot * RT * R_TILE;
 #pragma unroll
             for (int t = 0; t < RT; ++t)
 #pragma unroll
@@ -114,9 +118,16 @@ __global__ void __launch_bounds__(RowsLayout<UP>::W * 32, RowsLayout<UP>::CTAS) 
                     }
         }
         cp_async_commit();
+        ++s_step;
+        if (MANY && s_step == steps) {
+            s_step = 0;
+            s_tile += gridDim.x;
+            rows();
+        }
+        if (++s_slot == D) s_slot = 0;
     };
 #pragma unroll
-    for (int i = 0; i < D; ++i) stage(i);
+    for (int i = 0; i < D; ++i) stage();
     pdl_wait();
     pdl_trigger();
 
@@ -124,17 +135,15 @@ __global__ void __launch_bounds__(RowsLayout<UP>::W * 32, RowsLayout<UP>::CTAS) 
     const float *xd[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) xd[h] = 2 * c + h < p.m ? p.xd + (2 * c + h) * p.kb : nullptr;
-    float acc[RT][4];
-#pragma unroll
-    for (int t = 0; t < RT; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[t][e] = 0.0f;
 
-    // the activations and scales of the next F blocks, in registers
+    // the activations and scales of the next F steps, in registers
     uint4 xn[F][2];
     float fw[F][RT], fx[F][2];
-    auto fetch = [&](int u, int b) {
-        const bool in = b < p.kb;
+    int64_t f_tile = blockIdx.x;
+    int f_step = 0;
+    auto fetch = [&](int u) {
+        const int b = warp + RW * f_step;
+        const bool in = (!MANY || f_tile < p.tiles) && b < p.kb;
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
             const int col = b * EB + 64 * q + 16 * c;
@@ -142,91 +151,122 @@ __global__ void __launch_bounds__(RowsLayout<UP>::W * 32, RowsLayout<UP>::CTAS) 
             fx[u][q] = in && xd[q] ? xd[q][b] : 0.0f;
         }
 #pragma unroll
-        for (int t = 0; t < RT; ++t) fw[u][t] = in ? wd[t][b] : 0.0f;
+        for (int t = 0; t < RT; ++t)
+            fw[u][t] = in ? p.wd[((t ? p.up_block : 0) + f_tile * RR / EB) * p.kb + b] : 0.0f;
+        ++f_step;
+        if (MANY && f_step == steps) f_step = 0, f_tile += gridDim.x;
     };
 #pragma unroll
-    for (int u = 0; u < F; ++u) fetch(u, warp + RW * u);
+    for (int u = 0; u < F; ++u) fetch(u);
+
+    float acc[RT][4] = {};
+    int64_t tile = blockIdx.x;
+    int step = 0, slot_no = 0, parity = 0;
+    // the tile's sums of all warps, in warp order, and what becomes of them
+    auto finish = [&]() {
+        // [activation row][weight row]: values 0 and 1 are row g of activations 2c, 2c + 1, the others row g + 8
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) red[parity][warp][t][(2 * c + (e & 1)) * RR + g + 8 * (e >> 1)] = acc[t][e];
+        __syncthreads();
+
+        // a thread per output: activation row o / 16, weight row o % 16
+        const int o = threadIdx.x, row = o / RR;
+        const int64_t col = tile * RR + o % RR;
+        const bool mine = o < 8 * RR, live = mine && row < p.m && col < p.n;
+        float v[RT];
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+            v[t] = mine ? red[parity][0][t][o] : 0.0f;
+#pragma unroll
+            for (int w = 1; w < RW; ++w) v[t] += mine ? red[parity][w][t][o] : 0.0f;
+        }
+        if constexpr (UP) {
+            const float h = silu_mul_e(v[0], v[RT - 1]);
+            float a = live ? fmaxf(fabsf(h), 0.0f) : 0.0f;
+#pragma unroll
+            for (int s = RR / 2; s >= 1; s >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, s));
+            if (mine && o % RR == 0) top[row] = a;
+            cluster_sync();
+            if (live) {
+#pragma unroll
+                for (int r = 0; r < UP_CLUSTER; ++r) a = fmaxf(a, ld_cluster_f32(&top[row], r));
+                a = e4m3_floor(a);
+                p.hq[row * p.n + col] = static_cast<uint8_t>(e4m3_pack2(h * __fdiv_rn(448.0f, a), 0.0f));
+                if (col % EB == 0) p.hd[row * e4m3_blocks(p.n) + col / EB] = __fdiv_rn(a, 448.0f);
+            }
+            cluster_sync();  // the others have read this CTA's maxima
+        } else if (live) {
+            const int64_t at = row * p.n + col;
+            if (p.y_bf16) {
+                const __nv_bfloat16 *res = static_cast<const __nv_bfloat16 *>(p.residual);
+                const float out = res ? v[0] + __bfloat162float(res[at]) : v[0];
+                static_cast<__nv_bfloat16 *>(p.y)[at] = __float2bfloat16_rn(out);
+            } else {
+                const float *res = static_cast<const float *>(p.residual);
+                static_cast<float *>(p.y)[at] = res ? v[0] + res[at] : v[0];
+            }
+        }
+    };
+    bool more = true;
 #pragma unroll 1
-    for (int i0 = 0; warp + RW * i0 < p.kb; i0 += F) {
+    while (more) {
 #pragma unroll
         for (int u = 0; u < F; ++u) {
-            const int i = i0 + u, b = warp + RW * i;
-            if (b >= p.kb) break;
             cp_async_wait<D - 1>();
-            const uint8_t *slot = ring + (i % D) * RT * R_TILE;
+            if (warp + RW * step < p.kb) {
+                const uint8_t *slot = ring + slot_no * RT * R_TILE;
 #pragma unroll
-            for (int t = 0; t < RT; ++t) {
-                float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                for (int t = 0; t < RT; ++t) {
+                    float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const uint4 a = *reinterpret_cast<const uint4 *>(slot + (t * 4 + q) * 512);
-                    const uint4 a8 = *reinterpret_cast<const uint4 *>(slot + (t * 4 + 2 + q) * 512);
-                    mma_e4m3(d, a.x, a8.x, a.y, a8.y, xn[u][q].x, xn[u][q].y);
-                    mma_e4m3(d, a.z, a8.z, a.w, a8.w, xn[u][q].z, xn[u][q].w);
+                    for (int q = 0; q < 2; ++q) {
+                        const uint4 a = *reinterpret_cast<const uint4 *>(slot + (t * 4 + q) * 512);
+                        const uint4 a8 = *reinterpret_cast<const uint4 *>(slot + (t * 4 + 2 + q) * 512);
+                        mma_e4m3(d, a.x, a8.x, a.y, a8.y, xn[u][q].x, xn[u][q].y);
+                        mma_e4m3(d, a.z, a8.z, a.w, a8.w, xn[u][q].z, xn[u][q].w);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[t][e] = fmaf(d[e], fx[u][e & 1] * fw[u][t], acc[t][e]);
                 }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[t][e] = fmaf(d[e], fx[u][e & 1] * fw[u][t], acc[t][e]);
             }
-            stage(i + D);  // into the slot just read
-            fetch(u, b + RW * F);
+            if (++step == steps) {
+                if (!MANY) {
+                    more = false;
+                    break;
+                }
+                finish();
+#pragma unroll
+                for (int t = 0; t < RT; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[t][e] = 0.0f;
+                step = 0;
+                tile += gridDim.x;
+                parity ^= 1;
+                if (tile >= p.tiles) {
+                    more = false;
+                    break;
+                }
+            }
+            if (++slot_no == D) slot_no = 0;
+            stage();  // into the slot just read
+            fetch(u);
         }
     }
-    // [activation row][weight row]: values 0 and 1 are row g of activations 2c, 2c + 1, the others row g + 8
-#pragma unroll
-    for (int t = 0; t < RT; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) red[warp][t][(2 * c + (e & 1)) * RR + g + 8 * (e >> 1)] = acc[t][e];
-    __syncthreads();
-
-    // a thread per output: activation row o / 16, weight row o % 16
-    const int o = threadIdx.x, row = o / RR;
-    const int64_t col = n0 + o % RR;
-    const bool mine = o < 8 * RR, live = mine && row < p.m && col < p.n;
-    float v[RT];
-#pragma unroll
-    for (int t = 0; t < RT; ++t) {
-        v[t] = mine ? red[0][t][o] : 0.0f;
-#pragma unroll
-        for (int w = 1; w < RW; ++w) v[t] += mine ? red[w][t][o] : 0.0f;
-    }
-    if constexpr (UP) {
-        const float h = silu_mul_e(v[0], v[RT - 1]);
-        float a = live ? fmaxf(fabsf(h), 0.0f) : 0.0f;
-#pragma unroll
-        for (int s = RR / 2; s >= 1; s >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, s));
-        if (mine && o % RR == 0) top[row] = a;
-        cluster_sync();
-        if (live) {
-#pragma unroll
-            for (int r = 0; r < UP_CLUSTER; ++r) a = fmaxf(a, ld_cluster_f32(&top[row], r));
-            a = e4m3_floor(a);
-            p.hq[row * p.n + col] = static_cast<uint8_t>(e4m3_pack2(h * __fdiv_rn(448.0f, a), 0.0f));
-            if (col % EB == 0) p.hd[row * e4m3_blocks(p.n) + col / EB] = __fdiv_rn(a, 448.0f);
-        }
-        cluster_sync();  // the others have read this CTA's maxima
-    } else if (live) {
-        const int64_t at = row * p.n + col;
-        if (p.y_bf16) {
-            const __nv_bfloat16 *res = static_cast<const __nv_bfloat16 *>(p.residual);
-            const float out = res ? v[0] + __bfloat162float(res[at]) : v[0];
-            static_cast<__nv_bfloat16 *>(p.y)[at] = __float2bfloat16_rn(out);
-        } else {
-            const float *res = static_cast<const float *>(p.residual);
-            static_cast<float *>(p.y)[at] = res ? v[0] + res[at] : v[0];
-        }
-    }
+    if (!MANY) finish();
 }
 
-template <bool UP>
-static cudaError_t launch_rows(int64_t tiles, const RowsArgs &p, cudaStream_t s)
+template <bool UP, bool MANY>
+static cudaError_t launch_rows(int64_t ctas, const RowsArgs &p, cudaStream_t s)
 {
     using L = RowsLayout<UP>;
     const int need = (p.kb + L::W - 1) / L::W;
-    const int bytes = L::W * (need < L::D ? need : L::D) * L::T * R_TILE;
-    if (cudaError_t e = opt_in_smem(reinterpret_cast<const void *>(rows_e4m3_kernel<UP>), L::RING); e != cudaSuccess)
-        return e;
-    return launch_pdl_cluster(rows_e4m3_kernel<UP>, dim3(static_cast<unsigned>(tiles)), dim3(L::W * 32),
-                              static_cast<size_t>(bytes), s, UP ? UP_CLUSTER : 1, p);
+    const int bytes = L::W * (MANY || need > L::D ? L::D : need) * L::T * R_TILE;
+    const auto kernel = rows_e4m3_kernel<UP, MANY>;
+    if (cudaError_t e = opt_in_smem(reinterpret_cast<const void *>(kernel), L::RING); e != cudaSuccess) return e;
+    return launch_pdl_cluster(kernel, dim3(static_cast<unsigned>(ctas)), dim3(L::W * 32), static_cast<size_t>(bytes), s,
+                              UP ? UP_CLUSTER : 1, p);
 }
 
 cudaError_t launch_rows_e4m3(const uint8_t *w, const float *wd, int64_t n, int64_t k, const uint8_t *x, const float *xd,
@@ -244,7 +284,13 @@ cudaError_t launch_rows_e4m3(const uint8_t *w, const float *wd, int64_t n, int64
     p.residual = residual;
     p.y = y;
     p.y_bf16 = y_dtype == QG_BF16;
-    return launch_rows<false>((n + RR - 1) / RR, p, s);
+    p.tiles = (n + RR - 1) / RR;
+    // More tiles than CTAs find room: as many each (65536x1024: 18.1 us against 28.5 with
+    // a CTA to each; 1024x3584, one each: 2.3 us, and 2.8 by the kernel that walks).
+    const int64_t room = RowsLayout<false>::CTAS * static_cast<int64_t>(num_sms());
+    if (p.tiles <= room) return launch_rows<false, false>(p.tiles, p, s);
+    const int64_t each = (p.tiles + room - 1) / room;
+    return launch_rows<false, true>((p.tiles + each - 1) / each, p, s);
 }
 
 cudaError_t launch_rows_up_e4m3(const uint8_t *w, const float *wd, int64_t ffn, int64_t k, const uint8_t *x,
@@ -263,7 +309,8 @@ cudaError_t launch_rows_up_e4m3(const uint8_t *w, const float *wd, int64_t ffn, 
     p.m = m;
     p.hq = hq;
     p.hd = hd;
-    return launch_rows<true>(e4m3_blocks(ffn) * UP_CLUSTER, p, s);
+    p.tiles = e4m3_blocks(ffn) * UP_CLUSTER;
+    return launch_rows<true, false>(p.tiles, p, s);
 }
 
 }  // namespace qg

@@ -599,7 +599,10 @@ __global__ void __launch_bounds__(TileLayout<BN>::THREADS, TileLayout<BN>::SPLIT
     uint64_t acc[2][16];
     if (warp == L::TMA_WARP) {
         ok = tile_copies<BN, UP, true>(tx, tw, p, b, smem, m0, n0, kb0, kb1, it);
-        if (!ok && it > 0) mbar_wait_bounded(&b.full[(it - 1) % p.stages], ((it - 1) / p.stages) & 1, kCopyWaitLimitNs);
+        if (!ok) {  // let the last copies land (bounded), the early weights' among them
+            const uint32_t last = max(it, static_cast<uint32_t>(min(p.stages, kb1 - kb0))) - 1;
+            mbar_wait_bounded(&b.full[last % p.stages], (last / p.stages) & 1, kCopyWaitLimitNs);
+        }
     } else if (warp == L::MMA_WARP) {
         pdl_wait();
         ok = tile_mmas<BN, true>(p, b, tmem, desc0, kb1 - kb0, it);

@@ -216,6 +216,13 @@ def test_product_epilogues(torch, qg, m, kind, residual):
     check_product(torch, qg, np.random.default_rng(m), m, 328, 1168, kind, residual)
 
 
+# few rows over more 16-row tiles than CTAs find room: two, three, and a ragged last of each
+@pytest.mark.parametrize("m,n,k,kind,residual", [(1, 5001, 272, "f32", None), (8, 9744, 1040, "bf16", "place"),
+                                                 (5, 14600, 144, "bf16", "apart"), (3, 9729, 2576, "f32", "apart")])
+def test_product_few_rows_many_columns(torch, qg, m, n, k, kind, residual):
+    check_product(torch, qg, np.random.default_rng(n), m, n, k, kind, residual)
+
+
 def test_product_many_tiles(torch, qg):
     check_product(torch, qg, np.random.default_rng(5), 700, 2727, 656, "bf16", "apart")
     check_product(torch, qg, np.random.default_rng(6), 17, 5001, 1040, "f32", None)
@@ -430,6 +437,115 @@ def test_streams_at_once(torch, qg):
     torch.cuda.synchronize()
     for i in range(2):
         assert all(torch.equal(y, want[i]) for y in got[i])
+
+
+@pytest.mark.parametrize("m", [1, 40, 300])
+def test_streams_by_handle(torch, qg, m):
+    """stream= as a torch stream, its raw handle, and the legacy default stream's."""
+    layer = make_layer(torch, qg, np.random.default_rng(m), 256, 272, torch.float32)
+    x = torch.randn((m, 256), device="cuda")
+    want = chain(qg, x, layer, None)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream, torch.cuda.default_stream(), 0):
+        q, d, s = qg.rmsnorm_add_quantize_e4m3(x, layer.gamma, None, EPS, stream=stream)
+        h = qg.qg_ffn_up_e4m3(layer.gate_up, q, d, stream=stream)
+        y = qg.qgemm_e4m3(layer.down, *h, "residual", s, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
+        q2, d2 = qg.quantize_act_e4m3(x, stream=stream)
+        torch.cuda.synchronize()
+        same_codes(bits(q2), E.quantize(x.cpu().numpy())[0])
+
+
+def test_threads_at_once(torch, qg):
+    """Host threads with a stream each: the library's per-device caches are filled under a lock."""
+    import threading
+
+    layer = make_layer(torch, qg, np.random.default_rng(0), 384, 272, torch.bfloat16)
+    xs = [torch.randn((m, 384), device="cuda").bfloat16() for m in (1, 9, 70, 200)]
+    want = [chain(qg, x, layer, None) for x in xs]
+    torch.cuda.synchronize()
+    got, errors = [[] for _ in xs], []
+
+    def work(i):
+        try:
+            stream = torch.cuda.Stream()
+            for _ in range(10):
+                got[i].append(qg.qg_ffn_e4m3(xs[i], layer, None, EPS, stream=stream))
+            stream.synchronize()
+        except Exception as e:  # noqa: BLE001 - handed to the main thread
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(xs))]
+    [t.start() for t in threads], [t.join() for t in threads]
+    assert not errors, errors
+    assert all(torch.equal(y, want[i]) for i in range(len(xs)) for y in got[i])
+
+
+@pytest.mark.parametrize("m", [1, 30, 2500])
+def test_first_call_inside_a_capture(torch, m):
+    """A process whose first call of all is captured: nothing that the call asks the
+    driver for on first use breaks the capture."""
+    import subprocess
+    import sys
+
+    code = f"""
+import torch
+import block_quantized_decode_rmsnorm_gb300 as qg
+f8 = torch.float8_e4m3fn
+x = torch.randn(({m}, 256), device='cuda')
+w = lambda n, k: torch.randint(0, 120, (n, k), device='cuda').to(torch.uint8).view(f8)
+layer = qg.E4M3Layer(torch.ones(256, device='cuda'), qg.E4M3Weight(w(2 * 1040, 256), torch.full((18, 2), 1e-4, device='cuda')),
+                     qg.E4M3Weight(w(256, 1040), torch.full((2, 9), 1e-4, device='cuda')))
+buf, y = qg.E4M3Buffers.allocate({m}, 256, 1040, 'cuda'), torch.empty_like(x)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    qg.qg_ffn_e4m3(x, layer, x, 1e-6, buf, y)
+y.zero_()
+g.replay()
+assert torch.equal(y, qg.qg_ffn_e4m3(x, layer, x, 1e-6)) and bool(y.isfinite().all())
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("m", [1, 40, 300])
+def test_weights_replaced_in_stream_order(torch, qg, m):
+    """Weights written by a kernel of another library just before the call: that one has
+    ended when this one starts (the library's own kernels do not write weights that the
+    next call reads)."""
+    rng = np.random.default_rng(m)
+    ws = [E.weight(rng, 400, 1024) for _ in range(2)]
+    codes, scales = [codes_dev(torch, w[0]) for w in ws], [dev(torch, w[1]) for w in ws]
+    xq, xd = qg.quantize_act_e4m3(torch.randn((m, 1024), device="cuda"))
+    want = [qg.qgemm_e4m3(qg.E4M3Weight(c, s), xq, xd) for c, s in zip(codes, scales)]
+    w = qg.E4M3Weight(codes[0].clone(), scales[0].clone())
+    got = []
+    for i in range(20):
+        w.codes.view(torch.uint8).copy_(codes[i % 2].view(torch.uint8))
+        w.scales.copy_(scales[i % 2])
+        got.append(qg.qgemm_e4m3(w, xq, xd))
+    assert all(torch.equal(y, want[i % 2]) for i, y in enumerate(got))
+
+
+def test_rows_past_the_last(torch, qg):
+    """The first rows of a larger batch: what lies behind them is neither read into the
+    results nor written."""
+    rng = np.random.default_rng(2)
+    w = E.weight(rng, 144, 512)
+    w = qg.E4M3Weight(codes_dev(torch, w[0]), dev(torch, w[1]))
+    x = torch.randn((300, 512), device="cuda")
+    q, d = qg.quantize_act_e4m3(x)
+    for m in (1, 8, 9, 33, 129):
+        q2, d2 = q.clone(), d.clone()
+        q2.view(torch.uint8)[m:] = 0x7F
+        d2[m:] = float("nan")
+        y = torch.full((300, 144), -7.0, device="cuda")
+        qg.qgemm_e4m3(w, q2[:m], d2[:m], y=y[:m])
+        assert torch.equal(y[:m], qg.qgemm_e4m3(w, q[:m], d[:m]))
+        assert bool((y[m:] == -7.0).all())
 
 
 def test_results_repeat(torch, qg):
