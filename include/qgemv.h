@@ -622,7 +622,8 @@ QG_API qg_status qgemm_bf16_prefill(const uint16_t *w, int64_t n_rows, int64_t k
  * k: a positive multiple of 16 up to 2^20 (rmsnorm_add_quantize_e4m3: up to
  * 65536).  Code planes and stream tensors 16-byte aligned, scales 4-byte aligned.
  * Outputs must not overlap inputs or one another (QG_ERR_SHAPE) except where
- * stated.  Every sum is taken in a fixed order: results repeat bit for bit.
+ * stated.  Every sum is taken in an order that the shape alone fixes: results
+ * repeat bit for bit (a row's may differ between calls with other rows beside it).
  */
 typedef enum {
     QG_F32 = 0,
@@ -683,7 +684,7 @@ QG_API qg_status qgemm_e4m3(const uint8_t *w, const float *wd, int64_t n_rows, i
  *   matrix).  ffn a multiple of 16, ffn < 2^30 - 256.
  *   xq, xd: activations [m][k], m up to 2^24 (read)
  *   hq: device uint8[m][ffn], hd: device f32[m][ceil(ffn/128)] (written)
- * Stalled copies as qgemm_e4m3 (codes and scales NaN).
+ * Stalled copies as qgemm_e4m3 (NaN codes).
  */
 QG_API qg_status qg_ffn_up_e4m3(const uint8_t *w, const float *wd, int64_t ffn, int64_t k, const uint8_t *xq,
                                 const float *xd, int64_t m, uint8_t *hq, float *hd, qg_stream_t stream);

@@ -344,6 +344,29 @@ def test_up_padding_row(torch, qg):
         assert np.all(hd[1].cpu().numpy() == np.float32(2.0 ** -100) / np.float32(448))
 
 
+@pytest.mark.parametrize("m", [4, 30, 2500])
+def test_up_nan_row(torch, qg, m):
+    """A NaN activation makes its own row's codes NaN, with the floor's scale, and leaves
+    the other rows alone; a NaN weight its own column's."""
+    rng = np.random.default_rng(m)
+    f = 1040
+    halves = [E.weight(rng, f, 256) for _ in range(2)]
+    wq = np.concatenate([h[0] for h in halves])
+    w = qg.E4M3Weight(codes_dev(torch, wq), dev(torch, np.concatenate([h[1] for h in halves])))
+    xq, xd = acts(rng, m, 256)
+    clean = qg.qg_ffn_up_e4m3(w, codes_dev(torch, xq), dev(torch, xd))
+    xq[2, 77] = 0x7F
+    hq, hd = qg.qg_ffn_up_e4m3(w, codes_dev(torch, xq), dev(torch, xd))
+    assert np.all(bits(hq)[2] & 0x7F == 0x7F)
+    assert np.all(hd[2].cpu().numpy() == np.float32(2.0 ** -100) / np.float32(448))
+    rest = np.arange(m) != 2
+    assert np.array_equal(bits(hq)[rest], bits(clean[0])[rest]) and torch.equal(hd[rest], clean[1][rest])
+    wq[f + 500, 3] = 0x7F
+    hq, hd = qg.qg_ffn_up_e4m3(qg.E4M3Weight(codes_dev(torch, wq), w.scales), codes_dev(torch, xq), dev(torch, xd))
+    assert np.all(bits(hq)[:, 500] & 0x7F == 0x7F)
+    assert not np.any(np.delete(bits(hq)[rest], 500, axis=1) & 0x7F == 0x7F)
+
+
 # ---------------------------------------------------------------- together
 
 def make_layer(torch, qg, rng, hidden, ffn, t):
