@@ -26,7 +26,7 @@
 // outputs or codes for the tiles left) instead of hanging.
 //
 // Measured: gate|up 8192x9216x2560 305 us (2.53 PFLOP/s; 333 under the power cap that
-// sets in after a second), product 4096x2560x9216 with the residual 83 us (89), both
+// sets in after a second), product 4096x2560x9216 with the residual 80 us (88), both
 // bound by reading the block sums out of TMEM (365 to 390 of a block's 512 MMA cycles
 // at N = 256, whatever the loads' width) and, behind that, by the operands' way from L2
 // (227 and 73 us alone); 100x2727x3600 8.5 us, bound by its chain of latencies.
@@ -60,12 +60,12 @@ struct TileLayout {
     // where BN is 64).  Never more than the stages, or a phase could be missed.
     static constexpr int BUFS = BN <= 128 ? 4 : 2;
     static constexpr int TMEM = BN == 192 ? 512 : BUFS * BN;  // columns allocated: a power of two
-    static constexpr int UP_BYTES = STAGES * STAGE + 1024;  // + alignment of the base
-    static constexpr int BYTES = UP_BYTES + EW * 32 * T_XP * 4;
+    static constexpr int BYTES = STAGES * STAGE + 1024;     // + alignment of the base
+    static constexpr int ANY_BYTES = BYTES + EW * 32 * T_XP * 4;  // + the transpose buffers
     static constexpr int SPLIT_CTAS = BN == 64 ? 2 : 1;     // per SM, of the split kernel
     static constexpr int SPLIT_ROOM = (SPLIT_CTAS == 2 ? 100 : 210) * 1024;  // shared memory of its stages at most
     static constexpr int LD = BN + 4;                       // row stride (floats) of a split tile's sums
-    static_assert(BYTES <= 220 * 1024 && STAGES >= BUFS, "shared memory");
+    static_assert(ANY_BYTES <= 220 * 1024 && STAGES >= BUFS, "shared memory");
 };
 
 struct TileArgs {
@@ -80,7 +80,6 @@ struct TileArgs {
     const void *residual;
     void *y;
     int y_bf16;
-    int rows32;          // every row of y (and of the residual) starts on 32 bytes
     uint8_t *hq;
     float *hd;
 };
@@ -370,59 +369,75 @@ __device__ __forceinline__ void st_32B(void *p, const uint32_t (&v)[8])
                  "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                  : "memory");
 }
+// Read once, so past L1 (1500x3000x2560 with an f32 residual: 24.5 -> 19.3 us).
 __device__ __forceinline__ void ld_32B(const void *p, uint32_t (&v)[8])
 {
-    asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                  : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
                  : "l"(p)
                  : "memory");
 }
 
-// 32 columns from c0 of this thread's row of y, 32 bytes (a whole sector) per store;
-// every row of y starts on 32 bytes and n is a multiple of those 8 or 16 columns.
-__device__ __forceinline__ void store_row(const TileArgs &p, const uint64_t (&acc)[16], int64_t row, int64_t c0)
+// What becomes of a tile's sums: SiLU and codes; y of either type in whole 32-byte
+// sectors; any y without and with a residual.  Each has a kernel of its own: in a common
+// one the registers of one form's stores are taken from every form's main loop (98 us for
+// 4096x2560x9216 with a residual, where the bf16 kernel takes 79).
+enum class Out { UP, BF16, F32, ANY, ANY_ADD };
+
+// 32 columns from c0 of this thread's row of y, 32 bytes (a whole sector) per store,
+// the residual's loads of two pieces before their stores (all four f32 pieces at once cost
+// 96 bytes of spills and are no faster: 1500x3000x2560 25.5 us against 24.5); every row of
+// y starts on 32 bytes and n is a multiple of those 8 or 16 columns.
+template <Out OUT>
+__device__ __forceinline__ void store_row(const TileArgs &p, const uint64_t (&acc)[16], int64_t row, int c0)
 {
-    const int64_t at = row * p.n + c0;
-    if (p.y_bf16) {
+    constexpr int BYTES = OUT == Out::BF16 ? 2 : 4, PER = 32 / BYTES, G = 32 / PER;  // columns per 32 bytes, pieces
+    const int64_t at = (row * p.n + c0) * BYTES;
+    const uint8_t *res = static_cast<const uint8_t *>(p.residual) + at;
+    uint8_t *y = static_cast<uint8_t *>(p.y) + at;
+    const int groups = min(static_cast<int>(p.n - c0), 32) / PER;  // of this row, none or fewer at the edge
+#pragma unroll
+    for (int g0 = 0; g0 < G; g0 += 2) {
+        uint32_t e[2][8];
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-            if (c0 + 16 * g >= p.n) break;
-            uint32_t e[8] = {0, 0, 0, 0, 0, 0, 0, 0}, o[8];
-            if (p.residual) ld_32B(static_cast<const __nv_bfloat16 *>(p.residual) + at + 16 * g, e);
+            if (p.residual && g0 + g < groups) {
+                ld_32B(res + 32 * (g0 + g), e[g]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) e[g][j] = 0;
+            }
+        }
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            if (g0 + g >= groups) break;
+            uint32_t o[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                float2 v = unpack2(acc[8 * g + j]);
-                if (p.residual) {
-                    v.x += __uint_as_float(e[j] << 16);
-                    v.y += __uint_as_float(e[j] & 0xffff0000u);
+                if constexpr (OUT == Out::BF16) {
+                    const float2 v = unpack2(acc[8 * g + j]);
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(v.x + __uint_as_float(e[g][j] << 16),
+                                                                   v.y + __uint_as_float(e[g][j] & 0xffff0000u));
+                    o[j] = *reinterpret_cast<const uint32_t *>(&h);
+                } else {
+                    const float2 v = unpack2(acc[4 * (g0 + g) + j / 2]);
+                    o[j] = __float_as_uint((j & 1 ? v.y : v.x) + __uint_as_float(e[g][j]));
                 }
-                const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
-                o[j] = *reinterpret_cast<const uint32_t *>(&h);
             }
-            st_32B(static_cast<__nv_bfloat16 *>(p.y) + at + 16 * g, o);
-        }
-    } else {
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            if (c0 + 8 * g >= p.n) break;
-            uint32_t e[8] = {0, 0, 0, 0, 0, 0, 0, 0}, o[8];
-            if (p.residual) ld_32B(static_cast<const float *>(p.residual) + at + 8 * g, e);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 v = unpack2(acc[4 * g + j]);
-                o[2 * j] = __float_as_uint(p.residual ? v.x + __uint_as_float(e[2 * j]) : v.x);
-                o[2 * j + 1] = __float_as_uint(p.residual ? v.y + __uint_as_float(e[2 * j + 1]) : v.y);
-            }
-            st_32B(static_cast<float *>(p.y) + at + 8 * g, o);
+            st_32B(y + 32 * (g0 + g), o);
         }
     }
 }
 
-// The same for any n: eight columns of the warp's 32 rows at a time through its
-// transpose buffer, so that eight lanes write neighbouring values.
+// The same for any n and either type: eight columns of the warp's 32 rows at a time
+// through its transpose buffer, so that eight lanes write neighbouring values.  Of a lane's
+// eight rows four residuals are loaded ahead: 4096x2561x1024, bf16, takes 70 us with one,
+// 46 with two, 36 with four and 42 with eight (1 KB of spills).
+template <bool ADD>
 __device__ __forceinline__ void store_any(const TileArgs &p, const uint64_t (&acc)[16], float *xp, int64_t r0, int64_t c0,
                                           int lane)
 {
+    constexpr int AHEAD = ADD ? 4 : 1;  // rows whose residual a lane has loaded before it stores the first
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
         __syncwarp();
@@ -436,24 +451,34 @@ __device__ __forceinline__ void store_any(const TileArgs &p, const uint64_t (&ac
         const int64_t col = c0 + 8 * g + (lane & 7);
         if (col >= p.n) continue;
 #pragma unroll 1
-        for (int r = lane >> 3; r < 32; r += 4) {
-            if (r0 + r >= p.m) break;
-            const int64_t at = (r0 + r) * p.n + col;
-            const float v = xp[r * T_XP + (lane & 7)];
-            const float o = p.residual ? v + load_y(p.residual, at, p.y_bf16) : v;
-            if (p.y_bf16)
-                static_cast<__nv_bfloat16 *>(p.y)[at] = __float2bfloat16_rn(o);
-            else
-                static_cast<float *>(p.y)[at] = o;
+        for (int i0 = lane >> 3; i0 < 32; i0 += 4 * AHEAD) {
+            const int rows = static_cast<int>(min(p.m - r0, int64_t(32))) - i0;
+            if (rows <= 0) break;
+            const int64_t at = (r0 + i0) * p.n + col;
+            float e[AHEAD];
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i)
+                e[i] = ADD && 4 * i < rows ? load_y(p.residual, at + 4 * i * p.n, p.y_bf16) : 0.0f;
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                if (4 * i >= rows) break;
+                const float v = xp[(i0 + 4 * i) * T_XP + (lane & 7)];
+                const float o = ADD ? v + e[i] : v;
+                if (p.y_bf16)
+                    static_cast<__nv_bfloat16 *>(p.y)[at + 4 * i * p.n] = __float2bfloat16_rn(o);
+                else
+                    static_cast<float *>(p.y)[at + 4 * i * p.n] = o;
+            }
         }
     }
 }
 
-template <int BN, bool UP>
+template <int BN, Out OUT>
 __global__ void __launch_bounds__(TileLayout<BN>::THREADS, 1)
     tiles_e4m3_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tw, const TileArgs p)
 {
     using L = TileLayout<BN>;
+    constexpr bool UP = OUT == Out::UP;
     constexpr int BO = UP ? 128 : BN;  // output columns per tile
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(16) TileShared b;
@@ -531,14 +556,14 @@ __global__ void __launch_bounds__(TileLayout<BN>::THREADS, 1)
                     if (cg == 0)
                         p.hd[row * e4m3_blocks(p.n) + n0 / EB] = __fdiv_rn(a, 448.0f);
                 }
-            } else if (p.rows32) {
+            } else if constexpr (OUT != Out::ANY && OUT != Out::ANY_ADD) {
                 if (row < p.m) {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) store_row(p, acc[i], row, n0 + half_col<UP>(cg, i));
+                    for (int i = 0; i < 2; ++i) store_row<OUT>(p, acc[i], row, n0 + half_col<UP>(cg, i));
                 }
             } else {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) store_any(p, acc[i], xp, m0 + 32 * q, n0 + half_col<UP>(cg, i), lane);
+                for (int i = 0; i < 2; ++i) store_any<OUT == Out::ANY_ADD>(p, acc[i], xp, m0 + 32 * q, n0 + half_col<UP>(cg, i), lane);
             }
         }
     }
@@ -736,18 +761,30 @@ static cudaError_t tile_maps(const uint8_t *w, int64_t w_rows, int64_t k, const 
     return e4m3_map(enc, &tw, w, w_rows, k, UP ? 128 : BN);
 }
 
-template <int BN, bool UP>
+template <int BN, Out OUT>
 static cudaError_t launch_tiles(const uint8_t *w, int64_t w_rows, int64_t k, const uint8_t *x, TileArgs p, cudaStream_t s)
 {
     using L = TileLayout<BN>;
+    constexpr bool UP = OUT == Out::UP;
     CUtensorMap tx, tw;
     if (cudaError_t e = tile_maps<BN, UP>(w, w_rows, k, x, p, tx, tw); e != cudaSuccess) return e;
-    constexpr int bytes = UP ? L::UP_BYTES : L::BYTES;
-    if (cudaError_t e = opt_in_smem(reinterpret_cast<const void *>(tiles_e4m3_kernel<BN, UP>), bytes); e != cudaSuccess)
-        return e;
+    constexpr int bytes = OUT == Out::ANY || OUT == Out::ANY_ADD ? L::ANY_BYTES : L::BYTES;
+    const auto kernel = tiles_e4m3_kernel<BN, OUT>;
+    if (cudaError_t e = opt_in_smem(reinterpret_cast<const void *>(kernel), bytes); e != cudaSuccess) return e;
     const int64_t grid = p.tiles < num_sms() ? p.tiles : num_sms();
-    return launch_pdl(tiles_e4m3_kernel<BN, UP>, dim3(static_cast<unsigned>(grid)), dim3(L::THREADS),
-                      static_cast<size_t>(bytes), s, tx, tw, p);
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(L::THREADS), static_cast<size_t>(bytes), s, tx, tw, p);
+}
+
+template <int BN>
+static cudaError_t launch_tiles_out(const uint8_t *w, int64_t n, int64_t k, const uint8_t *x, const TileArgs &p,
+                                    cudaStream_t s)
+{
+    // every row of y (and of the residual) starts on 32 bytes
+    const bool rows32 = n % (p.y_bf16 ? 16 : 8) == 0 && reinterpret_cast<uintptr_t>(p.y) % 32 == 0 &&
+                        reinterpret_cast<uintptr_t>(p.residual) % 32 == 0;
+    if (!rows32)
+        return p.residual ? launch_tiles<BN, Out::ANY_ADD>(w, n, k, x, p, s) : launch_tiles<BN, Out::ANY>(w, n, k, x, p, s);
+    return p.y_bf16 ? launch_tiles<BN, Out::BF16>(w, n, k, x, p, s) : launch_tiles<BN, Out::F32>(w, n, k, x, p, s);
 }
 
 template <int BN, bool UP>
@@ -833,8 +870,6 @@ cudaError_t launch_tiles_e4m3(const uint8_t *w, const float *wd, int64_t n, int6
     p.residual = residual;
     p.y = y;
     p.y_bf16 = y_dtype == QG_BF16;
-    p.rows32 = n % (p.y_bf16 ? 16 : 8) == 0 && reinterpret_cast<uintptr_t>(y) % 32 == 0 &&
-               reinterpret_cast<uintptr_t>(residual) % 32 == 0;
     const int64_t sms = num_sms(), mt = (m + TM - 1) / TM;
     // Too few tiles for the SMs: 64 columns wide, and a cluster to each.  Where a cluster of
     // two does not find room the walk over wider tiles is as fast or faster (512x2560x9216:
@@ -848,9 +883,9 @@ cudaError_t launch_tiles_e4m3(const uint8_t *w, const float *wd, int64_t n, int6
         const int64_t c = (mt * ((n + bn - 1) / bn) + sms - 1) / sms * bn;
         if (c < cost) cost = c, best = bn;
     }
-    if (best == 256) return launch_tiles<256, false>(w, n, k, x, p, s);
-    if (best == 192) return launch_tiles<192, false>(w, n, k, x, p, s);
-    return launch_tiles<128, false>(w, n, k, x, p, s);
+    if (best == 256) return launch_tiles_out<256>(w, n, k, x, p, s);
+    if (best == 192) return launch_tiles_out<192>(w, n, k, x, p, s);
+    return launch_tiles_out<128>(w, n, k, x, p, s);
 }
 
 cudaError_t launch_tiles_up_e4m3(const uint8_t *w, const float *wd, int64_t ffn, int64_t k, const uint8_t *x,
@@ -869,7 +904,7 @@ cudaError_t launch_tiles_up_e4m3(const uint8_t *w, const float *wd, int64_t ffn,
     const int64_t tiles = (m + TM - 1) / TM * e4m3_blocks(ffn);
     if (const int split = split_of<256, true>(tiles, p.kb); split > 1)
         return launch_split<256, true>(w, 2 * ffn, k, x, p, split, s);
-    return launch_tiles<256, true>(w, 2 * ffn, k, x, p, s);
+    return launch_tiles<256, Out::UP>(w, 2 * ffn, k, x, p, s);
 }
 
 }  // namespace qg

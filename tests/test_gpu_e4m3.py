@@ -235,6 +235,14 @@ def test_product_prompts(torch, qg, m, n, kind):
     check_product(torch, qg, np.random.default_rng(n), m, n, 272, kind, "place" if n % 2 else None)
 
 
+# the same with y's rows on 32 bytes and not, with and without a residual
+@pytest.mark.parametrize("residual", [None, "apart", "place"])
+@pytest.mark.parametrize("m,n,kind", [(m, n, kind) for m, n0 in ((2601, 1408), (1701, 1408), (1701, 1040))
+                                      for n, kind in ((n0, "f32"), (n0, "bf16"), (n0 + 1, "f32"), (n0 - 7, "bf16"))])
+def test_product_stores(torch, qg, m, n, kind, residual):
+    check_product(torch, qg, np.random.default_rng(m + n), m, n, 160, kind, residual)
+
+
 def test_product_largest_codes(torch, qg):
     """Every code 448 or -448: the largest block sums; exact in f32 where they do not cancel."""
     for m in (3, 140):
