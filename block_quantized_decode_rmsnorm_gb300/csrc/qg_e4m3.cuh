@@ -89,13 +89,13 @@ struct Vec4<__nv_bfloat16> {
 // SiLU(g) * u = g u / (1 + e^-g) to a few f32 ulp over the whole range.  The exponent
 // is carried as a rounded product -x log2(e) and its remainder (an FMA, and the
 // constant's own second part), so that the error of e^-x does not grow with |x|: the
-// approximation of 2^y is all that is left of it.  x is g held within +-87, where
-// neither e^-x nor its reciprocal leaves f32's normal range; below, g's own product
-// with 2^-125 is smaller than any value that a code stands for.
+// approximation of 2^y is all that is left of it.  x is g held within +-88: e^88 is
+// finite, and its reciprocal, 2^-127, is flushed to zero, so that SiLU is a zero for every
+// g below -87.4 (in truth it is under 2^-119 there), whatever g's size.
 constexpr float kLog2e = 1.4426950216293335f;       // log2(e) rounded to f32
 constexpr float kLog2eRest = 1.925963033500011e-08f;  // and what that leaves
 constexpr float kLn2 = 0.693147181f;
-constexpr float kSiluRange = 87.0f;
+constexpr float kSiluRange = 88.0f;
 
 __device__ __forceinline__ float ex2_approx(float x)
 {

@@ -353,6 +353,21 @@ def test_up_padding_row(torch, qg):
 
 
 @pytest.mark.parametrize("m", [4, 30, 2500])
+@pytest.mark.parametrize("scale", [1e-3, 1.0, 1e6])
+def test_up_negative_gates(torch, qg, m, scale):
+    """SiLU of a large negative gate is zero, however large the gate and the up value are:
+    nothing but zeros in a block of them, and the floor's scale."""
+    f, k = 272, 256
+    wq = np.concatenate([np.full((f, k), 0xFE, np.uint8), np.full((f, k), 0x7E, np.uint8)])  # -448 and 448
+    wd = np.full((2 * E.blocks(f), 2), scale, np.float32)
+    hq, hd = qg.qg_ffn_up_e4m3(qg.E4M3Weight(codes_dev(torch, wq), dev(torch, wd)),
+                               codes_dev(torch, np.full((m, k), 0x7E, np.uint8)),
+                               dev(torch, np.ones((m, 2), np.float32)))
+    assert np.all(bits(hq) & 0x7F == 0)
+    assert np.all(hd.cpu().numpy() == np.float32(2.0 ** -100) / np.float32(448))
+
+
+@pytest.mark.parametrize("m", [4, 30, 2500])
 def test_up_nan_row(torch, qg, m):
     """A NaN activation makes its own row's codes NaN, with the floor's scale, and leaves
     the other rows alone; a NaN weight its own column's."""
