@@ -605,6 +605,22 @@ __device__ __forceinline__ float4 cluster_sum4(const float *at, int split)
     return v;
 }
 
+// Four neighbouring residual values from `at` on, column c of n; zeros past the row's
+// end and where there is no residual.  whole: n is a multiple of four.
+__device__ __forceinline__ float4 residual4(const TileArgs &p, int64_t at, int64_t c, bool whole)
+{
+    float4 e = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (!p.residual) return e;
+    if (whole)
+        return p.y_bf16 ? Vec4<__nv_bfloat16>::widen(*reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p.residual) + at))
+                        : *reinterpret_cast<const float4 *>(static_cast<const float *>(p.residual) + at);
+    e.x = load_y(p.residual, at, p.y_bf16);
+    if (c + 1 < p.n) e.y = load_y(p.residual, at + 1, p.y_bf16);
+    if (c + 2 < p.n) e.z = load_y(p.residual, at + 2, p.y_bf16);
+    if (c + 3 < p.n) e.w = load_y(p.residual, at + 3, p.y_bf16);
+    return e;
+}
+
 template <int BN, bool UP>
 __global__ void __launch_bounds__(TileLayout<BN>::THREADS, TileLayout<BN>::SPLIT_CTAS)
     split_e4m3_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tw, const TileArgs p)
@@ -688,39 +704,29 @@ __global__ void __launch_bounds__(TileLayout<BN>::THREADS, TileLayout<BN>::SPLIT
         }
     } else {
         constexpr int G = BN / 4;  // groups of four columns
+        const int items = (r_end - rank * per) * G;
         const bool whole = (p.n & 3) == 0;
-        for (int i = threadIdx.x; i < (r_end - rank * per) * G; i += L::THREADS) {
+        for (int i = threadIdx.x; i < items; i += L::THREADS) {
             const int r = rank * per + i / G, c = 4 * (i % G);
             if (n0 + c >= p.n) continue;
-            const float4 s = cluster_sum4(sums + r * L::LD + c, p.split);
-            float v[4] = {s.x, s.y, s.z, s.w};
             const int64_t at = static_cast<int64_t>(m0 + r) * p.n + n0 + c;
+            const float4 e = residual4(p, at, n0 + c, whole);  // its load beside the sums' (100x2727x3600: 10.2 -> 9.2 us)
+            const float4 s = cluster_sum4(sums + r * L::LD + c, p.split);
+            const float4 o = p.residual ? make_float4(s.x + e.x, s.y + e.y, s.z + e.z, s.w + e.w) : s;
             if (whole) {
-                if (p.y_bf16) {
-                    using V = Vec4<__nv_bfloat16>;
-                    float4 o = make_float4(v[0], v[1], v[2], v[3]);
-                    if (p.residual) {
-                        const float4 e = V::widen(*reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p.residual) + at));
-                        o = make_float4(o.x + e.x, o.y + e.y, o.z + e.z, o.w + e.w);
-                    }
-                    *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.y) + at) = V::narrow(o);
-                } else {
-                    float4 o = make_float4(v[0], v[1], v[2], v[3]);
-                    if (p.residual) {
-                        const float4 e = *reinterpret_cast<const float4 *>(static_cast<const float *>(p.residual) + at);
-                        o = make_float4(o.x + e.x, o.y + e.y, o.z + e.z, o.w + e.w);
-                    }
+                if (p.y_bf16)
+                    *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.y) + at) = Vec4<__nv_bfloat16>::narrow(o);
+                else
                     *reinterpret_cast<float4 *>(static_cast<float *>(p.y) + at) = o;
-                }
             } else {
+                const float v[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if (n0 + c + e >= p.n) break;
-                    const float o = p.residual ? v[e] + load_y(p.residual, at + e, p.y_bf16) : v[e];
+                for (int j = 0; j < 4; ++j) {
+                    if (n0 + c + j >= p.n) break;
                     if (p.y_bf16)
-                        static_cast<__nv_bfloat16 *>(p.y)[at + e] = __float2bfloat16_rn(o);
+                        static_cast<__nv_bfloat16 *>(p.y)[at + j] = __float2bfloat16_rn(v[j]);
                     else
-                        static_cast<float *>(p.y)[at + e] = o;
+                        static_cast<float *>(p.y)[at + j] = v[j];
                 }
             }
         }
