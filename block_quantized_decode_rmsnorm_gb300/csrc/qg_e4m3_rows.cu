@@ -14,15 +14,17 @@
 //
 // What bounds it is the bytes in flight: a lane copies its own pieces of the next
 // blocks to shared memory by cp.async (no barrier: nobody else reads them), without
-// registers, from before the previous kernel has ended on.  A product's CTA has eight
-// warps, so that few rows still fill the SMs' queues (1x1024x3584: 2.3 us; four CTAs
-// of a cluster sharing k took 3.5); gate|up has twice the rows and four warps per CTA,
-// four CTAs an SM, so that one wave holds them all (1x9216x2560: 10.5 us, 14.3 with
-// eight warps).
+// registers, from before the previous kernel has ended on.  A CTA has eight warps, so
+// that few rows still fill the SMs' queues (1x1024x3584: 2.3 us; four CTAs of a cluster
+// sharing k took 3.5); where it then takes more than one wave, gate|up has four warps
+// per CTA and four CTAs an SM (1x9216x2560: 10.5 us, 14.3 with eight warps; 1x2048x4096:
+// 7.9 us, 6.0 with eight).
 //
 // Gate|up: 16 gate and the 16 matching up rows per CTA, eight CTAs of a cluster
 // hold the 128 outputs of one block of h, and exchange their largest magnitudes
 // through distributed shared memory before each writes its 16 codes per row.
+#include <algorithm>
+
 #include "qg_e4m3.cuh"
 
 namespace qg {
@@ -39,6 +41,7 @@ struct RowsArgs {
     int64_t up_row;    // gate|up: first up row
     int64_t up_block;  // and its first row of scales
     int k, kb;
+    int ahead;         // bytes of a row, from behind the ring's first blocks on, to bring to L2
     const uint8_t *x;
     const float *xd;
     int64_t m;
@@ -58,25 +61,27 @@ __device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-template <bool UP>
+// NARROW (gate|up): half the warps, so that twice the CTAs find room.
+template <bool UP, bool NARROW>
 struct RowsLayout {
-    static constexpr int W = UP ? 4 : 8;   // warps per CTA
-    static constexpr int T = UP ? 2 : 1;   // weight tiles per CTA
-    static constexpr int D = UP ? 2 : 6;   // blocks on their way per warp
+    static constexpr int W = NARROW ? 4 : 8;  // warps per CTA
+    static constexpr int T = UP ? 2 : 1;      // weight tiles per CTA
+    static constexpr int D = NARROW ? 2 : UP ? 3 : 6;  // blocks on their way per warp
     static constexpr int F = 3;            // steps whose activations are
-    static constexpr int RING = W * D * T * R_TILE;  // 32 and 96 KB
-    static constexpr int CTAS = UP ? 4 : 2;          // per SM
+    static constexpr int RING = W * D * T * R_TILE;  // 96 KB, or 32
+    static constexpr int CTAS = NARROW ? 4 : 2;      // per SM
 };
 
 // MANY: a CTA walks over several tiles, the next one's weights on their way while a tile
 // ends; without it the tile is the CTA's only one and nothing is kept of the next.
-template <bool UP, bool MANY>
-__global__ void __launch_bounds__(RowsLayout<UP>::W * 32, RowsLayout<UP>::CTAS) rows_e4m3_kernel(const RowsArgs p)
+template <bool UP, bool NARROW, bool MANY>
+__global__ void __launch_bounds__(RowsLayout<UP, NARROW>::W * 32, RowsLayout<UP, NARROW>::CTAS)
+    rows_e4m3_kernel(const RowsArgs p)
 {
-    using L = RowsLayout<UP>;
+    using L = RowsLayout<UP, NARROW>;
     constexpr int RW = L::W, RT = L::T, D = L::D, F = L::F;
     extern __shared__ __align__(16) uint8_t ring_raw[];  // [warp][slot][tile][row half][block half][lane] of 16 bytes
-    __shared__ float red[2][RW][RT][8 * RR];             // [tile parity][warp]: one barrier a tile
+    __shared__ float red[MANY ? 2 : 1][RW][RT][8 * RR];  // [tile parity][warp]: one barrier a tile
     __shared__ float top[8];  // gate|up: the rows' largest magnitudes
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, c = lane & 3;
@@ -128,6 +133,15 @@ __global__ void __launch_bounds__(RowsLayout<UP>::W * 32, RowsLayout<UP>::CTAS) 
     };
 #pragma unroll
     for (int i = 0; i < D; ++i) stage();
+    // what comes behind the ring's blocks into L2 meanwhile, a piece per row
+    if (!NARROW && !MANY && p.ahead > 0 && threadIdx.x < RT * RR) {
+        const int64_t row = static_cast<int64_t>(blockIdx.x) * RR + threadIdx.x % RR;
+        if (row < p.n)
+            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                             p.w + ((threadIdx.x / RR ? p.up_row : 0) + row) * p.k + D * RW * EB),
+                         "r"(p.ahead)
+                         : "memory");
+    }
     pdl_wait();
     pdl_trigger();
 
@@ -269,13 +283,25 @@ __global__ void __launch_bounds__(RowsLayout<UP>::W * 32, RowsLayout<UP>::CTAS) 
     if (!MANY) finish();
 }
 
-template <bool UP, bool MANY>
-static cudaError_t launch_rows(int64_t ctas, const RowsArgs &p, cudaStream_t s)
+// At most three CTAs of eight warps on two SMs (of the four that find room).
+template <bool UP>
+static bool few(int64_t tiles)
 {
-    using L = RowsLayout<UP>;
+    return 4 * tiles <= 3 * RowsLayout<UP, false>::CTAS * static_cast<int64_t>(num_sms());
+}
+
+template <bool UP, bool NARROW, bool MANY>
+static cudaError_t launch_rows(int64_t ctas, RowsArgs p, cudaStream_t s)
+{
+    using L = RowsLayout<UP, NARROW>;
     const int need = (p.kb + L::W - 1) / L::W;
+    constexpr int ring = L::D * L::W * EB;  // columns in flight
+    // Where the next kernel's CTAs find room beside these, a second ring's columns go to L2
+    // before the wait (7x2560x9216 bf16: 7.9 -> 7.2 us, 1x2560x12288: 9.2 -> 8.6); with two
+    // CTAs an SM it is no gain (1x4096x14336: 11.4 us, 12.4 with all columns).
+    if (few<UP>(p.tiles)) p.ahead = std::max(0, std::min(p.k - ring, ring));
     const int bytes = L::W * (MANY || need > L::D ? L::D : need) * L::T * R_TILE;
-    const auto kernel = rows_e4m3_kernel<UP, MANY>;
+    const auto kernel = rows_e4m3_kernel<UP, NARROW, MANY>;
     if (cudaError_t e = opt_in_smem(reinterpret_cast<const void *>(kernel), L::RING); e != cudaSuccess) return e;
     return launch_pdl_cluster(kernel, dim3(static_cast<unsigned>(ctas)), dim3(L::W * 32), static_cast<size_t>(bytes), s,
                               UP ? UP_CLUSTER : 1, p);
@@ -299,10 +325,10 @@ cudaError_t launch_rows_e4m3(const uint8_t *w, const float *wd, int64_t n, int64
     p.tiles = (n + RR - 1) / RR;
     // More tiles than CTAs find room: as many each (65536x1024: 18.1 us against 28.5 with
     // a CTA to each; 1024x3584, one each: 2.3 us, and 2.8 by the kernel that walks).
-    const int64_t room = RowsLayout<false>::CTAS * static_cast<int64_t>(num_sms());
-    if (p.tiles <= room) return launch_rows<false, false>(p.tiles, p, s);
+    const int64_t room = RowsLayout<false, false>::CTAS * static_cast<int64_t>(num_sms());
+    if (p.tiles <= room) return launch_rows<false, false, false>(p.tiles, p, s);
     const int64_t each = (p.tiles + room - 1) / room;
-    return launch_rows<false, true>((p.tiles + each - 1) / each, p, s);
+    return launch_rows<false, false, true>((p.tiles + each - 1) / each, p, s);
 }
 
 cudaError_t launch_rows_up_e4m3(const uint8_t *w, const float *wd, int64_t ffn, int64_t k, const uint8_t *x,
@@ -322,7 +348,10 @@ cudaError_t launch_rows_up_e4m3(const uint8_t *w, const float *wd, int64_t ffn, 
     p.hq = hq;
     p.hd = hd;
     p.tiles = e4m3_blocks(ffn) * UP_CLUSTER;
-    return launch_rows<true, false>(p.tiles, p, s);
+    // Eight warps a CTA up to there: 1x512x2560 3.2 us and 4.1 with four, 8x3584x2560 6.5 and
+    // 6.9, 8x3584x1024 4.0 and 3.9; 8x4608x2560 8.8 and 7.7.
+    if (few<true>(p.tiles)) return launch_rows<true, false, false>(p.tiles, p, s);
+    return launch_rows<true, true, false>(p.tiles, p, s);
 }
 
 }  // namespace qg

@@ -332,6 +332,18 @@ def test_up_prompts(torch, qg, m, f, k):
     check_up(torch, qg, np.random.default_rng(f), m, f, k)
 
 
+# few rows: eight and four warps a CTA, blocks within the ring, behind it, and behind what goes to L2
+@pytest.mark.parametrize("m,f,k", [(1, 3648, 272), (8, 3664, 272), (3, 5008, 1168), (8, 512, 9216), (2, 400, 3088),
+                                   (5, 144, 6160)])
+def test_up_few_rows(torch, qg, m, f, k):
+    check_up(torch, qg, np.random.default_rng(f + k), m, f, k)
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 272, 6144), (8, 400, 6160), (3, 144, 12304), (2, 272, 18448), (7, 2560, 9216)])
+def test_product_few_rows_deep(torch, qg, m, n, k):
+    check_product(torch, qg, np.random.default_rng(n + k), m, n, k, "bf16" if m % 2 else "f32", "apart")
+
+
 def test_up_large_arguments(torch, qg):
     """Gates far into both tails of the SiLU."""
     for m in (4, 130):
