@@ -65,6 +65,7 @@ SIGNATURES = {
     "qgemm_e4m3": (ST, [P, P, I64, I64, P, P, I64, I32, P, P, I32, P]),
     "qg_ffn_up_e4m3": (ST, [P, P, I64, I64, P, P, I64, P, P, P]),
     "qg_ffn_e4m3": (ST, [P, P, P, I32, I64, I64, I64, F32, P, P, P, P, P, P, P, P, P, P]),
+    "qg_debug_stalled_e4m3": (ST, [P, P, I64, I64, P, P, I64, P, P, I64, I64, P]),
 }
 
 _lib = None

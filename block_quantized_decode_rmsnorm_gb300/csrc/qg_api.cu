@@ -80,6 +80,8 @@ cudaError_t launch_tiles_e4m3(const uint8_t *, const float *, int64_t, int64_t, 
                               const void *, void *, int, cudaStream_t);
 cudaError_t launch_tiles_up_e4m3(const uint8_t *, const float *, int64_t, int64_t, const uint8_t *, const float *,
                                  int64_t, uint8_t *, float *, cudaStream_t);
+cudaError_t launch_stalled_e4m3(const uint8_t *, const float *, int64_t, int64_t, const uint8_t *, const float *,
+                                int64_t, void *, float *, int64_t, int64_t, cudaStream_t);
 
 // SM count of the current device, read once per device.
 int num_sms()
@@ -757,6 +759,20 @@ qg_status qg_ffn_e4m3(const void *x, const void *residual, const void *gamma, in
         return st;
     if (qg_status st = qg_ffn_up_e4m3(wgu, wgu_d, ffn, hidden, xq, xd, m, hq, hd, stream); st != QG_OK) return st;
     return qgemm_e4m3(wdn, wdn_d, hidden, ffn, hq, hd, m, QG_EPI_RESIDUAL_ADD, s, y, dtype, stream);
+}
+
+qg_status qg_debug_stalled_e4m3(const uint8_t *w, const float *wd, int64_t n, int64_t k, const uint8_t *xq,
+                                const float *xd, int64_t m, void *out, float *out_d, int64_t cta, int64_t block,
+                                qg_stream_t stream)
+{
+    if (!e4m3_k_ok(k, kMaxK) || m <= kE4M3FewRows || m > kE4M3MaxM || n <= 0 || n >= (int64_t(1) << 30) - 256 ||
+        (out_d && n % 16 != 0) || cta < 0 || block < 0)
+        return QG_ERR_SHAPE;
+    if (!w || !wd || !xq || !xd || !out) return QG_ERR_NULL;
+    if (!aligned(w, 16) || !aligned(wd, 4) || !aligned(xq, 16) || !aligned(xd, 4) || !aligned(out, 16) ||
+        !aligned(out_d, 4))
+        return QG_ERR_ALIGN;
+    return from_cuda(qg::launch_stalled_e4m3(w, wd, n, k, xq, xd, m, out, out_d, cta, block, stream));
 }
 
 }  // extern "C"

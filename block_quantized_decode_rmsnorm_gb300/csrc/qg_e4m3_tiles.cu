@@ -22,8 +22,9 @@
 // up (in rank order, through distributed shared memory) and finishes a share of the
 // rows.
 //
-// Every barrier wait is bounded by the global timer; a stalled pipeline aborts (NaN
-// outputs or codes for the tiles left) instead of hanging.
+// Every barrier wait is bounded by the global timer; a stalled pipeline aborts instead
+// of hanging: the CTA waits (bounded) for the copies and MMAs that it has issued, and the
+// tiles that it has left become NaN outputs or codes (a cluster's tile as a whole).
 //
 // Measured: gate|up 8192x9216x2560 305 us (2.53 PFLOP/s; 333 under the power cap that
 // sets in after a second), product 4096x2560x9216 with the residual 80 us (88), both
@@ -32,6 +33,7 @@
 // (227 and 73 us alone); 100x2727x3600 8.5 us, bound by its chain of latencies.
 #include <algorithm>
 #include <cuda.h>
+#include <type_traits>
 
 #include "qg_e4m3.cuh"
 #include "qg_tc.cuh"
@@ -82,7 +84,18 @@ struct TileArgs {
     int y_bf16;
     uint8_t *hq;
     float *hd;
+    static constexpr uint64_t limit_ns = kCopyWaitLimitNs;  // of a barrier wait
 };
+
+// With a stall made on purpose (qg_debug_stalled_e4m3): CTA `cta` issues the copies of its
+// block number `block` late, and waits are shorter.  A type of its own, and kernels of its
+// own: the limit as a value and the comparison per block cost the others 1 %.
+struct StalledArgs : TileArgs {
+    int64_t cta, block;
+    static constexpr uint64_t limit_ns = 5000000, hold_ns = 50000000;
+};
+template <class P>
+constexpr bool kStalls = std::is_same<P, StalledArgs>::value;
 
 __device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
 {
@@ -100,6 +113,7 @@ struct TileShared {
     float2 f[2][T_SB][TM];
     uint32_t tmem;
     int abort_flag;
+    uint32_t issued[2];  // the walk: blocks that the copy warp and the MMA warp have issued, at the end
 };
 
 // First column (in the tile) of half i (32 columns) of column group cg.
@@ -139,9 +153,10 @@ __device__ __forceinline__ void tile_setup(TileShared &b, int warp)
 // tc_wait for barriers that have mostly completed by the time they are asked for: one
 // plain try first, 13 cycles against the 103 of tc_wait's way in (its suspended try and
 // what surrounds it), five times per block.
-__device__ __forceinline__ bool stage_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag)
+template <class P>
+__device__ __forceinline__ bool stage_wait(uint64_t *bar, uint32_t parity, TileShared &b)
 {
-    return mbar_try_wait(bar, parity) || tc_wait(bar, parity, abort_flag);
+    return mbar_try_wait(bar, parity) || tc_wait(bar, parity, &b.abort_flag, P::limit_ns);
 }
 
 // One lane of a converged warp.  The tensor core's and the copy engine's
@@ -186,8 +201,8 @@ __device__ __forceinline__ void copy_weights(const CUtensorMap &tw, const TileAr
 // Copies of blocks [kb0, kb1) of one tile; `it` counts blocks over all tiles.  A split
 // tile's first weights go out before the wait for the previous kernel, which makes the
 // activations.
-template <int BN, bool UP, bool SPLIT>
-__device__ __forceinline__ bool tile_copies(const CUtensorMap &tx, const CUtensorMap &tw, const TileArgs &p,
+template <int BN, bool UP, bool SPLIT, class P>
+__device__ __forceinline__ bool tile_copies(const CUtensorMap &tx, const CUtensorMap &tw, const P &p,
                                             TileShared &b, uint8_t *smem, int m0, int n0, int kb0, int kb1,
                                             uint32_t &it)
 {
@@ -203,7 +218,10 @@ __device__ __forceinline__ bool tile_copies(const CUtensorMap &tx, const CUtenso
     }
     for (int kb = kb0; kb < kb1; ++kb, ++it) {
         const uint32_t s = it % S, use = it / S;
-        if (!__all_sync(0xffffffffu, stage_wait(&b.done[s], (use & 1) ^ 1, &b.abort_flag))) return false;
+        if (!__all_sync(0xffffffffu, stage_wait<P>(&b.done[s], (use & 1) ^ 1, b))) return false;
+        if constexpr (kStalls<P>)
+            if (p.cta == blockIdx.x && p.block == it)
+                for (const uint64_t t0 = global_ns(); global_ns() - t0 < P::hold_ns;) __nanosleep(1000);
         if (elect_one()) {
             uint8_t *st = smem + s * bytes;
             if (kb >= early) copy_weights<BN, UP>(tw, p, b, st, s, n0, kb);
@@ -215,8 +233,8 @@ __device__ __forceinline__ bool tile_copies(const CUtensorMap &tx, const CUtenso
 }
 
 // The MMAs of one tile's blocks, each into its own TMEM buffer.
-template <int BN, bool SPLIT>
-__device__ __forceinline__ bool tile_mmas(const TileArgs &p, TileShared &b, uint32_t tmem, uint64_t desc0, int blocks,
+template <int BN, bool SPLIT, class P>
+__device__ __forceinline__ bool tile_mmas(const P &p, TileShared &b, uint32_t tmem, uint64_t desc0, int blocks,
                                           uint32_t &it)
 {
     using L = TileLayout<BN>;
@@ -225,8 +243,7 @@ __device__ __forceinline__ bool tile_mmas(const TileArgs &p, TileShared &b, uint
     constexpr uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(BN >> 3) << 17) | (static_cast<uint32_t>(TM >> 4) << 24);
     for (int i = 0; i < blocks; ++i, ++it) {
         const uint32_t s = it % S, use = it / S, t = it % L::BUFS, tuse = it / L::BUFS;
-        const bool ok = stage_wait(&b.full[s], use & 1, &b.abort_flag) &&
-                        stage_wait(&b.tempty[t], (tuse & 1) ^ 1, &b.abort_flag);
+        const bool ok = stage_wait<P>(&b.full[s], use & 1, b) && stage_wait<P>(&b.tempty[t], (tuse & 1) ^ 1, b);
         if (!__all_sync(0xffffffffu, ok)) return false;
         tc_fence_after();
         if (elect_one()) {
@@ -242,8 +259,8 @@ __device__ __forceinline__ bool tile_mmas(const TileArgs &p, TileShared &b, uint
 
 // The scale warp: the factors of blocks [kb0, kb1) of one tile, T_SB at a time, the
 // next scales on their way while the last factors are waited for.  `c` counts buffers.
-template <int BN, bool UP>
-__device__ __forceinline__ bool tile_scales(const TileArgs &p, TileShared &b, int lane, int m0, int n0, int kb0,
+template <int BN, bool UP, class P>
+__device__ __forceinline__ bool tile_scales(const P &p, TileShared &b, int lane, int m0, int n0, int kb0,
                                             int kb1, uint32_t &c)
 {
     const float *xr[TM / 32];
@@ -270,7 +287,7 @@ __device__ __forceinline__ bool tile_scales(const TileArgs &p, TileShared &b, in
             wb[o] = kb + o < kb1 ? w1[kb + o] : 0.0f;
         }
         const uint32_t t = c & 1, use = c >> 1;
-        if (!__all_sync(0xffffffffu, stage_wait(&b.sempty[t], (use & 1) ^ 1, &b.abort_flag))) return false;
+        if (!__all_sync(0xffffffffu, stage_wait<P>(&b.sempty[t], (use & 1) ^ 1, b))) return false;
 #pragma unroll
         for (int i = 0; i < TM / 32; ++i)
 #pragma unroll
@@ -283,8 +300,8 @@ __device__ __forceinline__ bool tile_scales(const TileArgs &p, TileShared &b, in
 
 // The sums of blocks [kb0, kb1) of one tile in registers: two halves of 32 columns of
 // this thread's row, in adjacent pairs.  `it` counts blocks, `c` buffers of scales.
-template <int BN, bool UP, bool SPLIT>
-__device__ __forceinline__ bool tile_sums(const TileArgs &p, TileShared &b, uint32_t tmem, int q, int cg, int lane,
+template <int BN, bool UP, bool SPLIT, class P>
+__device__ __forceinline__ bool tile_sums(const P &p, TileShared &b, uint32_t tmem, int q, int cg, int lane,
                                           int n0, int kb0, int kb1, uint32_t &it, uint32_t &c,
                                           uint64_t (&acc)[2][16])
 {
@@ -295,7 +312,7 @@ __device__ __forceinline__ bool tile_sums(const TileArgs &p, TileShared &b, uint
     const int second = UP ? 0 : (n0 + T_CW * cg) / EB - n0 / EB;  // this warp's columns lie in the second block
     for (int kb = kb0; kb < kb1; kb += T_SB, ++c) {
         const uint32_t sb = c & 1, suse = c >> 1;
-        if (!__all_sync(0xffffffffu, stage_wait(&b.sfull[sb], suse & 1, &b.abort_flag))) return false;
+        if (!__all_sync(0xffffffffu, stage_wait<P>(&b.sfull[sb], suse & 1, b))) return false;
 #pragma unroll 1
         for (int o = 0; o < T_SB; ++o) {
             if (kb + o >= kb1) break;
@@ -313,7 +330,7 @@ __device__ __forceinline__ bool tile_sums(const TileArgs &p, TileShared &b, uint
             const uint32_t t = it % TileLayout<BN>::BUFS, s = it % stages_of<BN, SPLIT>(p),
                            use = it / stages_of<BN, SPLIT>(p);
             // tcgen05.ld is warp-collective: the whole warp proceeds or stops
-            if (!__all_sync(0xffffffffu, stage_wait(&b.done[s], use & 1, &b.abort_flag))) return false;
+            if (!__all_sync(0xffffffffu, stage_wait<P>(&b.done[s], use & 1, b))) return false;
             tc_fence_after();
             const uint32_t ta = tmem + (static_cast<uint32_t>(32 * q) << 16) + t * BN;
 #pragma unroll
@@ -338,6 +355,29 @@ __device__ __forceinline__ bool tile_sums(const TileArgs &p, TileShared &b, uint
         }
     }
     return true;
+}
+
+// After every role's last block, and all threads behind a __syncthreads: without an abort
+// the MMA warp has waited for every copy and the epilogue for every MMA.  After one, waits
+// (bounded) for whatever this warp has issued (`issued` blocks, of the copy and of the MMA
+// warp), whichever role gave up: for the last copy into each stage (earlier ones were waited
+// for before a stage was filled again), and for the last commit, which covers those before.
+// False after an abort: shared memory and TMEM may be used again, the sums are not to be.
+// (The split kernel passes its count on in a register, the walk through shared memory:
+// registers there are all taken, and 512x2560x9216 took 22.5 us instead of 21.4.)
+template <int BN, bool SPLIT, class P>
+__device__ __forceinline__ bool tile_drain(const P &p, TileShared &b, int warp, uint32_t issued)
+{
+    using L = TileLayout<BN>;
+    if (*static_cast<volatile int *>(&b.abort_flag) == 0) return true;
+    const uint32_t S = stages_of<BN, SPLIT>(p);
+    if (warp == L::TMA_WARP)
+        for (uint32_t j = issued > S ? issued - S : 0; j < issued; ++j)
+            mbar_wait_bounded(&b.full[j % S], (j / S) & 1, kCopyWaitLimitNs);
+    if (warp == L::MMA_WARP && issued > 0)
+        mbar_wait_bounded(&b.done[(issued - 1) % S], ((issued - 1) / S) & 1, kCopyWaitLimitNs);
+    __syncthreads();
+    return false;
 }
 
 // silu_mul_e of two values, the products and FMAs packed.
@@ -473,9 +513,9 @@ __device__ __forceinline__ void store_any(const TileArgs &p, const uint64_t (&ac
     }
 }
 
-template <int BN, Out OUT>
+template <int BN, Out OUT, class P>
 __global__ void __launch_bounds__(TileLayout<BN>::THREADS, 1)
-    tiles_e4m3_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tw, const TileArgs p)
+    tiles_e4m3_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tw, const P p)
 {
     using L = TileLayout<BN>;
     constexpr bool UP = OUT == Out::UP;
@@ -497,14 +537,11 @@ __global__ void __launch_bounds__(TileLayout<BN>::THREADS, 1)
         for (int tile = blockIdx.x; ok && tile < p.tiles; tile += gridDim.x)
             ok = tile_copies<BN, UP, false>(tx, tw, p, b, smem, (tile % p.m_tiles) * TM, (tile / p.m_tiles) * BO, 0,
                                             p.kb, it);
-        // After an abort the last copies may still be landing: let them finish
-        // (bounded) before the CTA's shared memory goes away.
-        if (!ok && it > 0) mbar_wait_bounded(&b.full[(it - 1) % L::STAGES], ((it - 1) / L::STAGES) & 1, kCopyWaitLimitNs);
+        b.issued[0] = it;
     } else if (warp == L::MMA_WARP) {
         for (int tile = blockIdx.x; ok && tile < p.tiles; tile += gridDim.x)
             ok = tile_mmas<BN, false>(p, b, tmem, desc0, p.kb, it);
-        // After an abort, wait (bounded) for the last issued MMAs before TMEM is freed.
-        if (!ok && it > 0) mbar_wait_bounded(&b.done[(it - 1) % L::STAGES], ((it - 1) / L::STAGES) & 1, kCopyWaitLimitNs);
+        b.issued[1] = it;
     } else if (warp == L::SCALE_WARP) {
         for (int tile = blockIdx.x; ok && tile < p.tiles; tile += gridDim.x)
             ok = tile_scales<BN, UP>(p, b, lane, (tile % p.m_tiles) * TM, (tile / p.m_tiles) * BO, 0, p.kb, c);
@@ -569,6 +606,7 @@ __global__ void __launch_bounds__(TileLayout<BN>::THREADS, 1)
     }
     tc_fence_before();
     __syncthreads();
+    tile_drain<BN, false>(p, b, warp, b.issued[warp == L::MMA_WARP]);  // before the CTA's shared memory and TMEM go away
     if (warp == L::MMA_WARP) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(L::TMEM) : "memory");
@@ -621,9 +659,27 @@ __device__ __forceinline__ float4 residual4(const TileArgs &p, int64_t at, int64
     return e;
 }
 
-template <int BN, bool UP>
+// NaN outputs, or NaN codes and the floor's scales, for a whole tile.
+template <bool UP>
+__device__ __forceinline__ void nan_tile(const TileArgs &p, int m0, int rows, int n0, int width)
+{
+    const int cols = static_cast<int>(min(p.n - n0, static_cast<int64_t>(width)));
+    for (int i = threadIdx.x; i < rows * cols; i += blockDim.x) {
+        const int64_t row = m0 + i / cols, at = row * p.n + n0 + i % cols;
+        if constexpr (UP) {
+            p.hq[at] = 0x7f;
+            if (i % cols == 0) p.hd[row * e4m3_blocks(p.n) + n0 / EB] = __fdiv_rn(e4m3_floor(0.0f), 448.0f);
+        } else if (p.y_bf16) {
+            static_cast<__nv_bfloat16 *>(p.y)[at] = __ushort_as_bfloat16(0x7fff);
+        } else {
+            static_cast<float *>(p.y)[at] = __int_as_float(0x7fc00000);
+        }
+    }
+}
+
+template <int BN, bool UP, class P>
 __global__ void __launch_bounds__(TileLayout<BN>::THREADS, TileLayout<BN>::SPLIT_CTAS)
-    split_e4m3_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tw, const TileArgs p)
+    split_e4m3_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tw, const P p)
 {
     using L = TileLayout<BN>;
     constexpr int BO = UP ? 128 : BN;
@@ -643,27 +699,23 @@ __global__ void __launch_bounds__(TileLayout<BN>::THREADS, TileLayout<BN>::SPLIT
     const uint32_t tmem = __shfl_sync(0xffffffffu, b.tmem, 0);
     const uint64_t desc0 = umma_desc_sw128(smem_addr(smem));
     uint32_t it = 0, c = 0;
-    bool ok = true;
     uint64_t acc[2][16];
     if (warp == L::TMA_WARP) {
-        ok = tile_copies<BN, UP, true>(tx, tw, p, b, smem, m0, n0, kb0, kb1, it);
-        if (!ok) {  // let the last copies land (bounded), the early weights' among them
-            const uint32_t last = max(it, static_cast<uint32_t>(min(p.stages, kb1 - kb0))) - 1;
-            mbar_wait_bounded(&b.full[last % p.stages], (last / p.stages) & 1, kCopyWaitLimitNs);
-        }
+        // (the first use of a stage waits for nothing: early weights' blocks are always copied)
+        tile_copies<BN, UP, true>(tx, tw, p, b, smem, m0, n0, kb0, kb1, it);
     } else if (warp == L::MMA_WARP) {
         pdl_wait();
-        ok = tile_mmas<BN, true>(p, b, tmem, desc0, kb1 - kb0, it);
-        if (!ok && it > 0) mbar_wait_bounded(&b.done[(it - 1) % p.stages], ((it - 1) / p.stages) & 1, kCopyWaitLimitNs);
+        tile_mmas<BN, true>(p, b, tmem, desc0, kb1 - kb0, it);
     } else if (warp == L::SCALE_WARP) {
         pdl_wait();
         tile_scales<BN, UP>(p, b, lane, m0, n0, kb0, kb1, c);
     } else {
         pdl_wait();
-        ok = tile_sums<BN, UP, true>(p, b, tmem, q, cg, lane, n0, kb0, kb1, it, c, acc);
+        tile_sums<BN, UP, true>(p, b, tmem, q, cg, lane, n0, kb0, kb1, it, c, acc);
     }
     tc_fence_before();
-    __syncthreads();  // every copy has landed and every MMA is done: the stages are free
+    __syncthreads();
+    const bool whole = tile_drain<BN, true>(p, b, warp, it);  // copies landed, MMAs done: the stages are free
     if (warp == L::MMA_WARP) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(L::TMEM) : "memory");
@@ -671,15 +723,13 @@ __global__ void __launch_bounds__(TileLayout<BN>::THREADS, TileLayout<BN>::SPLIT
     float *sums = reinterpret_cast<float *>(smem);  // [128][LD]
     const int rows = static_cast<int>(min(p.m - m0, static_cast<int64_t>(TM)));
     if (warp < L::EW && 32 * q + lane < rows) {
-        const float nan = __int_as_float(0x7fc00000);
         float *r = sums + (32 * q + lane) * L::LD;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int j = 0; j < 16; j += 2) {
                 const float2 v0 = unpack2(acc[i][j]), v1 = unpack2(acc[i][j + 1]);
-                *reinterpret_cast<float4 *>(r + half_col<UP>(cg, i) + 2 * j) =
-                    ok ? make_float4(v0.x, v0.y, v1.x, v1.y) : make_float4(nan, nan, nan, nan);
+                *reinterpret_cast<float4 *>(r + half_col<UP>(cg, i) + 2 * j) = make_float4(v0.x, v0.y, v1.x, v1.y);
             }
     }
     cluster_sync();
@@ -705,15 +755,15 @@ __global__ void __launch_bounds__(TileLayout<BN>::THREADS, TileLayout<BN>::SPLIT
     } else {
         constexpr int G = BN / 4;  // groups of four columns
         const int items = (r_end - rank * per) * G;
-        const bool whole = (p.n & 3) == 0;
+        const bool fours = (p.n & 3) == 0;
         for (int i = threadIdx.x; i < items; i += L::THREADS) {
             const int r = rank * per + i / G, c = 4 * (i % G);
             if (n0 + c >= p.n) continue;
             const int64_t at = static_cast<int64_t>(m0 + r) * p.n + n0 + c;
-            const float4 e = residual4(p, at, n0 + c, whole);  // its load beside the sums' (100x2727x3600: 10.2 -> 9.2 us)
+            const float4 e = residual4(p, at, n0 + c, fours);  // its load beside the sums' (100x2727x3600: 10.2 -> 9.2 us)
             const float4 s = cluster_sum4(sums + r * L::LD + c, p.split);
             const float4 o = p.residual ? make_float4(s.x + e.x, s.y + e.y, s.z + e.z, s.w + e.w) : s;
-            if (whole) {
+            if (fours) {
                 if (p.y_bf16)
                     *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.y) + at) = Vec4<__nv_bfloat16>::narrow(o);
                 else
@@ -731,7 +781,8 @@ __global__ void __launch_bounds__(TileLayout<BN>::THREADS, TileLayout<BN>::SPLIT
             }
         }
     }
-    cluster_sync();  // the others have read this CTA's sums
+    cluster_sync();  // the others have read this CTA's sums, and written what they made of them
+    if (!whole) nan_tile<UP>(p, m0, rows, n0, BO);
 }
 
 // ---------------------------------------------------------------------------
@@ -767,15 +818,15 @@ static cudaError_t tile_maps(const uint8_t *w, int64_t w_rows, int64_t k, const 
     return e4m3_map(enc, &tw, w, w_rows, k, UP ? 128 : BN);
 }
 
-template <int BN, Out OUT>
-static cudaError_t launch_tiles(const uint8_t *w, int64_t w_rows, int64_t k, const uint8_t *x, TileArgs p, cudaStream_t s)
+template <int BN, Out OUT, class P>
+static cudaError_t launch_tiles(const uint8_t *w, int64_t w_rows, int64_t k, const uint8_t *x, P p, cudaStream_t s)
 {
     using L = TileLayout<BN>;
     constexpr bool UP = OUT == Out::UP;
     CUtensorMap tx, tw;
     if (cudaError_t e = tile_maps<BN, UP>(w, w_rows, k, x, p, tx, tw); e != cudaSuccess) return e;
     constexpr int bytes = OUT == Out::ANY || OUT == Out::ANY_ADD ? L::ANY_BYTES : L::BYTES;
-    const auto kernel = tiles_e4m3_kernel<BN, OUT>;
+    const auto kernel = tiles_e4m3_kernel<BN, OUT, P>;
     if (cudaError_t e = opt_in_smem(reinterpret_cast<const void *>(kernel), bytes); e != cudaSuccess) return e;
     const int64_t grid = p.tiles < num_sms() ? p.tiles : num_sms();
     return launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(L::THREADS), static_cast<size_t>(bytes), s, tx, tw, p);
@@ -793,8 +844,8 @@ static cudaError_t launch_tiles_out(const uint8_t *w, int64_t n, int64_t k, cons
     return p.y_bf16 ? launch_tiles<BN, Out::BF16>(w, n, k, x, p, s) : launch_tiles<BN, Out::F32>(w, n, k, x, p, s);
 }
 
-template <int BN, bool UP>
-static cudaError_t launch_split(const uint8_t *w, int64_t w_rows, int64_t k, const uint8_t *x, TileArgs p, int split,
+template <int BN, bool UP, class P>
+static cudaError_t launch_split(const uint8_t *w, int64_t w_rows, int64_t k, const uint8_t *x, P p, int split,
                                 cudaStream_t s)
 {
     using L = TileLayout<BN>;
@@ -809,10 +860,9 @@ static cudaError_t launch_split(const uint8_t *w, int64_t w_rows, int64_t k, con
     p.stages = std::min({blocks, T_STAGES, (L::SPLIT_ROOM - pad) / p.stage});
     const int rows = static_cast<int>(std::min<int64_t>(p.m, TM));
     const int bytes = std::max(p.stages * p.stage + pad, rows * L::LD * 4) + 1024;
-    if (cudaError_t e = opt_in_smem(reinterpret_cast<const void *>(split_e4m3_kernel<BN, UP>), L::SPLIT_ROOM + 1024);
-        e != cudaSuccess)
-        return e;
-    return launch_pdl_cluster(split_e4m3_kernel<BN, UP>, dim3(static_cast<unsigned>(p.tiles * split)), dim3(L::THREADS),
+    const auto kernel = split_e4m3_kernel<BN, UP, P>;
+    if (cudaError_t e = opt_in_smem(reinterpret_cast<const void *>(kernel), L::SPLIT_ROOM + 1024); e != cudaSuccess) return e;
+    return launch_pdl_cluster(kernel, dim3(static_cast<unsigned>(p.tiles * split)), dim3(L::THREADS),
                               static_cast<size_t>(bytes), s, static_cast<unsigned>(split), tx, tw, p);
 }
 
@@ -843,8 +893,9 @@ static int clusters_at_once(int split)
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
         int one = 0;
-        if (opt_in_smem(reinterpret_cast<const void *>(split_e4m3_kernel<BN, UP>), L::SPLIT_ROOM + 1024) != cudaSuccess ||
-            cudaOccupancyMaxActiveClusters(&one, split_e4m3_kernel<BN, UP>, &cfg) != cudaSuccess || one <= 0) {
+        const auto kernel = split_e4m3_kernel<BN, UP, TileArgs>;
+        if (opt_in_smem(reinterpret_cast<const void *>(kernel), L::SPLIT_ROOM + 1024) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&one, kernel, &cfg) != cudaSuccess || one <= 0) {
             cudaGetLastError();
             one = 1;
         }
@@ -864,8 +915,8 @@ static int split_of(int64_t tiles, int64_t kb)
     return 1;
 }
 
-cudaError_t launch_tiles_e4m3(const uint8_t *w, const float *wd, int64_t n, int64_t k, const uint8_t *x,
-                              const float *xd, int64_t m, const void *residual, void *y, int y_dtype, cudaStream_t s)
+static TileArgs product_args(const float *wd, int64_t n, int64_t k, const float *xd, int64_t m, const void *residual,
+                             void *y, int y_dtype)
 {
     TileArgs p = {};
     p.wd = wd;
@@ -876,12 +927,36 @@ cudaError_t launch_tiles_e4m3(const uint8_t *w, const float *wd, int64_t n, int6
     p.residual = residual;
     p.y = y;
     p.y_bf16 = y_dtype == QG_BF16;
+    return p;
+}
+
+static TileArgs up_args(const float *wd, int64_t ffn, int64_t k, const float *xd, int64_t m, uint8_t *hq, float *hd)
+{
+    TileArgs p = {};
+    p.wd = wd;
+    p.xd = xd;
+    p.m = m;
+    p.n = ffn;
+    p.up_row = ffn;
+    p.up_block = e4m3_blocks(ffn);
+    p.kb = static_cast<int>(e4m3_blocks(k));
+    p.hq = hq;
+    p.hd = hd;
+    return p;
+}
+
+static int product_split(const TileArgs &p) { return split_of<64, false>((p.m + TM - 1) / TM * ((p.n + 63) / 64), p.kb); }
+static int up_split(const TileArgs &p) { return split_of<256, true>((p.m + TM - 1) / TM * e4m3_blocks(p.n), p.kb); }
+
+cudaError_t launch_tiles_e4m3(const uint8_t *w, const float *wd, int64_t n, int64_t k, const uint8_t *x,
+                              const float *xd, int64_t m, const void *residual, void *y, int y_dtype, cudaStream_t s)
+{
+    const TileArgs p = product_args(wd, n, k, xd, m, residual, y, y_dtype);
     const int64_t sms = num_sms(), mt = (m + TM - 1) / TM;
     // Too few tiles for the SMs: 64 columns wide, and a cluster to each.  Where a cluster of
     // two does not find room the walk over wider tiles is as fast or faster (512x2560x9216:
     // 25.8 us against 33.3 with one CTA to each tile of 64).
-    if (const int split = split_of<64, false>(mt * ((n + 63) / 64), p.kb); split > 1)
-        return launch_split<64, false>(w, n, k, x, p, split, s);
+    if (const int split = product_split(p); split > 1) return launch_split<64, false>(w, n, k, x, p, split, s);
     // the tile width whose busiest SM covers the fewest columns
     int best = 256;
     int64_t cost = INT64_MAX;
@@ -897,20 +972,25 @@ cudaError_t launch_tiles_e4m3(const uint8_t *w, const float *wd, int64_t n, int6
 cudaError_t launch_tiles_up_e4m3(const uint8_t *w, const float *wd, int64_t ffn, int64_t k, const uint8_t *x,
                                  const float *xd, int64_t m, uint8_t *hq, float *hd, cudaStream_t s)
 {
-    TileArgs p = {};
-    p.wd = wd;
-    p.xd = xd;
-    p.m = m;
-    p.n = ffn;
-    p.up_row = ffn;
-    p.up_block = e4m3_blocks(ffn);
-    p.kb = static_cast<int>(e4m3_blocks(k));
-    p.hq = hq;
-    p.hd = hd;
-    const int64_t tiles = (m + TM - 1) / TM * e4m3_blocks(ffn);
-    if (const int split = split_of<256, true>(tiles, p.kb); split > 1)
-        return launch_split<256, true>(w, 2 * ffn, k, x, p, split, s);
+    const TileArgs p = up_args(wd, ffn, k, xd, m, hq, hd);
+    if (const int split = up_split(p); split > 1) return launch_split<256, true>(w, 2 * ffn, k, x, p, split, s);
     return launch_tiles<256, Out::UP>(w, 2 * ffn, k, x, p, s);
+}
+
+cudaError_t launch_stalled_e4m3(const uint8_t *w, const float *wd, int64_t n, int64_t k, const uint8_t *x, const float *xd,
+                                int64_t m, void *out, float *out_d, int64_t cta, int64_t block, cudaStream_t s)
+{
+    StalledArgs p = {};
+    if (out_d) {
+        static_cast<TileArgs &>(p) = up_args(wd, n, k, xd, m, static_cast<uint8_t *>(out), out_d);
+        p.cta = cta, p.block = block;
+        if (const int split = up_split(p); split > 1) return launch_split<256, true>(w, 2 * n, k, x, p, split, s);
+        return launch_tiles<256, Out::UP>(w, 2 * n, k, x, p, s);
+    }
+    static_cast<TileArgs &>(p) = product_args(wd, n, k, xd, m, nullptr, out, QG_F32);
+    p.cta = cta, p.block = block;
+    if (const int split = product_split(p); split > 1) return launch_split<64, false>(w, n, k, x, p, split, s);
+    return launch_tiles<128, Out::ANY>(w, n, k, x, p, s);
 }
 
 }  // namespace qg

@@ -186,7 +186,8 @@ __device__ __forceinline__ void s8x4_to_f16x4(uint32_t w, uint32_t &lo, uint32_t
 }
 
 // Bounded wait on phase `parity`; gives up when another role has aborted.
-__device__ __forceinline__ bool tc_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag)
+__device__ __forceinline__ bool tc_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
+                                        const uint64_t limit_ns = kCopyWaitLimitNs)
 {
     constexpr uint32_t kHintNs = 1000000;  // re-check the abort flag and the limit every millisecond
     if (mbar_try_wait_sleep(bar, parity, kHintNs)) return true;
@@ -194,7 +195,7 @@ __device__ __forceinline__ bool tc_wait(uint64_t *bar, uint32_t parity, volatile
     for (;;) {
         if (mbar_try_wait_sleep(bar, parity, kHintNs)) return true;
         if (*abort_flag) return false;
-        if (global_ns() - t0 > kCopyWaitLimitNs) {
+        if (global_ns() - t0 > limit_ns) {
             *abort_flag = 1;
             return false;
         }

@@ -667,7 +667,8 @@ QG_API qg_status rmsnorm_add_quantize_e4m3(const void *x, const void *residual, 
  *   aligned; residual may be y itself (otherwise no overlap).
  *   n_rows < 2^31 - 256.
  * If an operand copy stalls beyond one second the kernel stops waiting and
- * writes NaN for the tiles it has left, rather than hanging.
+ * writes NaN for the tiles it has left, rather than hanging (more than 8 rows; up
+ * to 8 there is no such wait).
  */
 QG_API qg_status qgemm_e4m3(const uint8_t *w, const float *wd, int64_t n_rows, int64_t k, const uint8_t *xq,
                             const float *xd, int64_t m, int epilogue, const void *residual, void *y, int y_dtype,
@@ -705,6 +706,18 @@ QG_API qg_status qg_ffn_e4m3(const void *x, const void *residual, const void *ga
                              int64_t hidden, int64_t ffn, float eps, const uint8_t *wgu, const float *wgu_d,
                              const uint8_t *wdn, const float *wdn_d, uint8_t *xq, float *xd, uint8_t *hq, float *hd,
                              void *y, qg_stream_t stream);
+
+/*
+ * qg_debug_stalled_e4m3 - a product (out_d NULL: out is y, f32[m][n], without a
+ * residual) or gate|up (out, out_d are hq, hd; n is ffn) of more than 8 rows in
+ * which CTA number `cta` copies block number `block` of those that it takes 50 ms
+ * late, and barrier waits give up after 5 ms instead of one second: what a stalled
+ * copy does, without one.  A CTA or block that does not exist stalls nothing.  For
+ * tests.  Arguments otherwise as qgemm_e4m3 and qg_ffn_up_e4m3.
+ */
+QG_API qg_status qg_debug_stalled_e4m3(const uint8_t *w, const float *wd, int64_t n, int64_t k, const uint8_t *xq,
+                                       const float *xd, int64_t m, void *out, float *out_d, int64_t cta, int64_t block,
+                                       qg_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -148,6 +148,18 @@ def test_ffn_refusals(lib):
     assert f(None, None, None, F32, 0, 16, 16, EPS, *([None] * 10)) == OK
 
 
+def test_stalled_refusals(lib):
+    f = lib.qg_debug_stalled_e4m3
+    good = [at(0), at(1), 144, 256, at(2), at(3), 9, at(4), at(5), 0, 0, None]
+    for i, v, want in [(2, 0, SHAPE), (2, 24, SHAPE), (2, 1 << 30, SHAPE), (3, 24, SHAPE), (6, 8, SHAPE),
+                       (6, (1 << 24) + 1, SHAPE), (9, -1, SHAPE), (10, -1, SHAPE), (0, None, NULL), (1, None, NULL),
+                       (4, None, NULL), (5, None, NULL), (7, None, NULL), (0, at(0, 8), ALIGN), (7, at(4, 8), ALIGN),
+                       (8, at(5, 2), ALIGN)]:
+        a = list(good)
+        a[i] = v
+        assert f(*a) == want, (i, v)
+
+
 # ---------------------------------------------------------------- binding refusals
 
 def test_binding_refuses_cpu_tensors(lib):
