@@ -385,14 +385,14 @@ __device__ __forceinline__ uint64_t silu_mul2(uint64_t g2, uint64_t u2)
 {
     const float2 g = unpack2(g2);
     const uint64_t x = pack2(fminf(fmaxf(g.x, -kSiluRange), kSiluRange), fminf(fmaxf(g.y, -kSiluRange), kSiluRange));
-    const uint64_t one = pack2(1.0f, 1.0f);
+    const uint64_t c = pack2(kSiluC, kSiluC);
     const uint64_t hi = mul2(x, pack2(-kLog2e, -kLog2e));
     const uint64_t rest = fma2(x, pack2(kLog2eRest, kLog2eRest), fma2(x, pack2(kLog2e, kLog2e), hi));
     const float2 h = unpack2(hi);
     uint64_t e = pack2(ex2_approx(h.x), ex2_approx(h.y));
     e = fma2(e, mul2(rest, pack2(-kLn2, -kLn2)), e);
-    const float2 d = unpack2(fma2(e, one, one));
-    return mul2(mul2(g2, pack2(rcp_approx(d.x), rcp_approx(d.y))), u2);
+    const float2 d = unpack2(fma2(e, c, c));
+    return mul2(mul2(mul2(g2, c), pack2(rcp_approx(d.x), rcp_approx(d.y))), u2);
 }
 
 __device__ __forceinline__ float load_y(const void *p, int64_t at, int bf16)

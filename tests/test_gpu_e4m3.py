@@ -380,6 +380,26 @@ def test_up_negative_gates(torch, qg, m, scale):
 
 
 @pytest.mark.parametrize("m", [4, 30, 2500])
+def test_up_tail_of_the_silu(torch, qg, m):
+    """Gates from -80 to -88.7, where e^-g nears f32's end, with up values large enough for h
+    to count; from -88.75 on h is zero.  One term a sum: g and u have three roundings each (to f32
+    of the scales' product and of its product with the term), which moves h by 88.7 * 3 * 2^-24
+    (g) and 3 * 2^-24 (u) of itself, and a code's half step is 2^-4; 2^-12 on top of that for h."""
+    g = np.append(np.linspace(-80.0, -88.7, m - 1), -88.75)
+    xd = (g / -448.0).astype(np.float32)[:, None]
+    xq, wq = np.zeros((m, 128), np.uint8), np.zeros((2 * 256, 128), np.uint8)
+    xq[:, 5], wq[:256, 5], wq[256:, 5] = 0x38, 0xFE, 0x7E  # 1, -448, 448
+    wd = np.array([1, 1, 1e30, 1e30], np.float32)[:, None]
+    hq, hd = qg.qg_ffn_up_e4m3(qg.E4M3Weight(codes_dev(torch, wq), dev(torch, wd)), codes_dev(torch, xq), dev(torch, xd))
+    got = E.decode(bits(hq)) * E.spread(hd.cpu().numpy().astype(np.float64), 256)
+    g64, u64 = -448.0 * xd.astype(np.float64), 448.0 * xd.astype(np.float64) * np.float64(np.float32(1e30))
+    h = np.repeat(g64 / (1 + np.exp(-g64)) * u64, 256, axis=1)
+    assert np.all(np.abs(h) > 1e-6)
+    assert np.all(np.abs(got[:-1] - h[:-1]) <= (2.0 ** -4 + 2.0 ** -12) * np.abs(h[:-1]))
+    assert np.all(got[-1] == 0)
+
+
+@pytest.mark.parametrize("m", [4, 30, 2500])
 def test_up_nan_row(torch, qg, m):
     """A NaN activation makes its own row's codes NaN, with the floor's scale, and leaves
     the other rows alone; a NaN weight its own column's."""
