@@ -854,7 +854,8 @@ def rmsnorm_add_quantize_e4m3(x: torch.Tensor, gamma: torch.Tensor, residual: to
     """s = x + residual; codes and scales of RMSNorm(s) * gamma; returns (q, d, s).
 
     x, residual, s and gamma are all f32 or all bf16, [rows, k] (or [k]); s may be
-    x or residual (the sum in place).  Without a residual s is x itself."""
+    x or residual (the sum in place).  Without a residual s is x itself.  The mean of
+    the squares is taken as in f64 for any s; eps is rounded to f32."""
     if stream is not None:
         with _on(stream):
             return rmsnorm_add_quantize_e4m3(x, gamma, residual, eps, s, q, d)

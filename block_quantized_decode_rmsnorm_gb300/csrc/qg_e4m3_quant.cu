@@ -1,5 +1,6 @@
 // Activations to e4m3 codes with one scale per row and block of 128, alone or
 // behind the residual's addition and the RMSNorm.
+#include <cfloat>
 #include <type_traits>
 
 #include "qg_e4m3.cuh"
@@ -127,9 +128,14 @@ __device__ __forceinline__ void add_squares(f32pair2 &acc, float4 v)
     add_square2<T>(acc, v.z, v.w);
 }
 
-// r for the CTA's row: every warp merges the W warps' sums itself (one barrier).
-template <int W>
-__device__ __forceinline__ float row_rms_inv(f32pair2 sums, int k, float inv_k, float eps, f32pair *scratch)
+// r for the CTA's row: every warp merges the W warps' sums itself (one barrier).  The pairs
+// hold for a = mean(s^2) + eps from 2^-100 (below, what a square loses in rounding is itself
+// rounded; the sum's error is under 2^-150 k) up to f32's end.  Any other row, NaN and
+// infinities among its values, is summed again in f64: the whole CTA, as every thread has the
+// same a.  values(f) calls f with each of this thread's values of s.
+template <int W, typename Values>
+__device__ __forceinline__ float row_rms_inv(f32pair2 sums, int k, float inv_k, float eps, f32pair *scratch,
+                                             const Values &values)
 {
     const float2 hi = unpack2(sums.hi), lo = unpack2(sums.lo);
     const f32pair acc = warp_pair_sum(pair_merge({hi.x, lo.x}, {hi.y, lo.y}));
@@ -143,7 +149,20 @@ __device__ __forceinline__ float row_rms_inv(f32pair2 sums, int k, float inv_k, 
         w.lo = __shfl_xor_sync(0xffffffffu, v.lo, o);
         v = pair_merge(v, w);
     }
-    return rms_inv_from_pair(v, k, inv_k, eps);
+    const float a = fmaf(v.hi, inv_k, eps);
+    if (a >= 0x1p-100f && a <= FLT_MAX) return rms_inv_from_pair(v, k, inv_k, eps);
+    double sum = 0.0;
+    values([&](float s) { sum = fma(static_cast<double>(s), static_cast<double>(s), sum); });
+#pragma unroll 1
+    for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    double *total = reinterpret_cast<double *>(scratch);
+    __syncthreads();  // every warp has read the pairs
+    if ((threadIdx.x & 31) == 0) total[threadIdx.x >> 5] = sum;
+    __syncthreads();
+    sum = 0.0;
+#pragma unroll 1
+    for (int w = 0; w < W; ++w) sum += total[w];
+    return static_cast<float>(1.0 / sqrt(sum / k + static_cast<double>(eps)));
 }
 
 // The codes of four values of one block, the whole warp on that block; live: this
@@ -172,7 +191,7 @@ __global__ void __launch_bounds__(32 * W) norm_e4m3_kernel(const NormArgs<T> p)
 {
     using V = Vec4<T>;
     using raw = typename V::raw;
-    __shared__ f32pair scratch[W];
+    __shared__ __align__(8) f32pair scratch[W];
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -190,8 +209,15 @@ __global__ void __launch_bounds__(32 * W) norm_e4m3_kernel(const NormArgs<T> p)
         }
         add_squares<T>(acc, s);
     }
-    const float r = row_rms_inv<W>(acc, p.k, p.inv_k, p.eps, scratch);
     const T *again = p.residual ? p.s : p.x;
+    const float r = row_rms_inv<W>(acc, p.k, p.inv_k, p.eps, scratch, [&](auto f) {
+        for (int b = warp; b < p.kb; b += W) {
+            const int c = b * EB + lane * 4;
+            if (c >= p.k) continue;
+            const float4 s = V::widen(*reinterpret_cast<const raw *>(again + base + c));
+            f(s.x), f(s.y), f(s.z), f(s.w);
+        }
+    });
     for (int b = warp; b < p.kb; b += W) {
         const int c = b * EB + lane * 4;
         const bool live = c < p.k;
@@ -210,7 +236,7 @@ __global__ void __launch_bounds__(32 * W) norm_row_e4m3_kernel(const NormArgs<T>
 {
     using V = Vec4<T>;
     using raw = typename V::raw;
-    __shared__ f32pair scratch[W];
+    __shared__ __align__(8) f32pair scratch[W];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t row = blockIdx.x;
     const int64_t base = row * p.k;
@@ -240,7 +266,13 @@ __global__ void __launch_bounds__(32 * W) norm_row_e4m3_kernel(const NormArgs<T>
             add_squares<T>(acc, V::widen(v[i]));
         }
     }
-    const float r = row_rms_inv<W>(acc, p.k, p.inv_k, p.eps, scratch);
+    const float r = row_rms_inv<W>(acc, p.k, p.inv_k, p.eps, scratch, [&](auto f) {
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {  // zeros where nothing is
+            const float4 s = V::widen(v[i]);
+            f(s.x), f(s.y), f(s.z), f(s.w);
+        }
+    });
     // the maxima of all blocks, then lane i divides for block i
     float4 h[NB];
     float mine = 0.0f;

@@ -645,8 +645,9 @@ QG_API qg_status quantize_act_e4m3(const void *x, int dtype, int64_t rows, int64
  *   s = x + residual        (f32 sum, rounded once to the stream's type)
  *   r = 1 / sqrt(mean_k(s^2) + eps), evaluated in f64 and rounded once to f32
  *   q, d = codes and scales of (s * r) * gamma (two f32 products)
- * as rmsnorm_quantize does for Q8_0 without the addition; the same range holds
- * (s^2 must not overflow f32).
+ * as rmsnorm_quantize does for Q8_0 without the addition, here for every s: squares
+ * beyond f32 at either end, and infinities (r = 0) and NaN (r NaN), as in f64.  eps is
+ * an f32.
  *   x, residual, s: device f32 or bf16 (dtype, a qg_dtype) [rows][k]; gamma [k] of
  *   the same type.  residual NULL: s = x, and the argument s is not used (NULL
  *   allowed); otherwise s is written, and may be x or residual itself.

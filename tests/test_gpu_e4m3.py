@@ -155,6 +155,39 @@ def test_norm_special_values(torch, qg):
     same_codes(q[3:], want_q), same_floats(d[3:], want_d)
 
 
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("place", ["none", "new"])
+@pytest.mark.parametrize("eps", [EPS, 0.0, float("inf")])
+@pytest.mark.parametrize("rows,k", [(11, 144), (11, 4112), (11, 8192), (11, 16400), (310, 1024), (310, 4096)])
+def test_norm_whole_range(torch, qg, kind, place, eps, rows, k):
+    """Rows whose squares leave f32 at either end, with infinities and NaN among them: the
+    mean is the formula's all the same, and rows beside them are what they are alone."""
+    t = types(torch)[kind]
+    gen = torch.Generator().manual_seed(rows + k)
+    x = torch.randn((rows, k), generator=gen)
+    x[0] *= 1e20
+    x[1] = torch.where(x[1] > 0, 3.3e38, 1.5e38)
+    x[2, k // 2] = float("inf")
+    x[3, 5], x[3, k - 1] = float("-inf"), float("inf")
+    x[4] *= 1e-25
+    x[5] *= 1e-41
+    x[6, 3] = float("nan")
+    x[7], x[7, 9] = 0, 2e19
+    x[8] = 0
+    x[9] *= 2.0 ** -50
+    x = x.to(t)
+    res = (torch.randn((rows, k), generator=gen) * x.float().abs().clamp(max=1e37) * 0.25).nan_to_num(0.0).to(t)
+    res[1:4] = 0
+    gamma = (1 + 0.1 * torch.randn(k, generator=gen)).to(t)
+    s = x if place == "none" else (x.float() + res.float()).to(t)
+    q, d, got = qg.rmsnorm_add_quantize_e4m3(x.cuda(), gamma.cuda(), None if place == "none" else res.cuda(), eps)
+    same_floats(got.float().cpu().numpy(), s.float().numpy())
+    with np.errstate(all="ignore"):
+        want_q, want_d = E.quantize(E.norm(s.float().numpy(), gamma.float().numpy(), eps))
+    same_floats(d.cpu().numpy(), want_d)
+    same_codes(bits(q), want_q)
+
+
 # ---------------------------------------------------------------- product
 
 def tol(k):
