@@ -821,7 +821,7 @@ def _load_front():
     try:
         from . import _qg_torch
     except ImportError as e:
-        raise RuntimeError("_qg_torch.so is missing or was built for another torch: build it first (python -m "
+        raise RuntimeError("the torch front end (_qg_torch) is missing or was built for another torch: build it first (python -m "
                            "block_quantized_decode_rmsnorm_gb300.builder, or __graft_entry__.build())") from e
     _qg_torch.set_error(_lib.QGError)
     _front = _qg_torch
