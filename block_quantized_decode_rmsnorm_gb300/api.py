@@ -18,6 +18,7 @@ Tensor formats
 
 from __future__ import annotations
 
+import ctypes
 from dataclasses import dataclass
 
 import torch
@@ -817,13 +818,14 @@ _front = None  # the native front end: checks, outputs and the C call (csrc/qg_t
 
 def _load_front():
     global _front
-    _lib.load()
+    lib = _lib.load()  # the one that every other call goes to
     try:
         from . import _qg_torch
     except ImportError as e:
         raise RuntimeError("the torch front end (_qg_torch) is missing or was built for another torch: build it first (python -m "
                            "block_quantized_decode_rmsnorm_gb300.builder, or __graft_entry__.build())") from e
-    _qg_torch.set_error(_lib.QGError)
+    _qg_torch.bind(_lib.QGError, *(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
+        "quantize_act_e4m3", "rmsnorm_add_quantize_e4m3", "qgemm_e4m3", "qg_ffn_up_e4m3", "qg_ffn_e4m3", "qg_status_str")))
     _front = _qg_torch
     return _front
 

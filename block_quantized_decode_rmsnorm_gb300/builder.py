@@ -67,8 +67,8 @@ def _compile_front(torch_dir: str, nvcc: str) -> None:
     tmp = FRONT + f".tmp{os.getpid()}"
     try:
         r = subprocess.run([_cxx(), "-std=c++17", "-O2", "-fPIC", "-fvisibility=hidden", *[f"-I{d}" for d in inc], "-shared",
-                            "-o", tmp, FRONT_SRC, f"-L{HERE}", "-lqgemv", f"-L{lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu",
-                            "-ltorch_cuda", "-ltorch_python", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"],
+                            "-o", tmp, FRONT_SRC, f"-L{lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python",
+                            f"-Wl,-rpath,{lib}"],
                            capture_output=True, text=True)
     except OSError as e:
         raise RuntimeError(f"{_cxx()}: {e}") from e
@@ -151,11 +151,13 @@ def build(force: bool = False, verbose: bool = False, strict: bool = False) -> s
     what needs no more than it are there (the 8-bit floating point calls for torch tensors
     then raise); with ``strict`` it is an error."""
     os.makedirs(BUILD, exist_ok=True)
-    _build_library(force, verbose)
     torch_dir = _torch_dir()
-    if torch_dir:
+    with ThreadPoolExecutor(max_workers=1) as ex:  # it is linked to torch alone: at the same time
+        front = ex.submit(_build_front, torch_dir, force) if torch_dir else None
+        _build_library(force, verbose)
+    if front:
         try:
-            _build_front(torch_dir, force)
+            front.result()
         except RuntimeError as e:
             if strict:
                 raise

@@ -24,6 +24,17 @@ using c10::ScalarType;
 
 PyObject *qg_error = nullptr;  // _lib.QGError
 
+// The entry points of the library that _lib has loaded (bind); this module is linked to none.
+struct Library {
+    decltype(&::quantize_act_e4m3) quantize_act_e4m3;
+    decltype(&::rmsnorm_add_quantize_e4m3) rmsnorm_add_quantize_e4m3;
+    decltype(&::qgemm_e4m3) qgemm_e4m3;
+    decltype(&::qg_ffn_up_e4m3) qg_ffn_up_e4m3;
+    decltype(&::qg_ffn_e4m3) qg_ffn_e4m3;
+    decltype(&::qg_status_str) qg_status_str;
+};
+Library lib = {};
+
 struct Refused {};  // a Python exception is set
 
 [[noreturn]] void refuse(PyObject *kind, const std::string &what)
@@ -113,7 +124,7 @@ qg_stream_t stream_on(int dev) { return c10::cuda::getCurrentCUDAStream(static_c
 void done(const char *fn, qg_status st)
 {
     if (st == QG_OK) return;
-    if (PyObject *e = PyObject_CallFunction(qg_error, "sis", fn, static_cast<int>(st), qg_status_str(st))) {
+    if (PyObject *e = PyObject_CallFunction(qg_error, "sis", fn, static_cast<int>(st), lib.qg_status_str(st))) {
         PyErr_SetObject(qg_error, e);
         Py_DECREF(e);
     }
@@ -135,6 +146,10 @@ PyObject *give(PyObject *a, PyObject *b, PyObject *c = nullptr)
 template <typename F>
 PyObject *guarded(Py_ssize_t got, Py_ssize_t want, F &&f)
 {
+    if (!qg_error) {
+        PyErr_SetString(PyExc_RuntimeError, "no library is bound");
+        return nullptr;
+    }
     if (got != want) {
         PyErr_Format(PyExc_TypeError, "expected %zd arguments, got %zd", want, got);
         return nullptr;
@@ -159,8 +174,8 @@ PyObject *quantize_act(PyObject *, PyObject *const *a, Py_ssize_t n)
         need(x, "x", x.scalar_type(), x.sizes(), dev);
         const Tensor q = output(a[1], "q", E4M3, {r.rows, r.k}, dev);
         const Tensor d = output(a[2], "d", ScalarType::Float, {r.rows, blocks(r.k)}, dev);
-        done("quantize_act_e4m3", quantize_act_e4m3(x.data_ptr(), kind, r.rows, r.k, at_<uint8_t>(q), at_<float>(d),
-                                                    stream_on(dev)));
+        done("quantize_act_e4m3", lib.quantize_act_e4m3(x.data_ptr(), kind, r.rows, r.k, at_<uint8_t>(q), at_<float>(d),
+                                                        stream_on(dev)));
         return give(give(q), give(d));
     });
 }
@@ -188,9 +203,9 @@ PyObject *rmsnorm_add_quantize(PyObject *, PyObject *const *a, Py_ssize_t n)
         const Tensor q = output(a[5], "q", E4M3, {r.rows, r.k}, dev);
         const Tensor d = output(a[6], "d", ScalarType::Float, {r.rows, blocks(r.k)}, dev);
         done("rmsnorm_add_quantize_e4m3",
-             rmsnorm_add_quantize_e4m3(x.data_ptr(), residual ? residual->data_ptr() : nullptr, gamma.data_ptr(), kind,
-                                       r.rows, r.k, static_cast<float>(eps), s.data_ptr(), at_<uint8_t>(q),
-                                       at_<float>(d), stream_on(dev)));
+             lib.rmsnorm_add_quantize_e4m3(x.data_ptr(), residual ? residual->data_ptr() : nullptr, gamma.data_ptr(),
+                                           kind, r.rows, r.k, static_cast<float>(eps), s.data_ptr(), at_<uint8_t>(q),
+                                           at_<float>(d), stream_on(dev)));
         return give(give(q), give(d), give(s));
     });
 }
@@ -239,9 +254,10 @@ PyObject *qgemm(PyObject *, PyObject *const *a, Py_ssize_t n)
         const int kind = stream_type(type, "y");
         const Tensor y = output(a[6], "y", type, {o.m, o.n_rows}, dev);
         if (residual) need(*residual, "residual", type, {o.m, o.n_rows}, dev);
-        done("qgemm_e4m3", qgemm_e4m3(at_<uint8_t>(codes), at_<float>(scales), o.n_rows, o.k, at_<uint8_t>(xq),
-                                      at_<float>(xd), o.m, static_cast<int>(epi),
-                                      residual ? residual->data_ptr() : nullptr, y.data_ptr(), kind, stream_on(dev)));
+        done("qgemm_e4m3", lib.qgemm_e4m3(at_<uint8_t>(codes), at_<float>(scales), o.n_rows, o.k, at_<uint8_t>(xq),
+                                          at_<float>(xd), o.m, static_cast<int>(epi),
+                                          residual ? residual->data_ptr() : nullptr, y.data_ptr(), kind,
+                                          stream_on(dev)));
         return give(y);
     });
 }
@@ -257,8 +273,9 @@ PyObject *ffn_up(PyObject *, PyObject *const *a, Py_ssize_t n)
         const int64_t ffn = o.n_rows / 2;
         const Tensor hq = output(a[4], "hq", E4M3, {o.m, ffn}, dev);
         const Tensor hd = output(a[5], "hd", ScalarType::Float, {o.m, blocks(ffn)}, dev);
-        done("qg_ffn_up_e4m3", qg_ffn_up_e4m3(at_<uint8_t>(codes), at_<float>(scales), ffn, o.k, at_<uint8_t>(xq),
-                                              at_<float>(xd), o.m, at_<uint8_t>(hq), at_<float>(hd), stream_on(dev)));
+        done("qg_ffn_up_e4m3",
+             lib.qg_ffn_up_e4m3(at_<uint8_t>(codes), at_<float>(scales), ffn, o.k, at_<uint8_t>(xq), at_<float>(xd), o.m,
+                                at_<uint8_t>(hq), at_<float>(hd), stream_on(dev)));
         return give(give(hq), give(hd));
     });
 }
@@ -293,24 +310,44 @@ PyObject *ffn(PyObject *, PyObject *const *a, Py_ssize_t n)
         const Tensor hd = output(a[11], "buf.hd", ScalarType::Float, {r.rows, fb}, dev);
         const Tensor y = output(a[12], "y", type, x.sizes(), dev);
         done("qg_ffn_e4m3",
-             qg_ffn_e4m3(x.data_ptr(), residual ? residual->data_ptr() : nullptr, gamma.data_ptr(), kind, r.rows, r.k, f,
-                         static_cast<float>(eps), at_<uint8_t>(gu), at_<float>(gud), at_<uint8_t>(dn), at_<float>(dnd),
-                         at_<uint8_t>(xq), at_<float>(xd), at_<uint8_t>(hq), at_<float>(hd), y.data_ptr(),
-                         stream_on(dev)));
+             lib.qg_ffn_e4m3(x.data_ptr(), residual ? residual->data_ptr() : nullptr, gamma.data_ptr(), kind, r.rows,
+                             r.k, f, static_cast<float>(eps), at_<uint8_t>(gu), at_<float>(gud), at_<uint8_t>(dn),
+                             at_<float>(dnd), at_<uint8_t>(xq), at_<float>(xd), at_<uint8_t>(hq), at_<float>(hd),
+                             y.data_ptr(), stream_on(dev)));
         return give(y);
     });
 }
 
-PyObject *set_error(PyObject *, PyObject *cls)
+// The entry point whose address is a[i].
+template <typename F>
+bool entry(PyObject *const *a, int i, F &f)
 {
-    Py_XINCREF(cls);
+    void *p = PyLong_AsVoidPtr(a[i]);
+    if (!p && !PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "an entry point is missing");
+    f = reinterpret_cast<F>(p);
+    return p != nullptr;
+}
+
+// (the error class, then the entry points' addresses in Library's order)
+PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    if (n != 7) {
+        PyErr_Format(PyExc_TypeError, "expected 7 arguments, got %zd", n);
+        return nullptr;
+    }
+    Library l;
+    if (!entry(a, 1, l.quantize_act_e4m3) || !entry(a, 2, l.rmsnorm_add_quantize_e4m3) || !entry(a, 3, l.qgemm_e4m3) ||
+        !entry(a, 4, l.qg_ffn_up_e4m3) || !entry(a, 5, l.qg_ffn_e4m3) || !entry(a, 6, l.qg_status_str))
+        return nullptr;
+    lib = l;
+    Py_INCREF(a[0]);
     Py_XDECREF(qg_error);
-    qg_error = cls;
+    qg_error = a[0];
     Py_RETURN_NONE;
 }
 
 #define FAST(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(f)), METH_FASTCALL, nullptr
-PyMethodDef methods[] = {{"set_error", set_error, METH_O, nullptr},
+PyMethodDef methods[] = {{"bind", FAST(bind)},
                          {"quantize_act", FAST(quantize_act)},
                          {"rmsnorm_add_quantize", FAST(rmsnorm_add_quantize)},
                          {"qgemm", FAST(qgemm)},

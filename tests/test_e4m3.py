@@ -176,3 +176,62 @@ def test_binding_refuses_cpu_tensors(lib):
             call()
     with pytest.raises(TypeError):
         qg.quantize_act_e4m3(np.zeros((2, 128), np.float32))
+
+
+def need_front():
+    from block_quantized_decode_rmsnorm_gb300 import builder
+
+    if builder._torch_dir() is None:
+        pytest.skip("torch with CUDA is not installed")
+
+
+def test_binding_calls_the_library_that_was_loaded(lib, tmp_path):
+    """_lib.load(path) decides for the e4m3 calls on torch tensors too."""
+    import shutil
+    import subprocess
+    import sys
+
+    need_front()
+    from block_quantized_decode_rmsnorm_gb300 import _lib
+
+    other = str(tmp_path / "other.so")
+    shutil.copy(_lib.LIB_PATH, other)
+    code = f"""
+import torch
+from block_quantized_decode_rmsnorm_gb300 import _lib, api
+_lib.load({other!r})
+front = api._load_front()
+maps = open('/proc/self/maps').read()
+assert {other!r} in maps and {_lib.LIB_PATH!r} not in maps
+try:
+    front.bind(_lib.QGError, 0, 0, 0, 0, 0, 0)
+except ValueError:
+    pass
+else:
+    raise AssertionError('a missing entry point was taken')
+try:
+    api.quantize_act_e4m3(torch.zeros(2, 128))
+except ValueError as e:
+    assert 'CUDA' in str(e)
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_binding_refuses_before_a_library_is_bound():
+    import subprocess
+    import sys
+
+    need_front()
+    code = """
+import torch
+from block_quantized_decode_rmsnorm_gb300 import _qg_torch
+try:
+    _qg_torch.quantize_act(torch.zeros(2, 128), None, None)
+except RuntimeError as e:
+    assert 'bound' in str(e)
+else:
+    raise AssertionError
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
