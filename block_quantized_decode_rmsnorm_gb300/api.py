@@ -795,7 +795,11 @@ class E4M3Weight:
     """e4m3 weight: codes float8_e4m3fn [n_rows, k] and f32 scales, one per
     128 x 128 block [ceil(n_rows/128), ceil(k/128)].  A stacked gate|up weight
     holds the two matrices' codes and the two matrices' scales one after the
-    other: codes [2 ffn, k], scales [2 ceil(ffn/128), ceil(k/128)]."""
+    other: codes [2 ffn, k], scales [2 ceil(ffn/128), ceil(k/128)].
+
+    The calls below may read codes before the previous kernel of the stream has ended:
+    codes that a call of this package writes (quantize_act_e4m3 and so on) are a weight
+    only once the host, or an event of another stream, has waited for that call."""
 
     codes: torch.Tensor
     scales: torch.Tensor
@@ -869,7 +873,8 @@ def qgemm_e4m3(w: E4M3Weight, xq: torch.Tensor, xd: torch.Tensor, epilogue: str 
                out_dtype: torch.dtype | None = None, stream=None) -> torch.Tensor:
     """Block-scaled e4m3 product of m >= 0 activation rows; y [m, n_rows], f32 or
     bf16 (out_dtype, by default y's or the residual's type, else f32).  The
-    residual has y's type and may be y itself."""
+    residual has y's type and may be y itself.  w.codes: not from a call of this
+    package that may still be running (E4M3Weight)."""
     if stream is not None:
         with _on(stream):
             return qgemm_e4m3(w, xq, xd, epilogue, residual, y, out_dtype)
@@ -885,7 +890,8 @@ def qgemm_e4m3(w: E4M3Weight, xq: torch.Tensor, xd: torch.Tensor, epilogue: str 
 def qg_ffn_up_e4m3(w: E4M3Weight, xq: torch.Tensor, xd: torch.Tensor, hq: torch.Tensor | None = None,
                    hd: torch.Tensor | None = None, stream=None):
     """Stacked gate|up product, SiLU(g) * u and its quantization in one launch:
-    (hq float8_e4m3fn [m, ffn], hd f32 [m, ceil(ffn/128)])."""
+    (hq float8_e4m3fn [m, ffn], hd f32 [m, ceil(ffn/128)]).  w.codes: not from a call of
+    this package that may still be running (E4M3Weight)."""
     if stream is not None:
         with _on(stream):
             return qg_ffn_up_e4m3(w, xq, xd, hq, hd)
@@ -927,7 +933,8 @@ def qg_ffn_e4m3(x: torch.Tensor, layer: E4M3Layer, residual: torch.Tensor | None
                 buf: E4M3Buffers | None = None, y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """s = x + residual; y = s + down(SiLU(g) * u), (g|u) = gate|up(RMSNorm(s) * gamma),
     over m rows in three launches.  x, residual and y are [m, hidden], all f32 or all
-    bf16; y may be x or residual (in place)."""
+    bf16; y may be x or residual (in place).  The layer's codes: not from a call of this
+    package that may still be running (E4M3Weight)."""
     if stream is not None:
         with _on(stream):
             return qg_ffn_e4m3(x, layer, residual, eps, buf, y)

@@ -624,6 +624,12 @@ QG_API qg_status qgemm_bf16_prefill(const uint16_t *w, int64_t n_rows, int64_t k
  * Outputs must not overlap inputs or one another (QG_ERR_SHAPE) except where
  * stated.  Every sum is taken in an order that the shape alone fixes: results
  * repeat bit for bit (a row's may differ between calls with other rows beside it).
+ * Weights' codes are, at some sizes, read before the previous kernel of the stream has
+ * ended (the convention at the top).  They must not be outputs of a kernel that may still
+ * run then and lets its successor start early: of quantize_act_e4m3,
+ * rmsnorm_add_quantize_e4m3 and qg_ffn_up_e4m3 above all, whose one row of codes and
+ * scales is a weight of one row.  Let the host or an event of another stream wait for
+ * such a kernel first.  Scales, activations and residuals may come from the kernel before.
  */
 typedef enum {
     QG_F32 = 0,

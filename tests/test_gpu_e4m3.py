@@ -641,6 +641,31 @@ def test_weights_replaced_in_stream_order(torch, qg, m):
     assert all(torch.equal(y, want[i % 2]) for i, y in enumerate(got))
 
 
+@pytest.mark.parametrize("m", [1, 40, 300])
+@pytest.mark.parametrize("wait", ["host", "event"])
+def test_codes_of_a_quantizer_as_a_weight(torch, qg, m, wait):
+    """One row's codes and scales are a weight of one row, once the call that writes them has
+    been waited for (which the documentation asks for)."""
+    gen = torch.Generator().manual_seed(m)
+    row, x = torch.randn((1, 4112), generator=gen), torch.randn((m, 4112), generator=gen)
+    xq, xd = qg.quantize_act_e4m3(x.cuda())
+    rows = [row.cuda() * (i + 1) for i in range(4)]
+    q, d = qg.quantize_act_e4m3(rows[0])
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for r in rows:
+        qg.quantize_act_e4m3(r, q, d)
+        if wait == "host":
+            torch.cuda.synchronize()
+            y = qg.qgemm_e4m3(qg.E4M3Weight(q, d), xq, xd)
+        else:
+            side.wait_stream(torch.cuda.current_stream())
+            y = qg.qgemm_e4m3(qg.E4M3Weight(q, d), xq, xd, stream=side)
+            torch.cuda.current_stream().wait_stream(side)
+        want, a = E.product(*E.quantize(r.cpu().numpy()), bits(xq), xd.cpu().numpy())
+        assert np.all(np.abs(y.cpu().numpy() - want) <= tol(4112) * a + 2.0 ** -23 * np.abs(want))
+
+
 def test_rows_past_the_last(torch, qg):
     """The first rows of a larger batch: what lies behind them is neither read into the
     results nor written."""
