@@ -61,9 +61,16 @@ __device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// NARROW (gate|up): half the warps, so that twice the CTAs find room.
-template <bool UP, bool NARROW>
+// What a CTA does: ONE tile of the product; a WALK over several, the next one's weights on
+// their way while a tile ends (in the others nothing is kept of a next tile); one tile of
+// gate and one of up, with eight warps or, NARROW, with half of them, so that twice the CTAs
+// find room.
+enum class Form { ONE, WALK, UP, UP_NARROW };
+
+template <Form FORM>
 struct RowsLayout {
+    static constexpr bool UP = FORM == Form::UP || FORM == Form::UP_NARROW;
+    static constexpr bool WALK = FORM == Form::WALK, NARROW = FORM == Form::UP_NARROW;
     static constexpr int W = NARROW ? 4 : 8;  // warps per CTA
     static constexpr int T = UP ? 2 : 1;      // weight tiles per CTA
     static constexpr int D = NARROW ? 2 : UP ? 3 : 6;  // blocks on their way per warp
@@ -72,21 +79,19 @@ struct RowsLayout {
     static constexpr int CTAS = NARROW ? 4 : 2;      // per SM
 };
 
-// MANY: a CTA walks over several tiles, the next one's weights on their way while a tile
-// ends; without it the tile is the CTA's only one and nothing is kept of the next.
-template <bool UP, bool NARROW, bool MANY>
-__global__ void __launch_bounds__(RowsLayout<UP, NARROW>::W * 32, RowsLayout<UP, NARROW>::CTAS)
-    rows_e4m3_kernel(const RowsArgs p)
+template <Form FORM>
+__global__ void __launch_bounds__(RowsLayout<FORM>::W * 32, RowsLayout<FORM>::CTAS) rows_e4m3_kernel(const RowsArgs p)
 {
-    using L = RowsLayout<UP, NARROW>;
+    using L = RowsLayout<FORM>;
+    constexpr bool UP = L::UP, WALK = L::WALK;
     constexpr int RW = L::W, RT = L::T, D = L::D, F = L::F;
     extern __shared__ __align__(16) uint8_t ring_raw[];  // [warp][slot][tile][row half][block half][lane] of 16 bytes
-    __shared__ float red[MANY ? 2 : 1][RW][RT][8 * RR];  // [tile parity][warp]: one barrier a tile
+    __shared__ float red[WALK ? 2 : 1][RW][RT][8 * RR];  // [tile parity][warp]: one barrier a tile
     __shared__ float top[8];  // gate|up: the rows' largest magnitudes
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, c = lane & 3;
     const int steps = (p.kb + RW - 1) / RW;  // of a tile: warp w takes blocks w, w + RW, ...
-    const int slots = MANY ? D : min(D, steps);
+    const int slots = WALK ? D : min(D, steps);
     uint8_t *ring = ring_raw + static_cast<size_t>(warp) * slots * RT * R_TILE + lane * 16;
 
     // The next step's weights into its slot, tile after tile: zeros where there are
@@ -106,7 +111,7 @@ __global__ void __launch_bounds__(RowsLayout<UP, NARROW>::W * 32, RowsLayout<UP,
     rows();
     auto stage = [&]() {
         const int b = warp + RW * s_step;
-        if ((!MANY || s_tile < p.tiles) && b < p.kb) {
+        if ((!WALK || s_tile < p.tiles) && b < p.kb) {
             uint8_t *slot = ring + s_slot * RT * R_TILE;
 #pragma unroll
             for (int t = 0; t < RT; ++t)
@@ -124,7 +129,7 @@ __global__ void __launch_bounds__(RowsLayout<UP, NARROW>::W * 32, RowsLayout<UP,
         }
         cp_async_commit();
         ++s_step;
-        if (MANY && s_step == steps) {
+        if (WALK && s_step == steps) {
             s_step = 0;
             s_tile += gridDim.x;
             rows();
@@ -134,7 +139,7 @@ __global__ void __launch_bounds__(RowsLayout<UP, NARROW>::W * 32, RowsLayout<UP,
 #pragma unroll
     for (int i = 0; i < D; ++i) stage();
     // what comes behind the ring's blocks into L2 meanwhile, a piece per row
-    if (!NARROW && !MANY && p.ahead > 0 && threadIdx.x < RT * RR) {
+    if (!L::NARROW && !WALK && p.ahead > 0 && threadIdx.x < RT * RR) {
         const int64_t row = static_cast<int64_t>(blockIdx.x) * RR + threadIdx.x % RR;
         if (row < p.n)
             asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
@@ -157,7 +162,7 @@ __global__ void __launch_bounds__(RowsLayout<UP, NARROW>::W * 32, RowsLayout<UP,
     int f_step = 0;
     auto fetch = [&](int u) {
         const int b = warp + RW * f_step;
-        const bool in = (!MANY || f_tile < p.tiles) && b < p.kb;
+        const bool in = (!WALK || f_tile < p.tiles) && b < p.kb;
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
             const int col = b * EB + 64 * q + 16 * c;
@@ -168,7 +173,7 @@ __global__ void __launch_bounds__(RowsLayout<UP, NARROW>::W * 32, RowsLayout<UP,
         for (int t = 0; t < RT; ++t)
             fw[u][t] = in ? p.wd[((t ? p.up_block : 0) + f_tile * RR / EB) * p.kb + b] : 0.0f;
         ++f_step;
-        if (MANY && f_step == steps) f_step = 0, f_tile += gridDim.x;
+        if (WALK && f_step == steps) f_step = 0, f_tile += gridDim.x;
     };
 #pragma unroll
     for (int u = 0; u < F; ++u) fetch(u);
@@ -257,7 +262,7 @@ __global__ void __launch_bounds__(RowsLayout<UP, NARROW>::W * 32, RowsLayout<UP,
                 }
             }
             if (++step == steps) {
-                if (!MANY) {
+                if (!WALK) {
                     more = false;
                     break;
                 }
@@ -280,31 +285,28 @@ __global__ void __launch_bounds__(RowsLayout<UP, NARROW>::W * 32, RowsLayout<UP,
             fetch(u);
         }
     }
-    if (!MANY) finish();
+    if (!WALK) finish();
 }
 
 // At most three CTAs of eight warps on two SMs (of the four that find room).
-template <bool UP>
-static bool few(int64_t tiles)
-{
-    return 4 * tiles <= 3 * RowsLayout<UP, false>::CTAS * static_cast<int64_t>(num_sms());
-}
+static bool few(int64_t tiles) { return 4 * tiles <= 3 * RowsLayout<Form::ONE>::CTAS * static_cast<int64_t>(num_sms()); }
+static_assert(RowsLayout<Form::ONE>::CTAS == RowsLayout<Form::UP>::CTAS, "few");
 
-template <bool UP, bool NARROW, bool MANY>
+template <Form FORM>
 static cudaError_t launch_rows(int64_t ctas, RowsArgs p, cudaStream_t s)
 {
-    using L = RowsLayout<UP, NARROW>;
+    using L = RowsLayout<FORM>;
     const int need = (p.kb + L::W - 1) / L::W;
     constexpr int ring = L::D * L::W * EB;  // columns in flight
     // Where the next kernel's CTAs find room beside these, a second ring's columns go to L2
     // before the wait (7x2560x9216 bf16: 7.9 -> 7.2 us, 1x2560x12288: 9.2 -> 8.6); with two
     // CTAs an SM it is no gain (1x4096x14336: 11.4 us, 12.4 with all columns).
-    if (few<UP>(p.tiles)) p.ahead = std::max(0, std::min(p.k - ring, ring));
-    const int bytes = L::W * (MANY || need > L::D ? L::D : need) * L::T * R_TILE;
-    const auto kernel = rows_e4m3_kernel<UP, NARROW, MANY>;
+    if (few(p.tiles)) p.ahead = std::max(0, std::min(p.k - ring, ring));
+    const int bytes = L::W * (L::WALK || need > L::D ? L::D : need) * L::T * R_TILE;
+    const auto kernel = rows_e4m3_kernel<FORM>;
     if (cudaError_t e = opt_in_smem(reinterpret_cast<const void *>(kernel), L::RING); e != cudaSuccess) return e;
     return launch_pdl_cluster(kernel, dim3(static_cast<unsigned>(ctas)), dim3(L::W * 32), static_cast<size_t>(bytes), s,
-                              UP ? UP_CLUSTER : 1, p);
+                              L::UP ? UP_CLUSTER : 1, p);
 }
 
 cudaError_t launch_rows_e4m3(const uint8_t *w, const float *wd, int64_t n, int64_t k, const uint8_t *x, const float *xd,
@@ -325,10 +327,10 @@ cudaError_t launch_rows_e4m3(const uint8_t *w, const float *wd, int64_t n, int64
     p.tiles = (n + RR - 1) / RR;
     // More tiles than CTAs find room: as many each (65536x1024: 18.1 us against 28.5 with
     // a CTA to each; 1024x3584, one each: 2.3 us, and 2.8 by the kernel that walks).
-    const int64_t room = RowsLayout<false, false>::CTAS * static_cast<int64_t>(num_sms());
-    if (p.tiles <= room) return launch_rows<false, false, false>(p.tiles, p, s);
+    const int64_t room = RowsLayout<Form::ONE>::CTAS * static_cast<int64_t>(num_sms());
+    if (p.tiles <= room) return launch_rows<Form::ONE>(p.tiles, p, s);
     const int64_t each = (p.tiles + room - 1) / room;
-    return launch_rows<false, false, true>((p.tiles + each - 1) / each, p, s);
+    return launch_rows<Form::WALK>((p.tiles + each - 1) / each, p, s);
 }
 
 cudaError_t launch_rows_up_e4m3(const uint8_t *w, const float *wd, int64_t ffn, int64_t k, const uint8_t *x,
@@ -350,8 +352,8 @@ cudaError_t launch_rows_up_e4m3(const uint8_t *w, const float *wd, int64_t ffn, 
     p.tiles = e4m3_blocks(ffn) * UP_CLUSTER;
     // Eight warps a CTA up to there: 1x512x2560 3.2 us and 4.1 with four, 8x3584x2560 6.5 and
     // 6.9, 8x3584x1024 4.0 and 3.9; 8x4608x2560 8.8 and 7.7.
-    if (few<true>(p.tiles)) return launch_rows<true, false, false>(p.tiles, p, s);
-    return launch_rows<true, true, false>(p.tiles, p, s);
+    if (few(p.tiles)) return launch_rows<Form::UP>(p.tiles, p, s);
+    return launch_rows<Form::UP_NARROW>(p.tiles, p, s);
 }
 
 }  // namespace qg
