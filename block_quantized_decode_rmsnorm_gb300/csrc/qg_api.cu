@@ -146,7 +146,12 @@ qg_status check_q8_k(int64_t k)
 
 // 8-bit floating point path
 constexpr int64_t kE4M3MaxM = int64_t(1) << 24;
-constexpr int64_t kE4M3FewRows = 8;  // activation rows that the few-row kernel takes
+// Activation rows that the few-row kernel takes: the N side of its MMA.  There it is ahead of
+// the tiles on the same rows nearly everywhere (us, tiles second; qg_e4m3_rows.cu says how
+// measured): product 8x2560x9216 7.3, 9.1; 8x1024x3584 2.9, 5.4; 8x18432x2560 11.5, 12.2;
+// gate|up 8x3584x1024 4.3, 5.4; 8x4608x2560 7.8, 9.3; 1x9216x2560 10.4, 11.0; but
+// 1x65536x1024 15.5, 14.1.
+constexpr int64_t kE4M3FewRows = 8;
 
 int64_t e4m3_kb(int64_t k) { return (k + 127) / 128; }
 bool dtype_ok(int t) { return t == QG_F32 || t == QG_BF16; }

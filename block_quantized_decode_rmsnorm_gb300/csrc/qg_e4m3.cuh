@@ -26,7 +26,7 @@ constexpr int EB = 128;  // values per scale
 
 __host__ __device__ constexpr int64_t e4m3_blocks(int64_t k) { return (k + EB - 1) / EB; }
 
-// Largest magnitude of a block, from the warp's (or half-warp's) values.
+// A block's largest magnitude, not below the floor.
 __device__ __forceinline__ float e4m3_floor(float a) { return fmaxf(a, 0x1p-100f); }
 
 // max over the warp of non-negative floats, none of them NaN: their bit patterns
@@ -91,9 +91,8 @@ struct Vec4<__nv_bfloat16> {
 // constant's own second part), so that the error of e^-x does not grow with |x|: the
 // approximations of 2^y and 1/y are what is left of it.  They are a choice: at most 2^-21.5
 // of the value over g in [-87, 100] (2^-23.7 in the mean square), and with expf and an IEEE
-// division 2^-22.1 (2^-24.3), far below a code's half step of 2^-4 either way, but 17 % of
-// the time of a long prompt's gate|up (2048x9216x2560: 82 us against 96; 512x3584x1024: 8.0
-// against 9.3).
+// division 2^-22.1 (2^-24.3), far below a code's half step of 2^-4 either way, but those
+// take 17 % longer (15 us at 2048x9216x2560's 84, 1.3 at 512x3584x1024's 8.8).
 // Both sides of the quotient carry the factor c, a little over a quarter: 1/y of a y
 // beyond 2^126 is flushed to zero, and c (1 + e^-g) gets there only where e^-g is within
 // 2^-10 of f32's end, 2^128.  x is g held at -88.7224, inside that last bit: whatever g's

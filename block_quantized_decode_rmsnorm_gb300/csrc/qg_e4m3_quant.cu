@@ -1,5 +1,7 @@
 // Activations to e4m3 codes with one scale per row and block of 128, alone or
 // behind the residual's addition and the RMSNorm.
+//
+// Times in this file are of graph replays over operands that rotate through 400 MB.
 #include <cfloat>
 #include <type_traits>
 
@@ -14,7 +16,7 @@ namespace qg {
 // store of codes; it takes QB consecutive blocks (rows run on into one another)
 // with all loads in flight before the first maximum, and lane i divides for
 // block i, so the two IEEE divisions are paid once per QB blocks.  Bound by HBM
-// where rows are many (8192x9216 bf16 below), by issue before that: EVEN is the
+// where rows are many (8192x9216 bf16: 33.2 us for 229 MB, 6.9 TB/s), by issue before that: EVEN is the
 // form for k a multiple of 128, where the blocks follow one another in memory and
 // every lane of a whole group is live, and no position is computed per block.
 constexpr int QB = 8;
@@ -79,9 +81,9 @@ __global__ void __launch_bounds__(QT) quantize_e4m3_kernel(const T *x, int64_t n
 // s = x + residual (rounded once to the stream's type), r = 1/sqrt(mean(s^2) + eps)
 // as in f64 rounded once to f32, v = (s * r) * gamma (two f32 products), then the
 // codes of v.  One CTA per row; block b of the row belongs to warp b mod W.  Bound by
-// HBM where rows are many and long (16383x4112 f32: 124.8 us for 878 MB, 7.0 TB/s; read
-// twice it took 136.7), by issue for bf16 rows of a few blocks (4096x2560: 73 % of the
-// copy rate), by one row's chain of loads, sums and divisions below that.
+// HBM where rows are many and long (16383x4112 f32: 124.3 us for 878 MB, 7.1 TB/s; read
+// twice it took 12 us more), by issue for bf16 rows of a few blocks (4096x2560: 13.6 us,
+// 80 % of the copy rate), by one row's chain of loads, sums and divisions below that.
 template <typename T>
 struct NormArgs {
     const T *x, *residual, *gamma;
@@ -317,9 +319,9 @@ static cudaError_t launch_norm_t(const void *x, const void *residual, const void
     p.inv_k = 1.0f / static_cast<float>(k);
     p.eps = eps;
     // Four warps a row where rows fill the SMs: what a warp does once a row (the merges of
-    // the compensated sums) is then shared by twice the blocks (4096x2560 bf16: 14.8 us,
-    // 17.2 with eight warps).  Eight where the row's own latency counts (1x1024: 1.6 us,
-    // 1.8 with four), and for the registers of long rows.
+    // the compensated sums) is then shared by twice the blocks (4096x2560 bf16: 13.6 us,
+    // 2.4 more with eight warps).  Eight where the row's own latency counts (1x1024: 1.5 us,
+    // 0.2 more with four), and for the registers of long rows.
     const bool many = rows > 2 * num_sms();
     if (many && p.kb <= 8) return launch_row<T, 4, 2>(p, rows, st);
     if (many && p.kb <= 12) return launch_row<T, 4, 3>(p, rows, st);

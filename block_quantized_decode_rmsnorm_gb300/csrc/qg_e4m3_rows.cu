@@ -15,14 +15,16 @@
 // What bounds it is the bytes in flight: a lane copies its own pieces of the next
 // blocks to shared memory by cp.async (no barrier: nobody else reads them), without
 // registers, from before the previous kernel has ended on.  A CTA has eight warps, so
-// that few rows still fill the SMs' queues (1x1024x3584: 2.3 us; four CTAs of a cluster
-// sharing k took 3.5); where it then takes more than one wave, gate|up has four warps
-// per CTA and four CTAs an SM (1x9216x2560: 10.5 us, 14.3 with eight warps; 1x2048x4096:
-// 7.9 us, 6.0 with eight).
+// that few rows still fill the SMs' queues (1x1024x3584 with a residual: 2.6 us; four CTAs
+// of a cluster sharing k took 1.2 more); where it then takes more than one wave, gate|up has
+// four warps per CTA and four CTAs an SM (1x9216x2560: 10.4 us, 13.8 with eight warps;
+// 1x2048x4096: 7.8 us, 5.9 with eight).
 //
 // Gate|up: 16 gate and the 16 matching up rows per CTA, eight CTAs of a cluster
 // hold the 128 outputs of one block of h, and exchange their largest magnitudes
 // through distributed shared memory before each writes its 16 codes per row.
+//
+// Times in this file are of graph replays over operands that rotate through 400 MB.
 #include <algorithm>
 
 #include "qg_e4m3.cuh"
@@ -182,9 +184,9 @@ __global__ void __launch_bounds__(RowsLayout<FORM>::W * 32, RowsLayout<FORM>::CT
     int64_t tile = blockIdx.x;
     int step = 0, slot_no = 0, parity = 0;
     // The residual of this thread's output of a tile (activation row threadIdx.x / 16,
-    // weight row threadIdx.x % 16), loaded while the tile's blocks are (8x2560x9216: 8.8 ->
-    // 8.1 us, 1x1024x3584: 2.4 -> 2.3, 8x18432x2560: 12.5 -> 11.7; 1x65536x1024 without a
-    // residual 15.1 -> 15.6).
+    // weight row threadIdx.x % 16), loaded while the tile's blocks are (7.3 us at
+    // 8x2560x9216 and 0.7 more without, 11.5 and 0.8 at 8x18432x2560, 2.6 and 0.1 at
+    // 1x1024x3584; it costs 0.5 of 15.5 at 1x65536x1024 without a residual).
     float res = 0.0f;
     auto residual = [&]() {
         if (UP || !p.residual) return;
@@ -299,8 +301,9 @@ static cudaError_t launch_rows(int64_t ctas, RowsArgs p, cudaStream_t s)
     const int need = (p.kb + L::W - 1) / L::W;
     constexpr int ring = L::D * L::W * EB;  // columns in flight
     // Where the next kernel's CTAs find room beside these, a second ring's columns go to L2
-    // before the wait (7x2560x9216 bf16: 7.9 -> 7.2 us, 1x2560x12288: 9.2 -> 8.6); with two
-    // CTAs an SM it is no gain (1x4096x14336: 11.4 us, 12.4 with all columns).
+    // before the wait (7x2560x9216 bf16: 7.9 -> 7.2 us, 1x2560x12288: 9.1 -> 8.3, gate|up
+    // 1x512x9216: 8.9 -> 8.6); with two CTAs an SM it is no gain (1x4096x14336: 11.2 us, 1.0
+    // more with all columns).
     if (few(p.tiles)) p.ahead = std::max(0, std::min(p.k - ring, ring));
     const int bytes = L::W * (L::WALK || need > L::D ? L::D : need) * L::T * R_TILE;
     const auto kernel = rows_e4m3_kernel<FORM>;
@@ -325,8 +328,9 @@ cudaError_t launch_rows_e4m3(const uint8_t *w, const float *wd, int64_t n, int64
     p.y = y;
     p.y_bf16 = y_dtype == QG_BF16;
     p.tiles = (n + RR - 1) / RR;
-    // More tiles than CTAs find room: as many each (65536x1024: 18.1 us against 28.5 with
-    // a CTA to each; 1024x3584, one each: 2.3 us, and 2.8 by the kernel that walks).
+    // More tiles than CTAs find room: as many each (1x65536x1024: 15.5 us against 22.3 with
+    // a CTA to each, 8x18432x2560 11.5 and 12.8; one each, 1x1024x3584: 2.6 us against 2.9 by
+    // the kernel that walks, 7x2560x9216 7.2 and 8.4).
     const int64_t room = RowsLayout<Form::ONE>::CTAS * static_cast<int64_t>(num_sms());
     if (p.tiles <= room) return launch_rows<Form::ONE>(p.tiles, p, s);
     const int64_t each = (p.tiles + room - 1) / room;
@@ -350,8 +354,8 @@ cudaError_t launch_rows_up_e4m3(const uint8_t *w, const float *wd, int64_t ffn, 
     p.hq = hq;
     p.hd = hd;
     p.tiles = e4m3_blocks(ffn) * UP_CLUSTER;
-    // Eight warps a CTA up to there: 1x512x2560 3.2 us and 4.1 with four, 8x3584x2560 6.5 and
-    // 6.9, 8x3584x1024 4.0 and 3.9; 8x4608x2560 8.8 and 7.7.
+    // Eight warps a CTA up to there: 1x512x2560 3.4 us and 4.9 with four, 8x3584x2560 6.4 and
+    // 7.0, 8x3584x1024 4.3 and 4.2; 8x4608x2560 8.9 and 7.8.
     if (few(p.tiles)) return launch_rows<Form::UP>(p.tiles, p, s);
     return launch_rows<Form::UP_NARROW>(p.tiles, p, s);
 }

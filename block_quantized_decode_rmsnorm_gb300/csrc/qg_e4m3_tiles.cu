@@ -26,11 +26,13 @@
 // of hanging: the CTA waits (bounded) for the copies and MMAs that it has issued, and the
 // tiles that it has left become NaN outputs or codes (a cluster's tile as a whole).
 //
-// Measured: gate|up 8192x9216x2560 305 us (2.53 PFLOP/s; 333 under the power cap that
-// sets in after a second), product 4096x2560x9216 with the residual 80 us (88), both
-// bound by reading the block sums out of TMEM (365 to 390 of a block's 512 MMA cycles
-// at N = 256, whatever the loads' width) and, behind that, by the operands' way from L2
-// (227 and 73 us alone); 100x2727x3600 8.5 us, bound by its chain of latencies.
+// Times in this file are of graph replays over operands that rotate through 400 MB.
+// Gate|up 8192x9216x2560 305 us (2.53 PFLOP/s; 333 under the power cap that sets in after a
+// second), product 4096x2560x9216 with the residual 79 us (87).  Both are bound by the
+// hand-over of the two TMEM buffers, all that TMEM holds at N = 256: an MMA's 512 cycles, the
+// 365 to 390 of reading its sums (whatever the loads' width) and some 700 between the two
+// make about 800 a block.  Behind that comes the operands' way from L2 (227 and 73 us
+// alone).  100x2727x3600 takes 8.7 us, bound by its chain of latencies.
 #include <algorithm>
 #include <cuda.h>
 #include <type_traits>
@@ -364,7 +366,7 @@ __device__ __forceinline__ bool tile_sums(const P &p, TileShared &b, uint32_t tm
 // for before a stage was filled again), and for the last commit, which covers those before.
 // False after an abort: shared memory and TMEM may be used again, the sums are not to be.
 // (The split kernel passes its count on in a register, the walk through shared memory:
-// registers there are all taken, and 512x2560x9216 took 22.5 us instead of 21.4.)
+// registers there are all taken, and 512x2560x9216 took 1.1 us more.)
 template <int BN, bool SPLIT, class P>
 __device__ __forceinline__ bool tile_drain(const P &p, TileShared &b, int warp, uint32_t issued)
 {
@@ -409,7 +411,7 @@ __device__ __forceinline__ void st_32B(void *p, const uint32_t (&v)[8])
                  "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                  : "memory");
 }
-// Read once, so past L1 (1500x3000x2560 with an f32 residual: 24.5 -> 19.3 us).
+// Read once, so past L1 (1500x3000x2560 with an f32 residual: 20.0 us, 5 more through L1).
 __device__ __forceinline__ void ld_32B(const void *p, uint32_t (&v)[8])
 {
     asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
@@ -426,7 +428,7 @@ enum class Out { UP, BF16, F32, ANY, ANY_ADD };
 
 // 32 columns from c0 of this thread's row of y, 32 bytes (a whole sector) per store,
 // the residual's loads of two pieces before their stores (all four f32 pieces at once cost
-// 96 bytes of spills and are no faster: 1500x3000x2560 25.5 us against 24.5); every row of
+// 96 bytes of spills, and 1 us more at 1500x3000x2560); every row of
 // y starts on 32 bytes and n is a multiple of those 8 or 16 columns.
 template <Out OUT>
 __device__ __forceinline__ void store_row(const TileArgs &p, const uint64_t (&acc)[16], int64_t row, int c0)
@@ -471,8 +473,8 @@ __device__ __forceinline__ void store_row(const TileArgs &p, const uint64_t (&ac
 
 // The same for any n and either type: eight columns of the warp's 32 rows at a time
 // through its transpose buffer, so that eight lanes write neighbouring values.  Of a lane's
-// eight rows four residuals are loaded ahead: 4096x2561x1024, bf16, takes 70 us with one,
-// 46 with two, 36 with four and 42 with eight (1 KB of spills).
+// eight rows four residuals are loaded ahead: 4096x2561x1024, bf16, takes 38 us, 34
+// more with one, 10 more with two and 6 more with eight (1 KB of spills).
 template <bool ADD>
 __device__ __forceinline__ void store_any(const TileArgs &p, const uint64_t (&acc)[16], float *xp, int64_t r0, int64_t c0,
                                           int lane)
@@ -760,7 +762,7 @@ __global__ void __launch_bounds__(TileLayout<BN>::THREADS, TileLayout<BN>::SPLIT
             const int r = rank * per + i / G, c = 4 * (i % G);
             if (n0 + c >= p.n) continue;
             const int64_t at = static_cast<int64_t>(m0 + r) * p.n + n0 + c;
-            const float4 e = residual4(p, at, n0 + c, fours);  // its load beside the sums' (100x2727x3600: 10.2 -> 9.2 us)
+            const float4 e = residual4(p, at, n0 + c, fours);  // its load beside the sums' (100x2727x3600 f32: 9.3 us, 1.0 more behind them)
             const float4 s = cluster_sum4(sums + r * L::LD + c, p.split);
             const float4 o = p.residual ? make_float4(s.x + e.x, s.y + e.y, s.z + e.z, s.w + e.w) : s;
             if (fours) {
@@ -869,7 +871,7 @@ static cudaError_t launch_split(const uint8_t *w, int64_t w_rows, int64_t k, con
 // How many clusters of `split` CTAs the device holds at once (asked once per device).
 // A cluster stays inside one processing cluster of the chip, of 18 to 20 SMs: 46
 // clusters of 6 CTAs at two an SM, but 30 of 7.  A grid one cluster too large takes
-// twice as long (2560 columns, 17 rows, k = 9216: 9.0 us with 6 a tile, 15.4 with 7).
+// twice as long (17x2560x9216: 9.5 us with 6 a tile, 6 more with 7).
 // The query is made for one CTA an SM, which is all that it counts for a kernel of
 // this kind.
 template <int BN, bool UP>
@@ -905,8 +907,8 @@ static int clusters_at_once(int split)
 }
 
 // CTAs per tile: the most that find room at once with four blocks of k each, below
-// which the cluster's own cost is no longer earned (gate|up 16x3584x1024: 5.4 us with
-// 2 of 4 blocks, 6.1 with 5).
+// which the cluster's own cost is no longer earned (gate|up 16x3584x1024: 5.6 us with
+// 2 CTAs of 4 blocks, 0.7 more with 5 CTAs).
 template <int BN, bool UP>
 static int split_of(int64_t tiles, int64_t kb)
 {
@@ -955,7 +957,7 @@ cudaError_t launch_tiles_e4m3(const uint8_t *w, const float *wd, int64_t n, int6
     const int64_t sms = num_sms(), mt = (m + TM - 1) / TM;
     // Too few tiles for the SMs: 64 columns wide, and a cluster to each.  Where a cluster of
     // two does not find room the walk over wider tiles is as fast or faster (512x2560x9216:
-    // 25.8 us against 33.3 with one CTA to each tile of 64).
+    // 22.8 us, 7.5 more with one CTA to each tile of 64).
     if (const int split = product_split(p); split > 1) return launch_split<64, false>(w, n, k, x, p, split, s);
     // the tile width whose busiest SM covers the fewest columns
     int best = 256;
