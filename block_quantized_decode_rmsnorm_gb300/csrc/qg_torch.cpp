@@ -12,6 +12,7 @@
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "qgemv.h"
@@ -142,7 +143,8 @@ PyObject *give(PyObject *a, PyObject *b, PyObject *c = nullptr)
     return r;
 }
 
-// No C++ exception leaves the module.
+// No C++ exception leaves the module: torch's own (a failed allocation, a CUDA error) become
+// the Python exceptions that torch itself raises for them.
 template <typename F>
 PyObject *guarded(Py_ssize_t got, Py_ssize_t want, F &&f)
 {
@@ -158,8 +160,8 @@ PyObject *guarded(Py_ssize_t got, Py_ssize_t want, F &&f)
         return f();
     } catch (const Refused &) {
         return nullptr;
-    } catch (const std::exception &e) {
-        if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());
+    } catch (...) {
+        torch::translate_exception_to_python(std::current_exception());
         return nullptr;
     }
 }

@@ -279,6 +279,34 @@ def test_product_tiles_of_a_few_row_cta(torch, qg, m, n):
     check_product(torch, qg, np.random.default_rng(n), m, n, 1040, "bf16", "apart")
 
 
+# ---------------------------------------------------------------- no memory left
+
+NO_MEMORY = """
+import torch
+import block_quantized_decode_rmsnorm_gb300 as qg
+
+x = torch.ones((1 << 14, 1 << 14), device='cuda')
+limit = torch.cuda.memory_reserved() + (1 << 26)  # not enough for the 2^28 codes
+torch.cuda.set_per_process_memory_fraction(limit / torch.cuda.mem_get_info()[1])
+try:
+    qg.quantize_act_e4m3(x)
+except torch.OutOfMemoryError:
+    pass
+else:
+    raise AssertionError(torch.cuda.memory_summary())
+torch.cuda.set_per_process_memory_fraction(1.0)
+q, d = qg.quantize_act_e4m3(x)
+assert bool((q.view(torch.uint8) == 0x7E).all()) and bool((d * 448 == 1).all())
+"""
+
+
+def test_no_memory_for_an_output():
+    """torch's own error, which programs catch to try again, and the next call as ever."""
+    need_gpu()
+    r = subprocess.run([sys.executable, "-c", NO_MEMORY], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-3000:]
+
+
 # ---------------------------------------------------------------- first calls, repeated calls
 
 FIRST_CALLS = """
