@@ -777,6 +777,10 @@ qg_status qg_debug_stalled_e4m3(const uint8_t *w, const float *wd, int64_t n, in
     if (!aligned(w, 16) || !aligned(wd, 4) || !aligned(xq, 16) || !aligned(xd, 4) || !aligned(out, 16) ||
         !aligned(out_d, 4))
         return QG_ERR_ALIGN;
+    const int64_t kb = e4m3_kb(k), halves = out_d ? 2 : 1;
+    const Span outs[] = {{out, m * n * (out_d ? 1 : 4)}, {out_d, m * e4m3_kb(n) * 4}},
+               in[] = {{w, halves * n * k}, {wd, halves * e4m3_kb(n) * kb * 4}, {xq, m * k}, {xd, m * kb * 4}};
+    if (any_overlap(outs, in)) return QG_ERR_SHAPE;
     return from_cuda(qg::launch_stalled_e4m3(w, wd, n, k, xq, xd, m, out, out_d, cta, block, stream));
 }
 

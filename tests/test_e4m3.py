@@ -154,10 +154,12 @@ def test_stalled_refusals(lib):
     for i, v, want in [(2, 0, SHAPE), (2, 24, SHAPE), (2, 1 << 30, SHAPE), (3, 24, SHAPE), (6, 8, SHAPE),
                        (6, (1 << 24) + 1, SHAPE), (9, -1, SHAPE), (10, -1, SHAPE), (0, None, NULL), (1, None, NULL),
                        (4, None, NULL), (5, None, NULL), (7, None, NULL), (0, at(0, 8), ALIGN), (7, at(4, 8), ALIGN),
-                       (8, at(5, 2), ALIGN)]:
+                       (8, at(5, 2), ALIGN), (7, at(2), SHAPE), (8, at(3), SHAPE), (8, at(4, 16), SHAPE),
+                       (7, at(0, 2 * 144 * 256 - 16), SHAPE)]:
         a = list(good)
         a[i] = v
         assert f(*a) == want, (i, v)
+    assert f(*good[:7], at(0, 144 * 256 - 16), None, *good[9:]) == SHAPE  # a product's f32 y over its weight
 
 
 # ---------------------------------------------------------------- binding refusals

@@ -264,6 +264,72 @@ def test_up_outputs_past_2_31(torch, qg):
         check_block(got[:, c], d[:, b], g[:, c], ag[:, c], u[:, c], au[:, c], k)
 
 
+# ---------------------------------------------------------------- the largest sizes
+
+@pytest.mark.parametrize("m", [1, 9, 20])
+def test_largest_depth(torch, qg, m):
+    k, f = 1 << 20, 16
+    wq, wd = random_codes(torch, 2 * f, k, 15), random_scales(torch, 2, E.blocks(k), 16)
+    x, xd = random_codes(torch, m, k, 17), random_scales(torch, m, E.blocks(k), 18)
+    wd.mul_(1e-2)
+    xq, at = x.view(torch.float8_e4m3fn), np.arange(f)
+    y = qg.qgemm_e4m3(qg.E4M3Weight(wq[:f].view(torch.float8_e4m3fn), wd[:1]), xq, xd).cpu().numpy()
+    hq, hd = qg.qg_ffn_up_e4m3(qg.E4M3Weight(wq.view(torch.float8_e4m3fn), wd), xq, xd)
+    acts64 = x.cpu().numpy(), xd.cpu().numpy()
+    g, ag = product_of_rows(wq, wd[:1], at, *acts64)
+    u, au = product_of_rows(wq[f:], wd[1:], at, *acts64)
+    assert np.all(np.abs(y - g) <= tol(k) * ag + 2.0 ** -24 * np.abs(g))
+    check_block(bits(hq), hd[:, 0].cpu().numpy(), g, ag, u, au, k)
+
+
+def test_most_rows(torch, qg):
+    """2^24 activation rows, and one more refused."""
+    m, k, n = 1 << 24, 16, 16
+    xq, xd = random_codes(torch, m + 1, k, 11), random_scales(torch, m + 1, 1, 12)
+    xq = xq.view(torch.float8_e4m3fn)
+    halves = [E.weight(np.random.default_rng(i), n, k) for i in range(2)]
+    w = qg.E4M3Weight(codes_dev(torch, halves[0][0]), dev(torch, halves[0][1]))
+    gu = qg.E4M3Weight(codes_dev(torch, np.concatenate([h[0] for h in halves])),
+                       dev(torch, np.concatenate([h[1] for h in halves])))
+    y = qg.qgemm_e4m3(w, xq[:m], xd[:m])
+    hq, hd = qg.qg_ffn_up_e4m3(gu, xq[:m], xd[:m])
+    at = np.r_[0:130, m - 130:m]
+    x = bits(xq.view(torch.uint8)[at]), xd[at].cpu().numpy()
+    (g, ag), (u, au) = (E.product(*h, *x) for h in halves)
+    assert np.all(np.abs(y[at].cpu().numpy() - g) <= tol(k) * ag + 2.0 ** -24 * np.abs(g))
+    check_block(bits(hq.view(torch.uint8)[at]), hd[at, 0].cpu().numpy(), g, ag, u, au, k)
+    from block_quantized_decode_rmsnorm_gb300._lib import QGError
+
+    with pytest.raises(QGError):
+        qg.qgemm_e4m3(w, xq, xd)
+    with pytest.raises(QGError):
+        qg.qg_ffn_up_e4m3(gu, xq, xd)
+
+
+@pytest.mark.parametrize("m", [1, 9])
+def test_many_columns(torch, qg, m):
+    n, k = (1 << 27) + 1, 16
+    wq, wd = random_codes(torch, n, k, 13), random_scales(torch, E.blocks(n), 1, 14)
+    xq, xd = acts(np.random.default_rng(m), m, k)
+    y = qg.qgemm_e4m3(qg.E4M3Weight(wq.view(torch.float8_e4m3fn), wd), codes_dev(torch, xq), dev(torch, xd),
+                      out_dtype=torch.bfloat16)
+    at = np.r_[0:3, n // 2 - 2:n // 2 + 2, n - 3:n]
+    want, a = product_of_rows(wq, wd, at, xq, xd)
+    got = y[:, torch.from_numpy(at).cuda()].double().cpu().numpy()
+    assert np.all(np.abs(got - want) <= tol(k) * a + 2.0 ** -8 * np.abs(want) * (1 + 2.0 ** -6))
+
+
+def test_most_norm_rows(torch, qg):
+    rows, k = (1 << 24) + 5, 16
+    x = torch.randn((rows, k), device="cuda", dtype=torch.bfloat16)
+    gamma = torch.ones(k, device="cuda", dtype=torch.bfloat16)
+    q, d, _ = qg.rmsnorm_add_quantize_e4m3(x, gamma, None, EPS)
+    at = np.r_[0:5, rows - 5:rows]
+    want_q, want_d = E.quantize(E.norm(x[at].float().cpu().numpy(), np.ones(k), EPS))
+    same_floats(d[at].cpu().numpy(), want_d)
+    same_codes(bits(q.view(torch.uint8)[at]), want_q)
+
+
 # ---------------------------------------------------------------- both sides of the rules
 
 # few rows of gate|up: eight warps a CTA up to 228 CTAs of 16 columns on 152 SMs, four beyond
