@@ -158,7 +158,7 @@ def build(force: bool = False, verbose: bool = False, strict: bool = False) -> s
     if front:
         try:
             front.result()
-        except RuntimeError as e:
+        except Exception as e:  # whatever it is, the library is there
             if strict:
                 raise
             warnings.warn(f"the torch front end was not built: {e}", RuntimeWarning, stacklevel=2)

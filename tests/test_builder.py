@@ -92,6 +92,18 @@ def test_a_failed_front_end_is_not_an_older_one(apart):
     assert not os.path.exists(builder.FRONT)
 
 
+@with_torch
+def test_a_torch_of_no_known_version_leaves_the_library(apart):
+    def version(name):
+        raise builder.importlib.metadata.PackageNotFoundError(name)
+
+    apart.setattr(builder.importlib.metadata, "version", version)
+    with pytest.warns(RuntimeWarning, match="front end"):
+        assert builder.build() == builder.LIB
+    with pytest.raises(ImportError):
+        builder.build(strict=True)
+
+
 def test_front_end_is_named_for_the_interpreter():
     import sysconfig
 
