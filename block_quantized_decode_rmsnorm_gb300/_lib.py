@@ -16,12 +16,22 @@ LIB_PATH = os.path.join(_HERE, "libqgemv.so")
 QG_OK, QG_ERR_NULL, QG_ERR_ALIGN, QG_ERR_SHAPE, QG_ERR_UNSUPPORTED, QG_ERR_CUDA = range(6)
 QG_EPI_NONE, QG_EPI_SILU_MUL_HALVES, QG_EPI_RESIDUAL_ADD = 0, 1, 2
 QG_F32, QG_BF16 = 0, 1
+QG_KV_Q8_0, QG_KV_E4M3 = 0, 1
 
 P = ctypes.c_void_p
 I64 = ctypes.c_int64
 F32 = ctypes.c_float
 I32 = ctypes.c_int
 ST = ctypes.c_int
+
+
+class KVCacheDesc(ctypes.Structure):
+    """qg_kv_cache of the header."""
+
+    _fields_ = [("k_codes", P), ("k_scales", P), ("v_codes", P), ("v_scales", P), ("n_pages", I64),
+                ("page_size", ctypes.c_int32), ("heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("format", ctypes.c_int32)]
+
 
 # name -> (restype, argtypes), in the order of include/qgemv.h
 SIGNATURES = {
@@ -66,6 +76,11 @@ SIGNATURES = {
     "qg_ffn_up_e4m3": (ST, [P, P, I64, I64, P, P, I64, P, P, P]),
     "qg_ffn_e4m3": (ST, [P, P, P, I32, I64, I64, I64, F32, P, P, P, P, P, P, P, P, P, P]),
     "qg_debug_stalled_e4m3": (ST, [P, P, I64, I64, P, P, I64, P, P, I64, I64, P]),
+    "qg_kv_write": (ST, [ctypes.POINTER(KVCacheDesc), P, I64, I64, P, I64, I64, I32, P, I64, P]),
+    "qg_kv_read": (ST, [ctypes.POINTER(KVCacheDesc), P, I64, P, P, I32, P]),
+    "qg_attn_decode_workspace_bytes": (I64, [I64, I64, I64]),
+    "qg_attn_decode": (ST, [ctypes.POINTER(KVCacheDesc), P, I64, I64, I32, I64, I64, P, I64, P, F32, I64, P, I32, P, P, I64,
+                            P]),
 }
 
 _lib = None

@@ -14,6 +14,7 @@ Tensor formats
 * e4m3 codes: ``torch.float8_e4m3fn [rows, k]``; their scales: ``torch.float32``,
   ``[rows, ceil(k/128)]`` for activations, ``[ceil(n_rows/128), ceil(k/128)]`` for
   weights (an ``E4M3Weight(codes, scales)`` pair).
+* A paged key-value cache in either block format: a ``KVCache`` of four planes.
 """
 
 from __future__ import annotations
@@ -817,7 +818,7 @@ class E4M3Weight:
         return self.codes.numel() + 4 * self.scales.numel()
 
 
-_front = None  # the native front end: checks, outputs and the C call (csrc/qg_torch.cpp)
+_front = None  # the native front end of the e4m3 and cache calls: checks, outputs and the C call (csrc/qg_torch.cpp)
 
 
 def _load_front():
@@ -830,6 +831,8 @@ def _load_front():
                            "block_quantized_decode_rmsnorm_gb300.builder, or __graft_entry__.build())") from e
     _qg_torch.bind(_lib.QGError, *(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
         "quantize_act_e4m3", "rmsnorm_add_quantize_e4m3", "qgemm_e4m3", "qg_ffn_up_e4m3", "qg_ffn_e4m3", "qg_status_str")))
+    _qg_torch.bind_kv(_lib.QGError, *(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
+        "qg_kv_write", "qg_kv_read", "qg_attn_decode", "qg_status_str")))
     _front = _qg_torch
     return _front
 
@@ -941,6 +944,149 @@ def qg_ffn_e4m3(x: torch.Tensor, layer: E4M3Layer, residual: torch.Tensor | None
     b = (buf.xq, buf.xd, buf.hq, buf.hd) if buf is not None else (None, None, None, None)
     return (_front or _load_front()).ffn(x, residual, layer.gamma, layer.gate_up.codes, layer.gate_up.scales,
                                          layer.down.codes, layer.down.scales, eps, *b, y)
+
+
+# --------------------------------------------------------------------------
+# key-value cache: paged, block-quantized, and the attention over it
+# --------------------------------------------------------------------------
+
+class KVCache:
+    """A pool of pages of cached keys and values in one of the library's block formats.
+
+    k, v: codes [n_pages, heads, page_size, head_dim], torch.int8 (Q8_0) or
+    torch.float8_e4m3fn; k_scales, v_scales: [n_pages, heads, page_size, B], torch.float16
+    with B = head_dim / 32 (Q8_0) or torch.float32 with B = ceil(head_dim / 128) (e4m3).
+    Slot s is token s % page_size of page s // page_size; which pages a sequence holds is
+    the caller's page table.  head_dim is 64, 96, 128, 192 or 256, page_size a multiple of
+    16 up to 4096."""
+
+    __slots__ = ("k", "k_scales", "v", "v_scales")
+
+    def __init__(self, k: torch.Tensor, k_scales: torch.Tensor, v: torch.Tensor, v_scales: torch.Tensor):
+        self.k, self.k_scales, self.v, self.v_scales = k, k_scales, v, v_scales
+
+    @classmethod
+    def allocate(cls, n_pages: int, page_size: int, heads: int, head_dim: int, device="cuda",
+                 format: str = "q8_0") -> "KVCache":
+        """An empty (zero-filled) pool; format "q8_0" or "e4m3"."""
+        if format not in ("q8_0", "e4m3"):
+            raise ValueError(f"format must be 'q8_0' or 'e4m3', got {format!r}")
+        if head_dim not in (64, 96, 128, 192, 256):
+            raise ValueError(f"head_dim must be 64, 96, 128, 192 or 256, got {head_dim}")
+        if page_size < 16 or page_size % 16 or page_size > 4096:
+            raise ValueError(f"page_size must be a multiple of 16 up to 4096, got {page_size}")
+        codes, scales, nb = ((torch.int8, torch.float16, head_dim // 32) if format == "q8_0" else
+                             (_E4M3, torch.float32, _blocks128(head_dim)))
+        shape = (n_pages, heads, page_size)
+
+        def plane():
+            return (torch.zeros((*shape, head_dim), dtype=torch.uint8, device=device).view(codes),
+                    torch.zeros((*shape, nb), dtype=scales, device=device))
+
+        return cls(*plane(), *plane())
+
+    @property
+    def n_pages(self) -> int:
+        return self.k.shape[0]
+
+    @property
+    def heads(self) -> int:
+        return self.k.shape[1]
+
+    @property
+    def page_size(self) -> int:
+        return self.k.shape[2]
+
+    @property
+    def head_dim(self) -> int:
+        return self.k.shape[3]
+
+    @property
+    def nbytes(self) -> int:
+        return 2 * (self.k.numel() + self.k_scales.numel() * self.k_scales.element_size())
+
+
+def qg_kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, stream=None) -> None:
+    """Quantize the keys and values of new tokens into the cache.
+
+    k, v: [rows, heads, head_dim], both f32 or both bf16; rows of head_dim values are
+    contiguous and start on 16 bytes, the other strides are free (parts of a stacked
+    projection's output).  slots: int64 [rows]; a row whose slot lies outside the cache
+    (negative: padding) is not written, the others' slots differ from one another."""
+    if stream is not None:
+        with _on(stream):
+            return qg_kv_write(cache, k, v, slots)
+    return (_front or _load_front()).kv_write(cache.k, cache.k_scales, cache.v, cache.v_scales, k, v, slots)
+
+
+def qg_kv_read(cache: KVCache, slots: torch.Tensor, dtype: torch.dtype | None = None, k: torch.Tensor | None = None,
+               v: torch.Tensor | None = None, stream=None):
+    """The cached keys and values at slots (int64 [rows]): (k, v) [rows, heads, head_dim] in
+    f32 or bf16 (dtype; by default k's type, else f32).  A slot outside the cache reads as zeros."""
+    if stream is not None:
+        with _on(stream):
+            return qg_kv_read(cache, slots, dtype, k, v)
+    if dtype is not None:
+        kind = _STREAM_TYPES.get(dtype)
+        if kind is None:
+            raise TypeError(f"dtype must be torch.float32 or torch.bfloat16, got {dtype}")
+        dtype = kind
+    return (_front or _load_front()).kv_read(cache.k, cache.k_scales, cache.v, cache.v_scales, slots, dtype, k, v)
+
+
+def qg_attn_decode_workspace_bytes(q_heads: int, heads: int, head_dim: int) -> int:
+    n = _lib.load().qg_attn_decode_workspace_bytes(q_heads, heads, head_dim)
+    if n < 0:
+        raise ValueError(f"decode attention: unsupported shape q_heads={q_heads} heads={heads} head_dim={head_dim}")
+    return n
+
+
+@dataclass
+class AttnWork:
+    """The zero-filled workspace of qg_attn_decode.  One serves the layers of a model one
+    after another; calls that share one must not overlap in time (two streams, or two
+    graphs replayed at once, need one each)."""
+
+    buf: torch.Tensor
+
+    @staticmethod
+    def allocate(q_heads: int, heads: int, head_dim: int, device="cuda") -> "AttnWork":
+        with torch.cuda.device(device):
+            n = qg_attn_decode_workspace_bytes(q_heads, heads, head_dim)
+            return AttnWork(torch.zeros((n,), dtype=torch.uint8, device=device))
+
+
+def qg_attn_decode(q: torch.Tensor, cache: KVCache, pages: torch.Tensor, lengths: torch.Tensor,
+                   scale: float | None = None, window: int = 0, out: torch.Tensor | None = None,
+                   out_dtype: torch.dtype | None = None, lse: torch.Tensor | None = None,
+                   work: AttnWork | None = None, stream=None) -> torch.Tensor:
+    """Attention of one new token per sequence over its cached tokens (its own among them).
+
+    q: [batch, q_heads, head_dim] f32 or bf16, strides as qg_kv_write's k; query head h reads
+    cache head h // (q_heads / heads).  pages: int32 [batch, max_pages], lengths: int32 [batch]:
+    sequence b's token t < lengths[b] is token t % page_size of page pages[b, t // page_size].
+    window > 0: the last window tokens only.  scale: by default head_dim ** -0.5.  Returns out
+    [batch, q_heads, head_dim], of out_dtype (by default out's type, else q's); lse, if given,
+    f32 [batch, q_heads], receives the logarithm of each softmax's sum.  A sequence without
+    tokens has out 0 and lse -inf, one with a page outside the cache has NaN.
+
+    work: the workspace; without one a new one is allocated and zeroed, which costs more than
+    a short call.  A captured graph keeps the one that it was captured with."""
+    if stream is not None:
+        with _on(stream):
+            return qg_attn_decode(q, cache, pages, lengths, scale, window, out, out_dtype, lse, work)
+    if out_dtype is not None:
+        kind = _STREAM_TYPES.get(out_dtype)
+        if kind is None:
+            raise TypeError(f"out_dtype must be torch.float32 or torch.bfloat16, got {out_dtype}")
+        out_dtype = kind
+    front = _front or _load_front()
+    if work is None:
+        if not (isinstance(q, torch.Tensor) and q.is_cuda and q.dim() == 3):
+            raise ValueError("q must be [batch, q_heads, head_dim] on a CUDA device (there is no CPU path)")
+        work = AttnWork.allocate(q.shape[1], cache.heads, cache.head_dim, q.device)
+    return front.attn_decode(cache.k, cache.k_scales, cache.v, cache.v_scales, q, pages, lengths, scale, window, out,
+                             out_dtype, lse, work.buf)
 
 
 # --------------------------------------------------------------------------

@@ -3,7 +3,7 @@
 #include <map>
 #include <mutex>
 
-#include "qg_common.cuh"
+#include "qg_kv.cuh"
 
 namespace qg {
 
@@ -82,6 +82,12 @@ cudaError_t launch_tiles_up_e4m3(const uint8_t *, const float *, int64_t, int64_
                                  int64_t, uint8_t *, float *, cudaStream_t);
 cudaError_t launch_stalled_e4m3(const uint8_t *, const float *, int64_t, int64_t, const uint8_t *, const float *,
                                 int64_t, void *, float *, int64_t, int64_t, cudaStream_t);
+cudaError_t launch_kv_write(const KvPlanes &, const void *, int64_t, int64_t, const void *, int64_t, int64_t, int,
+                            const int64_t *, int64_t, cudaStream_t);
+cudaError_t launch_kv_read(const KvPlanes &, const int64_t *, int64_t, void *, void *, int, cudaStream_t);
+int64_t attn_workspace_bytes(int64_t q_heads, int64_t heads, int64_t dim);
+cudaError_t launch_attn_decode(const KvPlanes &, const void *, int64_t, int64_t, int, int64_t, int64_t, const int32_t *,
+                               int64_t, const int32_t *, float, int64_t, void *, int, float *, void *, cudaStream_t);
 
 // SM count of the current device, read once per device.
 int num_sms()
@@ -782,6 +788,138 @@ qg_status qg_debug_stalled_e4m3(const uint8_t *w, const float *wd, int64_t n, in
                in[] = {{w, halves * n * k}, {wd, halves * e4m3_kb(n) * kb * 4}, {xq, m * k}, {xd, m * kb * 4}};
     if (any_overlap(outs, in)) return QG_ERR_SHAPE;
     return from_cuda(qg::launch_stalled_e4m3(w, wd, n, k, xq, xd, m, out, out_d, cta, block, stream));
+}
+
+// ---- key-value cache --------------------------------------------------------
+namespace {
+
+constexpr int64_t kKvMaxRows = INT32_MAX;
+constexpr int32_t kKvMaxHeads = 1024;
+constexpr int64_t kAttnMaxBatch = int64_t(1) << 20;
+constexpr int64_t kAttnMaxHeads = 16384;
+
+bool kv_dim_ok(int64_t d) { return d == 64 || d == 96 || d == 128 || d == 192 || d == 256; }
+
+// The sizes of a cache, then (need_planes) its pointers.
+qg_status check_kv(const qg_kv_cache *c, bool need_planes, qg::KvPlanes *planes, int64_t *code_bytes,
+                   int64_t *scale_bytes)
+{
+    if (!c) return QG_ERR_NULL;
+    if (c->format != QG_KV_Q8_0 && c->format != QG_KV_E4M3) return QG_ERR_UNSUPPORTED;
+    if (!kv_dim_ok(c->head_dim)) return QG_ERR_UNSUPPORTED;
+    if (c->heads < 1 || c->heads > kKvMaxHeads || c->page_size < qg::KV_TILE || c->page_size % qg::KV_TILE != 0 ||
+        c->page_size > 4096 || c->n_pages < 0 || c->n_pages > INT32_MAX)
+        return QG_ERR_SHAPE;
+    const bool e = c->format == QG_KV_E4M3;
+    const int64_t rows = c->n_pages * c->page_size * c->heads;
+    *code_bytes = rows * c->head_dim;
+    *scale_bytes = rows * qg::kv_blocks(e, c->head_dim) * (e ? 4 : 2);
+    *planes = {static_cast<uint8_t *>(c->k_codes), static_cast<uint8_t *>(c->v_codes), c->k_scales, c->v_scales,
+               c->n_pages, c->page_size, c->heads, c->head_dim, e};
+    if (!need_planes || c->n_pages == 0) return QG_OK;
+    const Span p[] = {{c->k_codes, *code_bytes}, {c->v_codes, *code_bytes}, {c->k_scales, *scale_bytes},
+                      {c->v_scales, *scale_bytes}}, none[] = {{nullptr, 0}};
+    for (const Span &s : p) {
+        if (!s.p) return QG_ERR_NULL;
+        if (!aligned(s.p, 16)) return QG_ERR_ALIGN;
+    }
+    return any_overlap(p, none) ? QG_ERR_SHAPE : QG_OK;
+}
+
+// Strides of rows [rows][heads][dim]; the elements from the first to behind the last, 0 if that leaves 64 bits.
+int64_t strided_extent(int64_t rows, int64_t row_stride, int64_t heads, int64_t head_stride, int64_t dim)
+{
+    const __int128 n = static_cast<__int128>(rows - 1) * row_stride + static_cast<__int128>(heads - 1) * head_stride + dim;
+    return n > (__int128(1) << 58) ? 0 : static_cast<int64_t>(n);
+}
+bool strides_aligned(int64_t rows, int64_t row_stride, int64_t heads, int64_t head_stride, int64_t size)
+{
+    return (rows == 1 || row_stride * size % 16 == 0) && (heads == 1 || head_stride * size % 16 == 0);
+}
+
+}  // namespace
+
+qg_status qg_kv_write(const qg_kv_cache *cache, const void *k, int64_t k_row_stride, int64_t k_head_stride, const void *v,
+                      int64_t v_row_stride, int64_t v_head_stride, int dtype, const int64_t *slots, int64_t rows,
+                      qg_stream_t stream)
+{
+    qg::KvPlanes c;
+    int64_t cb, sb;
+    if (qg_status st = check_kv(cache, false, &c, &cb, &sb); st != QG_OK) return st;
+    if (!dtype_ok(dtype)) return QG_ERR_UNSUPPORTED;
+    if (rows < 0 || rows > kKvMaxRows || k_row_stride < 0 || k_head_stride < 0 || v_row_stride < 0 || v_head_stride < 0)
+        return QG_ERR_SHAPE;
+    if (rows == 0) return QG_OK;
+    if (qg_status st = check_kv(cache, true, &c, &cb, &sb); st != QG_OK) return st;
+    if (!k || !v || !slots) return QG_ERR_NULL;
+    const int64_t e = dtype_size(dtype), kn = strided_extent(rows, k_row_stride, c.heads, k_head_stride, c.dim),
+                  vn = strided_extent(rows, v_row_stride, c.heads, v_head_stride, c.dim);
+    if (!kn || !vn) return QG_ERR_SHAPE;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 8) ||
+        !strides_aligned(rows, k_row_stride, c.heads, k_head_stride, e) ||
+        !strides_aligned(rows, v_row_stride, c.heads, v_head_stride, e))
+        return QG_ERR_ALIGN;
+    const Span out[] = {{c.kq, cb}, {c.vq, cb}, {c.kd, sb}, {c.vd, sb}}, in[] = {{k, kn * e}, {v, vn * e}, {slots, rows * 8}};
+    if (any_overlap(out, in)) return QG_ERR_SHAPE;
+    return from_cuda(qg::launch_kv_write(c, k, k_row_stride, k_head_stride, v, v_row_stride, v_head_stride, dtype, slots,
+                                         rows, stream));
+}
+
+qg_status qg_kv_read(const qg_kv_cache *cache, const int64_t *slots, int64_t rows, void *k, void *v, int dtype,
+                     qg_stream_t stream)
+{
+    qg::KvPlanes c;
+    int64_t cb, sb;
+    if (qg_status st = check_kv(cache, false, &c, &cb, &sb); st != QG_OK) return st;
+    if (!dtype_ok(dtype)) return QG_ERR_UNSUPPORTED;
+    if (rows < 0 || rows > kKvMaxRows) return QG_ERR_SHAPE;
+    if (rows == 0) return QG_OK;
+    if (qg_status st = check_kv(cache, true, &c, &cb, &sb); st != QG_OK) return st;
+    if (!k || !v || !slots) return QG_ERR_NULL;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 8)) return QG_ERR_ALIGN;
+    const int64_t ob = rows * c.heads * c.dim * dtype_size(dtype);
+    const Span out[] = {{k, ob}, {v, ob}}, in[] = {{c.kq, cb}, {c.vq, cb}, {c.kd, sb}, {c.vd, sb}, {slots, rows * 8}};
+    if (any_overlap(out, in)) return QG_ERR_SHAPE;
+    return from_cuda(qg::launch_kv_read(c, slots, rows, k, v, dtype, stream));
+}
+
+int64_t qg_attn_decode_workspace_bytes(int64_t q_heads, int64_t heads, int64_t head_dim)
+{
+    if (heads < 1 || heads > kKvMaxHeads || q_heads < heads || q_heads > kAttnMaxHeads || q_heads % heads != 0 ||
+        !kv_dim_ok(head_dim))
+        return -1;
+    return qg::attn_workspace_bytes(q_heads, heads, head_dim);
+}
+
+qg_status qg_attn_decode(const qg_kv_cache *cache, const void *q, int64_t q_row_stride, int64_t q_head_stride, int q_dtype,
+                         int64_t batch, int64_t q_heads, const int32_t *pages, int64_t max_pages, const int32_t *lengths,
+                         float scale, int64_t window, void *out, int out_dtype, float *lse, void *workspace,
+                         int64_t workspace_bytes, qg_stream_t stream)
+{
+    qg::KvPlanes c;
+    int64_t cb, sb;
+    if (qg_status st = check_kv(cache, false, &c, &cb, &sb); st != QG_OK) return st;
+    if (!dtype_ok(q_dtype) || !dtype_ok(out_dtype)) return QG_ERR_UNSUPPORTED;
+    if (batch < 0 || batch > kAttnMaxBatch || q_heads < c.heads || q_heads % c.heads != 0 || q_heads > kAttnMaxHeads ||
+        q_row_stride < 0 || q_head_stride < 0 || max_pages < 0 || max_pages > INT32_MAX / c.page || window < 0)
+        return QG_ERR_SHAPE;
+    if (batch == 0) return QG_OK;
+    if (qg_status st = check_kv(cache, true, &c, &cb, &sb); st != QG_OK) return st;
+    if (!q || (!pages && max_pages > 0) || !lengths || !out || !workspace) return QG_ERR_NULL;
+    const int64_t e = dtype_size(q_dtype), qn = strided_extent(batch, q_row_stride, q_heads, q_head_stride, c.dim);
+    if (!qn) return QG_ERR_SHAPE;
+    if (!aligned(q, 16) || !aligned(pages, 4) || !aligned(lengths, 4) || !aligned(out, 16) || !aligned(lse, 4) ||
+        !aligned(workspace, 16) || !strides_aligned(batch, q_row_stride, q_heads, q_head_stride, e))
+        return QG_ERR_ALIGN;
+    const int64_t wb = qg_attn_decode_workspace_bytes(q_heads, c.heads, c.dim);
+    if (workspace_bytes < wb) return QG_ERR_SHAPE;
+    const int64_t rows = batch * q_heads;
+    const Span outs[] = {{out, rows * c.dim * dtype_size(out_dtype)}, {lse, rows * 4}, {workspace, wb}},
+               in[] = {{q, qn * e}, {pages, batch * max_pages * 4}, {lengths, batch * 4}, {c.kq, cb}, {c.vq, cb},
+                       {c.kd, sb}, {c.vd, sb}};
+    if (any_overlap(outs, in)) return QG_ERR_SHAPE;
+    return from_cuda(qg::launch_attn_decode(c, q, q_row_stride, q_head_stride, q_dtype, batch, q_heads, pages, max_pages,
+                                            lengths, scale, window, out, out_dtype, lse, workspace, stream));
 }
 
 }  // extern "C"

@@ -1,5 +1,5 @@
-// Native front end of the 8-bit floating point calls for torch tensors: argument
-// checks, outputs that were not given, and the C call, in one step.
+// Native front end of the 8-bit floating point and key-value cache calls for torch
+// tensors: argument checks, outputs that were not given, and the C call, in one step.
 //
 // A decode step's kernels take 2 to 6 us each; the same checks and allocations in
 // Python took 5 to 12 us a call of the host (Neoverse V2) on top of the launch, here
@@ -14,6 +14,8 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
+
+#include <cmath>
 
 #include "qgemv.h"
 
@@ -35,6 +37,14 @@ struct Library {
     decltype(&::qg_status_str) qg_status_str;
 };
 Library lib = {};
+
+// The same for the key-value cache (bind_kv).
+struct KvLibrary {
+    decltype(&::qg_kv_write) qg_kv_write;
+    decltype(&::qg_kv_read) qg_kv_read;
+    decltype(&::qg_attn_decode) qg_attn_decode;
+};
+KvLibrary kv_lib = {};
 
 struct Refused {};  // a Python exception is set
 
@@ -320,6 +330,123 @@ PyObject *ffn(PyObject *, PyObject *const *a, Py_ssize_t n)
     });
 }
 
+// ---- key-value cache --------------------------------------------------------
+
+// The four planes of a cache (k codes, k scales, v codes, v scales), checked, as the library takes them.
+qg_kv_cache cache_of(PyObject *const *a, int dev)
+{
+    if (!kv_lib.qg_kv_write) refuse(PyExc_RuntimeError, "no library is bound");
+    const Tensor &kq = tensor(a[0], "cache.k"), &kd = tensor(a[1], "cache.k_scales");
+    const Tensor &vq = tensor(a[2], "cache.v"), &vd = tensor(a[3], "cache.v_scales");
+    if (kq.dim() != 4)
+        refuse(PyExc_ValueError, "cache.k must have shape [n_pages, heads, page_size, head_dim], got " + text(kq.sizes()));
+    const ScalarType t = kq.scalar_type();
+    if (t != ScalarType::Char && t != E4M3)
+        refuse(PyExc_TypeError, std::string("cache.k must be torch.int8 (Q8_0) or torch.float8_e4m3fn, got ") + c10::toString(t));
+    const bool e4m3 = t == E4M3;
+    const int64_t pages = kq.size(0), heads = kq.size(1), page = kq.size(2), dim = kq.size(3);
+    const int64_t nb = e4m3 ? blocks(dim) : dim / 32, most = INT32_MAX;
+    const ScalarType st = e4m3 ? ScalarType::Float : ScalarType::Half;
+    need(kq, "cache.k", t, kq.sizes(), dev);
+    need(vq, "cache.v", t, kq.sizes(), dev);
+    need(kd, "cache.k_scales", st, {pages, heads, page, nb}, dev);
+    need(vd, "cache.v_scales", st, {pages, heads, page, nb}, dev);
+    if (heads > most || page > most || dim > most) refuse(PyExc_ValueError, "cache.k has a side beyond 2^31");
+    return {kq.data_ptr(), kd.data_ptr(), vq.data_ptr(), vd.data_ptr(), pages, static_cast<int32_t>(page),
+            static_cast<int32_t>(heads), static_cast<int32_t>(dim), e4m3 ? QG_KV_E4M3 : QG_KV_Q8_0};
+}
+
+// [rows, heads, dim] with contiguous rows of dim values; the strides of its other sides.
+struct Strided {
+    int64_t row, head;
+};
+Strided strided(const Tensor &t, const char *name, ScalarType type, IntArrayRef shape, int dev)
+{
+    const std::string n = name;
+    if (!t.is_cuda()) refuse(PyExc_ValueError, n + " must be on a CUDA device (there is no CPU path)");
+    if (t.scalar_type() != type)
+        refuse(PyExc_TypeError, n + " must be " + c10::toString(type) + ", got " + c10::toString(t.scalar_type()));
+    if (t.sizes() != shape) refuse(PyExc_ValueError, n + " must have shape " + text(shape) + ", got " + text(t.sizes()));
+    if (t.get_device() != dev) refuse(PyExc_ValueError, n + " must be on cuda:" + std::to_string(dev));
+    if (t.size(2) > 1 && t.stride(2) != 1) refuse(PyExc_ValueError, n + " must have contiguous rows of head_dim values");
+    return {t.size(0) > 1 ? t.stride(0) : 0, t.size(1) > 1 ? t.stride(1) : 0};
+}
+
+// (k codes, k scales, v codes, v scales, k, v, slots) -> None
+PyObject *kv_write(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded(n, 7, [&]() -> PyObject * {
+        const Tensor &k = tensor(a[4], "k"), &v = tensor(a[5], "v"), &slots = tensor(a[6], "slots");
+        const int dev = device_of(k, "k"), kind = stream_type(k.scalar_type(), "k");
+        const qg_kv_cache c = cache_of(a, dev);
+        if (k.dim() != 3) refuse(PyExc_ValueError, "k must have shape [rows, heads, head_dim], got " + text(k.sizes()));
+        const int64_t rows = k.size(0), shape[] = {rows, c.heads, c.head_dim};
+        const Strided ks = strided(k, "k", k.scalar_type(), shape, dev), vs = strided(v, "v", k.scalar_type(), shape, dev);
+        need(slots, "slots", ScalarType::Long, {rows}, dev);
+        done("qg_kv_write", kv_lib.qg_kv_write(&c, k.data_ptr(), ks.row, ks.head, v.data_ptr(), vs.row, vs.head, kind,
+                                               at_<int64_t>(slots), rows, stream_on(dev)));
+        Py_RETURN_NONE;
+    });
+}
+
+// (k codes, k scales, v codes, v scales, slots, out type: 0 f32, 1 bf16, None, k, v) -> (k, v)
+PyObject *kv_read(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded(n, 8, [&] {
+        const Tensor &slots = tensor(a[4], "slots"), *k_in = optional(a[6], "k");
+        const int dev = device_of(slots, "slots");
+        const qg_kv_cache c = cache_of(a, dev);
+        if (slots.dim() != 1) refuse(PyExc_ValueError, "slots must have shape [rows], got " + text(slots.sizes()));
+        const int64_t rows = slots.size(0), shape[] = {rows, c.heads, c.head_dim};
+        need(slots, "slots", ScalarType::Long, {rows}, dev);
+        ScalarType type = k_in ? k_in->scalar_type() : ScalarType::Float;
+        if (a[5] != Py_None) type = PyLong_AsLong(a[5]) == QG_BF16 ? ScalarType::BFloat16 : ScalarType::Float;
+        const int kind = stream_type(type, "k");
+        const Tensor k = output(a[6], "k", type, shape, dev), v = output(a[7], "v", type, shape, dev);
+        done("qg_kv_read", kv_lib.qg_kv_read(&c, at_<int64_t>(slots), rows, k.data_ptr(), v.data_ptr(), kind, stream_on(dev)));
+        return give(give(k), give(v));
+    });
+}
+
+// (k codes, k scales, v codes, v scales, q, pages, lengths, scale or None, window, out, out type: 0 f32, 1 bf16, None,
+//  lse or None, work) -> out
+PyObject *attn_decode(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded(n, 13, [&] {
+        const Tensor &q = tensor(a[4], "q"), &pages = tensor(a[5], "pages"), &lengths = tensor(a[6], "lengths");
+        const Tensor *out_in = optional(a[9], "out"), *lse = optional(a[11], "lse"), &work = tensor(a[12], "work.buf");
+        const int dev = device_of(q, "q"), kind = stream_type(q.scalar_type(), "q");
+        const qg_kv_cache c = cache_of(a, dev);
+        if (q.dim() != 3 || q.size(2) != c.head_dim)
+            refuse(PyExc_ValueError, "q must have shape [batch, q_heads, " + std::to_string(c.head_dim) + "], got " + text(q.sizes()));
+        if (c.heads == 0 || q.size(1) == 0 || q.size(1) % c.heads)
+            refuse(PyExc_ValueError, "q's heads must be a multiple of the cache's " + std::to_string(c.heads) + ", got " +
+                                         std::to_string(q.size(1)));
+        const int64_t batch = q.size(0), heads = q.size(1);
+        const Strided qs = strided(q, "q", q.scalar_type(), q.sizes(), dev);
+        if (pages.dim() != 2 || pages.size(0) != batch)
+            refuse(PyExc_ValueError, "pages must have shape [" + std::to_string(batch) + ", max_pages], got " + text(pages.sizes()));
+        need(pages, "pages", ScalarType::Int, pages.sizes(), dev);
+        need(lengths, "lengths", ScalarType::Int, {batch}, dev);
+        double scale = 1.0 / std::sqrt(static_cast<double>(c.head_dim));
+        if (a[7] != Py_None) scale = PyFloat_AsDouble(a[7]);
+        if (scale == -1.0 && PyErr_Occurred()) throw Refused();
+        const long long window = PyLong_AsLongLong(a[8]);
+        if (window == -1 && PyErr_Occurred()) throw Refused();
+        ScalarType type = out_in ? out_in->scalar_type() : q.scalar_type();
+        if (a[10] != Py_None) type = PyLong_AsLong(a[10]) == QG_BF16 ? ScalarType::BFloat16 : ScalarType::Float;
+        const int out_kind = stream_type(type, "out");
+        const Tensor out = output(a[9], "out", type, q.sizes(), dev);
+        if (lse) need(*lse, "lse", ScalarType::Float, {batch, heads}, dev);
+        need(work, "work.buf", ScalarType::Byte, {work.numel()}, dev);
+        done("qg_attn_decode",
+             kv_lib.qg_attn_decode(&c, q.data_ptr(), qs.row, qs.head, kind, batch, heads, at_<int32_t>(pages), pages.size(1),
+                                   at_<int32_t>(lengths), static_cast<float>(scale), window, out.data_ptr(), out_kind,
+                                   lse ? at_<float>(*lse) : nullptr, work.data_ptr(), work.numel(), stream_on(dev)));
+        return give(out);
+    });
+}
+
 // The entry point whose address is a[i].
 template <typename F>
 bool entry(PyObject *const *a, int i, F &f)
@@ -348,13 +475,36 @@ PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n)
     Py_RETURN_NONE;
 }
 
+// (the error class, then the entry points' addresses in KvLibrary's order, then qg_status_str's)
+PyObject *bind_kv(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    if (n != 5) {
+        PyErr_Format(PyExc_TypeError, "expected 5 arguments, got %zd", n);
+        return nullptr;
+    }
+    KvLibrary l;
+    decltype(lib.qg_status_str) str;
+    if (!entry(a, 1, l.qg_kv_write) || !entry(a, 2, l.qg_kv_read) || !entry(a, 3, l.qg_attn_decode) || !entry(a, 4, str))
+        return nullptr;
+    kv_lib = l;
+    lib.qg_status_str = str;
+    Py_INCREF(a[0]);
+    Py_XDECREF(qg_error);
+    qg_error = a[0];
+    Py_RETURN_NONE;
+}
+
 #define FAST(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(f)), METH_FASTCALL, nullptr
 PyMethodDef methods[] = {{"bind", FAST(bind)},
+                         {"bind_kv", FAST(bind_kv)},
                          {"quantize_act", FAST(quantize_act)},
                          {"rmsnorm_add_quantize", FAST(rmsnorm_add_quantize)},
                          {"qgemm", FAST(qgemm)},
                          {"ffn_up", FAST(ffn_up)},
                          {"ffn", FAST(ffn)},
+                         {"kv_write", FAST(kv_write)},
+                         {"kv_read", FAST(kv_read)},
+                         {"attn_decode", FAST(attn_decode)},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_qg_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -36,11 +36,12 @@
  * - Outputs never alias inputs, except where a call says so.
  * - Threads and state: calls may be made from several host threads.  The
  *   library keeps per-device caches, filled on first use under a lock (the SM
- *   count, the shared-memory opt-in of each kernel).  Two entry points share
+ *   count, the shared-memory opt-in of each kernel).  Three entry points share
  *   device memory between calls: qg_decode_layers_q8_0_noalloc uses one fixed
- *   array per GPU compiled into the library, and qg_decode_stack_q8_0 a
- *   caller-owned workspace.  Calls that share that array, or a workspace, must
- *   not overlap in time; every other call is independent of every other.
+ *   array per GPU compiled into the library, qg_decode_stack_q8_0 and
+ *   qg_attn_decode a caller-owned workspace.  Calls that share that array, or a
+ *   workspace, must not overlap in time; every other call is independent of
+ *   every other.
  */
 #ifndef QGEMV_H
 #define QGEMV_H
@@ -725,6 +726,103 @@ QG_API qg_status qg_ffn_e4m3(const void *x, const void *residual, const void *ga
 QG_API qg_status qg_debug_stalled_e4m3(const uint8_t *w, const float *wd, int64_t n, int64_t k, const uint8_t *xq,
                                        const float *xd, int64_t m, void *out, float *out_d, int64_t cta, int64_t block,
                                        qg_stream_t stream);
+
+/*
+ * The key-value cache of a decode step and the attention that reads it: what lies
+ * between the qkv projection and the output projection ([Phobos] Opening the
+ * Floodgates: decode attention over a cache; Fast Decode: quantize once, exact codes
+ * and one scale per block).  The cache is block-quantized in either of the library's
+ * formats and paged, so that sequences of any length share one pool of pages.
+ *
+ * qg_kv_cache - a pool of n_pages pages of page_size tokens, owned by the caller:
+ *   k_codes, v_codes:   device uint8/int8[n_pages][heads][page_size][head_dim]
+ *   k_scales, v_scales: device [n_pages][heads][page_size][B], each row of head_dim
+ *       values in B blocks with a scale of its own:
+ *       QG_KV_Q8_0  int8 codes, binary16 scales, B = head_dim / 32, a row quantized as
+ *                   by quantize_act_q8_0
+ *       QG_KV_E4M3  e4m3 codes, f32 scales, B = ceil(head_dim / 128), a row quantized
+ *                   as by quantize_act_e4m3
+ *   Slot s is token s % page_size of page s / page_size; the cached value is
+ *   code * scale.  The four planes are 16-byte aligned and do not overlap.
+ *   head_dim: 64, 96, 128, 192 or 256 (else QG_ERR_UNSUPPORTED); page_size: a multiple
+ *   of 16 up to 4096; heads: 1 .. 1024; n_pages: 0 .. 2^31 - 1.
+ * The struct is read during the call only.
+ */
+typedef enum {
+    QG_KV_Q8_0 = 0,
+    QG_KV_E4M3 = 1
+} qg_kv_format;
+
+typedef struct {
+    void *k_codes, *k_scales, *v_codes, *v_scales;
+    int64_t n_pages;
+    int32_t page_size, heads, head_dim;
+    int32_t format; /* a qg_kv_format */
+} qg_kv_cache;
+
+/*
+ * qg_kv_write - quantize the keys and values of `rows` tokens into the cache.
+ *   k, v: device f32 or bf16 (dtype, a qg_dtype): value i of head h of row r is element
+ *       r * row_stride + h * head_stride + i of each (read); parts of a stacked
+ *       projection's rows are such tensors.  Every row of head_dim values starts on 16
+ *       bytes.  Strides are in elements, not negative.
+ *   slots: device int64[rows] (read), 8-byte aligned: where each row goes.  A row whose
+ *       slot is outside the cache (negative: a batch's padding) is not written.  Slots
+ *       inside the cache must differ from one another: what two rows of one slot leave
+ *       there is a mix of both.
+ *   The cache's other slots keep their contents.  k, v and slots must not overlap the
+ *   cache (QG_ERR_SHAPE).  rows <= 2^31 - 1.
+ */
+QG_API qg_status qg_kv_write(const qg_kv_cache *cache, const void *k, int64_t k_row_stride, int64_t k_head_stride,
+                             const void *v, int64_t v_row_stride, int64_t v_head_stride, int dtype,
+                             const int64_t *slots, int64_t rows, qg_stream_t stream);
+
+/*
+ * qg_kv_read - the cached keys and values at `rows` slots.
+ *   value = fl(code * scale), rounded once more to bf16 for bf16 outputs.  A slot outside
+ *   the cache reads as zeros; a slot may be read more than once.
+ *   k, v: device f32 or bf16 (dtype) [rows][heads][head_dim] (written), 16-byte aligned,
+ *   not overlapping the cache, the slots or each other (QG_ERR_SHAPE).
+ *   slots: device int64[rows] (read), 8-byte aligned.  rows <= 2^31 - 1.
+ */
+QG_API qg_status qg_kv_read(const qg_kv_cache *cache, const int64_t *slots, int64_t rows, void *k, void *v, int dtype,
+                            qg_stream_t stream);
+
+/*
+ * qg_attn_decode - attention of one new token of each of `batch` sequences over its
+ * cached tokens, the new one's own among them (write it first).  Query head h reads
+ * cache head h / (q_heads / heads).  Over the tokens t seen by sequence b,
+ * max(0, n - window) <= t < n, n = lengths[b] (window 0: all of them):
+ *   s_t = scale * sum_i q[i] K_t[i],  o = sum_t e^(s_t - m) V_t / sum_t e^(s_t - m),
+ *   m = max_t s_t,  lse = m + ln sum_t e^(s_t - m)
+ * in f32 (a weight is rounded to 11 significant bits for bf16 outputs, 22 for f32), o
+ * rounded once to its type.  A sequence that sees nothing has o = 0 and lse = -infinity.
+ * Codes and scales outside the tokens seen are never used, whatever they hold.
+ *   q: device f32 or bf16 (q_dtype) (read): value i of head h of sequence b is element
+ *       b * q_row_stride + h * q_head_stride + i; rows start on 16 bytes.
+ *   q_heads: a multiple of the cache's heads, at most 16384.
+ *   pages: device int32[batch][max_pages] (read): page t / page_size of sequence b's
+ *       token t is pages[b][t / page_size].  Entries past a sequence's tokens are not
+ *       read.  A page outside the cache under a token seen makes that sequence's
+ *       outputs NaN; nothing outside the cache is read.
+ *   lengths: device int32[batch] (read).  Negative counts as 0, more than
+ *       max_pages * page_size as that.
+ *   out: device f32 or bf16 (out_dtype) [batch][q_heads][head_dim] (written), 16-byte
+ *       aligned.  lse: device f32[batch][q_heads] (written) or NULL.
+ *   workspace: device memory of qg_attn_decode_workspace_bytes bytes,
+ *       16-byte aligned, ZERO-FILLED before its first use and then left to the library,
+ *       on the device of the call.  One workspace serves any calls of that many bytes or
+ *       fewer one after another; calls that share one must not overlap in time.
+ *   batch <= 2^20; max_pages * page_size < 2^31.  scale is any f32.
+ *   Outputs must not overlap inputs, the workspace or each other (QG_ERR_SHAPE).
+ * Every sum is taken in an order that the sizes and lengths fix: results repeat bit for
+ * bit.
+ */
+QG_API int64_t qg_attn_decode_workspace_bytes(int64_t q_heads, int64_t heads, int64_t head_dim); /* -1: unsupported */
+QG_API qg_status qg_attn_decode(const qg_kv_cache *cache, const void *q, int64_t q_row_stride, int64_t q_head_stride,
+                                int q_dtype, int64_t batch, int64_t q_heads, const int32_t *pages, int64_t max_pages,
+                                const int32_t *lengths, float scale, int64_t window, void *out, int out_dtype,
+                                float *lse, void *workspace, int64_t workspace_bytes, qg_stream_t stream);
 
 #ifdef __cplusplus
 }

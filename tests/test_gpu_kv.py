@@ -1,0 +1,601 @@
+"""GPU parity of the key-value cache and its attention against the numpy oracle.
+
+Writing: codes and scales bit for bit (their f32 roundings are part of the definition).
+Reading: one f32 product, exact for Q8_0 (8 + 11 bits), then half a step of a bf16 output.
+
+Attention.  A score is a sum of dim products in up to 8 blocks: the tensor core's additions of
+a block (at most 8 of them, 2^-22 of the terms each, its own alignment), the split of q (2^-22), the blocks'
+additions and the scale's product (10 2^-24): within 2^-18 of the sum of |terms|.  A weight moves by what its score
+moves, by the exponent's own rounding (3 2^-24 of |s_t - m|, taken as 2^-22) and by 2^-20 for the exponential, the
+product with V's scale and the split to 22 bits; for bf16 outputs instead of the split one rounding to f16, 2^-11.
+Weights under 2^-29 of the largest lose bits below f16's range: 2^-36 of the largest, with room.  The sum over
+tokens has a depth of n / 64 steps of a warp, the warps' and the splits' sums (64 with room), 2^-24 each; the result is
+rounded once, by half a step of its type.
+"""
+
+import threading
+
+import numpy as np
+import pytest
+
+from oracle import kv as K
+from tests._gpu import Guarded, need_gpu
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def torch():
+    return need_gpu()
+
+
+@pytest.fixture(scope="module")
+def qg():
+    import block_quantized_decode_rmsnorm_gb300 as m
+
+    return m
+
+
+def types(torch):
+    return {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def dev(torch, a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def upload(torch, qg, c):
+    """An oracle cache on the device."""
+    code = torch.int8 if c["format"] == "q8_0" else torch.float8_e4m3fn
+    return qg.KVCache(*(dev(torch, c[n].view(np.uint8)).view(code) if n in "kv" else dev(torch, c[n])
+                        for n in ("k", "kd", "v", "vd")))
+
+
+def download(cache, fmt):
+    """The device cache as the oracle holds one."""
+    u8 = __import__("torch").uint8
+    q = np.int8 if fmt == "q8_0" else np.uint8
+    return {"format": fmt, "k": cache.k.view(u8).cpu().numpy().view(q), "kd": cache.k_scales.cpu().numpy(),
+            "v": cache.v.view(u8).cpu().numpy().view(q), "vd": cache.v_scales.cpu().numpy()}
+
+
+def random_cache(rng, fmt, pages, heads, page, dim, spread=0.5):
+    """Every code, scales over a few powers of two."""
+    c = {"format": fmt}
+    for n in "kv":
+        shape = (pages, heads, page, dim)
+        if fmt == "q8_0":
+            c[n] = rng.integers(-127, 128, shape, dtype=np.int8)
+            d = np.exp2(spread * rng.standard_normal((*shape[:3], dim // 32))) / 64
+            c[n + "d"] = d.astype(np.float16)
+        else:
+            c[n] = rng.integers(0, 256, shape, dtype=np.uint8)
+            c[n][(c[n] & 0x7F) == 0x7F] = 0x30
+            d = np.exp2(spread * rng.standard_normal((*shape[:3], K.blocks(dim, fmt)))) / 128
+            c[n + "d"] = d.astype(np.float32)
+    return c
+
+
+def tables(rng, lengths, page, pages, extra=1):
+    """Page tables of distinct pages in any order; entries past a sequence's tokens are garbage."""
+    held = [-(-max(n, 0) // page) for n in lengths]
+    pool = rng.permutation(pages)[: sum(held)]
+    t = np.full((len(lengths), max(held + [0]) + extra), 2 ** 31 - 1, np.int32)
+    i = 0
+    for b, n in enumerate(held):
+        t[b, :n] = pool[i: i + n]
+        i += n
+    return t
+
+
+FORMATS = ["q8_0", "e4m3"]
+DIMS = [64, 96, 128, 192, 256]
+
+
+# ---------------------------------------------------------------- write
+
+def check_write(torch, qg, fmt, kind, x, slots, pages, page, strides="packed"):
+    """x: numpy f32 [2, rows, heads, dim]; every slot of the cache is compared, the untouched ones too."""
+    rng = np.random.default_rng(9)
+    _, rows, heads, dim = x.shape
+    before = random_cache(rng, fmt, pages, heads, page, dim)
+    cache = upload(torch, qg, before)
+    t = torch.from_numpy(x).to(types(torch)[kind])
+    if strides == "packed":
+        k, v = t[0].cuda(), t[1].cuda()
+    elif strides == "stacked":  # parts of a stacked projection's rows
+        qkv = torch.full((rows, 4 * heads + 1, dim), float("nan"), dtype=t.dtype, device="cuda")
+        k, v = qkv[:, 2 * heads: 3 * heads], qkv[:, 3 * heads: 4 * heads]
+        k.copy_(t[0]), v.copy_(t[1])
+    else:  # heads outermost
+        k, v = (t[i].transpose(0, 1).contiguous().cuda().transpose(0, 1) for i in range(2))
+    qg.qg_kv_write(cache, k, v, dev(torch, np.asarray(slots, np.int64)))
+    got, want = download(cache, fmt), {n: a.copy() if n != "format" else a for n, a in before.items()}
+    xf = t.float().numpy()
+    for i, n in enumerate("kv"):
+        q, d = K.quantize(xf[i], fmt)
+        for r, s in enumerate(slots):
+            if 0 <= s < pages * page:
+                want[n][s // page, :, s % page], want[n + "d"][s // page, :, s % page] = q[r], d[r]
+    for n in ("k", "v"):
+        w, g = want[n], got[n]
+        if fmt == "e4m3":
+            nan = (w & 0x7F) == 0x7F
+            assert np.array_equal((g & 0x7F) == 0x7F, nan)
+            w, g = np.where(nan, 0, w), np.where(nan, 0, g)
+        assert np.array_equal(g, w), (n, np.argwhere(g != w)[:4])
+        assert np.array_equal(got[n + "d"], want[n + "d"], equal_nan=True), n
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("dim", DIMS)
+@pytest.mark.parametrize("rows,heads,page,strides", [(1, 1, 16, "packed"), (1, 2, 16, "stacked"), (5, 3, 48, "packed"),
+                                                     (70, 2, 64, "stacked"), (33, 7, 16, "heads"), (130, 1, 112, "heads")])
+def test_write(torch, qg, fmt, kind, dim, rows, heads, page, strides):
+    rng = np.random.default_rng(rows * 1000 + dim)
+    x = (rng.standard_normal((2, rows, heads, dim)) * np.exp(2 * rng.standard_normal((2, rows, heads, 1)))).astype(np.float32)
+    x[:, -1, :, : dim // 2] = 0
+    pages = -(-rows // page) + 3
+    slots = rng.permutation(pages * page)[:rows]
+    if rows > 4:
+        slots[1], slots[3] = -1, -(2 ** 40)
+    if rows > 8:
+        slots[6], slots[7], slots[8] = pages * page, 2 ** 32 + 5, 2 ** 62
+    check_write(torch, qg, fmt, kind, x, slots, pages, page, strides)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_write_many_rows(torch, qg, fmt):
+    """Enough rows for the form that takes several a thread, and an end inside its last group."""
+    rng = np.random.default_rng(3)
+    rows, heads, dim, page = 9999, 4, 128, 16
+    x = rng.standard_normal((2, rows, heads, dim)).astype(np.float32)
+    pages = -(-rows // page) + 1
+    check_write(torch, qg, fmt, "bf16", x, rng.permutation(pages * page)[:rows], pages, page, "stacked")
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_write_special_values(torch, qg, fmt, kind):
+    x = np.zeros((2, 8, 1, 128), np.float32)
+    x[:, 1, 0, 3] = np.float32(3.3e38)
+    x[:, 2, 0] = 1e-35
+    x[:, 3, 0, ::2] = 1e-40
+    x[:, 4, 0] = (np.arange(128) - 63.5)       # ties
+    x[:, 4, 0, ::32] = 127
+    x[:, 5, 0, 0], x[:, 5, 0, 1:] = 448, np.tile([0.5, 1.5, 2.5, 17, 19, 416, 432], 19)[:127]
+    x[:, 6, 0] = -0.0
+    x[:, 7, 0, 5] = 65504 * 127                # the largest binary16 scale
+    if fmt == "e4m3":
+        x[0, 0, 0, 7], x[1, 0, 0, 9] = np.nan, np.inf
+    check_write(torch, qg, fmt, kind, x, np.arange(8), 1, 16)
+
+
+def test_write_nothing(torch, qg):
+    cache = qg.KVCache.allocate(2, 16, 2, 64)
+    empty = torch.empty((0, 2, 64), device="cuda")
+    qg.qg_kv_write(cache, empty, empty, torch.empty(0, dtype=torch.int64, device="cuda"))
+    none = qg.KVCache.allocate(0, 16, 2, 64)
+    one = torch.ones((1, 2, 64), device="cuda")
+    qg.qg_kv_write(none, one, one, torch.zeros(1, dtype=torch.int64, device="cuda"))
+    k, v = qg.qg_kv_read(none, torch.zeros(1, dtype=torch.int64, device="cuda"))
+    assert not k.any() and not v.any()
+    o = qg.qg_attn_decode(one, none, torch.zeros((1, 0), dtype=torch.int32, device="cuda"),
+                          torch.full((1,), 5, dtype=torch.int32, device="cuda"))
+    assert not o.any()
+
+
+# ---------------------------------------------------------------- read
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("dim", DIMS)
+@pytest.mark.parametrize("rows,heads,page", [(1, 1, 16), (7, 3, 48), (65, 2, 64), (300, 5, 32)])
+def test_read(torch, qg, fmt, kind, dim, rows, heads, page):
+    rng = np.random.default_rng(rows * 100 + dim)
+    pages = 9
+    c = random_cache(rng, fmt, pages, heads, page, dim, spread=3.0)
+    slots = rng.integers(0, pages * page, rows)  # some of them more than once
+    if rows > 4:
+        slots[2], slots[3], slots[4] = -1, pages * page, 2 ** 33
+    out = [Guarded(torch, (rows, heads, dim), types(torch)[kind]) for _ in range(2)]
+    qg.qg_kv_read(upload(torch, qg, c), dev(torch, slots), None, out[0].view, out[1].view)
+    for o, n in zip(out, "kv"):
+        o.check()
+        want = K.rows(c, slots, n).astype(np.float32)  # the definition's rounding
+        got = o.view.float().cpu().numpy()
+        if kind == "bf16":
+            want = torch.from_numpy(want).bfloat16().float().numpy()
+        assert np.array_equal(got, want), np.argwhere(got != want)[:4]
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_read_many_rows(torch, qg, fmt):
+    rng = np.random.default_rng(4)
+    c = random_cache(rng, fmt, 40, 4, 16, 64)
+    slots = rng.integers(-5, 40 * 16, 30011)
+    k, v = qg.qg_kv_read(upload(torch, qg, c), dev(torch, slots))
+    assert k.dtype == torch.float32
+    assert np.array_equal(k.cpu().numpy(), K.rows(c, slots, "k").astype(np.float32))
+    assert np.array_equal(v.cpu().numpy(), K.rows(c, slots, "v").astype(np.float32))
+
+
+def test_read_special_scales(torch, qg):
+    """Infinite and NaN scales and e4m3's NaN codes come back as such."""
+    for fmt in FORMATS:
+        c = random_cache(np.random.default_rng(5), fmt, 1, 1, 16, 64)
+        c["kd"][0, 0, 1], c["kd"][0, 0, 2] = np.inf, np.nan
+        c["k"][0, 0, 1] = np.where(c["k"][0, 0, 1] == 0, 1, c["k"][0, 0, 1])
+        if fmt == "e4m3":
+            c["v"][0, 0, 3, 5] = 0xFF
+        k, v = qg.qg_kv_read(upload(torch, qg, c), torch.arange(16, device="cuda"))
+        for got, n in ((k, "k"), (v, "v")):
+            with np.errstate(all="ignore"):
+                want = K.rows(c, np.arange(16), n).astype(np.float32)
+            assert np.array_equal(got.cpu().numpy(), want, equal_nan=True)
+
+
+# ---------------------------------------------------------------- attention
+
+def bounds(part, n, out_bf16):
+    each = 2.0 ** -20 + (2.0 ** -11 if out_bf16 else 0.0) + (n / 64 + 64) * 2.0 ** -24
+    return K.moved(part, each, 2.0 ** -18, 2.0 ** -22, 2.0 ** -36)
+
+
+def assert_attention(got, got_lse, want, what=""):
+    """want: the oracle's (o, lse, parts); got a torch tensor."""
+    o, lse, parts = want
+    bf16 = "bfloat16" in str(got.dtype)
+    got = got.double().cpu().numpy()
+    assert np.isfinite(got).all(), what
+    for b, part in enumerate(parts):
+        if part is None:
+            assert not got[b].any(), (what, b)
+            assert got_lse is None or np.all(np.isneginf(got_lse[b].cpu().numpy())), (what, b)
+            continue
+        off, off_lse = bounds(part, part[0].shape[-1], bf16)
+        lim = off + (np.abs(o[b]) + off) * (2.0 ** -8 if bf16 else 2.0 ** -23) + 2.0 ** -133
+        err = np.abs(got[b] - o[b])
+        assert np.all(err <= lim), (what, b, np.argwhere(err > lim)[:4], float((err / lim).max()))
+        if got_lse is not None:
+            _, off_lse = bounds(part, part[0].shape[-1], False)
+            e = np.abs(got_lse[b].double().cpu().numpy() - lse[b])
+            lim = off_lse + 2.0 ** -21 * (1 + np.abs(lse[b]))
+            assert np.all(e <= lim), (what, b, float((e / lim).max()))
+
+
+def run_attention(torch, qg, fmt, dim, heads, group, page, lengths, window=0, kinds=("f32", "f32"), seed=0, scale=None,
+                  gain=1.0, lse=True, q_view="packed", spread=0.5):
+    rng = np.random.default_rng(seed + dim * 7 + heads * 31 + group * 101 + page)
+    pages = sum(-(-max(n, 0) // page) for n in lengths) + 2
+    c = random_cache(rng, fmt, pages, heads, page, dim, spread)
+    t = tables(rng, lengths, page, pages)
+    batch, hq = len(lengths), heads * group
+    q = torch.from_numpy((gain * rng.standard_normal((batch, hq, dim))).astype(np.float32)).to(types(torch)[kinds[0]])
+    scale64 = dim ** -0.5 if scale is None else float(np.float32(scale))
+    want = K.attention(q.float().numpy(), c, t, lengths, float(np.float32(scale64)), window)
+    qd = q.cuda()
+    if q_view == "stacked":
+        qkv = torch.full((batch, hq + 2 * heads, dim), float("nan"), dtype=q.dtype, device="cuda")
+        qkv[:, :hq] = qd
+        qd = qkv[:, :hq]
+    elif q_view == "heads":
+        qd = qd.transpose(0, 1).contiguous().transpose(0, 1)
+    cache, td, ld = upload(torch, qg, c), dev(torch, t), dev(torch, np.asarray(lengths, np.int32))
+    out = Guarded(torch, (batch, hq, dim), types(torch)[kinds[1]])
+    ls = Guarded(torch, (batch, hq), torch.float32) if lse else None
+    work = qg.AttnWork.allocate(hq, heads, dim)
+    got = qg.qg_attn_decode(qd, cache, td, ld, scale, window, out=out.view, lse=ls.view if lse else None, work=work)
+    out.check()
+    if lse:
+        ls.check()
+    assert_attention(got, ls.view if lse else None, want, (fmt, dim, heads, group, page, lengths, window, kinds))
+    # the same bits again, from the same workspace and from a new one
+    a = qg.qg_attn_decode(qd, cache, td, ld, scale, window, out_dtype=types(torch)[kinds[1]], work=work)
+    b = qg.qg_attn_decode(qd, cache, td, ld, scale, window, out_dtype=types(torch)[kinds[1]])
+    assert torch.equal(a, got) and torch.equal(b, got)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dim", DIMS)
+@pytest.mark.parametrize("group", [1, 2, 3, 8, 9, 16, 17, 40])
+def test_attention_heads(torch, qg, fmt, dim, group):
+    run_attention(torch, qg, fmt, dim, 2, group, 16, [77, 1, 200], kinds=("bf16", "f32") if group % 2 else ("f32", "bf16"))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("kinds", [("f32", "f32"), ("bf16", "bf16")])
+@pytest.mark.parametrize("lengths", [[1], [2], [15], [16], [17], [31, 32, 33], [63, 64, 65], [127, 128, 129], [0], [0, 0, 5, 0],
+                                     [1000], [4097], [9000, 1, 0, 300, 12], [-3, 7, -2 ** 31]])
+def test_attention_lengths(torch, qg, fmt, kinds, lengths):
+    run_attention(torch, qg, fmt, 128, 2, 4, 16, lengths, kinds=kinds)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("page", [16, 32, 48, 80, 128, 256, 4096])
+def test_attention_pages(torch, qg, fmt, page):
+    run_attention(torch, qg, fmt, 64, 3, 2, page, [500, 33, 0, 777], q_view="stacked")
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("window", [1, 7, 16, 17, 100, 128, 700, 10 ** 6, 2 ** 62])
+def test_attention_window(torch, qg, fmt, dim, window):
+    run_attention(torch, qg, fmt, dim, 2, 3, 48, [900, 16, 0, 1, 129, 640], window=window, q_view="heads")
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_attention_many_sequences(torch, qg, fmt):
+    """More sequences than CTAs, most of them short, some empty; heads of one sequence on several CTAs."""
+    rng = np.random.default_rng(11)
+    lengths = [int(n) for n in rng.integers(0, 60, 700)]
+    lengths[100], lengths[699] = 1500, 0
+    run_attention(torch, qg, fmt, 64, 2, 2, 16, lengths, kinds=("bf16", "bf16"))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("heads", [1, 5, 24])
+def test_attention_long(torch, qg, fmt, heads):
+    run_attention(torch, qg, fmt, 128, heads, 2, 64, [30011 // heads * 2, 5], kinds=("f32", "f32"))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("gain,scale", [(0.0, None), (1e-20, None), (30.0, None), (1.0, 0.0), (1.0, -0.2), (1e6, 1e-7), (1.0, 3.0)])
+def test_attention_scores(torch, qg, fmt, gain, scale):
+    """Flat and peaked softmaxes, small and large queries, odd scales."""
+    run_attention(torch, qg, fmt, 128, 2, 4, 32, [300, 65], gain=gain, scale=scale)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_attention_scales_far_apart(torch, qg, fmt):
+    """Tokens whose values' scales differ by many powers of two: none is lost to the weights' 16 bits."""
+    run_attention(torch, qg, fmt, 128, 2, 4, 32, [300, 65], spread=4.0, gain=0.01)
+    run_attention(torch, qg, fmt, 128, 2, 4, 32, [300, 65], spread=4.0, gain=0.01, kinds=("bf16", "bf16"))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dim", [96, 128])
+@pytest.mark.parametrize("n,window", [(0, 0), (1, 0), (37, 0), (130, 0), (200, 50), (300, 130)])
+def test_attention_ignores_what_is_not_seen(torch, qg, fmt, dim, n, window):
+    """NaN and infinite scales and NaN codes in every token outside the ones seen, in all pages."""
+    rng = np.random.default_rng(n + 5)
+    page, heads, group = 48, 2, 3
+    pages = 12
+    c = random_cache(rng, fmt, pages, heads, page, dim)
+    t = tables(rng, [n], page, pages)
+    seen = np.zeros((pages, page), bool)
+    for i in range(max(0, n - window) if window else 0, n):
+        seen[t[0, i // page], i % page] = True
+    for name in "kv":
+        hidden = np.broadcast_to(~seen[:, None, :], (pages, heads, page))
+        c[name + "d"][hidden] = rng.choice(np.array([np.nan, np.inf, -np.inf], c[name + "d"].dtype), c[name + "d"][hidden].shape)
+        c[name][hidden] = -128 if fmt == "q8_0" else 0x7F
+    q = rng.standard_normal((1, heads * group, dim)).astype(np.float32)
+    t[t == 2 ** 31 - 1] = rng.choice([-1, 2 ** 31 - 1, pages, -2 ** 31])
+    if window:
+        t[0, : (n - window) // page] = -7  # pages given back
+    want = K.attention(q, c, np.where((t < 0) | (t >= pages), 0, t), [n], float(np.float32(dim ** -0.5)), window)
+    lse = torch.empty((1, heads * group), device="cuda")
+    got = qg.qg_attn_decode(dev(torch, q), upload(torch, qg, c), dev(torch, t), dev(torch, np.array([n], np.int32)),
+                            window=window, lse=lse)
+    assert_attention(got, lse, want)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("bad", [-1, 20, 2 ** 31 - 1, -2 ** 31])
+def test_attention_bad_page(torch, qg, fmt, bad):
+    """A page outside the cache makes its sequence NaN and leaves the others alone."""
+    rng = np.random.default_rng(6)
+    lengths, page, heads, group, dim, pages = [100, 300, 40], 16, 2, 2, 64, 32
+    c = random_cache(rng, fmt, pages, heads, page, dim)
+    t = tables(rng, lengths, page, pages)
+    q = rng.standard_normal((3, 4, dim)).astype(np.float32)
+    want = K.attention(q, c, t, lengths, dim ** -0.5)
+    if bad == 20:
+        bad = pages
+    t[1, 7] = bad
+    lse = torch.empty((3, 4), device="cuda")
+    got = qg.qg_attn_decode(dev(torch, q), upload(torch, qg, c), dev(torch, t), dev(torch, np.array(lengths, np.int32)), lse=lse)
+    assert torch.isnan(got[1]).all() and torch.isnan(lse[1]).all()
+    keep = [0, 2]
+    assert_attention(got[keep], lse[keep], (want[0][keep], want[1][keep], [want[2][i] for i in keep]))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_attention_nan_of_a_token_seen(torch, qg, fmt):
+    """NaN in a seen token's value reaches the dimensions that it has a part in, in its key all of them."""
+    rng = np.random.default_rng(7)
+    c = random_cache(rng, fmt, 8, 1, 16, 128)
+    t = tables(rng, [100, 20], 16, 8)
+    q = rng.standard_normal((2, 2, 128)).astype(np.float32)
+    p, off = t[0, 50 // 16], 50 % 16
+    if fmt == "q8_0":
+        c["vd"][p, 0, off, 1] = np.nan
+    else:
+        c["v"][p, 0, off, 40] = 0x7F
+    args = dev(torch, t), dev(torch, np.array([100, 20], np.int32))
+    got = qg.qg_attn_decode(dev(torch, q), upload(torch, qg, c), *args)
+    bad = torch.isnan(got[0]).all(dim=0)
+    assert bool(bad[40]) and torch.isfinite(got[1]).all()
+    if fmt == "q8_0":
+        assert torch.equal(bad.cpu(), torch.arange(128) // 32 == 1) and not torch.isnan(got[0][:, ~bad]).any()
+    c["kd"][p, 0, off] = np.nan
+    got = qg.qg_attn_decode(dev(torch, q), upload(torch, qg, c), *args)
+    assert torch.isnan(got[0]).all() and torch.isfinite(got[1]).all()
+
+
+def test_attention_length_beyond_the_table(torch, qg):
+    """A length beyond what the page table holds counts as that."""
+    rng = np.random.default_rng(8)
+    c = random_cache(rng, "q8_0", 4, 1, 16, 64)
+    t = np.array([[2, 0, 3]], np.int32)
+    q = rng.standard_normal((1, 1, 64)).astype(np.float32)
+    want = K.attention(q, c, t, [48], 0.125)
+    cache = upload(torch, qg, c)
+    for n in (48, 49, 2 ** 31 - 1):
+        assert_attention(qg.qg_attn_decode(dev(torch, q), cache, dev(torch, t), dev(torch, np.array([n], np.int32))), None, want)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_far_offsets(torch, qg, fmt):
+    """Pages whose codes lie past 2^32 bytes of their plane: written, read and attended to."""
+    heads, page, dim = 8, 64, 128
+    pages = (1 << 32) // (heads * page * dim) + 9
+    cache = qg.KVCache.allocate(pages, page, heads, dim, format=fmt)
+    rng = np.random.default_rng(10)
+    n = 200
+    t = np.array([[pages - 1, 0, pages - 5, pages - 2]], np.int32)
+    slots = t[0, np.arange(n) // page].astype(np.int64) * page + np.arange(n) % page
+    x = rng.standard_normal((2, n, heads, dim)).astype(np.float32)
+    qg.qg_kv_write(cache, dev(torch, x[0]), dev(torch, x[1]), dev(torch, slots))
+    k, v = qg.qg_kv_read(cache, dev(torch, slots))
+    small = {"format": fmt}
+    for i, name in enumerate("kv"):
+        q, d = K.quantize(x[i], fmt)
+        assert np.array_equal((k, v)[i].cpu().numpy(), K.values(q, d, fmt).astype(np.float32))
+        pad = 4 * page - n
+        small[name] = np.concatenate([q, np.zeros((pad, heads, dim), q.dtype)]).reshape(4, page, heads, dim).swapaxes(1, 2)
+        small[name + "d"] = np.concatenate([d, np.zeros((pad, *d.shape[1:]), d.dtype)]).reshape(4, page, heads, -1).swapaxes(1, 2)
+    q = rng.standard_normal((1, heads, dim)).astype(np.float32)
+    want = K.attention(q, small, np.arange(4, dtype=np.int32)[None], [n], float(np.float32(dim ** -0.5)))
+    assert_attention(qg.qg_attn_decode(dev(torch, q), cache, dev(torch, t), dev(torch, np.array([n], np.int32))), None, want)
+
+
+# ---------------------------------------------------------------- used together
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_decode_steps(torch, qg, fmt):
+    """A prompt written at once, then tokens one by one, as a captured step that is replayed: the new
+    token's slot and the lengths advance on the device."""
+    rng = np.random.default_rng(12)
+    batch, heads, group, dim, page, prompt, steps = 3, 2, 4, 128, 16, [30, 5, 47], 6
+    cache = qg.KVCache.allocate(24, page, heads, dim, format=fmt)
+    work = qg.AttnWork.allocate(heads * group, heads, dim)
+    t = rng.permutation(24)[: batch * 5].reshape(batch, 5).astype(np.int32)
+    slot = lambda b, i: int(t[b, i // page]) * page + i % page
+    history = [rng.standard_normal((2, n, heads, dim)).astype(np.float32) for n in prompt]
+    flat = np.concatenate(history, axis=1)
+    qg.qg_kv_write(cache, dev(torch, flat[0]), dev(torch, flat[1]),
+                   dev(torch, np.array([slot(b, i) for b in range(batch) for i in range(prompt[b])], np.int64)))
+    qkv = torch.zeros((batch, heads * (group + 2), dim), dtype=torch.bfloat16, device="cuda")
+    q, k, v = qkv[:, : heads * group], qkv[:, heads * group: heads * (group + 1)], qkv[:, heads * (group + 1):]
+    td, ld = dev(torch, t), dev(torch, np.array(prompt, np.int32))
+    out = torch.empty((batch, heads * group, dim), dtype=torch.bfloat16, device="cuda")
+
+    def step():
+        at = ld.long()
+        slots = td.gather(1, (at // page)[:, None])[:, 0].long() * page + at % page
+        ld.add_(1)
+        qg.qg_kv_write(cache, k, v, slots)
+        qg.qg_attn_decode(q, cache, td, ld, out=out, work=work)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()  # a first run of every kernel outside the capture; its token is written again below
+        ld.sub_(1)
+    torch.cuda.current_stream().wait_stream(s)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for i in range(steps):
+        x = torch.from_numpy(rng.standard_normal(qkv.shape).astype(np.float32)).bfloat16()
+        qkv.copy_(x)
+        g.replay()
+        x = x.float().numpy()
+        for b in range(batch):
+            new = np.stack([x[b, heads * group: heads * (group + 1)], x[b, heads * (group + 1):]])[:, None]
+            history[b] = np.concatenate([history[b], new], axis=1)
+        pages_of = {"format": fmt}
+        for j, name in enumerate("kv"):
+            q8, d8 = zip(*(K.quantize(h[j], fmt) for h in history))
+            pages_of[name] = np.zeros((24, heads, page, dim), q8[0].dtype)
+            pages_of[name + "d"] = np.zeros((24, heads, page, d8[0].shape[-1]), d8[0].dtype)
+            for b in range(batch):
+                for n in range(q8[b].shape[0]):
+                    p, o = divmod(slot(b, n), page)
+                    pages_of[name][p, :, o], pages_of[name + "d"][p, :, o] = q8[b][n], d8[b][n]
+        lengths = [n + i + 1 for n in prompt]
+        assert ld.tolist() == lengths
+        want = K.attention(x[:, : heads * group], pages_of, t, lengths, float(np.float32(dim ** -0.5)))
+        assert_attention(out, None, want, i)
+
+
+def test_two_streams_and_threads(torch, qg):
+    """Calls at once on streams of their own, each with its own workspace, against calls one by one."""
+    rng = np.random.default_rng(13)
+    c = random_cache(rng, "q8_0", 400, 2, 16, 128)
+    cache = upload(torch, qg, c)
+    t = dev(torch, rng.permutation(400)[:384].reshape(4, 96).astype(np.int32))
+    n = dev(torch, np.array([1500, 1, 700, 1536], np.int32))
+    qs = [torch.randn((4, 8, 128), device="cuda") for _ in range(4)]
+    alone = [qg.qg_attn_decode(q, cache, t, n) for q in qs]
+    torch.cuda.synchronize()
+    got, failed = [None] * 4, []
+
+    def work(i):
+        try:
+            s = torch.cuda.Stream()
+            w = qg.AttnWork.allocate(8, 2, 128)
+            torch.cuda.synchronize()
+            for _ in range(50):
+                got[i] = qg.qg_attn_decode(qs[i], cache, t, n, work=w, stream=s)
+            s.synchronize()
+        except Exception as e:  # shown by the assertion below
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    [x.start() for x in threads], [x.join() for x in threads]
+    assert not failed and all(torch.equal(a, b) for a, b in zip(got, alone))
+
+
+def test_one_workspace_for_several_shapes(torch, qg):
+    """A workspace of the largest need serves smaller calls in turn, and is left zeroed where it has to be."""
+    work = qg.AttnWork.allocate(32, 2, 256)
+    rng = np.random.default_rng(14)
+    first = None
+    for rounds in range(2):
+        for dim, heads, group, lengths in [(256, 2, 16, [3000, 40]), (64, 4, 1, [5000, 0, 7]), (128, 1, 8, [20000]), (96, 2, 3, [1] * 300)]:
+            rng = np.random.default_rng(dim)
+            pages = sum(-(-x // 16) for x in lengths) + 1
+            c = random_cache(rng, "e4m3", pages, heads, 16, dim)
+            t = tables(rng, lengths, 16, pages)
+            q = rng.standard_normal((len(lengths), heads * group, dim)).astype(np.float32)
+            args = dev(torch, q), upload(torch, qg, c), dev(torch, t), dev(torch, np.array(lengths, np.int32))
+            assert torch.equal(qg.qg_attn_decode(*args, work=work), qg.qg_attn_decode(*args))
+
+
+def test_binding_refusals(torch, qg):
+    cache = qg.KVCache.allocate(4, 16, 2, 64)
+    x, slots = torch.zeros((3, 2, 64), device="cuda"), torch.arange(3, device="cuda")
+    pages, n = torch.zeros((3, 2), dtype=torch.int32, device="cuda"), torch.ones(3, dtype=torch.int32, device="cuda")
+    work = qg.AttnWork.allocate(2, 2, 64)
+    for bad in (lambda: qg.qg_kv_write(cache, x[:, :1], x, slots), lambda: qg.qg_kv_write(cache, x, x[:2], slots),
+                lambda: qg.qg_kv_write(cache, x, x.bfloat16(), slots), lambda: qg.qg_kv_write(cache, x, x, slots.int()),
+                lambda: qg.qg_kv_write(cache, x, x, slots[:2]), lambda: qg.qg_kv_write(cache, x.half(), x.half(), slots),
+                lambda: qg.qg_kv_write(cache, torch.zeros((3, 64, 2), device="cuda").transpose(1, 2), x, slots),
+                lambda: qg.qg_kv_write(qg.KVCache(cache.k, cache.k_scales.float(), cache.v, cache.v_scales), x, x, slots),
+                lambda: qg.qg_kv_write(qg.KVCache(cache.k[:, :, ::2], cache.k_scales, cache.v, cache.v_scales), x, x, slots),
+                lambda: qg.qg_kv_write(qg.KVCache(cache.k.short(), cache.k_scales, cache.v, cache.v_scales), x, x, slots),
+                lambda: qg.qg_kv_read(cache, slots.int()), lambda: qg.qg_kv_read(cache, slots[None]),
+                lambda: qg.qg_kv_read(cache, slots, torch.float32, x.bfloat16(), x.bfloat16()),
+                lambda: qg.qg_kv_read(cache, slots, None, x[:2], x), lambda: qg.qg_kv_read(cache, slots, torch.float16),
+                lambda: qg.qg_attn_decode(x[:, :1], cache, pages, n), lambda: qg.qg_attn_decode(x[0], cache, pages, n),
+                lambda: qg.qg_attn_decode(x, cache, pages[:2], n), lambda: qg.qg_attn_decode(x, cache, pages.long(), n),
+                lambda: qg.qg_attn_decode(x, cache, pages, n[:2]), lambda: qg.qg_attn_decode(x, cache, pages, n.long()),
+                lambda: qg.qg_attn_decode(x, cache, pages, n, out=x[:2]), lambda: qg.qg_attn_decode(x, cache, pages, n, out_dtype=torch.half),
+                lambda: qg.qg_attn_decode(x, cache, pages, n, lse=x[:, :, 0]), lambda: qg.qg_attn_decode(x, cache, pages, n, scale="a"),
+                lambda: qg.qg_attn_decode(x, cache, pages.t().contiguous().t(), n),
+                lambda: qg.qg_attn_decode(x, cache, pages, n, work=qg.AttnWork(work.buf.int()))):
+        with pytest.raises((ValueError, TypeError)):
+            bad()
+    from block_quantized_decode_rmsnorm_gb300._lib import QGError
+
+    for bad in (lambda: qg.qg_attn_decode(x, cache, pages, n, window=-1), lambda: qg.qg_attn_decode(x, cache, pages, n, out=x),
+                lambda: qg.qg_attn_decode(x, cache, pages, n, work=qg.AttnWork(work.buf[:-16])),
+                lambda: qg.qg_kv_read(cache, slots, None, x, x),
+                lambda: qg.qg_kv_write(cache, torch.zeros(3 * 2 * 64 + 1, device="cuda")[1:].view(3, 2, 64), x, slots)):
+        with pytest.raises(QGError):
+            bad()
+    torch.cuda.synchronize()
