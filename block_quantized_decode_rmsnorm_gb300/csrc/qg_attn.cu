@@ -1,133 +1,84 @@
-// Attention of one new token per sequence over the paged cache (plain form: a CTA to
-// each sequence and query head, a warp to each token, one pass with a running maximum).
-#include <cfloat>
-
-#include "qg_kv.cuh"
+// Decode attention: the workspace and the choice of kernel (qg_attn.cuh).
+#include "qg_attn.cuh"
 
 namespace qg {
 
-struct AttnArgs {
-    KvPlanes c;
-    const void *q;
-    int64_t q_row, q_head;
-    int q_bf16, group, q_heads;
-    const int32_t *pages, *lengths;
-    int64_t max_pages, window;
-    float scale;
-    void *out;
-    int out_bf16;
-    float *lse;
+namespace {
+
+struct Sizes {
+    int ctas, record, heads, unit;  // CTAs per SM, floats of a record, query heads and tokens to a unit
 };
 
-constexpr int AW = 4;
-
 template <bool E4M3, int D>
-__global__ void __launch_bounds__(32 * AW) attn_plain_kernel(AttnArgs a)
+Sizes sizes_of(int64_t group)
 {
-    constexpr int N = D / 32, NB = kv_blocks(E4M3, D), BLOCK = E4M3 ? EB : QK;
-    __shared__ float part[AW][D + 2];
-    pdl_wait();
-    pdl_trigger();
-    const int b = blockIdx.y, hq = blockIdx.x, h = hq / a.group, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t held = a.max_pages * a.c.page;
-    const int64_t n = min(static_cast<int64_t>(max(a.lengths[b], 0)), held);
-    const int64_t first = a.window > 0 ? max(n - a.window, int64_t(0)) : 0;
-    float q[N], acc[N], m = -FLT_MAX, l = 0.0f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int64_t at = b * a.q_row + hq * a.q_head + lane + 32 * i;
-        q[i] = a.q_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(a.q)[at])
-                        : static_cast<const float *>(a.q)[at];
-        acc[i] = 0.0f;
-    }
-    for (int64_t t = first + warp; t < n; t += AW) {
-        const int32_t page = a.pages[b * a.max_pages + t / a.c.page];
-        const bool there = page >= 0 && page < a.c.n_pages;
-        const int64_t at = (static_cast<int64_t>(there ? page : 0) * a.c.heads + h) * a.c.page + t % a.c.page;
-        float s = 0.0f, v[N];
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int col = lane + 32 * i;
-            float kk = 0.0f;
-            v[i] = 0.0f;
-            if (there) {
-                const uint8_t ck = a.c.kq[at * D + col], cv = a.c.vq[at * D + col];
-                const int64_t blk = at * NB + col / BLOCK;
-                if (E4M3) {
-                    kk = __half2float(__half(__nv_cvt_fp8_to_halfraw(ck, __NV_E4M3))) * static_cast<const float *>(a.c.kd)[blk];
-                    v[i] = __half2float(__half(__nv_cvt_fp8_to_halfraw(cv, __NV_E4M3))) * static_cast<const float *>(a.c.vd)[blk];
-                } else {
-                    kk = static_cast<float>(static_cast<int8_t>(ck)) * h2f(static_cast<const uint16_t *>(a.c.kd)[blk]);
-                    v[i] = static_cast<float>(static_cast<int8_t>(cv)) * h2f(static_cast<const uint16_t *>(a.c.vd)[blk]);
-                }
-            }
-            s = fmaf(q[i], kk, s);
-        }
-        s = there ? warp_sum(s) * a.scale : __int_as_float(0x7fffffff);
-        const float top = fmaxf(m, s), f = expf(m - top), p = expf(s - top);
-        m = top;
-        l = fmaf(l, f, p);
-#pragma unroll
-        for (int i = 0; i < N; ++i) acc[i] = fmaf(acc[i], f, p * v[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i) part[warp][lane + 32 * i] = acc[i];
-    if (lane == 0) part[warp][D] = m, part[warp][D + 1] = l;
-    __syncthreads();
-    float top = -FLT_MAX, total = 0.0f;
-    for (int w = 0; w < AW; ++w) top = fmaxf(top, part[w][D]);
-    for (int w = 0; w < AW; ++w) total = fmaf(part[w][D + 1], expf(part[w][D] - top), total);
-    const bool none = first >= n;
-    for (int col = threadIdx.x; col < D; col += 32 * AW) {
-        float o = 0.0f;
-        for (int w = 0; w < AW; ++w) o = fmaf(part[w][col], expf(part[w][D] - top), o);
-        o = none ? 0.0f : o / total;
-        const int64_t at = (static_cast<int64_t>(b) * a.q_heads + hq) * D + col;
-        if (a.out_bf16)
-            static_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(o);
-        else
-            static_cast<float *>(a.out)[at] = o;
-    }
-    if (threadIdx.x == 0 && a.lse)
-        a.lse[static_cast<int64_t>(b) * a.q_heads + hq] = none ? -__int_as_float(0x7f800000) : top + logf(total);
+    using One = AttnShape<E4M3, D, 1>;
+    using Two = AttnShape<E4M3, D, 2>;
+    if (group <= 8) return {One::CTAS, One::RECORD, One::HEADS, One::TOK * AT_WARPS};
+    return {Two::CTAS, Two::RECORD, Two::HEADS, Two::TOK * AT_WARPS};
 }
 
-int64_t attn_workspace_bytes(int64_t, int64_t, int64_t) { return 16; }
-
-namespace {
 template <bool E4M3>
-cudaError_t plain(const AttnArgs &a, dim3 grid, cudaStream_t st)
+Sizes sizes_for(int64_t dim, int64_t group)
+{
+    switch (dim) {
+    case 64: return sizes_of<E4M3, 64>(group);
+    case 96: return sizes_of<E4M3, 96>(group);
+    case 128: return sizes_of<E4M3, 128>(group);
+    case 192: return sizes_of<E4M3, 192>(group);
+    default: return sizes_of<E4M3, 256>(group);
+    }
+}
+
+int64_t counter_bytes() { return (static_cast<int64_t>(num_sms()) * AT_CTAS_MAX * 4 + 255) / 256 * 256; }
+
+template <bool E4M3>
+cudaError_t launch_for(const AttnArgs &a, int64_t most, cudaStream_t st)
 {
     switch (a.c.dim) {
-    case 64: return launch_pdl(attn_plain_kernel<E4M3, 64>, grid, dim3(32 * AW), 0, st, a);
-    case 96: return launch_pdl(attn_plain_kernel<E4M3, 96>, grid, dim3(32 * AW), 0, st, a);
-    case 128: return launch_pdl(attn_plain_kernel<E4M3, 128>, grid, dim3(32 * AW), 0, st, a);
-    case 192: return launch_pdl(attn_plain_kernel<E4M3, 192>, grid, dim3(32 * AW), 0, st, a);
-    default: return launch_pdl(attn_plain_kernel<E4M3, 256>, grid, dim3(32 * AW), 0, st, a);
+    case 64: return launch_attn_dim<E4M3, 64>(a, most, st);
+    case 96: return launch_attn_dim<E4M3, 96>(a, most, st);
+    case 128: return launch_attn_dim<E4M3, 128>(a, most, st);
+    case 192: return launch_attn_dim<E4M3, 192>(a, most, st);
+    default: return launch_attn_dim<E4M3, 256>(a, most, st);
     }
 }
+
 }  // namespace
+
+// Counters, then two records for every CTA that the larger of the two formats' kernels has.
+int64_t attn_workspace_bytes(int64_t q_heads, int64_t heads, int64_t dim)
+{
+    const Sizes a = sizes_for<false>(dim, q_heads / heads), b = sizes_for<true>(dim, q_heads / heads);
+    const int64_t floats = a.ctas > b.ctas ? static_cast<int64_t>(a.ctas) * a.record : static_cast<int64_t>(b.ctas) * b.record;
+    return counter_bytes() + num_sms() * floats * 2 * 4;
+}
 
 cudaError_t launch_attn_decode(const KvPlanes &c, const void *q, int64_t q_row, int64_t q_head, int q_dtype,
                                int64_t batch, int64_t q_heads, const int32_t *pages, int64_t max_pages,
                                const int32_t *lengths, float scale, int64_t window, void *out, int out_dtype,
-                               float *lse, void *, cudaStream_t st)
+                               float *lse, void *workspace, cudaStream_t st)
 {
-    const AttnArgs a = {c, q, q_row, q_head, q_dtype == QG_BF16, static_cast<int>(q_heads / c.heads),
-                        static_cast<int>(q_heads), pages, lengths, max_pages, window, scale, out,
-                        out_dtype == QG_BF16, lse};
-    for (int64_t b = 0; b < batch; b += 32768) {
-        AttnArgs part = a;
-        const int64_t n = batch - b < 32768 ? batch - b : 32768;
-        part.q = static_cast<const char *>(q) + b * q_row * (a.q_bf16 ? 2 : 4);
-        part.pages = pages + b * max_pages;
-        part.lengths = lengths + b;
-        part.out = static_cast<char *>(out) + b * q_heads * c.dim * (a.out_bf16 ? 2 : 4);
-        part.lse = lse ? lse + b * q_heads : nullptr;
-        const dim3 grid(static_cast<unsigned>(q_heads), static_cast<unsigned>(n));
-        if (cudaError_t e = c.e4m3 ? plain<true>(part, grid, st) : plain<false>(part, grid, st); e != cudaSuccess) return e;
-    }
-    return cudaSuccess;
+    const int64_t group = q_heads / c.heads;
+    const Sizes s = c.e4m3 ? sizes_for<true>(c.dim, group) : sizes_for<false>(c.dim, group);
+    int shift = -1;
+    for (int i = 4; i <= 12; ++i)
+        if (c.page == 1 << i) shift = i;
+    AttnArgs a = {};
+    a.c = c;
+    a.q = q, a.q_row = q_row, a.q_head = q_head, a.q_bf16 = q_dtype == QG_BF16;
+    a.group = static_cast<int>(group), a.q_heads = static_cast<int>(q_heads);
+    a.chunks = static_cast<int>((group + s.heads - 1) / s.heads);
+    a.page_shift = shift;
+    a.batch = batch, a.pages = pages, a.lengths = lengths, a.max_pages = max_pages, a.window = window, a.scale = scale;
+    a.out = out, a.out_bf16 = out_dtype == QG_BF16, a.lse = lse;
+    a.counters = static_cast<int *>(workspace);
+    a.records = reinterpret_cast<float *>(static_cast<char *>(workspace) + counter_bytes());
+    // the units that there can be: the page tables' width, or a window that may begin inside a step
+    int64_t tokens = max_pages * c.page;
+    if (window > 0 && window < tokens) tokens = window + s.unit;
+    const int64_t most = batch * c.heads * a.chunks * ((tokens + s.unit - 1) / s.unit);
+    return c.e4m3 ? launch_for<true>(a, most, st) : launch_for<false>(a, most, st);
 }
 
 }  // namespace qg

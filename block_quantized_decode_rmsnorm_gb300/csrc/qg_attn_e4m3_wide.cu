@@ -1,0 +1,7 @@
+// Decode attention over a e4m3 cache: heads of 192 and 256 values.
+#include "qg_attn.cuh"
+
+namespace qg {
+QG_ATTN_DIM(true, 192)
+QG_ATTN_DIM(true, 256)
+}  // namespace qg
