@@ -86,6 +86,7 @@ cudaError_t launch_kv_write(const KvPlanes &, const void *, int64_t, int64_t, co
                             const int64_t *, int64_t, cudaStream_t);
 cudaError_t launch_kv_read(const KvPlanes &, const int64_t *, int64_t, void *, void *, int, cudaStream_t);
 int64_t attn_workspace_bytes(int64_t q_heads, int64_t heads, int64_t dim);
+int64_t attn_most_places(const KvPlanes &, int64_t batch, int64_t q_heads, int64_t max_pages, int64_t window);
 cudaError_t launch_attn_decode(const KvPlanes &, const void *, int64_t, int64_t, int, int64_t, int64_t, const int32_t *,
                                int64_t, const int32_t *, float, int64_t, void *, int, float *, void *, cudaStream_t);
 
@@ -797,6 +798,7 @@ constexpr int64_t kKvMaxRows = INT32_MAX;
 constexpr int32_t kKvMaxHeads = 1024;
 constexpr int64_t kAttnMaxBatch = int64_t(1) << 20;
 constexpr int64_t kAttnMaxHeads = 16384;
+constexpr int64_t kAttnMaxPlaces = int64_t(1) << 37;  // a CTA of 64 or more counts its part in 32 bits
 
 bool kv_dim_ok(int64_t d) { return d == 64 || d == 96 || d == 128 || d == 192 || d == 256; }
 
@@ -914,6 +916,7 @@ qg_status qg_attn_decode(const qg_kv_cache *cache, const void *q, int64_t q_row_
     const int64_t wb = qg_attn_decode_workspace_bytes(q_heads, c.heads, c.dim);
     if (workspace_bytes < wb) return QG_ERR_SHAPE;
     const int64_t rows = batch * q_heads;
+    if (qg::attn_most_places(c, batch, q_heads, max_pages, window) > kAttnMaxPlaces) return QG_ERR_UNSUPPORTED;
     const Span outs[] = {{out, rows * c.dim * dtype_size(out_dtype)}, {lse, rows * 4}, {workspace, wb}},
                in[] = {{q, qn * e}, {pages, batch * max_pages * 4}, {lengths, batch * 4}, {c.kq, cb}, {c.vq, cb},
                        {c.kd, sb}, {c.vd, sb}};

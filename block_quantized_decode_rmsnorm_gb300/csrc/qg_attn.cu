@@ -6,7 +6,7 @@ namespace qg {
 namespace {
 
 struct Sizes {
-    int ctas, record, heads, unit;  // CTAs per SM, floats of a record, query heads and tokens to a unit
+    int ctas, record, heads, unit, cost;  // CTAs per SM, floats of a record, query heads and tokens to a unit, an item's cost in units
 };
 
 template <bool E4M3, int D>
@@ -14,8 +14,8 @@ Sizes sizes_of(int64_t group)
 {
     using One = AttnShape<E4M3, D, 1>;
     using Two = AttnShape<E4M3, D, 2>;
-    if (group <= 8) return {One::CTAS, One::RECORD, One::HEADS, One::TOK * AT_WARPS};
-    return {Two::CTAS, Two::RECORD, Two::HEADS, Two::TOK * AT_WARPS};
+    if (group <= 8) return {One::CTAS, One::RECORD, One::HEADS, One::TOK * AT_WARPS, One::COST};
+    return {Two::CTAS, Two::RECORD, Two::HEADS, Two::TOK * AT_WARPS, Two::COST};
 }
 
 template <bool E4M3>
@@ -54,6 +54,16 @@ int64_t attn_workspace_bytes(int64_t q_heads, int64_t heads, int64_t dim)
     return counter_bytes() + num_sms() * floats * 2 * 4;
 }
 
+// The places that the line can have: by the page tables' width, or a window that may begin inside a step.
+int64_t attn_most_places(const KvPlanes &c, int64_t batch, int64_t q_heads, int64_t max_pages, int64_t window)
+{
+    const int64_t group = q_heads / c.heads;
+    const Sizes s = c.e4m3 ? sizes_for<true>(c.dim, group) : sizes_for<false>(c.dim, group);
+    int64_t tokens = max_pages * c.page;
+    if (window > 0 && window < tokens) tokens = window + s.unit;
+    return batch * c.heads * ((group + s.heads - 1) / s.heads) * ((tokens + s.unit - 1) / s.unit + s.cost);
+}
+
 cudaError_t launch_attn_decode(const KvPlanes &c, const void *q, int64_t q_row, int64_t q_head, int q_dtype,
                                int64_t batch, int64_t q_heads, const int32_t *pages, int64_t max_pages,
                                const int32_t *lengths, float scale, int64_t window, void *out, int out_dtype,
@@ -74,10 +84,7 @@ cudaError_t launch_attn_decode(const KvPlanes &c, const void *q, int64_t q_row, 
     a.out = out, a.out_bf16 = out_dtype == QG_BF16, a.lse = lse;
     a.counters = static_cast<int *>(workspace);
     a.records = reinterpret_cast<float *>(static_cast<char *>(workspace) + counter_bytes());
-    // the units that there can be: the page tables' width, or a window that may begin inside a step
-    int64_t tokens = max_pages * c.page;
-    if (window > 0 && window < tokens) tokens = window + s.unit;
-    const int64_t most = batch * c.heads * a.chunks * ((tokens + s.unit - 1) / s.unit);
+    const int64_t most = attn_most_places(c, batch, q_heads, max_pages, window);
     return c.e4m3 ? launch_for<true>(a, most, st) : launch_for<false>(a, most, st);
 }
 

@@ -42,6 +42,7 @@ namespace qg {
 constexpr int AT_WARPS = 4;
 constexpr int AT_THREADS = 32 * AT_WARPS;
 constexpr int AT_CTAS_MAX = 4;  // per SM
+constexpr int AT_JOIN = 8;
 
 struct AttnArgs {
     KvPlanes c;
@@ -60,40 +61,82 @@ struct AttnArgs {
     float *records;  // two per CTA
 };
 
+#ifndef QG_AT_CH
+#define QG_AT_CH 2
+#endif
+#ifndef QG_AT_STAGES
+#define QG_AT_STAGES 2
+#endif
+#ifndef QG_AT_COST
+#define QG_AT_COST 2
+#endif
+#ifndef QG_AT_LEAST
+#define QG_AT_LEAST 1
+#endif
+#ifndef QG_AT_CTAS
+#define QG_AT_CTAS (D <= 96 ? 4 : 2)
+#endif
+
 template <bool E4M3, int D, int NT>
 struct AttnShape {
     static constexpr int NB = kv_blocks(E4M3, D);
-    static constexpr int SB = E4M3 ? 4 : 2;  // bytes of a scale
-    static constexpr int CH = D <= 128 ? 2 : 1;                        // tiles of 16 tokens to a step
+    static constexpr int SB = E4M3 ? 4 : 2;      // bytes of a scale
+    static constexpr int CH = D <= 128 ? QG_AT_CH : 1;  // tiles of 16 tokens to a step
     static constexpr int TOK = KV_TILE * CH;
-    static constexpr int STAGES = D <= 128 ? 2 : 3;
-    static constexpr int KS = D % 64 == 32 ? D : D + 32;  // padded rows of keys: 32 or 96 bytes past a multiple of 128
-    static constexpr int VS = D + 16;                     // and of values: 16 bytes past a multiple of 32
+    static constexpr int STAGES = D <= 128 ? QG_AT_STAGES : 3;
+    static constexpr bool SWIZZLE = D % 128 == 0;
+    static constexpr int KS = SWIZZLE ? D : D % 64 == 32 ? D : D + 32;  // padded rows of keys: 32 or 96 bytes past a multiple of 128
+    static constexpr int VS = SWIZZLE ? D : D + 16;                     // and of values: 16 bytes past a multiple of 32
     static constexpr int SCALES = KV_TILE * NB * SB;      // bytes of a tile's scales
     static constexpr int TILE = KV_TILE * (KS + VS) + 2 * SCALES;
     static constexpr int STAGE = CH * TILE;
     static constexpr int HEADS = 8 * NT;
     static constexpr int OROW = D + 4;  // floats of a head's row when warps meet
+    static_assert(8 * OROW * 4 <= STAGE, "the warps' sums meet in the stages just read");
     static constexpr int RING = AT_WARPS * STAGES * STAGE;
     static constexpr int QF = HEADS * D * 4;  // bytes of q's fragments
-    static constexpr int MEET = AT_WARPS * HEADS * OROW * 4;
-    static constexpr int SMEM = RING + QF + MEET + AT_WARPS * HEADS * 8 + HEADS * 4;
-    static constexpr int CTAS = 227 * 1024 / (SMEM + 1024) < AT_CTAS_MAX ? 227 * 1024 / (SMEM + 1024) : AT_CTAS_MAX;
+    static constexpr int SMEM = RING + QF + AT_WARPS * HEADS * 8 + HEADS * 4 + HEADS * NB * 4;
+    static constexpr int CTAS = 227 * 1024 / (SMEM + 1024) < QG_AT_CTAS ? 227 * 1024 / (SMEM + 1024) : QG_AT_CTAS;
     static constexpr int RECORD = HEADS * (D + 2);  // floats
+    static constexpr int COST = QG_AT_COST;  // of an item's beginning and end, in units
+    static constexpr int QW = HEADS / AT_WARPS, QP = (D / 4 + 31) / 32;  // heads of q to a warp, 4 values a lane each
+
+    // Where 16-byte piece c of row r lies in a tile's keys or values.  Swizzled, the eight pieces of 128 bytes change
+    // places with the row, so that the fragments' rows (keys: any four following ones; values: any four even ones) lie in
+    // banks of their own.
+    static __device__ __forceinline__ int key_at(int r, int c) { return SWIZZLE ? r * KS + ((c ^ (r & 3) << 1) << 4) : r * KS + (c << 4); }
+    static __device__ __forceinline__ int value_at(int r, int c) { return SWIZZLE ? r * VS + ((c ^ (r >> 1 & 3) << 1) << 4) : r * VS + (c << 4); }
 };
 
-__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                        uint32_t b1)
+struct Quad {
+    float v[4];
+};
+__device__ __forceinline__ Quad mma_f16(uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1, const Quad &c)
 {
+    Quad d;
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-                 "{%0,%1,%2,%3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 "{%10,%11,%12,%13};"
+                 : "=f"(d.v[0]), "=f"(d.v[1]), "=f"(d.v[2]), "=f"(d.v[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c.v[0]), "f"(c.v[1]), "f"(c.v[2]), "f"(c.v[3]));
+    return d;
+}
+
+// The same from zero.
+__device__ __forceinline__ Quad mma_f16(uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    Quad d;
+    asm volatile("{ .reg .f32 z; mov.f32 z, 0f00000000; mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+                 "{%8,%9}, {z,z,z,z}; }"
+                 : "=f"(d.v[0]), "=f"(d.v[1]), "=f"(d.v[2]), "=f"(d.v[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    return d;
 }
 
 // Two codes, in bytes 0 and 1 of w (HI: 2 and 3), as an f16 pair.  Q8_0: w holds code + 128,
-// which placed in the mantissa of 1024 gives 1152 + code; exact.
-template <bool E4M3, bool HI>
+// which placed in the mantissa of 1024 gives 1152 + code (OFFSET); less 1152, the code.  All exact.
+constexpr float kOffset = 1152.0f;
+constexpr uint32_t kOffset2 = 0x64806480u;
+template <bool E4M3, bool OFFSET, bool HI>
 __device__ __forceinline__ uint32_t codes_f16(uint32_t w)
 {
     if constexpr (E4M3) {
@@ -103,7 +146,9 @@ __device__ __forceinline__ uint32_t codes_f16(uint32_t w)
         return r;
     } else {
         const uint32_t m = __byte_perm(w, 0x64646464u, HI ? 0x4342 : 0x4140);
-        const __half2 v = __hsub2(*reinterpret_cast<const __half2 *>(&m), __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480)));
+        if constexpr (OFFSET) return m;
+        const uint32_t k = kOffset2;
+        const __half2 v = __hsub2(*reinterpret_cast<const __half2 *>(&m), *reinterpret_cast<const __half2 *>(&k));
         return *reinterpret_cast<const uint32_t *>(&v);
     }
 }
@@ -113,37 +158,38 @@ __device__ __forceinline__ uint32_t code_bits(uint32_t w)
     return E4M3 ? w : w ^ 0x80808080u;
 }
 
-// The NB scales of two neighbouring tokens at p (4-byte aligned at least), as f32: [token][block].
+// The NB scales of two neighbouring tokens, [token][block], as they lie in memory (4-byte aligned at least).
 template <bool E4M3, int NB>
-__device__ __forceinline__ void two_scales(const uint8_t *p, float (&d)[2][NB])
-{
-    constexpr int WORDS = E4M3 ? 2 * NB : NB;
+struct PairScales {
+    static constexpr int WORDS = E4M3 ? 2 * NB : NB;
     uint32_t w[WORDS];
-    if constexpr (WORDS % 4 == 0) {
+    __device__ __forceinline__ void load(const uint8_t *p)
+    {
+        if constexpr (WORDS % 4 == 0) {
 #pragma unroll
-        for (int i = 0; i < WORDS / 4; ++i) {
-            const uint4 v = reinterpret_cast<const uint4 *>(p)[i];
-            w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
-        }
-    } else if constexpr (WORDS % 2 == 0) {
+            for (int i = 0; i < WORDS / 4; ++i) {
+                const uint4 v = reinterpret_cast<const uint4 *>(p)[i];
+                w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+            }
+        } else if constexpr (WORDS % 2 == 0) {
 #pragma unroll
-        for (int i = 0; i < WORDS / 2; ++i) {
-            const uint2 v = reinterpret_cast<const uint2 *>(p)[i];
-            w[2 * i] = v.x, w[2 * i + 1] = v.y;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < WORDS; ++i) w[i] = reinterpret_cast<const uint32_t *>(p)[i];
-    }
-#pragma unroll
-    for (int i = 0; i < 2 * NB; ++i) {
-        if constexpr (E4M3) {
-            d[i / NB][i % NB] = __uint_as_float(w[i]);
+            for (int i = 0; i < WORDS / 2; ++i) {
+                const uint2 v = reinterpret_cast<const uint2 *>(p)[i];
+                w[2 * i] = v.x, w[2 * i + 1] = v.y;
+            }
         } else {
-            d[i / NB][i % NB] = h2f(static_cast<uint16_t>(i % 2 ? w[i / 2] >> 16 : w[i / 2]));
+#pragma unroll
+            for (int i = 0; i < WORDS; ++i) w[i] = reinterpret_cast<const uint32_t *>(p)[i];
         }
     }
-}
+    __device__ __forceinline__ float get(int token, int b) const  // both known at compile time
+    {
+        const int i = token * NB + b;
+        if constexpr (E4M3) return __uint_as_float(w[i]);
+        const __half2 h = *reinterpret_cast<const __half2 *>(&w[i / 2]);
+        return i % 2 ? __high2float(h) : __low2float(h);
+    }
+};
 
 __device__ __forceinline__ void cp_async_16_if(uint32_t dst, const void *src, bool there)
 {
@@ -167,7 +213,7 @@ __device__ __forceinline__ Seen seen_of(const AttnArgs &a, int64_t b)
     return {a.window > 0 && a.window < n ? n - static_cast<int>(a.window) : 0, n};
 }
 
-template <bool E4M3, int D, int NT, bool SPLIT>
+template <bool E4M3, int D, int NT, bool FINE>
 struct Attn {
     using S = AttnShape<E4M3, D, NT>;
     static constexpr int NB = S::NB, CH = S::CH, TOK = S::TOK, DG = D / 32;
@@ -175,181 +221,290 @@ struct Attn {
     static __device__ __forceinline__ int steps(Seen s) { return s.n > s.first ? (s.n + TOK - 1) / TOK - s.first / TOK : 0; }
     static __device__ __forceinline__ int units(Seen s) { return (steps(s) + AT_WARPS - 1) / AT_WARPS; }
 
-    // A place in the line of units: sequence, item (a cache head and a chunk of its query heads), unit.
+    // A place in the line: sequence, item (a cache head and a chunk of its query heads), place in the item, whose first
+    // COST places stand for what beginning and ending it costs and whose others are its units.
     struct Place {
-        int64_t b, left;  // left: units of the CTA's stretch from here on
+        int b, left;  // left: places of the CTA's stretch from here on
         Seen seen;
-        int units, item, unit;
+        int units, item, at;
+        __device__ __forceinline__ int unit() const { return at - S::COST; }
+        __device__ __forceinline__ void settle()  // on to the item's units
+        {
+            if (at < S::COST) {
+                const int skip = min(S::COST - at, left);
+                at += skip;
+                left -= skip;
+            }
+        }
         __device__ __forceinline__ void next(const AttnArgs &a)
         {
             --left;
-            if (++unit < units) return;
-            unit = 0;
-            next_item(a);
+            if (++at == units + S::COST) next_item(a);
         }
         __device__ __forceinline__ void next_item(const AttnArgs &a)
         {
-            if (++item < a.c.heads * a.chunks) return;
-            item = 0;
-            if (left <= 0) return;
-            do {  // there is a further sequence with units while any of the stretch is left
-                seen = seen_of(a, ++b);
-                units = Attn::units(seen);
-            } while (units == 0 && b + 1 < a.batch);
-            if (units == 0) left = 0;
+            at = 0;
+            if (++item == a.c.heads * a.chunks) {
+                item = 0;
+                if (left <= 0) return;
+                do {  // there is a further sequence with units while any of the stretch is left
+                    seen = seen_of(a, ++b);
+                    units = Attn::units(seen);
+                } while (units == 0 && b + 1 < a.batch);
+                if (units == 0) left = 0;
+            }
+            settle();
         }
     };
 
-    // The tokens of this warp's step in a unit, [at, at + TOK), and their pages.
+    // The tokens of this warp's step in a unit, [at, at + TOK), and where they are.
     struct Step {
         int at;
         bool any;
-        int page[CH], off[CH];  // page number (loaded), first row in it
+        int page[CH], off[CH];  // of each tile: its page (-1: none of it is seen) and first row there
         __device__ __forceinline__ void find(const AttnArgs &a, const Place &p, int warp)
         {
-            const int step = p.seen.first / TOK + p.unit * AT_WARPS + warp;
+            const int step0 = static_cast<uint32_t>(p.seen.first) / TOK, step = step0 + p.unit() * AT_WARPS + warp;
             at = step * TOK;
-            any = p.left > 0 && step - p.seen.first / TOK < steps(p.seen);
+            any = p.left > 0 && at < p.seen.n;
+            const int32_t *const row = a.pages + p.b * a.max_pages;
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
                 const int t = at + i * KV_TILE;
-                const int col = a.page_shift >= 0 ? t >> a.page_shift : static_cast<int>(static_cast<uint32_t>(t) / static_cast<uint32_t>(a.c.page));
+                const uint32_t col = a.page_shift >= 0 ? static_cast<uint32_t>(t) >> a.page_shift : static_cast<uint32_t>(t) / static_cast<uint32_t>(a.c.page);
                 off[i] = t - col * a.c.page;
-                page[i] = any && t < p.seen.n && t + KV_TILE > p.seen.first ? a.pages[p.b * a.max_pages + col] : 0;
+                page[i] = -1;
+                if (any && t < p.seen.n && t + KV_TILE > p.seen.first) page[i] = row[col];
             }
         }
     };
 
-    // Start the copies of a step into a stage.  Rows outside the tokens seen are zeros (their
-    // codes may be NaN's); their scales come as they are and are passed over where they are
-    // used.  Bit i of the answer: tile i lies on a page outside the cache (nothing is copied).
+    // Start the copies of a step into a stage.  Rows outside the tokens seen are zeros (their codes may be NaN's); their
+    // scales come as they are and are passed over where they are used.  Bit i of the answer: tile i has tokens seen on a
+    // page outside the cache (nothing is copied).
+    template <bool WHOLE>
+    static __device__ __forceinline__ void copy_tile(const AttnArgs &a, Seen seen, int t, int64_t row, uint32_t dk, int lane)
+    {
+        const uint8_t *k = a.c.kq + row * D + lane * 16, *v = a.c.vq + row * D + lane * 16;
+        const uint32_t dv = dk + KV_TILE * S::KS, ds = dv + KV_TILE * S::VS;
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) {
+            const int u = lane + 32 * j, r = u / (D / 16), c = u % (D / 16);
+            if constexpr (WHOLE) {
+                cp_async_16(dk + S::key_at(r, c), k + j * 512);
+                cp_async_16(dv + S::value_at(r, c), v + j * 512);
+            } else {
+                const bool there = t + r >= seen.first && t + r < seen.n;
+                cp_async_16_if(dk + S::key_at(r, c), k + j * 512, there);
+                cp_async_16_if(dv + S::value_at(r, c), v + j * 512, there);
+            }
+        }
+        const int x = lane & 15;  // the tile's scales: keys' by lanes 0-15, values' by 16-31
+        if (x < S::SCALES / 16) {
+            const uint8_t *src = static_cast<const uint8_t *>(lane < 16 ? a.c.kd : a.c.vd) + row * (NB * S::SB);
+            cp_async_16(ds + (lane < 16 ? 0 : S::SCALES) + x * 16, src + x * 16);
+        }
+    }
     static __device__ __forceinline__ uint32_t copy(const AttnArgs &a, const Place &p, const Step &s, uint32_t stage, int lane)
     {
-        uint32_t bad = 0;
         const int h = a.chunks == 1 ? p.item : p.item / a.chunks;
+        const uint32_t pages = static_cast<uint32_t>(a.c.n_pages);
+        bool plain = s.at >= p.seen.first && s.at + TOK <= p.seen.n;
+#pragma unroll
+        for (int i = 0; i < CH; ++i) plain = plain && static_cast<uint32_t>(s.page[i]) < pages;
+        if (plain) {
+#pragma unroll
+            for (int i = 0; i < CH; ++i)
+                copy_tile<true>(a, p.seen, 0, (static_cast<int64_t>(s.page[i]) * a.c.heads + h) * a.c.page + s.off[i], stage + i * S::TILE, lane);
+            return 0;
+        }
+        uint32_t bad = 0;
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-            const int t = s.at + i * KV_TILE;
-            if (t >= p.seen.n || t + KV_TILE <= p.seen.first) {
-                // no token of it is seen: zeros, without a page to read from
-                const uint32_t dst = stage + i * S::TILE;
+            const int t = s.at + i * KV_TILE, page = s.page[i];
+            if (static_cast<uint32_t>(page) < pages) {
+                copy_tile<false>(a, p.seen, t, (static_cast<int64_t>(page) * a.c.heads + h) * a.c.page + s.off[i], stage + i * S::TILE, lane);
+            } else {  // zeros, without a page to read from
+                if (t < p.seen.n && t + KV_TILE > p.seen.first) bad |= 1u << i;
                 for (int x = lane; x < S::TILE / 16; x += 32)
-                    asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(dst + x * 16), "r"(0) : "memory");
-                continue;
-            }
-            if (s.page[i] < 0 || s.page[i] >= a.c.n_pages) {
-                bad |= 1u << i;
-                continue;
-            }
-            const int64_t row = (static_cast<int64_t>(s.page[i]) * a.c.heads + h) * a.c.page + s.off[i];
-            const uint8_t *k = a.c.kq + row * D + lane * 16, *v = a.c.vq + row * D + lane * 16;
-            const uint32_t dk = stage + i * S::TILE, dv = dk + KV_TILE * S::KS, ds = dv + KV_TILE * S::VS;
-            const bool whole = t >= p.seen.first && t + KV_TILE <= p.seen.n;
-            if (whole) {
-#pragma unroll
-                for (int j = 0; j < D / 32; ++j) {
-                    const int u = lane + 32 * j, r = u / (D / 16), c = u % (D / 16);
-                    cp_async_16(dk + r * S::KS + c * 16, k + j * 512);
-                    cp_async_16(dv + r * S::VS + c * 16, v + j * 512);
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < D / 32; ++j) {
-                    const int u = lane + 32 * j, r = u / (D / 16), c = u % (D / 16);
-                    const bool there = t + r >= p.seen.first && t + r < p.seen.n;
-                    cp_async_16_if(dk + r * S::KS + c * 16, k + j * 512, there);
-                    cp_async_16_if(dv + r * S::VS + c * 16, v + j * 512, there);
-                }
-            }
-            const int x = lane & 15;  // the tile's scales: keys' by lanes 0-15, values' by 16-31
-            if (x < S::SCALES / 16) {
-                const uint8_t *src = static_cast<const uint8_t *>(lane < 16 ? a.c.kd : a.c.vd) + row * NB * S::SB;
-                cp_async_16(ds + (lane < 16 ? 0 : S::SCALES) + x * 16, src + x * 16);
+                    asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(stage + i * S::TILE + x * 16), "r"(0) : "memory");
             }
         }
         return bad;
     }
 
-    float o[NT][2 * DG][4];  // O^T: tile of 16 dims, its accumulators
-    float m[NT], l[NT];      // of head lane / 4 of each tile: the running reference, this lane's part of the sum
+    // Q8_0 codes go into the products as 1152 + code where results are bf16 (!FINE), and 1152 times the other
+    // operand's sum is what the accumulators start from, with its sign turned: for the scores a constant of the query,
+    // for the outputs one more MMA on a constant operand.  The cancellation costs 1152 / |code| of the additions'
+    // accuracy (2^-22), 2^-18 of a block's largest value.
+    static constexpr bool OFFSET = !E4M3 && !FINE;
+    // Tiles of S: rows 0-7 are eight heads; rows 8-15 the low parts of the same heads (FINE), or eight heads more.
+    static constexpr int ST = FINE ? NT : 1;
 
-    __device__ __forceinline__ void reset()
+    Quad o[NT][2 * DG];  // O^T: tiles of 16 dims
+    float m[NT], l[NT];  // of head lane / 4 of each tile: the running reference, this lane's part of the sum
+    float c[NT];         // the factor of its scores, in log2 units
+
+    __device__ __forceinline__ void begin(const float *qc, int lane)
     {
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
             m[i] = -FLT_MAX;
             l[i] = 0.0f;
+            c[i] = qc[8 * i + (lane >> 2)];
 #pragma unroll
-            for (int j = 0; j < 2 * DG; ++j) o[i][j][0] = o[i][j][1] = o[i][j][2] = o[i][j][3] = 0.0f;
+            for (int j = 0; j < 2 * DG; ++j) o[i][j] = Quad{};
         }
     }
 
-    // One step: `st` its stage, `qf` q's fragments, c the factor of each tile's scores (log2 units).
-    __device__ __forceinline__ void step(const uint8_t *st, const uint4 *qf, const float (&c)[NT], int at, Seen seen,
-                                         uint32_t bad, int lane)
+    // Query heads warp, warp + AT_WARPS, ... of a place's item: lane's pieces of four values.
+    static __device__ __forceinline__ void load_query(const AttnArgs &a, const Place &p, float4 (&v)[S::QW][S::QP], int warp, int lane)
+    {
+        const int h = a.chunks == 1 ? p.item : p.item / a.chunks, h0 = (p.item - h * a.chunks) * S::HEADS;
+#pragma unroll
+        for (int y = 0; y < S::QW; ++y)
+#pragma unroll
+            for (int i = 0; i < S::QP; ++i) {
+                const int x = h0 + y * AT_WARPS + warp, piece = lane + 32 * i;
+                v[y][i] = make_float4(0, 0, 0, 0);
+                if (x < a.group && piece < D / 4) {
+                    const int64_t at = p.b * a.q_row + (h * a.group + x) * a.q_head + piece * 4;
+                    v[y][i] = a.q_bf16 ? Vec4<__nv_bfloat16>::widen(*reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(a.q) + at))
+                                       : *reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) + at);
+                }
+            }
+    }
+
+    // Their fragments, factors and (OFFSET) blocks' sums to shared memory.
+    static __device__ __forceinline__ void put_query(const AttnArgs &a, const float4 (&all)[S::QW][S::QP], uint4 *qf, float *qc, float *qz,
+                                                     int warp, int lane)
+    {
+#pragma unroll
+        for (int y = 0; y < S::QW; ++y) {
+            const int x = y * AT_WARPS + warp;
+            const float4(&v)[S::QP] = all[y];
+            float top = 0.0f;
+            bool odd = false;  // infinities or NaN in the row: no factor
+#pragma unroll
+            for (int i = 0; i < S::QP; ++i) {
+                top = fmaxf(top, max_abs4(v[i]));
+                odd |= !(fabsf(v[i].x) <= FLT_MAX && fabsf(v[i].y) <= FLT_MAX && fabsf(v[i].z) <= FLT_MAX && fabsf(v[i].w) <= FLT_MAX);
+            }
+            top = warp_max_nonneg(top);
+            // 2^(14 - exponent of the largest), within f32's exponents either way
+            int ex = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+            ex = top == 0.0f || __any_sync(0xffffffffu, odd) ? 14 : max(ex, -100);
+            const float up = __uint_as_float(static_cast<uint32_t>(14 - ex + 127) << 23);
+#pragma unroll
+            for (int i = 0; i < S::QP; ++i) {
+                const int p = lane + 32 * i;
+                const float4 w = make_float4(v[i].x * up, v[i].y * up, v[i].z * up, v[i].w * up);
+                uint4 r;
+                r.x = pack_f16(w.x, w.y);
+                r.z = pack_f16(w.z, w.w);
+                const float2 b01 = __half22float2(*reinterpret_cast<const __half2 *>(&r.x));
+                const float2 b23 = __half22float2(*reinterpret_cast<const __half2 *>(&r.z));
+                r.y = pack_f16(w.x - b01.x, w.y - b01.y);
+                r.w = pack_f16(w.z - b23.x, w.w - b23.y);
+                // piece p: dims 32 dg + 8 t + 4 k
+                const int dg = p >> 3, t = p >> 1 & 3, k = p & 1;
+                if (p < D / 4) {
+                    if constexpr (FINE || NT == 1) {
+                        if constexpr (!FINE) r.y = r.w = 0;
+                        qf[((dg * 2 + k) * NT + x / 8) * 32 + (x % 8) * 4 + t] = r;
+                    } else {  // rows 8-15: the second eight heads
+                        uint32_t *const at = reinterpret_cast<uint32_t *>(qf + (dg * 2 + k) * 32 + (x % 8) * 4 + t) + x / 8;
+                        at[0] = r.x, at[2] = r.z;
+                    }
+                }
+                if constexpr (OFFSET) {  // a block's sum, by its eight lanes
+                    float sum = (b01.x + b01.y) + (b23.x + b23.y);
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+                    if (p < D / 4 && (lane & 7) == 0) qz[x * S::NB + dg] = -kOffset * sum;
+                }
+            }
+            if (lane == 0) qc[x] = a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(ex - 14 + 127) << 23);
+        }
+    }
+
+    // One step: `st` its stage, `qf` q's fragments, qz what to take off a block's sum (OFFSET).  EDGE: some of its tokens
+    // are not seen, or on a page outside the cache.
+    template <bool EDGE>
+    __device__ __forceinline__ void step(const uint8_t *st, const uint4 *qf, const float *qz, int at, Seen seen, uint32_t bad, int lane)
     {
         const int g = lane >> 2, t = lane & 3;
+        constexpr int DX = S::SWIZZLE ? 4 : 1;  // offsets that differ by more than a constant
+        const uint8_t *kx[DX], *vx[DX];
+#pragma unroll
+        for (int i = 0; i < DX; ++i) {
+            kx[i] = st + S::key_at(g, 2 * i + (t >> 1)) + (t & 1) * 8;
+            vx[i] = st + KV_TILE * S::KS + S::value_at(2 * t, 2 * i + (g >> 2)) + (g & 3) * 4;
+        }
         // ---- scores
         float s[NT][2 * CH][2];
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int j = 0; j < 2 * CH; ++j) s[i][j][0] = s[i][j][1] = 0.0f;
-        float dk[2 * CH][2][NB];
+        PairScales<E4M3, NB> dk[2 * CH];
 #pragma unroll
         for (int j = 0; j < 2 * CH; ++j)
-            two_scales<E4M3, NB>(st + (j / 2) * S::TILE + KV_TILE * (S::KS + S::VS) + ((j % 2) * 8 + 2 * t) * NB * S::SB, dk[j]);
+            dk[j].load(st + (j / 2) * S::TILE + KV_TILE * (S::KS + S::VS) + ((j % 2) * 8 + 2 * t) * NB * S::SB);
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-            float acc[NT][2 * CH][4];
-#pragma unroll
-            for (int i = 0; i < NT; ++i)
-#pragma unroll
-                for (int j = 0; j < 2 * CH; ++j) acc[i][j][0] = acc[i][j][1] = acc[i][j][2] = acc[i][j][3] = 0.0f;
+            Quad acc[ST][2 * CH];
 #pragma unroll
             for (int dg = b * (E4M3 ? 4 : 1); dg < (b + 1) * (E4M3 ? 4 : 1) && dg < DG; ++dg) {
-                uint4 a[NT][2];
+                const bool first = dg == b * (E4M3 ? 4 : 1);
+                uint4 qa[ST][2];
 #pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    a[i][0] = qf[((dg * 2 + 0) * NT + i) * 32 + lane];
-                    a[i][1] = qf[((dg * 2 + 1) * NT + i) * 32 + lane];
+                for (int i = 0; i < ST; ++i) {
+                    qa[i][0] = qf[((dg * 2 + 0) * ST + i) * 32 + lane];
+                    qa[i][1] = qf[((dg * 2 + 1) * ST + i) * 32 + lane];
                 }
 #pragma unroll
                 for (int j = 0; j < 2 * CH; ++j) {
-                    const uint2 w = *reinterpret_cast<const uint2 *>(st + (j / 2) * S::TILE + ((j % 2) * 8 + g) * S::KS + dg * 32 + t * 8);
+                    const uint2 w = *reinterpret_cast<const uint2 *>(kx[dg % DX] + (dg - dg % DX) * 32 + (j / 2) * S::TILE + (j % 2) * 8 * S::KS);
                     const uint32_t x = code_bits<E4M3>(w.x), y = code_bits<E4M3>(w.y);
-                    const uint32_t b0 = codes_f16<E4M3, false>(x), b1 = codes_f16<E4M3, true>(x);
-                    const uint32_t b2 = codes_f16<E4M3, false>(y), b3 = codes_f16<E4M3, true>(y);
+                    const uint32_t b0 = codes_f16<E4M3, OFFSET, false>(x), b1 = codes_f16<E4M3, OFFSET, true>(x);
+                    const uint32_t b2 = codes_f16<E4M3, OFFSET, false>(y), b3 = codes_f16<E4M3, OFFSET, true>(y);
 #pragma unroll
-                    for (int i = 0; i < NT; ++i) {
-                        mma_f16(acc[i][j], a[i][0].x, a[i][0].y, a[i][0].z, a[i][0].w, b0, b1);
-                        mma_f16(acc[i][j], a[i][1].x, a[i][1].y, a[i][1].z, a[i][1].w, b2, b3);
+                    for (int i = 0; i < ST; ++i) {
+                        acc[i][j] = first ? mma_f16(qa[i][0].x, qa[i][0].y, qa[i][0].z, qa[i][0].w, b0, b1)
+                                          : mma_f16(qa[i][0].x, qa[i][0].y, qa[i][0].z, qa[i][0].w, b0, b1, acc[i][j]);
+                        acc[i][j] = mma_f16(qa[i][1].x, qa[i][1].y, qa[i][1].z, qa[i][1].w, b2, b3, acc[i][j]);
                     }
                 }
             }
 #pragma unroll
-            for (int i = 0; i < NT; ++i)
+            for (int i = 0; i < NT; ++i) {
+                float z = 0.0f;
+                if constexpr (OFFSET) z = qz[(8 * i + g) * NB + b];
 #pragma unroll
-                for (int j = 0; j < 2 * CH; ++j) {
-                    s[i][j][0] = fmaf(acc[i][j][0] + acc[i][j][2], dk[j][0][b], s[i][j][0]);
-                    s[i][j][1] = fmaf(acc[i][j][1] + acc[i][j][3], dk[j][1][b], s[i][j][1]);
-                }
+                for (int j = 0; j < 2 * CH; ++j)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const float v = FINE ? acc[FINE ? i : 0][j].v[x] + acc[FINE ? i : 0][j].v[2 + x]
+                                             : OFFSET ? acc[0][j].v[2 * i + x] + z : acc[0][j].v[2 * i + x];
+                        s[i][j][x] = b == 0 ? v * dk[j].get(x, 0) : fmaf(v, dk[j].get(x, b), s[i][j][x]);
+                    }
+            }
         }
         // ---- values' scales, and what is not seen
         float dv[2 * CH][2][NB], e[2 * CH][2];
 #pragma unroll
-        for (int j = 0; j < 2 * CH; ++j)
-            two_scales<E4M3, NB>(st + (j / 2) * S::TILE + KV_TILE * (S::KS + S::VS) + S::SCALES + ((j % 2) * 8 + 2 * t) * NB * S::SB, dv[j]);
-        const bool edge = at < seen.first || at + TOK > seen.n || bad != 0;
+        for (int j = 0; j < 2 * CH; ++j) {
+            PairScales<E4M3, NB> d;
+            d.load(st + (j / 2) * S::TILE + KV_TILE * (S::KS + S::VS) + S::SCALES + ((j % 2) * 8 + 2 * t) * NB * S::SB);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) dv[j][0][b] = d.get(0, b), dv[j][1][b] = d.get(1, b);
+        }
         uint32_t hidden = 0;  // bit 2 j + x: token x of pair j
-        if (edge) {
+        if constexpr (EDGE) {
 #pragma unroll
             for (int j = 0; j < 2 * CH; ++j)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     const int token = at + j * 8 + 2 * t + x;
-                    const bool h = token < seen.first || token >= seen.n;
-                    if (h) {
+                    if (token < seen.first || token >= seen.n) {
                         hidden |= 1u << (2 * j + x);
 #pragma unroll
                         for (int b = 0; b < NB; ++b) dv[j][x][b] = 0.0f;
@@ -380,7 +535,7 @@ struct Attn {
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     const float u = fmaf(s[i][j][x], c[i], e[j][x]);
-                    top = fmaxf(top, edge && (hidden >> (2 * j + x) & 1) ? top : u);
+                    if (!EDGE || !(hidden >> (2 * j + x) & 1)) top = fmaxf(top, u);
                 }
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
@@ -393,7 +548,7 @@ struct Attn {
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     float p = ex2_approx(fmaf(s[i][j][x], c[i], -now));
-                    if (edge && (hidden >> (2 * j + x) & 1)) p = 0.0f;
+                    if (EDGE && (hidden >> (2 * j + x) & 1)) p = 0.0f;
                     s[i][j][x] = p;
                     sum += p;
                 }
@@ -410,57 +565,68 @@ struct Attn {
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
             uint32_t hi[NT][CH][2], lo[NT][CH][2];
+            Quad y[NT];
 #pragma unroll
-            for (int i = 0; i < NT; ++i)
+            for (int i = 0; i < NT; ++i) {
 #pragma unroll
                 for (int j = 0; j < 2 * CH; ++j) {
                     const float w0 = s[i][j][0] * dv[j][0][b], w1 = s[i][j][1] * dv[j][1][b];
                     const uint32_t h = pack_f16(w0, w1);
                     hi[i][j / 2][j % 2] = h;
-                    if constexpr (SPLIT) {
+                    if constexpr (FINE) {
                         const float2 back = __half22float2(*reinterpret_cast<const __half2 *>(&h));
                         lo[i][j / 2][j % 2] = pack_f16(w0 - back.x, w1 - back.y);
                     }
                 }
+                if constexpr (OFFSET) {
+                    constexpr uint32_t k = kOffset2 ^ 0x80008000u;  // -1152
+                    y[i] = mma_f16(k, k, k, k, hi[i][0][0], hi[i][0][1]);
+#pragma unroll
+                    for (int ch = 1; ch < CH; ++ch) y[i] = mma_f16(k, k, k, k, hi[i][ch][0], hi[i][ch][1], y[i]);
+                }
+            }
 #pragma unroll
             for (int dg = b * (E4M3 ? 4 : 1); dg < (b + 1) * (E4M3 ? 4 : 1) && dg < DG; ++dg) {
-                float acc[NT][2][4];
-#pragma unroll
-                for (int i = 0; i < NT; ++i)
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) acc[i][x][0] = acc[i][x][1] = acc[i][x][2] = acc[i][x][3] = 0.0f;
+                Quad acc[NT][2];
 #pragma unroll
                 for (int ch = 0; ch < CH; ++ch) {
-                    const uint8_t *v = st + ch * S::TILE + KV_TILE * S::KS + (2 * t) * S::VS + dg * 32 + g * 4;
+                    const uint8_t *v = vx[dg % DX] + (dg - dg % DX) * 32 + ch * S::TILE;
                     const uint32_t v0 = code_bits<E4M3>(*reinterpret_cast<const uint32_t *>(v));
                     const uint32_t v1 = code_bits<E4M3>(*reinterpret_cast<const uint32_t *>(v + S::VS));
                     const uint32_t v8 = code_bits<E4M3>(*reinterpret_cast<const uint32_t *>(v + 8 * S::VS));
                     const uint32_t v9 = code_bits<E4M3>(*reinterpret_cast<const uint32_t *>(v + 9 * S::VS));
                     const uint32_t x0 = __byte_perm(v0, v1, 0x5140), x1 = __byte_perm(v0, v1, 0x7362);
                     const uint32_t y0 = __byte_perm(v8, v9, 0x5140), y1 = __byte_perm(v8, v9, 0x7362);
-                    const uint32_t a0 = codes_f16<E4M3, false>(x0), a1 = codes_f16<E4M3, true>(x0);
-                    const uint32_t a2 = codes_f16<E4M3, false>(y0), a3 = codes_f16<E4M3, true>(y0);
-                    const uint32_t a4 = codes_f16<E4M3, false>(x1), a5 = codes_f16<E4M3, true>(x1);
-                    const uint32_t a6 = codes_f16<E4M3, false>(y1), a7 = codes_f16<E4M3, true>(y1);
+                    const uint32_t va[2][4] = {{codes_f16<E4M3, OFFSET, false>(x0), codes_f16<E4M3, OFFSET, true>(x0),
+                                                codes_f16<E4M3, OFFSET, false>(y0), codes_f16<E4M3, OFFSET, true>(y0)},
+                                               {codes_f16<E4M3, OFFSET, false>(x1), codes_f16<E4M3, OFFSET, true>(x1),
+                                                codes_f16<E4M3, OFFSET, false>(y1), codes_f16<E4M3, OFFSET, true>(y1)}};
 #pragma unroll
-                    for (int i = 0; i < NT; ++i) {
-                        if constexpr (SPLIT) {
-                            mma_f16(acc[i][0], a0, a1, a2, a3, lo[i][ch][0], lo[i][ch][1]);
-                            mma_f16(acc[i][1], a4, a5, a6, a7, lo[i][ch][0], lo[i][ch][1]);
+                    for (int i = 0; i < NT; ++i)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const uint32_t(&q)[4] = va[x];
+                            Quad &d = acc[i][x];
+                            if constexpr (FINE) {
+                                d = ch == 0 ? mma_f16(q[0], q[1], q[2], q[3], lo[i][ch][0], lo[i][ch][1])
+                                            : mma_f16(q[0], q[1], q[2], q[3], lo[i][ch][0], lo[i][ch][1], d);
+                                d = mma_f16(q[0], q[1], q[2], q[3], hi[i][ch][0], hi[i][ch][1], d);
+                            } else {
+                                d = ch > 0 ? mma_f16(q[0], q[1], q[2], q[3], hi[i][ch][0], hi[i][ch][1], d)
+                                           : OFFSET ? mma_f16(q[0], q[1], q[2], q[3], hi[i][ch][0], hi[i][ch][1], y[i])
+                                                    : mma_f16(q[0], q[1], q[2], q[3], hi[i][ch][0], hi[i][ch][1]);
+                            }
                         }
-                        mma_f16(acc[i][0], a0, a1, a2, a3, hi[i][ch][0], hi[i][ch][1]);
-                        mma_f16(acc[i][1], a4, a5, a6, a7, hi[i][ch][0], hi[i][ch][1]);
-                    }
                 }
 #pragma unroll
                 for (int i = 0; i < NT; ++i)
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        float(&d)[4] = o[i][2 * dg + x];
-                        d[0] = fmaf(d[0], f0[i], acc[i][x][0]);
-                        d[1] = fmaf(d[1], f1[i], acc[i][x][1]);
-                        d[2] = fmaf(d[2], f0[i], acc[i][x][2]);
-                        d[3] = fmaf(d[3], f1[i], acc[i][x][3]);
+                        float(&d)[4] = o[i][2 * dg + x].v;
+                        d[0] = fmaf(d[0], f0[i], acc[i][x].v[0]);
+                        d[1] = fmaf(d[1], f1[i], acc[i][x].v[1]);
+                        d[2] = fmaf(d[2], f0[i], acc[i][x].v[2]);
+                        d[3] = fmaf(d[3], f1[i], acc[i][x].v[3]);
                     }
             }
         }
@@ -483,34 +649,66 @@ __device__ __forceinline__ void attn_store(const AttnArgs &a, int64_t row, int d
         store4(static_cast<float *>(a.out) + row * dim + col, r);
 }
 
-template <bool E4M3, int D, int NT, bool SPLIT>
+// The line's `total` places in equal stretches, the first `more` of them one longer.
+struct Share {
+    int64_t each, more;
+    int ctas;
+    __device__ __forceinline__ Share(int64_t total, int cost, unsigned grid)
+    {
+        // no shorter than QG_AT_LEAST
+        const int least = QG_AT_LEAST;
+        if (total < (int64_t(1) << 31)) {
+            const uint32_t t = static_cast<uint32_t>(total), n = max(min(t / least, grid), t > 0 ? 1u : 0u);
+            ctas = static_cast<int>(n);
+            each = n ? t / n : 0;
+            more = n ? t % n : 0;
+        } else {
+            ctas = static_cast<int>(grid);
+            each = total / grid;
+            more = total - each * grid;
+        }
+    }
+    __device__ __forceinline__ int64_t start(int c) const { return c * each + min(static_cast<int64_t>(c), more); }
+    __device__ __forceinline__ int cta_of(int64_t at) const
+    {
+        const int64_t cut = more * (each + 1);
+        if (cut + at < (int64_t(1) << 31) && each < (int64_t(1) << 30))
+            return at < cut ? static_cast<uint32_t>(at) / static_cast<uint32_t>(each + 1)
+                            : static_cast<int>(more) + static_cast<uint32_t>(at - cut) / static_cast<uint32_t>(each);
+        return static_cast<int>(at < cut ? at / (each + 1) : more + (at - cut) / each);
+    }
+};
+
+template <bool E4M3, int D, int NT, bool FINE>
 __global__ void __launch_bounds__(AT_THREADS, AttnShape<E4M3, D, NT>::CTAS) attn_decode_kernel(const __grid_constant__ AttnArgs a)
 {
     using S = AttnShape<E4M3, D, NT>;
-    using A = Attn<E4M3, D, NT, SPLIT>;
+    using A = Attn<E4M3, D, NT, FINE>;
     extern __shared__ __align__(16) uint8_t smem[];
     uint4 *const qf = reinterpret_cast<uint4 *>(smem + S::RING);
-    float *const meet = reinterpret_cast<float *>(smem + S::RING + S::QF);
-    float2 *const ml = reinterpret_cast<float2 *>(smem + S::RING + S::QF + S::MEET);  // [warp][head]: m, l
-    float *const qc = reinterpret_cast<float *>(ml + AT_WARPS * S::HEADS);
+    float2 *const ml = reinterpret_cast<float2 *>(smem + S::RING + S::QF);  // [warp][head]: m, l
+    float *const qc = reinterpret_cast<float *>(ml + AT_WARPS * S::HEADS), *const qz = qc + S::HEADS;
     __shared__ int64_t sums[AT_WARPS];
-    __shared__ int64_t place_at[2];  // sequence, units into it
+    __shared__ int64_t found_b;
+    __shared__ int found_item, found_at;
     __shared__ int last_one;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int cta = blockIdx.x, items = a.c.heads * a.chunks;
     pdl_wait();
     pdl_trigger();
 
-    // ---- this CTA's stretch of the line of units: a scan over the sequences, a slice to a thread
+    // ---- this CTA's stretch of the line: a scan over the sequences, a slice to a thread
     const int64_t per = (a.batch + AT_THREADS - 1) / AT_THREADS;
     const int64_t b0 = min(tid * per, a.batch), b1 = min(b0 + per, a.batch);
     bool empty = false;  // a sequence without tokens whose outputs this CTA writes
-    for (int64_t b = cta + static_cast<int64_t>(tid) * gridDim.x; b < a.batch; b += static_cast<int64_t>(AT_THREADS) * gridDim.x) {
-        const Seen s = seen_of(a, b);
-        empty |= s.n <= s.first;
-    }
     int64_t mine = 0;
-    for (int64_t b = b0; b < b1; ++b) mine += static_cast<int64_t>(A::units(seen_of(a, b))) * items;
+    int units0 = 0;  // of sequence b0
+    for (int64_t b = b0; b < b1; ++b) {
+        const int n = A::units(seen_of(a, b));
+        if (b == b0) units0 = n;
+        mine += n > 0 ? static_cast<int64_t>(n + S::COST) * items : 0;
+        empty |= n == 0 && b % gridDim.x == cta;
+    }
     int64_t incl = mine;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -535,29 +733,38 @@ __global__ void __launch_bounds__(AT_THREADS, AttnShape<E4M3, D, NT>::CTAS) attn
                 for (int i = tid; i < a.q_heads; i += AT_THREADS) a.lse[b * a.q_heads + i] = -__int_as_float(0x7f800000);
         }
     }
-    const int64_t ctas = min(static_cast<int64_t>(gridDim.x), total);
-    if (cta >= ctas) return;
-    const int64_t share = total / ctas, more = total - share * ctas;  // the first `more` CTAs take one unit more
-    const int64_t start = cta * share + min(static_cast<int64_t>(cta), more), end = start + share + (cta < more);
+    const Share share(total, S::COST, gridDim.x);
+    if (cta >= share.ctas) return;
+    const int64_t start = share.start(cta), end = share.start(cta + 1);
     if (start >= incl - mine && start < incl) {
         int64_t at = incl - mine, b = b0;
-        for (;; ++b) {
-            const int64_t n = static_cast<int64_t>(A::units(seen_of(a, b))) * items;
-            if (start < at + n) break;
-            at += n;
+        int n = units0;
+        for (;;) {
+            const int64_t cost = n > 0 ? static_cast<int64_t>(n + S::COST) * items : 0;
+            if (start < at + cost) break;
+            at += cost;
+            n = A::units(seen_of(a, ++b));
         }
-        place_at[0] = b;
-        place_at[1] = start - at;
+        const int64_t into = start - at;
+        const int item = into < INT32_MAX ? static_cast<int>(into) / (n + S::COST) : static_cast<int>(into / (n + S::COST));
+        found_b = b;
+        found_item = item;
+        found_at = static_cast<int>(into - static_cast<int64_t>(item) * (n + S::COST));
     }
     __syncthreads();
     typename A::Place use;
-    use.b = place_at[0];
+    use.b = static_cast<int>(found_b);
     use.seen = seen_of(a, use.b);
     use.units = A::units(use.seen);
-    use.item = static_cast<int>(place_at[1] / use.units);
-    use.unit = static_cast<int>(place_at[1] - static_cast<int64_t>(use.item) * use.units);
-    use.left = end - start;
+    use.item = found_item;
+    use.at = found_at;
+    use.left = static_cast<int>(end - start);  // the host's bound on the line keeps it below 2^31
+    if (use.units == 0) return;  // the lengths have changed under the call
+    use.settle();
+    if (use.left <= 0) return;
 
+    float4 qv[S::QW][S::QP];
+    A::load_query(a, use, qv, warp, lane);
     // ---- the first copies
     const uint32_t ring = smem_addr(smem) + warp * S::STAGES * S::STAGE;
     typename A::Place load = use;
@@ -582,116 +789,86 @@ __global__ void __launch_bounds__(AT_THREADS, AttnShape<E4M3, D, NT>::CTAS) attn
     int stage = 0, fill = S::STAGES - 1;
     while (use.left > 0) {
         // ---- a segment: the part of one item that lies in the stretch
-        const int h = use.item / a.chunks, h0 = (use.item - h * a.chunks) * S::HEADS;  // cache head; its first query head here
+        const int h = a.chunks == 1 ? use.item : use.item / a.chunks, h0 = (use.item - h * a.chunks) * S::HEADS;  // cache head; its first query head here
         const int heads = min(S::HEADS, a.group - h0);
-        const int unit0 = use.unit, n_units = static_cast<int>(min(static_cast<int64_t>(use.units - unit0), use.left));
-        for (int x = warp; x < S::HEADS; x += AT_WARPS) {
-            constexpr int P = (D / 4 + 31) / 32;
-            float4 v[P];
-            float top = 0.0f;
-            bool odd = false;  // infinities or NaN in the row: no factor
-#pragma unroll
-            for (int i = 0; i < P; ++i) {
-                const int p = lane + 32 * i;
-                v[i] = make_float4(0, 0, 0, 0);
-                if (x < heads && p < D / 4) {
-                    const int64_t at = use.b * a.q_row + (h * a.group + h0 + x) * a.q_head + p * 4;
-                    v[i] = a.q_bf16 ? Vec4<__nv_bfloat16>::widen(*reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(a.q) + at))
-                                    : *reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) + at);
-                }
-                top = fmaxf(top, max_abs4(v[i]));
-                odd |= !(fabsf(v[i].x) <= FLT_MAX && fabsf(v[i].y) <= FLT_MAX && fabsf(v[i].z) <= FLT_MAX && fabsf(v[i].w) <= FLT_MAX);
-            }
-            top = warp_max_nonneg(top);
-            // 2^(14 - exponent of the largest), within f32's exponents either way
-            int ex = static_cast<int>(__float_as_uint(top) >> 23) - 127;
-            ex = top == 0.0f || __any_sync(0xffffffffu, odd) ? 14 : max(ex, -100);
-            const float up = __uint_as_float(static_cast<uint32_t>(14 - ex + 127) << 23);
-#pragma unroll
-            for (int i = 0; i < P; ++i) {
-                const int p = lane + 32 * i;
-                if (p < D / 4) {
-                    const float4 w = make_float4(v[i].x * up, v[i].y * up, v[i].z * up, v[i].w * up);
-                    uint4 r;
-                    r.x = pack_f16(w.x, w.y);
-                    r.z = pack_f16(w.z, w.w);
-                    const float2 b01 = __half22float2(*reinterpret_cast<const __half2 *>(&r.x));
-                    const float2 b23 = __half22float2(*reinterpret_cast<const __half2 *>(&r.z));
-                    r.y = pack_f16(w.x - b01.x, w.y - b01.y);
-                    r.w = pack_f16(w.z - b23.x, w.w - b23.y);
-                    // piece p: dims 32 dg + 8 t + 4 k
-                    const int dg = p >> 3, t = p >> 1 & 3, k = p & 1;
-                    qf[((dg * 2 + k) * NT + x / 8) * 32 + (x % 8) * 4 + t] = r;
-                }
-            }
-            if (lane == 0) qc[x] = a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(ex - 14 + 127) << 23);
-        }
+        const int unit0 = use.unit(), n_units = min(use.units - unit0, use.left);
+        A::put_query(a, qv, qf, qc, qz, warp, lane);
         __syncthreads();
-        float c[NT];
-#pragma unroll
-        for (int i = 0; i < NT; ++i) c[i] = qc[8 * i + (lane >> 2)];
-        state.reset();
+        state.begin(qc, lane);
+        int last = 0;  // the stage read last
         for (int u = 0; u < n_units; ++u) {
             copy_next(fill);
             cp_async_wait<S::STAGES - 1>();
             __syncwarp();
             const int step = use.seen.first / S::TOK + (unit0 + u) * AT_WARPS + warp, at = step * S::TOK;
-            if (at < use.seen.n)
-                state.step(smem + (warp * S::STAGES + stage) * S::STAGE, qf, c, at, use.seen,
-                           bad >> (stage * S::CH) & ((1u << S::CH) - 1), lane);
+            const uint8_t *const st = smem + (warp * S::STAGES + stage) * S::STAGE;
+            const uint32_t off = bad >> (stage * S::CH) & ((1u << S::CH) - 1);
+            if (at < use.seen.n) {
+                if (at < use.seen.first || at + S::TOK > use.seen.n || off != 0)
+                    state.template step<true>(st, qf, qz, at, use.seen, off, lane);
+                else
+                    state.template step<false>(st, qf, qz, at, use.seen, 0, lane);
+            }
             __syncwarp();
+            last = stage;
             stage = stage + 1 == S::STAGES ? 0 : stage + 1;
             fill = fill + 1 == S::STAGES ? 0 : fill + 1;
         }
-        // ---- the warps meet
+        // ---- the warps meet, eight heads at a time, each in the stage that it has read last: the same one for
+        // all, and no copy into it is started before the next segment's first barrier
+        const bool whole = n_units == use.units;
+        const int64_t first_unit = end - use.left - unit0;  // of the item, in the line
+        const int units = use.units;
+        float *const record = a.records + (static_cast<int64_t>(cta) * 2 + (unit0 == 0)) * S::RECORD;
+        const int64_t row0 = static_cast<int64_t>(use.b) * a.q_heads + h * a.group + h0;
+        use.left -= n_units;
+        if (use.left > 0) {
+            use.next_item(a);
+            if (use.left > 0) A::load_query(a, use, qv, warp, lane);  // the next segment's, on its way while this one ends
+        }
+        float *const meet = reinterpret_cast<float *>(smem + last * S::STAGE);
+        constexpr int MEET = S::STAGES * S::STAGE / 4;  // floats from warp to warp
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
+            if (i > 0) __syncthreads();
             float l = state.l[i];
             l += __shfl_xor_sync(0xffffffffu, l, 1);
             l += __shfl_xor_sync(0xffffffffu, l, 2);
             if ((lane & 3) == 0) ml[warp * S::HEADS + 8 * i + (lane >> 2)] = make_float2(state.m[i], l);
-            float *row = meet + (warp * S::HEADS + 8 * i + 2 * (lane & 3)) * S::OROW + (lane >> 2) * 4;
+            float *const to = meet + warp * MEET + 2 * (lane & 3) * S::OROW + (lane >> 2) * 4;
 #pragma unroll
             for (int dg = 0; dg < D / 32; ++dg) {
-                const float(&p)[4] = state.o[i][2 * dg], (&r)[4] = state.o[i][2 * dg + 1];
-                *reinterpret_cast<float4 *>(row + dg * 32) = make_float4(p[0], p[2], r[0], r[2]);
-                *reinterpret_cast<float4 *>(row + S::OROW + dg * 32) = make_float4(p[1], p[3], r[1], r[3]);
+                const float(&p)[4] = state.o[i][2 * dg].v, (&r)[4] = state.o[i][2 * dg + 1].v;
+                *reinterpret_cast<float4 *>(to + dg * 32) = make_float4(p[0], p[2], r[0], r[2]);
+                *reinterpret_cast<float4 *>(to + S::OROW + dg * 32) = make_float4(p[1], p[3], r[1], r[3]);
             }
-        }
-        __syncthreads();
-        const bool whole = n_units == use.units;
-        float *const record = a.records + (static_cast<int64_t>(cta) * 2 + (unit0 == 0)) * S::RECORD;
-        const int64_t row0 = use.b * a.q_heads + h * a.group + h0;
-        for (int i = tid; i < heads * (D / 4); i += AT_THREADS) {
-            const int x = i / (D / 4), col = i % (D / 4) * 4;
-            float top = -FLT_MAX, l = 0.0f;
-            float4 v = make_float4(0, 0, 0, 0);
+            __syncthreads();
+            for (int j = tid; j < min(heads - 8 * i, 8) * (D / 4); j += AT_THREADS) {
+                const int y = j / (D / 4), x = 8 * i + y, col = j % (D / 4) * 4;
+                float top = -FLT_MAX, sum = 0.0f;
+                float4 v = make_float4(0, 0, 0, 0);
 #pragma unroll
-            for (int w = 0; w < AT_WARPS; ++w) top = fmaxf(top, ml[w * S::HEADS + x].x);
+                for (int w = 0; w < AT_WARPS; ++w) top = fmaxf(top, ml[w * S::HEADS + x].x);
 #pragma unroll
-            for (int w = 0; w < AT_WARPS; ++w) {
-                const float2 y = ml[w * S::HEADS + x];
-                const float k = ex2_approx(y.x - top);
-                const float4 z = *reinterpret_cast<const float4 *>(meet + (w * S::HEADS + x) * S::OROW + col);
-                l = fmaf(y.y, k, l);
-                v = make_float4(fmaf(z.x, k, v.x), fmaf(z.y, k, v.y), fmaf(z.z, k, v.z), fmaf(z.w, k, v.w));
-            }
-            if (whole) {
-                attn_store(a, row0 + x, D, col, v, l);
-                if (a.lse && col == 0) a.lse[row0 + x] = (top + log2f(l)) * kLn2;
-            } else {
-                *reinterpret_cast<float4 *>(record + x * D + col) = v;
-                if (col == 0) record[S::HEADS * D + 2 * x] = top, record[S::HEADS * D + 2 * x + 1] = l;
+                for (int w = 0; w < AT_WARPS; ++w) {
+                    const float2 part = ml[w * S::HEADS + x];
+                    const float k = ex2_approx(part.x - top);
+                    const float4 z = *reinterpret_cast<const float4 *>(meet + w * MEET + y * S::OROW + col);
+                    sum = fmaf(part.y, k, sum);
+                    v = make_float4(fmaf(z.x, k, v.x), fmaf(z.y, k, v.y), fmaf(z.z, k, v.z), fmaf(z.w, k, v.w));
+                }
+                if (whole) {
+                    attn_store(a, row0 + x, D, col, v, sum);
+                    if (a.lse && col == 0) a.lse[row0 + x] = (top + log2f(sum)) * kLn2;
+                } else {
+                    *reinterpret_cast<float4 *>(record + x * D + col) = v;
+                    if (col == 0) record[S::HEADS * D + 2 * x] = top, record[S::HEADS * D + 2 * x + 1] = sum;
+                }
             }
         }
         if (!whole) {
-            // the item's units [g0, g1) of the line, and the CTAs that share them
-            const int64_t g0 = end - use.left - unit0, g1 = g0 + use.units;
-            auto cta_of = [&](int64_t u) {
-                const int64_t cut = more * (share + 1);
-                return static_cast<int>(u < cut ? u / (share + 1) : more + (u - cut) / share);
-            };
-            const int c0 = cta_of(g0), c1 = cta_of(g1 - 1);
+            // the CTAs that share the item's units
+            const int c0 = share.cta_of(first_unit), c1 = share.cta_of(first_unit + units - 1);
             __threadfence();
             __syncthreads();
             if (tid == 0) {
@@ -708,35 +885,43 @@ __global__ void __launch_bounds__(AT_THREADS, AttnShape<E4M3, D, NT>::CTAS) attn
                     const int x = i / (D / 4), col = i % (D / 4) * 4;
                     float top = -FLT_MAX, l = 0.0f;
                     float4 v = make_float4(0, 0, 0, 0);
-                    for (int p = 0; p < parts; ++p) top = fmaxf(top, __ldcg(part(p) + S::HEADS * D + 2 * x));
-#pragma unroll 4
-                    for (int p = 0; p < parts; ++p) {
-                        const float2 y = __ldcg(reinterpret_cast<const float2 *>(part(p) + S::HEADS * D + 2 * x));
-                        const float4 z = __ldcg(reinterpret_cast<const float4 *>(part(p) + x * D + col));
-                        const float k = ex2_approx(y.x - top);
-                        l = fmaf(y.y, k, l);
-                        v = make_float4(fmaf(z.x, k, v.x), fmaf(z.y, k, v.y), fmaf(z.z, k, v.z), fmaf(z.w, k, v.w));
+                    for (int p0 = 0; p0 < parts; p0 += AT_JOIN) {  // AT_JOIN records on their way at a time
+                        float2 y[AT_JOIN];
+                        float4 z[AT_JOIN];
+#pragma unroll
+                        for (int p = 0; p < AT_JOIN; ++p) {
+                            const bool there = p0 + p < parts;
+                            y[p] = there ? __ldcg(reinterpret_cast<const float2 *>(part(p0 + p) + S::HEADS * D + 2 * x)) : make_float2(-FLT_MAX, 0.0f);
+                            z[p] = there ? __ldcg(reinterpret_cast<const float4 *>(part(p0 + p) + x * D + col)) : make_float4(0, 0, 0, 0);
+                        }
+                        float now = top;
+#pragma unroll
+                        for (int p = 0; p < AT_JOIN; ++p) now = fmaxf(now, y[p].x);
+                        const float f = ex2_approx(top - now);
+                        top = now;
+                        l *= f;
+                        v = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+#pragma unroll
+                        for (int p = 0; p < AT_JOIN; ++p) {
+                            const float k = ex2_approx(y[p].x - top);
+                            l = fmaf(y[p].y, k, l);
+                            v = make_float4(fmaf(z[p].x, k, v.x), fmaf(z[p].y, k, v.y), fmaf(z[p].z, k, v.z), fmaf(z[p].w, k, v.w));
+                        }
                     }
                     attn_store(a, row0 + x, D, col, v, l);
                     if (a.lse && col == 0) a.lse[row0 + x] = (top + log2f(l)) * kLn2;
                 }
             }
         }
-        // ---- on to the next item
-        use.left -= n_units;
-        if (use.left > 0) {
-            use.unit = 0;
-            use.next_item(a);
-        }
     }
     cp_async_wait<0>();
 }
 
-template <bool E4M3, int D, int NT, bool SPLIT>
+template <bool E4M3, int D, int NT, bool FINE>
 cudaError_t launch_attn_shape(const AttnArgs &a, int64_t most_units, cudaStream_t st)
 {
     using S = AttnShape<E4M3, D, NT>;
-    const auto kernel = attn_decode_kernel<E4M3, D, NT, SPLIT>;
+    const auto kernel = attn_decode_kernel<E4M3, D, NT, FINE>;
     if (cudaError_t e = opt_in_smem(reinterpret_cast<const void *>(kernel), S::SMEM); e != cudaSuccess) return e;
     const int64_t room = static_cast<int64_t>(num_sms()) * S::CTAS;
     const int grid = static_cast<int>(most_units < 1 ? 1 : most_units < room ? most_units : room);
@@ -751,11 +936,12 @@ cudaError_t launch_attn_dim(const AttnArgs &a, int64_t most_units, cudaStream_t 
     template <>                                                                                                    \
     cudaError_t launch_attn_dim<E4M3, D>(const AttnArgs &a, int64_t most_units, cudaStream_t st)                   \
     {                                                                                                              \
+        const bool fine = !a.q_bf16 || !a.out_bf16;                                                                \
         if (a.group <= 8)                                                                                          \
-            return a.out_bf16 ? launch_attn_shape<E4M3, D, 1, false>(a, most_units, st)                            \
-                              : launch_attn_shape<E4M3, D, 1, true>(a, most_units, st);                            \
-        return a.out_bf16 ? launch_attn_shape<E4M3, D, 2, false>(a, most_units, st)                                \
-                          : launch_attn_shape<E4M3, D, 2, true>(a, most_units, st);                                \
+            return fine ? launch_attn_shape<E4M3, D, 1, true>(a, most_units, st)                                   \
+                        : launch_attn_shape<E4M3, D, 1, false>(a, most_units, st);                                 \
+        return fine ? launch_attn_shape<E4M3, D, 2, true>(a, most_units, st)                                       \
+                    : launch_attn_shape<E4M3, D, 2, false>(a, most_units, st);                                     \
     }
 
 }  // namespace qg
