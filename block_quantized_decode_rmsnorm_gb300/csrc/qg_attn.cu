@@ -1,6 +1,10 @@
 // Decode attention: the workspace and the choice of kernel (qg_attn.cuh).
 #include "qg_attn.cuh"
 
+#ifndef QG_AT_DIRECT
+#define QG_AT_DIRECT 4
+#endif
+
 namespace qg {
 
 namespace {
@@ -64,6 +68,16 @@ int64_t attn_most_places(const KvPlanes &c, int64_t batch, int64_t q_heads, int6
     return batch * c.heads * ((group + s.heads - 1) / s.heads) * ((tokens + s.unit - 1) / s.unit + s.cost);
 }
 
+// The direct form's CTAs to an item, 0 for the line.
+int direct_cluster(int64_t items, int64_t most, const Sizes &s)
+{
+    const int64_t units = most / items - s.cost;
+    int n = 1;
+    while (n < AT_CLUSTER && n < units && items * n * 2 <= num_sms()) n *= 2;
+    const int64_t room = static_cast<int64_t>(num_sms()) * s.ctas;
+    return items * n <= room && (units + n - 1) / n <= QG_AT_DIRECT ? n : 0;
+}
+
 cudaError_t launch_attn_decode(const KvPlanes &c, const void *q, int64_t q_row, int64_t q_head, int q_dtype,
                                int64_t batch, int64_t q_heads, const int32_t *pages, int64_t max_pages,
                                const int32_t *lengths, float scale, int64_t window, void *out, int out_dtype,
@@ -80,11 +94,15 @@ cudaError_t launch_attn_decode(const KvPlanes &c, const void *q, int64_t q_row, 
     a.group = static_cast<int>(group), a.q_heads = static_cast<int>(q_heads);
     a.chunks = static_cast<int>((group + s.heads - 1) / s.heads);
     a.page_shift = shift;
-    a.batch = batch, a.pages = pages, a.lengths = lengths, a.max_pages = max_pages, a.window = window, a.scale = scale;
+    a.batch = batch, a.pages = pages, a.lengths = lengths, a.max_pages = max_pages, a.scale = scale;
+    a.held = static_cast<int>(max_pages * c.page);
+    a.window = window < a.held ? static_cast<int>(window) : 0;  // one that reaches over the whole table is none
     a.out = out, a.out_bf16 = out_dtype == QG_BF16, a.lse = lse;
     a.counters = static_cast<int *>(workspace);
     a.records = reinterpret_cast<float *>(static_cast<char *>(workspace) + counter_bytes());
     const int64_t most = attn_most_places(c, batch, q_heads, max_pages, window);
+    a.narrow = most < (int64_t(1) << 31);
+    a.cluster = direct_cluster(batch * c.heads * a.chunks, most, s);
     return c.e4m3 ? launch_for<true>(a, most, st) : launch_for<false>(a, most, st);
 }
 

@@ -43,6 +43,8 @@ constexpr int AT_WARPS = 4;
 constexpr int AT_THREADS = 32 * AT_WARPS;
 constexpr int AT_CTAS_MAX = 4;  // per SM
 constexpr int AT_JOIN = 8;
+constexpr int AT_FEW = 4;  // rows of 32 sequences that every warp scans for itself
+constexpr int AT_CLUSTER = 8;
 
 struct AttnArgs {
     KvPlanes c;
@@ -52,17 +54,26 @@ struct AttnArgs {
     int page_shift;                      // log2 of the page size, or -1
     int64_t batch;
     const int32_t *pages, *lengths;
-    int64_t max_pages, window;
+    int64_t max_pages;
+    int held, window;  // tokens that a page table holds; 0: no window
     float scale;
     void *out;
     int out_bf16;
     float *lse;
     int *counters;   // one per CTA, zero between calls
     float *records;  // two per CTA
+    int cluster;     // direct form: CTAs to an item
+    bool narrow;     // the line has fewer than 2^31 places
 };
 
 #ifndef QG_AT_CH
 #define QG_AT_CH 2
+#endif
+#ifndef QG_AT_WCH
+#define QG_AT_WCH 1
+#endif
+#ifndef QG_AT_WSTAGES
+#define QG_AT_WSTAGES 2
 #endif
 #ifndef QG_AT_STAGES
 #define QG_AT_STAGES 2
@@ -74,21 +85,19 @@ struct AttnArgs {
 #define QG_AT_LEAST 1
 #endif
 #ifndef QG_AT_CTAS
-#define QG_AT_CTAS (D <= 96 ? 4 : 2)
+#define QG_AT_CTAS (D <= 64 ? 4 : D <= 96 ? 3 : 2)
 #endif
 
 template <bool E4M3, int D, int NT>
 struct AttnShape {
     static constexpr int NB = kv_blocks(E4M3, D);
     static constexpr int SB = E4M3 ? 4 : 2;      // bytes of a scale
-    static constexpr int CH = D <= 128 ? QG_AT_CH : 1;  // tiles of 16 tokens to a step
+    static constexpr int CH = D <= 128 ? QG_AT_CH : QG_AT_WCH;  // tiles of 16 tokens to a step
     static constexpr int TOK = KV_TILE * CH;
-    static constexpr int STAGES = D <= 128 ? QG_AT_STAGES : 3;
-    static constexpr bool SWIZZLE = D % 128 == 0;
-    static constexpr int KS = SWIZZLE ? D : D % 64 == 32 ? D : D + 32;  // padded rows of keys: 32 or 96 bytes past a multiple of 128
-    static constexpr int VS = SWIZZLE ? D : D + 16;                     // and of values: 16 bytes past a multiple of 32
+    static constexpr int STAGES = D <= 128 ? QG_AT_STAGES : QG_AT_WSTAGES;
     static constexpr int SCALES = KV_TILE * NB * SB;      // bytes of a tile's scales
-    static constexpr int TILE = KV_TILE * (KS + VS) + 2 * SCALES;
+    static constexpr int CODES = KV_TILE * D;             // and of its keys' or values' codes
+    static constexpr int TILE = 2 * CODES + 2 * SCALES;
     static constexpr int STAGE = CH * TILE;
     static constexpr int HEADS = 8 * NT;
     static constexpr int OROW = D + 4;  // floats of a head's row when warps meet
@@ -96,25 +105,41 @@ struct AttnShape {
     static constexpr int RING = AT_WARPS * STAGES * STAGE;
     static constexpr int QF = HEADS * D * 4;  // bytes of q's fragments
     static constexpr int SMEM = RING + QF + AT_WARPS * HEADS * 8 + HEADS * 4 + HEADS * NB * 4;
+    static constexpr int RECORD_AT = (SMEM + 15) / 16 * 16;  // direct form: the CTA's part behind it
     static constexpr int CTAS = 227 * 1024 / (SMEM + 1024) < QG_AT_CTAS ? 227 * 1024 / (SMEM + 1024) : QG_AT_CTAS;
     static constexpr int RECORD = HEADS * (D + 2);  // floats
     static constexpr int COST = QG_AT_COST;  // of an item's beginning and end, in units
     static constexpr int QW = HEADS / AT_WARPS, QP = (D / 4 + 31) / 32;  // heads of q to a warp, 4 values a lane each
 
-    // Where 16-byte piece c of row r lies in a tile's keys or values.  Swizzled, the eight pieces of 128 bytes change
-    // places with the row, so that the fragments' rows (keys: any four following ones; values: any four even ones) lie in
-    // banks of their own.
-    static __device__ __forceinline__ int key_at(int r, int c) { return SWIZZLE ? r * KS + ((c ^ (r & 3) << 1) << 4) : r * KS + (c << 4); }
-    static __device__ __forceinline__ int value_at(int r, int c) { return SWIZZLE ? r * VS + ((c ^ (r >> 1 & 3) << 1) << 4) : r * VS + (c << 4); }
+    // A tile's keys or values in shared memory.  A step's fragments are 32-byte pieces of four rows at a time, which have
+    // to lie in banks of their own, and copies are fastest into whole lines of 128 bytes: so rows are unpadded and the
+    // 32-byte pieces of a line change places with the row.  Rows of 96 and 192 bytes are two planes, of 64 and 32 and
+    // of 128 and 64 bytes to a row.  Values' rows are permuted, for their fragments take every other row.
+    static __host__ __device__ constexpr int plane(int piece) { return D == 96 ? (piece < 2 ? 64 : 32) : D == 192 ? (piece < 4 ? 128 : 64) : D; }
+    static __host__ __device__ constexpr int plane_at(int piece) { return D == 96 && piece >= 2 ? KV_TILE * 64 : D == 192 && piece >= 4 ? KV_TILE * 128 : 0; }
+    static __host__ __device__ constexpr int first_piece(int piece) { return D == 96 && piece >= 2 ? 2 : D == 192 && piece >= 4 ? 4 : 0; }
+    static __device__ __forceinline__ int at(int r, int piece)
+    {
+        const int w = plane(piece), d = piece - first_piece(piece);
+        return plane_at(piece) + r * w + ((w >= 128 ? d ^ (r & 3) : w == 64 ? d ^ (r >> 1 & 1) : d) << 5);
+    }
+    // 16-byte piece c of row r.
+    static __device__ __forceinline__ int key_at(int r, int c) { return at(r, c >> 1) + ((c & 1) << 4); }
+    static __device__ __forceinline__ int value_at(int r, int c) { return key_at((r & 8) | (r & 1) << 2 | (r >> 1 & 3), c); }
+    static constexpr int NX = D >= 128 && D != 192 ? 4 : D / 32;  // pieces whose places differ by more than a constant
+    static __host__ __device__ constexpr int piece_at(int piece) { return D == 256 ? piece / 4 * 128 : 0; }  // that constant
 };
 
+#ifndef QG_V_VOL
+#define QG_V_VOL
+#endif
 struct Quad {
     float v[4];
 };
 __device__ __forceinline__ Quad mma_f16(uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1, const Quad &c)
 {
     Quad d;
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+    asm QG_V_VOL ("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
                  "{%10,%11,%12,%13};"
                  : "=f"(d.v[0]), "=f"(d.v[1]), "=f"(d.v[2]), "=f"(d.v[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c.v[0]), "f"(c.v[1]), "f"(c.v[2]), "f"(c.v[3]));
@@ -125,7 +150,7 @@ __device__ __forceinline__ Quad mma_f16(uint32_t a0, uint32_t a1, uint32_t a2, u
 __device__ __forceinline__ Quad mma_f16(uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
 {
     Quad d;
-    asm volatile("{ .reg .f32 z; mov.f32 z, 0f00000000; mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+    asm QG_V_VOL ("{ .reg .f32 z; mov.f32 z, 0f00000000; mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
                  "{%8,%9}, {z,z,z,z}; }"
                  : "=f"(d.v[0]), "=f"(d.v[1]), "=f"(d.v[2]), "=f"(d.v[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -208,9 +233,8 @@ struct Seen {
 };
 __device__ __forceinline__ Seen seen_of(const AttnArgs &a, int64_t b)
 {
-    const int64_t held = a.max_pages * a.c.page;  // < 2^31
-    const int n = static_cast<int>(min(static_cast<int64_t>(max(a.lengths[b], 0)), held));
-    return {a.window > 0 && a.window < n ? n - static_cast<int>(a.window) : 0, n};
+    const int n = min(max(a.lengths[b], 0), a.held);
+    return {a.window > 0 ? max(n - a.window, 0) : 0, n};
 }
 
 template <bool E4M3, int D, int NT, bool FINE>
@@ -277,6 +301,28 @@ struct Attn {
                 if (any && t < p.seen.n && t + KV_TILE > p.seen.first) page[i] = row[col];
             }
         }
+        // The same for a sequence seen from its first token on, before its length is known, ...
+        __device__ __forceinline__ void guess(const AttnArgs &a, const Place &p, int warp)
+        {
+            at = (p.unit() * AT_WARPS + warp) * TOK;
+            const int32_t *const row = a.pages + p.b * a.max_pages;
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+                const int t = at + i * KV_TILE;
+                const uint32_t col = a.page_shift >= 0 ? static_cast<uint32_t>(t) >> a.page_shift : static_cast<uint32_t>(t) / static_cast<uint32_t>(a.c.page);
+                off[i] = t - col * a.c.page;
+                page[i] = -1;
+                if (col < a.max_pages) page[i] = row[col];
+            }
+        }
+        // ... and once it is.
+        __device__ __forceinline__ void keep(const Place &p)
+        {
+            any = p.left > 0 && at < p.seen.n;
+#pragma unroll
+            for (int i = 0; i < CH; ++i)
+                if (at + i * KV_TILE >= p.seen.n) page[i] = -1;
+        }
     };
 
     // Start the copies of a step into a stage.  Rows outside the tokens seen are zeros (their codes may be NaN's); their
@@ -286,7 +332,7 @@ struct Attn {
     static __device__ __forceinline__ void copy_tile(const AttnArgs &a, Seen seen, int t, int64_t row, uint32_t dk, int lane)
     {
         const uint8_t *k = a.c.kq + row * D + lane * 16, *v = a.c.vq + row * D + lane * 16;
-        const uint32_t dv = dk + KV_TILE * S::KS, ds = dv + KV_TILE * S::VS;
+        const uint32_t dv = dk + S::CODES, ds = dv + S::CODES;
 #pragma unroll
         for (int j = 0; j < D / 32; ++j) {
             const int u = lane + 32 * j, r = u / (D / 16), c = u % (D / 16);
@@ -358,31 +404,48 @@ struct Attn {
     }
 
     // Query heads warp, warp + AT_WARPS, ... of a place's item: lane's pieces of four values.
-    static __device__ __forceinline__ void load_query(const AttnArgs &a, const Place &p, float4 (&v)[S::QW][S::QP], int warp, int lane)
-    {
-        const int h = a.chunks == 1 ? p.item : p.item / a.chunks, h0 = (p.item - h * a.chunks) * S::HEADS;
+    struct Query {
+        uint4 v[S::QW][S::QP];  // as they lie in memory: bf16 in the first two words
+        __device__ __forceinline__ void load(const AttnArgs &a, const Place &p, int warp, int lane)
+        {
+            const int h = a.chunks == 1 ? p.item : p.item / a.chunks, h0 = (p.item - h * a.chunks) * S::HEADS;
+            const int size = !FINE || a.q_bf16 ? 2 : 4;
+            const uint8_t *const row = static_cast<const uint8_t *>(a.q) + (p.b * a.q_row + (h * a.group + h0) * a.q_head) * size;
 #pragma unroll
-        for (int y = 0; y < S::QW; ++y)
+            for (int y = 0; y < S::QW; ++y)
 #pragma unroll
-            for (int i = 0; i < S::QP; ++i) {
-                const int x = h0 + y * AT_WARPS + warp, piece = lane + 32 * i;
-                v[y][i] = make_float4(0, 0, 0, 0);
-                if (x < a.group && piece < D / 4) {
-                    const int64_t at = p.b * a.q_row + (h * a.group + x) * a.q_head + piece * 4;
-                    v[y][i] = a.q_bf16 ? Vec4<__nv_bfloat16>::widen(*reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(a.q) + at))
-                                       : *reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) + at);
+                for (int i = 0; i < S::QP; ++i) {
+                    const int x = y * AT_WARPS + warp, piece = lane + 32 * i;
+                    v[y][i] = make_uint4(0, 0, 0, 0);
+                    if (h0 + x < a.group && piece < D / 4) {
+                        const uint8_t *const at = row + (x * a.q_head + piece * 4) * size;
+                        if (FINE && !a.q_bf16) {
+                            v[y][i] = *reinterpret_cast<const uint4 *>(at);
+                        } else {
+                            const uint2 w = *reinterpret_cast<const uint2 *>(at);
+                            v[y][i].x = w.x, v[y][i].y = w.y;
+                        }
+                    }
                 }
-            }
-    }
+        }
+        __device__ __forceinline__ float4 get(const AttnArgs &a, int y, int i) const
+        {
+            const uint4 w = v[y][i];
+            if (FINE && !a.q_bf16) return make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w));
+            return Vec4<__nv_bfloat16>::widen(make_uint2(w.x, w.y));
+        }
+    };
 
     // Their fragments, factors and (OFFSET) blocks' sums to shared memory.
-    static __device__ __forceinline__ void put_query(const AttnArgs &a, const float4 (&all)[S::QW][S::QP], uint4 *qf, float *qc, float *qz,
+    static __device__ __forceinline__ void put_query(const AttnArgs &a, const Query &query, uint4 *qf, float *qc, float *qz,
                                                      int warp, int lane)
     {
 #pragma unroll
         for (int y = 0; y < S::QW; ++y) {
             const int x = y * AT_WARPS + warp;
-            const float4(&v)[S::QP] = all[y];
+            float4 v[S::QP];
+#pragma unroll
+            for (int i = 0; i < S::QP; ++i) v[i] = query.get(a, y, i);
             float top = 0.0f;
             bool odd = false;  // infinities or NaN in the row: no factor
 #pragma unroll
@@ -435,19 +498,18 @@ struct Attn {
     __device__ __forceinline__ void step(const uint8_t *st, const uint4 *qf, const float *qz, int at, Seen seen, uint32_t bad, int lane)
     {
         const int g = lane >> 2, t = lane & 3;
-        constexpr int DX = S::SWIZZLE ? 4 : 1;  // offsets that differ by more than a constant
-        const uint8_t *kx[DX], *vx[DX];
+        const uint8_t *kx[S::NX], *vx[S::NX];
 #pragma unroll
-        for (int i = 0; i < DX; ++i) {
-            kx[i] = st + S::key_at(g, 2 * i + (t >> 1)) + (t & 1) * 8;
-            vx[i] = st + KV_TILE * S::KS + S::value_at(2 * t, 2 * i + (g >> 2)) + (g & 3) * 4;
+        for (int i = 0; i < S::NX; ++i) {
+            kx[i] = st + S::at(g, i) + t * 8;
+            vx[i] = st + S::CODES + S::at(t, i) + g * 4;  // row 2 t; rows 2 t + 1, + 8, + 9 lie 4, 8, 12 places on
         }
         // ---- scores
         float s[NT][2 * CH][2];
         PairScales<E4M3, NB> dk[2 * CH];
 #pragma unroll
         for (int j = 0; j < 2 * CH; ++j)
-            dk[j].load(st + (j / 2) * S::TILE + KV_TILE * (S::KS + S::VS) + ((j % 2) * 8 + 2 * t) * NB * S::SB);
+            dk[j].load(st + (j / 2) * S::TILE + 2 * S::CODES + ((j % 2) * 8 + 2 * t) * NB * S::SB);
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
             Quad acc[ST][2 * CH];
@@ -462,7 +524,7 @@ struct Attn {
                 }
 #pragma unroll
                 for (int j = 0; j < 2 * CH; ++j) {
-                    const uint2 w = *reinterpret_cast<const uint2 *>(kx[dg % DX] + (dg - dg % DX) * 32 + (j / 2) * S::TILE + (j % 2) * 8 * S::KS);
+                    const uint2 w = *reinterpret_cast<const uint2 *>(kx[dg % S::NX] + S::piece_at(dg) + (j / 2) * S::TILE + (j % 2) * 8 * S::plane(dg));
                     const uint32_t x = code_bits<E4M3>(w.x), y = code_bits<E4M3>(w.y);
                     const uint32_t b0 = codes_f16<E4M3, OFFSET, false>(x), b1 = codes_f16<E4M3, OFFSET, true>(x);
                     const uint32_t b2 = codes_f16<E4M3, OFFSET, false>(y), b3 = codes_f16<E4M3, OFFSET, true>(y);
@@ -493,7 +555,7 @@ struct Attn {
 #pragma unroll
         for (int j = 0; j < 2 * CH; ++j) {
             PairScales<E4M3, NB> d;
-            d.load(st + (j / 2) * S::TILE + KV_TILE * (S::KS + S::VS) + S::SCALES + ((j % 2) * 8 + 2 * t) * NB * S::SB);
+            d.load(st + (j / 2) * S::TILE + 2 * S::CODES + S::SCALES + ((j % 2) * 8 + 2 * t) * NB * S::SB);
 #pragma unroll
             for (int b = 0; b < NB; ++b) dv[j][0][b] = d.get(0, b), dv[j][1][b] = d.get(1, b);
         }
@@ -590,11 +652,11 @@ struct Attn {
                 Quad acc[NT][2];
 #pragma unroll
                 for (int ch = 0; ch < CH; ++ch) {
-                    const uint8_t *v = vx[dg % DX] + (dg - dg % DX) * 32 + ch * S::TILE;
+                    const uint8_t *v = vx[dg % S::NX] + S::piece_at(dg) + ch * S::TILE;
                     const uint32_t v0 = code_bits<E4M3>(*reinterpret_cast<const uint32_t *>(v));
-                    const uint32_t v1 = code_bits<E4M3>(*reinterpret_cast<const uint32_t *>(v + S::VS));
-                    const uint32_t v8 = code_bits<E4M3>(*reinterpret_cast<const uint32_t *>(v + 8 * S::VS));
-                    const uint32_t v9 = code_bits<E4M3>(*reinterpret_cast<const uint32_t *>(v + 9 * S::VS));
+                    const uint32_t v1 = code_bits<E4M3>(*reinterpret_cast<const uint32_t *>(v + 4 * S::plane(dg)));
+                    const uint32_t v8 = code_bits<E4M3>(*reinterpret_cast<const uint32_t *>(v + 8 * S::plane(dg)));
+                    const uint32_t v9 = code_bits<E4M3>(*reinterpret_cast<const uint32_t *>(v + 12 * S::plane(dg)));
                     const uint32_t x0 = __byte_perm(v0, v1, 0x5140), x1 = __byte_perm(v0, v1, 0x7362);
                     const uint32_t y0 = __byte_perm(v8, v9, 0x5140), y1 = __byte_perm(v8, v9, 0x7362);
                     const uint32_t va[2][4] = {{codes_f16<E4M3, OFFSET, false>(x0), codes_f16<E4M3, OFFSET, true>(x0),
@@ -653,12 +715,10 @@ __device__ __forceinline__ void attn_store(const AttnArgs &a, int64_t row, int d
 struct Share {
     int64_t each, more;
     int ctas;
-    __device__ __forceinline__ Share(int64_t total, int cost, unsigned grid)
+    __device__ __forceinline__ Share(int64_t total, unsigned grid)
     {
-        // no shorter than QG_AT_LEAST
-        const int least = QG_AT_LEAST;
         if (total < (int64_t(1) << 31)) {
-            const uint32_t t = static_cast<uint32_t>(total), n = max(min(t / least, grid), t > 0 ? 1u : 0u);
+            const uint32_t t = static_cast<uint32_t>(total), n = min(t, grid);
             ctas = static_cast<int>(n);
             each = n ? t / n : 0;
             more = n ? t % n : 0;
@@ -679,143 +739,327 @@ struct Share {
     }
 };
 
-template <bool E4M3, int D, int NT, bool FINE>
-__global__ void __launch_bounds__(AT_THREADS, AttnShape<E4M3, D, NT>::CTAS) attn_decode_kernel(const __grid_constant__ AttnArgs a)
+// Outputs of a sequence that sees nothing: query heads [first, first + heads).
+template <int D>
+__device__ __forceinline__ void attn_nothing(const AttnArgs &a, int64_t b, int first, int heads)
 {
+    const int64_t row = b * a.q_heads + first;
+    for (int i = threadIdx.x; i < heads * (D / 4); i += AT_THREADS)
+        attn_store(a, row + i / (D / 4), D, i % (D / 4) * 4, make_float4(0, 0, 0, 0), 1.0f);
+    if (a.lse)
+        for (int i = threadIdx.x; i < heads; i += AT_THREADS) a.lse[row + i] = -__int_as_float(0x7f800000);
+}
+
+__device__ __forceinline__ float2 ld_cluster_f2(const float *local, uint32_t rank)
+{
+    uint32_t remote;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_addr(local)), "r"(rank));
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(remote) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 ld_cluster_f4(const float *local, uint32_t rank)
+{
+    uint32_t remote;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_addr(local)), "r"(rank));
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(remote) : "memory");
+    return v;
+}
+
+// What a warp copies ahead of its steps.
+template <bool E4M3, int D, int NT, bool FINE>
+struct Feed {
     using S = AttnShape<E4M3, D, NT>;
     using A = Attn<E4M3, D, NT, FINE>;
-    extern __shared__ __align__(16) uint8_t smem[];
-    uint4 *const qf = reinterpret_cast<uint4 *>(smem + S::RING);
-    float2 *const ml = reinterpret_cast<float2 *>(smem + S::RING + S::QF);  // [warp][head]: m, l
-    float *const qc = reinterpret_cast<float *>(ml + AT_WARPS * S::HEADS), *const qz = qc + S::HEADS;
-    __shared__ int64_t sums[AT_WARPS];
-    __shared__ int64_t found_b;
-    __shared__ int found_item, found_at;
-    __shared__ int last_one;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int cta = blockIdx.x, items = a.c.heads * a.chunks;
-    pdl_wait();
-    pdl_trigger();
-
-    // ---- this CTA's stretch of the line: a scan over the sequences, a slice to a thread
-    const int64_t per = (a.batch + AT_THREADS - 1) / AT_THREADS;
-    const int64_t b0 = min(tid * per, a.batch), b1 = min(b0 + per, a.batch);
-    bool empty = false;  // a sequence without tokens whose outputs this CTA writes
-    int64_t mine = 0;
-    int units0 = 0;  // of sequence b0
-    for (int64_t b = b0; b < b1; ++b) {
-        const int n = A::units(seen_of(a, b));
-        if (b == b0) units0 = n;
-        mine += n > 0 ? static_cast<int64_t>(n + S::COST) * items : 0;
-        empty |= n == 0 && b % gridDim.x == cta;
-    }
-    int64_t incl = mine;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const int64_t up = __shfl_up_sync(0xffffffffu, incl, off);
-        if (lane >= off) incl += up;
-    }
-    if (lane == 31) sums[warp] = incl;
-    const bool any_empty = __syncthreads_or(empty);
-    int64_t total = 0;
-#pragma unroll
-    for (int w = 0; w < AT_WARPS; ++w) {
-        if (w < warp) incl += sums[w];
-        total += sums[w];
-    }
-    if (any_empty) {
-        for (int64_t b = cta; b < a.batch; b += gridDim.x) {
-            const Seen s = seen_of(a, b);
-            if (s.n > s.first) continue;
-            for (int i = tid; i < a.q_heads * (D / 4); i += AT_THREADS)
-                attn_store(a, b * a.q_heads + i / (D / 4), D, i % (D / 4) * 4, make_float4(0, 0, 0, 0), 1.0f);
-            if (a.lse)
-                for (int i = tid; i < a.q_heads; i += AT_THREADS) a.lse[b * a.q_heads + i] = -__int_as_float(0x7f800000);
-        }
-    }
-    const Share share(total, S::COST, gridDim.x);
-    if (cta >= share.ctas) return;
-    const int64_t start = share.start(cta), end = share.start(cta + 1);
-    if (start >= incl - mine && start < incl) {
-        int64_t at = incl - mine, b = b0;
-        int n = units0;
-        for (;;) {
-            const int64_t cost = n > 0 ? static_cast<int64_t>(n + S::COST) * items : 0;
-            if (start < at + cost) break;
-            at += cost;
-            n = A::units(seen_of(a, ++b));
-        }
-        const int64_t into = start - at;
-        const int item = into < INT32_MAX ? static_cast<int>(into) / (n + S::COST) : static_cast<int>(into / (n + S::COST));
-        found_b = b;
-        found_item = item;
-        found_at = static_cast<int>(into - static_cast<int64_t>(item) * (n + S::COST));
-    }
-    __syncthreads();
-    typename A::Place use;
-    use.b = static_cast<int>(found_b);
-    use.seen = seen_of(a, use.b);
-    use.units = A::units(use.seen);
-    use.item = found_item;
-    use.at = found_at;
-    use.left = static_cast<int>(end - start);  // the host's bound on the line keeps it below 2^31
-    if (use.units == 0) return;  // the lengths have changed under the call
-    use.settle();
-    if (use.left <= 0) return;
-
-    float4 qv[S::QW][S::QP];
-    A::load_query(a, use, qv, warp, lane);
-    // ---- the first copies
-    const uint32_t ring = smem_addr(smem) + warp * S::STAGES * S::STAGE;
-    typename A::Place load = use;
+    typename A::Place load;
     typename A::Step ahead;
-    ahead.find(a, load, warp);
-    uint32_t bad = 0;  // CH bits per stage
-    auto copy_next = [&](int stage) {
+    uint32_t bad, ring;  // bad: CH bits per stage
+
+    // The copies of the step ahead into a stage, and on to the one after it: the next unit of the stretch, or
+    // (STRIDE > 0) of the item.
+    template <bool DIRECT>
+    __device__ __forceinline__ void next(const AttnArgs &a, int stage, int stride, int warp, int lane)
+    {
         if (ahead.any) {
             const uint32_t x = A::copy(a, load, ahead, ring + stage * S::STAGE, lane);
             bad = (bad & ~(((1u << S::CH) - 1) << (stage * S::CH))) | x << (stage * S::CH);
         }
         cp_async_commit();
         if (load.left > 0) {
-            load.next(a);
+            if constexpr (DIRECT) {
+                --load.left;
+                load.at += stride;
+            } else {
+                load.next(a);
+            }
             ahead.find(a, load, warp);
         }
-    };
+    }
+};
+
+// n_units units of an item, `stride` apart from unit0 on, after the copies of the first STAGES - 1 have begun.  Returns
+// the stage that was read last.
+template <bool DIRECT, bool E4M3, int D, int NT, bool FINE>
+__device__ __forceinline__ int attn_units(const AttnArgs &a, Attn<E4M3, D, NT, FINE> &state, Feed<E4M3, D, NT, FINE> &feed, Seen seen,
+                                          int unit0, int n_units, int stride, int &stage, const uint8_t *smem, const uint4 *qf,
+                                          const float *qz, int warp, int lane)
+{
+    using S = AttnShape<E4M3, D, NT>;
+    int last = 0;
+#ifndef QG_V_UNROLL
+#pragma unroll 1
+#endif
+    for (int u = 0; u < n_units; ++u) {
+        feed.template next<DIRECT>(a, stage == 0 ? S::STAGES - 1 : stage - 1, stride, warp, lane);
+        cp_async_wait<S::STAGES - 1>();
+        __syncwarp();
+        const int step = static_cast<uint32_t>(seen.first) / S::TOK + (unit0 + u * stride) * AT_WARPS + warp, at = step * S::TOK;
+        const uint8_t *const st = smem + (warp * S::STAGES + stage) * S::STAGE;
+        const uint32_t off = feed.bad >> (stage * S::CH) & ((1u << S::CH) - 1);
+        if (at < seen.n) {
+            if (at < seen.first || at + S::TOK > seen.n || off != 0)
+                state.template step<true>(st, qf, qz, at, seen, off, lane);
+            else
+                state.template step<false>(st, qf, qz, at, seen, 0, lane);
+        }
+        __syncwarp();
+        last = stage;
+        stage = stage + 1 == S::STAGES ? 0 : stage + 1;
+    }
+    return last;
+}
+
+// The warps meet, eight heads at a time, each in its stage `last`, into which no copy is under way.
+// out(head, column, four sums, their reference, the sum of weights).
+template <bool E4M3, int D, int NT, bool FINE, typename Out>
+__device__ __forceinline__ void attn_meet(const Attn<E4M3, D, NT, FINE> &state, uint8_t *smem, int last, float2 *ml, int heads, const Out &out)
+{
+    using S = AttnShape<E4M3, D, NT>;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    float *const meet = reinterpret_cast<float *>(smem + last * S::STAGE);
+    constexpr int MEET = S::STAGES * S::STAGE / 4;  // floats from warp to warp
 #pragma unroll
-    for (int i = 0; i < S::STAGES - 1; ++i) copy_next(i);
+    for (int i = 0; i < NT; ++i) {
+        if (i > 0) __syncthreads();
+        float l = state.l[i];
+        l += __shfl_xor_sync(0xffffffffu, l, 1);
+        l += __shfl_xor_sync(0xffffffffu, l, 2);
+        if ((lane & 3) == 0) ml[warp * S::HEADS + 8 * i + (lane >> 2)] = make_float2(state.m[i], l);
+        float *const to = meet + warp * MEET + 2 * (lane & 3) * S::OROW + (lane >> 2) * 4;
+#pragma unroll
+        for (int dg = 0; dg < D / 32; ++dg) {
+            const float(&p)[4] = state.o[i][2 * dg].v, (&r)[4] = state.o[i][2 * dg + 1].v;
+            *reinterpret_cast<float4 *>(to + dg * 32) = make_float4(p[0], p[2], r[0], r[2]);
+            *reinterpret_cast<float4 *>(to + S::OROW + dg * 32) = make_float4(p[1], p[3], r[1], r[3]);
+        }
+        __syncthreads();
+        for (int j = tid; j < min(heads - 8 * i, 8) * (D / 4); j += AT_THREADS) {
+            const int y = j / (D / 4), x = 8 * i + y, col = j % (D / 4) * 4;
+            float top = -FLT_MAX, sum = 0.0f;
+            float4 v = make_float4(0, 0, 0, 0);
+#pragma unroll
+            for (int w = 0; w < AT_WARPS; ++w) top = fmaxf(top, ml[w * S::HEADS + x].x);
+#pragma unroll
+            for (int w = 0; w < AT_WARPS; ++w) {
+                const float2 part = ml[w * S::HEADS + x];
+                const float k = ex2_approx(part.x - top);
+                const float4 z = *reinterpret_cast<const float4 *>(meet + w * MEET + y * S::OROW + col);
+                sum = fmaf(part.y, k, sum);
+                v = make_float4(fmaf(z.x, k, v.x), fmaf(z.y, k, v.y), fmaf(z.z, k, v.z), fmaf(z.w, k, v.w));
+            }
+            out(x, col, v, top, sum);
+        }
+    }
+}
+
+// Parts of an item joined in order, AT_JOIN of them on their way at a time.  part(p, y, z): part p's reference and sum
+// of weights, and its four sums.
+template <typename Part>
+__device__ __forceinline__ void attn_join(int parts, const Part &part, float4 &v, float &top, float &l)
+{
+    top = -FLT_MAX, l = 0.0f;
+    v = make_float4(0, 0, 0, 0);
+    for (int p0 = 0; p0 < parts; p0 += AT_JOIN) {
+        float2 y[AT_JOIN];
+        float4 z[AT_JOIN];
+#pragma unroll
+        for (int p = 0; p < AT_JOIN; ++p) {
+            y[p] = make_float2(-FLT_MAX, 0.0f);
+            z[p] = make_float4(0, 0, 0, 0);
+            if (p0 + p < parts) part(p0 + p, y[p], z[p]);
+        }
+        float now = top;
+#pragma unroll
+        for (int p = 0; p < AT_JOIN; ++p) now = fmaxf(now, y[p].x);
+        const float f = ex2_approx(top - now);
+        top = now;
+        l *= f;
+        v = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+#pragma unroll
+        for (int p = 0; p < AT_JOIN; ++p) {
+            const float k = ex2_approx(y[p].x - top);
+            l = fmaf(y[p].y, k, l);
+            v = make_float4(fmaf(z[p].x, k, v.x), fmaf(z[p].y, k, v.y), fmaf(z[p].z, k, v.z), fmaf(z[p].w, k, v.w));
+        }
+    }
+}
+
+__device__ __forceinline__ void attn_store_lse(const AttnArgs &a, int64_t row, int col, float top, float l)
+{
+    if (a.lse && col == 0) a.lse[row] = (top + log2f(l)) * kLn2;
+}
+
+template <bool E4M3, int D, int NT, bool FINE>
+__global__ void __launch_bounds__(AT_THREADS, AttnShape<E4M3, D, NT>::CTAS) attn_decode_kernel(const __grid_constant__ AttnArgs a)
+{
+    using S = AttnShape<E4M3, D, NT>;
+    using A = Attn<E4M3, D, NT, FINE>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    uint4 *const qf = reinterpret_cast<uint4 *>(smem + S::RING);
+    float2 *const ml = reinterpret_cast<float2 *>(smem + S::RING + S::QF);  // [warp][head]: m, l
+    float *const qc = reinterpret_cast<float *>(ml + AT_WARPS * S::HEADS), *const qz = qc + S::HEADS;
+    __shared__ int64_t sums[AT_WARPS];
+    __shared__ int64_t found_at;
+    __shared__ int found_b;
+    __shared__ int last_one;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int cta = blockIdx.x, items = a.c.heads * a.chunks;
+    pdl_wait();
+    pdl_trigger();
+
+    // ---- this CTA's stretch of the line, by a scan over the sequences
+    typename A::Place use;
+    int64_t total, start, end;
+    bool any_empty;  // a sequence without tokens whose outputs this CTA writes
+    if (a.narrow && a.batch <= 32 * AT_FEW) {  // every warp for itself, rows of 32 sequences: no barrier
+        int incl[AT_FEW], base = 0;
+        bool empty = false;
+#pragma unroll
+        for (int r = 0; r < AT_FEW; ++r) {
+            const int b = r * 32 + lane;
+            incl[r] = 0;
+            if (r * 32 >= a.batch) continue;
+            if (b < a.batch) {
+                const int n = A::units(seen_of(a, b));
+                incl[r] = n > 0 ? (n + S::COST) * items : 0;
+                empty |= n == 0 && b % gridDim.x == cta;
+            }
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int up = __shfl_up_sync(0xffffffffu, incl[r], off);
+                if (lane >= off) incl[r] += up;
+            }
+            incl[r] += base;
+            base = __shfl_sync(0xffffffffu, incl[r], 31);
+        }
+        any_empty = __any_sync(0xffffffffu, empty);
+        total = base;
+        base = 0;
+        const Share share(total, gridDim.x);
+        start = share.start(cta), end = share.start(cta + 1);
+        use.b = 0, use.at = static_cast<int>(start);
+        bool found = cta >= share.ctas;
+#pragma unroll
+        for (int r = 0; r < AT_FEW; ++r) {
+            if (found || r * 32 >= a.batch) continue;
+            const uint32_t past = __ballot_sync(0xffffffffu, incl[r] > static_cast<int>(start));
+            if (past) {
+                const int at = __ffs(past) - 1;
+                const int before = __shfl_sync(0xffffffffu, incl[r], at > 0 ? at - 1 : 0);
+                use.b = r * 32 + at;
+                use.at = static_cast<int>(start) - (at > 0 ? before : base);
+                found = true;
+            } else {
+                base = __shfl_sync(0xffffffffu, incl[r], 31);
+            }
+        }
+    } else {
+        const int64_t per = (a.batch + AT_THREADS - 1) / AT_THREADS;
+        const int64_t b0 = min(tid * per, a.batch), b1 = min(b0 + per, a.batch);
+        bool empty = false;
+        int64_t mine = 0;
+        for (int64_t b = b0; b < b1; ++b) {
+            const int n = A::units(seen_of(a, b));
+            mine += n > 0 ? static_cast<int64_t>(n + S::COST) * items : 0;
+            empty |= n == 0 && b % gridDim.x == cta;
+        }
+        int64_t incl = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int64_t up = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += up;
+        }
+        if (lane == 31) sums[warp] = incl;
+        any_empty = __syncthreads_or(empty);
+        total = 0;
+#pragma unroll
+        for (int w = 0; w < AT_WARPS; ++w) {
+            if (w < warp) incl += sums[w];
+            total += sums[w];
+        }
+        const Share share(total, gridDim.x);
+        start = share.start(cta), end = share.start(cta + 1);
+        if (cta < share.ctas && start >= incl - mine && start < incl) {
+            int64_t at = incl - mine, b = b0;
+            for (;; ++b) {
+                const int n = A::units(seen_of(a, b));
+                const int64_t cost = n > 0 ? static_cast<int64_t>(n + S::COST) * items : 0;
+                if (start < at + cost || b + 1 == b1) break;
+                at += cost;
+            }
+            found_b = static_cast<int>(b);
+            found_at = start - at;
+        }
+        __syncthreads();
+        use.b = found_b;
+        use.at = 0;
+    }
+    if (any_empty) {
+        for (int64_t b = cta; b < a.batch; b += gridDim.x) {
+            const Seen s = seen_of(a, b);
+            if (s.n <= s.first) attn_nothing<D>(a, b, 0, a.q_heads);
+        }
+    }
+    const Share share(total, gridDim.x);
+    if (cta >= share.ctas) return;
+    use.seen = seen_of(a, use.b);
+    use.units = A::units(use.seen);
+    if (use.units == 0) return;  // the lengths have changed under the call
+    if (a.narrow && a.batch <= 32 * AT_FEW) {
+        use.item = static_cast<int>(static_cast<uint32_t>(use.at) / static_cast<uint32_t>(use.units + S::COST));
+        use.at -= use.item * (use.units + S::COST);
+    } else {
+        use.item = static_cast<int>(found_at / (use.units + S::COST));
+        use.at = static_cast<int>(found_at - static_cast<int64_t>(use.item) * (use.units + S::COST));
+    }
+    use.left = static_cast<int>(end - start);  // the host's bound on the line keeps it below 2^31
+    use.settle();
+    if (use.left <= 0) return;
+
+    typename A::Query query;
+    query.load(a, use, warp, lane);
+    // ---- the first copies
+    Feed<E4M3, D, NT, FINE> feed;
+    feed.load = use;
+    feed.bad = 0;
+    feed.ring = smem_addr(smem) + warp * S::STAGES * S::STAGE;
+    feed.ahead.find(a, use, warp);
+#pragma unroll
+    for (int i = 0; i < S::STAGES - 1; ++i) feed.template next<false>(a, i, 1, warp, lane);
 
     A state;
-    int stage = 0, fill = S::STAGES - 1;
+    int stage = 0;
     while (use.left > 0) {
         // ---- a segment: the part of one item that lies in the stretch
         const int h = a.chunks == 1 ? use.item : use.item / a.chunks, h0 = (use.item - h * a.chunks) * S::HEADS;  // cache head; its first query head here
         const int heads = min(S::HEADS, a.group - h0);
         const int unit0 = use.unit(), n_units = min(use.units - unit0, use.left);
-        A::put_query(a, qv, qf, qc, qz, warp, lane);
+        A::put_query(a, query, qf, qc, qz, warp, lane);
         __syncthreads();
         state.begin(qc, lane);
-        int last = 0;  // the stage read last
-        for (int u = 0; u < n_units; ++u) {
-            copy_next(fill);
-            cp_async_wait<S::STAGES - 1>();
-            __syncwarp();
-            const int step = use.seen.first / S::TOK + (unit0 + u) * AT_WARPS + warp, at = step * S::TOK;
-            const uint8_t *const st = smem + (warp * S::STAGES + stage) * S::STAGE;
-            const uint32_t off = bad >> (stage * S::CH) & ((1u << S::CH) - 1);
-            if (at < use.seen.n) {
-                if (at < use.seen.first || at + S::TOK > use.seen.n || off != 0)
-                    state.template step<true>(st, qf, qz, at, use.seen, off, lane);
-                else
-                    state.template step<false>(st, qf, qz, at, use.seen, 0, lane);
-            }
-            __syncwarp();
-            last = stage;
-            stage = stage + 1 == S::STAGES ? 0 : stage + 1;
-            fill = fill + 1 == S::STAGES ? 0 : fill + 1;
-        }
-        // ---- the warps meet, eight heads at a time, each in the stage that it has read last: the same one for
-        // all, and no copy into it is started before the next segment's first barrier
+        const int last = attn_units<false>(a, state, feed, use.seen, unit0, n_units, 1, stage, smem, qf, qz, warp, lane);
+        // ---- the warps meet: no copy into the stage read last is begun before the next segment's first barrier
         const bool whole = n_units == use.units;
         const int64_t first_unit = end - use.left - unit0;  // of the item, in the line
         const int units = use.units;
@@ -824,48 +1068,17 @@ __global__ void __launch_bounds__(AT_THREADS, AttnShape<E4M3, D, NT>::CTAS) attn
         use.left -= n_units;
         if (use.left > 0) {
             use.next_item(a);
-            if (use.left > 0) A::load_query(a, use, qv, warp, lane);  // the next segment's, on its way while this one ends
+            if (use.left > 0) query.load(a, use, warp, lane);  // the next segment's, on its way while this one ends
         }
-        float *const meet = reinterpret_cast<float *>(smem + last * S::STAGE);
-        constexpr int MEET = S::STAGES * S::STAGE / 4;  // floats from warp to warp
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            if (i > 0) __syncthreads();
-            float l = state.l[i];
-            l += __shfl_xor_sync(0xffffffffu, l, 1);
-            l += __shfl_xor_sync(0xffffffffu, l, 2);
-            if ((lane & 3) == 0) ml[warp * S::HEADS + 8 * i + (lane >> 2)] = make_float2(state.m[i], l);
-            float *const to = meet + warp * MEET + 2 * (lane & 3) * S::OROW + (lane >> 2) * 4;
-#pragma unroll
-            for (int dg = 0; dg < D / 32; ++dg) {
-                const float(&p)[4] = state.o[i][2 * dg].v, (&r)[4] = state.o[i][2 * dg + 1].v;
-                *reinterpret_cast<float4 *>(to + dg * 32) = make_float4(p[0], p[2], r[0], r[2]);
-                *reinterpret_cast<float4 *>(to + S::OROW + dg * 32) = make_float4(p[1], p[3], r[1], r[3]);
+        attn_meet(state, smem, last, ml, heads, [&](int x, int col, float4 v, float top, float sum) {
+            if (whole) {
+                attn_store(a, row0 + x, D, col, v, sum);
+                attn_store_lse(a, row0 + x, col, top, sum);
+            } else {
+                *reinterpret_cast<float4 *>(record + x * D + col) = v;
+                if (col == 0) *reinterpret_cast<float2 *>(record + S::HEADS * D + 2 * x) = make_float2(top, sum);
             }
-            __syncthreads();
-            for (int j = tid; j < min(heads - 8 * i, 8) * (D / 4); j += AT_THREADS) {
-                const int y = j / (D / 4), x = 8 * i + y, col = j % (D / 4) * 4;
-                float top = -FLT_MAX, sum = 0.0f;
-                float4 v = make_float4(0, 0, 0, 0);
-#pragma unroll
-                for (int w = 0; w < AT_WARPS; ++w) top = fmaxf(top, ml[w * S::HEADS + x].x);
-#pragma unroll
-                for (int w = 0; w < AT_WARPS; ++w) {
-                    const float2 part = ml[w * S::HEADS + x];
-                    const float k = ex2_approx(part.x - top);
-                    const float4 z = *reinterpret_cast<const float4 *>(meet + w * MEET + y * S::OROW + col);
-                    sum = fmaf(part.y, k, sum);
-                    v = make_float4(fmaf(z.x, k, v.x), fmaf(z.y, k, v.y), fmaf(z.z, k, v.z), fmaf(z.w, k, v.w));
-                }
-                if (whole) {
-                    attn_store(a, row0 + x, D, col, v, sum);
-                    if (a.lse && col == 0) a.lse[row0 + x] = (top + log2f(sum)) * kLn2;
-                } else {
-                    *reinterpret_cast<float4 *>(record + x * D + col) = v;
-                    if (col == 0) record[S::HEADS * D + 2 * x] = top, record[S::HEADS * D + 2 * x + 1] = sum;
-                }
-            }
-        }
+        });
         if (!whole) {
             // the CTAs that share the item's units
             const int c0 = share.cta_of(first_unit), c1 = share.cta_of(first_unit + units - 1);
@@ -879,37 +1092,18 @@ __global__ void __launch_bounds__(AT_THREADS, AttnShape<E4M3, D, NT>::CTAS) attn
             }
             __syncthreads();
             if (last_one) {
-                auto part = [&](int p) { return a.records + (static_cast<int64_t>(c0 + p) * 2 + (p == 0)) * S::RECORD; };
                 const int parts = c1 - c0 + 1;
                 for (int i = tid; i < heads * (D / 4); i += AT_THREADS) {
                     const int x = i / (D / 4), col = i % (D / 4) * 4;
-                    float top = -FLT_MAX, l = 0.0f;
-                    float4 v = make_float4(0, 0, 0, 0);
-                    for (int p0 = 0; p0 < parts; p0 += AT_JOIN) {  // AT_JOIN records on their way at a time
-                        float2 y[AT_JOIN];
-                        float4 z[AT_JOIN];
-#pragma unroll
-                        for (int p = 0; p < AT_JOIN; ++p) {
-                            const bool there = p0 + p < parts;
-                            y[p] = there ? __ldcg(reinterpret_cast<const float2 *>(part(p0 + p) + S::HEADS * D + 2 * x)) : make_float2(-FLT_MAX, 0.0f);
-                            z[p] = there ? __ldcg(reinterpret_cast<const float4 *>(part(p0 + p) + x * D + col)) : make_float4(0, 0, 0, 0);
-                        }
-                        float now = top;
-#pragma unroll
-                        for (int p = 0; p < AT_JOIN; ++p) now = fmaxf(now, y[p].x);
-                        const float f = ex2_approx(top - now);
-                        top = now;
-                        l *= f;
-                        v = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
-#pragma unroll
-                        for (int p = 0; p < AT_JOIN; ++p) {
-                            const float k = ex2_approx(y[p].x - top);
-                            l = fmaf(y[p].y, k, l);
-                            v = make_float4(fmaf(z[p].x, k, v.x), fmaf(z[p].y, k, v.y), fmaf(z[p].z, k, v.z), fmaf(z[p].w, k, v.w));
-                        }
-                    }
+                    float top, l;
+                    float4 v;
+                    attn_join(parts, [&](int p, float2 &y, float4 &z) {
+                        const float *const from = a.records + (static_cast<int64_t>(c0 + p) * 2 + (p == 0)) * S::RECORD;
+                        y = __ldcg(reinterpret_cast<const float2 *>(from + S::HEADS * D + 2 * x));
+                        z = __ldcg(reinterpret_cast<const float4 *>(from + x * D + col));
+                    }, v, top, l);
                     attn_store(a, row0 + x, D, col, v, l);
-                    if (a.lse && col == 0) a.lse[row0 + x] = (top + log2f(l)) * kLn2;
+                    attn_store_lse(a, row0 + x, col, top, l);
                 }
             }
         }
@@ -917,31 +1111,130 @@ __global__ void __launch_bounds__(AT_THREADS, AttnShape<E4M3, D, NT>::CTAS) attn
     cp_async_wait<0>();
 }
 
+// The direct form, for few units to an item: a cluster of a.cluster CTAs to each item, whose CTAs take its units in turn
+// and join their parts through distributed shared memory.  No scan, no workspace, no counter; the first page numbers
+// are loaded beside the length.
 template <bool E4M3, int D, int NT, bool FINE>
-cudaError_t launch_attn_shape(const AttnArgs &a, int64_t most_units, cudaStream_t st)
+__global__ void __launch_bounds__(AT_THREADS, AttnShape<E4M3, D, NT>::CTAS) attn_direct_kernel(const __grid_constant__ AttnArgs a)
+{
+    using S = AttnShape<E4M3, D, NT>;
+    using A = Attn<E4M3, D, NT, FINE>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    uint4 *const qf = reinterpret_cast<uint4 *>(smem + S::RING);
+    float2 *const ml = reinterpret_cast<float2 *>(smem + S::RING + S::QF);  // [warp][head]: m, l
+    float *const qc = reinterpret_cast<float *>(ml + AT_WARPS * S::HEADS), *const qz = qc + S::HEADS;
+    float *const record = reinterpret_cast<float *>(smem + S::RECORD_AT);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int ctas = a.cluster, rank = static_cast<int>(blockIdx.x) % ctas;  // clusters are runs of the grid
+    const int items = a.c.heads * a.chunks, which = static_cast<int>(blockIdx.x) / ctas;
+    typename A::Place use;
+    use.b = which / items;
+    use.item = which - use.b * items;
+    use.at = S::COST + rank;
+    pdl_wait();
+    pdl_trigger();
+    typename A::Query query;
+    query.load(a, use, warp, lane);
+    Feed<E4M3, D, NT, FINE> feed;
+    if (a.window == 0) feed.ahead.guess(a, use, warp);
+    use.seen = seen_of(a, use.b);
+    use.units = A::units(use.seen);
+    use.left = use.units > rank ? (use.units - rank + ctas - 1) / ctas : 0;
+    const int h = a.chunks == 1 ? use.item : use.item / a.chunks, h0 = (use.item - h * a.chunks) * S::HEADS;
+    const int heads = min(S::HEADS, a.group - h0);
+    if (use.units == 0) {
+        if (rank == 0) attn_nothing<D>(a, use.b, h * a.group + h0, heads);
+        return;  // the whole cluster
+    }
+    const int64_t row0 = static_cast<int64_t>(use.b) * a.q_heads + h * a.group + h0;
+    const bool alone = use.units == 1 || ctas == 1;
+    if (use.left > 0) {
+        feed.load = use;
+        feed.bad = 0;
+        feed.ring = smem_addr(smem) + warp * S::STAGES * S::STAGE;
+        if (a.window == 0)
+            feed.ahead.keep(use);
+        else
+            feed.ahead.find(a, use, warp);
+#pragma unroll
+        for (int i = 0; i < S::STAGES - 1; ++i) feed.template next<true>(a, i, ctas, warp, lane);
+        A::put_query(a, query, qf, qc, qz, warp, lane);
+        __syncthreads();
+        A state;
+        state.begin(qc, lane);
+        int stage = 0;
+        const int last = attn_units<true>(a, state, feed, use.seen, rank, use.left, ctas, stage, smem, qf, qz, warp, lane);
+        cp_async_wait<0>();
+        attn_meet(state, smem, last, ml, heads, [&](int x, int col, float4 v, float top, float sum) {
+            if (alone) {
+                attn_store(a, row0 + x, D, col, v, sum);
+                attn_store_lse(a, row0 + x, col, top, sum);
+            } else {
+                *reinterpret_cast<float4 *>(record + x * D + col) = v;
+                if (col == 0) *reinterpret_cast<float2 *>(record + S::HEADS * D + 2 * x) = make_float2(top, sum);
+            }
+        });
+    }
+    if (alone) return;  // the whole cluster
+    cluster_sync();
+    const int parts = min(use.units, ctas), pieces = heads * (D / 4);
+    for (int i = rank + ctas * tid; i < pieces; i += ctas * AT_THREADS) {
+        const int x = i / (D / 4), col = i % (D / 4) * 4;
+        float top, l;
+        float4 v;
+        attn_join(parts, [&](int p, float2 &y, float4 &z) {
+            y = ld_cluster_f2(record + S::HEADS * D + 2 * x, p);
+            z = ld_cluster_f4(record + x * D + col, p);
+        }, v, top, l);
+        attn_store(a, row0 + x, D, col, v, l);
+        attn_store_lse(a, row0 + x, col, top, l);
+    }
+    cluster_sync();  // no CTA leaves while another reads its part
+}
+
+template <bool E4M3, int D, int NT, bool FINE>
+cudaError_t launch_attn_line(const AttnArgs &a, int64_t most, cudaStream_t st)
 {
     using S = AttnShape<E4M3, D, NT>;
     const auto kernel = attn_decode_kernel<E4M3, D, NT, FINE>;
     if (cudaError_t e = opt_in_smem(reinterpret_cast<const void *>(kernel), S::SMEM); e != cudaSuccess) return e;
     const int64_t room = static_cast<int64_t>(num_sms()) * S::CTAS;
-    const int grid = static_cast<int>(most_units < 1 ? 1 : most_units < room ? most_units : room);
+    const int grid = static_cast<int>(most < 1 ? 1 : most < room ? most : room);
     return launch_pdl(kernel, dim3(grid), dim3(AT_THREADS), S::SMEM, st, a);
 }
 
-// One translation unit per format and head size: definitions in qg_attn_*.cu.
+template <bool E4M3, int D, int NT, bool FINE>
+cudaError_t launch_attn_direct(const AttnArgs &a, cudaStream_t st)
+{
+    using S = AttnShape<E4M3, D, NT>;
+    constexpr int SMEM = S::RECORD_AT + S::RECORD * 4;
+    const auto kernel = attn_direct_kernel<E4M3, D, NT, FINE>;
+    if (cudaError_t e = opt_in_smem(reinterpret_cast<const void *>(kernel), SMEM); e != cudaSuccess) return e;
+    const dim3 grid(static_cast<unsigned>(a.batch * a.c.heads * a.chunks * a.cluster));
+    if (a.cluster == 1) return launch_pdl(kernel, grid, dim3(AT_THREADS), SMEM, st, a);
+    return launch_pdl_cluster(kernel, grid, dim3(AT_THREADS), SMEM, st, static_cast<unsigned>(a.cluster), a);
+}
+
+// One translation unit per format and head size: definitions in qg_attn_*.cu.  most: the places that the line can have.
 template <bool E4M3, int D>
-cudaError_t launch_attn_dim(const AttnArgs &a, int64_t most_units, cudaStream_t st);
+cudaError_t launch_attn_dim(const AttnArgs &a, int64_t most, cudaStream_t st);
+
+template <bool E4M3, int D, int NT, bool FINE>
+cudaError_t launch_attn_shape(const AttnArgs &a, int64_t most, cudaStream_t st)
+{
+    return a.cluster > 0 ? launch_attn_direct<E4M3, D, NT, FINE>(a, st) : launch_attn_line<E4M3, D, NT, FINE>(a, most, st);
+}
 
 #define QG_ATTN_DIM(E4M3, D)                                                                                       \
     template <>                                                                                                    \
-    cudaError_t launch_attn_dim<E4M3, D>(const AttnArgs &a, int64_t most_units, cudaStream_t st)                   \
+    cudaError_t launch_attn_dim<E4M3, D>(const AttnArgs &a, int64_t most, cudaStream_t st)                         \
     {                                                                                                              \
         const bool fine = !a.q_bf16 || !a.out_bf16;                                                                \
         if (a.group <= 8)                                                                                          \
-            return fine ? launch_attn_shape<E4M3, D, 1, true>(a, most_units, st)                                   \
-                        : launch_attn_shape<E4M3, D, 1, false>(a, most_units, st);                                 \
-        return fine ? launch_attn_shape<E4M3, D, 2, true>(a, most_units, st)                                       \
-                    : launch_attn_shape<E4M3, D, 2, false>(a, most_units, st);                                     \
+            return fine ? launch_attn_shape<E4M3, D, 1, true>(a, most, st)                                         \
+                        : launch_attn_shape<E4M3, D, 1, false>(a, most, st);                                       \
+        return fine ? launch_attn_shape<E4M3, D, 2, true>(a, most, st)                                             \
+                    : launch_attn_shape<E4M3, D, 2, false>(a, most, st);                                           \
     }
 
 }  // namespace qg
