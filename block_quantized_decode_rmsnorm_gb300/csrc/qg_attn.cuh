@@ -260,11 +260,6 @@ struct Attn {
                 left -= skip;
             }
         }
-        __device__ __forceinline__ void next(const AttnArgs &a)
-        {
-            --left;
-            if (++at == units + S::COST) next_item(a);
-        }
         __device__ __forceinline__ void next_item(const AttnArgs &a)
         {
             at = 0;
@@ -278,50 +273,6 @@ struct Attn {
                 if (units == 0) left = 0;
             }
             settle();
-        }
-    };
-
-    // The tokens of this warp's step in a unit, [at, at + TOK), and where they are.
-    struct Step {
-        int at;
-        bool any;
-        int page[CH], off[CH];  // of each tile: its page (-1: none of it is seen) and first row there
-        __device__ __forceinline__ void find(const AttnArgs &a, const Place &p, int warp)
-        {
-            const int step0 = static_cast<uint32_t>(p.seen.first) / TOK, step = step0 + p.unit() * AT_WARPS + warp;
-            at = step * TOK;
-            any = p.left > 0 && at < p.seen.n;
-            const int32_t *const row = a.pages + p.b * a.max_pages;
-#pragma unroll
-            for (int i = 0; i < CH; ++i) {
-                const int t = at + i * KV_TILE;
-                const uint32_t col = a.page_shift >= 0 ? static_cast<uint32_t>(t) >> a.page_shift : static_cast<uint32_t>(t) / static_cast<uint32_t>(a.c.page);
-                off[i] = t - col * a.c.page;
-                page[i] = -1;
-                if (any && t < p.seen.n && t + KV_TILE > p.seen.first) page[i] = row[col];
-            }
-        }
-        // The same for a sequence seen from its first token on, before its length is known, ...
-        __device__ __forceinline__ void guess(const AttnArgs &a, const Place &p, int warp)
-        {
-            at = (p.unit() * AT_WARPS + warp) * TOK;
-            const int32_t *const row = a.pages + p.b * a.max_pages;
-#pragma unroll
-            for (int i = 0; i < CH; ++i) {
-                const int t = at + i * KV_TILE;
-                const uint32_t col = a.page_shift >= 0 ? static_cast<uint32_t>(t) >> a.page_shift : static_cast<uint32_t>(t) / static_cast<uint32_t>(a.c.page);
-                off[i] = t - col * a.c.page;
-                page[i] = -1;
-                if (col < a.max_pages) page[i] = row[col];
-            }
-        }
-        // ... and once it is.
-        __device__ __forceinline__ void keep(const Place &p)
-        {
-            any = p.left > 0 && at < p.seen.n;
-#pragma unroll
-            for (int i = 0; i < CH; ++i)
-                if (at + i * KV_TILE >= p.seen.n) page[i] = -1;
         }
     };
 
@@ -351,27 +302,27 @@ struct Attn {
             cp_async_16(ds + (lane < 16 ? 0 : S::SCALES) + x * 16, src + x * 16);
         }
     }
-    static __device__ __forceinline__ uint32_t copy(const AttnArgs &a, const Place &p, const Step &s, uint32_t stage, int lane)
+    // at: the step's first token; rows: of each tile the planes' row of its first token, kNone if none of it is seen, kBad
+    // for a page outside the cache.
+    static constexpr int64_t kNone = -1, kBad = -2;
+    static __device__ __forceinline__ uint32_t copy(const AttnArgs &a, Seen seen, int at, const int64_t (&rows)[CH], uint32_t stage, int lane)
     {
-        const int h = a.chunks == 1 ? p.item : p.item / a.chunks;
-        const uint32_t pages = static_cast<uint32_t>(a.c.n_pages);
-        bool plain = s.at >= p.seen.first && s.at + TOK <= p.seen.n;
+        bool plain = at >= seen.first && at + TOK <= seen.n, none = true;
 #pragma unroll
-        for (int i = 0; i < CH; ++i) plain = plain && static_cast<uint32_t>(s.page[i]) < pages;
+        for (int i = 0; i < CH; ++i) plain = plain && rows[i] >= 0, none = none && rows[i] == kNone;
         if (plain) {
 #pragma unroll
-            for (int i = 0; i < CH; ++i)
-                copy_tile<true>(a, p.seen, 0, (static_cast<int64_t>(s.page[i]) * a.c.heads + h) * a.c.page + s.off[i], stage + i * S::TILE, lane);
+            for (int i = 0; i < CH; ++i) copy_tile<true>(a, seen, 0, rows[i], stage + i * S::TILE, lane);
             return 0;
         }
         uint32_t bad = 0;
+        if (none) return bad;
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-            const int t = s.at + i * KV_TILE, page = s.page[i];
-            if (static_cast<uint32_t>(page) < pages) {
-                copy_tile<false>(a, p.seen, t, (static_cast<int64_t>(page) * a.c.heads + h) * a.c.page + s.off[i], stage + i * S::TILE, lane);
+            if (rows[i] >= 0) {
+                copy_tile<false>(a, seen, at + i * KV_TILE, rows[i], stage + i * S::TILE, lane);
             } else {  // zeros, without a page to read from
-                if (t < p.seen.n && t + KV_TILE > p.seen.first) bad |= 1u << i;
+                if (rows[i] == kBad) bad |= 1u << i;
                 for (int x = lane; x < S::TILE / 16; x += 32)
                     asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(stage + i * S::TILE + x * 16), "r"(0) : "memory");
             }
@@ -767,34 +718,73 @@ __device__ __forceinline__ float4 ld_cluster_f4(const float *local, uint32_t ran
     return v;
 }
 
-// What a warp copies ahead of its steps.
+// What a warp copies ahead of its steps.  Page numbers are looked up for 32 tiles at a time, one to a lane, and turned
+// into rows when the first of them is used.
 template <bool E4M3, int D, int NT, bool FINE>
 struct Feed {
     using S = AttnShape<E4M3, D, NT>;
     using A = Attn<E4M3, D, NT, FINE>;
     typename A::Place load;
-    typename A::Step ahead;
+    int64_t row;      // of this lane's tile
+    uint32_t token;   // its first token
+    int page, used;   // its page (0 where not looked up); tiles of the 32 that have been copied, -1 before the first
     uint32_t bad, ring;  // bad: CH bits per stage
 
+    __device__ __forceinline__ void start(const typename A::Place &p, uint8_t *smem, int warp)
+    {
+        load = p;
+        bad = 0;
+        ring = smem_addr(smem) + warp * S::STAGES * S::STAGE;
+    }
+    // The pages of this warp's tiles from p's unit on, units `stride` apart, of tokens in [first, end).
+    __device__ __forceinline__ void look_up(const AttnArgs &a, const typename A::Place &p, int first, int end, int stride, int warp, int lane)
+    {
+        const uint32_t step = static_cast<uint32_t>(first) / S::TOK + (p.unit() + lane / S::CH * stride) * AT_WARPS + warp;
+        token = step * S::TOK + lane % S::CH * KV_TILE;
+        page = 0;
+        used = -1;
+        if (token < static_cast<uint32_t>(end) && token + KV_TILE > static_cast<uint32_t>(first)) {
+            const uint32_t col = a.page_shift >= 0 ? token >> a.page_shift : token / static_cast<uint32_t>(a.c.page);
+            page = a.pages[p.b * a.max_pages + col];
+        }
+    }
+    __device__ __forceinline__ void resolve(const AttnArgs &a)
+    {
+        used = 0;
+        row = A::kNone;
+        if (load.left > 0 && token < static_cast<uint32_t>(load.seen.n) && token + KV_TILE > static_cast<uint32_t>(load.seen.first)) {
+            const int h = a.chunks == 1 ? load.item : load.item / a.chunks;
+            const uint32_t off = a.page_shift >= 0 ? token & (a.c.page - 1) : token % static_cast<uint32_t>(a.c.page);
+            row = static_cast<uint32_t>(page) < static_cast<uint32_t>(a.c.n_pages)
+                      ? (static_cast<int64_t>(page) * a.c.heads + h) * a.c.page + off : A::kBad;
+        }
+    }
+
     // The copies of the step ahead into a stage, and on to the one after it: the next unit of the stretch, or
-    // (STRIDE > 0) of the item.
+    // (DIRECT) of the item, `stride` on.
     template <bool DIRECT>
     __device__ __forceinline__ void next(const AttnArgs &a, int stage, int stride, int warp, int lane)
     {
-        if (ahead.any) {
-            const uint32_t x = A::copy(a, load, ahead, ring + stage * S::STAGE, lane);
+        if (used < 0) resolve(a);
+        if (load.left > 0) {
+            int64_t rows[S::CH];
+#pragma unroll
+            for (int i = 0; i < S::CH; ++i) rows[i] = __shfl_sync(0xffffffffu, row, used + i);
+            const int at = (static_cast<uint32_t>(load.seen.first) / S::TOK + load.unit() * AT_WARPS + warp) * S::TOK;
+            const uint32_t x = A::copy(a, load.seen, at, rows, ring + stage * S::STAGE, lane);
             bad = (bad & ~(((1u << S::CH) - 1) << (stage * S::CH))) | x << (stage * S::CH);
+            used += S::CH;
+            bool look = used == 32;
+            --load.left;
+            if constexpr (DIRECT) {
+                load.at += stride;
+            } else if (++load.at == load.units + S::COST) {
+                load.next_item(a);
+                look = true;
+            }
+            if (look && load.left > 0) look_up(a, load, load.seen.first, load.seen.n, stride, warp, lane);
         }
         cp_async_commit();
-        if (load.left > 0) {
-            if constexpr (DIRECT) {
-                --load.left;
-                load.at += stride;
-            } else {
-                load.next(a);
-            }
-            ahead.find(a, load, warp);
-        }
     }
 };
 
@@ -1041,10 +1031,8 @@ __global__ void __launch_bounds__(AT_THREADS, AttnShape<E4M3, D, NT>::CTAS) attn
     query.load(a, use, warp, lane);
     // ---- the first copies
     Feed<E4M3, D, NT, FINE> feed;
-    feed.load = use;
-    feed.bad = 0;
-    feed.ring = smem_addr(smem) + warp * S::STAGES * S::STAGE;
-    feed.ahead.find(a, use, warp);
+    feed.start(use, smem, warp);
+    feed.look_up(a, use, use.seen.first, use.seen.n, 1, warp, lane);
 #pragma unroll
     for (int i = 0; i < S::STAGES - 1; ++i) feed.template next<false>(a, i, 1, warp, lane);
 
@@ -1136,7 +1124,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnShape<E4M3, D, NT>::CTAS) attn
     typename A::Query query;
     query.load(a, use, warp, lane);
     Feed<E4M3, D, NT, FINE> feed;
-    if (a.window == 0) feed.ahead.guess(a, use, warp);
+    if (a.window == 0) feed.look_up(a, use, 0, a.held, ctas, warp, lane);
     use.seen = seen_of(a, use.b);
     use.units = A::units(use.seen);
     use.left = use.units > rank ? (use.units - rank + ctas - 1) / ctas : 0;
@@ -1149,13 +1137,8 @@ __global__ void __launch_bounds__(AT_THREADS, AttnShape<E4M3, D, NT>::CTAS) attn
     const int64_t row0 = static_cast<int64_t>(use.b) * a.q_heads + h * a.group + h0;
     const bool alone = use.units == 1 || ctas == 1;
     if (use.left > 0) {
-        feed.load = use;
-        feed.bad = 0;
-        feed.ring = smem_addr(smem) + warp * S::STAGES * S::STAGE;
-        if (a.window == 0)
-            feed.ahead.keep(use);
-        else
-            feed.ahead.find(a, use, warp);
+        feed.start(use, smem, warp);
+        if (a.window > 0) feed.look_up(a, use, use.seen.first, use.seen.n, ctas, warp, lane);
 #pragma unroll
         for (int i = 0; i < S::STAGES - 1; ++i) feed.template next<true>(a, i, ctas, warp, lane);
         A::put_query(a, query, qf, qc, qz, warp, lane);
