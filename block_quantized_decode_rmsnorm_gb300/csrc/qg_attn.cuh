@@ -42,7 +42,7 @@ namespace qg {
 constexpr int AT_WARPS = 4;
 constexpr int AT_THREADS = 32 * AT_WARPS;
 constexpr int AT_CTAS_MAX = 4;  // per SM
-constexpr int AT_JOIN = 8;
+constexpr int AT_JOIN = 16;         // records of the workspace that are on their way at a time
 constexpr int AT_FEW = 4;  // rows of 32 sequences that every warp scans for itself
 constexpr int AT_CLUSTER = 8;
 
@@ -863,31 +863,31 @@ __device__ __forceinline__ void attn_meet(const Attn<E4M3, D, NT, FINE> &state, 
     }
 }
 
-// Parts of an item joined in order, AT_JOIN of them on their way at a time.  part(p, y, z): part p's reference and sum
+// Parts of an item joined in order, N of them on their way at a time.  part(p, y, z): part p's reference and sum
 // of weights, and its four sums.
-template <typename Part>
+template <int N, typename Part>
 __device__ __forceinline__ void attn_join(int parts, const Part &part, float4 &v, float &top, float &l)
 {
     top = -FLT_MAX, l = 0.0f;
     v = make_float4(0, 0, 0, 0);
-    for (int p0 = 0; p0 < parts; p0 += AT_JOIN) {
-        float2 y[AT_JOIN];
-        float4 z[AT_JOIN];
+    for (int p0 = 0; p0 < parts; p0 += N) {
+        float2 y[N];
+        float4 z[N];
 #pragma unroll
-        for (int p = 0; p < AT_JOIN; ++p) {
+        for (int p = 0; p < N; ++p) {
             y[p] = make_float2(-FLT_MAX, 0.0f);
             z[p] = make_float4(0, 0, 0, 0);
             if (p0 + p < parts) part(p0 + p, y[p], z[p]);
         }
         float now = top;
 #pragma unroll
-        for (int p = 0; p < AT_JOIN; ++p) now = fmaxf(now, y[p].x);
+        for (int p = 0; p < N; ++p) now = fmaxf(now, y[p].x);
         const float f = ex2_approx(top - now);
         top = now;
         l *= f;
         v = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
 #pragma unroll
-        for (int p = 0; p < AT_JOIN; ++p) {
+        for (int p = 0; p < N; ++p) {
             const float k = ex2_approx(y[p].x - top);
             l = fmaf(y[p].y, k, l);
             v = make_float4(fmaf(z[p].x, k, v.x), fmaf(z[p].y, k, v.y), fmaf(z[p].z, k, v.z), fmaf(z[p].w, k, v.w));
@@ -1085,7 +1085,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnShape<E4M3, D, NT>::CTAS) attn
                     const int x = i / (D / 4), col = i % (D / 4) * 4;
                     float top, l;
                     float4 v;
-                    attn_join(parts, [&](int p, float2 &y, float4 &z) {
+                    attn_join<AT_JOIN>(parts, [&](int p, float2 &y, float4 &z) {
                         const float *const from = a.records + (static_cast<int64_t>(c0 + p) * 2 + (p == 0)) * S::RECORD;
                         y = __ldcg(reinterpret_cast<const float2 *>(from + S::HEADS * D + 2 * x));
                         z = __ldcg(reinterpret_cast<const float4 *>(from + x * D + col));
@@ -1165,7 +1165,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnShape<E4M3, D, NT>::CTAS) attn
         const int x = i / (D / 4), col = i % (D / 4) * 4;
         float top, l;
         float4 v;
-        attn_join(parts, [&](int p, float2 &y, float4 &z) {
+        attn_join<AT_CLUSTER>(parts, [&](int p, float2 &y, float4 &z) {
             y = ld_cluster_f2(record + S::HEADS * D + 2 * x, p);
             z = ld_cluster_f4(record + x * D + col, p);
         }, v, top, l);

@@ -2,7 +2,7 @@
 //
 // Both walk over rows of 2 * heads * dim values (keys, then values) at slots that the
 // caller gives.  A thread keeps its place in the row - key or value, head, block, piece
-// of 8 or 16 values - and takes several rows, so that the place is computed once and a
+// of 16 values - and takes several rows, so that the place is computed once and a
 // row costs one slot, one division by the page size and one product.
 #include "qg_kv.cuh"
 
@@ -40,32 +40,38 @@ struct KvSource {
     int64_t k_row, k_head, v_row, v_head;
 };
 
-// Eight values of a row: two or one 16-byte loads.
+// Sixteen values of a row.
 template <typename T>
-struct Vec8;
+struct Vec16;
 template <>
-struct Vec8<float> {
-    float4 a, b;
+struct Vec16<float> {
+    float4 r[4];
     __device__ __forceinline__ void load(const float *p)
     {
-        a = *reinterpret_cast<const float4 *>(p);
-        b = *reinterpret_cast<const float4 *>(p + 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[i] = reinterpret_cast<const float4 *>(p)[i];
     }
-    __device__ __forceinline__ float4 lo() const { return a; }
-    __device__ __forceinline__ float4 hi() const { return b; }
+    __device__ __forceinline__ float4 get(int i) const { return r[i]; }
 };
 template <>
-struct Vec8<__nv_bfloat16> {
-    uint4 r;
-    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { r = *reinterpret_cast<const uint4 *>(p); }
-    __device__ __forceinline__ float4 lo() const { return Vec4<__nv_bfloat16>::widen(make_uint2(r.x, r.y)); }
-    __device__ __forceinline__ float4 hi() const { return Vec4<__nv_bfloat16>::widen(make_uint2(r.z, r.w)); }
+struct Vec16<__nv_bfloat16> {
+    uint4 r[2];
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p)
+    {
+        r[0] = reinterpret_cast<const uint4 *>(p)[0];
+        r[1] = reinterpret_cast<const uint4 *>(p)[1];
+    }
+    __device__ __forceinline__ float4 get(int i) const
+    {
+        const uint4 v = r[i / 2];
+        return Vec4<__nv_bfloat16>::widen(i % 2 ? make_uint2(v.z, v.w) : make_uint2(v.x, v.y));
+    }
 };
 
-// Lanes that hold one scale's block, eight values each.
-__host__ __device__ constexpr int write_lanes(bool e4m3, int dim) { return !e4m3 ? QK / 8 : dim == 64 ? 8 : 16; }
+// Lanes that hold one scale's block, sixteen values each.
+__host__ __device__ constexpr int write_lanes(bool e4m3, int dim) { return !e4m3 ? QK / 16 : dim == 64 ? 4 : 8; }
 
-// The largest magnitude over the L lanes of a block (fmaxf passes over NaN).
+// The largest magnitude over the L lanes of a block, NaN passed over, ...
 template <int L>
 __device__ __forceinline__ float block_max(float m)
 {
@@ -73,34 +79,79 @@ __device__ __forceinline__ float block_max(float m)
     for (int o = L / 2; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     return m;
 }
+// ... and NaN if there is one.
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
 
+// The Q8_0 codes of sixteen values of a block with scale d, 2^-100 <= d < infinity, none of them NaN: those of q8_code,
+// without a branch (in a bf16 row 0.4 % of the values are exact halves of d, so that a branch to the division is taken by
+// most warps).  The quotient is corrected once (Markstein): with y = 1 / d correctly rounded, t = fl(v y) and the exact
+// r = v - t d, fl(t + r y) is the rounded quotient up to 2^-24 of an ulp; that it lies on the same side of every
+// half-integer as fl(v / d) was checked for all 2^23 mantissas of d and the five floats around each of the 127 places
+// where it matters.  Adding 1/2 and 2^23 toward zero leaves the magnitude rounded half away from zero.
+__device__ __forceinline__ uint4 q8_codes16(const float4 (&v)[4], float d)
+{
+    const float y = __frcp_rn(d);
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        uint32_t s[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float t = __fmul_rn(x[j], y), r = __fmaf_rn(-t, d, x[j]);
+            const float q = __fmaf_rn(r, y, t);
+            s[j] = __float_as_uint(__fadd_rz(__fadd_rz(fabsf(q), 0.5f), 8388608.0f));
+        }
+        const uint32_t p = __byte_perm(__byte_perm(s[0], s[1], 0x0040), __byte_perm(s[2], s[3], 0x0040), 0x5410);
+        // bytes of negative values other than 0 to two's complement
+        const uint32_t top = __byte_perm(__byte_perm(__float_as_uint(x[0]), __float_as_uint(x[1]), 0x0073),
+                                         __byte_perm(__float_as_uint(x[2]), __float_as_uint(x[3]), 0x0073), 0x5410);
+        uint32_t minus;  // 255 where top's byte has its highest bit and p's is not 0
+        asm("prmt.b32 %0, %1, 0, 0xba98;" : "=r"(minus) : "r"(top & (p + 0x7f7f7f7fu)));
+        w[i] = (p ^ minus) + (minus & 0x01010101u);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// Any block's, one value after the other.
+__device__ __noinline__ uint4 q8_codes16_any(float4 a, float4 b, float4 c, float4 e, float d)
+{
+    const float rd = q8_recip(d);
+    return make_uint4(q8_pack4(a, d, rd), q8_pack4(b, d, rd), q8_pack4(c, d, rd), q8_pack4(e, d, rd));
+}
+
+// Bound by issue: 145 instructions for a lane's sixteen values, a third of them the slot's and the addresses'.
 template <typename T, bool E4M3, int L, int RB>
 __global__ void __launch_bounds__(KT) kv_write_kernel(KvRows a, KvSource<T> s)
 {
     pdl_wait();
     pdl_trigger();
     const int nb = kv_blocks(E4M3, a.c.dim), block = E4M3 ? EB : QK;
-    // this thread's place in a row; U (a.lanes) and KT are multiples of L, so a block's lanes stay in one warp
+    // this thread's place in a row; a.lanes and KT are multiples of L, so a block's lanes stay in one warp
     const int tid = threadIdx.x;
     const int r0 = a.rows_at_once > 1 ? tid / a.lanes : 0;
     const int j = a.rows_at_once > 1 ? tid - r0 * a.lanes : blockIdx.y * KT + tid;
-    const int unit = j / L, b = unit % nb, hh = unit / nb;
+    const int unit = j / L, hh = unit / nb, b = unit - hh * nb;
     const bool value = hh >= a.c.heads;
     const int h = value ? hh - a.c.heads : hh;
-    const int col = b * block + (j % L) * 8;
-    const bool in_row = j < a.lanes && r0 < a.rows_at_once, live = in_row && col < a.c.dim;
+    const int col = b * block + (j % L) * 16;
+    const bool live = j < a.lanes && r0 < a.rows_at_once && col < a.c.dim;
     const T *src = value ? s.v + h * s.v_head + col : s.k + h * s.k_head + col;
     const int64_t stride = value ? s.v_row : s.k_row;
-    uint8_t *codes = value ? a.c.vq : a.c.kq;
+    uint8_t *codes = (value ? a.c.vq : a.c.kq) + col;
     void *scales = value ? a.c.vd : a.c.kd;
 
-    Vec8<T> x[RB];
+    Vec16<T> x[RB];
     int64_t slot[RB];
     const int64_t first = static_cast<int64_t>(blockIdx.x) * RB * a.rows_at_once + r0;
 #pragma unroll
     for (int i = 0; i < RB; ++i) {
         const int64_t row = first + static_cast<int64_t>(i) * a.rows_at_once;
-        x[i] = Vec8<T>{};
+        x[i] = Vec16<T>{};
         slot[i] = -1;
         if (live && row < a.rows) {
             slot[i] = a.slots[row];
@@ -109,28 +160,50 @@ __global__ void __launch_bounds__(KT) kv_write_kernel(KvRows a, KvSource<T> s)
     }
 #pragma unroll
     for (int i = 0; i < RB; ++i) {
-        const float4 lo = x[i].lo(), hi = x[i].hi();
-        int64_t page;
-        int off;
+        float4 v[4];
+        float m = 0.0f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            v[q] = x[i].get(q);
+            if constexpr (E4M3)
+                m = fmaxf(m, max_abs4(v[q]));
+            else
+                m = max_nan(max_nan(max_nan(m, fabsf(v[q].x)), max_nan(fabsf(v[q].y), fabsf(v[q].z))), fabsf(v[q].w));
+        }
+        int64_t page = 0;
+        int off = 0;
         const bool there = kv_place(a, slot[i], page, off);
         const int64_t at = (page * a.c.heads + h) * a.c.page + off;  // row of the planes
-        uint2 w;
+        uint4 w;
         if constexpr (E4M3) {
-            const float m = e4m3_floor(block_max<L>(fmaxf(max_abs4(lo), max_abs4(hi))));
+            m = e4m3_floor(block_max<L>(m));
             const float f = __fdiv_rn(448.0f, m);
-            w.x = e4m3_pack4(lo.x * f, lo.y * f, lo.z * f, lo.w * f);
-            w.y = e4m3_pack4(hi.x * f, hi.y * f, hi.z * f, hi.w * f);
+            w.x = e4m3_pack4(v[0].x * f, v[0].y * f, v[0].z * f, v[0].w * f);
+            w.y = e4m3_pack4(v[1].x * f, v[1].y * f, v[1].z * f, v[1].w * f);
+            w.z = e4m3_pack4(v[2].x * f, v[2].y * f, v[2].z * f, v[2].w * f);
+            w.w = e4m3_pack4(v[3].x * f, v[3].y * f, v[3].z * f, v[3].w * f);
             if (there && j % L == 0) static_cast<float *>(scales)[at * nb + b] = __fdiv_rn(m, 448.0f);
         } else {
-            float m = fmaxf(fmaxf(fmaxf(fabsf(lo.x), fabsf(lo.y)), fmaxf(fabsf(lo.z), fabsf(lo.w))),
-                            fmaxf(fmaxf(fabsf(hi.x), fabsf(hi.y)), fmaxf(fabsf(hi.z), fabsf(hi.w))));
-            m = block_max<L>(m);
-            const float d = div127(m), rd = q8_recip(d);
-            w.x = q8_pack4(lo, d, rd);
-            w.y = q8_pack4(hi, d, rd);
+#pragma unroll
+            for (int o = L / 2; o >= 1; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+            float d = div127(m);
+            if (d >= 0x1p-100f && d < __int_as_float(0x7f800000)) {
+                w = q8_codes16(v, d);
+            } else {
+                // fmaxf's maximum: NaN passed over, as quantize_act_q8_0 does.  A block's lanes are here together, other
+                // blocks' may not be
+                float n = fmaxf(fmaxf(fabsf(v[0].x), fabsf(v[0].y)), fmaxf(fabsf(v[0].z), fabsf(v[0].w)));
+#pragma unroll
+                for (int q = 1; q < 4; ++q) n = fmaxf(n, fmaxf(fmaxf(fabsf(v[q].x), fabsf(v[q].y)), fmaxf(fabsf(v[q].z), fabsf(v[q].w))));
+                const uint32_t block_lanes = ((1u << L) - 1) << (threadIdx.x & 31 & ~(L - 1));
+#pragma unroll
+                for (int o = L / 2; o >= 1; o >>= 1) n = fmaxf(n, __shfl_xor_sync(block_lanes, n, o));
+                d = div127(n);
+                w = q8_codes16_any(v[0], v[1], v[2], v[3], d);
+            }
             if (there && j % L == 0) static_cast<uint16_t *>(scales)[at * nb + b] = f2h_rn(d);
         }
-        if (there) *reinterpret_cast<uint2 *>(codes + at * a.c.dim + col) = w;
+        if (there) *reinterpret_cast<uint4 *>(codes + at * a.c.dim) = w;
     }
 }
 
@@ -162,8 +235,8 @@ __device__ __forceinline__ void kv_values(uint4 q, float d, T *out)
     } else {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const uint2 a = Vec4<__nv_bfloat16>::narrow(f[2 * i]), b = Vec4<__nv_bfloat16>::narrow(f[2 * i + 1]);
-            reinterpret_cast<uint4 *>(out)[i] = make_uint4(a.x, a.y, b.x, b.y);
+            const uint2 p = Vec4<__nv_bfloat16>::narrow(f[2 * i]), r = Vec4<__nv_bfloat16>::narrow(f[2 * i + 1]);
+            reinterpret_cast<uint4 *>(out)[i] = make_uint4(p.x, p.y, r.x, r.y);
         }
     }
 }
@@ -187,14 +260,19 @@ __global__ void __launch_bounds__(KT) kv_read_kernel(KvRows a, T *k, T *v)
     const int64_t first = static_cast<int64_t>(blockIdx.x) * RB * a.rows_at_once + r0;
     uint4 q[RB];
     float d[RB];
+    int64_t slot[RB];
 #pragma unroll
     for (int i = 0; i < RB; ++i) {
         const int64_t row = first + static_cast<int64_t>(i) * a.rows_at_once;
+        slot[i] = row < a.rows ? a.slots[row] : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < RB; ++i) {
         q[i] = make_uint4(0, 0, 0, 0);
         d[i] = 0.0f;
         int64_t page;
         int off;
-        if (row < a.rows && kv_place(a, a.slots[row], page, off)) {
+        if (kv_place(a, slot[i], page, off)) {
             const int64_t at = (page * a.c.heads + h) * a.c.page + off;
             q[i] = *reinterpret_cast<const uint4 *>(codes + at * a.c.dim + col);
             const int64_t b = at * nb + col / block;
@@ -224,13 +302,16 @@ dim3 rows_grid(const KvRows &a, int rb)
     return dim3(static_cast<unsigned>((a.rows + per - 1) / per), a.rows_at_once > 1 ? 1 : (a.lanes + KT - 1) / KT);
 }
 
-// Four rows a thread where they still give every SM eight CTAs, one where rows are few.
-bool many_rows(const KvRows &a) { return a.rows * a.lanes >= int64_t(num_sms()) * 8 * 4 * KT; }
+// Four rows a thread where they still give every SM six CTAs, one where rows are few.
+#ifndef QG_KV_RB
+#define QG_KV_RB 4
+#endif
+bool many_rows(const KvRows &a) { return a.rows * a.lanes >= int64_t(num_sms()) * 6 * QG_KV_RB * KT; }
 
 template <typename T, bool E4M3, int L>
 cudaError_t write_rows(const KvRows &a, const KvSource<T> &s, cudaStream_t st)
 {
-    if (many_rows(a)) return launch_pdl(kv_write_kernel<T, E4M3, L, 4>, rows_grid(a, 4), dim3(KT), 0, st, a, s);
+    if (many_rows(a)) return launch_pdl(kv_write_kernel<T, E4M3, L, QG_KV_RB>, rows_grid(a, QG_KV_RB), dim3(KT), 0, st, a, s);
     return launch_pdl(kv_write_kernel<T, E4M3, L, 1>, rows_grid(a, 1), dim3(KT), 0, st, a, s);
 }
 
@@ -239,15 +320,15 @@ cudaError_t write_type(const KvPlanes &c, const KvSource<T> &s, const int64_t *s
 {
     const int L = write_lanes(c.e4m3, c.dim);
     const KvRows a = rows_args(c, slots, rows, 2 * c.heads * kv_blocks(c.e4m3, c.dim) * L);
-    if (!c.e4m3) return write_rows<T, false, 4>(a, s, st);
-    return L == 8 ? write_rows<T, true, 8>(a, s, st) : write_rows<T, true, 16>(a, s, st);
+    if (!c.e4m3) return write_rows<T, false, 2>(a, s, st);
+    return L == 4 ? write_rows<T, true, 4>(a, s, st) : write_rows<T, true, 8>(a, s, st);
 }
 
 template <typename T, bool E4M3>
 cudaError_t read_rows(const KvRows &a, void *k, void *v, cudaStream_t st)
 {
     T *kt = static_cast<T *>(k), *vt = static_cast<T *>(v);
-    if (many_rows(a)) return launch_pdl(kv_read_kernel<T, E4M3, 4>, rows_grid(a, 4), dim3(KT), 0, st, a, kt, vt);
+    if (many_rows(a)) return launch_pdl(kv_read_kernel<T, E4M3, QG_KV_RB>, rows_grid(a, QG_KV_RB), dim3(KT), 0, st, a, kt, vt);
     return launch_pdl(kv_read_kernel<T, E4M3, 1>, rows_grid(a, 1), dim3(KT), 0, st, a, kt, vt);
 }
 
