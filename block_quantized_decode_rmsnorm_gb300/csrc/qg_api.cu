@@ -798,6 +798,7 @@ constexpr int64_t kKvMaxRows = INT32_MAX;
 constexpr int32_t kKvMaxHeads = 1024;
 constexpr int64_t kAttnMaxBatch = int64_t(1) << 20;
 constexpr int64_t kAttnMaxHeads = 16384;
+constexpr int64_t kAttnMaxTokens = int64_t(1) << 30;
 constexpr int64_t kAttnMaxPlaces = int64_t(1) << 37;  // a CTA of 64 or more counts its part in 32 bits
 
 bool kv_dim_ok(int64_t d) { return d == 64 || d == 96 || d == 128 || d == 192 || d == 256; }
@@ -903,7 +904,7 @@ qg_status qg_attn_decode(const qg_kv_cache *cache, const void *q, int64_t q_row_
     if (qg_status st = check_kv(cache, false, &c, &cb, &sb); st != QG_OK) return st;
     if (!dtype_ok(q_dtype) || !dtype_ok(out_dtype)) return QG_ERR_UNSUPPORTED;
     if (batch < 0 || batch > kAttnMaxBatch || q_heads < c.heads || q_heads % c.heads != 0 || q_heads > kAttnMaxHeads ||
-        q_row_stride < 0 || q_head_stride < 0 || max_pages < 0 || max_pages > INT32_MAX / c.page || window < 0)
+        q_row_stride < 0 || q_head_stride < 0 || max_pages < 0 || max_pages > kAttnMaxTokens / c.page || window < 0)
         return QG_ERR_SHAPE;
     if (batch == 0) return QG_OK;
     if (qg_status st = check_kv(cache, true, &c, &cb, &sb); st != QG_OK) return st;

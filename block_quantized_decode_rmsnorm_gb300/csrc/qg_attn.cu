@@ -1,10 +1,6 @@
 // Decode attention: the workspace and the choice of kernel (qg_attn.cuh).
 #include "qg_attn.cuh"
 
-#ifndef QG_AT_DIRECT
-#define QG_AT_DIRECT 4
-#endif
-
 namespace qg {
 
 namespace {
@@ -68,14 +64,16 @@ int64_t attn_most_places(const KvPlanes &c, int64_t batch, int64_t q_heads, int6
     return batch * c.heads * ((group + s.heads - 1) / s.heads) * ((tokens + s.unit - 1) / s.unit + s.cost);
 }
 
-// The direct form's CTAs to an item, 0 for the line.
+// The direct form's CTAs to an item, 0 for the line: where each CTA has at most four units of the widest item (four units:
+// 1 x 4096 tokens, 8 heads 8.3 us, 10.1 in the line; eight: 8 x 2048 tokens 12.4, 10.9 in the line), and all items are
+// resident at once.  Clusters double while they are not more than half of the SMs together.
 int direct_cluster(int64_t items, int64_t most, const Sizes &s)
 {
     const int64_t units = most / items - s.cost;
     int n = 1;
     while (n < AT_CLUSTER && n < units && items * n * 2 <= num_sms()) n *= 2;
     const int64_t room = static_cast<int64_t>(num_sms()) * s.ctas;
-    return items * n <= room && (units + n - 1) / n <= QG_AT_DIRECT ? n : 0;
+    return items * n <= room && (units + n - 1) / n <= 4 ? n : 0;
 }
 
 cudaError_t launch_attn_decode(const KvPlanes &c, const void *q, int64_t q_row, int64_t q_head, int q_dtype,

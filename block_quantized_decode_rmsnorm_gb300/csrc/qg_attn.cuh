@@ -21,16 +21,23 @@
 //               is split into two f16 parts like q; for bf16 outputs its one rounding (2^-11,
 //               of either sign from token to token) is under the output's own (2^-8).
 //
-// A warp takes TOK tokens a step and copies its own steps to shared memory by cp.async,
-// STAGES - 1 of them ahead: no barrier, nothing shared between warps.  The rows there are
-// padded so that a step's fragment loads (8 bytes of eight tokens' keys, 4 bytes of values
-// of four tokens at a time) touch every bank once.
+// A warp takes TOK tokens a step and copies its own steps to shared memory by cp.async, one step ahead: no barrier,
+// nothing shared between warps.
 //
-// Work is split evenly whatever the lengths are: the units (a step of each of the CTA's
-// warps) of all sequences and heads lie in one line, and each CTA takes a stretch of it.
-// A CTA finds its place by a scan over the lengths.  A head that lies inside one stretch
-// is finished there; the parts of the others go to the workspace, and the CTA that brings
-// the last of them (a counter per head that starts in a CTA) joins them in order.
+// Two forms.  In the line (attn_decode_kernel) work is split evenly whatever the lengths are: the units (a step of each of
+// the CTA's warps) of all sequences and heads lie in one line, each item - a cache head of a sequence and up to 16 of its
+// query heads - behind COST places that stand for its beginning and end, and each CTA takes a stretch of it, which it
+// finds by a scan over the lengths.  An item that lies inside one stretch is finished there; the parts of the others go to
+// the workspace, and the CTA that brings the last of them (a counter per CTA in which an item begins) joins them in
+// order.  Where an item has few units at most, as the page tables' width tells the host, the direct form
+// (attn_direct_kernel) gives it a cluster, without scan, workspace and counter (one sequence of 700 tokens: 5.0 us, 7.3 in
+// the line).
+//
+// What bounds it: HBM where there is much to read (64 sequences of up to 8192 tokens, 8 heads of 128, 64 query heads, bf16:
+// Q8_0 97 us, 88 % of the copy rate, e4m3 93 us, 90 %), issue for heads of 64 (256 sequences of up to 1000, 16 heads, a
+// query head each: 69 us, 61 %, 0.6 instructions a cycle and scheduler, seven eighths of the MMA's columns unused), latency
+// below some 50 MB: about 4 us to the first unit's end (length, pages, tokens, each a round trip to memory), 2 us from the
+// last to the joined output.  Times in these files are of graph replays over operands that rotate.
 #pragma once
 
 #include <cfloat>
@@ -42,9 +49,11 @@ namespace qg {
 constexpr int AT_WARPS = 4;
 constexpr int AT_THREADS = 32 * AT_WARPS;
 constexpr int AT_CTAS_MAX = 4;  // per SM
-constexpr int AT_JOIN = 16;         // records of the workspace that are on their way at a time
-constexpr int AT_FEW = 4;  // rows of 32 sequences that every warp scans for itself
-constexpr int AT_CLUSTER = 8;
+// Records of the workspace that are on their way at a time where an item's parts are joined: one sequence of 32768 tokens,
+// 4 heads 18.8 us, 19.8 with 8, 17.9 with 24; but 48 ragged sequences 35.2, 34.8, 36.0.
+constexpr int AT_JOIN = 16;
+constexpr int AT_FEW = 4;      // rows of 32 sequences that every warp scans for itself
+constexpr int AT_CLUSTER = 8;  // CTAs to an item in the direct form, at most
 
 struct AttnArgs {
     KvPlanes c;
@@ -66,35 +75,15 @@ struct AttnArgs {
     bool narrow;     // the line has fewer than 2^31 places
 };
 
-#ifndef QG_AT_CH
-#define QG_AT_CH 2
-#endif
-#ifndef QG_AT_WCH
-#define QG_AT_WCH 1
-#endif
-#ifndef QG_AT_WSTAGES
-#define QG_AT_WSTAGES 2
-#endif
-#ifndef QG_AT_STAGES
-#define QG_AT_STAGES 2
-#endif
-#ifndef QG_AT_COST
-#define QG_AT_COST 2
-#endif
-#ifndef QG_AT_LEAST
-#define QG_AT_LEAST 1
-#endif
-#ifndef QG_AT_CTAS
-#define QG_AT_CTAS (D <= 64 ? 4 : D <= 96 ? 3 : 2)
-#endif
-
 template <bool E4M3, int D, int NT>
 struct AttnShape {
     static constexpr int NB = kv_blocks(E4M3, D);
     static constexpr int SB = E4M3 ? 4 : 2;      // bytes of a scale
-    static constexpr int CH = D <= 128 ? QG_AT_CH : QG_AT_WCH;  // tiles of 16 tokens to a step
+    // Tiles of 16 tokens to a step.  128 values: two (serving 105 us, 108 with one); 256: one (30.7, 44 with two, whose
+    // stages leave room for one CTA an SM).
+    static constexpr int CH = D <= 128 ? 2 : 1;
     static constexpr int TOK = KV_TILE * CH;
-    static constexpr int STAGES = D <= 128 ? QG_AT_STAGES : QG_AT_WSTAGES;
+    static constexpr int STAGES = 2;  // a third costs a CTA an SM (32 x 4000 tokens, 256 values: 31.8 us, 33.4 with three)
     static constexpr int SCALES = KV_TILE * NB * SB;      // bytes of a tile's scales
     static constexpr int CODES = KV_TILE * D;             // and of its keys' or values' codes
     static constexpr int TILE = 2 * CODES + 2 * SCALES;
@@ -106,9 +95,15 @@ struct AttnShape {
     static constexpr int QF = HEADS * D * 4;  // bytes of q's fragments
     static constexpr int SMEM = RING + QF + AT_WARPS * HEADS * 8 + HEADS * 4 + HEADS * NB * 4;
     static constexpr int RECORD_AT = (SMEM + 15) / 16 * 16;  // direct form: the CTA's part behind it
-    static constexpr int CTAS = 227 * 1024 / (SMEM + 1024) < QG_AT_CTAS ? 227 * 1024 / (SMEM + 1024) : QG_AT_CTAS;
+    // CTAs an SM: four for 64 values (chats 78 us, 113 with two), three for 96 (48, 53 with four, whose 128 registers
+    // spill), two for more (131072 tokens of 128: 55, 60 with three: the stretches get shorter, not the latencies).
+    static constexpr int WANT = D <= 64 ? 4 : D <= 96 ? 3 : 2, FIT = 227 * 1024 / (SMEM + 1024);
+    static constexpr int CTAS = FIT < WANT ? FIT : WANT;
+    static_assert(CTAS >= 1 && CTAS <= AT_CTAS_MAX, "the workspace has counters for so many");
     static constexpr int RECORD = HEADS * (D + 2);  // floats
-    static constexpr int COST = QG_AT_COST;  // of an item's beginning and end, in units
+    // Of an item's beginning and end, in units: with 1, 2, 3 the serving batch takes 99.4, 97.7, 98.7 us, in e4m3 with 16
+    // query heads to a head 37.4, 35.2, 35.0, windows of 1024 20.2, 19.3, 19.7.
+    static constexpr int COST = 2;
     static constexpr int QW = HEADS / AT_WARPS, QP = (D / 4 + 31) / 32;  // heads of q to a warp, 4 values a lane each
 
     // A tile's keys or values in shared memory.  A step's fragments are 32-byte pieces of four rows at a time, which have
@@ -130,16 +125,13 @@ struct AttnShape {
     static __host__ __device__ constexpr int piece_at(int piece) { return D == 256 ? piece / 4 * 128 : 0; }  // that constant
 };
 
-#ifndef QG_V_VOL
-#define QG_V_VOL
-#endif
 struct Quad {
     float v[4];
 };
 __device__ __forceinline__ Quad mma_f16(uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1, const Quad &c)
 {
     Quad d;
-    asm QG_V_VOL ("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
                  "{%10,%11,%12,%13};"
                  : "=f"(d.v[0]), "=f"(d.v[1]), "=f"(d.v[2]), "=f"(d.v[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c.v[0]), "f"(c.v[1]), "f"(c.v[2]), "f"(c.v[3]));
@@ -150,7 +142,7 @@ __device__ __forceinline__ Quad mma_f16(uint32_t a0, uint32_t a1, uint32_t a2, u
 __device__ __forceinline__ Quad mma_f16(uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
 {
     Quad d;
-    asm QG_V_VOL ("{ .reg .f32 z; mov.f32 z, 0f00000000; mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+    asm("{ .reg .f32 z; mov.f32 z, 0f00000000; mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
                  "{%8,%9}, {z,z,z,z}; }"
                  : "=f"(d.v[0]), "=f"(d.v[1]), "=f"(d.v[2]), "=f"(d.v[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -797,9 +789,7 @@ __device__ __forceinline__ int attn_units(const AttnArgs &a, Attn<E4M3, D, NT, F
 {
     using S = AttnShape<E4M3, D, NT>;
     int last = 0;
-#ifndef QG_V_UNROLL
 #pragma unroll 1
-#endif
     for (int u = 0; u < n_units; ++u) {
         feed.template next<DIRECT>(a, stage == 0 ? S::STAGES - 1 : stage - 1, stride, warp, lane);
         cp_async_wait<S::STAGES - 1>();

@@ -813,7 +813,10 @@ QG_API qg_status qg_kv_read(const qg_kv_cache *cache, const int64_t *slots, int6
  *       16-byte aligned, ZERO-FILLED before its first use and then left to the library,
  *       on the device of the call.  One workspace serves any calls of that many bytes or
  *       fewer one after another; calls that share one must not overlap in time.
- *   batch <= 2^20; max_pages * page_size < 2^31.  scale is any f32.
+ *   batch <= 2^20; max_pages * page_size <= 2^30 (QG_ERR_SHAPE); a batch whose page tables together
+ *   hold more than some 2^43 tokens times heads is QG_ERR_UNSUPPORTED.  scale is any f32.
+ *   Page tables no wider than the sequences need make short calls faster: where the widest
+ *   has few tokens, a cluster of CTAs takes each head, without a scan over the lengths.
  *   Outputs must not overlap inputs, the workspace or each other (QG_ERR_SHAPE).
  * Every sum is taken in an order that the sizes and lengths fix: results repeat bit for
  * bit.

@@ -266,11 +266,12 @@ def assert_attention(got, got_lse, want, what=""):
 
 
 def run_attention(torch, qg, fmt, dim, heads, group, page, lengths, window=0, kinds=("f32", "f32"), seed=0, scale=None,
-                  gain=1.0, lse=True, q_view="packed", spread=0.5):
+                  gain=1.0, lse=True, q_view="packed", spread=0.5, wide=False):
+    """wide: page tables for 5000 tokens more, with which calls on few short sequences take the form for long ones."""
     rng = np.random.default_rng(seed + dim * 7 + heads * 31 + group * 101 + page)
     pages = sum(-(-max(n, 0) // page) for n in lengths) + 2
     c = random_cache(rng, fmt, pages, heads, page, dim, spread)
-    t = tables(rng, lengths, page, pages)
+    t = tables(rng, lengths, page, pages, extra=5000 // page + 1 if wide else 1)
     batch, hq = len(lengths), heads * group
     q = torch.from_numpy((gain * rng.standard_normal((batch, hq, dim))).astype(np.float32)).to(types(torch)[kinds[0]])
     scale64 = dim ** -0.5 if scale is None else float(np.float32(scale))
@@ -295,34 +296,49 @@ def run_attention(torch, qg, fmt, dim, heads, group, page, lengths, window=0, ki
     a = qg.qg_attn_decode(qd, cache, td, ld, scale, window, out_dtype=types(torch)[kinds[1]], work=work)
     b = qg.qg_attn_decode(qd, cache, td, ld, scale, window, out_dtype=types(torch)[kinds[1]])
     assert torch.equal(a, got) and torch.equal(b, got)
+    assert not work.buf[:256].any()  # the counters are zero again
+
+
+WIDE = pytest.mark.parametrize("wide", [False, True])
+
+
+@WIDE
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dim", DIMS)
+@pytest.mark.parametrize("kinds", [("f32", "f32"), ("bf16", "bf16")])
+@pytest.mark.parametrize("group", [1, 2, 3, 8, 9, 16, 17, 40])
+def test_attention_heads(torch, qg, fmt, dim, kinds, group, wide):
+    run_attention(torch, qg, fmt, dim, 2, group, 16, [277, 1, 600], kinds=kinds, wide=wide)
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
-@pytest.mark.parametrize("dim", DIMS)
-@pytest.mark.parametrize("group", [1, 2, 3, 8, 9, 16, 17, 40])
-def test_attention_heads(torch, qg, fmt, dim, group):
-    run_attention(torch, qg, fmt, dim, 2, group, 16, [77, 1, 200], kinds=("bf16", "f32") if group % 2 else ("f32", "bf16"))
+@pytest.mark.parametrize("kinds", [("f32", "bf16"), ("bf16", "f32")])
+def test_attention_mixed_types(torch, qg, fmt, kinds):
+    run_attention(torch, qg, fmt, 128, 2, 4, 16, [277, 1, 600], kinds=kinds)
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("kinds", [("f32", "f32"), ("bf16", "bf16")])
 @pytest.mark.parametrize("lengths", [[1], [2], [15], [16], [17], [31, 32, 33], [63, 64, 65], [127, 128, 129], [0], [0, 0, 5, 0],
                                      [1000], [4097], [9000, 1, 0, 300, 12], [-3, 7, -2 ** 31]])
-def test_attention_lengths(torch, qg, fmt, kinds, lengths):
-    run_attention(torch, qg, fmt, 128, 2, 4, 16, lengths, kinds=kinds)
+@WIDE
+def test_attention_lengths(torch, qg, fmt, kinds, lengths, wide):
+    run_attention(torch, qg, fmt, 128, 2, 4, 16, lengths, kinds=kinds, wide=wide)
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("page", [16, 32, 48, 80, 128, 256, 4096])
-def test_attention_pages(torch, qg, fmt, page):
-    run_attention(torch, qg, fmt, 64, 3, 2, page, [500, 33, 0, 777], q_view="stacked")
+@WIDE
+def test_attention_pages(torch, qg, fmt, page, wide):
+    run_attention(torch, qg, fmt, 64, 3, 2, page, [500, 33, 0, 777], q_view="stacked", wide=wide)
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("dim", [64, 128, 256])
 @pytest.mark.parametrize("window", [1, 7, 16, 17, 100, 128, 700, 10 ** 6, 2 ** 62])
-def test_attention_window(torch, qg, fmt, dim, window):
-    run_attention(torch, qg, fmt, dim, 2, 3, 48, [900, 16, 0, 1, 129, 640], window=window, q_view="heads")
+@WIDE
+def test_attention_window(torch, qg, fmt, dim, window, wide):
+    run_attention(torch, qg, fmt, dim, 2, 3, 48, [900, 16, 0, 1, 129, 640], window=window, q_view="heads", wide=wide)
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
@@ -335,6 +351,30 @@ def test_attention_many_sequences(torch, qg, fmt):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("batch", [32, 33, 127, 128, 129, 300])
+def test_attention_batches(torch, qg, fmt, batch):
+    """Both sides of the scans' limits: rows of 32 sequences, up to four of them by every warp for itself."""
+    rng = np.random.default_rng(batch)
+    lengths = [int(n) for n in rng.integers(0, 300, batch)]
+    lengths[rng.integers(batch)] = 1700
+    run_attention(torch, qg, fmt, 64, 1, 3, 16, lengths, kinds=("f32", "f32"))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_attention_widest_tables(torch, qg, fmt):
+    """Page tables of 2^30 tokens for 128 heads: a line of 2^30 and more places, of which few are used."""
+    run = np.random.default_rng(21)
+    heads, dim, page, n = 128, 64, 4096, [300, 0, 7]
+    c = random_cache(run, fmt, 3, heads, page, dim)
+    t = np.zeros((3, (1 << 30) // page), np.int32)
+    t[0, 0], t[2, 0] = 2, 1
+    q = run.standard_normal((3, heads, dim)).astype(np.float32)
+    want = K.attention(q, c, t, n, 0.125)
+    got = qg.qg_attn_decode(dev(torch, q), upload(torch, qg, c), dev(torch, t), dev(torch, np.array(n, np.int32)))
+    assert_attention(got, None, want)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("heads", [1, 5, 24])
 def test_attention_long(torch, qg, fmt, heads):
     run_attention(torch, qg, fmt, 128, heads, 2, 64, [30011 // heads * 2, 5], kinds=("f32", "f32"))
@@ -342,9 +382,11 @@ def test_attention_long(torch, qg, fmt, heads):
 
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("gain,scale", [(0.0, None), (1e-20, None), (30.0, None), (1.0, 0.0), (1.0, -0.2), (1e6, 1e-7), (1.0, 3.0)])
-def test_attention_scores(torch, qg, fmt, gain, scale):
+@WIDE
+def test_attention_scores(torch, qg, fmt, gain, scale, wide):
     """Flat and peaked softmaxes, small and large queries, odd scales."""
-    run_attention(torch, qg, fmt, 128, 2, 4, 32, [300, 65], gain=gain, scale=scale)
+    run_attention(torch, qg, fmt, 128, 2, 4, 32, [300, 65], gain=gain, scale=scale, wide=wide)
+    run_attention(torch, qg, fmt, 128, 2, 4, 32, [300, 65], gain=gain, scale=scale, wide=wide, kinds=("bf16", "bf16"))
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
@@ -357,13 +399,14 @@ def test_attention_scales_far_apart(torch, qg, fmt):
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("dim", [96, 128])
 @pytest.mark.parametrize("n,window", [(0, 0), (1, 0), (37, 0), (130, 0), (200, 50), (300, 130)])
-def test_attention_ignores_what_is_not_seen(torch, qg, fmt, dim, n, window):
+@WIDE
+def test_attention_ignores_what_is_not_seen(torch, qg, fmt, dim, n, window, wide):
     """NaN and infinite scales and NaN codes in every token outside the ones seen, in all pages."""
     rng = np.random.default_rng(n + 5)
     page, heads, group = 48, 2, 3
     pages = 12
     c = random_cache(rng, fmt, pages, heads, page, dim)
-    t = tables(rng, [n], page, pages)
+    t = tables(rng, [n], page, pages, extra=120 if wide else 1)
     seen = np.zeros((pages, page), bool)
     for i in range(max(0, n - window) if window else 0, n):
         seen[t[0, i // page], i % page] = True
@@ -384,12 +427,13 @@ def test_attention_ignores_what_is_not_seen(torch, qg, fmt, dim, n, window):
 
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("bad", [-1, 20, 2 ** 31 - 1, -2 ** 31])
-def test_attention_bad_page(torch, qg, fmt, bad):
+@WIDE
+def test_attention_bad_page(torch, qg, fmt, bad, wide):
     """A page outside the cache makes its sequence NaN and leaves the others alone."""
     rng = np.random.default_rng(6)
     lengths, page, heads, group, dim, pages = [100, 300, 40], 16, 2, 2, 64, 32
     c = random_cache(rng, fmt, pages, heads, page, dim)
-    t = tables(rng, lengths, page, pages)
+    t = tables(rng, lengths, page, pages, extra=400 if wide else 1)
     q = rng.standard_normal((3, 4, dim)).astype(np.float32)
     want = K.attention(q, c, t, lengths, dim ** -0.5)
     if bad == 20:
@@ -423,6 +467,58 @@ def test_attention_nan_of_a_token_seen(torch, qg, fmt):
     c["kd"][p, 0, off] = np.nan
     got = qg.qg_attn_decode(dev(torch, q), upload(torch, qg, c), *args)
     assert torch.isnan(got[0]).all() and torch.isfinite(got[1]).all()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("odd", [np.nan, np.inf])
+@pytest.mark.parametrize("group", [3, 12])
+def test_attention_odd_query_head(torch, qg, fmt, kind, odd, group):
+    """NaN or an infinity in one query head leaves the other heads' bits alone."""
+    rng = np.random.default_rng(17)
+    c = random_cache(rng, fmt, 40, 2, 16, 128)
+    args = upload(torch, qg, c), dev(torch, tables(rng, [500, 70], 16, 40)), dev(torch, np.array([500, 70], np.int32))
+    q = torch.from_numpy(rng.standard_normal((2, 2 * group, 128)).astype(np.float32)).to(types(torch)[kind]).cuda()
+    plain = qg.qg_attn_decode(q, *args)
+    q2 = q.clone()
+    q2[0, 1, 77] = odd
+    got = qg.qg_attn_decode(q2, *args)
+    assert torch.isnan(got[0, 1]).all()
+    got[0, 1] = plain[0, 1]
+    assert torch.equal(got, plain)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("columns", [3, 40, 600])
+def test_attention_replayed(torch, qg, fmt, columns):
+    """A captured call replayed as lengths, pages and queries change, for tables that lead to each form (one CTA, a cluster,
+    the line), beside eager calls on another workspace."""
+    rng = np.random.default_rng(columns)
+    heads, group, dim, page, batch = 2, 4, 128, 16, 3
+    pages = 3 * columns
+    c = random_cache(rng, fmt, pages, heads, page, dim)
+    cache = upload(torch, qg, c)
+    q = torch.zeros((batch, heads * group, dim), device="cuda")
+    t = torch.zeros((batch, columns), dtype=torch.int32, device="cuda")
+    n = torch.zeros(batch, dtype=torch.int32, device="cuda")
+    out, lse, work = torch.empty_like(q), torch.empty((batch, heads * group), device="cuda"), qg.AttnWork.allocate(heads * group, heads, dim)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        qg.qg_attn_decode(q, cache, t, n, out=out, lse=lse, work=work)
+    torch.cuda.current_stream().wait_stream(s)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        qg.qg_attn_decode(q, cache, t, n, out=out, lse=lse, work=work)
+        inner = qg.qg_attn_decode(q, cache, t, n)  # a workspace of the capture's own
+    for lengths in ([1, columns * 16, 5], [0, 17, columns * 7], [columns * 16] * 3, [0, 0, 0]):
+        tn = rng.permutation(pages).reshape(batch, columns).astype(np.int32)
+        qn = rng.standard_normal(q.shape).astype(np.float32)
+        q.copy_(torch.from_numpy(qn)), t.copy_(torch.from_numpy(tn)), n.copy_(torch.tensor(lengths, dtype=torch.int32))
+        g.replay()
+        want = K.attention(qn, c, tn, lengths, float(np.float32(dim ** -0.5)))
+        assert_attention(out, lse, want, lengths)
+        assert torch.equal(inner, out) and torch.equal(qg.qg_attn_decode(q, cache, t, n), out)
 
 
 def test_attention_length_beyond_the_table(torch, qg):
@@ -522,12 +618,14 @@ def test_decode_steps(torch, qg, fmt):
         assert_attention(out, None, want, i)
 
 
-def test_two_streams_and_threads(torch, qg):
+@pytest.mark.parametrize("columns", [96, 600])
+def test_two_streams_and_threads(torch, qg, columns):
     """Calls at once on streams of their own, each with its own workspace, against calls one by one."""
     rng = np.random.default_rng(13)
     c = random_cache(rng, "q8_0", 400, 2, 16, 128)
     cache = upload(torch, qg, c)
-    t = dev(torch, rng.permutation(400)[:384].reshape(4, 96).astype(np.int32))
+    t = rng.permutation(400)[:384].reshape(4, 96).astype(np.int32)
+    t = dev(torch, np.pad(t, ((0, 0), (0, columns - 96))))
     n = dev(torch, np.array([1500, 1, 700, 1536], np.int32))
     qs = [torch.randn((4, 8, 128), device="cuda") for _ in range(4)]
     alone = [qg.qg_attn_decode(q, cache, t, n) for q in qs]

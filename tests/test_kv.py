@@ -151,7 +151,8 @@ def test_attention_refusals(lib):
     for kw, want in [(dict(qt=2), UNSUPPORTED), (dict(ot=-1), UNSUPPORTED), (dict(b=-1), SHAPE),
                      (dict(b=(1 << 20) + 1), SHAPE), (dict(hq=0), SHAPE), (dict(hq=1), SHAPE), (dict(hq=7), SHAPE),
                      (dict(hq=16386), SHAPE), (dict(qr=-8), SHAPE), (dict(qh=-8), SHAPE), (dict(mp=-1), SHAPE),
-                     (dict(mp=1 << 27), SHAPE), (dict(w=-1), SHAPE), (dict(q=None), NULL), (dict(p=None), NULL),
+                     (dict(mp=1 << 27), SHAPE), (dict(mp=(1 << 26) + 1), SHAPE), (dict(w=-1), SHAPE),
+                     (dict(mp=1 << 26, b=1 << 20, qr=0), UNSUPPORTED), (dict(q=None), NULL), (dict(p=None), NULL),
                      (dict(n=None), NULL), (dict(o=None), NULL), (dict(ws=None), NULL), (dict(q=at(5, 8)), ALIGN),
                      (dict(p=at(6, 2)), ALIGN), (dict(n=at(7, 1)), ALIGN), (dict(o=at(8, 8)), ALIGN),
                      (dict(lse=at(9, 2)), ALIGN), (dict(ws=at(10, 8)), ALIGN), (dict(qr=1026), ALIGN),
