@@ -64,15 +64,18 @@ int64_t attn_most_places(const KvPlanes &c, int64_t batch, int64_t q_heads, int6
     return batch * c.heads * ((group + s.heads - 1) / s.heads) * ((tokens + s.unit - 1) / s.unit + s.cost);
 }
 
-// The direct form's CTAs to an item, 0 for the line: where each CTA has at most four units of the widest item (four units:
+// The form of a call on `items` items of at most `tokens` tokens.  -1, the warps' form: where the items are more than find
+// room at a CTA to each, and short (8 heads of 128, 256 sequences of 16 tokens: 12.3 us, 21.7 in the line; 128 of 512: 27.0,
+// 28.8; 128 of 1024: 48.4, 39.0 in the line).  Otherwise the direct form's CTAs to an item, or 0 for the line: direct where each CTA has at most four units of the widest item (four units:
 // 1 x 4096 tokens, 8 heads 8.3 us, 10.1 in the line; eight: 8 x 2048 tokens 12.4, 10.9 in the line), and all items are
 // resident at once.  Clusters double while they are not more than half of the SMs together.
-int direct_cluster(int64_t items, int64_t most, const Sizes &s)
+int form_of(int64_t items, int64_t most, int64_t tokens, const Sizes &s)
 {
     const int64_t units = most / items - s.cost;
     int n = 1;
     while (n < AT_CLUSTER && n < units && items * n * 2 <= num_sms()) n *= 2;
     const int64_t room = static_cast<int64_t>(num_sms()) * s.ctas;
+    if (items > room && tokens <= AT_SHORT) return -1;
     return items * n <= room && (units + n - 1) / n <= 4 ? n : 0;
 }
 
@@ -100,7 +103,7 @@ cudaError_t launch_attn_decode(const KvPlanes &c, const void *q, int64_t q_row, 
     a.records = reinterpret_cast<float *>(static_cast<char *>(workspace) + counter_bytes());
     const int64_t most = attn_most_places(c, batch, q_heads, max_pages, window);
     a.narrow = most < (int64_t(1) << 31);
-    a.cluster = direct_cluster(batch * c.heads * a.chunks, most, s);
+    a.cluster = form_of(batch * c.heads * a.chunks, most, window > 0 && window < max_pages * c.page ? window : max_pages * c.page, s);
     return c.e4m3 ? launch_for<true>(a, most, st) : launch_for<false>(a, most, st);
 }
 

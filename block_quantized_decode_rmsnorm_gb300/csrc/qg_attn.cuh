@@ -24,14 +24,14 @@
 // A warp takes TOK tokens a step and copies its own steps to shared memory by cp.async, one step ahead: no barrier,
 // nothing shared between warps.
 //
-// Two forms.  In the line (attn_decode_kernel) work is split evenly whatever the lengths are: the units (a step of each of
+// Three forms.  In the line (attn_decode_kernel) work is split evenly whatever the lengths are: the units (a step of each of
 // the CTA's warps) of all sequences and heads lie in one line, each item - a cache head of a sequence and up to 16 of its
 // query heads - behind COST places that stand for its beginning and end, and each CTA takes a stretch of it, which it
 // finds by a scan over the lengths.  An item that lies inside one stretch is finished there; the parts of the others go to
 // the workspace, and the CTA that brings the last of them (a counter per CTA in which an item begins) joins them in
 // order.  Where an item has few units at most, as the page tables' width tells the host, the direct form
 // (attn_direct_kernel) gives it a cluster, without scan, workspace and counter (one sequence of 700 tokens: 5.0 us, 7.3 in
-// the line).
+// the line), and where there are many such items the warps' form (attn_warps_kernel) gives it a warp.
 //
 // What bounds it: HBM where there is much to read (64 sequences of up to 8192 tokens, 8 heads of 128, 64 query heads, bf16:
 // Q8_0 97 us, 88 % of the copy rate, e4m3 93 us, 90 %), issue for heads of 64 (256 sequences of up to 1000, 16 heads, a
@@ -49,11 +49,9 @@ namespace qg {
 constexpr int AT_WARPS = 4;
 constexpr int AT_THREADS = 32 * AT_WARPS;
 constexpr int AT_CTAS_MAX = 4;  // per SM
-// Records of the workspace that are on their way at a time where an item's parts are joined: one sequence of 32768 tokens,
-// 4 heads 18.8 us, 19.8 with 8, 17.9 with 24; but 48 ragged sequences 35.2, 34.8, 36.0.
-constexpr int AT_JOIN = 16;
 constexpr int AT_FEW = 4;      // rows of 32 sequences that every warp scans for itself
 constexpr int AT_CLUSTER = 8;  // CTAs to an item in the direct form, at most
+constexpr int AT_SHORT = 512;  // tokens of an item in the warps' form, at most
 
 struct AttnArgs {
     KvPlanes c;
@@ -71,7 +69,7 @@ struct AttnArgs {
     float *lse;
     int *counters;   // one per CTA, zero between calls
     float *records;  // two per CTA
-    int cluster;     // direct form: CTAs to an item
+    int cluster;     // direct form: CTAs to an item; 0: the line; -1: warps
     bool narrow;     // the line has fewer than 2^31 places
 };
 
@@ -93,7 +91,7 @@ struct AttnShape {
     static_assert(8 * OROW * 4 <= STAGE, "the warps' sums meet in the stages just read");
     static constexpr int RING = AT_WARPS * STAGES * STAGE;
     static constexpr int QF = HEADS * D * 4;  // bytes of q's fragments
-    static constexpr int SMEM = RING + QF + AT_WARPS * HEADS * 8 + HEADS * 4 + HEADS * NB * 4;
+    static constexpr int SMEM = RING + QF + AT_WARPS * HEADS * 8 + HEADS * 4;
     static constexpr int RECORD_AT = (SMEM + 15) / 16 * 16;  // direct form: the CTA's part behind it
     // CTAs an SM: four for 64 values (chats 78 us, 113 with two), three for 96 (48, 53 with four, whose 128 registers
     // spill), two for more (131072 tokens of 128: 55, 60 with three: the stretches get shorter, not the latencies).
@@ -101,6 +99,13 @@ struct AttnShape {
     static constexpr int CTAS = FIT < WANT ? FIT : WANT;
     static_assert(CTAS >= 1 && CTAS <= AT_CTAS_MAX, "the workspace has counters for so many");
     static constexpr int RECORD = HEADS * (D + 2);  // floats
+    // Records that are on their way at a time where an item's parts are joined: one sequence of 32768 tokens, 4 heads 18.8
+    // us, 19.8 with 8, 17.9 with 24; 48 ragged sequences 35.2, 34.8, 36.0; the 128 registers of 64 values leave room for 8
+    // (chats 69 us, 72 with 16).
+    static constexpr int JOIN = D <= 64 ? 8 : 16;
+    static constexpr int QUERY = (QF + HEADS * 4 + 15) / 16 * 16;  // warps' form: a warp's query
+    static constexpr int SMEM_WARPS = RING + AT_WARPS * QUERY, FIT_WARPS = 227 * 1024 / (SMEM_WARPS + 1024);
+    static constexpr int CTAS_WARPS = FIT_WARPS < WANT ? FIT_WARPS : WANT;
     // Of an item's beginning and end, in units: with 1, 2, 3 the serving batch takes 99.4, 97.7, 98.7 us, in e4m3 with 16
     // query heads to a head 37.4, 35.2, 35.0, windows of 1024 20.2, 19.3, 19.7.
     static constexpr int COST = 2;
@@ -149,11 +154,10 @@ __device__ __forceinline__ Quad mma_f16(uint32_t a0, uint32_t a1, uint32_t a2, u
     return d;
 }
 
-// Two codes, in bytes 0 and 1 of w (HI: 2 and 3), as an f16 pair.  Q8_0: w holds code + 128,
-// which placed in the mantissa of 1024 gives 1152 + code (OFFSET); less 1152, the code.  All exact.
-constexpr float kOffset = 1152.0f;
-constexpr uint32_t kOffset2 = 0x64806480u;
-template <bool E4M3, bool OFFSET, bool HI>
+// Two codes, in bytes 0 and 1 of w (HI: 2 and 3), as an f16 pair.  Q8_0: w holds code + 128, which placed in the
+// mantissa of 1024 gives 1152 + code; less 1152, the code.  All exact.  (Codes with the 1152 left on, which the sums then
+// start without, took as long, and left a residue of it where codes are small.)
+template <bool E4M3, bool HI>
 __device__ __forceinline__ uint32_t codes_f16(uint32_t w)
 {
     if constexpr (E4M3) {
@@ -162,9 +166,7 @@ __device__ __forceinline__ uint32_t codes_f16(uint32_t w)
         asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(h));
         return r;
     } else {
-        const uint32_t m = __byte_perm(w, 0x64646464u, HI ? 0x4342 : 0x4140);
-        if constexpr (OFFSET) return m;
-        const uint32_t k = kOffset2;
+        const uint32_t m = __byte_perm(w, 0x64646464u, HI ? 0x4342 : 0x4140), k = 0x64806480u;
         const __half2 v = __hsub2(*reinterpret_cast<const __half2 *>(&m), *reinterpret_cast<const __half2 *>(&k));
         return *reinterpret_cast<const uint32_t *>(&v);
     }
@@ -322,11 +324,6 @@ struct Attn {
         return bad;
     }
 
-    // Q8_0 codes go into the products as 1152 + code where results are bf16 (!FINE), and 1152 times the other
-    // operand's sum is what the accumulators start from, with its sign turned: for the scores a constant of the query,
-    // for the outputs one more MMA on a constant operand.  The cancellation costs 1152 / |code| of the additions'
-    // accuracy (2^-22), 2^-18 of a block's largest value.
-    static constexpr bool OFFSET = !E4M3 && !FINE;
     // Tiles of S: rows 0-7 are eight heads; rows 8-15 the low parts of the same heads (FINE), or eight heads more.
     static constexpr int ST = FINE ? NT : 1;
 
@@ -346,10 +343,10 @@ struct Attn {
         }
     }
 
-    // Query heads warp, warp + AT_WARPS, ... of a place's item: lane's pieces of four values.
+    // Query heads first, first + AT_WARPS, ... of a place's item: lane's pieces of four values.
     struct Query {
         uint4 v[S::QW][S::QP];  // as they lie in memory: bf16 in the first two words
-        __device__ __forceinline__ void load(const AttnArgs &a, const Place &p, int warp, int lane)
+        __device__ __forceinline__ void load(const AttnArgs &a, const Place &p, int first, int lane)
         {
             const int h = a.chunks == 1 ? p.item : p.item / a.chunks, h0 = (p.item - h * a.chunks) * S::HEADS;
             const int size = !FINE || a.q_bf16 ? 2 : 4;
@@ -358,7 +355,7 @@ struct Attn {
             for (int y = 0; y < S::QW; ++y)
 #pragma unroll
                 for (int i = 0; i < S::QP; ++i) {
-                    const int x = y * AT_WARPS + warp, piece = lane + 32 * i;
+                    const int x = y * AT_WARPS + first, piece = lane + 32 * i;
                     v[y][i] = make_uint4(0, 0, 0, 0);
                     if (h0 + x < a.group && piece < D / 4) {
                         const uint8_t *const at = row + (x * a.q_head + piece * 4) * size;
@@ -379,13 +376,26 @@ struct Attn {
         }
     };
 
-    // Their fragments, factors and (OFFSET) blocks' sums to shared memory.
-    static __device__ __forceinline__ void put_query(const AttnArgs &a, const Query &query, uint4 *qf, float *qc, float *qz,
-                                                     int warp, int lane)
+    // Piece p, dims 4 p to 4 p + 3 = 32 dg + 8 t + 4 k, of row x among q's fragments: high parts, low, high, low.
+    static __device__ __forceinline__ void put_piece(uint4 *qf, int x, int p, uint4 r)
+    {
+        const int dg = p >> 3, t = p >> 1 & 3, k = p & 1;
+        if constexpr (FINE || NT == 1) {
+            if constexpr (!FINE) r.y = r.w = 0;
+            qf[((dg * 2 + k) * NT + x / 8) * 32 + (x % 8) * 4 + t] = r;
+        } else {  // rows 8-15: the second eight heads
+            uint32_t *const at = reinterpret_cast<uint32_t *>(qf + (dg * 2 + k) * 32 + (x % 8) * 4 + t) + x / 8;
+            at[0] = r.x, at[2] = r.z;
+        }
+    }
+
+    // Their fragments and factors to shared memory.  Rows past the group's are zeros like any other: a
+    // branch around them keeps a warp's rows from running beside one another (4 sequences of 16 tokens: 3.4 us, 4.0 with it).
+    static __device__ __forceinline__ void put_query(const AttnArgs &a, const Query &query, uint4 *qf, float *qc, int first, int lane)
     {
 #pragma unroll
         for (int y = 0; y < S::QW; ++y) {
-            const int x = y * AT_WARPS + warp;
+            const int x = y * AT_WARPS + first;
             float4 v[S::QP];
 #pragma unroll
             for (int i = 0; i < S::QP; ++i) v[i] = query.get(a, y, i);
@@ -412,33 +422,15 @@ struct Attn {
                 const float2 b23 = __half22float2(*reinterpret_cast<const __half2 *>(&r.z));
                 r.y = pack_f16(w.x - b01.x, w.y - b01.y);
                 r.w = pack_f16(w.z - b23.x, w.w - b23.y);
-                // piece p: dims 32 dg + 8 t + 4 k
-                const int dg = p >> 3, t = p >> 1 & 3, k = p & 1;
-                if (p < D / 4) {
-                    if constexpr (FINE || NT == 1) {
-                        if constexpr (!FINE) r.y = r.w = 0;
-                        qf[((dg * 2 + k) * NT + x / 8) * 32 + (x % 8) * 4 + t] = r;
-                    } else {  // rows 8-15: the second eight heads
-                        uint32_t *const at = reinterpret_cast<uint32_t *>(qf + (dg * 2 + k) * 32 + (x % 8) * 4 + t) + x / 8;
-                        at[0] = r.x, at[2] = r.z;
-                    }
-                }
-                if constexpr (OFFSET) {  // a block's sum, by its eight lanes
-                    float sum = (b01.x + b01.y) + (b23.x + b23.y);
-                    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-                    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                    sum += __shfl_xor_sync(0xffffffffu, sum, 4);
-                    if (p < D / 4 && (lane & 7) == 0) qz[x * S::NB + dg] = -kOffset * sum;
-                }
+                if (p < D / 4) put_piece(qf, x, p, r);
             }
             if (lane == 0) qc[x] = a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(ex - 14 + 127) << 23);
         }
     }
 
-    // One step: `st` its stage, `qf` q's fragments, qz what to take off a block's sum (OFFSET).  EDGE: some of its tokens
-    // are not seen, or on a page outside the cache.
+    // One step: `st` its stage, `qf` q's fragments.  EDGE: some of its tokens are not seen, or on a page outside the cache.
     template <bool EDGE>
-    __device__ __forceinline__ void step(const uint8_t *st, const uint4 *qf, const float *qz, int at, Seen seen, uint32_t bad, int lane)
+    __device__ __forceinline__ void step(const uint8_t *st, const uint4 *qf, int at, Seen seen, uint32_t bad, int lane)
     {
         const int g = lane >> 2, t = lane & 3;
         const uint8_t *kx[S::NX], *vx[S::NX];
@@ -469,8 +461,8 @@ struct Attn {
                 for (int j = 0; j < 2 * CH; ++j) {
                     const uint2 w = *reinterpret_cast<const uint2 *>(kx[dg % S::NX] + S::piece_at(dg) + (j / 2) * S::TILE + (j % 2) * 8 * S::plane(dg));
                     const uint32_t x = code_bits<E4M3>(w.x), y = code_bits<E4M3>(w.y);
-                    const uint32_t b0 = codes_f16<E4M3, OFFSET, false>(x), b1 = codes_f16<E4M3, OFFSET, true>(x);
-                    const uint32_t b2 = codes_f16<E4M3, OFFSET, false>(y), b3 = codes_f16<E4M3, OFFSET, true>(y);
+                    const uint32_t b0 = codes_f16<E4M3, false>(x), b1 = codes_f16<E4M3, true>(x);
+                    const uint32_t b2 = codes_f16<E4M3, false>(y), b3 = codes_f16<E4M3, true>(y);
 #pragma unroll
                     for (int i = 0; i < ST; ++i) {
                         acc[i][j] = first ? mma_f16(qa[i][0].x, qa[i][0].y, qa[i][0].z, qa[i][0].w, b0, b1)
@@ -481,14 +473,12 @@ struct Attn {
             }
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
-                float z = 0.0f;
-                if constexpr (OFFSET) z = qz[(8 * i + g) * NB + b];
 #pragma unroll
                 for (int j = 0; j < 2 * CH; ++j)
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         const float v = FINE ? acc[FINE ? i : 0][j].v[x] + acc[FINE ? i : 0][j].v[2 + x]
-                                             : OFFSET ? acc[0][j].v[2 * i + x] + z : acc[0][j].v[2 * i + x];
+                                             : acc[0][j].v[2 * i + x];
                         s[i][j][x] = b == 0 ? v * dk[j].get(x, 0) : fmaf(v, dk[j].get(x, b), s[i][j][x]);
                     }
             }
@@ -570,7 +560,6 @@ struct Attn {
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
             uint32_t hi[NT][CH][2], lo[NT][CH][2];
-            Quad y[NT];
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
 #pragma unroll
@@ -582,12 +571,6 @@ struct Attn {
                         const float2 back = __half22float2(*reinterpret_cast<const __half2 *>(&h));
                         lo[i][j / 2][j % 2] = pack_f16(w0 - back.x, w1 - back.y);
                     }
-                }
-                if constexpr (OFFSET) {
-                    constexpr uint32_t k = kOffset2 ^ 0x80008000u;  // -1152
-                    y[i] = mma_f16(k, k, k, k, hi[i][0][0], hi[i][0][1]);
-#pragma unroll
-                    for (int ch = 1; ch < CH; ++ch) y[i] = mma_f16(k, k, k, k, hi[i][ch][0], hi[i][ch][1], y[i]);
                 }
             }
 #pragma unroll
@@ -602,10 +585,10 @@ struct Attn {
                     const uint32_t v9 = code_bits<E4M3>(*reinterpret_cast<const uint32_t *>(v + 12 * S::plane(dg)));
                     const uint32_t x0 = __byte_perm(v0, v1, 0x5140), x1 = __byte_perm(v0, v1, 0x7362);
                     const uint32_t y0 = __byte_perm(v8, v9, 0x5140), y1 = __byte_perm(v8, v9, 0x7362);
-                    const uint32_t va[2][4] = {{codes_f16<E4M3, OFFSET, false>(x0), codes_f16<E4M3, OFFSET, true>(x0),
-                                                codes_f16<E4M3, OFFSET, false>(y0), codes_f16<E4M3, OFFSET, true>(y0)},
-                                               {codes_f16<E4M3, OFFSET, false>(x1), codes_f16<E4M3, OFFSET, true>(x1),
-                                                codes_f16<E4M3, OFFSET, false>(y1), codes_f16<E4M3, OFFSET, true>(y1)}};
+                    const uint32_t va[2][4] = {{codes_f16<E4M3, false>(x0), codes_f16<E4M3, true>(x0),
+                                                codes_f16<E4M3, false>(y0), codes_f16<E4M3, true>(y0)},
+                                               {codes_f16<E4M3, false>(x1), codes_f16<E4M3, true>(x1),
+                                                codes_f16<E4M3, false>(y1), codes_f16<E4M3, true>(y1)}};
 #pragma unroll
                     for (int i = 0; i < NT; ++i)
 #pragma unroll
@@ -618,8 +601,7 @@ struct Attn {
                                 d = mma_f16(q[0], q[1], q[2], q[3], hi[i][ch][0], hi[i][ch][1], d);
                             } else {
                                 d = ch > 0 ? mma_f16(q[0], q[1], q[2], q[3], hi[i][ch][0], hi[i][ch][1], d)
-                                           : OFFSET ? mma_f16(q[0], q[1], q[2], q[3], hi[i][ch][0], hi[i][ch][1], y[i])
-                                                    : mma_f16(q[0], q[1], q[2], q[3], hi[i][ch][0], hi[i][ch][1]);
+                                           : mma_f16(q[0], q[1], q[2], q[3], hi[i][ch][0], hi[i][ch][1]);
                             }
                         }
                 }
@@ -683,14 +665,14 @@ struct Share {
 };
 
 // Outputs of a sequence that sees nothing: query heads [first, first + heads).
-template <int D>
+template <int D, int THREADS = AT_THREADS>
 __device__ __forceinline__ void attn_nothing(const AttnArgs &a, int64_t b, int first, int heads)
 {
     const int64_t row = b * a.q_heads + first;
-    for (int i = threadIdx.x; i < heads * (D / 4); i += AT_THREADS)
+    for (int i = threadIdx.x % THREADS; i < heads * (D / 4); i += THREADS)
         attn_store(a, row + i / (D / 4), D, i % (D / 4) * 4, make_float4(0, 0, 0, 0), 1.0f);
     if (a.lse)
-        for (int i = threadIdx.x; i < heads; i += AT_THREADS) a.lse[row + i] = -__int_as_float(0x7f800000);
+        for (int i = threadIdx.x % THREADS; i < heads; i += THREADS) a.lse[row + i] = -__int_as_float(0x7f800000);
 }
 
 __device__ __forceinline__ float2 ld_cluster_f2(const float *local, uint32_t rank)
@@ -728,10 +710,11 @@ struct Feed {
         bad = 0;
         ring = smem_addr(smem) + warp * S::STAGES * S::STAGE;
     }
-    // The pages of this warp's tiles from p's unit on, units `stride` apart, of tokens in [first, end).
+    // The pages of this warp's tiles from p's unit on, units of W steps `stride` apart, of tokens in [first, end).
+    template <int W>
     __device__ __forceinline__ void look_up(const AttnArgs &a, const typename A::Place &p, int first, int end, int stride, int warp, int lane)
     {
-        const uint32_t step = static_cast<uint32_t>(first) / S::TOK + (p.unit() + lane / S::CH * stride) * AT_WARPS + warp;
+        const uint32_t step = static_cast<uint32_t>(first) / S::TOK + (p.unit() + lane / S::CH * stride) * W + warp;
         token = step * S::TOK + lane % S::CH * KV_TILE;
         page = 0;
         used = -1;
@@ -754,7 +737,7 @@ struct Feed {
 
     // The copies of the step ahead into a stage, and on to the one after it: the next unit of the stretch, or
     // (DIRECT) of the item, `stride` on.
-    template <bool DIRECT>
+    template <bool DIRECT, int W>
     __device__ __forceinline__ void next(const AttnArgs &a, int stage, int stride, int warp, int lane)
     {
         if (used < 0) resolve(a);
@@ -762,7 +745,7 @@ struct Feed {
             int64_t rows[S::CH];
 #pragma unroll
             for (int i = 0; i < S::CH; ++i) rows[i] = __shfl_sync(0xffffffffu, row, used + i);
-            const int at = (static_cast<uint32_t>(load.seen.first) / S::TOK + load.unit() * AT_WARPS + warp) * S::TOK;
+            const int at = (static_cast<uint32_t>(load.seen.first) / S::TOK + load.unit() * W + warp) * S::TOK;
             const uint32_t x = A::copy(a, load.seen, at, rows, ring + stage * S::STAGE, lane);
             bad = (bad & ~(((1u << S::CH) - 1) << (stage * S::CH))) | x << (stage * S::CH);
             used += S::CH;
@@ -774,34 +757,33 @@ struct Feed {
                 load.next_item(a);
                 look = true;
             }
-            if (look && load.left > 0) look_up(a, load, load.seen.first, load.seen.n, stride, warp, lane);
+            if (look && load.left > 0) look_up<W>(a, load, load.seen.first, load.seen.n, stride, warp, lane);
         }
         cp_async_commit();
     }
 };
 
-// n_units units of an item, `stride` apart from unit0 on, after the copies of the first STAGES - 1 have begun.  Returns
+// n_units units of W steps of an item, `stride` apart from unit0 on, after the copies of the first STAGES - 1 have begun.  Returns
 // the stage that was read last.
-template <bool DIRECT, bool E4M3, int D, int NT, bool FINE>
+template <bool DIRECT, int W, bool E4M3, int D, int NT, bool FINE>
 __device__ __forceinline__ int attn_units(const AttnArgs &a, Attn<E4M3, D, NT, FINE> &state, Feed<E4M3, D, NT, FINE> &feed, Seen seen,
-                                          int unit0, int n_units, int stride, int &stage, const uint8_t *smem, const uint4 *qf,
-                                          const float *qz, int warp, int lane)
+                                          int unit0, int n_units, int stride, int &stage, const uint8_t *ring, const uint4 *qf, int warp, int lane)
 {
     using S = AttnShape<E4M3, D, NT>;
     int last = 0;
 #pragma unroll 1
     for (int u = 0; u < n_units; ++u) {
-        feed.template next<DIRECT>(a, stage == 0 ? S::STAGES - 1 : stage - 1, stride, warp, lane);
+        feed.template next<DIRECT, W>(a, stage == 0 ? S::STAGES - 1 : stage - 1, stride, warp, lane);
         cp_async_wait<S::STAGES - 1>();
         __syncwarp();
-        const int step = static_cast<uint32_t>(seen.first) / S::TOK + (unit0 + u * stride) * AT_WARPS + warp, at = step * S::TOK;
-        const uint8_t *const st = smem + (warp * S::STAGES + stage) * S::STAGE;
+        const int step = static_cast<uint32_t>(seen.first) / S::TOK + (unit0 + u * stride) * W + warp, at = step * S::TOK;
+        const uint8_t *const st = ring + stage * S::STAGE;
         const uint32_t off = feed.bad >> (stage * S::CH) & ((1u << S::CH) - 1);
         if (at < seen.n) {
             if (at < seen.first || at + S::TOK > seen.n || off != 0)
-                state.template step<true>(st, qf, qz, at, seen, off, lane);
+                state.template step<true>(st, qf, at, seen, off, lane);
             else
-                state.template step<false>(st, qf, qz, at, seen, 0, lane);
+                state.template step<false>(st, qf, at, seen, 0, lane);
         }
         __syncwarp();
         last = stage;
@@ -898,7 +880,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnShape<E4M3, D, NT>::CTAS) attn
     extern __shared__ __align__(128) uint8_t smem[];
     uint4 *const qf = reinterpret_cast<uint4 *>(smem + S::RING);
     float2 *const ml = reinterpret_cast<float2 *>(smem + S::RING + S::QF);  // [warp][head]: m, l
-    float *const qc = reinterpret_cast<float *>(ml + AT_WARPS * S::HEADS), *const qz = qc + S::HEADS;
+    float *const qc = reinterpret_cast<float *>(ml + AT_WARPS * S::HEADS);
     __shared__ int64_t sums[AT_WARPS];
     __shared__ int64_t found_at;
     __shared__ int found_b;
@@ -1022,9 +1004,9 @@ __global__ void __launch_bounds__(AT_THREADS, AttnShape<E4M3, D, NT>::CTAS) attn
     // ---- the first copies
     Feed<E4M3, D, NT, FINE> feed;
     feed.start(use, smem, warp);
-    feed.look_up(a, use, use.seen.first, use.seen.n, 1, warp, lane);
+    feed.template look_up<AT_WARPS>(a, use, use.seen.first, use.seen.n, 1, warp, lane);
 #pragma unroll
-    for (int i = 0; i < S::STAGES - 1; ++i) feed.template next<false>(a, i, 1, warp, lane);
+    for (int i = 0; i < S::STAGES - 1; ++i) feed.template next<false, AT_WARPS>(a, i, 1, warp, lane);
 
     A state;
     int stage = 0;
@@ -1033,10 +1015,10 @@ __global__ void __launch_bounds__(AT_THREADS, AttnShape<E4M3, D, NT>::CTAS) attn
         const int h = a.chunks == 1 ? use.item : use.item / a.chunks, h0 = (use.item - h * a.chunks) * S::HEADS;  // cache head; its first query head here
         const int heads = min(S::HEADS, a.group - h0);
         const int unit0 = use.unit(), n_units = min(use.units - unit0, use.left);
-        A::put_query(a, query, qf, qc, qz, warp, lane);
+        A::put_query(a, query, qf, qc, warp, lane);
         __syncthreads();
         state.begin(qc, lane);
-        const int last = attn_units<false>(a, state, feed, use.seen, unit0, n_units, 1, stage, smem, qf, qz, warp, lane);
+        const int last = attn_units<false, AT_WARPS>(a, state, feed, use.seen, unit0, n_units, 1, stage, smem + warp * S::STAGES * S::STAGE, qf, warp, lane);
         // ---- the warps meet: no copy into the stage read last is begun before the next segment's first barrier
         const bool whole = n_units == use.units;
         const int64_t first_unit = end - use.left - unit0;  // of the item, in the line
@@ -1075,7 +1057,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnShape<E4M3, D, NT>::CTAS) attn
                     const int x = i / (D / 4), col = i % (D / 4) * 4;
                     float top, l;
                     float4 v;
-                    attn_join<AT_JOIN>(parts, [&](int p, float2 &y, float4 &z) {
+                    attn_join<S::JOIN>(parts, [&](int p, float2 &y, float4 &z) {
                         const float *const from = a.records + (static_cast<int64_t>(c0 + p) * 2 + (p == 0)) * S::RECORD;
                         y = __ldcg(reinterpret_cast<const float2 *>(from + S::HEADS * D + 2 * x));
                         z = __ldcg(reinterpret_cast<const float4 *>(from + x * D + col));
@@ -1100,7 +1082,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnShape<E4M3, D, NT>::CTAS) attn
     extern __shared__ __align__(128) uint8_t smem[];
     uint4 *const qf = reinterpret_cast<uint4 *>(smem + S::RING);
     float2 *const ml = reinterpret_cast<float2 *>(smem + S::RING + S::QF);  // [warp][head]: m, l
-    float *const qc = reinterpret_cast<float *>(ml + AT_WARPS * S::HEADS), *const qz = qc + S::HEADS;
+    float *const qc = reinterpret_cast<float *>(ml + AT_WARPS * S::HEADS);
     float *const record = reinterpret_cast<float *>(smem + S::RECORD_AT);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int ctas = a.cluster, rank = static_cast<int>(blockIdx.x) % ctas;  // clusters are runs of the grid
@@ -1114,7 +1096,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnShape<E4M3, D, NT>::CTAS) attn
     typename A::Query query;
     query.load(a, use, warp, lane);
     Feed<E4M3, D, NT, FINE> feed;
-    if (a.window == 0) feed.look_up(a, use, 0, a.held, ctas, warp, lane);
+    if (a.window == 0) feed.template look_up<AT_WARPS>(a, use, 0, a.held, ctas, warp, lane);
     use.seen = seen_of(a, use.b);
     use.units = A::units(use.seen);
     use.left = use.units > rank ? (use.units - rank + ctas - 1) / ctas : 0;
@@ -1128,15 +1110,15 @@ __global__ void __launch_bounds__(AT_THREADS, AttnShape<E4M3, D, NT>::CTAS) attn
     const bool alone = use.units == 1 || ctas == 1;
     if (use.left > 0) {
         feed.start(use, smem, warp);
-        if (a.window > 0) feed.look_up(a, use, use.seen.first, use.seen.n, ctas, warp, lane);
+        if (a.window > 0) feed.template look_up<AT_WARPS>(a, use, use.seen.first, use.seen.n, ctas, warp, lane);
 #pragma unroll
-        for (int i = 0; i < S::STAGES - 1; ++i) feed.template next<true>(a, i, ctas, warp, lane);
-        A::put_query(a, query, qf, qc, qz, warp, lane);
+        for (int i = 0; i < S::STAGES - 1; ++i) feed.template next<true, AT_WARPS>(a, i, ctas, warp, lane);
+        A::put_query(a, query, qf, qc, warp, lane);
         __syncthreads();
         A state;
         state.begin(qc, lane);
         int stage = 0;
-        const int last = attn_units<true>(a, state, feed, use.seen, rank, use.left, ctas, stage, smem, qf, qz, warp, lane);
+        const int last = attn_units<true, AT_WARPS>(a, state, feed, use.seen, rank, use.left, ctas, stage, smem + warp * S::STAGES * S::STAGE, qf, warp, lane);
         cp_async_wait<0>();
         attn_meet(state, smem, last, ml, heads, [&](int x, int col, float4 v, float top, float sum) {
             if (alone) {
@@ -1163,6 +1145,73 @@ __global__ void __launch_bounds__(AT_THREADS, AttnShape<E4M3, D, NT>::CTAS) attn
         attn_store_lse(a, row0 + x, col, top, l);
     }
     cluster_sync();  // no CTA leaves while another reads its part
+}
+
+// The warps' form, for many items of few steps: an item to each warp, which finishes it by itself.
+template <bool E4M3, int D, int NT, bool FINE>
+__global__ void __launch_bounds__(AT_THREADS, AttnShape<E4M3, D, NT>::CTAS_WARPS) attn_warps_kernel(const __grid_constant__ AttnArgs a)
+{
+    using S = AttnShape<E4M3, D, NT>;
+    using A = Attn<E4M3, D, NT, FINE>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    uint8_t *const ring = smem + warp * S::STAGES * S::STAGE;
+    uint4 *const qf = reinterpret_cast<uint4 *>(smem + S::RING + warp * S::QUERY);
+    float *const qc = reinterpret_cast<float *>(qf) + S::QF / 4;
+    const int items = a.c.heads * a.chunks;
+    const int64_t which = static_cast<int64_t>(blockIdx.x) * AT_WARPS + warp;
+    pdl_wait();
+    pdl_trigger();
+    if (which >= a.batch * items) return;  // no barrier of the CTA's below
+    typename A::Place use;
+    use.b = static_cast<int>(which / items);
+    use.item = static_cast<int>(which - static_cast<int64_t>(use.b) * items);
+    use.at = S::COST;
+    typename A::Query query[AT_WARPS];
+#pragma unroll
+    for (int i = 0; i < AT_WARPS; ++i) query[i].load(a, use, i, lane);
+    Feed<E4M3, D, NT, FINE> feed;
+    if (a.window == 0) feed.template look_up<1>(a, use, 0, a.held, 1, 0, lane);
+    use.seen = seen_of(a, use.b);
+    use.units = use.left = A::steps(use.seen);  // units of one step here
+    const int h = a.chunks == 1 ? use.item : use.item / a.chunks, h0 = (use.item - h * a.chunks) * S::HEADS;
+    const int heads = min(S::HEADS, a.group - h0);
+    if (use.units == 0) {
+        attn_nothing<D, 32>(a, use.b, h * a.group + h0, heads);
+        return;
+    }
+    feed.start(use, ring, 0);
+    if (a.window > 0) feed.template look_up<1>(a, use, use.seen.first, use.seen.n, 1, 0, lane);
+#pragma unroll
+    for (int i = 0; i < S::STAGES - 1; ++i) feed.template next<true, 1>(a, i, 1, 0, lane);
+#pragma unroll
+    for (int i = 0; i < AT_WARPS; ++i) A::put_query(a, query[i], qf, qc, i, lane);
+    __syncwarp();
+    A state;
+    state.begin(qc, lane);
+    int stage = 0;
+    attn_units<true, 1>(a, state, feed, use.seen, 0, use.units, 1, stage, ring, qf, 0, lane);
+    cp_async_wait<0>();
+    const int64_t row0 = static_cast<int64_t>(use.b) * a.q_heads + h * a.group + h0;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        float l = state.l[i];
+        l += __shfl_xor_sync(0xffffffffu, l, 1);
+        l += __shfl_xor_sync(0xffffffffu, l, 2);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {  // the heads of this lane's columns
+            const float total = __shfl_sync(0xffffffffu, l, 8 * t + 4 * x), top = __shfl_sync(0xffffffffu, state.m[i], 8 * t + 4 * x);
+            const int head = 8 * i + 2 * t + x;
+            if (head < heads) {
+#pragma unroll
+                for (int dg = 0; dg < D / 32; ++dg) {
+                    const float(&p)[4] = state.o[i][2 * dg].v, (&r)[4] = state.o[i][2 * dg + 1].v;
+                    attn_store(a, row0 + head, D, dg * 32 + g * 4, make_float4(p[x], p[2 + x], r[x], r[2 + x]), total);
+                }
+                attn_store_lse(a, row0 + head, g, top, total);
+            }
+        }
+    }
 }
 
 template <bool E4M3, int D, int NT, bool FINE>
@@ -1193,8 +1242,19 @@ template <bool E4M3, int D>
 cudaError_t launch_attn_dim(const AttnArgs &a, int64_t most, cudaStream_t st);
 
 template <bool E4M3, int D, int NT, bool FINE>
+cudaError_t launch_attn_warps(const AttnArgs &a, cudaStream_t st)
+{
+    using S = AttnShape<E4M3, D, NT>;
+    const auto kernel = attn_warps_kernel<E4M3, D, NT, FINE>;
+    if (cudaError_t e = opt_in_smem(reinterpret_cast<const void *>(kernel), S::SMEM_WARPS); e != cudaSuccess) return e;
+    const int64_t items = a.batch * a.c.heads * a.chunks;
+    return launch_pdl(kernel, dim3(static_cast<unsigned>((items + AT_WARPS - 1) / AT_WARPS)), dim3(AT_THREADS), S::SMEM_WARPS, st, a);
+}
+
+template <bool E4M3, int D, int NT, bool FINE>
 cudaError_t launch_attn_shape(const AttnArgs &a, int64_t most, cudaStream_t st)
 {
+    if (a.cluster < 0) return launch_attn_warps<E4M3, D, NT, FINE>(a, st);
     return a.cluster > 0 ? launch_attn_direct<E4M3, D, NT, FINE>(a, st) : launch_attn_line<E4M3, D, NT, FINE>(a, most, st);
 }
 

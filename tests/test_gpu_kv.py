@@ -351,6 +351,34 @@ def test_attention_many_sequences(torch, qg, fmt):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dim", DIMS)
+@pytest.mark.parametrize("group,kinds", [(1, ("f32", "f32")), (7, ("bf16", "bf16")), (13, ("f32", "f32")), (20, ("bf16", "bf16"))])
+@pytest.mark.parametrize("longest,window", [(31, 0), (200, 0), (500, 40)])
+def test_attention_many_short(torch, qg, fmt, dim, group, kinds, longest, window):
+    """More heads than CTAs find room for, all of them short: a warp to each."""
+    rng = np.random.default_rng(longest)
+    lengths = [int(n) for n in rng.integers(0, longest + 1, 320)]
+    lengths[0], lengths[-1] = longest, 0
+    run_attention(torch, qg, fmt, dim, 2, group, 16, lengths, window=window, kinds=kinds)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_attention_bad_page_many_short(torch, qg, fmt):
+    rng = np.random.default_rng(23)
+    lengths, dim, pages = [40] * 400, 64, 1300
+    c = random_cache(rng, fmt, pages, 2, 16, dim)
+    t = tables(rng, lengths, 16, pages)
+    q = rng.standard_normal((400, 4, dim)).astype(np.float32)
+    want = K.attention(q, c, t, lengths, dim ** -0.5)
+    t[7, 1], t[200, 2], t[399, 0] = -1, pages, 2 ** 31 - 1
+    got = qg.qg_attn_decode(dev(torch, q), upload(torch, qg, c), dev(torch, t), dev(torch, np.array(lengths, np.int32)))
+    bad = [7, 200, 399]
+    assert torch.isnan(got[bad]).all()
+    keep = [i for i in range(400) if i not in bad]
+    assert_attention(got[keep], None, (want[0][keep], want[1][keep], [want[2][i] for i in keep]))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("batch", [32, 33, 127, 128, 129, 300])
 def test_attention_batches(torch, qg, fmt, batch):
     """Both sides of the scans' limits: rows of 32 sequences, up to four of them by every warp for itself."""
@@ -394,6 +422,25 @@ def test_attention_scales_far_apart(torch, qg, fmt):
     """Tokens whose values' scales differ by many powers of two: none is lost to the weights' 16 bits."""
     run_attention(torch, qg, fmt, 128, 2, 4, 32, [300, 65], spread=4.0, gain=0.01)
     run_attention(torch, qg, fmt, 128, 2, 4, 32, [300, 65], spread=4.0, gain=0.01, kinds=("bf16", "bf16"))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("lengths", [[2], [100, 3, 1500], [20] * 400])
+def test_attention_small_beside_large(torch, qg, fmt, kind, lengths):
+    """One large channel to a block of values: the others, small or zero, come out as exactly as if it were not there."""
+    rng = np.random.default_rng(29)
+    pages = sum(-(-n // 16) for n in lengths) + 1
+    c = random_cache(rng, fmt, pages, 2, 16, 128)
+    c["v"][..., 1::2] = rng.integers(0, 3, c["v"][..., 1::2].shape)
+    c["v"][..., ::32] = 0x7F if fmt == "q8_0" else 0x7E
+    c["v"][..., 5::16] = 0
+    t = tables(rng, lengths, 16, pages)
+    q = torch.from_numpy(rng.standard_normal((len(lengths), 6, 128)).astype(np.float32)).to(types(torch)[kind])
+    want = K.attention(q.float().numpy(), c, t, lengths, float(np.float32(128 ** -0.5)))
+    got = qg.qg_attn_decode(q.cuda(), upload(torch, qg, c), dev(torch, t), dev(torch, np.array(lengths, np.int32)))
+    assert_attention(got, None, want)
+    assert not got[..., 5::16].any()
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
