@@ -14,12 +14,15 @@
 //               scale the sums are exact up to the tensor core's additions, then
 //               s += d_K * (high + low).
 //   O^T = V^T P^T   16 dims x 8 heads.  S's accumulators are P^T's operand as they lie in
-//               the registers.  V's scale belongs to the summed index, so it goes into the
+//               the registers; ldmatrix turns the values' bytes round, four tokens of a
+//               dim to a register.  V's scale belongs to the summed index, so it goes into the
 //               weight: p_t d_V,t.  The running maximum is taken over s_t + log2 d_V,t, less
 //               14: the largest weight is about 2^14 whatever the scales are, and f16
-//               holds 11 bits of every weight down to 2^-28 of it.  For f32 outputs the weight
-//               is split into two f16 parts like q; for bf16 outputs its one rounding (2^-11,
-//               of either sign from token to token) is under the output's own (2^-8).
+//               holds 11 bits of every weight down to 2^-28 of it.  For f32 outputs (or queries)
+//               the weight is split into two f16 parts like q; for bf16 outputs its one
+//               rounding (2^-11, of either sign from token to token) is under the output's own
+//               (2^-9).  Each step's part is summed by itself and added in f32, which the
+//               tensor core's own additions would not do to half a step.
 //
 // A warp takes TOK tokens a step and copies its own steps to shared memory by cp.async, one step ahead: no barrier,
 // nothing shared between warps.
@@ -33,11 +36,16 @@
 // (attn_direct_kernel) gives it a cluster, without scan, workspace and counter (one sequence of 700 tokens: 5.0 us, 7.3 in
 // the line), and where there are many such items the warps' form (attn_warps_kernel) gives it a warp.
 //
-// What bounds it: HBM where there is much to read (64 sequences of up to 8192 tokens, 8 heads of 128, 64 query heads, bf16:
-// Q8_0 97 us, 88 % of the copy rate, e4m3 93 us, 90 %), issue for heads of 64 (256 sequences of up to 1000, 16 heads, a
-// query head each: 69 us, 61 %, 0.6 instructions a cycle and scheduler, seven eighths of the MMA's columns unused), latency
-// below some 50 MB: about 4 us to the first unit's end (length, pages, tokens, each a round trip to memory), 2 us from the
-// last to the joined output.  Times in these files are of graph replays over operands that rotate.
+// What bounds it: HBM where there is much to read, issue for narrow heads, latency below some 50 MB: about 4 us to
+// the first unit's end (length, pages, tokens, each a round trip to memory), 2 us from the last to the joined output.
+// Measured, the share of the copy rate and the names that the comments below give the cases:
+//   serving   64 sequences of up to 8192 tokens, 8 heads of 128, 64 query heads, bf16: Q8_0 96 us (89 %), e4m3 93 us (90 %)
+//   document  one sequence of 131072 tokens, 8 heads of 128, 32 query heads, Q8_0, bf16: 51 us (83 %)
+//   chats     256 sequences of up to 1000 tokens, 16 heads of 64, a query head each, Q8_0, bf16: 69 us (61 %; 0.6
+//             instructions a cycle and scheduler, seven eighths of the MMAs' columns unused)
+//   windows   32 sequences of up to 16384 tokens, the last 1024 of them, 4 heads of 256, 8 query heads, e4m3, f32: 19 us (52 %)
+// Figures of a choice are of the day it was made: they compare its two sides.  Times in these files are of graph replays
+// over operands that rotate.
 #pragma once
 
 #include <cfloat>
@@ -107,25 +115,32 @@ struct AttnShape {
     static constexpr int SMEM_WARPS = RING + AT_WARPS * QUERY, FIT_WARPS = 227 * 1024 / (SMEM_WARPS + 1024);
     static constexpr int CTAS_WARPS = FIT_WARPS < WANT ? FIT_WARPS : WANT;
     // Of an item's beginning and end, in units: with 1, 2, 3 the serving batch takes 99.4, 97.7, 98.7 us, in e4m3 with 16
-    // query heads to a head 37.4, 35.2, 35.0, windows of 1024 20.2, 19.3, 19.7.
+    // query heads to a head (48 of up to 6000) 37.4, 35.2, 35.0, windows 20.2, 19.3, 19.7.
     static constexpr int COST = 2;
     static constexpr int QW = HEADS / AT_WARPS, QP = (D / 4 + 31) / 32;  // heads of q to a warp, 4 values a lane each
 
-    // A tile's keys or values in shared memory.  A step's fragments are 32-byte pieces of four rows at a time, which have
-    // to lie in banks of their own, and copies are fastest into whole lines of 128 bytes: so rows are unpadded and the
-    // 32-byte pieces of a line change places with the row.  Rows of 96 and 192 bytes are two planes, of 64 and 32 and
-    // of 128 and 64 bytes to a row.  Values' rows are permuted, for their fragments take every other row.
+    // A tile's keys and values in shared memory.  Fragments of keys are 32-byte pieces of four rows at a time, of values 16
+    // bytes of eight rows (ldmatrix), which have to lie in banks of their own, and copies are fastest into whole lines of
+    // 128 bytes: so rows are unpadded and the pieces of a line change places with the row.  Rows of 96 and 192 bytes are
+    // two planes, of 64 and 32 and of 128 and 64 bytes to a row.
     static __host__ __device__ constexpr int plane(int piece) { return D == 96 ? (piece < 2 ? 64 : 32) : D == 192 ? (piece < 4 ? 128 : 64) : D; }
     static __host__ __device__ constexpr int plane_at(int piece) { return D == 96 && piece >= 2 ? KV_TILE * 64 : D == 192 && piece >= 4 ? KV_TILE * 128 : 0; }
     static __host__ __device__ constexpr int first_piece(int piece) { return D == 96 && piece >= 2 ? 2 : D == 192 && piece >= 4 ? 4 : 0; }
-    static __device__ __forceinline__ int at(int r, int piece)
+    // 32-byte piece of a row of keys.
+    static __device__ __forceinline__ int key_piece(int r, int piece)
     {
         const int w = plane(piece), d = piece - first_piece(piece);
         return plane_at(piece) + r * w + ((w >= 128 ? d ^ (r & 3) : w == 64 ? d ^ (r >> 1 & 1) : d) << 5);
     }
-    // 16-byte piece c of row r.
-    static __device__ __forceinline__ int key_at(int r, int c) { return at(r, c >> 1) + ((c & 1) << 4); }
-    static __device__ __forceinline__ int value_at(int r, int c) { return key_at((r & 8) | (r & 1) << 2 | (r >> 1 & 3), c); }
+    // 16-byte pieces, c, of token r: keys, and values, whose rows are in the order in which ldmatrix hands them to the
+    // lanes: tokens 2 t, 2 t + 1, 2 t + 8 and 2 t + 9 are rows 4 t to 4 t + 3.
+    static __device__ __forceinline__ int key_at(int r, int c) { return key_piece(r, c >> 1) + ((c & 1) << 4); }
+    static __device__ __forceinline__ int value_row_at(int r, int c)
+    {
+        const int w = plane(c >> 1), d = c - 2 * first_piece(c >> 1);
+        return plane_at(c >> 1) + r * w + ((w >= 128 ? d ^ (r & 7) : w == 64 ? d ^ (r >> 1 & 3) : d ^ (r >> 2 & 1)) << 4);
+    }
+    static __device__ __forceinline__ int value_at(int r, int c) { return value_row_at((r >> 1 & 3) * 4 + (r >> 3 & 1) * 2 + (r & 1), c); }
     static constexpr int NX = D >= 128 && D != 192 ? 4 : D / 32;  // pieces whose places differ by more than a constant
     static __host__ __device__ constexpr int piece_at(int piece) { return D == 256 ? piece / 4 * 128 : 0; }  // that constant
 };
@@ -327,7 +342,7 @@ struct Attn {
     // Tiles of S: rows 0-7 are eight heads; rows 8-15 the low parts of the same heads (FINE), or eight heads more.
     static constexpr int ST = FINE ? NT : 1;
 
-    Quad o[NT][2 * DG];  // O^T: tiles of 16 dims
+    Quad o[NT][2 * DG];  // O^T: tiles of 16 dims, of which this lane has dims g and g + 8 of heads 2 t and 2 t + 1
     float m[NT], l[NT];  // of head lane / 4 of each tile: the running reference, this lane's part of the sum
     float c[NT];         // the factor of its scores, in log2 units
 
@@ -340,6 +355,18 @@ struct Attn {
             c[i] = qc[8 * i + (lane >> 2)];
 #pragma unroll
             for (int j = 0; j < 2 * DG; ++j) o[i][j] = Quad{};
+        }
+    }
+
+    // Tile i's eight heads to rows of OROW floats.
+    __device__ __forceinline__ void put(int i, float *rows, int lane) const
+    {
+        float *const to = rows + 2 * (lane & 3) * S::OROW + (lane >> 2);
+#pragma unroll
+        for (int j = 0; j < 2 * DG; ++j) {
+            const float(&p)[4] = o[i][j].v;
+            to[j * 16] = p[0], to[j * 16 + 8] = p[2];
+            to[S::OROW + j * 16] = p[1], to[S::OROW + j * 16 + 8] = p[3];
         }
     }
 
@@ -433,11 +460,12 @@ struct Attn {
     __device__ __forceinline__ void step(const uint8_t *st, const uint4 *qf, int at, Seen seen, uint32_t bad, int lane)
     {
         const int g = lane >> 2, t = lane & 3;
-        const uint8_t *kx[S::NX], *vx[S::NX];
+        const uint8_t *kx[S::NX];
+        uint32_t vx[S::NX];
 #pragma unroll
         for (int i = 0; i < S::NX; ++i) {
-            kx[i] = st + S::at(g, i) + t * 8;
-            vx[i] = st + S::CODES + S::at(t, i) + g * 4;  // row 2 t; rows 2 t + 1, + 8, + 9 lie 4, 8, 12 places on
+            kx[i] = st + S::key_piece(g, i) + t * 8;
+            vx[i] = smem_addr(st) + S::CODES + S::value_row_at(lane & 15, 2 * i + (lane >> 4));
         }
         // ---- scores
         float s[NT][2 * CH][2];
@@ -578,17 +606,17 @@ struct Attn {
                 Quad acc[NT][2];
 #pragma unroll
                 for (int ch = 0; ch < CH; ++ch) {
-                    const uint8_t *v = vx[dg % S::NX] + S::piece_at(dg) + ch * S::TILE;
-                    const uint32_t v0 = code_bits<E4M3>(*reinterpret_cast<const uint32_t *>(v));
-                    const uint32_t v1 = code_bits<E4M3>(*reinterpret_cast<const uint32_t *>(v + 4 * S::plane(dg)));
-                    const uint32_t v8 = code_bits<E4M3>(*reinterpret_cast<const uint32_t *>(v + 8 * S::plane(dg)));
-                    const uint32_t v9 = code_bits<E4M3>(*reinterpret_cast<const uint32_t *>(v + 12 * S::plane(dg)));
-                    const uint32_t x0 = __byte_perm(v0, v1, 0x5140), x1 = __byte_perm(v0, v1, 0x7362);
-                    const uint32_t y0 = __byte_perm(v8, v9, 0x5140), y1 = __byte_perm(v8, v9, 0x7362);
-                    const uint32_t va[2][4] = {{codes_f16<E4M3, false>(x0), codes_f16<E4M3, true>(x0),
-                                                codes_f16<E4M3, false>(y0), codes_f16<E4M3, true>(y0)},
-                                               {codes_f16<E4M3, false>(x1), codes_f16<E4M3, true>(x1),
-                                                codes_f16<E4M3, false>(y1), codes_f16<E4M3, true>(y1)}};
+                    // four tokens' codes of dims g, g + 8, g + 16 and g + 24 of the block
+                    uint32_t r[4];
+                    asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];"
+                        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                        : "r"(vx[dg % S::NX] + S::piece_at(dg) + ch * S::TILE) : "memory");
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) r[i] = code_bits<E4M3>(r[i]);
+                    const uint32_t va[2][4] = {{codes_f16<E4M3, false>(r[0]), codes_f16<E4M3, false>(r[1]),
+                                                codes_f16<E4M3, true>(r[0]), codes_f16<E4M3, true>(r[1])},
+                                               {codes_f16<E4M3, false>(r[2]), codes_f16<E4M3, false>(r[3]),
+                                                codes_f16<E4M3, true>(r[2]), codes_f16<E4M3, true>(r[3])}};
 #pragma unroll
                     for (int i = 0; i < NT; ++i)
 #pragma unroll
@@ -808,13 +836,7 @@ __device__ __forceinline__ void attn_meet(const Attn<E4M3, D, NT, FINE> &state, 
         l += __shfl_xor_sync(0xffffffffu, l, 1);
         l += __shfl_xor_sync(0xffffffffu, l, 2);
         if ((lane & 3) == 0) ml[warp * S::HEADS + 8 * i + (lane >> 2)] = make_float2(state.m[i], l);
-        float *const to = meet + warp * MEET + 2 * (lane & 3) * S::OROW + (lane >> 2) * 4;
-#pragma unroll
-        for (int dg = 0; dg < D / 32; ++dg) {
-            const float(&p)[4] = state.o[i][2 * dg].v, (&r)[4] = state.o[i][2 * dg + 1].v;
-            *reinterpret_cast<float4 *>(to + dg * 32) = make_float4(p[0], p[2], r[0], r[2]);
-            *reinterpret_cast<float4 *>(to + S::OROW + dg * 32) = make_float4(p[1], p[3], r[1], r[3]);
-        }
+        state.put(i, meet + warp * MEET, lane);
         __syncthreads();
         for (int j = tid; j < min(heads - 8 * i, 8) * (D / 4); j += AT_THREADS) {
             const int y = j / (D / 4), x = 8 * i + y, col = j % (D / 4) * 4;
@@ -1154,7 +1176,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnShape<E4M3, D, NT>::CTAS_WARPS
     using S = AttnShape<E4M3, D, NT>;
     using A = Attn<E4M3, D, NT, FINE>;
     extern __shared__ __align__(128) uint8_t smem[];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint8_t *const ring = smem + warp * S::STAGES * S::STAGE;
     uint4 *const qf = reinterpret_cast<uint4 *>(smem + S::RING + warp * S::QUERY);
     float *const qc = reinterpret_cast<float *>(qf) + S::QF / 4;
@@ -1198,17 +1220,17 @@ __global__ void __launch_bounds__(AT_THREADS, AttnShape<E4M3, D, NT>::CTAS_WARPS
         float l = state.l[i];
         l += __shfl_xor_sync(0xffffffffu, l, 1);
         l += __shfl_xor_sync(0xffffffffu, l, 2);
+        float *const rows = reinterpret_cast<float *>(ring);  // nothing is being copied
+        __syncwarp();
+        state.put(i, rows, lane);
+        __syncwarp();
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {  // the heads of this lane's columns
-            const float total = __shfl_sync(0xffffffffu, l, 8 * t + 4 * x), top = __shfl_sync(0xffffffffu, state.m[i], 8 * t + 4 * x);
-            const int head = 8 * i + 2 * t + x;
-            if (head < heads) {
-#pragma unroll
-                for (int dg = 0; dg < D / 32; ++dg) {
-                    const float(&p)[4] = state.o[i][2 * dg].v, (&r)[4] = state.o[i][2 * dg + 1].v;
-                    attn_store(a, row0 + head, D, dg * 32 + g * 4, make_float4(p[x], p[2 + x], r[x], r[2 + x]), total);
-                }
-                attn_store_lse(a, row0 + head, g, top, total);
+        for (int j = lane; j < 8 * (D / 4); j += 32) {
+            const int y = j / (D / 4), col = j % (D / 4) * 4;
+            const float total = __shfl_sync(0xffffffffu, l, 4 * y), top = __shfl_sync(0xffffffffu, state.m[i], 4 * y);
+            if (8 * i + y < heads) {
+                attn_store(a, row0 + 8 * i + y, D, col, *reinterpret_cast<const float4 *>(rows + y * S::OROW + col), total);
+                attn_store_lse(a, row0 + 8 * i + y, col, top, total);
             }
         }
     }
