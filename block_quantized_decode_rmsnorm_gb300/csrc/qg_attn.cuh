@@ -8,20 +8,21 @@
 // matrix products, the softmax - so both products run on mma.sync m16n8k16 with the codes
 // as exact f16 integers (or e4m3 values), scales applied outside in f32:
 //
-//   S = Q K^T   16 rows x 8 tokens.  q's row, scaled by a power of two, is split into two
-//               f16 parts (22 bits); rows 0-7 of the tile are eight heads' high parts, rows
-//               8-15 their low parts, so the split costs no instruction.  Per block of a
-//               scale the sums are exact up to the tensor core's additions, then
-//               s += d_K * (high + low).
+//   S = Q K^T   16 rows x 8 tokens.  q's row is scaled by a power of two and, where queries or
+//               outputs are f32 (FINE), split into two f16 parts (22 bits): rows 0-7 of the tile
+//               are eight heads' high parts, rows 8-15 their low parts, so the split costs no
+//               instruction.  bf16's 8 bits need one part; rows 8-15 are then eight heads more
+//               or none.  Per block of a scale the sums are exact up to the tensor core's
+//               additions, then s += d_K * (high + low).
 //   O^T = V^T P^T   16 dims x 8 heads.  S's accumulators are P^T's operand as they lie in
 //               the registers; ldmatrix turns the values' bytes round, four tokens of a
 //               dim to a register.  V's scale belongs to the summed index, so it goes into the
 //               weight: p_t d_V,t.  The running maximum is taken over s_t + log2 d_V,t, less
 //               14: the largest weight is about 2^14 whatever the scales are, and f16
-//               holds 11 bits of every weight down to 2^-28 of it.  For f32 outputs (or queries)
-//               the weight is split into two f16 parts like q; for bf16 outputs its one
+//               holds 11 bits of every weight down to 2^-28 of it.  Where FINE
+//               the weight is split into two f16 parts like q; otherwise its one
 //               rounding (2^-11, of either sign from token to token) is under the output's own
-//               (2^-9).  Each step's part is summed by itself and added in f32, which the
+//               (2^-8).  Each step's part is summed by itself and added in f32, which the
 //               tensor core's own additions would not do to half a step.
 //
 // A warp takes TOK tokens a step and copies its own steps to shared memory by cp.async, one step ahead: no barrier,
