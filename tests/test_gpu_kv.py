@@ -695,6 +695,79 @@ def test_two_streams_and_threads(torch, qg, columns):
     assert not failed and all(torch.equal(a, b) for a, b in zip(got, alone))
 
 
+@pytest.mark.parametrize("columns", [4, 600])
+def test_first_call_inside_a_capture(torch, columns):
+    """A process whose first calls of all are captured, and its workspace allocated there too."""
+    import subprocess
+    import sys
+
+    code = f"""
+import torch
+import block_quantized_decode_rmsnorm_gb300 as qg
+cache = qg.KVCache.allocate(40, 16, 2, 128)
+k, v = torch.randn((2, 50, 2, 128), device='cuda')
+q = torch.randn((1, 8, 128), device='cuda')
+slots = torch.arange(50, device='cuda') + 32
+pages = (torch.arange({columns}, dtype=torch.int32, device='cuda') + 2)[None]
+n = torch.full((1,), 50, dtype=torch.int32, device='cuda')
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    qg.qg_kv_write(cache, k, v, slots)
+    back = qg.qg_kv_read(cache, slots)
+    o = qg.qg_attn_decode(q, cache, pages, n)
+g.replay()
+again = qg.qg_attn_decode(q, cache, pages, n)
+assert torch.equal(o, again) and bool(o.isfinite().all()) and torch.equal(back[0], qg.qg_kv_read(cache, slots)[0])
+assert (back[0] - k).abs().max() < 0.05
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_decode_layer(torch, qg):
+    """The decode step around the cache - norm, stacked qkv product, cache, attention, output product with the residual -
+    each call against f64 from what the calls before it left."""
+    rng = np.random.default_rng(31)
+    hidden, heads, group, dim, n = 256, 2, 2, 64, 21
+    hq = heads * group
+    from oracle import quantize_q8_0
+
+    def weight(rows, k):
+        w = (0.06 * rng.standard_normal((rows, k))).astype(np.float32)
+        q, d = quantize_q8_0(w)
+        return qg.Q8Weight(dev(torch, q), dev(torch, d).view(torch.float16)), q.astype(np.float64) * np.repeat(
+            d.view(np.float16).astype(np.float64), 32, axis=1)
+
+    def q8(x):
+        q, d = quantize_q8_0(np.ascontiguousarray(x, np.float32))
+        return q.astype(np.float64) * np.repeat(d.view(np.float16).astype(np.float64), 32, axis=1)
+
+    (wqkv, fqkv), (wo, fo) = weight((hq + 2 * heads) * dim, hidden), weight(hidden, hq * dim)
+    gamma = torch.ones(hidden, device="cuda")
+    cache = qg.KVCache.allocate(3, 16, heads, dim)
+    pages = torch.tensor([[2, 0]], dtype=torch.int32, device="cuda")
+    past = rng.standard_normal((2, n - 1, heads, dim)).astype(np.float32)
+    slots = np.array([2 * 16 + i if i < 16 else i - 16 for i in range(n)], np.int64)
+    qg.qg_kv_write(cache, dev(torch, past[0]), dev(torch, past[1]), dev(torch, slots[:-1]))
+    x = torch.from_numpy(rng.standard_normal((1, hidden)).astype(np.float32)).cuda()
+    xq, xd, _ = qg.rmsnorm_quantize(x, gamma, 1e-6)
+    qkv = qg.qgemv_q8_0(wqkv, xq, xd).view(1, hq + 2 * heads, dim)
+    qg.qg_kv_write(cache, qkv[:, hq: hq + heads], qkv[:, hq + heads:], dev(torch, slots[-1:]))
+    o = qg.qg_attn_decode(qkv[:, :hq], cache, pages, torch.tensor([n], dtype=torch.int32, device="cuda"))
+    oq, od = qg.quantize_act_q8_0(o.view(1, -1))
+    y = qg.qgemv_q8_0(wo, oq, od, epilogue="residual", residual=x)
+    want_qkv = (xq.double().cpu().numpy() * np.repeat(xd.double().cpu().numpy(), 32, axis=1)) @ fqkv.T
+    assert np.allclose(qkv.cpu().numpy().reshape(1, -1), want_qkv, rtol=0, atol=1e-5 * np.abs(want_qkv).max())
+    held = download(cache, "q8_0")
+    want, _, parts = K.attention(qkv[:, :hq].cpu().numpy(), held, pages.cpu().numpy(), [n], float(np.float32(dim ** -0.5)))
+    assert_attention(o, None, (want, None, parts))
+    new = K.rows(held, slots[-1:], "k")[0]
+    assert np.array_equal(new, K.values(*K.quantize(qkv[0, hq: hq + heads].cpu().numpy(), "q8_0"), "q8_0"))
+    want_y = q8(o.cpu().numpy().reshape(1, -1)) @ fo.T + x.double().cpu().numpy()
+    assert np.allclose(y.cpu().numpy(), want_y, rtol=0, atol=1e-5 * np.abs(want_y).max())
+
+
 def test_one_workspace_for_several_shapes(torch, qg):
     """A workspace of the largest need serves smaller calls in turn, and is left zeroed where it has to be."""
     work = qg.AttnWork.allocate(32, 2, 256)
