@@ -802,8 +802,8 @@ QG_API qg_status qg_kv_read(const qg_kv_cache *cache, const int64_t *slots, int6
  *       b * q_row_stride + h * q_head_stride + i; rows start on 16 bytes.
  *   q_heads: a multiple of the cache's heads, at most 16384.
  *   pages: device int32[batch][max_pages] (read): page t / page_size of sequence b's
- *       token t is pages[b][t / page_size].  Entries past a sequence's tokens are not
- *       read.  A page outside the cache under a token seen makes that sequence's
+ *       token t is pages[b][t / page_size].  Entries of pages without a token seen are not
+ *       used, whatever they hold.  A page outside the cache under a token seen makes that sequence's
  *       outputs NaN; nothing outside the cache is read.
  *   lengths: device int32[batch] (read).  Negative counts as 0, more than
  *       max_pages * page_size as that.

@@ -184,6 +184,10 @@ def test_write_nothing(torch, qg):
     o = qg.qg_attn_decode(one, none, torch.zeros((1, 0), dtype=torch.int32, device="cuda"),
                           torch.full((1,), 5, dtype=torch.int32, device="cuda"))
     assert not o.any()
+    for columns in (1, 600):  # pages of an empty pool: none of them exists
+        o = qg.qg_attn_decode(one, none, torch.zeros((1, columns), dtype=torch.int32, device="cuda"),
+                              torch.full((1,), 5, dtype=torch.int32, device="cuda"))
+        assert torch.isnan(o).all()
 
 
 # ---------------------------------------------------------------- read
