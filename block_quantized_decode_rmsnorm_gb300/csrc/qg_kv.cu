@@ -8,7 +8,7 @@
 
 namespace qg {
 
-constexpr int KT = 256;
+constexpr int KT = 128;  // with 256: 8192 rows written 13.8 us, 13.1 with 128; 16384 read 21.5, 20.6
 
 struct KvRows {
     KvPlanes c;
@@ -127,7 +127,7 @@ __device__ __noinline__ uint4 q8_codes16_any(float4 a, float4 b, float4 c, float
     return make_uint4(q8_pack4(a, d, rd), q8_pack4(b, d, rd), q8_pack4(c, d, rd), q8_pack4(e, d, rd));
 }
 
-// Bound by issue where rows are many (8192 rows of 8 heads of 128 bf16 values: 13.6 us for 51 MB, 0.7 instructions a cycle
+// Bound by issue where rows are many (8192 rows of 8 heads of 128 bf16 values: 13.1 us for 51 MB, 0.7 instructions a cycle
 // and scheduler): eight instructions a code, and the slot's, the addresses' and the maximum's beside them.
 template <typename T, bool E4M3, int L, int RB>
 __global__ void __launch_bounds__(KT) kv_write_kernel(KvRows a, KvSource<T> s)
@@ -305,10 +305,10 @@ dim3 rows_grid(const KvRows &a, int rb)
     return dim3(static_cast<unsigned>((a.rows + per - 1) / per), a.rows_at_once > 1 ? 1 : (a.lanes + KT - 1) / KT);
 }
 
-// Rows a thread: two where they still give every SM six CTAs (8192 rows written: 15.1 us with one, 13.7 with two, 13.9 with
+// Rows a thread: two where they still give every SM twelve CTAs (with CTAs of 256: 8192 rows written: 15.1 us with one, 13.7 with two, 13.9 with
 // four; 16384 read: 23.0, 21.3, 23.3), one where rows are few.
 constexpr int KRB = 2;
-bool many_rows(const KvRows &a) { return a.rows * a.lanes >= int64_t(num_sms()) * 6 * KRB * KT; }
+bool many_rows(const KvRows &a) { return a.rows * a.lanes >= int64_t(num_sms()) * 12 * KRB * KT; }
 
 template <typename T, bool E4M3, int L>
 cudaError_t write_rows(const KvRows &a, const KvSource<T> &s, cudaStream_t st)
