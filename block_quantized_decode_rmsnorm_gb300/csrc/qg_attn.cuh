@@ -538,13 +538,13 @@ struct Attn {
                     }
                 }
         }
-        // log2 of a token's largest scale, held where the sum of weights stays in range and infinities and NaN
-        // stay in their own blocks
+        // log2 of a token's largest scale, held where the sum of weights stays in range (2^30 tokens of up to
+        // 2^(14 + 82): 2^126) and infinities and NaN stay in their own blocks
 #pragma unroll
         for (int j = 0; j < 2 * CH; ++j)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                float top = E4M3 ? 0x1p-88f : 0x1p-25f;
+                float top = E4M3 ? 0x1p-82f : 0x1p-25f;
 #pragma unroll
                 for (int b = 0; b < NB; ++b) top = fmaxf(top, fabsf(dv[j][x][b]));
                 asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(e[j][x]) : "f"(fminf(top, E4M3 ? 0x1p119f : 65504.0f)));

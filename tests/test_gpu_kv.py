@@ -407,6 +407,31 @@ def test_attention_widest_tables(torch, qg, fmt):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("exponent", [-90, -24, 0])
+def test_attention_longest(torch, qg, fmt, exponent):
+    """2^30 tokens, one page over and over, of equal scores and values: o is the value, lse 30 ln 2.  The sum of weights stays
+    in range, whatever the values' scale.  Each of four warps in 608 CTAs adds its 13797 steps one after another, and their
+    sums are joined in 608 more: 2^14 roundings of 2^-24 in each of the two sums, 2^-20 for a weight."""
+    if fmt == "q8_0" and exponent < -24:
+        exponent = -25  # no binary16: the scale is zero
+    run = np.random.default_rng(37)
+    page, dim = 4096, 64
+    c = random_cache(run, fmt, 1, 1, page, dim)
+    code = run.integers(0, 0x7F, dim)
+    c["v"][...] = code.astype(c["v"].dtype)
+    c["vd"][...] = 2.0 ** exponent
+    t = np.zeros((1, (1 << 30) // page), np.int32)
+    lse = torch.empty((1, 1), device="cuda")
+    got = qg.qg_attn_decode(torch.zeros((1, 1, dim), device="cuda"), upload(torch, qg, c), dev(torch, t),
+                            dev(torch, np.array([1 << 30], np.int32)), lse=lse)
+    want = torch.from_numpy(code.astype(np.uint8))
+    want = (want.double() if fmt == "q8_0" else want.view(torch.float8_e4m3fn).double()) * float(c["vd"].flat[0])
+    each = 2.0 ** -10 + 2.0 ** -20 + 2.0 ** -23
+    assert ((got.double().cpu() - want).abs() <= 2 * each * want.abs()).all()
+    assert abs(lse.item() - 30 * np.log(2.0)) <= each
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("heads", [1, 5, 24])
 def test_attention_long(torch, qg, fmt, heads):
     run_attention(torch, qg, fmt, 128, heads, 2, 64, [30011 // heads * 2, 5], kinds=("f32", "f32"))
