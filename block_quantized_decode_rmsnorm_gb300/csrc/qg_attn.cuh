@@ -8,8 +8,8 @@
 // matrix products, the softmax - so both products run on mma.sync m16n8k16 with the codes
 // as exact f16 integers (or e4m3 values), scales applied outside in f32:
 //
-//   S = Q K^T   16 rows x 8 tokens.  q's row is scaled by a power of two and, where queries or
-//               outputs are f32 (FINE), split into two f16 parts (22 bits): rows 0-7 of the tile
+//   S = Q K^T   16 rows x 8 tokens.  q's row is scaled by a power of two and, where queries are f32
+//               (FINE), split into two f16 parts (22 bits): rows 0-7 of the tile
 //               are eight heads' high parts, rows 8-15 their low parts, so the split costs no
 //               instruction.  bf16's 8 bits need one part; rows 8-15 are then eight heads more
 //               or none.  Per block of a scale the sums are exact up to the tensor core's
@@ -18,12 +18,10 @@
 //               the registers; ldmatrix turns the values' bytes round, four tokens of a
 //               dim to a register.  V's scale belongs to the summed index, so it goes into the
 //               weight: p_t d_V,t.  The running maximum is taken over s_t + log2 d_V,t, less
-//               14: the largest weight is about 2^14 whatever the scales are, and f16
-//               holds 11 bits of every weight down to 2^-28 of it.  Where FINE
-//               the weight is split into two f16 parts like q; otherwise its one
-//               rounding (2^-11, of either sign from token to token) is under the output's own
-//               (2^-8).  Each step's part is summed by itself and added in f32, which the
-//               tensor core's own additions would not do to half a step.
+//               14: the largest weight is about 2^14 whatever the scales are.  The weight is split into
+//               two f16 parts like q (22 bits), whatever the outputs' type is: one part alone (11 bits, serving 97 us for 100)
+//               moved 8 to 10 % of bf16 outputs by a step, two 0.1 %.  Each step's part is summed by itself and added in f32, which
+//               the tensor core's own additions would not do to half a step.
 //
 // A warp takes TOK tokens a step and copies its own steps to shared memory by cp.async, one step ahead: no barrier,
 // nothing shared between warps.
@@ -237,6 +235,15 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
+// What a pair rounded to f16 leaves of its two values, as an f16 pair.  (With the pair widened first: serving 100.9 us, 100.3 so.)
+__device__ __forceinline__ uint32_t rest_f16(uint32_t rounded, float lo, float hi)
+{
+    float x, y;
+    asm("{ .reg .b16 a, b, m; mov.b32 {a, b}, %2; mov.b16 m, 0xBC00; fma.rn.f32.f16 %0, a, m, %3; fma.rn.f32.f16 %1, b, m, %4; }"
+        : "=f"(x), "=f"(y) : "r"(rounded), "f"(lo), "f"(hi));
+    return pack_f16(x, y);
+}
+
 // One sequence's tokens in steps of TOK: the first and the end of what it sees.
 struct Seen {
     int first, n;
@@ -377,7 +384,7 @@ struct Attn {
         __device__ __forceinline__ void load(const AttnArgs &a, const Place &p, int first, int lane)
         {
             const int h = a.chunks == 1 ? p.item : p.item / a.chunks, h0 = (p.item - h * a.chunks) * S::HEADS;
-            const int size = !FINE || a.q_bf16 ? 2 : 4;
+            constexpr int size = FINE ? 4 : 2;
             const uint8_t *const row = static_cast<const uint8_t *>(a.q) + (p.b * a.q_row + (h * a.group + h0) * a.q_head) * size;
 #pragma unroll
             for (int y = 0; y < S::QW; ++y)
@@ -387,7 +394,7 @@ struct Attn {
                     v[y][i] = make_uint4(0, 0, 0, 0);
                     if (h0 + x < a.group && piece < D / 4) {
                         const uint8_t *const at = row + (x * a.q_head + piece * 4) * size;
-                        if (FINE && !a.q_bf16) {
+                        if constexpr (FINE) {
                             v[y][i] = *reinterpret_cast<const uint4 *>(at);
                         } else {
                             const uint2 w = *reinterpret_cast<const uint2 *>(at);
@@ -396,11 +403,11 @@ struct Attn {
                     }
                 }
         }
-        __device__ __forceinline__ float4 get(const AttnArgs &a, int y, int i) const
+        __device__ __forceinline__ float4 get(int y, int i) const
         {
             const uint4 w = v[y][i];
-            if (FINE && !a.q_bf16) return make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w));
-            return Vec4<__nv_bfloat16>::widen(make_uint2(w.x, w.y));
+            if constexpr (FINE) return make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w));
+            else return Vec4<__nv_bfloat16>::widen(make_uint2(w.x, w.y));
         }
     };
 
@@ -426,7 +433,7 @@ struct Attn {
             const int x = y * AT_WARPS + first;
             float4 v[S::QP];
 #pragma unroll
-            for (int i = 0; i < S::QP; ++i) v[i] = query.get(a, y, i);
+            for (int i = 0; i < S::QP; ++i) v[i] = query.get(y, i);
             float top = 0.0f;
             bool odd = false;  // infinities or NaN in the row: no factor
 #pragma unroll
@@ -596,10 +603,7 @@ struct Attn {
                     const float w0 = s[i][j][0] * dv[j][0][b], w1 = s[i][j][1] * dv[j][1][b];
                     const uint32_t h = pack_f16(w0, w1);
                     hi[i][j / 2][j % 2] = h;
-                    if constexpr (FINE) {
-                        const float2 back = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-                        lo[i][j / 2][j % 2] = pack_f16(w0 - back.x, w1 - back.y);
-                    }
+                    lo[i][j / 2][j % 2] = rest_f16(h, w0, w1);
                 }
             }
 #pragma unroll
@@ -624,14 +628,9 @@ struct Attn {
                         for (int x = 0; x < 2; ++x) {
                             const uint32_t(&q)[4] = va[x];
                             Quad &d = acc[i][x];
-                            if constexpr (FINE) {
-                                d = ch == 0 ? mma_f16(q[0], q[1], q[2], q[3], lo[i][ch][0], lo[i][ch][1])
-                                            : mma_f16(q[0], q[1], q[2], q[3], lo[i][ch][0], lo[i][ch][1], d);
-                                d = mma_f16(q[0], q[1], q[2], q[3], hi[i][ch][0], hi[i][ch][1], d);
-                            } else {
-                                d = ch > 0 ? mma_f16(q[0], q[1], q[2], q[3], hi[i][ch][0], hi[i][ch][1], d)
-                                           : mma_f16(q[0], q[1], q[2], q[3], hi[i][ch][0], hi[i][ch][1]);
-                            }
+                            d = ch == 0 ? mma_f16(q[0], q[1], q[2], q[3], lo[i][ch][0], lo[i][ch][1])
+                                        : mma_f16(q[0], q[1], q[2], q[3], lo[i][ch][0], lo[i][ch][1], d);
+                            d = mma_f16(q[0], q[1], q[2], q[3], hi[i][ch][0], hi[i][ch][1], d);
                         }
                 }
 #pragma unroll
@@ -655,7 +654,9 @@ __device__ __forceinline__ void store4(T *p, float4 v)
     *reinterpret_cast<typename Vec4<T>::raw *>(p) = Vec4<T>::narrow(v);
 }
 
-// Four outputs of a head, o / l; by the reciprocal where they are rounded to bf16.
+// Four outputs of a head, o / l; by the correctly rounded reciprocal where they are rounded to bf16: within 1.5 * 2^-24 of
+// the quotient, against the half step of 2^-8 that follows, and 142 sequences of 11 tokens with 168 query heads of 256 take
+// 33 us, 58 with four divisions.
 __device__ __forceinline__ void attn_store(const AttnArgs &a, int64_t row, int dim, int col, float4 v, float l)
 {
     float4 r;
@@ -1293,7 +1294,7 @@ cudaError_t launch_attn_shape(const AttnArgs &a, int64_t most, cudaStream_t st)
     template <>                                                                                                    \
     cudaError_t launch_attn_dim<E4M3, D>(const AttnArgs &a, int64_t most, cudaStream_t st)                         \
     {                                                                                                              \
-        const bool fine = !a.q_bf16 || !a.out_bf16;                                                                \
+        const bool fine = !a.q_bf16;                                                                               \
         if (a.group <= 8)                                                                                          \
             return fine ? launch_attn_shape<E4M3, D, 1, true>(a, most, st)                                         \
                         : launch_attn_shape<E4M3, D, 1, false>(a, most, st);                                       \

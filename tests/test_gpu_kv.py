@@ -447,6 +447,33 @@ def test_attention_scores(torch, qg, fmt, gain, scale, wide):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dim,group", [(128, 6), (64, 1), (96, 12)])
+@pytest.mark.parametrize("lengths,columns", [([2, 6], 1), ([100, 36, 1500], 600), ([20] * 400, 2)])
+def test_attention_bf16_weights(torch, qg, fmt, dim, group, lengths, columns):
+    """Pairs of tokens of opposite values and nearly the same weight, in each form (a CTA or cluster, the line, warps): the
+    outputs are what is left of the weights' last bits, so that bf16 outputs hold them to 22 bits like f32 ones.  The
+    limit is that of f32 outputs and half a step of bf16; one rounding of each weight to 11 bits leaves up to 2^-12 of each
+    term, some 2^-4 of these outputs."""
+    rng = np.random.default_rng(dim + len(lengths))
+    page, heads = 16, 2
+    pages = sum(-(-n // page) for n in lengths) + 1
+    c = random_cache(rng, fmt, pages, heads, page, dim)
+    c["vd"][...] = c["vd"].flat[0]
+    c["v"][:, :, 1::2] = -c["v"][:, :, ::2] if fmt == "q8_0" else c["v"][:, :, ::2] ^ 0x80
+    t = tables(rng, lengths, page, pages, extra=columns)
+    q = torch.from_numpy((2e-3 * rng.standard_normal((len(lengths), heads * group, dim))).astype(np.float32)).bfloat16()
+    want, _, parts = K.attention(q.float().numpy(), c, t, lengths, float(np.float32(dim ** -0.5)))
+    got = qg.qg_attn_decode(q.cuda(), upload(torch, qg, c), dev(torch, t), dev(torch, np.array(lengths, np.int32)))
+    assert got.dtype == torch.bfloat16
+    got = got.double().cpu().numpy()
+    for b, part in enumerate(parts):
+        off, _ = bounds(part, part[0].shape[-1], False)
+        lim = off + (np.abs(want[b]) + off) * 2.0 ** -8
+        err = np.abs(got[b] - want[b])
+        assert np.all(err <= lim), (b, np.argwhere(err > lim)[:4], float((err / lim).max()))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 def test_attention_scales_far_apart(torch, qg, fmt):
     """Tokens whose values' scales differ by many powers of two: none is lost to the weights' 16 bits."""
     run_attention(torch, qg, fmt, 128, 2, 4, 32, [300, 65], spread=4.0, gain=0.01)
