@@ -17,11 +17,17 @@
 //   O^T = V^T P^T   16 dims x 8 heads.  S's accumulators are P^T's operand as they lie in
 //               the registers; ldmatrix turns the values' bytes round, four tokens of a
 //               dim to a register.  V's scale belongs to the summed index, so it goes into the
-//               weight: p_t d_V,t.  The running maximum is taken over s_t + log2 d_V,t, less
-//               14: the largest weight is about 2^14 whatever the scales are.  The weight is split into
+//               weight: p_t d_V,t.  The running maximum is taken over s_t + log2 d_V,t, with the
+//               largest of the token's scales, less 14: the largest weight is about 2^14 whatever the
+//               scales are.  The weight is split into
 //               two f16 parts like q (22 bits), whatever the outputs' type is: one part alone (11 bits, serving 97 us for 100)
 //               moved 8 to 10 % of bf16 outputs by a step, two 0.1 %.  Each step's part is summed by itself and added in f32, which
 //               the tensor core's own additions would not do to half a step.
+//               The other blocks' weights are then as large as their scales are near to the token's largest.  Where
+//               a token's scales lie more than 2^8 apart (AT_NEAR), from there to the item's end each step brings the weights of
+//               each block to 2^14 by a power of two of their own and takes it off the sums.  Looking for such tokens, one to a
+//               lane, and the branch cost 1 to 5 % (serving 100 us, 105 with them; e4m3 93.6, 94); without
+//               them a block 2^-36 of its neighbour came out wrong by a half.
 //
 // A warp takes TOK tokens a step and copies its own steps to shared memory by cp.async, one step ahead: no barrier,
 // nothing shared between warps.
@@ -58,6 +64,10 @@ constexpr int AT_THREADS = 32 * AT_WARPS;
 constexpr int AT_CTAS_MAX = 4;  // per SM
 constexpr int AT_FEW = 4;      // rows of 32 sequences that every warp scans for itself
 constexpr int AT_CLUSTER = 8;  // CTAs to an item in the direct form, at most
+// Between these e4m3 scales the running maximum follows a token's largest: the sum of weights stays in range for 2^30 tokens
+// of up to 2^(14 + 82), and the sums of values for the largest scale there is, 2^119.2.
+constexpr float AT_E4M3_LEAST = 0x1p-82f, AT_E4M3_MOST = 0x1p64f;
+constexpr float AT_NEAR = 256.0f;  // a token's scales this near to one another share a reference for the weights' 16 bits
 constexpr int AT_SHORT = 512;  // tokens of an item in the warps' form, at most
 
 struct AttnArgs {
@@ -224,6 +234,40 @@ struct PairScales {
     }
 };
 
+// Whether a token's values' scales, as they lie in memory, are not all within AT_NEAR of one another and in the range that
+// the running maximum follows; all zero is not either.
+template <bool E4M3, int NB>
+__device__ __forceinline__ bool scales_far(const uint8_t *p)
+{
+    if constexpr (E4M3) {
+        const float *const d = reinterpret_cast<const float *>(p);
+        const float a = fabsf(d[0]), b = fabsf(d[NB - 1]);
+        return !(fminf(a, b) * AT_NEAR > fmaxf(fmaxf(a, b), AT_E4M3_LEAST) && fmaxf(a, b) <= AT_E4M3_MOST);
+    } else {
+        uint32_t w[(NB + 1) / 2];
+        if constexpr (NB % 2) {  // 6 bytes, at even addresses
+            const uint16_t *const h = reinterpret_cast<const uint16_t *>(p);
+            w[0] = h[0] | static_cast<uint32_t>(h[1]) << 16, w[1] = h[2] | static_cast<uint32_t>(h[2]) << 16;
+        } else if constexpr (NB == 4) {
+            const uint2 v = *reinterpret_cast<const uint2 *>(p);
+            w[0] = v.x, w[1] = v.y;
+        } else if constexpr (NB == 8) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(p);
+            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < NB / 2; ++i) w[i] = reinterpret_cast<const uint32_t *>(p)[i];
+        }
+        __half2 top = __habs2(*reinterpret_cast<const __half2 *>(&w[0])), low = top;  // NaN is passed over
+#pragma unroll
+        for (int i = 1; i < (NB + 1) / 2; ++i) {
+            const __half2 h = __habs2(*reinterpret_cast<const __half2 *>(&w[i]));
+            top = __hmax2(top, h), low = __hmin2(low, h);
+        }
+        return !(fminf(__low2float(low), __high2float(low)) * AT_NEAR > fmaxf(__low2float(top), __high2float(top)));
+    }
+}
+
 __device__ __forceinline__ void cp_async_16_if(uint32_t dst, const void *src, bool there)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
@@ -353,9 +397,11 @@ struct Attn {
     Quad o[NT][2 * DG];  // O^T: tiles of 16 dims, of which this lane has dims g and g + 8 of heads 2 t and 2 t + 1
     float m[NT], l[NT];  // of head lane / 4 of each tile: the running reference, this lane's part of the sum
     float c[NT];         // the factor of its scores, in log2 units
+    bool far;            // a token of this item had scales far from one another
 
     __device__ __forceinline__ void begin(const float *qc, int lane)
     {
+        far = false;
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
             m[i] = -FLT_MAX;
@@ -463,6 +509,87 @@ struct Attn {
         }
     }
 
+    // O^T = f O^T + V^T P^T, where s holds the tokens' p and vx where their values lie.  FAR: the weights of each block of values
+    // are brought to 2^14 by a power of two of their own, so that f16 holds them wherever the block's scales lie.
+    template <bool FAR>
+    __device__ __forceinline__ void add(const float (&s)[NT][2 * CH][2], const float (&dv)[2 * CH][2][NB], const float (&f0)[NT],
+                                        const float (&f1)[NT], const uint32_t (&vx)[S::NX], int lane)
+    {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            uint32_t hi[NT][CH][2], lo[NT][CH][2];
+            float down0[NT], down1[NT];
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                float lift = 1.0f;
+                if constexpr (FAR) {
+                    float top = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 2 * CH; ++j)
+                        top = fmaxf(top, fmaxf(fabsf(s[i][j][0] * dv[j][0][b]), fabsf(s[i][j][1] * dv[j][1][b])));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    const int k = min(max(14 + 127 - static_cast<int>(__float_as_uint(top) >> 23), -110), 110);
+                    lift = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
+                    const float down = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+                    down0[i] = __shfl_sync(0xffffffffu, down, 8 * (lane & 3));
+                    down1[i] = __shfl_sync(0xffffffffu, down, 8 * (lane & 3) + 4);
+                }
+#pragma unroll
+                for (int j = 0; j < 2 * CH; ++j) {
+                    float w0 = s[i][j][0] * dv[j][0][b], w1 = s[i][j][1] * dv[j][1][b];
+                    if constexpr (FAR) w0 *= lift, w1 *= lift;
+                    const uint32_t h = pack_f16(w0, w1);
+                    hi[i][j / 2][j % 2] = h;
+                    if constexpr (FAR)  // an infinite scale's weight has no second part
+                        lo[i][j / 2][j % 2] = rest_f16(h, w0, w1) & (fabsf(w0) <= FLT_MAX ? 0xffffu : 0u) |
+                                              rest_f16(h, w0, w1) & (fabsf(w1) <= FLT_MAX ? 0xffff0000u : 0u);
+                    else
+                        lo[i][j / 2][j % 2] = rest_f16(h, w0, w1);
+                }
+            }
+#pragma unroll
+            for (int dg = b * (E4M3 ? 4 : 1); dg < (b + 1) * (E4M3 ? 4 : 1) && dg < DG; ++dg) {
+                Quad acc[NT][2];
+#pragma unroll
+                for (int ch = 0; ch < CH; ++ch) {
+                    // four tokens' codes of dims g, g + 8, g + 16 and g + 24 of the block
+                    uint32_t r[4];
+                    asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];"
+                        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                        : "r"(vx[dg % S::NX] + S::piece_at(dg) + ch * S::TILE) : "memory");
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) r[i] = code_bits<E4M3>(r[i]);
+                    const uint32_t va[2][4] = {{codes_f16<E4M3, false>(r[0]), codes_f16<E4M3, false>(r[1]),
+                                                codes_f16<E4M3, true>(r[0]), codes_f16<E4M3, true>(r[1])},
+                                               {codes_f16<E4M3, false>(r[2]), codes_f16<E4M3, false>(r[3]),
+                                                codes_f16<E4M3, true>(r[2]), codes_f16<E4M3, true>(r[3])}};
+#pragma unroll
+                    for (int i = 0; i < NT; ++i)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const uint32_t(&q)[4] = va[x];
+                            Quad &d = acc[i][x];
+                            d = ch == 0 ? mma_f16(q[0], q[1], q[2], q[3], lo[i][ch][0], lo[i][ch][1])
+                                        : mma_f16(q[0], q[1], q[2], q[3], lo[i][ch][0], lo[i][ch][1], d);
+                            d = mma_f16(q[0], q[1], q[2], q[3], hi[i][ch][0], hi[i][ch][1], d);
+                        }
+                }
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        float(&d)[4] = o[i][2 * dg + x].v;
+                        if constexpr (FAR) acc[i][x].v[0] *= down0[i], acc[i][x].v[1] *= down1[i], acc[i][x].v[2] *= down0[i], acc[i][x].v[3] *= down1[i];
+                        d[0] = fmaf(d[0], f0[i], acc[i][x].v[0]);
+                        d[1] = fmaf(d[1], f1[i], acc[i][x].v[1]);
+                        d[2] = fmaf(d[2], f0[i], acc[i][x].v[2]);
+                        d[3] = fmaf(d[3], f1[i], acc[i][x].v[3]);
+                    }
+            }
+        }
+    }
+
     // One step: `st` its stage, `qf` q's fragments.  EDGE: some of its tokens are not seen, or on a page outside the cache.
     template <bool EDGE>
     __device__ __forceinline__ void step(const uint8_t *st, const uint4 *qf, int at, Seen seen, uint32_t bad, int lane)
@@ -474,6 +601,13 @@ struct Attn {
         for (int i = 0; i < S::NX; ++i) {
             kx[i] = st + S::key_piece(g, i) + t * 8;
             vx[i] = smem_addr(st) + S::CODES + S::value_row_at(lane & 15, 2 * i + (lane >> 4));
+        }
+        // ---- a token to each lane: are its values' scales near one another?
+        {
+            const int token = lane % TOK;
+            bool is = scales_far<E4M3, NB>(st + token / KV_TILE * S::TILE + 2 * S::CODES + S::SCALES + token % KV_TILE * NB * S::SB);
+            if constexpr (EDGE) is = is && at + token >= seen.first && at + token < seen.n;
+            far = __any_sync(0xffffffffu, is) || far;
         }
         // ---- scores
         float s[NT][2 * CH][2];
@@ -545,16 +679,15 @@ struct Attn {
                     }
                 }
         }
-        // log2 of a token's largest scale, held where the sum of weights stays in range (2^30 tokens of up to
-        // 2^(14 + 82): 2^126) and infinities and NaN stay in their own blocks
+        // log2 of a token's largest scale, held where sums stay in range
 #pragma unroll
         for (int j = 0; j < 2 * CH; ++j)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                float top = E4M3 ? 0x1p-82f : 0x1p-25f;
+                float top = E4M3 ? AT_E4M3_LEAST : 0x1p-25f;
 #pragma unroll
                 for (int b = 0; b < NB; ++b) top = fmaxf(top, fabsf(dv[j][x][b]));
-                asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(e[j][x]) : "f"(fminf(top, E4M3 ? 0x1p119f : 65504.0f)));
+                asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(e[j][x]) : "f"(fminf(top, E4M3 ? AT_E4M3_MOST : 65504.0f)));
             }
         // ---- weights
         float f[NT];
@@ -593,58 +726,10 @@ struct Attn {
             f1[i] = __shfl_sync(0xffffffffu, f[i], 8 * t + 4);
         }
         // ---- O^T = f O^T + V^T P^T, this step's part summed by itself
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            uint32_t hi[NT][CH][2], lo[NT][CH][2];
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-#pragma unroll
-                for (int j = 0; j < 2 * CH; ++j) {
-                    const float w0 = s[i][j][0] * dv[j][0][b], w1 = s[i][j][1] * dv[j][1][b];
-                    const uint32_t h = pack_f16(w0, w1);
-                    hi[i][j / 2][j % 2] = h;
-                    lo[i][j / 2][j % 2] = rest_f16(h, w0, w1);
-                }
-            }
-#pragma unroll
-            for (int dg = b * (E4M3 ? 4 : 1); dg < (b + 1) * (E4M3 ? 4 : 1) && dg < DG; ++dg) {
-                Quad acc[NT][2];
-#pragma unroll
-                for (int ch = 0; ch < CH; ++ch) {
-                    // four tokens' codes of dims g, g + 8, g + 16 and g + 24 of the block
-                    uint32_t r[4];
-                    asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];"
-                        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                        : "r"(vx[dg % S::NX] + S::piece_at(dg) + ch * S::TILE) : "memory");
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) r[i] = code_bits<E4M3>(r[i]);
-                    const uint32_t va[2][4] = {{codes_f16<E4M3, false>(r[0]), codes_f16<E4M3, false>(r[1]),
-                                                codes_f16<E4M3, true>(r[0]), codes_f16<E4M3, true>(r[1])},
-                                               {codes_f16<E4M3, false>(r[2]), codes_f16<E4M3, false>(r[3]),
-                                                codes_f16<E4M3, true>(r[2]), codes_f16<E4M3, true>(r[3])}};
-#pragma unroll
-                    for (int i = 0; i < NT; ++i)
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            const uint32_t(&q)[4] = va[x];
-                            Quad &d = acc[i][x];
-                            d = ch == 0 ? mma_f16(q[0], q[1], q[2], q[3], lo[i][ch][0], lo[i][ch][1])
-                                        : mma_f16(q[0], q[1], q[2], q[3], lo[i][ch][0], lo[i][ch][1], d);
-                            d = mma_f16(q[0], q[1], q[2], q[3], hi[i][ch][0], hi[i][ch][1], d);
-                        }
-                }
-#pragma unroll
-                for (int i = 0; i < NT; ++i)
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        float(&d)[4] = o[i][2 * dg + x].v;
-                        d[0] = fmaf(d[0], f0[i], acc[i][x].v[0]);
-                        d[1] = fmaf(d[1], f1[i], acc[i][x].v[1]);
-                        d[2] = fmaf(d[2], f0[i], acc[i][x].v[2]);
-                        d[3] = fmaf(d[3], f1[i], acc[i][x].v[3]);
-                    }
-            }
-        }
+        if (far)
+            add<true>(s, dv, f0, f1, vx, lane);
+        else
+            add<false>(s, dv, f0, f1, vx, lane);
     }
 };
 

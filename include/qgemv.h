@@ -795,8 +795,10 @@ QG_API qg_status qg_kv_read(const qg_kv_cache *cache, const int64_t *slots, int6
  * max(0, n - window) <= t < n, n = lengths[b] (window 0: all of them):
  *   s_t = scale * sum_i q[i] K_t[i],  o = sum_t e^(s_t - m) V_t / sum_t e^(s_t - m),
  *   m = max_t s_t,  lse = m + ln sum_t e^(s_t - m)
- * in f32 (a weight is rounded to 22 significant bits), o rounded once to its type.  A
- * sequence that sees nothing has o = 0 and lse = -infinity.
+ * in f32, o rounded once to its type.  A weight is held to 22 significant bits, or to
+ * 2^-31 of the largest weight times scale of its own block of the head's values where
+ * that is coarser; a value of q to 22 bits, or to 2^-39 of the largest of its head.
+ * A sequence that sees nothing has o = 0 and lse = -infinity.
  * Codes and scales outside the tokens seen are never used, whatever they hold.
  *   q: device f32 or bf16 (q_dtype) (read): value i of head h of sequence b is element
  *       b * q_row_stride + h * q_head_stride + i; rows start on 16 bytes.

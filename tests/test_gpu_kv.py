@@ -480,6 +480,83 @@ def test_attention_scales_far_apart(torch, qg, fmt):
     run_attention(torch, qg, fmt, 128, 2, 4, 32, [300, 65], spread=4.0, gain=0.01, kinds=("bf16", "bf16"))
 
 
+def assert_by_blocks(got, c, t, lengths, want, what=""):
+    """As assert_attention, each block of values by itself: a weight keeps 22 bits, or 2^-31 of the largest weight times scale
+    of its own block of the head's values, whatever the other blocks hold (each of n tokens' codes is at most 127 or 448)."""
+    o, _, parts = want
+    bf16 = "bfloat16" in str(got.dtype)
+    got = got.double().cpu().numpy()
+    page, block = c["v"].shape[2], K.BLOCK[c["format"]]
+    for b, part in enumerate(parts):
+        if part is None:
+            assert not got[b].any(), (what, b)
+            continue
+        p = part[0]
+        n, dim = p.shape[-1], got.shape[-1]
+        at = np.arange(lengths[b] - n, lengths[b])
+        d = np.abs(c["vd"][t[b, at // page], :, at % page].astype(np.float64))  # [tokens, heads, blocks]
+        each = 2.0 ** -20 + (n / 64 + 64) * 2.0 ** -24
+        with np.errstate(all="ignore"):
+            off, _ = K.moved((*part[:3], np.where(np.isfinite(part[3]), part[3], 0.0)), each, 2.0 ** -18, 2.0 ** -22, 0.0)
+            top = np.einsum("hgt,thb->hgtb", p, d).max(axis=2) * (n * 2.0 ** -31 * (127 if block == 32 else 448))
+            off = off + np.repeat(top, block, axis=-1)[..., :dim].reshape(-1, dim)
+            lim = off + (np.abs(o[b]) + off) * (2.0 ** -8 if bf16 else 2.0 ** -23) + 2.0 ** -133
+            odd = ~np.isfinite(o[b])
+            assert np.array_equal(got[b][odd], o[b][odd], equal_nan=True), (what, b)
+            err = np.where(odd, 0.0, np.abs(got[b] - o[b]))
+            lim = np.where(odd, 0.0, lim)
+        assert np.all(err <= lim), (what, b, np.argwhere(~(err <= lim))[:4], float(np.nanmax(err / np.maximum(lim, 1e-300))))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dim,group,kind", [(64, 2, "bf16"), (96, 3, "f32"), (128, 12, "f32"), (192, 4, "bf16"), (256, 9, "f32")])
+@pytest.mark.parametrize("scales", ["steps", "any", "late", "early", "silent", "least", "most", "infinite"])
+@pytest.mark.parametrize("lengths,columns", [([70, 3], 1), ([300, 1, 650], 400), ([37] * 330, 1)])
+def test_attention_blocks_far_apart(torch, qg, fmt, dim, group, kind, scales, lengths, columns):
+    """Scales of one token's blocks of values many powers of two apart, in each form (a CTA or cluster, the line, warps):
+    every block comes out as if it were alone."""
+    rng = np.random.default_rng(dim + 17 * len(scales) + lengths[0])
+    page, heads = 16, 2
+    pages = sum(-(-n // page) for n in lengths) + 1
+    c = random_cache(rng, fmt, pages, heads, page, dim)
+    t = tables(rng, lengths, page, pages, extra=columns)
+    vd, nb = c["vd"], c["vd"].shape[-1]
+    low, high = (-24, 15) if fmt == "q8_0" else (-45, 45)
+    x = np.exp2(0.5 * rng.standard_normal(vd.shape))
+    anywhere = np.exp2(rng.uniform(low, high, vd.shape))
+    step = np.exp2(np.linspace(high - 2, low + 2, nb)) if nb > 1 else np.exp2([high])
+    if scales == "steps":
+        vd[...] = x * step
+    elif scales == "any":
+        vd[...] = anywhere
+        vd[rng.random(vd.shape) < 0.1] = 0
+    elif scales in ("late", "early"):  # in the last or the first page of each sequence
+        vd[...] = x / 64
+        for b, n in enumerate(lengths):
+            i = (n - 1) // page if scales == "late" else 0
+            vd[t[b, i]] = (x * step)[t[b, i]]
+    elif scales == "silent":  # a token without values has most of the weight
+        for b, n in enumerate(lengths):
+            at = n // 2
+            vd[t[b, at // page], :, at % page] = 0
+            c["k"][t[b, at // page], :, at % page] = 0x7F if fmt == "q8_0" else 0x7E
+            c["kd"][t[b, at // page], :, at % page] = (2.0 if fmt == "q8_0" else 0.5) * 24 / np.sqrt(dim) / 127
+    elif scales in ("least", "most"):
+        vd[...] = x * (2.0 ** -22 if fmt == "q8_0" else 2.0 ** -106) if scales == "least" else np.minimum(
+            x * (2.0 ** 15 if fmt == "q8_0" else 2.0 ** 116), 65504 if fmt == "q8_0" else 2.0 ** 118)
+    else:
+        at = lengths[0] // 2
+        vd[t[0, at // page], 1, at % page, nb // 2] = np.inf
+    q = rng.standard_normal((len(lengths), heads * group, dim)).astype(np.float32)
+    if scales == "silent":
+        q = np.abs(q)
+    q = torch.from_numpy(q).to(types(torch)[kind])
+    with np.errstate(all="ignore"):
+        want = K.attention(q.float().numpy(), c, t, lengths, float(np.float32(dim ** -0.5)))
+    got = qg.qg_attn_decode(q.cuda(), upload(torch, qg, c), dev(torch, t), dev(torch, np.array(lengths, np.int32)))
+    assert_by_blocks(got, c, t, lengths, want, scales)
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
 @pytest.mark.parametrize("lengths", [[2], [100, 3, 1500], [20] * 400])
