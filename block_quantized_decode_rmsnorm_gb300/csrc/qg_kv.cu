@@ -4,6 +4,8 @@
 // caller gives.  A thread keeps its place in the row - key or value, head, block, piece
 // of 16 values - and takes several rows, so that the place is computed once and a
 // row costs one slot, one division by the page size and one product.
+#include <cfloat>
+
 #include "qg_kv.cuh"
 
 namespace qg {
@@ -190,21 +192,13 @@ __global__ void __launch_bounds__(KT) kv_write_kernel(KvRows a, KvSource<T> s)
         } else {
 #pragma unroll
             for (int o = L / 2; o >= 1; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-            float d = div127(m);
-            if (d >= 0x1p-100f && d < __int_as_float(0x7f800000)) {
+            // a block with a NaN or an infinity has that for its scale, so that it reads as NaN: none passes for a number
+            const bool odd = !(m <= FLT_MAX);
+            const float d = odd ? m : div127(m);
+            if (d >= 0x1p-100f && !odd)
                 w = q8_codes16(v, d);
-            } else {
-                // fmaxf's maximum: NaN passed over, as quantize_act_q8_0 does.  A block's lanes are here together, other
-                // blocks' may not be
-                float n = fmaxf(fmaxf(fabsf(v[0].x), fabsf(v[0].y)), fmaxf(fabsf(v[0].z), fabsf(v[0].w)));
-#pragma unroll
-                for (int q = 1; q < 4; ++q) n = fmaxf(n, fmaxf(fmaxf(fabsf(v[q].x), fabsf(v[q].y)), fmaxf(fabsf(v[q].z), fabsf(v[q].w))));
-                const uint32_t block_lanes = ((1u << L) - 1) << (threadIdx.x & 31 & ~(L - 1));
-#pragma unroll
-                for (int o = L / 2; o >= 1; o >>= 1) n = fmaxf(n, __shfl_xor_sync(block_lanes, n, o));
-                d = div127(n);
-                w = q8_codes16_any(v[0], v[1], v[2], v[3], d);
-            }
+            else
+                w = odd ? make_uint4(0, 0, 0, 0) : q8_codes16_any(v[0], v[1], v[2], v[3], d);
             if (there && j % L == 0) static_cast<uint16_t *>(scales)[at * nb + scale_at] = f2h_rn(d);
         }
         if (there) *reinterpret_cast<uint4 *>(codes + at * a.c.dim) = w;

@@ -739,9 +739,10 @@ QG_API qg_status qg_debug_stalled_e4m3(const uint8_t *w, const float *wd, int64_
  *   k_scales, v_scales: device [n_pages][heads][page_size][B], each row of head_dim
  *       values in B blocks with a scale of its own:
  *       QG_KV_Q8_0  int8 codes, binary16 scales, B = head_dim / 32, a row quantized as
- *                   by quantize_act_q8_0
+ *                   by quantize_act_q8_0; a block with a NaN has scale NaN, one with an
+ *                   infinity scale infinity, both codes 0: they stand for NaN throughout
  *       QG_KV_E4M3  e4m3 codes, f32 scales, B = ceil(head_dim / 128), a row quantized
- *                   as by quantize_act_e4m3
+ *                   as by quantize_act_e4m3, which keeps NaN too
  *   Slot s is token s % page_size of page s / page_size; the cached value is
  *   code * scale.  The four planes are 16-byte aligned and do not overlap.
  *   head_dim: 64, 96, 128, 192 or 256 (else QG_ERR_UNSUPPORTED); page_size: a multiple

@@ -172,6 +172,38 @@ def test_write_special_values(torch, qg, fmt, kind):
     check_write(torch, qg, fmt, kind, x, np.arange(8), 1, 16)
 
 
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("dim", DIMS)
+def test_write_q8_0_keeps_nan(torch, qg, dim, kind):
+    """A NaN or an infinity in a block of a Q8_0 row: scale NaN or infinity, codes 0, the block reads as NaN; the other blocks
+    of the row, the other rows and heads are as they are without it."""
+    rng = np.random.default_rng(dim)
+    x = rng.standard_normal((2, 9, 2, dim)).astype(np.float32)
+    x = torch.from_numpy(x).to(types(torch)[kind]).float().numpy()
+    odd = np.zeros((2, 9, 2, dim // 32), bool)
+    y, scale = x.copy(), np.zeros(odd.shape)
+    for i, (row, block, at, value) in enumerate([(1, 0, 5, np.nan), (2, 1, 31, np.inf), (3, 0, 0, -np.inf), (4, 1, slice(None), np.nan),
+                                                 (5, 0, slice(None), np.inf), (6, 1, 16, np.nan), (7, 1, 3, -np.nan)]):
+        which, head = i % 2, i // 2 % 2
+        y[which, row, head, 32 * block: 32 * block + 32][at] = value
+        odd[which, row, head, block], scale[which, row, head, block] = True, abs(value)
+    y[0, 8, 1, 33], y[0, 8, 1, 49] = np.inf, np.nan  # in two lanes of one block
+    odd[0, 8, 1, 1], scale[0, 8, 1, 1] = True, np.nan
+    cache = qg.KVCache.allocate(1, 16, 2, dim)
+    t = torch.from_numpy(y).to(types(torch)[kind]).cuda()
+    qg.qg_kv_write(cache, t[0], t[1], torch.arange(9, device="cuda"))
+    back = qg.qg_kv_read(cache, torch.arange(9, device="cuda"))
+    held = download(cache, "q8_0")
+    for i, n in enumerate("kv"):
+        q, d = K.quantize(x[i], "q8_0")
+        at = odd[i]
+        d = np.where(at, scale[i], d.astype(np.float64))
+        q = np.where(np.repeat(at, 32, axis=-1), 0, q)
+        assert np.array_equal(held[n][0, :, :9].swapaxes(0, 1), q)
+        assert np.array_equal(held[n + "d"][0, :, :9].swapaxes(0, 1).astype(np.float64), d, equal_nan=True)
+        assert np.array_equal(torch.isnan(back[i]).cpu().numpy(), np.repeat(at, 32, axis=-1))
+
+
 def test_write_nothing(torch, qg):
     cache = qg.KVCache.allocate(2, 16, 2, 64)
     empty = torch.empty((0, 2, 64), device="cuda")
