@@ -505,7 +505,10 @@ struct Attn {
                 r.w = pack_f16(w.z - b23.x, w.w - b23.y);
                 if (p < D / 4) put_piece(qf, x, p, r);
             }
-            if (lane == 0) qc[x] = a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(ex - 14 + 127) << 23);
+            if (lane == 0) {  // the power of two first; finite where the scale is, so that scores of zero stay zero
+                const float k = a.scale * __uint_as_float(static_cast<uint32_t>(ex - 14 + 127) << 23) * kLog2e;
+                qc[x] = fabsf(a.scale) <= FLT_MAX ? fminf(fmaxf(k, -FLT_MAX), FLT_MAX) : k;
+            }
         }
     }
 

@@ -818,6 +818,8 @@ QG_API qg_status qg_kv_read(const qg_kv_cache *cache, const int64_t *slots, int6
  *       fewer one after another; calls that share one must not overlap in time.
  *   batch <= 2^20; max_pages * page_size <= 2^30 (QG_ERR_SHAPE); a batch whose page tables together
  *   hold more than some 2^43 tokens times heads is QG_ERR_UNSUPPORTED.  scale is any f32.
+ *   Bits are lost in heads of q whose largest value is below 2^-100 and with e4m3 scales
+ *   beyond 2^64 of keys.
  *   Page tables no wider than the sequences need make short calls faster: where the widest
  *   has few tokens, a cluster of CTAs takes each head, without a scan over the lengths.
  *   Outputs must not overlap inputs, the workspace or each other (QG_ERR_SHAPE).

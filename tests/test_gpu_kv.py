@@ -479,6 +479,53 @@ def test_attention_scores(torch, qg, fmt, gain, scale, wide):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("scale", [3.4e38, -3.4e38, 2.4e38, 1e38, 1e-44])
+@pytest.mark.parametrize("lengths,columns", [([70, 3], 1), ([300, 1, 650], 400), ([37] * 330, 1)])
+def test_attention_largest_scales(torch, qg, fmt, kind, scale, lengths, columns):
+    """Scales up to f32's ends: scores of zero stay zero, and keys and queries that are as small come out right."""
+    rng = np.random.default_rng(41)
+    pages, scale = sum(-(-n // 16) for n in lengths) + 1, float(np.float32(scale))
+    c = random_cache(rng, fmt, pages, 2, 16, 128)
+    t = tables(rng, lengths, 16, pages, extra=columns)
+    args = dev(torch, t), dev(torch, np.array(lengths, np.int32)), scale
+    zero = torch.zeros((len(lengths), 6, 128), dtype=types(torch)[kind])
+    want = K.attention(zero.float().numpy(), c, t, lengths, scale)
+    assert_attention(qg.qg_attn_decode(zero.cuda(), upload(torch, qg, c), *args), None, want)
+    if fmt == "e4m3" and abs(scale) > 1:  # scores of some units
+        c["kd"] *= np.float32(2.0 ** -63)
+        q = torch.from_numpy((1e-20 * rng.standard_normal(zero.shape)).astype(np.float32)).to(types(torch)[kind])
+        want = K.attention(q.float().numpy(), c, t, lengths, scale)
+        assert 1 < max(np.abs(p[1]).max() for p in want[2]) < 60
+        assert_attention(qg.qg_attn_decode(q.cuda(), upload(torch, qg, c), *args), None, want)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_attention_small_beside_large_query(torch, qg, fmt):
+    """A query's values 2^-16 and 2^-24 of the head's largest, which meets keys of zero: held to 22 bits or 2^-39 of the largest."""
+    rng = np.random.default_rng(43)
+    lengths, dim, heads, group = [400, 33], 128, 2, 3
+    pages = sum(-(-n // 16) for n in lengths) + 1
+    c = random_cache(rng, fmt, pages, heads, 16, dim)
+    c["k"][..., 7] = 0
+    t = tables(rng, lengths, 16, pages)
+    for ratio in (16, 24):
+        q = rng.standard_normal((2, heads * group, dim)).astype(np.float32)
+        q[..., 7] = 2.0 ** ratio
+        want = K.attention(q, c, t, lengths, float(np.float32(dim ** -0.5)))
+        got = qg.qg_attn_decode(dev(torch, q), upload(torch, qg, c), dev(torch, t), dev(torch, np.array(lengths, np.int32)))
+        for b, part in enumerate(want[2]):
+            # each value off by 2^-39 of the largest: scores by that times the keys' sums
+            n = part[0].shape[-1]
+            k = np.abs(K.rows(c, t[b, np.arange(n) // 16].astype(np.int64) * 16 + np.arange(n) % 16, "k")).sum(axis=-1).max()
+            each = 2.0 ** -20 + (n / 64 + 64) * 2.0 ** -24 + dim ** -0.5 * k * 2.0 ** (ratio - 39)
+            off, _ = K.moved(part, each, 2.0 ** -18, 2.0 ** -22, 2.0 ** -36)
+            lim = off + (np.abs(want[0][b]) + off) * 2.0 ** -23
+            err = np.abs(got[b].double().cpu().numpy() - want[0][b])
+            assert np.all(err <= lim), (ratio, b, float((err / lim).max()))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("dim,group", [(128, 6), (64, 1), (96, 12)])
 @pytest.mark.parametrize("lengths,columns", [([2, 6], 1), ([100, 36, 1500], 600), ([20] * 400, 2)])
 def test_attention_bf16_weights(torch, qg, fmt, dim, group, lengths, columns):
