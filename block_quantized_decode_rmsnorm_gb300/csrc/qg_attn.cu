@@ -65,8 +65,12 @@ int64_t attn_most_places(const KvPlanes &c, int64_t batch, int64_t q_heads, int6
 }
 
 // The form of a call on `items` items of at most `tokens` tokens.  -1, the warps' form: where the items are more than find
-// room at a CTA to each, and short (8 heads of 128, 256 sequences of 16 tokens: 12.3 us, 21.7 in the line; 128 of 512: 27.0,
-// 28.8; 128 of 1024: 48.4, 39.0 in the line).  Otherwise the direct form's CTAs to an item, or 0 for the line: direct where each CTA has at most four units of the widest item (four units:
+// room at a CTA to each, and a warp has few steps to an item: AT_SHORT, or twice as many where the items are three times
+// the room.  Measured from just above the room to twelve times it, for all head sizes (4 query heads of 128 to a head, Q8_0,
+// the warps' time and the line's): 1024 items of 16 tokens 6.1 and 14.9 us, of 256 (8 steps) 18.1 and 28.5, of 512 (16) 31.1
+// and 36.3; 305 of 256 13.7 and 13.7, of 512 22.8 and 16.4; 608 of 512 23.8 and 24.9.  Heads of 256: 305 of 256 (16 steps)
+// 26.5 and 18.3, 1024 of 256 33.1 and 39.3, of 512 58.4 and 48.4.
+// Otherwise the direct form's CTAs to an item, or 0 for the line: direct where each CTA has at most four units of the widest item (four units:
 // 1 x 4096 tokens, 8 heads 8.3 us, 10.1 in the line; eight: 8 x 2048 tokens 12.4, 10.9 in the line), and all items are
 // resident at once.  Clusters double while they are not more than half of the SMs together.
 int form_of(int64_t items, int64_t most, int64_t tokens, const Sizes &s)
@@ -75,7 +79,8 @@ int form_of(int64_t items, int64_t most, int64_t tokens, const Sizes &s)
     int n = 1;
     while (n < AT_CLUSTER && n < units && items * n * 2 <= num_sms()) n *= 2;
     const int64_t room = static_cast<int64_t>(num_sms()) * s.ctas;
-    if (items > room && tokens <= AT_SHORT) return -1;
+    const int64_t step = s.unit / AT_WARPS, steps = (tokens + step - 1) / step;
+    if (items > room && steps <= (items < 3 * room ? AT_SHORT : 2 * AT_SHORT)) return -1;
     return items * n <= room && (units + n - 1) / n <= 4 ? n : 0;
 }
 

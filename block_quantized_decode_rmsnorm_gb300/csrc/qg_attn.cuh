@@ -68,7 +68,7 @@ constexpr int AT_CLUSTER = 8;  // CTAs to an item in the direct form, at most
 // of up to 2^(14 + 82), and the sums of values for the largest scale there is, 2^119.2.
 constexpr float AT_E4M3_LEAST = 0x1p-82f, AT_E4M3_MOST = 0x1p64f;
 constexpr float AT_NEAR = 256.0f;  // a token's scales this near to one another share a reference for the weights' 16 bits
-constexpr int AT_SHORT = 512;  // tokens of an item in the warps' form, at most
+constexpr int AT_SHORT = 8;  // steps of an item in the warps' form, at most; twice as many where there are many items
 
 struct AttnArgs {
     KvPlanes c;

@@ -399,6 +399,21 @@ def test_attention_many_short(torch, qg, fmt, dim, group, kinds, longest, window
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dim,batch,tokens", [(128, 170, 256), (128, 170, 257), (128, 460, 512), (128, 460, 513), (128, 450, 512),
+                                              (256, 170, 128), (256, 170, 144), (256, 460, 256), (64, 920, 512)])
+def test_attention_limits_of_the_warps(torch, qg, fmt, dim, batch, tokens):
+    """Both sides of the limits between the warps' form and the line: steps to an item, items to a GPU's room."""
+    rng = np.random.default_rng(batch + tokens)
+    lengths = [int(n) for n in rng.integers(0, 90, batch)]
+    lengths[3], lengths[-1] = tokens, tokens - 1
+    c = random_cache(rng, fmt, sum(-(-n // 16) for n in lengths) + 1, 2, 16, dim)
+    t = tables(rng, lengths, 16, len(c["k"]), extra=0)
+    q = rng.standard_normal((batch, 4, dim)).astype(np.float32)
+    got = qg.qg_attn_decode(dev(torch, q), upload(torch, qg, c), dev(torch, t), dev(torch, np.array(lengths, np.int32)))
+    assert_attention(got, None, K.attention(q, c, t, lengths, float(np.float32(dim ** -0.5))))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 def test_attention_bad_page_many_short(torch, qg, fmt):
     rng = np.random.default_rng(23)
     lengths, dim, pages = [40] * 400, 64, 1300
