@@ -97,7 +97,7 @@ __device__ __forceinline__ float max_nan(float a, float b)
 // most warps).  The quotient is corrected once (Markstein): with y = 1 / d correctly rounded, t = fl(v y) and the exact
 // r = v - t d, fl(t + r y) is the rounded quotient up to 2^-24 of an ulp; that it lies on the same side of every
 // half-integer as fl(v / d) was checked for all 2^23 mantissas of d and the five floats around each of the 127 places
-// where it matters.  Adding 1/2 and 2^23 toward zero leaves the magnitude rounded half away from zero.
+// where it matters (orc_corrected_quotients_off of the oracle; the tests run a part of it).  Adding 1/2 and 2^23 toward zero leaves the magnitude rounded half away from zero.
 __device__ __forceinline__ uint4 q8_codes16(const float4 (&v)[4], float d)
 {
     const float y = __frcp_rn(d);

@@ -227,6 +227,28 @@ void orc_quantize_q8_0(const float *x, int64_t rows, int64_t k, int8_t *q, uint1
             quantize_block(x + r * k + b * QK, q + r * k + b * QK, d + r * nb + b);
 }
 
+/* The cache's Q8_0 codes take a quotient corrected once in place of the division:
+ * y = fl(1 / d), t = fl(v y), q = fl(t + fl(v - t d) y), code floor(|q| + 1/2).  The
+ * number of v, among the five floats around each half-integer multiple of d below 127,
+ * whose code is not that of fl(v / d); over the mantissas first, first + step, ... below
+ * last of d = (1 + mantissa / 2^23) 2^exponent. */
+int64_t orc_corrected_quotients_off(int64_t first, int64_t last, int64_t step, int exponent)
+{
+    int64_t off = 0;
+    for (int64_t m = first; m < last; m += step) {
+        const float d = ldexpf(1.0f + (float)m * 0x1p-23f, exponent), y = 1.0f / d;
+        for (int n = 0; n < 127; ++n) {
+            float v = (float)((n + 0.5) * (double)d);
+            v = nextafterf(nextafterf(v, 0.0f), 0.0f);
+            for (int i = 0; i < 5; ++i, v = nextafterf(v, INFINITY)) {
+                const float t = v * y, q = fmaf(fmaf(-t, d, v), y, t);
+                off += floor((double)q + 0.5) != floor((double)(v / d) + 0.5); /* exact: below 2^8 */
+            }
+        }
+    }
+    return off;
+}
+
 /* ------------------------------------------------------------------------ */
 /* RMSNorm                                                                    */
 /* ------------------------------------------------------------------------ */

@@ -88,6 +88,22 @@ def test_moved_covers_a_change_of_the_weights():
         assert abs(np.log(w.sum() / p.sum())) <= lse[0] * 1.01
 
 
+# ---------------------------------------------------------------- the kernel's arithmetic
+
+@pytest.mark.parametrize("exponent", [-100, -24, 0, 120])
+def test_corrected_quotients_give_the_divisions_codes(orc, exponent):
+    """Every 4099th mantissa of a block's scale, at both ends of the exponents for which the cache's writing takes the
+    corrected quotient; all 2^23 of them (5.3e9 quotients, some minutes) with QG_ALL_QUOTIENTS=1."""
+    import os
+
+    from oracle import _load
+
+    count = _load().orc_corrected_quotients_off
+    count.restype, count.argtypes = ctypes.c_int64, [ctypes.c_int64] * 3 + [ctypes.c_int]
+    assert count(0, 1 << 23, 1 if os.environ.get("QG_ALL_QUOTIENTS") else 4099, exponent) == 0
+    assert count((1 << 23) - 64, 1 << 23, 1, exponent) == 0 and count(0, 64, 1, exponent) == 0
+
+
 # ---------------------------------------------------------------- C refusals
 
 BAD_CACHES = [(dict(format=2), UNSUPPORTED), (dict(format=-1), UNSUPPORTED), (dict(head_dim=80), UNSUPPORTED),
