@@ -172,6 +172,44 @@ def test_write_special_values(torch, qg, fmt, kind):
     check_write(torch, qg, fmt, kind, x, np.arange(8), 1, 16)
 
 
+@pytest.mark.parametrize("exponent", [-101, -100, -99, -60, -7, 0, 60, 119])
+def test_write_q8_0_near_ties(torch, qg, exponent):
+    """Values within two floats of a half-integer multiple of their block's scale, at scales over the whole range, those for
+    which each of the two ways to a code is taken among them."""
+    rng = np.random.default_rng(exponent + 200)
+    rows, dim = 2048, 256
+    top = np.ldexp(rng.uniform(127, 254, (2, rows, 1, dim // 32)), exponent).astype(np.float32)
+    d = (top / np.float32(127)).astype(np.float64)[..., None]
+    v = ((rng.integers(0, 127, (2, rows, 1, dim // 32, 32)) + 0.5) * d).astype(np.float32)
+    for _ in range(2):
+        v = np.where(rng.random(v.shape) < 0.4, np.nextafter(v, np.float32(0)), v)
+        v = np.where(rng.random(v.shape) < 0.4, np.nextafter(v, np.float32(np.inf)), v)
+    v = np.minimum(v, top[..., None]) * rng.choice(np.float32([-1, 1]), v.shape)
+    v[..., 9] = top
+    check_write(torch, qg, "q8_0", "f32", v.reshape(2, rows, 1, dim), rng.permutation(2064)[:rows], 129, 16)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("dim,rows", [(64, 19999), (96, 13007), (192, 6999), (256, 5003)])
+def test_many_rows_of_every_width(torch, qg, fmt, kind, dim, rows):
+    """The form that takes two rows a thread, written and read, three heads: rows whose threads do not divide a CTA."""
+    rng = np.random.default_rng(rows)
+    page, heads = 16, 3
+    pages = -(-rows // page) + 1
+    slots = rng.permutation(pages * page)[:rows]
+    x = rng.standard_normal((2, rows, heads, dim)).astype(np.float32)
+    check_write(torch, qg, fmt, kind, x, slots, pages, page, "stacked")
+    c = random_cache(rng, fmt, 64, heads, page, dim, spread=3.0)
+    slots = rng.integers(-3, 64 * page, 3 * rows)
+    out = [Guarded(torch, (3 * rows, heads, dim), types(torch)[kind]) for _ in range(2)]
+    qg.qg_kv_read(upload(torch, qg, c), dev(torch, slots), None, out[0].view, out[1].view)
+    for o, n in zip(out, "kv"):
+        o.check()
+        want = torch.from_numpy(K.rows(c, slots, n).astype(np.float32)).to(types(torch)[kind])
+        assert torch.equal(o.view.cpu(), want)
+
+
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
 @pytest.mark.parametrize("dim", DIMS)
 def test_write_q8_0_keeps_nan(torch, qg, dim, kind):
@@ -1009,6 +1047,31 @@ def test_one_workspace_for_several_shapes(torch, qg):
             q = rng.standard_normal((len(lengths), heads * group, dim)).astype(np.float32)
             args = dev(torch, q), upload(torch, qg, c), dev(torch, t), dev(torch, np.array(lengths, np.int32))
             assert torch.equal(qg.qg_attn_decode(*args, work=work), qg.qg_attn_decode(*args))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dim", DIMS)
+@pytest.mark.parametrize("group", [1, 8, 16])
+def test_workspace_bounds_and_counters(torch, qg, fmt, dim, group):
+    """A workspace of exactly the reported size between guard bands: every CTA's counter is zero again after calls whose items
+    lie on two CTAs, on many and on one, and nothing is written outside."""
+    rng = np.random.default_rng(dim + group)
+    heads = 2
+    ws = Guarded(torch, (qg.qg_attn_decode_workspace_bytes(heads * group, heads, dim),), torch.uint8)
+    work = qg.AttnWork(ws.view.zero_())
+    counters = 4 * 4 * torch.cuda.get_device_properties(0).multi_processor_count  # four CTAs an SM at most
+    for lengths in ([9000], [700, 0, 5200, 31, 1], [int(n) for n in rng.integers(0, 1200, 400)]):
+        c = random_cache(rng, fmt, 700, heads, 16, dim)
+        t = rng.integers(0, 700, (len(lengths), -(-max(lengths) // 16) + 300)).astype(np.int32)  # pages shared by sequences
+        q = rng.standard_normal((len(lengths), heads * group, dim)).astype(np.float32)
+        args = dev(torch, q), upload(torch, qg, c), dev(torch, t), dev(torch, np.array(lengths, np.int32))
+        got = qg.qg_attn_decode(*args, work=work)
+        ws.check()
+        assert not ws.view[:counters].any()
+        assert ws.view[counters:].any()  # the line's records
+        if len(lengths) < 10:
+            assert_attention(got, None, K.attention(q, c, t, lengths, float(np.float32(dim ** -0.5))))
+        assert torch.equal(qg.qg_attn_decode(*args, work=work), got)
 
 
 def test_binding_refusals(torch, qg):
