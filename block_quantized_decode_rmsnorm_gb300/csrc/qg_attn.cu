@@ -1,6 +1,8 @@
 // Decode attention: the workspace and the choice of kernel (qg_attn.cuh).
 #include "qg_attn.cuh"
 
+#include <cmath>
+
 namespace qg {
 
 namespace {
@@ -100,7 +102,10 @@ cudaError_t launch_attn_decode(const KvPlanes &c, const void *q, int64_t q_row, 
     a.group = static_cast<int>(group), a.q_heads = static_cast<int>(q_heads);
     a.chunks = static_cast<int>((group + s.heads - 1) / s.heads);
     a.page_shift = shift;
-    a.batch = batch, a.pages = pages, a.lengths = lengths, a.max_pages = max_pages, a.scale = scale;
+    a.batch = batch, a.pages = pages, a.lengths = lengths, a.max_pages = max_pages;
+    a.exponent = std::fabs(scale) > 0x1p126f ? 2 : 0;
+    a.factor = (a.exponent ? scale * 0.25f : scale) * kLog2e;
+    a.most = std::isfinite(scale) ? FLT_MAX : INFINITY;
     a.held = static_cast<int>(max_pages * c.page);
     a.window = window < a.held ? static_cast<int>(window) : 0;  // one that reaches over the whole table is none
     a.out = out, a.out_bf16 = out_dtype == QG_BF16, a.lse = lse;

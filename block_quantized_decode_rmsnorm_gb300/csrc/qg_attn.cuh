@@ -80,7 +80,8 @@ struct AttnArgs {
     const int32_t *pages, *lengths;
     int64_t max_pages;
     int held, window;  // tokens that a page table holds; 0: no window
-    float scale;
+    float factor, most;  // scale log2(e) = factor 2^exponent; what a row's factor is held at, infinity where the scale is not finite
+    int exponent;        // 0, or 2 where factor would leave f32
     void *out;
     int out_bf16;
     float *lse;
@@ -505,10 +506,9 @@ struct Attn {
                 r.w = pack_f16(w.z - b23.x, w.w - b23.y);
                 if (p < D / 4) put_piece(qf, x, p, r);
             }
-            if (lane == 0) {  // the power of two first; finite where the scale is, so that scores of zero stay zero
-                const float k = a.scale * __uint_as_float(static_cast<uint32_t>(ex - 14 + 127) << 23) * kLog2e;
-                qc[x] = fabsf(a.scale) <= FLT_MAX ? fminf(fmaxf(k, -FLT_MAX), FLT_MAX) : k;
-            }
+            // finite where the scale is, so that scores of zero stay zero
+            const float k = a.factor * __uint_as_float(static_cast<uint32_t>(ex - 14 + a.exponent + 127) << 23);
+            if (lane == 0) qc[x] = fminf(fmaxf(k, -a.most), a.most);
         }
     }
 
