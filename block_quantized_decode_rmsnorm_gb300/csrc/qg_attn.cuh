@@ -512,11 +512,19 @@ struct Attn {
         }
     }
 
-    // O^T = f O^T + V^T P^T, where s holds the tokens' p and vx where their values lie.  FAR: the weights of each block of values
-    // are brought to 2^14 by a power of two of their own, so that f16 holds them wherever the block's scales lie.
+    // Four tokens' codes of dims g, g + 8, g + 16 and g + 24 of 32.
+    static __device__ __forceinline__ void values(uint32_t at, uint32_t (&r)[4])
+    {
+        asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];"
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+    }
+
+    // O^T = f O^T + V^T P^T, where s holds the tokens' p, vx where their values lie, early the first of them.  FAR: the weights
+    // of each block of values are brought to 2^14 by a power of two of their own, so that f16 holds them wherever the block's
+    // scales lie.
     template <bool FAR>
     __device__ __forceinline__ void add(const float (&s)[NT][2 * CH][2], const float (&dv)[2 * CH][2][NB], const float (&f0)[NT],
-                                        const float (&f1)[NT], const uint32_t (&vx)[S::NX], int lane)
+                                        const float (&f1)[NT], const uint32_t (&vx)[S::NX], const uint32_t (&early)[CH][4], int lane)
     {
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
@@ -556,11 +564,13 @@ struct Attn {
                 Quad acc[NT][2];
 #pragma unroll
                 for (int ch = 0; ch < CH; ++ch) {
-                    // four tokens' codes of dims g, g + 8, g + 16 and g + 24 of the block
                     uint32_t r[4];
-                    asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];"
-                        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                        : "r"(vx[dg % S::NX] + S::piece_at(dg) + ch * S::TILE) : "memory");
+                    if (dg == 0) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) r[i] = early[ch][i];
+                    } else {
+                        values(vx[dg % S::NX] + S::piece_at(dg) + ch * S::TILE, r);
+                    }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) r[i] = code_bits<E4M3>(r[i]);
                     const uint32_t va[2][4] = {{codes_f16<E4M3, false>(r[0]), codes_f16<E4M3, false>(r[1]),
@@ -583,7 +593,9 @@ struct Attn {
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         float(&d)[4] = o[i][2 * dg + x].v;
-                        if constexpr (FAR) acc[i][x].v[0] *= down0[i], acc[i][x].v[1] *= down1[i], acc[i][x].v[2] *= down0[i], acc[i][x].v[3] *= down1[i];
+                        if constexpr (FAR)
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) acc[i][x].v[y] *= y % 2 ? down1[i] : down0[i];
                         d[0] = fmaf(d[0], f0[i], acc[i][x].v[0]);
                         d[1] = fmaf(d[1], f1[i], acc[i][x].v[1]);
                         d[2] = fmaf(d[2], f0[i], acc[i][x].v[2]);
@@ -604,13 +616,6 @@ struct Attn {
         for (int i = 0; i < S::NX; ++i) {
             kx[i] = st + S::key_piece(g, i) + t * 8;
             vx[i] = smem_addr(st) + S::CODES + S::value_row_at(lane & 15, 2 * i + (lane >> 4));
-        }
-        // ---- a token to each lane: are its values' scales near one another?
-        {
-            const int token = lane % TOK;
-            bool is = scales_far<E4M3, NB>(st + token / KV_TILE * S::TILE + 2 * S::CODES + S::SCALES + token % KV_TILE * NB * S::SB);
-            if constexpr (EDGE) is = is && at + token >= seen.first && at + token < seen.n;
-            far = __any_sync(0xffffffffu, is) || far;
         }
         // ---- scores
         float s[NT][2 * CH][2];
@@ -656,6 +661,13 @@ struct Attn {
                     }
             }
         }
+        // ---- a token to each lane: are its values' scales near one another?
+        {
+            const int token = lane % TOK;
+            bool is = scales_far<E4M3, NB>(st + token / KV_TILE * S::TILE + 2 * S::CODES + S::SCALES + token % KV_TILE * NB * S::SB);
+            if constexpr (EDGE) is = is && at + token >= seen.first && at + token < seen.n;
+            far = __any_sync(0xffffffffu, is) || far;
+        }
         // ---- values' scales, and what is not seen
         float dv[2 * CH][2][NB], e[2 * CH][2];
 #pragma unroll
@@ -692,6 +704,9 @@ struct Attn {
                 for (int b = 0; b < NB; ++b) top = fmaxf(top, fabsf(dv[j][x][b]));
                 asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(e[j][x]) : "f"(fminf(top, E4M3 ? AT_E4M3_MOST : 65504.0f)));
             }
+        uint32_t early[CH][4];  // before the branch, which would wait for them
+#pragma unroll
+        for (int ch = 0; ch < CH; ++ch) values(vx[0] + ch * S::TILE, early[ch]);
         // ---- weights
         float f[NT];
 #pragma unroll
@@ -730,9 +745,9 @@ struct Attn {
         }
         // ---- O^T = f O^T + V^T P^T, this step's part summed by itself
         if (far)
-            add<true>(s, dv, f0, f1, vx, lane);
+            add<true>(s, dv, f0, f1, vx, early, lane);
         else
-            add<false>(s, dv, f0, f1, vx, lane);
+            add<false>(s, dv, f0, f1, vx, early, lane);
     }
 };
 
