@@ -2,8 +2,8 @@
 //
 //   o = sum_t p_t V_t / sum_t p_t,  p_t = e^(scale q . K_t),  one pass with a running maximum
 //
-// The cache is read once, whatever the number of query heads that share a cache head (up
-// to 16), so HBM bounds it: 2 (D + D/16) bytes a token and head (Q8_0).  What has to
+// The cache is read once for the query heads that share a cache head, up to 16 of them (again for every 16 more: serving's
+// cache with 16 query heads to a head 140 us, with 32 264), so HBM bounds it: 2 (D + D/16) bytes a token and head (Q8_0).  What has to
 // fit under that bound is the work on each byte - its code made a binary16 operand, two
 // matrix products, the softmax - so both products run on mma.sync m16n8k16 with the codes
 // as exact f16 integers (or e4m3 values), scales applied outside in f32:
@@ -26,7 +26,8 @@
 //               The other blocks' weights are then as large as their scales are near to the token's largest.  Where
 //               a token's scales lie more than 2^8 apart (AT_NEAR), from there to the item's end each step brings the weights of
 //               each block to 2^14 by a power of two of their own and takes it off the sums.  Looking for such tokens, one to a
-//               lane, and the branch cost 1 to 5 % (serving 100 us, 105 with them; e4m3 93.6, 94); without
+//               lane, and the branch cost 1 to 4 % (serving 100.4 us, 104.0 with them; e4m3 93.5, 93.7) and such items 15 to
+//               35 % (a block 2^-12 of the others in every token: serving 120); without
 //               them a block 2^-36 of its neighbour came out wrong by a half.
 //
 // A warp takes TOK tokens a step and copies its own steps to shared memory by cp.async, one step ahead: no barrier,
@@ -38,15 +39,15 @@
 // finds by a scan over the lengths.  An item that lies inside one stretch is finished there; the parts of the others go to
 // the workspace, and the CTA that brings the last of them (a counter per CTA in which an item begins) joins them in
 // order.  Where an item has few units at most, as the page tables' width tells the host, the direct form
-// (attn_direct_kernel) gives it a cluster, without scan, workspace and counter (one sequence of 700 tokens: 5.0 us, 7.3 in
+// (attn_direct_kernel) gives it a cluster, without scan, workspace and counter (one sequence of 700 tokens: 5.1 us, 7.2 in
 // the line), and where there are many such items the warps' form (attn_warps_kernel) gives it a warp.
 //
 // What bounds it: HBM where there is much to read, issue for narrow heads, latency below some 50 MB: about 4 us to
 // the first unit's end (length, pages, tokens, each a round trip to memory), 2 us from the last to the joined output.
 // Measured, the share of the copy rate and the names that the comments below give the cases:
-//   serving   64 sequences of up to 8192 tokens, 8 heads of 128, 64 query heads, bf16: Q8_0 96 us (89 %), e4m3 93 us (90 %)
-//   document  one sequence of 131072 tokens, 8 heads of 128, 32 query heads, Q8_0, bf16: 51 us (83 %)
-//   chats     256 sequences of up to 1000 tokens, 16 heads of 64, a query head each, Q8_0, bf16: 69 us (61 %; 0.6
+//   serving   64 sequences of up to 8192 tokens, 8 heads of 128, 64 query heads, bf16: Q8_0 104 us (83 %), e4m3 94 us (88 %)
+//   document  one sequence of 131072 tokens, 8 heads of 128, 32 query heads, Q8_0, bf16: 54 us (79 %)
+//   chats     256 sequences of up to 1000 tokens, 16 heads of 64, a query head each, Q8_0, bf16: 76 us (55 %; 0.6
 //             instructions a cycle and scheduler, seven eighths of the MMAs' columns unused)
 //   windows   32 sequences of up to 16384 tokens, the last 1024 of them, 4 heads of 256, 8 query heads, e4m3, f32: 19 us (52 %)
 // Figures of a choice are of the day it was made: they compare its two sides.  Times in these files are of graph replays

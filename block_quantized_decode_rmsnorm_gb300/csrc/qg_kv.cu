@@ -129,7 +129,7 @@ __device__ __noinline__ uint4 q8_codes16_any(float4 a, float4 b, float4 c, float
     return make_uint4(q8_pack4(a, d, rd), q8_pack4(b, d, rd), q8_pack4(c, d, rd), q8_pack4(e, d, rd));
 }
 
-// Bound by issue where rows are many (8192 rows of 8 heads of 128 bf16 values: 13.1 us for 51 MB, 0.7 instructions a cycle
+// Bound by issue where rows are many (8192 rows of 8 heads of 128 bf16 values in Q8_0: 12.8 us for 51 MB, in e4m3 10.3; 0.7 instructions a cycle
 // and scheduler): eight instructions a code, and the slot's, the addresses' and the maximum's beside them.
 template <typename T, bool E4M3, int L, int RB>
 __global__ void __launch_bounds__(KT) kv_write_kernel(KvRows a, KvSource<T> s)
