@@ -509,7 +509,7 @@ struct Attn {
             }
             // finite where the scale is, so that scores of zero stay zero
             const float k = a.factor * __uint_as_float(static_cast<uint32_t>(ex - 14 + a.exponent + 127) << 23);
-            if (lane == 0) qc[x] = fminf(fmaxf(k, -a.most), a.most);
+            if (lane == 0) qc[x] = k == k ? fminf(fmaxf(k, -a.most), a.most) : k;
         }
     }
 

@@ -97,7 +97,8 @@ __device__ __forceinline__ float max_nan(float a, float b)
 // most warps).  The quotient is corrected once (Markstein): with y = 1 / d correctly rounded, t = fl(v y) and the exact
 // r = v - t d, fl(t + r y) is the rounded quotient up to 2^-24 of an ulp; that it lies on the same side of every
 // half-integer as fl(v / d) was checked for all 2^23 mantissas of d and the five floats around each of the 127 places
-// where it matters (orc_corrected_quotients_off of the oracle; the tests run a part of it).  Adding 1/2 and 2^23 toward zero leaves the magnitude rounded half away from zero.
+// where it matters (orc_corrected_quotients_off of the oracle; the tests run a part of it).  Adding 1/2 and 2^23 toward zero
+// leaves the magnitude rounded half away from zero.
 __device__ __forceinline__ uint4 q8_codes16(const float4 (&v)[4], float d)
 {
     const float y = __frcp_rn(d);
@@ -129,8 +130,8 @@ __device__ __noinline__ uint4 q8_codes16_any(float4 a, float4 b, float4 c, float
     return make_uint4(q8_pack4(a, d, rd), q8_pack4(b, d, rd), q8_pack4(c, d, rd), q8_pack4(e, d, rd));
 }
 
-// Bound by issue where rows are many (8192 rows of 8 heads of 128 bf16 values in Q8_0: 12.8 us for 51 MB, in e4m3 10.3; 0.7 instructions a cycle
-// and scheduler): eight instructions a code, and the slot's, the addresses' and the maximum's beside them.
+// Bound by issue where rows are many (8192 rows of 8 heads of 128 bf16 values in Q8_0: 12.8 us for 51 MB, in e4m3 10.3; 0.7
+// instructions a cycle and scheduler): eight instructions a code, and the slot's, the addresses' and the maximum's beside them.
 template <typename T, bool E4M3, int L, int RB>
 __global__ void __launch_bounds__(KT) kv_write_kernel(KvRows a, KvSource<T> s)
 {

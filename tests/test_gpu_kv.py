@@ -554,6 +554,29 @@ def test_attention_largest_scales(torch, qg, fmt, kind, scale, lengths, columns)
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("kinds", [("f32", "bf16"), ("bf16", "f32")])
+@pytest.mark.parametrize("dim,group", [(64, 3), (128, 12), (256, 16)])
+@pytest.mark.parametrize("lengths,wide", [([70, 3], False), ([300, 1, 650], True), ([20] * 330, False)])
+def test_attention_mixed_types_of_each_form(torch, qg, fmt, kinds, dim, group, lengths, wide):
+    run_attention(torch, qg, fmt, dim, 2, group, 16, lengths, kinds=kinds, wide=wide)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("scale", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("lengths,columns", [([70, 3], 1), ([300, 5, 650], 400), ([37] * 330, 1)])
+def test_attention_scale_not_finite(torch, qg, kind, scale, lengths, columns):
+    """No number comes of a scale that is none."""
+    rng = np.random.default_rng(47)
+    pages = sum(-(-n // 16) for n in lengths) + 1
+    c = random_cache(rng, "q8_0", pages, 2, 16, 128)
+    q = torch.from_numpy(rng.standard_normal((len(lengths), 6, 128)).astype(np.float32)).to(types(torch)[kind]).cuda()
+    lse = torch.empty((len(lengths), 6), device="cuda")
+    got = qg.qg_attn_decode(q, upload(torch, qg, c), dev(torch, tables(rng, lengths, 16, pages, extra=columns)),
+                            dev(torch, np.array(lengths, np.int32)), scale, lse=lse)
+    assert torch.isnan(got).all() and not torch.isfinite(lse).any()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 def test_attention_small_beside_large_query(torch, qg, fmt):
     """A query's values 2^-16 and 2^-24 of the head's largest, which meets keys of zero: held to 22 bits or 2^-39 of the largest."""
     rng = np.random.default_rng(43)
