@@ -65,9 +65,13 @@ constexpr int AT_THREADS = 32 * AT_WARPS;
 constexpr int AT_CTAS_MAX = 4;  // per SM
 constexpr int AT_FEW = 4;      // rows of 32 sequences that every warp scans for itself
 constexpr int AT_CLUSTER = 8;  // CTAs to an item in the direct form, at most
-// Between these e4m3 scales the running maximum follows a token's largest: the sum of weights stays in range for 2^30 tokens
-// of up to 2^(14 + 82), and the sums of values for the largest scale there is, 2^119.2.
-constexpr float AT_E4M3_LEAST = 0x1p-82f, AT_E4M3_MOST = 0x1p64f;
+// Between these scales the running maximum follows a token's largest (all of binary16's; e4m3's are f32).  Below the least
+// weights reach 2^(14 + 25) of the softmax's: 2^30 tokens of them stay in range.  Above the most, 2^119.2 at the end,
+// 2^30 tokens' sums of values stay in range as their p are under 2^-31.  2^70 between the two: where the maximum moves by so
+// much, from a token without values to one of large ones, the factor 2^-70 of what came before is far from f32's end.
+constexpr float AT_LEAST = 0x1p-25f;
+template <bool E4M3>
+constexpr float kAttnMost = E4M3 ? 0x1p45f : 65504.0f;
 constexpr float AT_NEAR = 256.0f;  // a token's scales this near to one another share a reference for the weights' 16 bits
 constexpr int AT_SHORT = 8;  // steps of an item in the warps' form, at most; twice as many where there are many items
 
@@ -244,7 +248,7 @@ __device__ __forceinline__ bool scales_far(const uint8_t *p)
     if constexpr (E4M3) {
         const float *const d = reinterpret_cast<const float *>(p);
         const float a = fabsf(d[0]), b = fabsf(d[NB - 1]);
-        return !(fminf(a, b) * AT_NEAR > fmaxf(fmaxf(a, b), AT_E4M3_LEAST) && fmaxf(a, b) <= AT_E4M3_MOST);
+        return !(fminf(a, b) * AT_NEAR > fmaxf(fmaxf(a, b), AT_LEAST) && fmaxf(a, b) <= kAttnMost<E4M3>);
     } else {
         uint32_t w[(NB + 1) / 2];
         if constexpr (NB % 2) {  // 6 bytes, at even addresses
@@ -700,10 +704,10 @@ struct Attn {
         for (int j = 0; j < 2 * CH; ++j)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                float top = E4M3 ? AT_E4M3_LEAST : 0x1p-25f;
+                float top = AT_LEAST;
 #pragma unroll
                 for (int b = 0; b < NB; ++b) top = fmaxf(top, fabsf(dv[j][x][b]));
-                asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(e[j][x]) : "f"(fminf(top, E4M3 ? AT_E4M3_MOST : 65504.0f)));
+                asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(e[j][x]) : "f"(fminf(top, kAttnMost<E4M3>)));
             }
         uint32_t early[CH][4];  // before the branch, which would wait for them
 #pragma unroll

@@ -712,6 +712,29 @@ def test_attention_blocks_far_apart(torch, qg, fmt, dim, group, kind, scales, le
     assert_by_blocks(got, c, t, lengths, want, scales)
 
 
+@pytest.mark.parametrize("fmt,exponent", [("q8_0", 15), ("e4m3", 15), ("e4m3", 42), ("e4m3", 50), ("e4m3", 80), ("e4m3", 118)])
+@pytest.mark.parametrize("kind,dim,group", [("f32", 128, 4), ("bf16", 96, 9), ("f32", 256, 3)])
+@pytest.mark.parametrize("where", ["first", "last"])
+@pytest.mark.parametrize("lengths,columns", [([70, 33, 17], 1), ([300, 33, 650], 400), ([33] * 330, 1)])
+def test_attention_without_values_beside_large_ones(torch, qg, fmt, exponent, kind, dim, group, where, lengths, columns):
+    """The first 32 tokens have no values, or the last alone: what they have of the softmax's sum counts beside tokens of the
+    largest values, met later by the same warp or by another."""
+    rng = np.random.default_rng(exponent + dim)
+    page, heads = 16, 2
+    pages = sum(-(-n // page) for n in lengths) + 1
+    c = random_cache(rng, fmt, pages, heads, page, dim)
+    t = tables(rng, lengths, page, pages, extra=columns)
+    c["vd"][...] = 2.0 ** exponent
+    for b, n in enumerate(lengths):
+        silent = np.arange(min(32, n - 1)) if where == "first" else np.array([n - 1])
+        c["v"][t[b, silent // page], :, silent % page] = 0
+        c["vd"][t[b, silent // page], :, silent % page] = 0 if fmt == "q8_0" else 2.0 ** -108
+    q = torch.from_numpy(rng.standard_normal((len(lengths), heads * group, dim)).astype(np.float32)).to(types(torch)[kind])
+    want = K.attention(q.float().numpy(), c, t, lengths, float(np.float32(dim ** -0.5)))
+    got = qg.qg_attn_decode(q.cuda(), upload(torch, qg, c), dev(torch, t), dev(torch, np.array(lengths, np.int32)))
+    assert_by_blocks(got, c, t, lengths, want)
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
 @pytest.mark.parametrize("lengths", [[2], [100, 3, 1500], [20] * 400])
